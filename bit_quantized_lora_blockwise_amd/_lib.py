@@ -31,7 +31,11 @@ EXPORTS = ("nf4_quantize", "nf4_quantize_dq", "nf4_double_quant", "nf4_dequantiz
            "q4_quantize", "q4_double_quant", "q4_dequantize", "q4_levels",
            "qlora_group_fwd_workspace", "qlora_group_fwd", "qlora_group_bwd_workspace", "qlora_group_bwd",
            "qlora_adamw_step", "qlora_linear_fwd_noalloc",
-           "lora_linear_fwd", "lora_linear_bwd", "lora_linear_fwd_t", "lora_linear_dx")
+           "lora_linear_fwd", "lora_linear_bwd", "lora_linear_fwd_t", "lora_linear_dx",
+           "lora_dropout", "qlora_linear_fwd_dropout_workspace", "qlora_linear_fwd_dropout",
+           "qlora_linear_bwd_dropout_workspace", "qlora_linear_bwd_dropout",
+           "mx4_codes_bytes", "mx4_scales_bytes", "mx4_quantize", "mx4_dequantize", "mx4_matmul",
+           "mx4_linear_fwd_workspace", "mx4_linear_fwd", "mx4_linear_bwd_workspace", "mx4_linear_bwd")
 
 
 class QloraError(RuntimeError):
@@ -49,6 +53,7 @@ def lib():
                                "`python -m bit_quantized_lora_blockwise_amd.build`")
         L = ctypes.CDLL(_LIB_PATH)
         P, I64, I32, F32, SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+        F64, U64 = ctypes.c_double, ctypes.c_uint64
         sig = {
             "nf4_quantize": ([P, I32, I64, I64, P, P, P], I32),
             "nf4_double_quant": ([P, I64, P, P, P], I32),
@@ -81,6 +86,22 @@ def lib():
             "lora_linear_bwd": ([P, P, I64, I64, I64, P, P, P, I32, F32, P, P, P, P, P, SZ, P], I32),
             "lora_linear_fwd_t": ([P, I64, I64, I64, P, P, P, I32, F32, P, P], I32),
             "lora_linear_dx": ([P, I64, I64, I64, P, P, P, I32, P, P], I32),
+            "lora_dropout": ([P, I32, I64, I64, I64, F64, U64, U64, P, P], I32),
+            "qlora_linear_fwd_dropout_workspace": ([I64, I64, I64, I32], SZ),
+            "qlora_linear_fwd_dropout": ([P, I64, I64, I64, P, P, P, P, P, I32, F32, F64, U64, U64, P, P, P, SZ, P],
+                                         I32),
+            "qlora_linear_bwd_dropout_workspace": ([I64, I64, I64, I32], SZ),
+            "qlora_linear_bwd_dropout": ([P, P, I64, I64, I64, P, P, P, P, P, I32, F32, F64, U64, U64, P, P, P, P, P,
+                                          SZ, P], I32),
+            "mx4_codes_bytes": ([I64, I64], SZ),
+            "mx4_scales_bytes": ([I64, I64], SZ),
+            "mx4_quantize": ([P, I32, I64, I64, I64, I32, P, P, P], I32),
+            "mx4_dequantize": ([P, P, I64, I64, P, P], I32),
+            "mx4_matmul": ([P, P, I64, P, P, I64, I64, P, P], I32),
+            "mx4_linear_fwd_workspace": ([I64, I64, I64, I32], SZ),
+            "mx4_linear_fwd": ([P, I64, I64, I64, P, P, P, P, I32, F32, F64, U64, U64, P, P, P, SZ, P], I32),
+            "mx4_linear_bwd_workspace": ([I64, I64, I64, I32], SZ),
+            "mx4_linear_bwd": ([P, P, I64, I64, I64, P, P, P, P, I32, F32, F64, U64, U64, P, P, P, P, P, SZ, P], I32),
         }
         for name, (args, res) in sig.items():
             f = getattr(L, name)
@@ -603,3 +624,169 @@ def lora_linear_dx(dY, W, G, L1, dX=None, stream=None):
     _check("lora_linear_dx", lib().lora_linear_dx(
         _ptr(dY), M, K, N, _ptr(W), _ptr(G), _ptr(L1), r, _ptr(dX), _stream(stream)))
     return dX
+
+
+# --- dropout on the adapter's input --------------------------------------------
+
+def _rows(X, name):
+    """(dtype code, rows, cols, ld) of a 2-D fp32 or bf16 matrix whose rows are contiguous (and may be apart)."""
+    if not isinstance(X, torch.Tensor) or X.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"{name} must be a float32 or bfloat16 torch.Tensor")
+    if X.dim() != 2:
+        raise ValueError(f"{name} must have 2 dims, got {X.dim()}")
+    rows, cols = X.shape
+    ld = X.stride(0) if rows > 1 else cols
+    if (cols > 1 and X.stride(1) != 1) or ld < cols:
+        raise ValueError(f"{name} must have contiguous rows that do not overlap, got strides {X.stride()}")
+    return QL_BF16 if X.dtype == torch.bfloat16 else QL_F32, rows, cols, ld
+
+
+def _u64(v, name):
+    if int(v) != v or not 0 <= v < 1 << 64:
+        raise ValueError(f"{name} must be a whole number in [0, 2^64), got {v}")
+    return int(v)
+
+
+def _draw(p, seed, offset):
+    return float(p), _u64(seed, "seed"), _u64(offset, "offset")
+
+
+def lora_dropout(X, p, seed, offset=0, out=None, stream=None):
+    """D o X for X [rows, cols] (fp32 or bf16, rows may be apart): kept elements over 1 - p, the others 0.
+    The mask is a function of (p, seed, offset) and is never stored; the same call is the backward."""
+    dt, rows, cols, ld = _rows(X, "X")
+    out = _out(out, "out", X.dtype, (rows, cols), X)
+    _check("lora_dropout", lib().lora_dropout(_ptr(X), dt, rows, cols, ld, *_draw(p, seed, offset), _ptr(out),
+                                              _stream(stream)))
+    return out
+
+
+def qlora_linear_fwd_dropout(X, codes, c2, c1, N, L1, L2, lora_scale=1.0, p=0.0, seed=0, offset=0, Y=None, T_out=None,
+                             workspace=None, stream=None):
+    """qlora_linear_fwd with T = bf16((D o X) L1).  Returns (Y, T_out or None)."""
+    _need(X, "X", torch.bfloat16, ndim=2)
+    M, K = X.shape
+    _packed(codes, c2, c1, N, K)
+    r = _rank(L1, K)
+    _need(L2, "L2", torch.bfloat16, shape=(r, N))
+    Y = _out(Y, "Y", torch.bfloat16, (M, N), X)
+    T_out = _opt_out(T_out, "T_out", torch.bfloat16, (M, r), X)
+    ws = _workspace(int(lib().qlora_linear_fwd_dropout_workspace(M, K, N, r)), X, workspace)
+    _check("qlora_linear_fwd_dropout", lib().qlora_linear_fwd_dropout(
+        _ptr(X), M, K, N, _ptr(codes), _ptr(c2), _ptr(c1), _ptr(L1), _ptr(L2), r, float(lora_scale),
+        *_draw(p, seed, offset), _ptr(Y), _ptr(T_out), _ptr(ws), ws.numel(), _stream(stream)))
+    return Y, T_out
+
+
+def qlora_linear_bwd_dropout(X, dY, codes, c2, c1, L1, L2, lora_scale=1.0, p=0.0, seed=0, offset=0, T=None, dX=True,
+                             dL1=None, dL2=None, workspace=None, stream=None):
+    """(dX or None, dL1 fp32 [K, r], dL2 fp32 [r, N]) of qlora_linear_fwd_dropout; dX as in qlora_linear_bwd."""
+    _need(X, "X", torch.bfloat16, ndim=2)
+    M, K = X.shape
+    _need(dY, "dY", torch.bfloat16, ndim=2)
+    if dY.shape[0] != M:
+        raise ValueError(f"dY must have {M} rows, got {tuple(dY.shape)}")
+    N = dY.shape[1]
+    _packed(codes, c2, c1, N, K)
+    r = _rank(L1, K)
+    _need(L2, "L2", torch.bfloat16, shape=(r, N))
+    if T is not None:
+        _need(T, "T", torch.bfloat16, numel=M * r)
+    dX = _opt_out(dX, "dX", torch.bfloat16, (M, K), X)
+    dL1 = _out(dL1, "dL1", torch.float32, (K, r), X)
+    dL2 = _out(dL2, "dL2", torch.float32, (r, N), X)
+    ws = _workspace(int(lib().qlora_linear_bwd_dropout_workspace(M, K, N, r)), X, workspace)
+    _check("qlora_linear_bwd_dropout", lib().qlora_linear_bwd_dropout(
+        _ptr(X), _ptr(dY), M, K, N, _ptr(codes), _ptr(c2), _ptr(c1), _ptr(L1), _ptr(L2), r, float(lora_scale),
+        *_draw(p, seed, offset), _ptr(T), _ptr(dX), _ptr(dL1), _ptr(dL2), _ptr(ws), ws.numel(), _stream(stream)))
+    return dX, dL1, dL2
+
+
+# --- microscaled 4-bit (MXFP4) --------------------------------------------------
+
+def _mx4_shapes(rows, cols):
+    if rows <= 0 or cols <= 0:
+        raise ValueError(f"matrix [{rows}, {cols}]: sizes must be > 0")
+    kp = -(-cols // 128) * 128
+    return (kp // 32, rows, 16), (kp // 128, rows, 4)
+
+
+def _mx4_packed(codes, scales, rows, cols, what=""):
+    """The packed form of a [rows, cols] matrix: codes [Kp/32, rows, 16], scales [Kp/128, rows, 4]."""
+    sc, ss = _mx4_shapes(rows, cols)
+    _need(codes, what + "codes", torch.uint8, shape=sc)
+    _need(scales, what + "scales", torch.uint8, shape=ss)
+
+
+def mx4_quantize(X, transpose=False, codes=None, scales=None, stream=None):
+    """(codes [Kp/32, R, 16], scales [Kp/128, R, 4]) of X (fp32 or bf16, rows may be apart) in blocks of 32 along
+    its rows (R = rows), or with transpose down its columns (the packed matrix is X^T, R = cols)."""
+    dt, rows, cols, ld = _rows(X, "X")
+    sc, ss = _mx4_shapes(*((cols, rows) if transpose else (rows, cols)))
+    codes = _out(codes, "codes", torch.uint8, sc, X)
+    scales = _out(scales, "scales", torch.uint8, ss, X)
+    _check("mx4_quantize", lib().mx4_quantize(_ptr(X), dt, rows, cols, ld, int(bool(transpose)), _ptr(codes),
+                                              _ptr(scales), _stream(stream)))
+    return codes, scales
+
+
+def mx4_dequantize(codes, scales, rows, cols, out=None, stream=None):
+    """bf16 values [rows, cols] of a packed matrix (exact)."""
+    _mx4_packed(codes, scales, rows, cols)
+    out = _out(out, "out", torch.bfloat16, (rows, cols), codes)
+    _check("mx4_dequantize", lib().mx4_dequantize(_ptr(codes), _ptr(scales), rows, cols, _ptr(out), _stream(stream)))
+    return out
+
+
+def mx4_matmul(a_codes, a_scales, M, b_codes, b_scales, N, K, out=None, stream=None):
+    """bf16 [M, N] = A B^T of packed A [M, K] and B [N, K]."""
+    _mx4_packed(a_codes, a_scales, M, K, "a_")
+    _mx4_packed(b_codes, b_scales, N, K, "b_")
+    out = _out(out, "out", torch.bfloat16, (M, N), a_codes)
+    _check("mx4_matmul", lib().mx4_matmul(_ptr(a_codes), _ptr(a_scales), M, _ptr(b_codes), _ptr(b_scales), N, K,
+                                          _ptr(out), _stream(stream)))
+    return out
+
+
+def mx4_linear_fwd(X, codes, scales, N, L1, L2, lora_scale=1.0, p=0.0, seed=0, offset=0, Y=None, T_out=None,
+                   workspace=None, stream=None):
+    """Y = bf16(q(X) W'^T + s T L2), T = bf16((D o X) L1), with W [N, K] packed by mx4_quantize.
+    Returns (Y, T_out or None); T_out as in qlora_linear_fwd."""
+    _need(X, "X", torch.bfloat16, ndim=2)
+    M, K = X.shape
+    _mx4_packed(codes, scales, N, K)
+    r = _rank(L1, K)
+    _need(L2, "L2", torch.bfloat16, shape=(r, N))
+    Y = _out(Y, "Y", torch.bfloat16, (M, N), X)
+    T_out = _opt_out(T_out, "T_out", torch.bfloat16, (M, r), X)
+    ws = _workspace(int(lib().mx4_linear_fwd_workspace(M, K, N, r)), X, workspace)
+    _check("mx4_linear_fwd", lib().mx4_linear_fwd(
+        _ptr(X), M, K, N, _ptr(codes), _ptr(scales), _ptr(L1), _ptr(L2), r, float(lora_scale),
+        *_draw(p, seed, offset), _ptr(Y), _ptr(T_out), _ptr(ws), ws.numel(), _stream(stream)))
+    return Y, T_out
+
+
+def mx4_linear_bwd(X, dY, codes_t, scales_t, L1, L2, lora_scale=1.0, p=0.0, seed=0, offset=0, T=None, dX=True,
+                   dL1=None, dL2=None, workspace=None, stream=None):
+    """(dX or None, dL1 fp32 [K, r], dL2 fp32 [r, N]); codes_t and scales_t pack W [N, K] with transpose=True.
+
+    dX: True (allocated here), False/None (skipped) or a bf16 [M, K] tensor."""
+    _need(X, "X", torch.bfloat16, ndim=2)
+    M, K = X.shape
+    _need(dY, "dY", torch.bfloat16, ndim=2)
+    if dY.shape[0] != M:
+        raise ValueError(f"dY must have {M} rows, got {tuple(dY.shape)}")
+    N = dY.shape[1]
+    _mx4_packed(codes_t, scales_t, K, N)
+    r = _rank(L1, K)
+    _need(L2, "L2", torch.bfloat16, shape=(r, N))
+    if T is not None:
+        _need(T, "T", torch.bfloat16, numel=M * r)
+    dX = _opt_out(dX, "dX", torch.bfloat16, (M, K), X)
+    dL1 = _out(dL1, "dL1", torch.float32, (K, r), X)
+    dL2 = _out(dL2, "dL2", torch.float32, (r, N), X)
+    ws = _workspace(int(lib().mx4_linear_bwd_workspace(M, K, N, r)), X, workspace)
+    _check("mx4_linear_bwd", lib().mx4_linear_bwd(
+        _ptr(X), _ptr(dY), M, K, N, _ptr(codes_t), _ptr(scales_t), _ptr(L1), _ptr(L2), r, float(lora_scale),
+        *_draw(p, seed, offset), _ptr(T), _ptr(dX), _ptr(dL1), _ptr(dL2), _ptr(ws), ws.numel(), _stream(stream)))
+    return dX, dL1, dL2

@@ -71,17 +71,19 @@ __device__ __forceinline__ void stage_rows128(LDS_AS uint16_t* dst, const uint16
 // the N stored rows of W in steps of 64.  The W' tile is dequantised in its
 // stored [n][k] orientation and read transposed (ds_read_b64_tr_b16) as the
 // MFMA B operand.
+template <bool kDrop>
 __global__ __launch_bounds__(kThreads) void k_qgemm_dx(const uint16_t* __restrict__ dY, int64_t M, int64_t K,
                                                        int64_t N, const uint8_t* __restrict__ codes,
                                                        const uint8_t* __restrict__ c2,
                                                        const float* __restrict__ c1,
                                                        const uint16_t* __restrict__ G,
                                                        const uint16_t* __restrict__ L1, int r,
-                                                       uint16_t* __restrict__ dX, Nf4Params p) {
+                                                       uint16_t* __restrict__ dX, Nf4Params p, drop::Params d) {
   constexpr int kBsElems = (kBN * kPA > kBK * kPB) ? kBN * kPA : kBK * kPB;
   __shared__ __attribute__((aligned(16))) uint16_t As[kBM * kPA];
   __shared__ __attribute__((aligned(16))) uint16_t Bs[kBsElems];
   __shared__ __attribute__((aligned(16))) float qs[16];
+  __shared__ __attribute__((aligned(16))) uint8_t mask[kDrop ? kBM * drop::bit_pitch(kBN) : 16];
   const int t = threadIdx.x;
   const int w = t >> 6;
   const int wm = w & 1, wk = w >> 1;
@@ -96,7 +98,9 @@ __global__ __launch_bounds__(kThreads) void k_qgemm_dx(const uint16_t* __restric
     for (int j = 0; j < 2; ++j) acc[i][j] = f32x16{};
 
   // LoRA term: acc = G L1^T; A = G [m][c], B(c, k) = L1[k][c] staged as Bs[k][c].
+  // kDrop: acc = D o (G L1^T), the tile's decisions drawn once into LDS.
   {
+    if constexpr (kDrop) drop::fill_bits<kBM, kBN>((LDS_AS uint8_t*)mask, d, m0, k0, t, kThreads);
     stage_rows128((LDS_AS uint16_t*)As, G, r, M, r, m0, 0);
     stage_rows128((LDS_AS uint16_t*)Bs, L1, r, K, r, k0, 0);
     __syncthreads();
@@ -110,6 +114,18 @@ __global__ __launch_bounds__(kThreads) void k_qgemm_dx(const uint16_t* __restric
       acc[0][1] = qk::mfma32(a0, b1, acc[0][1]);
       acc[1][0] = qk::mfma32(a1, b0, acc[1][0]);
       acc[1][1] = qk::mfma32(a1, b1, acc[1][1]);
+    }
+    if constexpr (kDrop) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            acc[i][j][e] = drop::kept<kBN>((const LDS_AS uint8_t*)mask, 64 * wm + 32 * i + qk::acc_row(e),
+                                           64 * wk + 32 * j + qk::acc_col())
+                               ? d.scale * acc[i][j][e]
+                               : 0.0f;
     }
     __syncthreads();
   }
@@ -163,9 +179,13 @@ __global__ __launch_bounds__(kThreads) void k_qgemm_dx(const uint16_t* __restric
 
 hipError_t launch_qgemm_dx(const uint16_t* dY, int64_t M, int64_t K, int64_t N, const uint8_t* codes,
                            const uint8_t* c2, const float* c1, const uint16_t* G, const uint16_t* L1, int r,
-                           uint16_t* dX, hipStream_t s) {
+                           uint16_t* dX, hipStream_t s, const drop::Params* d) {
   dim3 grid((unsigned)((K + kBN - 1) / kBN), (unsigned)((M + kBM - 1) / kBM));
-  hipLaunchKernelGGL(k_qgemm_dx, grid, dim3(kThreads), 0, s, dY, M, K, N, codes, c2, c1, G, L1, r, dX,
-                     nf4_params());
+  if (d && d->cut)
+    hipLaunchKernelGGL(k_qgemm_dx<true>, grid, dim3(kThreads), 0, s, dY, M, K, N, codes, c2, c1, G, L1, r, dX,
+                       nf4_params(), *d);
+  else
+    hipLaunchKernelGGL(k_qgemm_dx<false>, grid, dim3(kThreads), 0, s, dY, M, K, N, codes, c2, c1, G, L1, r, dX,
+                       nf4_params(), drop::Params{});
   return hipGetLastError();
 }

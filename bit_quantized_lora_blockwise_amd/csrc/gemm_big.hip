@@ -144,7 +144,10 @@ __device__ __forceinline__ bf16x8 frag_kmajor_sw(const LDS_AS uint16_t* base, in
 // swizzle), or stage the dX weight tile [64 rows of W][256 columns] through
 // registers into a padded LDS tile that the consumers read with the transposing
 // LDS read.  No dequantisation.
-template <bool kDx, bool kTail, bool kB16 = false>
+// kDrop (dX): the adapter term is D o (G L1^T).  The producers draw the tile's
+// decisions into LDS (a bit an element) beside the LoRA operands, and the
+// consumers apply them to the accumulators before the base product.
+template <bool kDx, bool kTail, bool kB16 = false, bool kDrop = false>
 __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict__ A, int64_t M, int64_t K,
                                                      int64_t N, const uint8_t* __restrict__ codes,
                                                      const uint8_t* __restrict__ c2,
@@ -153,10 +156,11 @@ __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict_
                                                      const uint16_t* __restrict__ LB,   // L2 (fwd) / L1 (dX)
                                                      int r, float scale, uint16_t* __restrict__ C,
                                                      Nf4Params p, int nseg, int64_t seg,
-                                                     const uint16_t* __restrict__ Wb) {
+                                                     const uint16_t* __restrict__ Wb, drop::Params dp) {
   __shared__ __attribute__((aligned(16))) uint16_t lds_b[2 * kBufElems];   // weight tiles; LoRA operands first
   __shared__ __attribute__((aligned(16))) uint16_t lds_a0[kBM * kBR];      // activation tiles (two buffers,
   __shared__ __attribute__((aligned(16))) uint16_t lds_a1[kBM * kBR];      //  filled by buffer-to-LDS loads)
+  __shared__ __attribute__((aligned(16))) uint8_t mask[kDrop ? kBM * drop::bit_pitch(kBP) : 16];
   const int t = threadIdx.x;
   const int w = __builtin_amdgcn_readfirstlane(t >> 6), l = t & 63;
   const bool producer = w >= 8;           // uniform per wave
@@ -337,6 +341,7 @@ __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict_
     for (int v = vfirst; v < ntiles; v += vstride) {
     set_tile(v);
     Stage hA, hB, h0;
+    if constexpr (kDrop) drop::fill_bits<kBM, kBP>((LDS_AS uint8_t*)mask, dp, m0, p0, tp, 256);
     for (int g = 0; g < ng; ++g) {
       const int64_t gs = kDx ? g : p0 / seg;
       const uint16_t* la_src = LA + gs * M * r;
@@ -531,6 +536,18 @@ __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict_
         }
       }
     }
+    if constexpr (kDrop) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            acc[i][j][e] = drop::kept<kBP>((const LDS_AS uint8_t*)mask, 64 * rg + 32 * i + qk::acc_row(e),
+                                           128 * ch + 32 * j + (kPerm ? dx_slot_col(l & 31) : (l & 31)))
+                               ? dp.scale * acc[i][j][e]
+                               : 0.0f;
+    }
     __builtin_amdgcn_s_waitcnt(0xC07F);    // lgkmcnt(0): this wave's reads of the LoRA operands are done
     __builtin_amdgcn_s_barrier();
   }
@@ -607,20 +624,27 @@ static dim3 tile_grid(int64_t M, int64_t P) {
 
 hipError_t launch_qgemm_big(bool dx, const uint16_t* A, int64_t M, int64_t K, int64_t N, const uint8_t* codes,
                             const uint8_t* c2, const float* c1, const uint16_t* LA, const uint16_t* LB, int r,
-                            float scale, uint16_t* C, hipStream_t s, int nseg) {
+                            float scale, uint16_t* C, hipStream_t s, int nseg, const drop::Params* d) {
   const int64_t P = dx ? K : N;
   const int64_t seg = N / nseg;   // columns of W per segment (a multiple of 256 when nseg > 1)
   const dim3 grid = tile_grid(M, P);
   const uint16_t* nw = nullptr;
   if (!dx)
     hipLaunchKernelGGL((k_qgemm_big<false, false>), grid, dim3(kT), 0, s, A, M, K, N, codes, c2, c1, LA, LB, r,
-                       scale, C, nf4_params(), nseg, seg, nw);
-  else if (N % kBR == 0)
+                       scale, C, nf4_params(), nseg, seg, nw, drop::Params{});
+  else if (d && d->cut) {
+    if (N % kBR == 0)
+      hipLaunchKernelGGL((k_qgemm_big<true, false, false, true>), grid, dim3(kT), 0, s, A, M, K, N, codes, c2, c1, LA,
+                         LB, r, scale, C, nf4_params(), nseg, seg, nw, *d);
+    else
+      hipLaunchKernelGGL((k_qgemm_big<true, true, false, true>), grid, dim3(kT), 0, s, A, M, K, N, codes, c2, c1, LA,
+                         LB, r, scale, C, nf4_params(), nseg, seg, nw, *d);
+  } else if (N % kBR == 0)
     hipLaunchKernelGGL((k_qgemm_big<true, false>), grid, dim3(kT), 0, s, A, M, K, N, codes, c2, c1, LA, LB, r,
-                       scale, C, nf4_params(), nseg, seg, nw);
+                       scale, C, nf4_params(), nseg, seg, nw, drop::Params{});
   else
     hipLaunchKernelGGL((k_qgemm_big<true, true>), grid, dim3(kT), 0, s, A, M, K, N, codes, c2, c1, LA, LB, r,
-                       scale, C, nf4_params(), nseg, seg, nw);
+                       scale, C, nf4_params(), nseg, seg, nw, drop::Params{});
   return hipGetLastError();
 }
 
@@ -640,12 +664,12 @@ hipError_t launch_bgemm_big(bool dx, const uint16_t* A, int64_t M, int64_t K, in
   const float* nf = nullptr;
   if (!dx)
     hipLaunchKernelGGL((k_qgemm_big<false, false, true>), grid, dim3(kT), 0, s, A, M, K, N, nc, nc, nf, LA, LB, r,
-                       scale, C, nf4_params(), 1, N, W);
+                       scale, C, nf4_params(), 1, N, W, drop::Params{});
   else if (N % kBR == 0)
     hipLaunchKernelGGL((k_qgemm_big<true, false, true>), grid, dim3(kT), 0, s, A, M, K, N, nc, nc, nf, LA, LB, r,
-                       scale, C, nf4_params(), 1, N, W);
+                       scale, C, nf4_params(), 1, N, W, drop::Params{});
   else
     hipLaunchKernelGGL((k_qgemm_big<true, true, true>), grid, dim3(kT), 0, s, A, M, K, N, nc, nc, nf, LA, LB, r,
-                       scale, C, nf4_params(), 1, N, W);
+                       scale, C, nf4_params(), 1, N, W, drop::Params{});
   return hipGetLastError();
 }

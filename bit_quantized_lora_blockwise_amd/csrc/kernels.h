@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include "common.h"
+#include "philox.h"
 
 // Keeps a HIP error for ql_status_string and returns QL_ERR_HIP (abi.cpp).
 int ql_record_hip_error(hipError_t e);
@@ -80,6 +81,44 @@ hipError_t launch_lora_tn_pair(const uint16_t* A0, int64_t lda0, const uint16_t*
 hipError_t launch_lora_tn(const uint16_t* A, int64_t lda, const uint16_t* B, int64_t M, int64_t P, int r,
                           float scale, bool transpose_out, float* out, float* ws, hipStream_t s);
 
+// The adapter branch with dropout on its input (d.cut = 0: none) and G to 24 bits:
+//   T = bf16((D o X) L1); ws as lora_skinny_ws(M, K, r)
+//   G = scale dY L2^T as three bf16 planes [3][M, r] whose sum it is (the first one
+//     is bf16(G)); ws as lora_skinny_ws(M, N, r)
+//   dL1 [K, r] = (D o X)^T G from the planes, dL2 [r, N] = scale T^T dY, fp32; ws as
+//     lora_tn_pair_ws(M, K, N, r)
+hipError_t launch_lora_down_drop(const uint16_t* X, int64_t M, int64_t K, const uint16_t* L1, int r,
+                                 const drop::Params& d, uint16_t* T, float* ws, hipStream_t s);
+hipError_t launch_lora_grad_in3(const uint16_t* dY, int64_t M, int64_t N, const uint16_t* L2, int r, float scale,
+                                uint16_t* G, float* ws, hipStream_t s);
+hipError_t launch_lora_grads3(const uint16_t* X, int64_t K, const uint16_t* G, const drop::Params& d, float* dL1,
+                              const uint16_t* dY, int64_t N, const uint16_t* T, float scale, float* dL2, int64_t M,
+                              int r, float* ws, hipStream_t s);
+// Y = D o X, elementwise; X rows `ld` elements apart, Y dense (dropout.hip).
+hipError_t launch_dropout(const void* X, bool bf16, int64_t rows, int64_t cols, int64_t ld, const drop::Params& d,
+                          void* Y, hipStream_t s);
+
+// --- microscaled 4-bit (mx4.hip, mx4_gemm.hip) -----------------------------------
+// Quantisation along the rows of X [rows, cols] (packed rows = rows), or along its
+// columns (X [len, cols], packed rows = cols); X rows `ld` elements apart.
+hipError_t launch_mx4_quant(const void* X, bool bf16, int64_t rows, int64_t cols, int64_t ld, uint8_t* codes,
+                            uint8_t* scales, hipStream_t s);
+hipError_t launch_mx4_quant_t(const void* X, bool bf16, int64_t len, int64_t cols, int64_t ld, uint8_t* codes,
+                              uint8_t* scales, hipStream_t s);
+hipError_t launch_mx4_dequant(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, uint16_t* out,
+                              hipStream_t s);
+// C[M, P] = bf16(A B^T + the adapter term), A [M, R] and B [P, R] packed.
+struct Mx4Lora {
+  const uint16_t* A;    // [M, r]: T (forward) or G (backward); nullptr: no adapter
+  const uint16_t* B;    // forward L2 [r, P]: + scale A B; backward L1 [P, r]: + D o (A B^T)
+  int r;
+  bool bwd;
+  float scale;          // forward only
+  drop::Params d;       // backward only
+};
+hipError_t launch_mx4_gemm(const uint8_t* ac, const uint8_t* as, int64_t M, const uint8_t* bc, const uint8_t* bs,
+                           int64_t P, int64_t R, const Mx4Lora& lora, uint16_t* C, hipStream_t s);
+
 // --- adapter merge (merge.hip) ---------------------------------------------
 // W[n][k] = bf16(W'[n][k] + scale * sum_c L1[k][c] L2[c][n]), W' the bf16
 // dequantised base; W [N, K], K a multiple of 64.
@@ -130,18 +169,20 @@ hipError_t launch_qgemv_fwd_fused(const uint16_t* X, int64_t M, int64_t K, int64
 // LB = L1, C = dX).  qgemm_big_ok says whether the shapes qualify.  nseg > 1:
 // W [N, K] is nseg matrices of N / nseg rows stacked (N / nseg a multiple of
 // 256), each with its own adapter: LA holds nseg [M, r] blocks, LB nseg L2
-// [r, N / nseg] (fwd) or L1 [K, r] (dX) blocks.
+// [r, N / nseg] (fwd) or L1 [K, r] (dX) blocks.  d (dX, nseg = 1): dropout of the
+// adapter term, dX = bf16(dY W' + D o (G L1^T)).
 bool qgemm_big_ok(bool dx, int64_t M, int64_t K, int64_t N);
 hipError_t launch_qgemm_big(bool dx, const uint16_t* A, int64_t M, int64_t K, int64_t N, const uint8_t* codes,
                             const uint8_t* c2, const float* c1, const uint16_t* LA, const uint16_t* LB, int r,
-                            float scale, uint16_t* C, hipStream_t s, int nseg = 1);
+                            float scale, uint16_t* C, hipStream_t s, int nseg = 1,
+                            const drop::Params* d = nullptr);
 // The same two GEMMs with a bf16 weight W [N, K] in place of the packed one
 // (LoRA over a bf16 base): dx = false Y = bf16(X W^T + scale T L2), dx = true
 // dX = bf16(dY W + G L1^T).  bgemm_ok says whether the shapes qualify.
 bool bgemm_ok(bool dx, int64_t M, int64_t K, int64_t N);
 hipError_t launch_bgemm_big(bool dx, const uint16_t* A, int64_t M, int64_t K, int64_t N, const uint16_t* W,
                             const uint16_t* LA, const uint16_t* LB, int r, float scale, uint16_t* C, hipStream_t s);
-// dX[M, K] = bf16(dY W' + G L1^T)
+// dX[M, K] = bf16(dY W' + G L1^T), d as above
 hipError_t launch_qgemm_dx(const uint16_t* dY, int64_t M, int64_t K, int64_t N, const uint8_t* codes,
                            const uint8_t* c2, const float* c1, const uint16_t* G, const uint16_t* L1, int r,
-                           uint16_t* dX, hipStream_t s);
+                           uint16_t* dX, hipStream_t s, const drop::Params* d = nullptr);

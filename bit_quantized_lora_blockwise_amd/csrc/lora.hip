@@ -9,12 +9,16 @@
 // All four are memory-bound passes over an [M, R] bf16 activation.  Each work
 // group owns a 64-row tile of the long dimension and one slice of the
 // reduction; slices write fp32 partials that a second kernel sums in a fixed
-// order, so results are deterministic.  Within a slice the 64-wide steps are
+// order, so results are deterministic.  With dropout on the adapter's input (T and
+// dL1 of D o X) the mask of philox.h is drawn where a thread holds eight elements
+// of a row, between the load and the LDS store or the MFMA; its scale goes into
+// the sum of the slices.  Within a slice the 64-wide steps are
 // pipelined: the tiles of step st + 2 are loaded into registers while step st
 // multiplies out of one LDS buffer and step st + 1's tiles go into the other.
 #include <algorithm>
 
 #include "kernels.h"
+#include "philox.h"
 #include "tpart.h"
 
 namespace {
@@ -85,12 +89,22 @@ __device__ __forceinline__ void store_tile(const Tile& tl, LDS_AS uint16_t* dst)
   for (int i = 0; i < 2; ++i) *(LDS_AS u32x4*)(dst + ((t >> 3) + 32 * i) * kPitch + (t & 7) * 8) = tl.v[i];
 }
 
+// Zeroes the dropped elements of a tile whose element (0, 0) is (m0, k0), k0 a
+// multiple of 8.
+__device__ __forceinline__ void drop_tile(Tile& tl, const drop::Params& d, int64_t m0, int64_t k0) {
+  const int t = threadIdx.x;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    tl.v[i] = drop::mask8(tl.v[i], d, (uint32_t)(m0 + (t >> 3) + 32 * i), (uint32_t)(k0 >> 3) + (t & 7));
+}
+
 // C[M, r] partial over one reduction slice: A [M, R] (row stride lda) times B, where
 // B(k, c) = Bm[k * r + c] (kBkr, L1 [R, r]) or Bm[c * R + k] (!kBkr, L2 [r, R]).
-template <bool kBkr, bool kVecA, bool kVecB>
+// kDrop: of D o A, not scaled.
+template <bool kBkr, bool kVecA, bool kVecB, bool kDrop = false>
 __global__ __launch_bounds__(kThreads) void k_lora_skinny(const uint16_t* __restrict__ A, int64_t M, int64_t R,
                                                           int64_t lda, const uint16_t* __restrict__ Bm, int r,
-                                                          int64_t chunk, float* __restrict__ part) {
+                                                          int64_t chunk, float* __restrict__ part, drop::Params d) {
   __shared__ __attribute__((aligned(16))) uint16_t As[2][kTile * kPitch];
   __shared__ __attribute__((aligned(16))) uint16_t Bs[2][kTile * kPitch];
   const int w = threadIdx.x >> 6;
@@ -109,10 +123,11 @@ __global__ __launch_bounds__(kThreads) void k_lora_skinny(const uint16_t* __rest
     else tb = load_tile<kVecB>(Bm + k0c, R, r, kl, (uint64_t)(r * R - k0c) * 2);
   };
   f32x16 acc = {};
-  auto step = [&](int64_t st, const Tile& na, const Tile& nb, Tile& la, Tile& lb) {
+  auto step = [&](int64_t st, Tile& na, const Tile& nb, Tile& la, Tile& lb) {
     tiles(st + 2, la, lb);
     const LDS_AS uint16_t* as = (const LDS_AS uint16_t*)As[st & 1];
     const LDS_AS uint16_t* bs = (const LDS_AS uint16_t*)Bs[st & 1];
+    if constexpr (kDrop) drop_tile(na, d, m0, k_beg + (st + 1) * kTile);
     if (wc * 32 < r) {
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
@@ -128,6 +143,7 @@ __global__ __launch_bounds__(kThreads) void k_lora_skinny(const uint16_t* __rest
   Tile a0, b0, aA, bA, aB, bB;
   tiles(0, a0, b0);
   tiles(1, aA, bA);
+  if constexpr (kDrop) drop_tile(a0, d, m0, k_beg);
   store_tile(a0, (LDS_AS uint16_t*)As[0]);
   store_tile(b0, (LDS_AS uint16_t*)Bs[0]);
   __syncthreads();
@@ -163,11 +179,12 @@ constexpr int kSkPhases = 4;                       // steps taken in turn
 constexpr int kSkThreads = 64 * kSkGroups * kSkPhases;
 constexpr int kSkDepth = 4;                        // groups of A and B in flight
 
-template <bool kBkr>
+template <bool kBkr, bool kDrop = false>
 __global__ __launch_bounds__(kSkThreads, 1) void k_lora_skinny_stream(const uint16_t* __restrict__ A, int64_t M,
                                                                      int64_t R, int64_t lda,
                                                                      const uint16_t* __restrict__ Bm, int r,
-                                                                     int64_t chunk, float* __restrict__ part) {
+                                                                     int64_t chunk, float* __restrict__ part,
+                                                                     drop::Params d) {
   __shared__ __attribute__((aligned(16))) uint16_t Bs[2][kSkPhases][kTile * kPitch];
   const int t = threadIdx.x;
   const int w = __builtin_amdgcn_readfirstlane(t >> 6), l = t & 63;
@@ -259,6 +276,10 @@ __global__ __launch_bounds__(kSkThreads, 1) void k_lora_skinny_stream(const uint
     const LDS_AS uint16_t* bs = (const LDS_AS uint16_t*)Bs[gi & 1][ph];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
+      if constexpr (kDrop) {
+        const int64_t k = k_beg + (int64_t)(kSkPhases * gi + ph) * kTile + 32 * u + akq;
+        av[u] = drop::mask8(av[u], d, (uint32_t)arow, (uint32_t)(k >> 3));
+      }
       const bf16x8 x = __builtin_bit_cast(bf16x8, av[u]);
 #pragma unroll
       for (int j = 0; j < 4; ++j)
@@ -338,49 +359,81 @@ __global__ __launch_bounds__(kThreads) void k_skinny_reduce(const float* __restr
   }
 }
 
+// The same sum kept to 24 bits as three bf16 planes out[i], out[n + i], out[2 n + i]
+// whose sum it is: each plane takes what the ones before it rounded off (exact in
+// fp32), so a product with the planes loses nothing that fp32 would keep, while
+// the first plane alone is the bf16 rounding.
+__global__ __launch_bounds__(kThreads) void k_skinny_reduce3(const float* __restrict__ part, int splits, int64_t n,
+                                                             float scale, uint16_t* __restrict__ out) {
+  const int64_t stride = (int64_t)gridDim.x * kThreads;
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += stride) {
+    float s = 0.0f;
+    for (int k = 0; k < splits; ++k) s += part[k * n + i];
+    float x = scale * s;
+#pragma unroll
+    for (int j = 0; j < 3; ++j) {
+      const uint16_t h = qk::f32_to_bf16(x);
+      out[j * n + i] = h;
+      x -= qk::bf16_to_f32(h);
+    }
+  }
+}
+
 // C[p, c] partial over one slice of m: sum_m A[m][p] * B[m][c], A [M, P], B [M, r];
-// this work group's tile of 64 p is `tile`, its slice of m is `split`.
-template <bool kVecA, bool kVecB>
+// this work group's tile of 64 p is `tile`, its slice of m is `split`.  kDrop: of
+// D o A, not scaled.  kPlanes: B is the sum of that many matrices, B + j M r.
+// lds: (2 + 2 kPlanes) tiles of kTile * kPitch.
+template <bool kVecA, bool kVecB, bool kDrop = false, int kPlanes = 1>
 __device__ __forceinline__ void tn_tile(const uint16_t* __restrict__ A, int64_t lda, const uint16_t* __restrict__ B,
                                         int64_t M, int64_t P, int r, int64_t chunk, float* __restrict__ part,
-                                        int tile, int split) {
-  __shared__ __attribute__((aligned(16))) uint16_t As[2][kTile * kPitch];
-  __shared__ __attribute__((aligned(16))) uint16_t Bs[2][kTile * kPitch];
+                                        int tile, int split, uint16_t* lds, const drop::Params& d) {
+  LDS_AS uint16_t* const sm = (LDS_AS uint16_t*)lds;
+  auto abuf = [&](int64_t b) { return sm + (b & 1) * kTile * kPitch; };
+  auto bbuf = [&](int64_t b, int j) { return sm + (2 + kPlanes * (b & 1) + j) * kTile * kPitch; };
+  struct BTiles {
+    Tile p[kPlanes];
+  };
   const int w = threadIdx.x >> 6;
   const int wp = w & 1, wc = w >> 1;
   const int64_t p0 = (int64_t)tile * kTile;
   const int64_t m_beg = split * chunk;
   const int64_t m_end = min(M, m_beg + chunk);
   const int64_t nsteps = (m_end - m_beg + kTile - 1) / kTile;
-  auto tiles = [&](int64_t st, Tile& ta, Tile& tb) {
+  auto tiles = [&](int64_t st, Tile& ta, BTiles& tb) {
     const int64_t mm = m_beg + st * kTile;
     const int64_t ml = m_end - mm;                     // rows of the slice left (<= 0: zeros)
     const int64_t mmc = ml > 0 ? mm : 0;
     ta = load_tile<kVecA>(A + mmc * lda + p0, lda, ml, P - p0, (uint64_t)((M - mmc) * lda - p0) * 2);   // [m][p]
-    tb = load_tile<kVecB>(B + mmc * r, r, ml, r, (uint64_t)((M - mmc) * r) * 2);                // [m][c]
+#pragma unroll
+    for (int j = 0; j < kPlanes; ++j)
+      tb.p[j] = load_tile<kVecB>(B + (j * M + mmc) * r, r, ml, r, (uint64_t)((M - mmc) * r) * 2);       // [m][c]
+  };
+  auto store = [&](int64_t st, Tile& ta, const BTiles& tb) {
+    if constexpr (kDrop) drop_tile(ta, d, m_beg + st * kTile, p0);
+    store_tile(ta, abuf(st));
+#pragma unroll
+    for (int j = 0; j < kPlanes; ++j) store_tile(tb.p[j], bbuf(st, j));
   };
   f32x16 acc = {};
-  auto step = [&](int64_t st, const Tile& na, const Tile& nb, Tile& la, Tile& lb) {
+  auto step = [&](int64_t st, Tile& na, const BTiles& nb, Tile& la, BTiles& lb) {
     tiles(st + 2, la, lb);
-    const LDS_AS uint16_t* as = (const LDS_AS uint16_t*)As[st & 1];
-    const LDS_AS uint16_t* bs = (const LDS_AS uint16_t*)Bs[st & 1];
     if (wc * 32 < r) {
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
-        bf16x8 a = qk::frag_kmajor(as, kPitch, 16 * s, 32 * wp);
-        bf16x8 b = qk::frag_kmajor(bs, kPitch, 16 * s, 32 * wc);
-        acc = qk::mfma32(a, b, acc);
+        bf16x8 a = qk::frag_kmajor(abuf(st), kPitch, 16 * s, 32 * wp);
+#pragma unroll
+        for (int j = 0; j < kPlanes; ++j)
+          acc = qk::mfma32(a, qk::frag_kmajor(bbuf(st, j), kPitch, 16 * s, 32 * wc), acc);
       }
     }
-    store_tile(na, (LDS_AS uint16_t*)As[(st + 1) & 1]);
-    store_tile(nb, (LDS_AS uint16_t*)Bs[(st + 1) & 1]);
+    store(st + 1, na, nb);
     __syncthreads();
   };
-  Tile a0, b0, aA, bA, aB, bB;
+  Tile a0, aA, aB;
+  BTiles b0, bA, bB;
   tiles(0, a0, b0);
   tiles(1, aA, bA);
-  store_tile(a0, (LDS_AS uint16_t*)As[0]);
-  store_tile(b0, (LDS_AS uint16_t*)Bs[0]);
+  store(0, a0, b0);
   __syncthreads();
   for (int64_t st = 0; st < nsteps; st += 2) {
     step(st, aA, bA, aB, bB);
@@ -400,7 +453,8 @@ template <bool kVecA, bool kVecB>
 __global__ __launch_bounds__(kThreads) void k_lora_tn(const uint16_t* __restrict__ A, int64_t lda,
                                                       const uint16_t* __restrict__ B, int64_t M, int64_t P, int r,
                                                       int64_t chunk, float* __restrict__ part) {
-  tn_tile<kVecA, kVecB>(A, lda, B, M, P, r, chunk, part, blockIdx.x, blockIdx.y);
+  __shared__ __attribute__((aligned(16))) uint16_t lds[4 * kTile * kPitch];
+  tn_tile<kVecA, kVecB>(A, lda, B, M, P, r, chunk, part, blockIdx.x, blockIdx.y, lds, drop::Params{});
 }
 
 // Two independent products of this kind in one launch (the backward's dL1 and
@@ -420,7 +474,21 @@ __global__ __launch_bounds__(kThreads) void k_lora_tn_pair(TnJob j0, TnJob j1, i
   const bool second = (int)blockIdx.x >= n0;         // uniform over the work group
   const TnJob j = second ? j1 : j0;
   const int b = second ? (int)blockIdx.x - n0 : (int)blockIdx.x;
-  tn_tile<kVecA, kVecB>(j.A, j.lda, j.B, M, j.P, r, j.chunk, j.part, b % j.tiles, b / j.tiles);
+  __shared__ __attribute__((aligned(16))) uint16_t lds[4 * kTile * kPitch];
+  tn_tile<kVecA, kVecB>(j.A, j.lda, j.B, M, j.P, r, j.chunk, j.part, b % j.tiles, b / j.tiles, lds, drop::Params{});
+}
+
+// The pair with dropout on the first product's A and its B in three planes.
+template <bool kVec, bool kDrop>
+__global__ __launch_bounds__(kThreads) void k_lora_tn_pair3(TnJob j0, TnJob j1, int64_t M, int r, drop::Params d) {
+  __shared__ __attribute__((aligned(16))) uint16_t lds[8 * kTile * kPitch];
+  const int n0 = j0.tiles * j0.splits;
+  const int b = (int)blockIdx.x;
+  if (b < n0)
+    tn_tile<kVec, kVec, kDrop, 3>(j0.A, j0.lda, j0.B, M, j0.P, r, j0.chunk, j0.part, b % j0.tiles, b / j0.tiles, lds, d);
+  else
+    tn_tile<kVec, kVec>(j1.A, j1.lda, j1.B, M, j1.P, r, j1.chunk, j1.part, (b - n0) % j1.tiles, (b - n0) / j1.tiles,
+                        lds, d);
 }
 
 // out[i] = scale * (sum of the slices), i over P * r, by work groups blk of nblk.
@@ -613,9 +681,11 @@ hipError_t launch_lora_skinny(const uint16_t* A, int64_t M, int64_t R, int64_t l
     const SplitPlan sp = plan_stream(tiles, R);
     dim3 grid((unsigned)tiles, (unsigned)sp.splits);
     if (b_is_kr)
-      hipLaunchKernelGGL((k_lora_skinny_stream<true>), grid, dim3(kSkThreads), 0, s, A, M, R, lda, B, r, sp.chunk, ws);
+      hipLaunchKernelGGL((k_lora_skinny_stream<true>), grid, dim3(kSkThreads), 0, s, A, M, R, lda, B, r, sp.chunk, ws,
+                         drop::Params{});
     else
-      hipLaunchKernelGGL((k_lora_skinny_stream<false>), grid, dim3(kSkThreads), 0, s, A, M, R, lda, B, r, sp.chunk, ws);
+      hipLaunchKernelGGL((k_lora_skinny_stream<false>), grid, dim3(kSkThreads), 0, s, A, M, R, lda, B, r, sp.chunk, ws,
+                         drop::Params{});
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(k_skinny_reduce, dim3(grid_for((M * r + 3) / 4)), dim3(kThreads), 0, s, ws, sp.splits,
@@ -627,7 +697,8 @@ hipError_t launch_lora_skinny(const uint16_t* A, int64_t M, int64_t R, int64_t l
   const bool avec = (R % 8) == 0 && (lda % 8) == 0 && ((uintptr_t)A & 15) == 0;
   const bool bvec = (b_is_kr ? (r % 8) == 0 : (R % 8) == 0) && ((uintptr_t)B & 15) == 0;
 #define QL_SKINNY(BKR, VA, VB)                                                                                \
-  hipLaunchKernelGGL((k_lora_skinny<BKR, VA, VB>), grid, dim3(kThreads), 0, s, A, M, R, lda, B, r, sp.chunk, ws)
+  hipLaunchKernelGGL((k_lora_skinny<BKR, VA, VB>), grid, dim3(kThreads), 0, s, A, M, R, lda, B, r, sp.chunk, ws, \
+                     drop::Params{})
   if (b_is_kr) {
     if (avec && bvec) QL_SKINNY(true, true, true);
     else if (avec) QL_SKINNY(true, true, false);
@@ -705,5 +776,85 @@ hipError_t launch_lora_tn(const uint16_t* A, int64_t lda, const uint16_t* B, int
   else
     hipLaunchKernelGGL(k_tn_reduce, dim3(grid_for((P * r + 3) / 4)), dim3(kThreads), 0, s, ws, sp.splits, P, r, scale,
                        out);
+  return hipGetLastError();
+}
+
+// ---- with dropout, and with G kept to 24 bits ---------------------------------
+hipError_t launch_lora_down_drop(const uint16_t* X, int64_t M, int64_t K, const uint16_t* L1, int r,
+                                 const drop::Params& d, uint16_t* T, float* ws, hipStream_t s) {
+  if (d.cut == 0) return launch_lora_skinny(X, M, K, K, L1, true, r, 1.0f, T, ws, s);
+  const int64_t tiles = (M + kTile - 1) / kTile;
+  SplitPlan sp;
+  if (skinny_stream_ok(X, M, K, K, L1, r)) {
+    sp = plan_stream(tiles, K);
+    hipLaunchKernelGGL((k_lora_skinny_stream<true, true>), dim3((unsigned)tiles, (unsigned)sp.splits), dim3(kSkThreads),
+                       0, s, X, M, K, K, L1, r, sp.chunk, ws, d);
+  } else {
+    sp = plan_rowsplit(tiles, K);
+    const dim3 grid((unsigned)tiles, (unsigned)sp.splits);
+    if ((K % 8) == 0)
+      hipLaunchKernelGGL((k_lora_skinny<true, true, false, true>), grid, dim3(kThreads), 0, s, X, M, K, K, L1, r,
+                         sp.chunk, ws, d);
+    else
+      hipLaunchKernelGGL((k_lora_skinny<true, false, false, true>), grid, dim3(kThreads), 0, s, X, M, K, K, L1, r,
+                         sp.chunk, ws, d);
+  }
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(k_skinny_reduce, dim3(grid_for((M * r + 3) / 4)), dim3(kThreads), 0, s, ws, sp.splits,
+                     M * (int64_t)r, d.scale, T);
+  return hipGetLastError();
+}
+
+hipError_t launch_lora_grad_in3(const uint16_t* dY, int64_t M, int64_t N, const uint16_t* L2, int r, float scale,
+                                uint16_t* G, float* ws, hipStream_t s) {
+  const int64_t tiles = (M + kTile - 1) / kTile;
+  SplitPlan sp;
+  if (skinny_stream_ok(dY, M, N, N, L2, r)) {
+    sp = plan_stream(tiles, N);
+    hipLaunchKernelGGL((k_lora_skinny_stream<false>), dim3((unsigned)tiles, (unsigned)sp.splits), dim3(kSkThreads), 0, s,
+                       dY, M, N, N, L2, r, sp.chunk, ws, drop::Params{});
+  } else {
+    sp = plan_rowsplit(tiles, N);
+    const dim3 grid((unsigned)tiles, (unsigned)sp.splits);
+    if ((N % 8) == 0)
+      hipLaunchKernelGGL((k_lora_skinny<false, true, true>), grid, dim3(kThreads), 0, s, dY, M, N, N, L2, r, sp.chunk,
+                         ws, drop::Params{});
+    else
+      hipLaunchKernelGGL((k_lora_skinny<false, false, false>), grid, dim3(kThreads), 0, s, dY, M, N, N, L2, r, sp.chunk,
+                         ws, drop::Params{});
+  }
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(k_skinny_reduce3, dim3(grid_for(M * r)), dim3(kThreads), 0, s, ws, sp.splits, M * (int64_t)r,
+                     scale, G);
+  return hipGetLastError();
+}
+
+hipError_t launch_lora_grads3(const uint16_t* X, int64_t K, const uint16_t* G, const drop::Params& d, float* dL1,
+                              const uint16_t* dY, int64_t N, const uint16_t* T, float scale, float* dL2, int64_t M,
+                              int r, float* ws, hipStream_t s) {
+  const bool vec = (K % 8) == 0 && (N % 8) == 0 && (r % 8) == 0;
+  float* part1 = ws + (lora_tn_ws(M, K, r) + 255) / 256 * 256 / sizeof(float);
+  const SplitPlan sp0 = plan_rowsplit((K + kTile - 1) / kTile, M);
+  const SplitPlan sp1 = plan_rowsplit((N + kTile - 1) / kTile, M);
+  const TnJob j0{X, K, G, K, sp0.chunk, ws, (int)((K + kTile - 1) / kTile), sp0.splits};
+  const TnJob j1{dY, N, T, N, sp1.chunk, part1, (int)((N + kTile - 1) / kTile), sp1.splits};
+  const unsigned nwg = (unsigned)(j0.tiles * j0.splits + j1.tiles * j1.splits);
+#define QL_TN3(V, D) hipLaunchKernelGGL((k_lora_tn_pair3<V, D>), dim3(nwg), dim3(kThreads), 0, s, j0, j1, M, r, d)
+  if (vec) {
+    if (d.cut) QL_TN3(true, true);
+    else QL_TN3(true, false);
+  } else {
+    if (d.cut) QL_TN3(false, true);
+    else QL_TN3(false, false);
+  }
+#undef QL_TN3
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int nb0 = grid_for((K * r + 3) / 4);
+  const unsigned nb1 = (unsigned)((N + kTrP - 1) / kTrP);
+  hipLaunchKernelGGL(k_tn_reduce_pair, dim3((unsigned)nb0 + nb1), dim3(kThreads), 0, s, ws, sp0.splits, K, d.scale, dL1,
+                     nb0, part1, sp1.splits, N, scale, dL2, r);
   return hipGetLastError();
 }

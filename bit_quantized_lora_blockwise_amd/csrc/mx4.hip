@@ -1,0 +1,259 @@
+// Quantisation to microscaled 4-bit (layout and rule: mx4.h) along the rows or the
+// columns of a matrix, and back.  Memory-bound: 2 (bf16) or 4 (fp32) bytes read
+// and 17/32 byte written per element.
+#include "mx4.h"
+
+#include "kernels.h"
+
+namespace {
+
+using namespace mx4;
+
+constexpr int kThreads = 256;
+
+
+// Largest of the four lanes of a quad.
+__device__ __forceinline__ uint32_t quad_max(uint32_t v) {
+  v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, true));   // quad_perm [1,0,3,2]
+  return max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, true)); // quad_perm [2,3,0,1]
+}
+
+// Or over the 16 lanes of a DPP row of values that are equal within quads.
+__device__ __forceinline__ uint32_t row_or(uint32_t v) {
+  v |= (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x124, 0xF, 0xF, true);   // row_ror:4
+  return v | (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x128, 0xF, 0xF, true);   // row_ror:8
+}
+
+// Along the rows: 16 lanes take 128 elements of a row (a quad one block, a lane
+// eight elements), a wave four rows at a time and kRows / 4 such groups with all
+// their loads in flight: 256 contiguous bytes read per row, 64 written per block
+// position and group.
+constexpr int kRows = 16;
+
+template <bool kBf16, bool kVec>
+__global__ __launch_bounds__(kThreads) void k_mx4_quant(const void* __restrict__ X, int64_t rows, int64_t cols,
+                                                        int64_t ld, int64_t words, uint32_t* __restrict__ codes,
+                                                        uint32_t* __restrict__ scales) {
+  const int l = threadIdx.x & 63, part = l & 15, rl = l >> 4;
+  const int64_t tiles = (rows + kRows - 1) / kRows * words;
+  const int64_t stride = (int64_t)gridDim.x * (kThreads / 64);
+  for (int64_t tile = (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6); tile < tiles; tile += stride) {
+    const int64_t rt = tile / words, w = tile - rt * words;      // row tile, 128-element piece
+    const int64_t col = 128 * w + 8 * part;
+    u32x4 v[kRows / 4];
+    float f[kRows / 4][8];
+#pragma unroll
+    for (int i = 0; i < kRows / 4; ++i) {
+      const int64_t row = kRows * rt + 4 * i + rl;
+      const bool in = row < rows && col < cols;
+      if constexpr (kBf16) {
+        const uint16_t* p = (const uint16_t*)X + row * ld + col;
+        v[i] = u32x4{0, 0, 0, 0};
+        if (kVec) {
+          if (in) v[i] = *(const u32x4*)p;
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (in && col + j < cols) v[i][j >> 1] |= (uint32_t)p[j] << (16 * (j & 1));
+        }
+      } else {
+        const float* p = (const float*)X + row * ld + col;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[i][j] = 0.0f;
+        if (kVec) {
+          if (in) {
+            *(f32x4*)f[i] = *(const f32x4*)p;
+            *(f32x4*)(f[i] + 4) = *(const f32x4*)(p + 4);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (in && col + j < cols) f[i][j] = p[j];
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kRows / 4; ++i) {
+      const int64_t row = kRows * rt + 4 * i + rl;
+      uint32_t top = 0;
+      if constexpr (kBf16) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) top = max(top, max((v[i][j] << 16) & 0x7FFFFFFFu, v[i][j] & 0x7FFF0000u));
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(f[i][j]) & 0x7FFFFFFFu);
+      }
+      const uint32_t sb = scale_byte(quad_max(top));
+      uint32_t c;
+      if constexpr (kBf16) c = encode8(v[i], scale_f32(sb));
+      else c = encode8(f[i], scale_f32(sb));
+      if (sb == 255u) c = 0;
+      const uint32_t word = row_or(sb << (8 * (part >> 2)));
+      if (row < rows) {
+        codes[((4 * w + (part >> 2)) * rows + row) * 4 + (part & 3)] = c;
+        if (part == 0) scales[w * rows + row] = word;
+      }
+    }
+  }
+}
+
+// Along the columns: the packed rows are the columns of X [len, cols].  A work
+// group takes 128 columns and 128 rows, wave w its rows 32 w .. +31 (one block of
+// each column), a lane two columns: no exchange between lanes, 256 contiguous
+// bytes read per row (bf16), 32 written per lane.  The four waves' scale bytes
+// meet in LDS.
+template <bool kBf16, bool kVec>
+__global__ __launch_bounds__(kThreads) void k_mx4_quant_t(const void* __restrict__ X, int64_t len, int64_t cols,
+                                                          int64_t ld, u32x4* __restrict__ codes,
+                                                          uint32_t* __restrict__ scales) {
+  __shared__ uint8_t sbytes[128][4];
+  const int l = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  const int64_t ctiles = (cols + 127) / 128;
+  const int64_t ct = blockIdx.x % ctiles, word = blockIdx.x / ctiles;
+  const int64_t c0 = 128 * ct + 2 * l, r0 = 128 * word + 32 * wv;
+  float x[2][32];
+  if constexpr (kBf16) {
+    uint32_t d[32];
+#pragma unroll
+    for (int k = 0; k < 32; ++k) {
+      const uint16_t* p = (const uint16_t*)X + (r0 + k) * ld + c0;
+      d[k] = 0;
+      if (r0 + k < len) {
+        if (kVec) {
+          if (c0 < cols) d[k] = *(const uint32_t*)p;
+        } else {
+          if (c0 < cols) d[k] = p[0];
+          if (c0 + 1 < cols) d[k] |= (uint32_t)p[1] << 16;
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 32; ++k) {
+      x[0][k] = __uint_as_float(d[k] << 16);
+      x[1][k] = __uint_as_float(d[k] & 0xFFFF0000u);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 32; ++k) {
+      const float* p = (const float*)X + (r0 + k) * ld + c0;
+      x[0][k] = x[1][k] = 0.0f;
+      if (r0 + k < len) {
+        if (c0 < cols) x[0][k] = p[0];
+        if (c0 + 1 < cols) x[1][k] = p[1];
+      }
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int k = 0; k < 32; ++k) top = max(top, __float_as_uint(x[c][k]) & 0x7FFFFFFFu);
+    const uint32_t sb = scale_byte(top);
+    const float s = scale_f32(sb);
+    u32x4 o;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const float e[8] = {x[c][8 * g], x[c][8 * g + 1], x[c][8 * g + 2], x[c][8 * g + 3],
+                          x[c][8 * g + 4], x[c][8 * g + 5], x[c][8 * g + 6], x[c][8 * g + 7]};
+      o[g] = sb == 255u ? 0u : encode8(e, s);
+    }
+    if (c0 + c < cols) codes[(4 * word + wv) * cols + c0 + c] = o;
+    sbytes[2 * l + c][wv] = (uint8_t)sb;
+  }
+  __syncthreads();
+  if (threadIdx.x < 128 && 128 * ct + threadIdx.x < cols)
+    scales[word * cols + 128 * ct + threadIdx.x] = *(const uint32_t*)sbytes[threadIdx.x];
+}
+
+// Packed -> bf16 [rows, cols], the lanes as in k_mx4_quant.
+template <bool kVec>
+__global__ __launch_bounds__(kThreads) void k_mx4_dequant(const uint32_t* __restrict__ codes,
+                                                          const uint32_t* __restrict__ scales, int64_t rows,
+                                                          int64_t cols, int64_t words, uint16_t* __restrict__ out) {
+  const int l = threadIdx.x & 63, part = l & 15, rl = l >> 4;
+  const int64_t tiles = (rows + kRows - 1) / kRows * words;
+  const int64_t stride = (int64_t)gridDim.x * (kThreads / 64);
+  for (int64_t tile = (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6); tile < tiles; tile += stride) {
+    const int64_t rt = tile / words, w = tile - rt * words;
+    const int64_t col = 128 * w + 8 * part;
+    uint32_t c[kRows / 4], sw[kRows / 4];
+#pragma unroll
+    for (int i = 0; i < kRows / 4; ++i) {
+      const int64_t row = kRows * rt + 4 * i + rl;
+      const bool in = row < rows;
+      c[i] = in ? codes[((4 * w + (part >> 2)) * rows + row) * 4 + (part & 3)] : 0u;
+      sw[i] = in ? scales[w * rows + row] : 0u;
+    }
+#pragma unroll
+    for (int i = 0; i < kRows / 4; ++i) {
+      const int64_t row = kRows * rt + 4 * i + rl;
+      const uint32_t sb = (sw[i] >> (8 * (part >> 2))) & 255u;
+      u32x4 v = decode8(c[i], scale_f32(sb));
+      if (sb == 255u) v = u32x4{0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u};
+      if (row >= rows) continue;
+      uint16_t* p = out + row * cols + col;
+      if (kVec) {
+        if (col < cols) *(u32x4*)p = v;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (col + j < cols) p[j] = (uint16_t)(v[j >> 1] >> (16 * (j & 1)));
+      }
+    }
+  }
+}
+
+unsigned tile_grid(int64_t rows, int64_t words) {
+  const int64_t tiles = (rows + kRows - 1) / kRows * words;
+  const int64_t g = (tiles + kThreads / 64 - 1) / (kThreads / 64);
+  return (unsigned)(g > 65536 ? 65536 : g);
+}
+
+}  // namespace
+
+hipError_t launch_mx4_quant(const void* X, bool bf16, int64_t rows, int64_t cols, int64_t ld, uint8_t* codes,
+                            uint8_t* scales, hipStream_t s) {
+  const int64_t words = padded(cols) / kPad;
+  const bool vec = (cols % 8) == 0 && (ld % 8) == 0;
+#define QL_Q(B, V)                                                                                             \
+  hipLaunchKernelGGL((k_mx4_quant<B, V>), dim3(tile_grid(rows, words)), dim3(kThreads), 0, s, X, rows, cols, ld, \
+                     words, (uint32_t*)codes, (uint32_t*)scales)
+  if (bf16) {
+    if (vec) QL_Q(true, true);
+    else QL_Q(true, false);
+  } else {
+    if (vec) QL_Q(false, true);
+    else QL_Q(false, false);
+  }
+#undef QL_Q
+  return hipGetLastError();
+}
+
+hipError_t launch_mx4_quant_t(const void* X, bool bf16, int64_t len, int64_t cols, int64_t ld, uint8_t* codes,
+                              uint8_t* scales, hipStream_t s) {
+  const unsigned grid = (unsigned)((cols + 127) / 128 * (padded(len) / kPad));
+  const bool vec = (cols % 2) == 0 && (ld % 2) == 0;
+#define QL_QT(B, V)                                                                                            \
+  hipLaunchKernelGGL((k_mx4_quant_t<B, V>), dim3(grid), dim3(kThreads), 0, s, X, len, cols, ld, (u32x4*)codes, \
+                     (uint32_t*)scales)
+  if (bf16) {
+    if (vec) QL_QT(true, true);
+    else QL_QT(true, false);
+  } else {
+    QL_QT(false, false);
+  }
+#undef QL_QT
+  return hipGetLastError();
+}
+
+hipError_t launch_mx4_dequant(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, uint16_t* out,
+                              hipStream_t s) {
+  const int64_t words = padded(cols) / kPad;
+  if ((cols % 8) == 0)
+    hipLaunchKernelGGL((k_mx4_dequant<true>), dim3(tile_grid(rows, words)), dim3(kThreads), 0, s,
+                       (const uint32_t*)codes, (const uint32_t*)scales, rows, cols, words, out);
+  else
+    hipLaunchKernelGGL((k_mx4_dequant<false>), dim3(tile_grid(rows, words)), dim3(kThreads), 0, s,
+                       (const uint32_t*)codes, (const uint32_t*)scales, rows, cols, words, out);
+  return hipGetLastError();
+}

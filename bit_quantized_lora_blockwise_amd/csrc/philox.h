@@ -1,0 +1,90 @@
+// Dropout mask of an adapter's input from a counter-based generator: element
+// (m, k) is kept when the 16-bit number drawn for it is at least `cut`.  Nothing
+// of the mask is stored: forward and backward draw the same numbers again.
+//
+// Generator: Philox4x32 (J. Salmon, M. Moraes, R. Dror, D. Shaw, "Parallel random
+// numbers: as easy as 1, 2, 3", SC 2011) with seven rounds, the fewest for which
+// the paper reports that it passes BigCrush.  Counter (k / 8, m, offset low,
+// offset high), key (seed low, seed high); element k takes half k % 2 (low half
+// first) of output word (k % 8) / 2, so one call decides the eight elements that
+// a 16-byte load of bf16 brings.  32-bit products run at a quarter of the VALU
+// rate, which makes the seven rounds about 340 cycles a wave; 16 bits a decision
+// rather than 32 halve that, and leave p a step of 2^-16.
+#pragma once
+
+#include "common.h"
+
+namespace drop {
+
+// cut = 0: nothing is dropped and nothing is drawn.
+struct Params {
+  uint32_t k0, k1;      // key
+  uint32_t o0, o1;      // offset
+  uint32_t cut;         // round(65536 p), below 65536
+  float scale;          // 65536 / (65536 - cut)
+};
+
+__device__ __forceinline__ u32x4 philox7(uint32_t c0, uint32_t c1, uint32_t c2, uint32_t c3, uint32_t k0,
+                                         uint32_t k1) {
+#pragma unroll
+  for (int n = 0; n < 7; ++n) {
+    const uint64_t a = (uint64_t)c0 * 0xD2511F53u, b = (uint64_t)c2 * 0xCD9E8D57u;
+    c0 = (uint32_t)(b >> 32) ^ c1 ^ k0;
+    c2 = (uint32_t)(a >> 32) ^ c3 ^ k1;
+    c1 = (uint32_t)b;
+    c3 = (uint32_t)a;
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+  return u32x4{c0, c1, c2, c3};
+}
+
+// The numbers of elements (m, 8 q) .. (m, 8 q + 7).
+__device__ __forceinline__ u32x4 draw8(const Params& d, uint32_t m, uint32_t q) {
+  return philox7(q, m, d.o0, d.o1, d.k0, d.k1);
+}
+
+// 0xFFFF in each half of a word whose number keeps its element, else 0.
+__device__ __forceinline__ uint32_t keep2(uint32_t u, uint32_t cut) {
+  return ((u & 0xFFFFu) >= cut ? 0xFFFFu : 0u) | (u >= (cut << 16) ? 0xFFFF0000u : 0u);
+}
+
+// Eight bf16 of row m from column 8 q with the dropped ones zeroed (not scaled).
+__device__ __forceinline__ u32x4 mask8(u32x4 v, const Params& d, uint32_t m, uint32_t q) {
+  const u32x4 u = draw8(d, m, q);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] &= keep2(u[j], d.cut);
+  return v;
+}
+
+// The same eight decisions as bits 0 .. 7.
+__device__ __forceinline__ uint32_t bits8(const Params& d, uint32_t m, uint32_t q) {
+  const u32x4 u = draw8(d, m, q);
+  uint32_t b = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    b |= ((u[j] & 0xFFFFu) >= d.cut ? 1u << (2 * j) : 0u) | (u[j] >= (d.cut << 16) ? 2u << (2 * j) : 0u);
+  return b;
+}
+
+// A tile's decisions in LDS, a bit an element: row i at byte i * bit_pitch(cols),
+// column c in bit c % 8 of byte c / 8.  One word of padding a row keeps rows that
+// lanes read together on different banks.
+__host__ __device__ constexpr int bit_pitch(int cols) { return cols / 8 + 4; }
+
+// Decisions of elements (m0 + i, k0 + c) of a kRows x kCols tile (k0 % 8 == 0), by
+// threads t of n.
+template <int kRows, int kCols>
+__device__ __forceinline__ void fill_bits(LDS_AS uint8_t* lds, const Params& d, int64_t m0, int64_t k0, int t, int n) {
+  for (int i = t; i < kRows * (kCols / 8); i += n) {
+    const int row = i / (kCols / 8), q = i % (kCols / 8);
+    lds[row * bit_pitch(kCols) + q] = (uint8_t)bits8(d, (uint32_t)(m0 + row), (uint32_t)(k0 >> 3) + q);
+  }
+}
+
+template <int kCols>
+__device__ __forceinline__ bool kept(const LDS_AS uint8_t* lds, int row, int col) {
+  return (lds[row * bit_pitch(kCols) + (col >> 3)] >> (col & 7)) & 1;
+}
+
+}  // namespace drop

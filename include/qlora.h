@@ -353,6 +353,103 @@ int lora_linear_fwd_t(const uint16_t* X, int64_t M, int64_t K, int64_t N, const 
 int lora_linear_dx(const uint16_t* dY, int64_t M, int64_t K, int64_t N, const uint16_t* W,
                    const uint16_t* G, const uint16_t* L1, int r, uint16_t* dX, void* stream);
 
+/* Dropout on the adapter's input. D o X keeps element (m, k) of a matrix when the
+ * 16-bit number drawn for it is at least cut = round(65536 p) and multiplies it
+ * by 65536 / (65536 - cut), so that its expectation is X; dropped elements are 0
+ * whatever they hold. The numbers come from a counter-based generator and nothing
+ * of the mask is stored: element (m, k) takes half k % 2 (low half first) of word
+ * (k % 8) / 2 of Philox4x32 with 7 rounds, counter (k / 8, m, offset low 32 bits,
+ * offset high), key (seed low, seed high). The same p, seed and offset give the
+ * same mask in every call; a caller uses an offset of its own for each step and
+ * layer. 0 <= p < 1 (QL_ERR_VALUE otherwise; p = 0 is no dropout).
+ *
+ * lora_dropout: Y = D o X, elementwise, for X [rows, cols] with rows `ld` elements
+ * apart (fp32 or bf16 per x_dtype; rounded once to that type), Y dense. D o is
+ * its own transpose: the same call is its backward.                             */
+int lora_dropout(const void* X, int x_dtype, int64_t rows, int64_t cols, int64_t ld, double p, uint64_t seed,
+                 uint64_t offset, void* Y, void* stream);
+
+/* The quantised LoRA linear with dropout on the adapter's input:
+ *   T   = bf16((D o X) L1),  Y = bf16(X W'^T + lora_scale * (T L2))
+ *   G   = lora_scale * dY L2^T
+ *   dX  = bf16(dY W' + D o (G L1^T))          (skipped when dX == NULL)
+ *   dL1 = fp32((D o X)^T G),  dL2 = fp32(lora_scale * T^T dY)
+ * Sizes, layouts and errors as qlora_linear_fwd and qlora_linear_bwd, each with a
+ * workspace query of its own. G is kept to 24 bits for dL1 (and rounded to bf16 for dX
+ * alone), so dL1 is nearer the formula than qlora_linear_bwd's, which rounds G.
+ * T is the forward's T_out; when NULL it is formed again with the same mask.
+ * With p = 0 the forward is qlora_linear_fwd.                                    */
+size_t qlora_linear_fwd_dropout_workspace(int64_t M, int64_t K, int64_t N, int r);
+int qlora_linear_fwd_dropout(const uint16_t* X, int64_t M, int64_t K, int64_t N,
+                             const uint8_t* codes, const uint8_t* c2, const float* c1,
+                             const uint16_t* L1, const uint16_t* L2, int r, float lora_scale,
+                             double p, uint64_t seed, uint64_t offset, uint16_t* Y, uint16_t* T_out,
+                             void* workspace, size_t ws_bytes, void* stream);
+size_t qlora_linear_bwd_dropout_workspace(int64_t M, int64_t K, int64_t N, int r);
+int qlora_linear_bwd_dropout(const uint16_t* X, const uint16_t* dY, int64_t M, int64_t K, int64_t N,
+                             const uint8_t* codes, const uint8_t* c2, const float* c1,
+                             const uint16_t* L1, const uint16_t* L2, int r, float lora_scale,
+                             double p, uint64_t seed, uint64_t offset,
+                             const uint16_t* T, uint16_t* dX, float* dL1, float* dL2,
+                             void* workspace, size_t ws_bytes, void* stream);
+
+/* Microscaled 4-bit matrices (OCP Microscaling Formats v1.0, MXFP4): E2M1 elements,
+ * one power-of-two scale for each 32 consecutive elements of a row, and products
+ * that the matrix cores take in this form. Any number of rows and columns.
+ *   block:  e = max(floor(log2 max|v|) - 2, -123), scale byte e + 127; element =
+ *           the E2M1 value nearest to v / 2^e (ties to the even code), at most 6.
+ *           A block of zeros has e = -123. A block with an infinity or NaN has
+ *           scale byte 255 and codes 0, and stands for 32 NaN.
+ *   code:   sign bit 3, magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6 in order.
+ *   packed: rows of cols elements, padded with zeros to Kp = 128 ceil(cols / 128):
+ *           codes [Kp / 32][rows][16] bytes, even element in the low nibble;
+ *           scales [Kp / 128][rows][4] bytes. mx4_codes_bytes and mx4_scales_bytes
+ *           are their sizes (host calls; 0 for sizes out of range).
+ *
+ * mx4_quantize: X [rows, cols] (fp32 or bf16 per x_dtype, rows `ld` elements apart) to
+ * packed form; with `transpose` the packed matrix is X^T, cols rows of length rows
+ * (blocks run down the columns).
+ * mx4_dequantize: the bf16 values [rows, cols] of a packed matrix (exact).
+ * mx4_matmul: C [M, N] = bf16(A B^T) of packed A [M, K] and B [N, K], fp32
+ * accumulation. Sizes as mx4_linear_fwd.                                         */
+size_t mx4_codes_bytes(int64_t rows, int64_t cols);
+size_t mx4_scales_bytes(int64_t rows, int64_t cols);
+int mx4_quantize(const void* X, int x_dtype, int64_t rows, int64_t cols, int64_t ld, int transpose,
+                 uint8_t* codes, uint8_t* scales, void* stream);
+int mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
+                   uint16_t* out, void* stream);
+int mx4_matmul(const uint8_t* a_codes, const uint8_t* a_scales, int64_t M,
+               const uint8_t* b_codes, const uint8_t* b_scales, int64_t N, int64_t K,
+               uint16_t* C, void* stream);
+
+/* The LoRA linear over a frozen microscaled base, the activations quantised on the
+ * way in (q: mx4_quantize along the rows), the adapter in bf16 with dropout:
+ *   fwd: T = bf16((D o X) L1), Y = bf16(q(X) W'^T + lora_scale * (T L2))
+ *        codes/scales: mx4_quantize of W [N, K]
+ *   bwd: G = lora_scale * dY L2^T, dX = bf16(q(dY) W'_t^T + D o (G L1^T)) (NULL: skipped),
+ *        dL1 = fp32((D o X)^T G), dL2 = fp32(lora_scale * T^T dY)
+ *        codes_t/scales_t: mx4_quantize of the same W with `transpose` ([K, N]: the
+ *        product's sums run over N, and a scale has to be common to 32 terms of a
+ *        sum, so the backward reads a packing of its own, whose values may differ
+ *        from the forward's by their rounding). The quantisation of X and dY is
+ *        passed straight through. The base gets no gradient.
+ * G is kept to 24 bits for dL1 and rounded to bf16 for dX. T is the forward's T_out;
+ * when NULL it is formed again with the same mask. Any K and N >= 1, 1 <= r <= 64;
+ * X and dX, Y and dY, and each packed matrix must stay below 2^31 bytes. Device
+ * pointers 16-byte aligned; workspaces from the queries.                         */
+size_t mx4_linear_fwd_workspace(int64_t M, int64_t K, int64_t N, int r);
+int mx4_linear_fwd(const uint16_t* X, int64_t M, int64_t K, int64_t N, const uint8_t* codes, const uint8_t* scales,
+                   const uint16_t* L1, const uint16_t* L2, int r, float lora_scale,
+                   double p, uint64_t seed, uint64_t offset, uint16_t* Y, uint16_t* T_out,
+                   void* workspace, size_t ws_bytes, void* stream);
+size_t mx4_linear_bwd_workspace(int64_t M, int64_t K, int64_t N, int r);
+int mx4_linear_bwd(const uint16_t* X, const uint16_t* dY, int64_t M, int64_t K, int64_t N,
+                   const uint8_t* codes_t, const uint8_t* scales_t,
+                   const uint16_t* L1, const uint16_t* L2, int r, float lora_scale,
+                   double p, uint64_t seed, uint64_t offset,
+                   const uint16_t* T, uint16_t* dX, float* dL1, float* dL2,
+                   void* workspace, size_t ws_bytes, void* stream);
+
 /* Host-only helpers (no GPU needed). */
 /* The 16 NF4 levels (fp32, ascending) that the kernels use, copied to out[16].  */
 int qlora_nf4_levels(float* out16);

@@ -14,3 +14,4 @@ from .qlora_oracle import (  # noqa: F401
 )
 from . import variants  # noqa: F401,E402  (code-book and second-level-scale variants)
 from . import block  # noqa: F401,E402  (stacked linears and the adapter-only optimizer step)
+from . import mx4  # noqa: F401,E402  (microscaled 4-bit layer and adapter dropout)
