@@ -4,6 +4,8 @@
 //   forward   adapter = s (T L2)         T [M, r], L2 [r, P]
 //   backward  adapter = D o (G L1^T)     G [M, r], L1 [P, r]
 // fp32 accumulators throughout, one rounding at the end.
+#include <type_traits>
+
 #include "mx4.h"
 
 #include "kernels.h"
@@ -111,45 +113,45 @@ __global__ __launch_bounds__(64 * kWM * kWP) void k_mx4_gemm(const uint8_t* __re
         : "s"(__builtin_amdgcn_readfirstlane(dst)), "v"(vo), "s"(rs), "s"(__builtin_amdgcn_readfirstlane(so))
         : "memory");
   };
-  auto issue = [&](int q) {
+  // Load n (of kLoads) of step q into its stage.
+  auto load = [&](int q, int n) {
     const uint32_t st = lds0 + (uint32_t)(q % kStages) * G::kStage;
-#pragma unroll
-    for (int i = 0; i < G::kPerA; ++i) {
-      const int c = w + i * G::kWaves;                       // chunk: block position c / (kBM / 64)
-      dma16(st + 1024u * c, va[i], rac, (uint32_t)(4 * q + c / (G::kBM / 64)) * 16u * (uint32_t)M);
+    if (n < G::kPerA) {
+      const int c = w + n * G::kWaves;                       // chunk: block position c / (kBM / 64)
+      dma16(st + 1024u * c, va[n], rac, (uint32_t)(4 * q + c / (G::kBM / 64)) * 16u * (uint32_t)M);
+    } else if (n < G::kPerA + G::kPerB) {
+      const int c = w + (n - G::kPerA) * G::kWaves;
+      dma16(st + G::kCodesA + 1024u * c, vb[n - G::kPerA], rbc, (uint32_t)(4 * q + c / (G::kBP / 64)) * 16u * (uint32_t)P);
+    } else {
+      dma4(st + G::kCodesA + G::kCodesB + 256u * w, vs, rsc, (uint32_t)q * 4u * (uint32_t)srows);
     }
+  };
+  auto issue = [&](int q) {
 #pragma unroll
-    for (int i = 0; i < G::kPerB; ++i) {
-      const int c = w + i * G::kWaves;
-      dma16(st + G::kCodesA + 1024u * c, vb[i], rbc, (uint32_t)(4 * q + c / (G::kBP / 64)) * 16u * (uint32_t)P);
-    }
-    dma4(st + G::kCodesA + G::kCodesB + 256u * w, vs, rsc, (uint32_t)q * 4u * (uint32_t)srows);
+    for (int n = 0; n < G::kLoads; ++n) load(q, n);
   };
 
   // ---- fragments of half s of a step: lane half h takes block 2 h + s of its row,
-  // whose scale is byte s of the 16 bits at 2 h of the row's scale word
+  // whose scale is byte s of the 16 bits at 2 h of the row's scale word.
+  // Read n (of kMT + kPT): a row's codes; the first half's bring its scale as well.
   struct Frags {
     u32x4 a[kMT], b[kPT];
-  };
-  const LDS_AS uint8_t* const smem = (const LDS_AS uint8_t*)lds;
-  const int ra = 32 * kMT * wm + (l & 31), rb = 32 * kPT * wp + (l & 31);
-  auto frags = [&](int q, int s, Frags& f) {
-    const LDS_AS uint8_t* st = smem + (q % kStages) * G::kStage;
-#pragma unroll
-    for (int i = 0; i < kMT; ++i) f.a[i] = *(const LDS_AS u32x4*)(st + ((2 * h + s) * G::kBM + ra + 32 * i) * 16);
-#pragma unroll
-    for (int j = 0; j < kPT; ++j)
-      f.b[j] = *(const LDS_AS u32x4*)(st + G::kCodesA + ((2 * h + s) * G::kBP + rb + 32 * j) * 16);
   };
   struct Scales {
     uint32_t a[kMT], b[kPT];
   };
-  auto scales = [&](int q, Scales& f) {
-    const LDS_AS uint8_t* st = smem + (q % kStages) * G::kStage + G::kCodesA + G::kCodesB + 2 * h;
-#pragma unroll
-    for (int i = 0; i < kMT; ++i) f.a[i] = *(const LDS_AS uint16_t*)(st + 4 * (ra + 32 * i));
-#pragma unroll
-    for (int j = 0; j < kPT; ++j) f.b[j] = *(const LDS_AS uint16_t*)(st + 4 * (G::kBM + rb + 32 * j));
+  const LDS_AS uint8_t* const smem = (const LDS_AS uint8_t*)lds;
+  const int ra = 32 * kMT * wm + (l & 31), rb = 32 * kPT * wp + (l & 31);
+  auto read = [&](int q, int s, int n, Frags& f, Scales& sc) {
+    const LDS_AS uint8_t* st = smem + (q % kStages) * G::kStage;
+    const LDS_AS uint8_t* ss = st + G::kCodesA + G::kCodesB + 2 * h;
+    if (n < kMT) {
+      f.a[n] = *(const LDS_AS u32x4*)(st + ((2 * h + s) * G::kBM + ra + 32 * n) * 16);
+      if (s == 0) sc.a[n] = *(const LDS_AS uint16_t*)(ss + 4 * (ra + 32 * n));
+    } else {
+      f.b[n - kMT] = *(const LDS_AS u32x4*)(st + G::kCodesA + ((2 * h + s) * G::kBP + rb + 32 * (n - kMT)) * 16);
+      if (s == 0) sc.b[n - kMT] = *(const LDS_AS uint16_t*)(ss + 4 * (G::kBM + rb + 32 * (n - kMT)));
+    }
   };
   // The rows of an accumulator are columns of C (operand order B, A): a lane holds
   // four neighbouring columns of one row of C.
@@ -228,7 +230,7 @@ __global__ __launch_bounds__(64 * kWM * kWP) void k_mx4_gemm(const uint8_t* __re
 
   // ---- reduction.  Step q's second half is read while its first half multiplies;
   // then one barrier (stage q is read by every wave, stage q + 1 has arrived) lets
-  // stage q + 4 go into stage q's buffer and the first half of q + 1 be read
+  // step q + 4 go into stage q's buffer and the first half of q + 1 be read
   // while the second half multiplies: the matrix unit has work on both sides of
   // the barrier.
   if (words > 2) issue(2);
@@ -242,34 +244,53 @@ __global__ __launch_bounds__(64 * kWM * kWP) void k_mx4_gemm(const uint8_t* __re
   auto barrier = [&]() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
   Frags f0, f1;
   Scales sc, sn;
+  constexpr int kMfma = kMT * kPT, kReads = kMT + kPT;
   wait(min(words - 1, 3));
   barrier();
-  frags(0, 0, f0);
-  scales(0, sc);
-  for (int q = 0; q < words; ++q) {
-    frags(q, 1, f1);
-    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int i = 0; i < kMT; ++i)
+  for (int n = 0; n < kReads; ++n) read(0, 0, n, f0, sc);
+  // One step with kLeft steps after it (4: four or more).  Between two products a
+  // wave issues one read or load: they go out in the shadow of the matrix unit.
+  auto step = [&](int q, auto left_c) __attribute__((always_inline)) {
+    constexpr int kLeft = decltype(left_c)::value;
 #pragma unroll
-      for (int j = 0; j < kPT; ++j) acc[i][j] = mx4::mfma32<0, 0>(f0.b[j], sc.b[j], f0.a[i], sc.a[i], acc[i][j]);
-    __builtin_amdgcn_sched_barrier(0);
-    const int left = words - 1 - q;     // steps after this one
-    if (left > 0) {
-      wait(left >= 3 ? 2 : left - 1);
+    for (int n = 0; n < kMfma; ++n) {
+      const int i = n % kMT, j = n / kMT;
+      acc[i][j] = mx4::mfma32<0, 0>(f0.b[j], sc.b[j], f0.a[i], sc.a[i], acc[i][j]);
+      if (n < kReads) read(q, 1, n, f1, sc);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int n = kMfma; n < kReads; ++n) read(q, 1, n, f1, sc);
+    if constexpr (kLeft > 0) {
+      wait(kLeft >= 3 ? 2 : kLeft - 1);
       barrier();
-      if (left > 3) issue(q + 4);
-      frags(q + 1, 0, f0);
-      scales(q + 1, sn);
     }
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int i = 0; i < kMT; ++i)
+    for (int n = 0; n < kMfma; ++n) {
+      const int i = n % kMT, j = n / kMT;
+      acc[i][j] = mx4::mfma32<1, 1>(f1.b[j], sc.b[j], f1.a[i], sc.a[i], acc[i][j]);
+      if (kLeft > 0 && n < kReads) read(q + 1, 0, n, f0, sn);
+      if (kLeft > 3 && n < G::kLoads) load(q + 4, n);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if constexpr (kLeft > 0) {
 #pragma unroll
-      for (int j = 0; j < kPT; ++j) acc[i][j] = mx4::mfma32<1, 1>(f1.b[j], sc.b[j], f1.a[i], sc.a[i], acc[i][j]);
-    __builtin_amdgcn_sched_barrier(0);
-    sc = sn;
-  }
+      for (int n = kMfma; n < kReads; ++n) read(q + 1, 0, n, f0, sn);
+      sc = sn;
+    }
+    if constexpr (kLeft > 3) {
+#pragma unroll
+      for (int n = kMfma; n < G::kLoads; ++n) load(q + 4, n);
+    }
+  };
+  int q = 0;
+  for (; q + 4 < words; ++q) step(q, std::integral_constant<int, 4>{});
+  if (words - q == 4) step(q++, std::integral_constant<int, 3>{});
+  if (words - q == 3) step(q++, std::integral_constant<int, 2>{});
+  if (words - q == 2) step(q++, std::integral_constant<int, 1>{});
+  step(q, std::integral_constant<int, 0>{});
 
   // ---- store: lane (h, m) holds columns 8 g + 4 h + e, e = 0..3, of row m; a swap of
   // the halves of a register pair gives half h columns 16 gp + 8 h .. +7
