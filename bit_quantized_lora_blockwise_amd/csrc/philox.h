@@ -24,24 +24,31 @@ struct Params {
   float scale;          // 65536 / (65536 - cut)
 };
 
-__device__ __forceinline__ u32x4 philox7(uint32_t c0, uint32_t c1, uint32_t c2, uint32_t c3, uint32_t k0,
-                                         uint32_t k1) {
-#pragma unroll
-  for (int n = 0; n < 7; ++n) {
-    const uint64_t a = (uint64_t)c0 * 0xD2511F53u, b = (uint64_t)c2 * 0xCD9E8D57u;
-    c0 = (uint32_t)(b >> 32) ^ c1 ^ k0;
-    c2 = (uint32_t)(a >> 32) ^ c3 ^ k1;
-    c1 = (uint32_t)b;
-    c3 = (uint32_t)a;
-    k0 += 0x9E3779B9u;
-    k1 += 0xBB67AE85u;
-  }
-  return u32x4{c0, c1, c2, c3};
+// A call in flight: counter words and the key of the next round.
+struct State {
+  uint32_t c0, c1, c2, c3, k0, k1;
+};
+
+__device__ __forceinline__ State begin(const Params& d, uint32_t m, uint32_t q) {
+  return State{q, m, d.o0, d.o1, d.k0, d.k1};
+}
+
+__device__ __forceinline__ void round(State& s) {
+  const uint64_t a = (uint64_t)s.c0 * 0xD2511F53u, b = (uint64_t)s.c2 * 0xCD9E8D57u;
+  s.c0 = (uint32_t)(b >> 32) ^ s.c1 ^ s.k0;
+  s.c2 = (uint32_t)(a >> 32) ^ s.c3 ^ s.k1;
+  s.c1 = (uint32_t)b;
+  s.c3 = (uint32_t)a;
+  s.k0 += 0x9E3779B9u;
+  s.k1 += 0xBB67AE85u;
 }
 
 // The numbers of elements (m, 8 q) .. (m, 8 q + 7).
 __device__ __forceinline__ u32x4 draw8(const Params& d, uint32_t m, uint32_t q) {
-  return philox7(q, m, d.o0, d.o1, d.k0, d.k1);
+  State s = begin(d, m, q);
+#pragma unroll
+  for (int n = 0; n < 7; ++n) round(s);
+  return u32x4{s.c0, s.c1, s.c2, s.c3};
 }
 
 // 0xFFFF in each half of a word whose number keeps its element, else 0.
@@ -57,14 +64,17 @@ __device__ __forceinline__ u32x4 mask8(u32x4 v, const Params& d, uint32_t m, uin
   return v;
 }
 
-// The same eight decisions as bits 0 .. 7.
-__device__ __forceinline__ uint32_t bits8(const Params& d, uint32_t m, uint32_t q) {
-  const u32x4 u = draw8(d, m, q);
+// Eight numbers' decisions as bits 0 .. 7.
+__device__ __forceinline__ uint32_t bits8_of(u32x4 u, uint32_t cut) {
   uint32_t b = 0;
 #pragma unroll
   for (int j = 0; j < 4; ++j)
-    b |= ((u[j] & 0xFFFFu) >= d.cut ? 1u << (2 * j) : 0u) | (u[j] >= (d.cut << 16) ? 2u << (2 * j) : 0u);
+    b |= ((u[j] & 0xFFFFu) >= cut ? 1u << (2 * j) : 0u) | (u[j] >= (cut << 16) ? 2u << (2 * j) : 0u);
   return b;
+}
+
+__device__ __forceinline__ uint32_t bits8(const Params& d, uint32_t m, uint32_t q) {
+  return bits8_of(draw8(d, m, q), d.cut);
 }
 
 // A tile's decisions in LDS, a bit an element: row i at byte i * bit_pitch(cols),

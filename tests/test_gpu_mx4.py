@@ -266,6 +266,22 @@ def test_layer(M, K, N, r, p):
     assert torch.equal(dX, dX2)
 
 
+# the persistent kernel: several tiles a work group with the fewest reduction steps and with many, each direction, rows
+# of C and ranks that are whole 16-byte pieces or not
+LARGE = [(2100, 700, 8200, 16), (2100, 8200, 700, 24), (2093, 701, 8197, 5), (2093, 8197, 701, 5), (2100, 3912, 3920, 64)]
+
+
+@pytest.mark.parametrize("M,K,N,r", LARGE)
+@pytest.mark.parametrize("p", [0.0, 0.1])
+def test_large_layer(M, K, N, r, p):
+    test_layer(M, K, N, r, p)
+
+
+@pytest.mark.parametrize("M,N,K", [(2100, 8200, 700), (2093, 8197, 1301), (4352, 4360, 1024)])
+def test_large_matmul(M, N, K):
+    test_matmul(M, N, K)
+
+
 NF4 = [(1, 64, 1, 1), (1, 4096, 300, 64), (16, 512, 136, 8), (17, 512, 200, 12), (32, 512, 512, 8), (130, 576, 333, 5),
        (300, 1152, 264, 64), (260, 320, 520, 16)]
 
