@@ -115,15 +115,19 @@ def _ptr(t):
     the library through here, after all size checks: this is the device check."""
     if t is None:
         return None
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"every tensor argument must be on the GPU (got a {t.device} tensor of shape "
                          f"{tuple(t.shape)})")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _stream(stream=None):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    """The HIP stream of a call.  Without one given, the current device's current
+    stream, asked for as a number: building a torch.cuda.Stream for it takes 3 us,
+    as long as a kernel launch."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
 
 
 def _need(t, name, dtype, ndim=None, shape=None, numel=None):

@@ -16,10 +16,10 @@ bool matrix_ok(int64_t rows, int64_t cols, int64_t ld) {
 }
 
 // Layer sizes: X, Y and their gradients, the packed activations and the packed
-// weight below 2^31 bytes each.
+// weight, the adapters, T and G below 2^31 bytes each (the kernels' offsets are 32-bit).
 bool layer_ok(int64_t M, int64_t K, int64_t N, int r) {
   return M > 0 && K > 0 && N > 0 && M < kLim && K < kLim && N < kLim && r >= 1 && r <= 64 && M <= kLim / 2 / K &&
-         M <= kLim / 2 / N && M * K * 2 < kLim && M * N * 2 < kLim && mx4::padded(K) <= kLim / N &&
+         M <= kLim / 2 / N && M < kLim / 2 / r && K < kLim / 2 / r && N < kLim / 2 / r && M * K * 2 < kLim && M * N * 2 < kLim && mx4::padded(K) <= kLim / N &&
          mx4::padded(N) <= kLim / K && mx4::code_bytes(N, K) < kLim && mx4::code_bytes(K, N) < kLim &&
          mx4::code_bytes(M, K) < kLim && mx4::code_bytes(M, N) < kLim;
 }
@@ -30,7 +30,7 @@ struct Ws {
 };
 Ws fwd_ws(int64_t M, int64_t K, int r) {
   Ws w{round_up(mx4::code_bytes(M, K)), round_up(mx4::scale_bytes(M, K)), round_up((size_t)M * r * 2), 0,
-       round_up(lora_skinny_ws(M, K, r)), 0};
+       round_up(std::max(lora_skinny_ws(M, K, r), mx4_small_ws(M, r))), 0};
   w.total = w.codes + w.scales + w.low + w.part;
   return w;
 }
@@ -38,7 +38,8 @@ Ws fwd_ws(int64_t M, int64_t K, int r) {
 Ws bwd_ws(int64_t M, int64_t K, int64_t N, int r, bool packed) {
   Ws w{packed ? round_up(mx4::code_bytes(M, N)) : 0, packed ? round_up(mx4::scale_bytes(M, N)) : 0,
        round_up((size_t)3 * M * r * 2), round_up((size_t)M * r * 2), 0, 0};
-  w.part = round_up(std::max({lora_skinny_ws(M, N, r), lora_skinny_ws(M, K, r), lora_tn_pair_ws(M, K, N, r)}));
+  w.part = round_up(std::max({lora_skinny_ws(M, N, r), lora_skinny_ws(M, K, r), lora_tn_pair_ws(M, K, N, r),
+                              packed ? mx4_small_ws(M, r) : 0}));
   w.total = w.codes + w.scales + w.low + w.t + w.part;
   return w;
 }
@@ -118,6 +119,10 @@ int mx4_linear_fwd(const uint16_t* X, int64_t M, int64_t K, int64_t N, const uin
   uint8_t* as = ac + w.codes;
   uint16_t* T = T_out ? T_out : (uint16_t*)(as + w.scales);
   float* part = (float*)(as + w.scales + w.low);
+  if (mx4_small_ok(M, N)) {
+    QL_TRY(launch_mx4_small_fwd(X, M, K, N, codes, scales, L1, L2, r, lora_scale, d, Y, T_out, ac, as, part, s));
+    return QL_OK;
+  }
   QL_TRY(launch_mx4_quant(X, true, M, K, K, ac, as, s));
   QL_TRY(launch_lora_down_drop(X, M, K, L1, r, d, T, part, s));
   QL_TRY(launch_mx4_gemm(ac, as, M, codes, scales, N, K, Mx4Lora{T, L2, r, false, lora_scale, drop::Params{}}, Y, s));
@@ -146,14 +151,22 @@ int mx4_linear_bwd(const uint16_t* X, const uint16_t* dY, int64_t M, int64_t K, 
   uint16_t* G = (uint16_t*)(as + w.scales);
   uint16_t* Tw = (uint16_t*)((uint8_t*)G + w.low);
   float* part = (float*)((uint8_t*)Tw + w.t);
+  const bool small = mx4_small_ok(M, K);
   if (!T) {
-    QL_TRY(launch_lora_down_drop(X, M, K, L1, r, d, Tw, part, s));
+    if (mx4_small_ok(M, N)) QL_TRY(launch_mx4_small_t(X, M, K, L1, r, d, Tw, part, s));
+    else QL_TRY(launch_lora_down_drop(X, M, K, L1, r, d, Tw, part, s));
     T = Tw;
   }
-  QL_TRY(launch_lora_grad_in3(dY, M, N, L2, r, lora_scale, G, part, s));
-  if (dX) {
-    QL_TRY(launch_mx4_quant(dY, true, M, N, N, ac, as, s));
-    QL_TRY(launch_mx4_gemm(ac, as, M, codes_t, scales_t, K, N, Mx4Lora{G, L1, r, true, 1.0f, d}, dX, s));
+  if (dX && small) {
+    QL_TRY(launch_mx4_small_dx(dY, M, K, N, codes_t, scales_t, L1, L2, r, lora_scale, d, dX, G, ac, as, part, s));
+  } else if (small) {
+    QL_TRY(launch_mx4_small_g(dY, M, N, L2, r, lora_scale, G, part, s));
+  } else {
+    QL_TRY(launch_lora_grad_in3(dY, M, N, L2, r, lora_scale, G, part, s));
+    if (dX) {
+      QL_TRY(launch_mx4_quant(dY, true, M, N, N, ac, as, s));
+      QL_TRY(launch_mx4_gemm(ac, as, M, codes_t, scales_t, K, N, Mx4Lora{G, L1, r, true, 1.0f, d}, dX, s));
+    }
   }
   QL_TRY(launch_lora_grads3(X, K, G, d, dL1, dY, N, T, lora_scale, dL2, M, r, part, s));
   return QL_OK;

@@ -65,6 +65,10 @@ int64_t decode_t_rows(int64_t K);   // rows of K per slice (a multiple of 32)
 bool decode_t_ok(int64_t M, int64_t K, const void* X, const void* L1);
 hipError_t launch_lora_part(const uint16_t* X, int64_t M, int64_t K, const uint16_t* L1, int r, float* part,
                             hipStream_t s, int G = 1);
+// out[i] = bf16(scale * (part[i] + part[n + i] + ...)), slices added in order; planes:
+// as three bf16 planes out[i], out[n + i], out[2 n + i] whose sum it is.
+hipError_t launch_skinny_reduce(const float* part, int slices, int64_t n, float scale, uint16_t* out, hipStream_t s,
+                                bool planes = false);
 hipError_t launch_lora_skinny(const uint16_t* A, int64_t M, int64_t R, int64_t lda, const uint16_t* B, bool b_is_kr,
                               int r, float scale, uint16_t* out, float* ws, hipStream_t s);
 
@@ -118,6 +122,23 @@ struct Mx4Lora {
 };
 hipError_t launch_mx4_gemm(const uint8_t* ac, const uint8_t* as, int64_t M, const uint8_t* bc, const uint8_t* bs,
                            int64_t P, int64_t R, const Mx4Lora& lora, uint16_t* C, hipStream_t s);
+
+// The layer for few rows (mx4_small.hip): one call quantises the activations (into ac,
+// as), forms T or G and multiplies.  part: mx4_small_ws bytes.  Forward: T_out may be
+// nullptr.  Backward: G receives the three planes of launch_lora_grad_in3.
+bool mx4_small_ok(int64_t M, int64_t P);   // P: columns of the result
+size_t mx4_small_ws(int64_t M, int r);
+hipError_t launch_mx4_small_fwd(const uint16_t* X, int64_t M, int64_t K, int64_t N, const uint8_t* bc, const uint8_t* bs,
+                                const uint16_t* L1, const uint16_t* L2, int r, float scale, const drop::Params& d,
+                                uint16_t* Y, uint16_t* T_out, uint8_t* ac, uint8_t* as, float* part, hipStream_t s);
+hipError_t launch_mx4_small_dx(const uint16_t* dY, int64_t M, int64_t K, int64_t N, const uint8_t* bc, const uint8_t* bs,
+                               const uint16_t* L1, const uint16_t* L2, int r, float scale, const drop::Params& d,
+                               uint16_t* dX, uint16_t* G, uint8_t* ac, uint8_t* as, float* part, hipStream_t s);
+// The forward's T and the backward's G alone (same bits).
+hipError_t launch_mx4_small_t(const uint16_t* X, int64_t M, int64_t K, const uint16_t* L1, int r, const drop::Params& d,
+                              uint16_t* T, float* part, hipStream_t s);
+hipError_t launch_mx4_small_g(const uint16_t* dY, int64_t M, int64_t N, const uint16_t* L2, int r, float scale,
+                              uint16_t* G, float* part, hipStream_t s);
 
 // --- adapter merge (merge.hip) ---------------------------------------------
 // W[n][k] = bf16(W'[n][k] + scale * sum_c L1[k][c] L2[c][n]), W' the bf16

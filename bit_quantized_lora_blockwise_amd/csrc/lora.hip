@@ -33,19 +33,6 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p, uint64_t b
                                            0x00020000);
 }
 
-// 8 consecutive bf16 of a row starting at column `col`, zero past `ncols`.
-__device__ __forceinline__ u32x4 load_row8(const uint16_t* __restrict__ row, int64_t col, int64_t ncols) {
-  const uint16_t* p = row + col;
-  if (col + 8 <= ncols && ((uintptr_t)p & 15) == 0) return *(const u32x4*)p;
-  u32x4 v = {0, 0, 0, 0};
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const uint32_t h = (col + j < ncols) ? p[j] : 0;
-    v[j >> 1] |= h << (16 * (j & 1));
-  }
-  return v;
-}
-
 // A 64 x 64 bf16 tile of a row-major matrix held in registers: thread t holds
 // rows (t / 8) + 32 i, columns 8 (t % 8) .. +8.
 struct Tile {
@@ -55,29 +42,28 @@ struct Tile {
 // Tile at `base` (its element (0, 0)) of a matrix with `ld` elements per row;
 // rows at or past `rows` and columns at or past `cols` read as zero.  With
 // kVec (ld and cols multiples of 8, base 16-byte aligned) each thread issues
-// two 16-byte buffer loads with no branch, so that the loads of later steps
-// stay in flight; otherwise it reads element by element.  `bytes`: extent of
-// the matrix from `base`.
+// two 16-byte buffer loads, otherwise sixteen of one element, with no branch, so
+// that the loads of later steps stay in flight.  `bytes`: extent of the matrix
+// from `base`.
 template <bool kVec>
 __device__ __forceinline__ Tile load_tile(const uint16_t* base, int64_t ld, int64_t rows, int64_t cols,
                                           uint64_t bytes) {
-  constexpr bool vec = kVec;
   const int t = threadIdx.x;
   const int cc = (t & 7) * 8;
+  const __amdgpu_buffer_rsrc_t rs = rsrc(base, bytes);
   Tile tl;
-  if (vec) {
-    const __amdgpu_buffer_rsrc_t rs = rsrc(base, bytes);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int row = (t >> 3) + 32 * i;
-      const bool ok = row < rows && cc < cols;
-      tl.v[i] = __builtin_amdgcn_raw_buffer_load_b128(rs, ok ? (uint32_t)((row * ld + cc) * 2) : kOOB, 0, 0);
-    }
-  } else {
+  for (int i = 0; i < 2; ++i) {
+    const int row = (t >> 3) + 32 * i;
+    const uint32_t at = (uint32_t)((row * ld + cc) * 2);
+    if constexpr (kVec) {
+      tl.v[i] = __builtin_amdgcn_raw_buffer_load_b128(rs, row < rows && cc < cols ? at : kOOB, 0, 0);
+    } else {
+      uint32_t e[8];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int row = (t >> 3) + 32 * i;
-      tl.v[i] = (row < rows) ? load_row8(base + row * ld, cc, cols) : u32x4{0, 0, 0, 0};
+      for (int j = 0; j < 8; ++j)
+        e[j] = __builtin_amdgcn_raw_buffer_load_b16(rs, row < rows && cc + j < cols ? at + 2 * j : kOOB, 0, 0);
+      tl.v[i] = u32x4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
     }
   }
   return tl;
@@ -382,11 +368,13 @@ __global__ __launch_bounds__(kThreads) void k_skinny_reduce3(const float* __rest
 // C[p, c] partial over one slice of m: sum_m A[m][p] * B[m][c], A [M, P], B [M, r];
 // this work group's tile of 64 p is `tile`, its slice of m is `split`.  kDrop: of
 // D o A, not scaled.  kPlanes: B is the sum of that many matrices, B + j M r.
-// lds: (2 + 2 kPlanes) tiles of kTile * kPitch.
+// lds: (2 + 2 kPlanes) tiles of kTile * kPitch.  scale: of what is written; tr: written
+// as part[c][p] (both for a product of one slice, whose partial is the result).
 template <bool kVecA, bool kVecB, bool kDrop = false, int kPlanes = 1>
 __device__ __forceinline__ void tn_tile(const uint16_t* __restrict__ A, int64_t lda, const uint16_t* __restrict__ B,
                                         int64_t M, int64_t P, int r, int64_t chunk, float* __restrict__ part,
-                                        int tile, int split, uint16_t* lds, const drop::Params& d) {
+                                        int tile, int split, uint16_t* lds, const drop::Params& d,
+                                        float scale = 1.0f, bool tr = false) {
   LDS_AS uint16_t* const sm = (LDS_AS uint16_t*)lds;
   auto abuf = [&](int64_t b) { return sm + (b & 1) * kTile * kPitch; };
   auto bbuf = [&](int64_t b, int j) { return sm + (2 + kPlanes * (b & 1) + j) * kTile * kPitch; };
@@ -444,7 +432,7 @@ __device__ __forceinline__ void tn_tile(const uint16_t* __restrict__ A, int64_t 
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
       const int64_t p = p0 + 32 * wp + qk::acc_row(j);
-      if (p < P && c < r) part[((int64_t)split * P + p) * r + c] = acc[j];
+      if (p < P && c < r) part[tr ? c * P + p : ((int64_t)split * P + p) * r + c] = scale * acc[j];
     }
   }
 }
@@ -478,17 +466,20 @@ __global__ __launch_bounds__(kThreads) void k_lora_tn_pair(TnJob j0, TnJob j1, i
   tn_tile<kVecA, kVecB>(j.A, j.lda, j.B, M, j.P, r, j.chunk, j.part, b % j.tiles, b / j.tiles, lds, drop::Params{});
 }
 
-// The pair with dropout on the first product's A and its B in three planes.
+// The pair with dropout on the first product's A and its B in three planes.  With
+// one slice each, j0.part and j1.part are the results: scaled, the second transposed.
 template <bool kVec, bool kDrop>
-__global__ __launch_bounds__(kThreads) void k_lora_tn_pair3(TnJob j0, TnJob j1, int64_t M, int r, drop::Params d) {
+__global__ __launch_bounds__(kThreads) void k_lora_tn_pair3(TnJob j0, TnJob j1, int64_t M, int r, drop::Params d,
+                                                            float scale0, float scale1, bool whole) {
   __shared__ __attribute__((aligned(16))) uint16_t lds[8 * kTile * kPitch];
   const int n0 = j0.tiles * j0.splits;
   const int b = (int)blockIdx.x;
   if (b < n0)
-    tn_tile<kVec, kVec, kDrop, 3>(j0.A, j0.lda, j0.B, M, j0.P, r, j0.chunk, j0.part, b % j0.tiles, b / j0.tiles, lds, d);
+    tn_tile<kVec, kVec, kDrop, 3>(j0.A, j0.lda, j0.B, M, j0.P, r, j0.chunk, j0.part, b % j0.tiles, b / j0.tiles, lds, d,
+                                  scale0);
   else
     tn_tile<kVec, kVec>(j1.A, j1.lda, j1.B, M, j1.P, r, j1.chunk, j1.part, (b - n0) % j1.tiles, (b - n0) / j1.tiles,
-                        lds, d);
+                        lds, d, scale1, whole);
 }
 
 // out[i] = scale * (sum of the slices), i over P * r, by work groups blk of nblk.
@@ -779,6 +770,15 @@ hipError_t launch_lora_tn(const uint16_t* A, int64_t lda, const uint16_t* B, int
   return hipGetLastError();
 }
 
+hipError_t launch_skinny_reduce(const float* part, int slices, int64_t n, float scale, uint16_t* out, hipStream_t s,
+                                bool planes) {
+  if (planes)
+    hipLaunchKernelGGL(k_skinny_reduce3, dim3(grid_for(n)), dim3(kThreads), 0, s, part, slices, n, scale, out);
+  else
+    hipLaunchKernelGGL(k_skinny_reduce, dim3(grid_for((n + 3) / 4)), dim3(kThreads), 0, s, part, slices, n, scale, out);
+  return hipGetLastError();
+}
+
 // ---- with dropout, and with G kept to 24 bits ---------------------------------
 hipError_t launch_lora_down_drop(const uint16_t* X, int64_t M, int64_t K, const uint16_t* L1, int r,
                                  const drop::Params& d, uint16_t* T, float* ws, hipStream_t s) {
@@ -801,9 +801,7 @@ hipError_t launch_lora_down_drop(const uint16_t* X, int64_t M, int64_t K, const 
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(k_skinny_reduce, dim3(grid_for((M * r + 3) / 4)), dim3(kThreads), 0, s, ws, sp.splits,
-                     M * (int64_t)r, d.scale, T);
-  return hipGetLastError();
+  return launch_skinny_reduce(ws, sp.splits, M * r, d.scale, T, s);
 }
 
 hipError_t launch_lora_grad_in3(const uint16_t* dY, int64_t M, int64_t N, const uint16_t* L2, int r, float scale,
@@ -826,9 +824,7 @@ hipError_t launch_lora_grad_in3(const uint16_t* dY, int64_t M, int64_t N, const 
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(k_skinny_reduce3, dim3(grid_for(M * r)), dim3(kThreads), 0, s, ws, sp.splits, M * (int64_t)r,
-                     scale, G);
-  return hipGetLastError();
+  return launch_skinny_reduce(ws, sp.splits, M * r, scale, G, s, true);
 }
 
 hipError_t launch_lora_grads3(const uint16_t* X, int64_t K, const uint16_t* G, const drop::Params& d, float* dL1,
@@ -838,10 +834,13 @@ hipError_t launch_lora_grads3(const uint16_t* X, int64_t K, const uint16_t* G, c
   float* part1 = ws + (lora_tn_ws(M, K, r) + 255) / 256 * 256 / sizeof(float);
   const SplitPlan sp0 = plan_rowsplit((K + kTile - 1) / kTile, M);
   const SplitPlan sp1 = plan_rowsplit((N + kTile - 1) / kTile, M);
-  const TnJob j0{X, K, G, K, sp0.chunk, ws, (int)((K + kTile - 1) / kTile), sp0.splits};
-  const TnJob j1{dY, N, T, N, sp1.chunk, part1, (int)((N + kTile - 1) / kTile), sp1.splits};
+  const bool whole = sp0.splits == 1 && sp1.splits == 1;
+  const TnJob j0{X, K, G, K, sp0.chunk, whole ? dL1 : ws, (int)((K + kTile - 1) / kTile), sp0.splits};
+  const TnJob j1{dY, N, T, N, sp1.chunk, whole ? dL2 : part1, (int)((N + kTile - 1) / kTile), sp1.splits};
+  const float s0 = whole ? d.scale : 1.0f, s1 = whole ? scale : 1.0f;
   const unsigned nwg = (unsigned)(j0.tiles * j0.splits + j1.tiles * j1.splits);
-#define QL_TN3(V, D) hipLaunchKernelGGL((k_lora_tn_pair3<V, D>), dim3(nwg), dim3(kThreads), 0, s, j0, j1, M, r, d)
+#define QL_TN3(V, D) hipLaunchKernelGGL((k_lora_tn_pair3<V, D>), dim3(nwg), dim3(kThreads), 0, s, j0, j1, M, r, d, s0, \
+                                       s1, whole)
   if (vec) {
     if (d.cut) QL_TN3(true, true);
     else QL_TN3(true, false);
@@ -851,7 +850,7 @@ hipError_t launch_lora_grads3(const uint16_t* X, int64_t K, const uint16_t* G, c
   }
 #undef QL_TN3
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
+  if (e != hipSuccess || whole) return e;
   const int nb0 = grid_for((K * r + 3) / 4);
   const unsigned nb1 = (unsigned)((N + kTrP - 1) / kTrP);
   hipLaunchKernelGGL(k_tn_reduce_pair, dim3((unsigned)nb0 + nb1), dim3(kThreads), 0, s, ws, sp0.splits, K, d.scale, dL1,

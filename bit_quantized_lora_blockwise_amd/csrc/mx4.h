@@ -75,4 +75,11 @@ __device__ __forceinline__ f32x16 mfma32(u32x4 a, uint32_t sa, u32x4 b, uint32_t
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(av, bv, acc, 4, 4, ia, (int)sa, ib, (int)sb);
 }
 
+// The same over 128 for 16 x 16 tiles: lane l holds row / column l % 16, block l / 16.
+__device__ __forceinline__ f32x4 mfma16(u32x4 a, uint32_t sa, u32x4 b, uint32_t sb, f32x4 acc) {
+  const i32x8 av = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
+  const i32x8 bv = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, acc, 4, 4, 0, (int)sa, 0, (int)sb);
+}
+
 }  // namespace mx4
