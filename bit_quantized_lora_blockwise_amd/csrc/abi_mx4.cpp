@@ -38,7 +38,7 @@ Ws fwd_ws(int64_t M, int64_t K, int r) {
 Ws bwd_ws(int64_t M, int64_t K, int64_t N, int r, bool packed) {
   Ws w{packed ? round_up(mx4::code_bytes(M, N)) : 0, packed ? round_up(mx4::scale_bytes(M, N)) : 0,
        round_up((size_t)3 * M * r * 2), round_up((size_t)M * r * 2), 0, 0};
-  w.part = round_up(std::max({lora_skinny_ws(M, N, r), lora_skinny_ws(M, K, r), lora_tn_pair_ws(M, K, N, r),
+  w.part = round_up(std::max({lora_skinny_ws(M, N, r), lora_skinny_ws(M, K, r), lora_grads3_ws(M, K, N, r),
                               packed ? mx4_small_ws(M, r) : 0}));
   w.total = w.codes + w.scales + w.low + w.t + w.part;
   return w;
@@ -123,8 +123,7 @@ int mx4_linear_fwd(const uint16_t* X, int64_t M, int64_t K, int64_t N, const uin
     QL_TRY(launch_mx4_small_fwd(X, M, K, N, codes, scales, L1, L2, r, lora_scale, d, Y, T_out, ac, as, part, s));
     return QL_OK;
   }
-  QL_TRY(launch_mx4_quant(X, true, M, K, K, ac, as, s));
-  QL_TRY(launch_lora_down_drop(X, M, K, L1, r, d, T, part, s));
+  QL_TRY(launch_lora_down_drop(X, M, K, L1, r, d, T, ac, as, part, s));
   QL_TRY(launch_mx4_gemm(ac, as, M, codes, scales, N, K, Mx4Lora{T, L2, r, false, lora_scale, drop::Params{}}, Y, s));
   return QL_OK;
 }
@@ -154,7 +153,7 @@ int mx4_linear_bwd(const uint16_t* X, const uint16_t* dY, int64_t M, int64_t K, 
   const bool small = mx4_small_ok(M, K);
   if (!T) {
     if (mx4_small_ok(M, N)) QL_TRY(launch_mx4_small_t(X, M, K, L1, r, d, Tw, part, s));
-    else QL_TRY(launch_lora_down_drop(X, M, K, L1, r, d, Tw, part, s));
+    else QL_TRY(launch_lora_down_drop(X, M, K, L1, r, d, Tw, nullptr, nullptr, part, s));
     T = Tw;
   }
   if (dX && small) {
@@ -162,11 +161,8 @@ int mx4_linear_bwd(const uint16_t* X, const uint16_t* dY, int64_t M, int64_t K, 
   } else if (small) {
     QL_TRY(launch_mx4_small_g(dY, M, N, L2, r, lora_scale, G, part, s));
   } else {
-    QL_TRY(launch_lora_grad_in3(dY, M, N, L2, r, lora_scale, G, part, s));
-    if (dX) {
-      QL_TRY(launch_mx4_quant(dY, true, M, N, N, ac, as, s));
-      QL_TRY(launch_mx4_gemm(ac, as, M, codes_t, scales_t, K, N, Mx4Lora{G, L1, r, true, 1.0f, d}, dX, s));
-    }
+    QL_TRY(launch_lora_grad_in3(dY, M, N, L2, r, lora_scale, G, dX ? ac : nullptr, as, part, s));
+    if (dX) QL_TRY(launch_mx4_gemm(ac, as, M, codes_t, scales_t, K, N, Mx4Lora{G, L1, r, true, 1.0f, d}, dX, s));
   }
   QL_TRY(launch_lora_grads3(X, K, G, d, dL1, dY, N, T, lora_scale, dL2, M, r, part, s));
   return QL_OK;
@@ -193,7 +189,7 @@ int qlora_linear_fwd_dropout(const uint16_t* X, int64_t M, int64_t K, int64_t N,
   if (!aligned16(workspace)) return QL_ERR_ALIGN;
   uint16_t* T = T_out ? T_out : (uint16_t*)workspace;
   float* part = (float*)((char*)workspace + round_up((size_t)M * r * 2));
-  QL_TRY(launch_lora_down_drop(X, M, K, L1, r, d, T, part, (hipStream_t)stream));
+  QL_TRY(launch_lora_down_drop(X, M, K, L1, r, d, T, nullptr, nullptr, part, (hipStream_t)stream));
   return qlora_linear_fwd_t(X, M, K, N, codes, c2, c1, T, L2, r, lora_scale, Y, stream);
 }
 
@@ -219,10 +215,10 @@ int qlora_linear_bwd_dropout(const uint16_t* X, const uint16_t* dY, int64_t M, i
   uint16_t* Tw = (uint16_t*)((uint8_t*)G + w.low);
   float* part = (float*)((uint8_t*)Tw + w.t);
   if (!T) {
-    QL_TRY(launch_lora_down_drop(X, M, K, L1, r, d, Tw, part, s));
+    QL_TRY(launch_lora_down_drop(X, M, K, L1, r, d, Tw, nullptr, nullptr, part, s));
     T = Tw;
   }
-  QL_TRY(launch_lora_grad_in3(dY, M, N, L2, r, lora_scale, G, part, s));
+  QL_TRY(launch_lora_grad_in3(dY, M, N, L2, r, lora_scale, G, nullptr, nullptr, part, s));
   if (dX) {
     if (qgemm_big_ok(true, M, K, N))
       QL_TRY(launch_qgemm_big(true, dY, M, K, N, codes, c2, c1, G, L1, r, 1.0f, dX, s, 1, &d));

@@ -86,18 +86,30 @@ hipError_t launch_lora_tn(const uint16_t* A, int64_t lda, const uint16_t* B, int
                           float scale, bool transpose_out, float* out, float* ws, hipStream_t s);
 
 // The adapter branch with dropout on its input (d.cut = 0: none) and G to 24 bits:
-//   T = bf16((D o X) L1); ws as lora_skinny_ws(M, K, r)
+//   T = bf16((D o X) L1); ws as lora_skinny_ws(M, K, r).  With `codes`, the same pass
+//     also packs X (not D o X) in microscaled 4-bit; G and dY likewise
 //   G = scale dY L2^T as three bf16 planes [3][M, r] whose sum it is (the first one
 //     is bf16(G)); ws as lora_skinny_ws(M, N, r)
 //   dL1 [K, r] = (D o X)^T G from the planes, dL2 [r, N] = scale T^T dY, fp32; ws as
-//     lora_tn_pair_ws(M, K, N, r)
+//     lora_grads3_ws(M, K, N, r).  Many rows of 16-byte pieces go to lora_grads.hip.
 hipError_t launch_lora_down_drop(const uint16_t* X, int64_t M, int64_t K, const uint16_t* L1, int r,
-                                 const drop::Params& d, uint16_t* T, float* ws, hipStream_t s);
+                                 const drop::Params& d, uint16_t* T, uint8_t* codes, uint8_t* scales, float* ws,
+                                 hipStream_t s);
 hipError_t launch_lora_grad_in3(const uint16_t* dY, int64_t M, int64_t N, const uint16_t* L2, int r, float scale,
-                                uint16_t* G, float* ws, hipStream_t s);
+                                uint16_t* G, uint8_t* codes, uint8_t* scales, float* ws, hipStream_t s);
 hipError_t launch_lora_grads3(const uint16_t* X, int64_t K, const uint16_t* G, const drop::Params& d, float* dL1,
                               const uint16_t* dY, int64_t N, const uint16_t* T, float scale, float* dL2, int64_t M,
                               int r, float* ws, hipStream_t s);
+size_t lora_grads3_ws(int64_t M, int64_t K, int64_t N, int r);
+bool lora_grads_wide_ok(int64_t M, int64_t K, int64_t N, int r);
+size_t lora_grads_wide_ws(int64_t M, int64_t K, int64_t N, int r);
+hipError_t launch_lora_grads_wide(const uint16_t* X, int64_t K, const uint16_t* G, const drop::Params& d, float* dL1,
+                                  const uint16_t* dY, int64_t N, const uint16_t* T, float scale, float* dL2, int64_t M,
+                                  int r, float* ws, hipStream_t s);
+// The sums of two such products' slices: out0 [P0, r], out1_t [r, P1] (transposed).
+hipError_t launch_tn_reduce_pair(const float* part0, int splits0, int64_t P0, float scale0, float* out0,
+                                 const float* part1, int splits1, int64_t P1, float scale1, float* out1_t, int r,
+                                 hipStream_t s);
 // Y = D o X, elementwise; X rows `ld` elements apart, Y dense (dropout.hip).
 hipError_t launch_dropout(const void* X, bool bf16, int64_t rows, int64_t cols, int64_t ld, const drop::Params& d,
                           void* Y, hipStream_t s);

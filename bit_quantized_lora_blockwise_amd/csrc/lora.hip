@@ -18,6 +18,7 @@
 #include <algorithm>
 
 #include "kernels.h"
+#include "mx4.h"
 #include "philox.h"
 #include "tpart.h"
 
@@ -160,17 +161,27 @@ __global__ __launch_bounds__(kThreads) void k_lora_skinny(const uint16_t* __rest
 // At the end the four phases' sums are added in LDS in the order p = 0 .. 3.
 // Per CU this keeps well over 100 KB of A in flight with four waves per SIMD,
 // while each slice of B is read once per 64 rows and the slices stay few.
+// kQuant: the pass also writes A in microscaled 4-bit (layout: mx4.h), which a pass of
+// its own would read A again for (9.5 us at 2048 x 8192).  Lanes l, l + 16, l + 32 and
+// l + 48 hold the four quarters of a block: its largest magnitude is two register
+// swaps away, and each lane packs its own eight elements.
 constexpr int kSkGroups = 4;                       // row groups of 16
 constexpr int kSkPhases = 4;                       // steps taken in turn
 constexpr int kSkThreads = 64 * kSkGroups * kSkPhases;
 constexpr int kSkDepth = 4;                        // groups of A and B in flight
 
-template <bool kBkr, bool kDrop = false>
+struct PackTo {
+  uint32_t* codes;
+  uint8_t* scales;
+  int64_t padded;      // row length as packed, a multiple of 128
+};
+
+template <bool kBkr, bool kDrop = false, bool kQuant = false>
 __global__ __launch_bounds__(kSkThreads, 1) void k_lora_skinny_stream(const uint16_t* __restrict__ A, int64_t M,
                                                                      int64_t R, int64_t lda,
                                                                      const uint16_t* __restrict__ Bm, int r,
                                                                      int64_t chunk, float* __restrict__ part,
-                                                                     drop::Params d) {
+                                                                     drop::Params d, PackTo to) {
   __shared__ __attribute__((aligned(16))) uint16_t Bs[2][kSkPhases][kTile * kPitch];
   const int t = threadIdx.x;
   const int w = __builtin_amdgcn_readfirstlane(t >> 6), l = t & 63;
@@ -179,7 +190,9 @@ __global__ __launch_bounds__(kSkThreads, 1) void k_lora_skinny_stream(const uint
   const int split = blockIdx.y;
   const int64_t k_beg = split * chunk;
   const int64_t k_end = min(R, k_beg + chunk);
-  const int nsteps = (int)((k_end - k_beg + kTile - 1) / kTile);
+  // the last slice's steps go on to the end of the packed length, over zeros
+  const int64_t k_pack = kQuant ? (k_end == R ? to.padded : k_end) : k_end;
+  const int nsteps = (int)((k_pack - k_beg + kTile - 1) / kTile);
   const int ngroups = (nsteps + kSkPhases - 1) / kSkPhases;   // group gi: steps kSkPhases gi + p
 
   // A operand: lane l reads row m0 + 16 rg + l % 16, columns k + 8 (l / 16) .. +8
@@ -262,6 +275,18 @@ __global__ __launch_bounds__(kSkThreads, 1) void k_lora_skinny_stream(const uint
     const LDS_AS uint16_t* bs = (const LDS_AS uint16_t*)Bs[gi & 1][ph];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
+      if constexpr (kQuant) {
+        const int64_t k = k_beg + (int64_t)(kSkPhases * gi + ph) * kTile + 32 * u;
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) top = max(top, max((av[u][j] << 16) & 0x7FFFFFFFu, av[u][j] & 0x7FFF0000u));
+        const uint32_t sb = mx4::scale_byte(mx4::max_over_rows(top));
+        if (arow < M && k < k_pack) {
+          const int64_t blk = k >> 5;
+          to.codes[(blk * M + arow) * 4 + (l >> 4)] = sb == 255u ? 0u : mx4::encode8(av[u], mx4::scale_f32(sb));
+          if (l < 16) to.scales[((blk >> 2) * M + arow) * 4 + (blk & 3)] = (uint8_t)sb;
+        }
+      }
       if constexpr (kDrop) {
         const int64_t k = k_beg + (int64_t)(kSkPhases * gi + ph) * kTile + 32 * u + akq;
         av[u] = drop::mask8(av[u], d, (uint32_t)arow, (uint32_t)(k >> 3));
@@ -673,10 +698,10 @@ hipError_t launch_lora_skinny(const uint16_t* A, int64_t M, int64_t R, int64_t l
     dim3 grid((unsigned)tiles, (unsigned)sp.splits);
     if (b_is_kr)
       hipLaunchKernelGGL((k_lora_skinny_stream<true>), grid, dim3(kSkThreads), 0, s, A, M, R, lda, B, r, sp.chunk, ws,
-                         drop::Params{});
+                         drop::Params{}, PackTo{});
     else
       hipLaunchKernelGGL((k_lora_skinny_stream<false>), grid, dim3(kSkThreads), 0, s, A, M, R, lda, B, r, sp.chunk, ws,
-                         drop::Params{});
+                         drop::Params{}, PackTo{});
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(k_skinny_reduce, dim3(grid_for((M * r + 3) / 4)), dim3(kThreads), 0, s, ws, sp.splits,
@@ -780,56 +805,80 @@ hipError_t launch_skinny_reduce(const float* part, int slices, int64_t n, float 
 }
 
 // ---- with dropout, and with G kept to 24 bits ---------------------------------
-hipError_t launch_lora_down_drop(const uint16_t* X, int64_t M, int64_t K, const uint16_t* L1, int r,
-                                 const drop::Params& d, uint16_t* T, float* ws, hipStream_t s) {
-  if (d.cut == 0) return launch_lora_skinny(X, M, K, K, L1, true, r, 1.0f, T, ws, s);
+// One pass over A [M, R] (dense): fp32 slices of the skinny product with B, of D o A with
+// d.cut != 0 (L1 only), and A packed into `to` when that is given.
+static hipError_t low_pass(const uint16_t* A, int64_t M, int64_t R, const uint16_t* B, bool b_is_kr, int r,
+                           const drop::Params& d, uint8_t* codes, uint8_t* scales, float* ws, int* slices,
+                           hipStream_t s) {
   const int64_t tiles = (M + kTile - 1) / kTile;
-  SplitPlan sp;
-  if (skinny_stream_ok(X, M, K, K, L1, r)) {
-    sp = plan_stream(tiles, K);
-    hipLaunchKernelGGL((k_lora_skinny_stream<true, true>), dim3((unsigned)tiles, (unsigned)sp.splits), dim3(kSkThreads),
-                       0, s, X, M, K, K, L1, r, sp.chunk, ws, d);
-  } else {
-    sp = plan_rowsplit(tiles, K);
+  if (skinny_stream_ok(A, M, R, R, B, r)) {
+    const SplitPlan sp = plan_stream(tiles, R);
+    const PackTo to{(uint32_t*)codes, scales, mx4::padded(R)};
+    *slices = sp.splits;
     const dim3 grid((unsigned)tiles, (unsigned)sp.splits);
-    if ((K % 8) == 0)
-      hipLaunchKernelGGL((k_lora_skinny<true, true, false, true>), grid, dim3(kThreads), 0, s, X, M, K, K, L1, r,
-                         sp.chunk, ws, d);
-    else
-      hipLaunchKernelGGL((k_lora_skinny<true, false, false, true>), grid, dim3(kThreads), 0, s, X, M, K, K, L1, r,
-                         sp.chunk, ws, d);
+#define QL_LOW(BKR, D, Q)                                                                                           \
+  hipLaunchKernelGGL((k_lora_skinny_stream<BKR, D, Q>), grid, dim3(kSkThreads), 0, s, A, M, R, R, B, r, sp.chunk, ws, \
+                     d, to)
+    if (!b_is_kr) {
+      if (codes) QL_LOW(false, false, true);
+      else QL_LOW(false, false, false);
+    } else if (d.cut) {
+      if (codes) QL_LOW(true, true, true);
+      else QL_LOW(true, true, false);
+    } else {
+      if (codes) QL_LOW(true, false, true);
+      else QL_LOW(true, false, false);
+    }
+#undef QL_LOW
+    return hipGetLastError();
   }
-  hipError_t e = hipGetLastError();
+  if (codes) {
+    const hipError_t e = launch_mx4_quant(A, true, M, R, R, codes, scales, s);
+    if (e != hipSuccess) return e;
+  }
+  const SplitPlan sp = plan_rowsplit(tiles, R);
+  *slices = sp.splits;
+  const dim3 grid((unsigned)tiles, (unsigned)sp.splits);
+  const bool vec = (R % 8) == 0;
+#define QL_LOW(BKR, VA, VB, D)                                                                                     \
+  hipLaunchKernelGGL((k_lora_skinny<BKR, VA, VB, D>), grid, dim3(kThreads), 0, s, A, M, R, R, B, r, sp.chunk, ws, d)
+  if (!b_is_kr) {
+    if (vec) QL_LOW(false, true, true, false);
+    else QL_LOW(false, false, false, false);
+  } else if (d.cut) {
+    if (vec) QL_LOW(true, true, false, true);
+    else QL_LOW(true, false, false, true);
+  } else {
+    if (vec) QL_LOW(true, true, false, false);
+    else QL_LOW(true, false, false, false);
+  }
+#undef QL_LOW
+  return hipGetLastError();
+}
+
+hipError_t launch_lora_down_drop(const uint16_t* X, int64_t M, int64_t K, const uint16_t* L1, int r,
+                                 const drop::Params& d, uint16_t* T, uint8_t* codes, uint8_t* scales, float* ws,
+                                 hipStream_t s) {
+  if (d.cut == 0 && !codes) return launch_lora_skinny(X, M, K, K, L1, true, r, 1.0f, T, ws, s);
+  int slices = 0;
+  const hipError_t e = low_pass(X, M, K, L1, true, r, d, codes, scales, ws, &slices, s);
   if (e != hipSuccess) return e;
-  return launch_skinny_reduce(ws, sp.splits, M * r, d.scale, T, s);
+  return launch_skinny_reduce(ws, slices, M * r, d.cut ? d.scale : 1.0f, T, s);
 }
 
 hipError_t launch_lora_grad_in3(const uint16_t* dY, int64_t M, int64_t N, const uint16_t* L2, int r, float scale,
-                                uint16_t* G, float* ws, hipStream_t s) {
-  const int64_t tiles = (M + kTile - 1) / kTile;
-  SplitPlan sp;
-  if (skinny_stream_ok(dY, M, N, N, L2, r)) {
-    sp = plan_stream(tiles, N);
-    hipLaunchKernelGGL((k_lora_skinny_stream<false>), dim3((unsigned)tiles, (unsigned)sp.splits), dim3(kSkThreads), 0, s,
-                       dY, M, N, N, L2, r, sp.chunk, ws, drop::Params{});
-  } else {
-    sp = plan_rowsplit(tiles, N);
-    const dim3 grid((unsigned)tiles, (unsigned)sp.splits);
-    if ((N % 8) == 0)
-      hipLaunchKernelGGL((k_lora_skinny<false, true, true>), grid, dim3(kThreads), 0, s, dY, M, N, N, L2, r, sp.chunk,
-                         ws, drop::Params{});
-    else
-      hipLaunchKernelGGL((k_lora_skinny<false, false, false>), grid, dim3(kThreads), 0, s, dY, M, N, N, L2, r, sp.chunk,
-                         ws, drop::Params{});
-  }
-  hipError_t e = hipGetLastError();
+                                uint16_t* G, uint8_t* codes, uint8_t* scales, float* ws, hipStream_t s) {
+  int slices = 0;
+  const hipError_t e = low_pass(dY, M, N, L2, false, r, drop::Params{}, codes, scales, ws, &slices, s);
   if (e != hipSuccess) return e;
-  return launch_skinny_reduce(ws, sp.splits, M * r, scale, G, s, true);
+  return launch_skinny_reduce(ws, slices, M * r, scale, G, s, true);
 }
 
 hipError_t launch_lora_grads3(const uint16_t* X, int64_t K, const uint16_t* G, const drop::Params& d, float* dL1,
                               const uint16_t* dY, int64_t N, const uint16_t* T, float scale, float* dL2, int64_t M,
                               int r, float* ws, hipStream_t s) {
+  if (lora_grads_wide_ok(M, K, N, r))
+    return launch_lora_grads_wide(X, K, G, d, dL1, dY, N, T, scale, dL2, M, r, ws, s);
   const bool vec = (K % 8) == 0 && (N % 8) == 0 && (r % 8) == 0;
   float* part1 = ws + (lora_tn_ws(M, K, r) + 255) / 256 * 256 / sizeof(float);
   const SplitPlan sp0 = plan_rowsplit((K + kTile - 1) / kTile, M);
@@ -851,9 +900,19 @@ hipError_t launch_lora_grads3(const uint16_t* X, int64_t K, const uint16_t* G, c
 #undef QL_TN3
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || whole) return e;
-  const int nb0 = grid_for((K * r + 3) / 4);
-  const unsigned nb1 = (unsigned)((N + kTrP - 1) / kTrP);
-  hipLaunchKernelGGL(k_tn_reduce_pair, dim3((unsigned)nb0 + nb1), dim3(kThreads), 0, s, ws, sp0.splits, K, d.scale, dL1,
-                     nb0, part1, sp1.splits, N, scale, dL2, r);
+  return launch_tn_reduce_pair(ws, sp0.splits, K, d.scale, dL1, part1, sp1.splits, N, scale, dL2, r, s);
+}
+
+hipError_t launch_tn_reduce_pair(const float* part0, int splits0, int64_t P0, float scale0, float* out0,
+                                 const float* part1, int splits1, int64_t P1, float scale1, float* out1_t, int r,
+                                 hipStream_t s) {
+  const int nb0 = grid_for((P0 * r + 3) / 4);
+  const unsigned nb1 = (unsigned)((P1 + kTrP - 1) / kTrP);
+  hipLaunchKernelGGL(k_tn_reduce_pair, dim3((unsigned)nb0 + nb1), dim3(kThreads), 0, s, part0, splits0, P0, scale0, out0,
+                     nb0, part1, splits1, P1, scale1, out1_t, r);
   return hipGetLastError();
+}
+
+size_t lora_grads3_ws(int64_t M, int64_t K, int64_t N, int r) {
+  return lora_grads_wide_ok(M, K, N, r) ? lora_grads_wide_ws(M, K, N, r) : lora_tn_pair_ws(M, K, N, r);
 }

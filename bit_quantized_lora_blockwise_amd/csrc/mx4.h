@@ -38,6 +38,14 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t top) {
 
 __device__ __forceinline__ float scale_f32(uint32_t byte) { return __uint_as_float(byte << 23); }
 
+// Largest over lanes l, l ^ 16, l ^ 32, l ^ 48.
+__device__ __forceinline__ uint32_t max_over_rows(uint32_t v) {
+  u32x2 s = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  v = max(s[0], s[1]);
+  s = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return max(s[0], s[1]);
+}
+
 // Eight bf16 (four words) -> eight codes, nearest with ties to even, at most 6.
 __device__ __forceinline__ uint32_t encode8(u32x4 v, float s) {
   uint32_t c = 0;

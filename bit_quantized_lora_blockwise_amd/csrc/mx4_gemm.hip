@@ -640,8 +640,10 @@ __global__ __launch_bounds__(kRT, 2) void k_mx4_gemm_ring(const uint8_t* __restr
             const uint32_t keep =
                 *(const LDS_AS uint32_t*)(bits + (ra + 32 * i) * drop::bit_pitch(kRB) + 4 * (kPT * wp + j)) >> (4 * h);
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              acc[i][j][e] += (keep >> (8 * (e >> 2) + (e & 3))) & 1u ? lo.d.scale * x[e] : 0.0f;
+            for (int e = 0; e < 16; ++e) {   // the bit spread over a word clears what is dropped
+              const uint32_t m = (uint32_t)__builtin_amdgcn_sbfe((int)keep, 8 * (e >> 2) + (e & 3), 1);
+              acc[i][j][e] += lo.d.scale * __uint_as_float(__float_as_uint(x[e]) & m);
+            }
           }
           asm volatile("" ::: "memory");
           __builtin_amdgcn_sched_barrier(0);

@@ -35,14 +35,6 @@ int slice_blocks(int64_t M, int64_t blocks, int r) {
   return kDW * (int)((blocks + kDW * s - 1) / (kDW * s));
 }
 
-// Largest over lanes l, l ^ 16, l ^ 32, l ^ 48.
-__device__ __forceinline__ uint32_t max_over_rows(uint32_t v) {
-  u32x2 s = __builtin_amdgcn_permlane16_swap(v, v, false, false);
-  v = max(s[0], s[1]);
-  s = __builtin_amdgcn_permlane32_swap(v, v, false, false);
-  return max(s[0], s[1]);
-}
-
 // Loads through buffer descriptors: an offset out of range reads as 0 with no branch,
 // so that every load of a round is in flight before the first is used.
 constexpr uint32_t kOOB = 0x80000000u;
