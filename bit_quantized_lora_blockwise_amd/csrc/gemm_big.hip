@@ -144,9 +144,10 @@ __device__ __forceinline__ bf16x8 frag_kmajor_sw(const LDS_AS uint16_t* base, in
 // swizzle), or stage the dX weight tile [64 rows of W][256 columns] through
 // registers into a padded LDS tile that the consumers read with the transposing
 // LDS read.  No dequantisation.
-// kDrop (dX): the adapter term is D o (G L1^T).  The producers draw the tile's
-// decisions into LDS (a bit an element) beside the LoRA operands, and the
-// consumers apply them to the accumulators before the base product.
+// kDrop (dX): the adapter term is D o (G L1^T).  All waves draw the tile's decisions
+// into LDS (a bit an element) while the LoRA operands arrive (by the producers alone,
+// one wave a SIMD, the draws took 12 us a tile), and the consumers apply them to the
+// accumulators before the base product.
 template <bool kDx, bool kTail, bool kB16 = false, bool kDrop = false>
 __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict__ A, int64_t M, int64_t K,
                                                      int64_t N, const uint8_t* __restrict__ codes,
@@ -341,7 +342,7 @@ __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict_
     for (int v = vfirst; v < ntiles; v += vstride) {
     set_tile(v);
     Stage hA, hB, h0;
-    if constexpr (kDrop) drop::fill_bits<kBM, kBP>((LDS_AS uint8_t*)mask, dp, m0, p0, tp, 256);
+    if constexpr (kDrop) drop::fill_bits<kBM, kBP>((LDS_AS uint8_t*)mask, dp, m0, p0, t, kT);
     for (int g = 0; g < ng; ++g) {
       const int64_t gs = kDx ? g : p0 / seg;
       const uint16_t* la_src = LA + gs * M * r;
@@ -516,6 +517,10 @@ __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict_
   for (int i = 0; i < 2; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = f32x16{};
+  if constexpr (kDrop) {
+    drop::fill_bits<kBM, kBP>((LDS_AS uint8_t*)mask, dp, m0, p0, t, kT);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  }
   for (int g = 0; g < ng; ++g) {
     __builtin_amdgcn_s_barrier();          // the producers' LoRA operands are in LDS
     const int ksteps = (r + 15) / 16;

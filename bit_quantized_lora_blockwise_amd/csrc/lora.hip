@@ -377,7 +377,22 @@ __global__ __launch_bounds__(kThreads) void k_skinny_reduce(const float* __restr
 __global__ __launch_bounds__(kThreads) void k_skinny_reduce3(const float* __restrict__ part, int splits, int64_t n,
                                                              float scale, uint16_t* __restrict__ out) {
   const int64_t stride = (int64_t)gridDim.x * kThreads;
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += stride) {
+  const int64_t t0 = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  if ((n & 3) == 0) {
+    const int64_t n4 = n >> 2;
+    for (int64_t i4 = t0; i4 < n4; i4 += stride) {
+      f32x4 x = scale * sum_splits4((const f32x4*)part, splits, n4, i4);
+#pragma unroll
+      for (int j = 0; j < 3; ++j) {
+        const u32x2 h = {qk::pack_bf16x2(x[0], x[1]), qk::pack_bf16x2(x[2], x[3])};
+        *(u32x2*)(out + j * n + 4 * i4) = h;
+        x -= f32x4{__uint_as_float(h[0] << 16), __uint_as_float(h[0] & 0xFFFF0000u), __uint_as_float(h[1] << 16),
+                   __uint_as_float(h[1] & 0xFFFF0000u)};
+      }
+    }
+    return;
+  }
+  for (int64_t i = t0; i < n; i += stride) {
     float s = 0.0f;
     for (int k = 0; k < splits; ++k) s += part[k * n + i];
     float x = scale * s;
@@ -798,7 +813,7 @@ hipError_t launch_lora_tn(const uint16_t* A, int64_t lda, const uint16_t* B, int
 hipError_t launch_skinny_reduce(const float* part, int slices, int64_t n, float scale, uint16_t* out, hipStream_t s,
                                 bool planes) {
   if (planes)
-    hipLaunchKernelGGL(k_skinny_reduce3, dim3(grid_for(n)), dim3(kThreads), 0, s, part, slices, n, scale, out);
+    hipLaunchKernelGGL(k_skinny_reduce3, dim3(grid_for((n + 3) / 4)), dim3(kThreads), 0, s, part, slices, n, scale, out);
   else
     hipLaunchKernelGGL(k_skinny_reduce, dim3(grid_for((n + 3) / 4)), dim3(kThreads), 0, s, part, slices, n, scale, out);
   return hipGetLastError();

@@ -33,10 +33,15 @@ __device__ __forceinline__ State begin(const Params& d, uint32_t m, uint32_t q) 
   return State{q, m, d.o0, d.o1, d.k0, d.k1};
 }
 
+// In one instruction (the compiler makes two of a ^ b ^ c).
+__device__ __forceinline__ uint32_t xor3(uint32_t a, uint32_t b, uint32_t c) {
+  return (uint32_t)__builtin_amdgcn_bitop3_b32((int)a, (int)b, (int)c, 0x96);
+}
+
 __device__ __forceinline__ void round(State& s) {
   const uint64_t a = (uint64_t)s.c0 * 0xD2511F53u, b = (uint64_t)s.c2 * 0xCD9E8D57u;
-  s.c0 = (uint32_t)(b >> 32) ^ s.c1 ^ s.k0;
-  s.c2 = (uint32_t)(a >> 32) ^ s.c3 ^ s.k1;
+  s.c0 = xor3((uint32_t)(b >> 32), s.c1, s.k0);
+  s.c2 = xor3((uint32_t)(a >> 32), s.c3, s.k1);
   s.c1 = (uint32_t)b;
   s.c3 = (uint32_t)a;
   s.k0 += 0x9E3779B9u;
