@@ -24,12 +24,12 @@ bool layer_ok(int64_t M, int64_t K, int64_t N, int r) {
          mx4::code_bytes(M, K) < kLim && mx4::code_bytes(M, N) < kLim;
 }
 
-// [packed activations: codes, scales][T or the three planes of G][T of a backward without one][fp32 partials]
+// [packed activations: codes, scales][T or the three planes of G][dense G][T of a backward without one][fp32 partials]
 struct Ws {
-  size_t codes, scales, low, t, part, total;
+  size_t codes, scales, low, dense, t, part, total;
 };
 Ws fwd_ws(int64_t M, int64_t K, int r) {
-  Ws w{round_up(mx4::code_bytes(M, K)), round_up(mx4::scale_bytes(M, K)), round_up((size_t)M * r * 2), 0,
+  Ws w{round_up(mx4::code_bytes(M, K)), round_up(mx4::scale_bytes(M, K)), round_up((size_t)M * r * 2), 0, 0,
        round_up(std::max(lora_skinny_ws(M, K, r), mx4_small_ws(M, r))), 0};
   w.total = w.codes + w.scales + w.low + w.part;
   return w;
@@ -37,10 +37,11 @@ Ws fwd_ws(int64_t M, int64_t K, int r) {
 // packed = false: the backward over another base, which multiplies the bf16 gradient
 Ws bwd_ws(int64_t M, int64_t K, int64_t N, int r, bool packed) {
   Ws w{packed ? round_up(mx4::code_bytes(M, N)) : 0, packed ? round_up(mx4::scale_bytes(M, N)) : 0,
-       round_up((size_t)3 * M * r * 2), round_up((size_t)M * r * 2), 0, 0};
+       round_up((size_t)3 * M * g_pitch(r) * 2), r == g_pitch(r) ? 0 : round_up((size_t)M * r * 2),
+       round_up((size_t)M * r * 2), 0, 0};
   w.part = round_up(std::max({lora_skinny_ws(M, N, r), lora_skinny_ws(M, K, r), lora_grads3_ws(M, K, N, r),
                               packed ? mx4_small_ws(M, r) : 0}));
-  w.total = w.codes + w.scales + w.low + w.t + w.part;
+  w.total = w.codes + w.scales + w.low + w.dense + w.t + w.part;
   return w;
 }
 
@@ -147,8 +148,9 @@ int mx4_linear_bwd(const uint16_t* X, const uint16_t* dY, int64_t M, int64_t K, 
   hipStream_t s = (hipStream_t)stream;
   uint8_t* ac = (uint8_t*)workspace;
   uint8_t* as = ac + w.codes;
-  uint16_t* G = (uint16_t*)(as + w.scales);
-  uint16_t* Tw = (uint16_t*)((uint8_t*)G + w.low);
+  uint8_t* low = as + w.scales;
+  const GPlanes G{(uint16_t*)low, (uint16_t*)(w.dense ? low + w.low : low)};
+  uint16_t* Tw = (uint16_t*)(low + w.low + w.dense);
   float* part = (float*)((uint8_t*)Tw + w.t);
   const bool small = mx4_small_ok(M, K);
   if (!T) {
@@ -157,14 +159,14 @@ int mx4_linear_bwd(const uint16_t* X, const uint16_t* dY, int64_t M, int64_t K, 
     T = Tw;
   }
   if (dX && small) {
-    QL_TRY(launch_mx4_small_dx(dY, M, K, N, codes_t, scales_t, L1, L2, r, lora_scale, d, dX, G, ac, as, part, s));
+    QL_TRY(launch_mx4_small_dx(dY, M, K, N, codes_t, scales_t, L1, L2, r, lora_scale, d, dX, G.planes, ac, as, part, s));
   } else if (small) {
-    QL_TRY(launch_mx4_small_g(dY, M, N, L2, r, lora_scale, G, part, s));
+    QL_TRY(launch_mx4_small_g(dY, M, N, L2, r, lora_scale, G.planes, part, s));
   } else {
     QL_TRY(launch_lora_grad_in3(dY, M, N, L2, r, lora_scale, G, dX ? ac : nullptr, as, part, s));
-    if (dX) QL_TRY(launch_mx4_gemm(ac, as, M, codes_t, scales_t, K, N, Mx4Lora{G, L1, r, true, 1.0f, d}, dX, s));
+    if (dX) QL_TRY(launch_mx4_gemm(ac, as, M, codes_t, scales_t, K, N, Mx4Lora{G.dense, L1, r, true, 1.0f, d}, dX, s));
   }
-  QL_TRY(launch_lora_grads3(X, K, G, d, dL1, dY, N, T, lora_scale, dL2, M, r, part, s));
+  QL_TRY(launch_lora_grads3(X, K, G.planes, d, dL1, dY, N, T, lora_scale, dL2, M, r, part, s));
   return QL_OK;
 }
 
@@ -211,8 +213,9 @@ int qlora_linear_bwd_dropout(const uint16_t* X, const uint16_t* dY, int64_t M, i
   if (!workspace || ws_bytes < w.total) return QL_ERR_WORKSPACE;
   if (!aligned16(workspace)) return QL_ERR_ALIGN;
   hipStream_t s = (hipStream_t)stream;
-  uint16_t* G = (uint16_t*)workspace;
-  uint16_t* Tw = (uint16_t*)((uint8_t*)G + w.low);
+  uint8_t* low = (uint8_t*)workspace;
+  const GPlanes G{(uint16_t*)low, (uint16_t*)(w.dense ? low + w.low : low)};
+  uint16_t* Tw = (uint16_t*)(low + w.low + w.dense);
   float* part = (float*)((uint8_t*)Tw + w.t);
   if (!T) {
     QL_TRY(launch_lora_down_drop(X, M, K, L1, r, d, Tw, nullptr, nullptr, part, s));
@@ -221,11 +224,11 @@ int qlora_linear_bwd_dropout(const uint16_t* X, const uint16_t* dY, int64_t M, i
   QL_TRY(launch_lora_grad_in3(dY, M, N, L2, r, lora_scale, G, nullptr, nullptr, part, s));
   if (dX) {
     if (qgemm_big_ok(true, M, K, N))
-      QL_TRY(launch_qgemm_big(true, dY, M, K, N, codes, c2, c1, G, L1, r, 1.0f, dX, s, 1, &d));
+      QL_TRY(launch_qgemm_big(true, dY, M, K, N, codes, c2, c1, G.dense, L1, r, 1.0f, dX, s, 1, &d));
     else
-      QL_TRY(launch_qgemm_dx(dY, M, K, N, codes, c2, c1, G, L1, r, dX, s, &d));
+      QL_TRY(launch_qgemm_dx(dY, M, K, N, codes, c2, c1, G.dense, L1, r, dX, s, &d));
   }
-  QL_TRY(launch_lora_grads3(X, K, G, d, dL1, dY, N, T, lora_scale, dL2, M, r, part, s));
+  QL_TRY(launch_lora_grads3(X, K, G.planes, d, dL1, dY, N, T, lora_scale, dL2, M, r, part, s));
   return QL_OK;
 }
 

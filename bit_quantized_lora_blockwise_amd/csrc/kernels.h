@@ -65,10 +65,17 @@ int64_t decode_t_rows(int64_t K);   // rows of K per slice (a multiple of 32)
 bool decode_t_ok(int64_t M, int64_t K, const void* X, const void* L1);
 hipError_t launch_lora_part(const uint16_t* X, int64_t M, int64_t K, const uint16_t* L1, int r, float* part,
                             hipStream_t s, int G = 1);
-// out[i] = bf16(scale * (part[i] + part[n + i] + ...)), slices added in order; planes:
-// as three bf16 planes out[i], out[n + i], out[2 n + i] whose sum it is.
-hipError_t launch_skinny_reduce(const float* part, int slices, int64_t n, float scale, uint16_t* out, hipStream_t s,
-                                bool planes = false);
+// out[i] = bf16(scale * (part[i] + part[n + i] + ...)), slices added in order.
+hipError_t launch_skinny_reduce(const float* part, int slices, int64_t n, float scale, uint16_t* out, hipStream_t s);
+// G = scale * (sum of the slices) [M, r] to 24 bits: three bf16 planes of pitch
+// g_pitch(r) whose sum it is, and the first of them (bf16(G)) as a dense [M, r].
+inline int g_pitch(int r) { return (r + 7) / 8 * 8; }
+struct GPlanes {
+  uint16_t* planes;     // [3][M][g_pitch(r)]
+  uint16_t* dense;      // [M][r]; the first plane itself where r is its pitch
+};
+hipError_t launch_skinny_reduce3(const float* part, int slices, int64_t M, int r, float scale, const GPlanes& g,
+                                 hipStream_t s);
 hipError_t launch_lora_skinny(const uint16_t* A, int64_t M, int64_t R, int64_t lda, const uint16_t* B, bool b_is_kr,
                               int r, float scale, uint16_t* out, float* ws, hipStream_t s);
 
@@ -88,15 +95,14 @@ hipError_t launch_lora_tn(const uint16_t* A, int64_t lda, const uint16_t* B, int
 // The adapter branch with dropout on its input (d.cut = 0: none) and G to 24 bits:
 //   T = bf16((D o X) L1); ws as lora_skinny_ws(M, K, r).  With `codes`, the same pass
 //     also packs X (not D o X) in microscaled 4-bit; G and dY likewise
-//   G = scale dY L2^T as three bf16 planes [3][M, r] whose sum it is (the first one
-//     is bf16(G)); ws as lora_skinny_ws(M, N, r)
+//   G = scale dY L2^T; ws as lora_skinny_ws(M, N, r)
 //   dL1 [K, r] = (D o X)^T G from the planes, dL2 [r, N] = scale T^T dY, fp32; ws as
 //     lora_grads3_ws(M, K, N, r).  Many rows of 16-byte pieces go to lora_grads.hip.
 hipError_t launch_lora_down_drop(const uint16_t* X, int64_t M, int64_t K, const uint16_t* L1, int r,
                                  const drop::Params& d, uint16_t* T, uint8_t* codes, uint8_t* scales, float* ws,
                                  hipStream_t s);
 hipError_t launch_lora_grad_in3(const uint16_t* dY, int64_t M, int64_t N, const uint16_t* L2, int r, float scale,
-                                uint16_t* G, uint8_t* codes, uint8_t* scales, float* ws, hipStream_t s);
+                                const GPlanes& G, uint8_t* codes, uint8_t* scales, float* ws, hipStream_t s);
 hipError_t launch_lora_grads3(const uint16_t* X, int64_t K, const uint16_t* G, const drop::Params& d, float* dL1,
                               const uint16_t* dY, int64_t N, const uint16_t* T, float scale, float* dL2, int64_t M,
                               int r, float* ws, hipStream_t s);
@@ -137,7 +143,7 @@ hipError_t launch_mx4_gemm(const uint8_t* ac, const uint8_t* as, int64_t M, cons
 
 // The layer for few rows (mx4_small.hip): one call quantises the activations (into ac,
 // as), forms T or G and multiplies.  part: mx4_small_ws bytes.  Forward: T_out may be
-// nullptr.  Backward: G receives the three planes of launch_lora_grad_in3.
+// nullptr.  Backward: G receives the planes alone.
 bool mx4_small_ok(int64_t M, int64_t P);   // P: columns of the result
 size_t mx4_small_ws(int64_t M, int r);
 hipError_t launch_mx4_small_fwd(const uint16_t* X, int64_t M, int64_t K, int64_t N, const uint8_t* bc, const uint8_t* bs,

@@ -370,50 +370,59 @@ __global__ __launch_bounds__(kThreads) void k_skinny_reduce(const float* __restr
   }
 }
 
-// The same sum kept to 24 bits as three bf16 planes out[i], out[n + i], out[2 n + i]
-// whose sum it is: each plane takes what the ones before it rounded off (exact in
-// fp32), so a product with the planes loses nothing that fp32 would keep, while
-// the first plane alone is the bf16 rounding.
-__global__ __launch_bounds__(kThreads) void k_skinny_reduce3(const float* __restrict__ part, int splits, int64_t n,
-                                                             float scale, uint16_t* __restrict__ out) {
-  const int64_t stride = (int64_t)gridDim.x * kThreads;
+// The same sum kept to 24 bits as three bf16 planes [M][rp] (rp = r rounded up to 8,
+// zeros past r) whose sum it is: each plane takes what the ones before it rounded
+// off (exact in fp32), so a product with the planes loses nothing that fp32 would
+// keep, while the first plane alone is the bf16 rounding.  Whole 16-byte pieces
+// whatever r is: the planes are read again for every 64 columns of the activation.
+// dense (rp != r): the first plane as [M][r] too.
+__global__ __launch_bounds__(kThreads) void k_skinny_reduce3(const float* __restrict__ part, int splits, int64_t M, int r,
+                                                             int rp, float scale, uint16_t* __restrict__ out,
+                                                             uint16_t* __restrict__ dense) {
+  const int64_t stride = (int64_t)gridDim.x * kThreads, n = M * rp;
   const int64_t t0 = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  if ((n & 3) == 0) {
-    const int64_t n4 = n >> 2;
-    for (int64_t i4 = t0; i4 < n4; i4 += stride) {
-      f32x4 x = scale * sum_splits4((const f32x4*)part, splits, n4, i4);
+  for (int64_t i4 = t0; i4 < n / 4; i4 += stride) {
+    f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+    int64_t at = 0;
+    int c = 0;
+    if (r == rp) {
+      x = scale * sum_splits4((const f32x4*)part, splits, n >> 2, i4);
+    } else {
+      const int64_t m = 4 * i4 / rp;
+      c = (int)(4 * i4 - m * rp);
+      at = m * r + c;
 #pragma unroll
-      for (int j = 0; j < 3; ++j) {
-        const u32x2 h = {qk::pack_bf16x2(x[0], x[1]), qk::pack_bf16x2(x[2], x[3])};
-        *(u32x2*)(out + j * n + 4 * i4) = h;
-        x -= f32x4{__uint_as_float(h[0] << 16), __uint_as_float(h[0] & 0xFFFF0000u), __uint_as_float(h[1] << 16),
-                   __uint_as_float(h[1] & 0xFFFF0000u)};
+      for (int j = 0; j < 4; ++j) {
+        float s = 0.0f;
+        if (c + j < r)
+          for (int k = 0; k < splits; ++k) s += part[k * M * r + at + j];
+        x[j] = scale * s;
       }
     }
-    return;
-  }
-  for (int64_t i = t0; i < n; i += stride) {
-    float s = 0.0f;
-    for (int k = 0; k < splits; ++k) s += part[k * n + i];
-    float x = scale * s;
 #pragma unroll
     for (int j = 0; j < 3; ++j) {
-      const uint16_t h = qk::f32_to_bf16(x);
-      out[j * n + i] = h;
-      x -= qk::bf16_to_f32(h);
+      const u32x2 h = {qk::pack_bf16x2(x[0], x[1]), qk::pack_bf16x2(x[2], x[3])};
+      *(u32x2*)(out + j * n + 4 * i4) = h;
+      if (j == 0 && dense) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (c + e < r) dense[at + e] = (uint16_t)(h[e >> 1] >> (16 * (e & 1)));
+      }
+      x -= f32x4{__uint_as_float(h[0] << 16), __uint_as_float(h[0] & 0xFFFF0000u), __uint_as_float(h[1] << 16),
+                 __uint_as_float(h[1] & 0xFFFF0000u)};
     }
   }
 }
 
 // C[p, c] partial over one slice of m: sum_m A[m][p] * B[m][c], A [M, P], B [M, r];
 // this work group's tile of 64 p is `tile`, its slice of m is `split`.  kDrop: of
-// D o A, not scaled.  kPlanes: B is the sum of that many matrices, B + j M r.
+// D o A, not scaled.  kPlanes: B is the sum of that many matrices, B + j M ldb.
 // lds: (2 + 2 kPlanes) tiles of kTile * kPitch.  scale: of what is written; tr: written
 // as part[c][p] (both for a product of one slice, whose partial is the result).
 template <bool kVecA, bool kVecB, bool kDrop = false, int kPlanes = 1>
 __device__ __forceinline__ void tn_tile(const uint16_t* __restrict__ A, int64_t lda, const uint16_t* __restrict__ B,
                                         int64_t M, int64_t P, int r, int64_t chunk, float* __restrict__ part,
-                                        int tile, int split, uint16_t* lds, const drop::Params& d,
+                                        int tile, int split, uint16_t* lds, const drop::Params& d, int ldb,
                                         float scale = 1.0f, bool tr = false) {
   LDS_AS uint16_t* const sm = (LDS_AS uint16_t*)lds;
   auto abuf = [&](int64_t b) { return sm + (b & 1) * kTile * kPitch; };
@@ -434,7 +443,7 @@ __device__ __forceinline__ void tn_tile(const uint16_t* __restrict__ A, int64_t 
     ta = load_tile<kVecA>(A + mmc * lda + p0, lda, ml, P - p0, (uint64_t)((M - mmc) * lda - p0) * 2);   // [m][p]
 #pragma unroll
     for (int j = 0; j < kPlanes; ++j)
-      tb.p[j] = load_tile<kVecB>(B + (j * M + mmc) * r, r, ml, r, (uint64_t)((M - mmc) * r) * 2);       // [m][c]
+      tb.p[j] = load_tile<kVecB>(B + (j * M + mmc) * ldb, ldb, ml, r, (uint64_t)((M - mmc) * ldb) * 2);   // [m][c]
   };
   auto store = [&](int64_t st, Tile& ta, const BTiles& tb) {
     if constexpr (kDrop) drop_tile(ta, d, m_beg + st * kTile, p0);
@@ -482,7 +491,7 @@ __global__ __launch_bounds__(kThreads) void k_lora_tn(const uint16_t* __restrict
                                                       const uint16_t* __restrict__ B, int64_t M, int64_t P, int r,
                                                       int64_t chunk, float* __restrict__ part) {
   __shared__ __attribute__((aligned(16))) uint16_t lds[4 * kTile * kPitch];
-  tn_tile<kVecA, kVecB>(A, lda, B, M, P, r, chunk, part, blockIdx.x, blockIdx.y, lds, drop::Params{});
+  tn_tile<kVecA, kVecB>(A, lda, B, M, P, r, chunk, part, blockIdx.x, blockIdx.y, lds, drop::Params{}, r);
 }
 
 // Two independent products of this kind in one launch (the backward's dL1 and
@@ -503,23 +512,25 @@ __global__ __launch_bounds__(kThreads) void k_lora_tn_pair(TnJob j0, TnJob j1, i
   const TnJob j = second ? j1 : j0;
   const int b = second ? (int)blockIdx.x - n0 : (int)blockIdx.x;
   __shared__ __attribute__((aligned(16))) uint16_t lds[4 * kTile * kPitch];
-  tn_tile<kVecA, kVecB>(j.A, j.lda, j.B, M, j.P, r, j.chunk, j.part, b % j.tiles, b / j.tiles, lds, drop::Params{});
+  tn_tile<kVecA, kVecB>(j.A, j.lda, j.B, M, j.P, r, j.chunk, j.part, b % j.tiles, b / j.tiles, lds, drop::Params{},
+                        r);
 }
 
-// The pair with dropout on the first product's A and its B in three planes.  With
-// one slice each, j0.part and j1.part are the results: scaled, the second transposed.
-template <bool kVec, bool kDrop>
-__global__ __launch_bounds__(kThreads) void k_lora_tn_pair3(TnJob j0, TnJob j1, int64_t M, int r, drop::Params d,
-                                                            float scale0, float scale1, bool whole) {
+// The pair with dropout on the first product's A and its B in three planes of pitch
+// rp.  With one slice each, j0.part and j1.part are the results: scaled, the second
+// transposed.
+template <bool kVecA, bool kVecT, bool kDrop>
+__global__ __launch_bounds__(kThreads) void k_lora_tn_pair3(TnJob j0, TnJob j1, int64_t M, int r, int rp,
+                                                            drop::Params d, float scale0, float scale1, bool whole) {
   __shared__ __attribute__((aligned(16))) uint16_t lds[8 * kTile * kPitch];
   const int n0 = j0.tiles * j0.splits;
   const int b = (int)blockIdx.x;
   if (b < n0)
-    tn_tile<kVec, kVec, kDrop, 3>(j0.A, j0.lda, j0.B, M, j0.P, r, j0.chunk, j0.part, b % j0.tiles, b / j0.tiles, lds, d,
-                                  scale0);
+    tn_tile<kVecA, true, kDrop, 3>(j0.A, j0.lda, j0.B, M, j0.P, r, j0.chunk, j0.part, b % j0.tiles, b / j0.tiles, lds, d,
+                                   rp, scale0);
   else
-    tn_tile<kVec, kVec>(j1.A, j1.lda, j1.B, M, j1.P, r, j1.chunk, j1.part, (b - n0) % j1.tiles, (b - n0) / j1.tiles,
-                        lds, d, scale1, whole);
+    tn_tile<kVecA, kVecT>(j1.A, j1.lda, j1.B, M, j1.P, r, j1.chunk, j1.part, (b - n0) % j1.tiles, (b - n0) / j1.tiles,
+                          lds, d, r, scale1, whole);
 }
 
 // out[i] = scale * (sum of the slices), i over P * r, by work groups blk of nblk.
@@ -810,12 +821,16 @@ hipError_t launch_lora_tn(const uint16_t* A, int64_t lda, const uint16_t* B, int
   return hipGetLastError();
 }
 
-hipError_t launch_skinny_reduce(const float* part, int slices, int64_t n, float scale, uint16_t* out, hipStream_t s,
-                                bool planes) {
-  if (planes)
-    hipLaunchKernelGGL(k_skinny_reduce3, dim3(grid_for((n + 3) / 4)), dim3(kThreads), 0, s, part, slices, n, scale, out);
-  else
-    hipLaunchKernelGGL(k_skinny_reduce, dim3(grid_for((n + 3) / 4)), dim3(kThreads), 0, s, part, slices, n, scale, out);
+hipError_t launch_skinny_reduce(const float* part, int slices, int64_t n, float scale, uint16_t* out, hipStream_t s) {
+  hipLaunchKernelGGL(k_skinny_reduce, dim3(grid_for((n + 3) / 4)), dim3(kThreads), 0, s, part, slices, n, scale, out);
+  return hipGetLastError();
+}
+
+hipError_t launch_skinny_reduce3(const float* part, int slices, int64_t M, int r, float scale, const GPlanes& g,
+                                 hipStream_t s) {
+  const int rp = g_pitch(r);
+  hipLaunchKernelGGL(k_skinny_reduce3, dim3(grid_for(M * rp / 4)), dim3(kThreads), 0, s, part, slices, M, r, rp, scale,
+                     g.planes, rp == r ? nullptr : g.dense);
   return hipGetLastError();
 }
 
@@ -882,11 +897,11 @@ hipError_t launch_lora_down_drop(const uint16_t* X, int64_t M, int64_t K, const 
 }
 
 hipError_t launch_lora_grad_in3(const uint16_t* dY, int64_t M, int64_t N, const uint16_t* L2, int r, float scale,
-                                uint16_t* G, uint8_t* codes, uint8_t* scales, float* ws, hipStream_t s) {
+                                const GPlanes& G, uint8_t* codes, uint8_t* scales, float* ws, hipStream_t s) {
   int slices = 0;
   const hipError_t e = low_pass(dY, M, N, L2, false, r, drop::Params{}, codes, scales, ws, &slices, s);
   if (e != hipSuccess) return e;
-  return launch_skinny_reduce(ws, slices, M * r, scale, G, s, true);
+  return launch_skinny_reduce3(ws, slices, M, r, scale, G, s);
 }
 
 hipError_t launch_lora_grads3(const uint16_t* X, int64_t K, const uint16_t* G, const drop::Params& d, float* dL1,
@@ -894,7 +909,7 @@ hipError_t launch_lora_grads3(const uint16_t* X, int64_t K, const uint16_t* G, c
                               int r, float* ws, hipStream_t s) {
   if (lora_grads_wide_ok(M, K, N, r))
     return launch_lora_grads_wide(X, K, G, d, dL1, dY, N, T, scale, dL2, M, r, ws, s);
-  const bool vec = (K % 8) == 0 && (N % 8) == 0 && (r % 8) == 0;
+  const bool vec = (K % 8) == 0 && (N % 8) == 0, vect = (r % 8) == 0;
   float* part1 = ws + (lora_tn_ws(M, K, r) + 255) / 256 * 256 / sizeof(float);
   const SplitPlan sp0 = plan_rowsplit((K + kTile - 1) / kTile, M);
   const SplitPlan sp1 = plan_rowsplit((N + kTile - 1) / kTile, M);
@@ -903,15 +918,19 @@ hipError_t launch_lora_grads3(const uint16_t* X, int64_t K, const uint16_t* G, c
   const TnJob j1{dY, N, T, N, sp1.chunk, whole ? dL2 : part1, (int)((N + kTile - 1) / kTile), sp1.splits};
   const float s0 = whole ? d.scale : 1.0f, s1 = whole ? scale : 1.0f;
   const unsigned nwg = (unsigned)(j0.tiles * j0.splits + j1.tiles * j1.splits);
-#define QL_TN3(V, D) hipLaunchKernelGGL((k_lora_tn_pair3<V, D>), dim3(nwg), dim3(kThreads), 0, s, j0, j1, M, r, d, s0, \
-                                       s1, whole)
-  if (vec) {
-    if (d.cut) QL_TN3(true, true);
-    else QL_TN3(true, false);
-  } else {
-    if (d.cut) QL_TN3(false, true);
-    else QL_TN3(false, false);
-  }
+#define QL_TN3(V, T)                                                                                                \
+  do {                                                                                                              \
+    if (d.cut)                                                                                                      \
+      hipLaunchKernelGGL((k_lora_tn_pair3<V, T, true>), dim3(nwg), dim3(kThreads), 0, s, j0, j1, M, r, g_pitch(r), d, \
+                         s0, s1, whole);                                                                            \
+    else                                                                                                            \
+      hipLaunchKernelGGL((k_lora_tn_pair3<V, T, false>), dim3(nwg), dim3(kThreads), 0, s, j0, j1, M, r, g_pitch(r), d, \
+                         s0, s1, whole);                                                                            \
+  } while (0)
+  if (vec && vect) QL_TN3(true, true);
+  else if (vec) QL_TN3(true, false);
+  else if (vect) QL_TN3(false, true);
+  else QL_TN3(false, false);
 #undef QL_TN3
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || whole) return e;

@@ -123,7 +123,8 @@ struct SmallArgs {
   const float* part;                // slices of T or G, [S][M][r]
   int S;
   float low_scale;                  // T = bf16(low_scale sum), G likewise
-  uint16_t* low_out;                // T [M, r] or G's three planes, may be nullptr (T)
+  uint16_t* low_out;                // T [M, r] (may be nullptr) or G's three planes
+  int low_pitch;                    // of those planes
   const uint16_t* LB;               // L2 [r, P] (forward), L1 [P, r] (backward)
   int r;
   float scale;                      // forward: Y += scale (T L2)
@@ -197,7 +198,7 @@ __global__ __launch_bounds__(64 * (kPW + 2 * kMG), kMG == 1 ? 8 : 4) void k_mx4_
     }
   }
   // sums over the slices, in order
-  const int64_t plane = (int64_t)a.M * a.r;
+  const int64_t plane = (int64_t)a.M * a.r;             // of the slices
   const __amdgpu_buffer_rsrc_t rp = rsrc(a.part, (uint64_t)a.S * plane * 4);
   const uint32_t at = 4u * (uint32_t)(min(ml, a.M - 1) * a.r + c);
   float sum[8];
@@ -228,17 +229,20 @@ __global__ __launch_bounds__(64 * (kPW + 2 * kMG), kMG == 1 ? 8 : 4) void k_mx4_
                                                      f32x4{0, 0, 0, 0}, 0, 0, 0);
   }
   if (a.low_out && blockIdx.x == 0 && ml < a.M) {
+    // T [M][r]; G's planes (k_skinny_reduce3) [3][M][pitch], zeros past the rank
+    const int pitch = kMode == 1 ? a.r : a.low_pitch;
+    const int64_t gp = (int64_t)a.M * pitch;
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-      if (c + k < a.r) {
-        uint16_t* o = a.low_out + (int64_t)ml * a.r + c + k;
+      if (c + k < pitch) {
+        uint16_t* o = a.low_out + (int64_t)ml * pitch + c + k;
         uint16_t hi = qk::f32_to_bf16(sum[k]);
         o[0] = hi;
-        if constexpr (kMode != 1) {        // G to 24 bits: each plane what the ones before rounded off
+        if constexpr (kMode != 1) {
           const float rest = sum[k] - qk::bf16_to_f32(hi);
           hi = qk::f32_to_bf16(rest);
-          o[plane] = hi;
-          o[2 * plane] = qk::f32_to_bf16(rest - qk::bf16_to_f32(hi));
+          o[gp] = hi;
+          o[2 * gp] = qk::f32_to_bf16(rest - qk::bf16_to_f32(hi));
         }
       }
   }
@@ -345,8 +349,8 @@ hipError_t launch_mx4_small_fwd(const uint16_t* X, int64_t M, int64_t K, int64_t
   hipError_t e = launch_down<true>(X, M, K, L1, r, d, ac, as, part, &S, s);
   if (e != hipSuccess) return e;
   return launch_product<1>(SmallArgs{(const uint32_t*)ac, (const uint32_t*)as, (const uint32_t*)bc, (const uint32_t*)bs,
-                                     (int)M, (int)N, (int)(padded(K) / kPad), part, S, d.cut ? d.scale : 1.0f, T_out, L2,
-                                     r, scale, drop::Params{}, Y},
+                                     (int)M, (int)N, (int)(padded(K) / kPad), part, S, d.cut ? d.scale : 1.0f, T_out, r,
+                                     L2, r, scale, drop::Params{}, Y},
                            s);
 }
 
@@ -357,7 +361,7 @@ hipError_t launch_mx4_small_dx(const uint16_t* dY, int64_t M, int64_t K, int64_t
   hipError_t e = launch_down<false>(dY, M, N, L2, r, drop::Params{}, ac, as, part, &S, s);
   if (e != hipSuccess) return e;
   const SmallArgs a{(const uint32_t*)ac, (const uint32_t*)as, (const uint32_t*)bc, (const uint32_t*)bs, (int)M, (int)K,
-                    (int)(padded(N) / kPad), part, S, scale, G, L1, r, 1.0f, d, dX};
+                    (int)(padded(N) / kPad), part, S, scale, G, g_pitch(r), L1, r, 1.0f, d, dX};
   return d.cut ? launch_product<3>(a, s) : launch_product<2>(a, s);
 }
 
@@ -374,5 +378,5 @@ hipError_t launch_mx4_small_g(const uint16_t* dY, int64_t M, int64_t N, const ui
   int S = 0;
   hipError_t e = launch_down<false>(dY, M, N, L2, r, drop::Params{}, nullptr, nullptr, part, &S, s);
   if (e != hipSuccess) return e;
-  return launch_skinny_reduce(part, S, M * r, scale, G, s, true);
+  return launch_skinny_reduce3(part, S, M, r, scale, GPlanes{G, nullptr}, s);
 }
