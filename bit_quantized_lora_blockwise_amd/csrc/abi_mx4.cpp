@@ -192,7 +192,16 @@ int qlora_linear_fwd_dropout(const uint16_t* X, int64_t M, int64_t K, int64_t N,
   uint16_t* T = T_out ? T_out : (uint16_t*)workspace;
   float* part = (float*)((char*)workspace + round_up((size_t)M * r * 2));
   QL_TRY(launch_lora_down_drop(X, M, K, L1, r, d, T, nullptr, nullptr, part, (hipStream_t)stream));
-  return qlora_linear_fwd_t(X, M, K, N, codes, c2, c1, T, L2, r, lora_scale, Y, stream);
+  // The decode kernel takes 16 rows; up to three passes of it over the packed weight stay
+  // below the 256-row tiles of the large kernel (48 rows: 4096 -> 11008 41 and 80 us,
+  // 11008 -> 4096 47 and 204 us, 8192 -> 22016 115 and 152 us, 512 -> 512 11 and 19 us).
+  const int64_t step = M <= 48 ? 16 : M;
+  for (int64_t m = 0; m < M; m += step) {
+    const int e = qlora_linear_fwd_t(X + m * K, std::min(step, M - m), K, N, codes, c2, c1, T + m * r, L2, r, lora_scale,
+                                     Y + m * N, stream);
+    if (e != QL_OK) return e;
+  }
+  return QL_OK;
 }
 
 size_t qlora_linear_bwd_dropout_workspace(int64_t M, int64_t K, int64_t N, int r) {
@@ -223,7 +232,9 @@ int qlora_linear_bwd_dropout(const uint16_t* X, const uint16_t* dY, int64_t M, i
   }
   QL_TRY(launch_lora_grad_in3(dY, M, N, L2, r, lora_scale, G, nullptr, nullptr, part, s));
   if (dX) {
-    if (qgemm_big_ok(true, M, K, N))
+    if (d.cut && dx_small_ok(M, K))
+      QL_TRY(launch_dx_small(dY, M, K, N, codes, c2, c1, G.dense, L1, r, dX, d, s));
+    else if (qgemm_big_ok(true, M, K, N))
       QL_TRY(launch_qgemm_big(true, dY, M, K, N, codes, c2, c1, G.dense, L1, r, 1.0f, dX, s, 1, &d));
     else
       QL_TRY(launch_qgemm_dx(dY, M, K, N, codes, c2, c1, G.dense, L1, r, dX, s, &d));

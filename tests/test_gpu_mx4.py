@@ -282,8 +282,9 @@ def test_large_matmul(M, N, K):
     test_matmul(M, N, K)
 
 
-NF4 = [(1, 64, 1, 1), (1, 4096, 300, 64), (16, 512, 136, 8), (17, 512, 200, 12), (32, 512, 512, 8), (130, 576, 333, 5),
-       (300, 1152, 264, 64), (260, 320, 520, 16)]
+NF4 = [(1, 64, 1, 1), (1, 4096, 300, 64), (16, 512, 136, 8), (17, 512, 200, 12), (32, 512, 512, 8), (33, 704, 71, 20),
+       (48, 128, 1000, 64), (63, 1024, 96, 3), (130, 576, 333, 5), (300, 1152, 264, 64), (260, 320, 520, 16),
+       (520, 4224, 72, 8)]
 
 
 @pytest.mark.parametrize("M,K,N,r", NF4)
