@@ -44,7 +44,53 @@ struct Nf4Buckets {
 // margin below is 2.3 times that.
 static constexpr float kNf4Near = 0x1p-17f;
 
+// 16 bytes at any 2- or 4-byte boundary: one global load or store all the same (the
+// target's memory operations take unaligned addresses), so that rows of any length
+// move in 16-byte pieces.
+typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
+typedef f32x4 f32x4_a4 __attribute__((aligned(4)));
+
 namespace qk {
+
+// Eight bf16 moved down by s (0 .. 8) places, zeros behind them.
+__device__ __forceinline__ u32x4 drop_front8(u32x4 v, int s) {
+  uint32_t d[5] = {v[0], v[1], v[2], v[3], 0};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) d[j] = s >= 4 ? (j < 2 ? d[j + 2] : 0u) : d[j];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) d[j] = (s & 2) ? d[j + 1] : d[j];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) d[j] = (s & 1) ? (d[j] >> 16 | d[j + 1] << 16) : d[j];
+  return s >= 8 ? u32x4{0, 0, 0, 0} : u32x4{d[0], d[1], d[2], d[3]};
+}
+
+// Elements c .. c + 7 of a row of `cols` bf16, zeros past its end, reading within the row
+// alone: a piece that crosses the end is read as the row's last eight and shifted.
+__device__ __forceinline__ u32x4 load8_row(const uint16_t* __restrict__ row, int64_t c, int64_t cols) {
+  if (cols < 8) {
+    u32x4 v = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (c + j < cols) v[j >> 1] |= (uint32_t)row[c + j] << (16 * (j & 1));
+    return v;
+  }
+  const int64_t at = c + 8 <= cols ? c : cols - 8;
+  const u32x4 v = *(const u32x4_a2*)(row + at);
+  return drop_front8(v, (int)(c - at < 8 ? c - at : 8));
+}
+
+// Stores the first n (at most 8) of eight bf16.
+__device__ __forceinline__ void store8_row(uint16_t* __restrict__ dst, u32x4 v, int n) {
+  if (n >= 8) {
+    *(u32x4_a2*)dst = v;
+  } else {
+#pragma unroll 1
+    for (int j = 0; j < n; ++j) {
+      dst[j] = (uint16_t)v[0];
+      v = u32x4{v[0] >> 16 | v[1] << 16, v[1] >> 16 | v[2] << 16, v[2] >> 16 | v[3] << 16, v[3] >> 16};
+    }
+  }
+}
 
 static constexpr int kBlock = 64;   // weights per first-level scale
 static constexpr int kGroup = 256;  // first-level scales per second-level scale

@@ -40,34 +40,48 @@ struct Tile {
   u32x4 v[2];
 };
 
-// Tile at `base` (its element (0, 0)) of a matrix with `ld` elements per row;
-// rows at or past `rows` and columns at or past `cols` read as zero.  With
-// kVec (ld and cols multiples of 8, base 16-byte aligned) each thread issues
-// two 16-byte buffer loads, otherwise sixteen of one element, with no branch, so
-// that the loads of later steps stay in flight.  `bytes`: extent of the matrix
-// from `base`.
+// Tile of a matrix with `ld` elements per row, its first row at `base`, its first column
+// c0; rows at or past `rows` and columns at or past `cols` read as zero.  Each thread
+// issues two 16-byte buffer loads, with no branch, so that the loads of later steps stay
+// in flight: aligned ones with kVec (ld and cols multiples of 8, base 16-byte aligned),
+// otherwise at any element, a piece that crosses the row's end read as the last eight
+// of the row and moved into place by fit_tile.  `bytes`: extent of the matrix from `base`.
 template <bool kVec>
-__device__ __forceinline__ Tile load_tile(const uint16_t* base, int64_t ld, int64_t rows, int64_t cols,
+__device__ __forceinline__ Tile load_tile(const uint16_t* base, int64_t c0, int64_t ld, int64_t rows, int64_t cols,
                                           uint64_t bytes) {
   const int t = threadIdx.x;
-  const int cc = (t & 7) * 8;
+  const int64_t cc = c0 + (t & 7) * 8;
   const __amdgpu_buffer_rsrc_t rs = rsrc(base, bytes);
   Tile tl;
+  if (kVec || cols >= 8) {                 // uniform
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int row = (t >> 3) + 32 * i;
-    const uint32_t at = (uint32_t)((row * ld + cc) * 2);
-    if constexpr (kVec) {
-      tl.v[i] = __builtin_amdgcn_raw_buffer_load_b128(rs, row < rows && cc < cols ? at : kOOB, 0, 0);
-    } else {
+    for (int i = 0; i < 2; ++i) {
+      const int row = (t >> 3) + 32 * i;
+      const int64_t at = row * ld + (kVec ? cc : min(cc, cols - 8));
+      tl.v[i] = __builtin_amdgcn_raw_buffer_load_b128(rs, row < rows && cc < cols ? (uint32_t)(at * 2) : kOOB, 0, 0);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int row = (t >> 3) + 32 * i;
       uint32_t e[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        e[j] = __builtin_amdgcn_raw_buffer_load_b16(rs, row < rows && cc + j < cols ? at + 2 * j : kOOB, 0, 0);
+        e[j] = __builtin_amdgcn_raw_buffer_load_b16(
+            rs, row < rows && cc + j < cols ? (uint32_t)((row * ld + cc + j) * 2) : kOOB, 0, 0);
       tl.v[i] = u32x4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
     }
   }
   return tl;
+}
+
+template <bool kVec>
+__device__ __forceinline__ void fit_tile(Tile& tl, int64_t c0, int64_t cols) {
+  if (kVec || cols < 8 || c0 + kTile <= cols) return;        // uniform
+  const int64_t over = c0 + (threadIdx.x & 7) * 8 + 8 - cols;
+  const int s = (int)max((int64_t)0, min((int64_t)8, over));
+#pragma unroll
+  for (int i = 0; i < 2; ++i) tl.v[i] = qk::drop_front8(tl.v[i], s);
 }
 
 __device__ __forceinline__ void store_tile(const Tile& tl, LDS_AS uint16_t* dst) {
@@ -105,16 +119,25 @@ __global__ __launch_bounds__(kThreads) void k_lora_skinny(const uint16_t* __rest
     const int64_t k0 = k_beg + st * kTile;
     const int64_t kl = k_end - k0;                     // columns of the slice left (<= 0: zeros)
     const int64_t k0c = kl > 0 ? k0 : 0;
-    ta = load_tile<kVecA>(A + m0 * lda + k0c, lda, M - m0, kl, (uint64_t)((M - m0) * lda - k0c) * 2);
-    if (kBkr) tb = load_tile<kVecB>(Bm + k0c * r, r, kl, r, (uint64_t)((R - k0c) * r) * 2);
-    else tb = load_tile<kVecB>(Bm + k0c, R, r, kl, (uint64_t)(r * R - k0c) * 2);
+    const int64_t ke = kl > 0 ? k_end : 0;             // past the slice: no columns
+    ta = load_tile<kVecA>(A + m0 * lda, k0c, lda, M - m0, ke, (uint64_t)((M - m0) * lda) * 2);
+    if (kBkr) tb = load_tile<kVecB>(Bm + k0c * r, 0, r, kl, r, (uint64_t)((R - k0c) * r) * 2);
+    else tb = load_tile<kVecB>(Bm, k0c, R, r, ke, (uint64_t)(r * R) * 2);
+  };
+  auto store = [&](int64_t st, Tile& ta, Tile& tb) {
+    const int64_t k0 = k_beg + st * kTile;
+    fit_tile<kVecA>(ta, k0, k_end);
+    if (kBkr) fit_tile<kVecB>(tb, 0, r);
+    else fit_tile<kVecB>(tb, k0, k_end);
+    if constexpr (kDrop) drop_tile(ta, d, m0, k0);
+    store_tile(ta, (LDS_AS uint16_t*)As[st & 1]);
+    store_tile(tb, (LDS_AS uint16_t*)Bs[st & 1]);
   };
   f32x16 acc = {};
-  auto step = [&](int64_t st, Tile& na, const Tile& nb, Tile& la, Tile& lb) {
+  auto step = [&](int64_t st, Tile& na, Tile& nb, Tile& la, Tile& lb) {
     tiles(st + 2, la, lb);
     const LDS_AS uint16_t* as = (const LDS_AS uint16_t*)As[st & 1];
     const LDS_AS uint16_t* bs = (const LDS_AS uint16_t*)Bs[st & 1];
-    if constexpr (kDrop) drop_tile(na, d, m0, k_beg + (st + 1) * kTile);
     if (wc * 32 < r) {
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
@@ -123,16 +146,13 @@ __global__ __launch_bounds__(kThreads) void k_lora_skinny(const uint16_t* __rest
         acc = qk::mfma32(a, b, acc);
       }
     }
-    store_tile(na, (LDS_AS uint16_t*)As[(st + 1) & 1]);
-    store_tile(nb, (LDS_AS uint16_t*)Bs[(st + 1) & 1]);
+    store(st + 1, na, nb);
     __syncthreads();
   };
   Tile a0, b0, aA, bA, aB, bB;
   tiles(0, a0, b0);
   tiles(1, aA, bA);
-  if constexpr (kDrop) drop_tile(a0, d, m0, k_beg);
-  store_tile(a0, (LDS_AS uint16_t*)As[0]);
-  store_tile(b0, (LDS_AS uint16_t*)Bs[0]);
+  store(0, a0, b0);
   __syncthreads();
   for (int64_t st = 0; st < nsteps; st += 2) {   // an odd count runs one more step over zeros
     step(st, aA, bA, aB, bB);
@@ -440,19 +460,23 @@ __device__ __forceinline__ void tn_tile(const uint16_t* __restrict__ A, int64_t 
     const int64_t mm = m_beg + st * kTile;
     const int64_t ml = m_end - mm;                     // rows of the slice left (<= 0: zeros)
     const int64_t mmc = ml > 0 ? mm : 0;
-    ta = load_tile<kVecA>(A + mmc * lda + p0, lda, ml, P - p0, (uint64_t)((M - mmc) * lda - p0) * 2);   // [m][p]
+    ta = load_tile<kVecA>(A + mmc * lda, p0, lda, ml, P, (uint64_t)((M - mmc) * lda) * 2);   // [m][p]
 #pragma unroll
     for (int j = 0; j < kPlanes; ++j)
-      tb.p[j] = load_tile<kVecB>(B + (j * M + mmc) * ldb, ldb, ml, r, (uint64_t)((M - mmc) * ldb) * 2);   // [m][c]
+      tb.p[j] = load_tile<kVecB>(B + (j * M + mmc) * ldb, 0, ldb, ml, r, (uint64_t)((M - mmc) * ldb) * 2);   // [m][c]
   };
-  auto store = [&](int64_t st, Tile& ta, const BTiles& tb) {
+  auto store = [&](int64_t st, Tile& ta, BTiles& tb) {
+    fit_tile<kVecA>(ta, p0, P);
     if constexpr (kDrop) drop_tile(ta, d, m_beg + st * kTile, p0);
     store_tile(ta, abuf(st));
 #pragma unroll
-    for (int j = 0; j < kPlanes; ++j) store_tile(tb.p[j], bbuf(st, j));
+    for (int j = 0; j < kPlanes; ++j) {
+      fit_tile<kVecB>(tb.p[j], 0, r);
+      store_tile(tb.p[j], bbuf(st, j));
+    }
   };
   f32x16 acc = {};
-  auto step = [&](int64_t st, Tile& na, const BTiles& nb, Tile& la, BTiles& lb) {
+  auto step = [&](int64_t st, Tile& na, BTiles& nb, Tile& la, BTiles& lb) {
     tiles(st + 2, la, lb);
     if (wc * 32 < r) {
 #pragma unroll

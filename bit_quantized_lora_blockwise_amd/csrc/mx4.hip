@@ -27,10 +27,10 @@ __device__ __forceinline__ uint32_t row_or(uint32_t v) {
 // Along the rows: 16 lanes take 128 elements of a row (a quad one block, a lane
 // eight elements), a wave four rows at a time and kRows / 4 such groups with all
 // their loads in flight: 256 contiguous bytes read per row, 64 written per block
-// position and group.
+// position and group.  Rows past the end repeat the last one and are not written.
 constexpr int kRows = 16;
 
-template <bool kBf16, bool kVec>
+template <bool kBf16>
 __global__ __launch_bounds__(kThreads) void k_mx4_quant(const void* __restrict__ X, int64_t rows, int64_t cols,
                                                         int64_t ld, int64_t words, uint32_t* __restrict__ codes,
                                                         uint32_t* __restrict__ scales) {
@@ -45,30 +45,19 @@ __global__ __launch_bounds__(kThreads) void k_mx4_quant(const void* __restrict__
 #pragma unroll
     for (int i = 0; i < kRows / 4; ++i) {
       const int64_t row = kRows * rt + 4 * i + rl;
-      const bool in = row < rows && col < cols;
+      const bool whole = 128 * (w + 1) <= cols;                  // uniform
       if constexpr (kBf16) {
-        const uint16_t* p = (const uint16_t*)X + row * ld + col;
-        v[i] = u32x4{0, 0, 0, 0};
-        if (kVec) {
-          if (in) v[i] = *(const u32x4*)p;
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (in && col + j < cols) v[i][j >> 1] |= (uint32_t)p[j] << (16 * (j & 1));
-        }
+        const uint16_t* p = (const uint16_t*)X + min(row, rows - 1) * ld;
+        if (whole) v[i] = *(const u32x4_a2*)(p + col);
+        else v[i] = qk::load8_row(p, col, cols);
       } else {
-        const float* p = (const float*)X + row * ld + col;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[i][j] = 0.0f;
-        if (kVec) {
-          if (in) {
-            *(f32x4*)f[i] = *(const f32x4*)p;
-            *(f32x4*)(f[i] + 4) = *(const f32x4*)(p + 4);
-          }
+        const float* p = (const float*)X + min(row, rows - 1) * ld;
+        if (whole) {
+          *(f32x4*)f[i] = *(const f32x4_a4*)(p + col);
+          *(f32x4*)(f[i] + 4) = *(const f32x4_a4*)(p + col + 4);
         } else {
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (in && col + j < cols) f[i][j] = p[j];
+          for (int j = 0; j < 8; ++j) f[i][j] = col + j < cols ? p[col + j] : 0.0f;
         }
       }
     }
@@ -102,7 +91,7 @@ __global__ __launch_bounds__(kThreads) void k_mx4_quant(const void* __restrict__
 // each column), a lane two columns: no exchange between lanes, 256 contiguous
 // bytes read per row (bf16), 32 written per lane.  The four waves' scale bytes
 // meet in LDS.
-template <bool kBf16, bool kVec>
+template <bool kBf16>
 __global__ __launch_bounds__(kThreads) void k_mx4_quant_t(const void* __restrict__ X, int64_t len, int64_t cols,
                                                           int64_t ld, u32x4* __restrict__ codes,
                                                           uint32_t* __restrict__ scales) {
@@ -111,19 +100,23 @@ __global__ __launch_bounds__(kThreads) void k_mx4_quant_t(const void* __restrict
   const int64_t ctiles = (cols + 127) / 128;
   const int64_t ct = blockIdx.x % ctiles, word = blockIdx.x / ctiles;
   const int64_t c0 = 128 * ct + 2 * l, r0 = 128 * word + 32 * wv;
+  const bool whole = 128 * (ct + 1) <= cols && r0 + 32 <= len;    // uniform
+  typedef uint32_t u32_a2 __attribute__((aligned(2)));
+  typedef float f32x2_a4 __attribute__((ext_vector_type(2), aligned(4)));
   float x[2][32];
   if constexpr (kBf16) {
+    const uint16_t* p = (const uint16_t*)X + r0 * ld + c0;
     uint32_t d[32];
+    if (whole) {
 #pragma unroll
-    for (int k = 0; k < 32; ++k) {
-      const uint16_t* p = (const uint16_t*)X + (r0 + k) * ld + c0;
-      d[k] = 0;
-      if (r0 + k < len) {
-        if (kVec) {
-          if (c0 < cols) d[k] = *(const uint32_t*)p;
-        } else {
-          if (c0 < cols) d[k] = p[0];
-          if (c0 + 1 < cols) d[k] |= (uint32_t)p[1] << 16;
+      for (int k = 0; k < 32; ++k) d[k] = *(const u32_a2*)(p + k * ld);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 32; ++k) {
+        d[k] = 0;
+        if (r0 + k < len) {
+          if (c0 < cols) d[k] = p[k * ld];
+          if (c0 + 1 < cols) d[k] |= (uint32_t)p[k * ld + 1] << 16;
         }
       }
     }
@@ -133,13 +126,19 @@ __global__ __launch_bounds__(kThreads) void k_mx4_quant_t(const void* __restrict
       x[1][k] = __uint_as_float(d[k] & 0xFFFF0000u);
     }
   } else {
+    const float* p = (const float*)X + r0 * ld + c0;
+    if (whole) {
 #pragma unroll
-    for (int k = 0; k < 32; ++k) {
-      const float* p = (const float*)X + (r0 + k) * ld + c0;
-      x[0][k] = x[1][k] = 0.0f;
-      if (r0 + k < len) {
-        if (c0 < cols) x[0][k] = p[0];
-        if (c0 + 1 < cols) x[1][k] = p[1];
+      for (int k = 0; k < 32; ++k) {
+        const f32x2_a4 y = *(const f32x2_a4*)(p + k * ld);
+        x[0][k] = y[0];
+        x[1][k] = y[1];
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 32; ++k) {
+        x[0][k] = r0 + k < len && c0 < cols ? p[k * ld] : 0.0f;
+        x[1][k] = r0 + k < len && c0 + 1 < cols ? p[k * ld + 1] : 0.0f;
       }
     }
   }
@@ -166,7 +165,6 @@ __global__ __launch_bounds__(kThreads) void k_mx4_quant_t(const void* __restrict
 }
 
 // Packed -> bf16 [rows, cols], the lanes as in k_mx4_quant.
-template <bool kVec>
 __global__ __launch_bounds__(kThreads) void k_mx4_dequant(const uint32_t* __restrict__ codes,
                                                           const uint32_t* __restrict__ scales, int64_t rows,
                                                           int64_t cols, int64_t words, uint16_t* __restrict__ out) {
@@ -191,14 +189,7 @@ __global__ __launch_bounds__(kThreads) void k_mx4_dequant(const uint32_t* __rest
       u32x4 v = decode8(c[i], scale_f32(sb));
       if (sb == 255u) v = u32x4{0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u};
       if (row >= rows) continue;
-      uint16_t* p = out + row * cols + col;
-      if (kVec) {
-        if (col < cols) *(u32x4*)p = v;
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (col + j < cols) p[j] = (uint16_t)(v[j >> 1] >> (16 * (j & 1)));
-      }
+      if (col < cols) qk::store8_row(out + row * cols + col, v, (int)min((int64_t)8, cols - col));
     }
   }
 }
@@ -214,46 +205,32 @@ unsigned tile_grid(int64_t rows, int64_t words) {
 hipError_t launch_mx4_quant(const void* X, bool bf16, int64_t rows, int64_t cols, int64_t ld, uint8_t* codes,
                             uint8_t* scales, hipStream_t s) {
   const int64_t words = padded(cols) / kPad;
-  const bool vec = (cols % 8) == 0 && (ld % 8) == 0;
-#define QL_Q(B, V)                                                                                             \
-  hipLaunchKernelGGL((k_mx4_quant<B, V>), dim3(tile_grid(rows, words)), dim3(kThreads), 0, s, X, rows, cols, ld, \
-                     words, (uint32_t*)codes, (uint32_t*)scales)
-  if (bf16) {
-    if (vec) QL_Q(true, true);
-    else QL_Q(true, false);
-  } else {
-    if (vec) QL_Q(false, true);
-    else QL_Q(false, false);
-  }
-#undef QL_Q
+  const dim3 grid(tile_grid(rows, words));
+  if (bf16)
+    hipLaunchKernelGGL(k_mx4_quant<true>, grid, dim3(kThreads), 0, s, X, rows, cols, ld, words, (uint32_t*)codes,
+                       (uint32_t*)scales);
+  else
+    hipLaunchKernelGGL(k_mx4_quant<false>, grid, dim3(kThreads), 0, s, X, rows, cols, ld, words, (uint32_t*)codes,
+                       (uint32_t*)scales);
   return hipGetLastError();
 }
 
 hipError_t launch_mx4_quant_t(const void* X, bool bf16, int64_t len, int64_t cols, int64_t ld, uint8_t* codes,
                               uint8_t* scales, hipStream_t s) {
-  const unsigned grid = (unsigned)((cols + 127) / 128 * (padded(len) / kPad));
-  const bool vec = (cols % 2) == 0 && (ld % 2) == 0;
-#define QL_QT(B, V)                                                                                            \
-  hipLaunchKernelGGL((k_mx4_quant_t<B, V>), dim3(grid), dim3(kThreads), 0, s, X, len, cols, ld, (u32x4*)codes, \
-                     (uint32_t*)scales)
-  if (bf16) {
-    if (vec) QL_QT(true, true);
-    else QL_QT(true, false);
-  } else {
-    QL_QT(false, false);
-  }
-#undef QL_QT
+  const dim3 grid((unsigned)((cols + 127) / 128 * (padded(len) / kPad)));
+  if (bf16)
+    hipLaunchKernelGGL(k_mx4_quant_t<true>, grid, dim3(kThreads), 0, s, X, len, cols, ld, (u32x4*)codes,
+                       (uint32_t*)scales);
+  else
+    hipLaunchKernelGGL(k_mx4_quant_t<false>, grid, dim3(kThreads), 0, s, X, len, cols, ld, (u32x4*)codes,
+                       (uint32_t*)scales);
   return hipGetLastError();
 }
 
 hipError_t launch_mx4_dequant(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, uint16_t* out,
                               hipStream_t s) {
   const int64_t words = padded(cols) / kPad;
-  if ((cols % 8) == 0)
-    hipLaunchKernelGGL((k_mx4_dequant<true>), dim3(tile_grid(rows, words)), dim3(kThreads), 0, s,
-                       (const uint32_t*)codes, (const uint32_t*)scales, rows, cols, words, out);
-  else
-    hipLaunchKernelGGL((k_mx4_dequant<false>), dim3(tile_grid(rows, words)), dim3(kThreads), 0, s,
-                       (const uint32_t*)codes, (const uint32_t*)scales, rows, cols, words, out);
+  hipLaunchKernelGGL(k_mx4_dequant, dim3(tile_grid(rows, words)), dim3(kThreads), 0, s, (const uint32_t*)codes,
+                     (const uint32_t*)scales, rows, cols, words, out);
   return hipGetLastError();
 }

@@ -16,22 +16,10 @@ using namespace mx4;
 
 constexpr int kStages = 4;        // reduction steps of 128 in LDS
 constexpr int kPL = 64 + 8;       // pitch of [row][c] adapter tiles
+constexpr uint32_t kOOB = 0x80000000u;   // past every buffer: loads read 0, stores are dropped
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p, uint64_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc((void*)p, (short)0, (int)bytes, 0x00020000);
-}
-
-// 8 consecutive bf16 of a row starting at column `col`, zero past `ncols`.
-__device__ __forceinline__ u32x4 load_row8(const uint16_t* __restrict__ row, int64_t col, int64_t ncols) {
-  const uint16_t* p = row + col;
-  if (col + 8 <= ncols && ((uintptr_t)p & 15) == 0) return *(const u32x4*)p;
-  u32x4 v = {0, 0, 0, 0};
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const uint32_t h = (col + j < ncols) ? p[j] : 0;
-    v[j >> 1] |= h << (16 * (j & 1));
-  }
-  return v;
 }
 
 // Loads to LDS (16 or 4 bytes a lane, lane l's at dst + 16 l or 4 l).  Issued from
@@ -72,7 +60,8 @@ __device__ __forceinline__ void tile_at(int v, int tm, int tp, int nt, int& im, 
 // its row and of column 8 h of the wave's first tile (out of range for a row past
 // the end: the hardware drops the store); off: columns from there to this tile;
 // left: columns of C from column 8 h of this tile on.
-template <bool kVec>
+// kPieces: in whole 16-byte pieces, at any address (P % 8 == 0, or the tile is inside).
+template <bool kPieces>
 __device__ __forceinline__ void store_tile(const f32x16& v, __amdgpu_buffer_rsrc_t rc, uint32_t vo, int off, int left) {
 #pragma unroll
   for (int gp = 0; gp < 2; ++gp) {
@@ -82,19 +71,19 @@ __device__ __forceinline__ void store_tile(const f32x16& v, __amdgpu_buffer_rsrc
                                                      qk::pack_bf16x2(v[8 * gp + 6], v[8 * gp + 7]), false, false);
     const u32x4 o = {x[0], y[0], x[1], y[1]};
     const int at = 2 * (off + 16 * gp), n = left - 16 * gp;
-    if constexpr (kVec) {                   // whole 16-byte pieces: P % 8 == 0
-      __builtin_amdgcn_raw_buffer_store_b128(o, rc, n > 0 ? vo + at : 0x80000000u, 0, 0);
+    if constexpr (kPieces) {
+      __builtin_amdgcn_raw_buffer_store_b128(o, rc, n > 0 ? vo + at : kOOB, 0, 0);
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
         __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(o[e >> 1] >> (16 * (e & 1))), rc,
-                                              e < n ? vo + at + 2 * e : 0x80000000u, 0, 0);
+                                              e < n ? vo + at + 2 * e : kOOB, 0, 0);
     }
   }
 }
 
 // All of a wave's tiles: rows m, m + 32, ... (m this lane's) and columns p0, p0 + 32, ...
-template <bool kVec, int kMT, int kPT>
+template <bool kPieces, int kMT, int kPT>
 __device__ __forceinline__ void store_tiles(const f32x16 (&acc)[kMT][kPT], uint16_t* __restrict__ C, int m, int p0, int M,
                                             int P) {
   const __amdgpu_buffer_rsrc_t rc = rsrc(C, (uint64_t)M * P * 2);
@@ -102,10 +91,20 @@ __device__ __forceinline__ void store_tiles(const f32x16 (&acc)[kMT][kPT], uint1
   asm volatile("" : "+v"(h));               // addresses are formed here, not held through the reduction
 #pragma unroll
   for (int i = 0; i < kMT; ++i) {
-    const uint32_t vo = m + 32 * i < M ? 2u * ((uint32_t)(m + 32 * i) * (uint32_t)P + p0 + 8 * h) : 0x80000000u;
+    const uint32_t vo = m + 32 * i < M ? 2u * ((uint32_t)(m + 32 * i) * (uint32_t)P + p0 + 8 * h) : kOOB;
 #pragma unroll
-    for (int j = 0; j < kPT; ++j) store_tile<kVec>(acc[i][j], rc, vo, 32 * j, P - p0 - 8 * h - 32 * j);
+    for (int j = 0; j < kPT; ++j) store_tile<kPieces>(acc[i][j], rc, vo, 32 * j, P - p0 - 8 * h - 32 * j);
   }
+}
+
+// Rows of no whole 16-byte pieces: waves whose columns end inside the matrix store whole
+// pieces all the same, those on the edge single elements (which throughout took 130 us
+// of a 4093 x 11007 product).
+template <int kMT, int kPT>
+__device__ __forceinline__ void store_any(const f32x16 (&acc)[kMT][kPT], uint16_t* __restrict__ C, int m, int p0, int M,
+                                          int P) {
+  if (p0 + 32 * kPT <= P) store_tiles<true, kMT, kPT>(acc, C, m, p0, M, P);
+  else store_tiles<false, kMT, kPT>(acc, C, m, p0, M, P);
 }
 
 // kMode: 0 no adapter, 1 forward, 2 backward, 3 backward with dropout.
@@ -227,21 +226,21 @@ __global__ __launch_bounds__(64 * kWM * kWP) void k_mx4_gemm(const uint8_t* __re
     for (int i = t; i < G::kBM * 8; i += G::kThreads) {
       const int row = i >> 3, c = (i & 7) * 8;
       u32x4 v = {0, 0, 0, 0};
-      if (m0 + row < M && c < r) v = load_row8(lo.A + (int64_t)(m0 + row) * r, c, r);
+      if (m0 + row < M && c < r) v = qk::load8_row(lo.A + (int64_t)(m0 + row) * r, c, r);
       *(LDS_AS u32x4*)(la + row * kPL + c) = v;
     }
     if constexpr (kMode == 1) {
       for (int i = t; i < 64 * (G::kBP / 8); i += G::kThreads) {
         const int c = i / (G::kBP / 8), p = (i % (G::kBP / 8)) * 8;
         u32x4 v = {0, 0, 0, 0};
-        if (c < r && p0 + p < P) v = load_row8(lo.B + (int64_t)c * P, p0 + p, P);
+        if (c < r && p0 + p < P) v = qk::load8_row(lo.B + (int64_t)c * P, p0 + p, P);
         *(LDS_AS u32x4*)(lb + c * G::kPD + p) = v;
       }
     } else {
       for (int i = t; i < G::kBP * 8; i += G::kThreads) {
         const int row = i >> 3, c = (i & 7) * 8;
         u32x4 v = {0, 0, 0, 0};
-        if (p0 + row < P && c < r) v = load_row8(lo.B + (int64_t)(p0 + row) * r, c, r);
+        if (p0 + row < P && c < r) v = qk::load8_row(lo.B + (int64_t)(p0 + row) * r, c, r);
         *(LDS_AS u32x4*)(lb + row * kPL + c) = v;
       }
     }
@@ -347,7 +346,7 @@ __global__ __launch_bounds__(64 * kWM * kWP) void k_mx4_gemm(const uint8_t* __re
   step(q, std::integral_constant<int, 0>{});
 
   if ((P & 7) == 0) store_tiles<true, kMT, kPT>(acc, C, m0 + ra, p0 + 32 * kPT * wp, M, P);
-  else store_tiles<false, kMT, kPT>(acc, C, m0 + ra, p0 + 32 * kPT * wp, M, P);
+  else store_any<kMT, kPT>(acc, C, m0 + ra, p0 + 32 * kPT * wp, M, P);
 }
 
 // ---------------------------------------------------------------------------
@@ -429,7 +428,6 @@ __global__ __launch_bounds__(kRT, 2) void k_mx4_gemm_ring(const uint8_t* __restr
   // others are sent as zeros and written over by hand before they are read.
   const int r = kMode ? lo.r : 0;
   const __amdgpu_buffer_rsrc_t rla = rsrc(lo.A, (uint64_t)M * r * 2), rlb = rsrc(lo.B, (uint64_t)P * r * 2);
-  constexpr uint32_t kOOB = 0x80000000u;
   auto load_rc = [&](__amdgpu_buffer_rsrc_t rs, int row0, int rows, int ring, int n) {
     const int row = 32 * w + 8 * n + (l >> 3), c = (l & 7) ^ ((row >> 1) & 7);
     const bool ok = kVec && row0 + row < rows && 8 * c < r;
@@ -590,15 +588,15 @@ __global__ __launch_bounds__(kRT, 2) void k_mx4_gemm_ring(const uint8_t* __restr
         for (int i = t; i < kRB * 8; i += kRT) {
           const int row = i >> 3, c = i & 7;
           u32x4 x = {0, 0, 0, 0};
-          if (m0 + row < M && 8 * c < r) x = load_row8(lo.A + (int64_t)(m0 + row) * r, 8 * c, r);
+          if (m0 + row < M && 8 * c < r) x = qk::load8_row(lo.A + (int64_t)(m0 + row) * r, 8 * c, r);
           *(LDS_AS u32x4*)(la + slot_rc(row, c)) = x;
           x = u32x4{0, 0, 0, 0};
           if constexpr (kMode == 1) {
             const int cc = i >> 5, p = i & 31;
-            if (cc < r && p0 + 8 * p < P) x = load_row8(lo.B + (int64_t)cc * P, p0 + 8 * p, P);
+            if (cc < r && p0 + 8 * p < P) x = qk::load8_row(lo.B + (int64_t)cc * P, p0 + 8 * p, P);
             *(LDS_AS u32x4*)(lb + slot_cp(cc, p)) = x;
           } else {
-            if (p0 + row < P && 8 * c < r) x = load_row8(lo.B + (int64_t)(p0 + row) * r, 8 * c, r);
+            if (p0 + row < P && 8 * c < r) x = qk::load8_row(lo.B + (int64_t)(p0 + row) * r, 8 * c, r);
             *(LDS_AS u32x4*)(lb + slot_rc(row, c)) = x;
           }
         }
@@ -652,7 +650,8 @@ __global__ __launch_bounds__(kRT, 2) void k_mx4_gemm_ring(const uint8_t* __restr
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");       // the next tile's steps 0 and 1
       barrier();                                             // and every wave is past the adapter's buffers
     }
-    store_tiles<kVec, kMT, kPT>(acc, C, m0 + ra, p0 + 128 * wp, M, P);
+    if constexpr (kVec) store_tiles<true, kMT, kPT>(acc, C, m0 + ra, p0 + 128 * wp, M, P);
+    else store_any<kMT, kPT>(acc, C, m0 + ra, p0 + 128 * wp, M, P);
     if (!more) break;
     ring0 += words;
     if constexpr (kMode != 0) {

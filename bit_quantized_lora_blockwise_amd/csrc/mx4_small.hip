@@ -42,13 +42,21 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p, uint64_t b
   return __builtin_amdgcn_make_buffer_rsrc((void*)p, (short)0, (int)bytes, 0x00020000);
 }
 
-// Eight bf16 from byte offset `at`, element j present if j < n (n <= 0: none).
+// Elements k .. k + 7 of a row of `len` bf16 that begins at byte `row`, zeros past its
+// end (all of them if !on).  kVec: 16-byte pieces; else a piece that crosses the end is
+// read as the last eight of the row and moved.
 template <bool kVec>
-__device__ __forceinline__ u32x4 load8(__amdgpu_buffer_rsrc_t rs, uint32_t at, int n) {
-  if (kVec) return __builtin_amdgcn_raw_buffer_load_b128(rs, n > 0 ? at : kOOB, 0, 0);
+__device__ __forceinline__ u32x4 load8(__amdgpu_buffer_rsrc_t rs, uint32_t row, int k, int len, bool on) {
+  const bool in = on && k < len;
+  if (kVec) return __builtin_amdgcn_raw_buffer_load_b128(rs, in ? row + 2 * k : kOOB, 0, 0);
+  if (len >= 8) {
+    const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(rs, in ? row + 2 * min(k, len - 8) : kOOB, 0, 0);
+    return k + 8 <= len ? v : qk::drop_front8(v, min(8, k + 8 - len));
+  }
   uint32_t e[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) e[j] = __builtin_amdgcn_raw_buffer_load_b16(rs, j < n ? at + 2 * j : kOOB, 0, 0);
+  for (int j = 0; j < 8; ++j)
+    e[j] = __builtin_amdgcn_raw_buffer_load_b16(rs, on && k + j < len ? row + 2 * (k + j) : kOOB, 0, 0);
   return u32x4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
 }
 
@@ -77,9 +85,9 @@ __global__ __launch_bounds__(kDThreads) void k_small_down(const uint16_t* __rest
 #pragma unroll
       for (int j = 0; j < 4; ++j) b[j] = e[2 * j] | e[2 * j + 1] << 16;
     } else {
-      b = load8<kVec>(rb, (uint32_t)(c * R + k) * 2u, c < r ? R - k : 0);
+      b = load8<kVec>(rb, (uint32_t)(c * R) * 2u, k, R, c < r);
     }
-    u32x4 a = load8<kVec>(ra, (uint32_t)(m * R + k) * 2u, m < M ? R - k : 0);
+    u32x4 a = load8<kVec>(ra, (uint32_t)(m * R) * 2u, k, R, m < M);
     if (kQuant && blockIdx.z == 0) {
       uint32_t top = 0;
 #pragma unroll
