@@ -52,16 +52,26 @@ typedef f32x4 f32x4_a4 __attribute__((aligned(4)));
 
 namespace qk {
 
-// Eight bf16 moved down by s (0 .. 8) places, zeros behind them.
+// Eight elements moved down by s (0 .. 8) places, zeros behind them.
 __device__ __forceinline__ u32x4 drop_front8(u32x4 v, int s) {
-  uint32_t d[5] = {v[0], v[1], v[2], v[3], 0};
-#pragma unroll
-  for (int j = 0; j < 4; ++j) d[j] = s >= 4 ? (j < 2 ? d[j + 2] : 0u) : d[j];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) d[j] = (s & 2) ? d[j + 1] : d[j];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) d[j] = (s & 1) ? (d[j] >> 16 | d[j + 1] << 16) : d[j];
-  return s >= 8 ? u32x4{0, 0, 0, 0} : u32x4{d[0], d[1], d[2], d[3]};
+  uint64_t lo = (uint64_t)v[1] << 32 | v[0], hi = (uint64_t)v[3] << 32 | v[2];
+  const int b = 16 * (s & 3);
+  lo = b ? lo >> b | hi << (64 - b) : lo;
+  hi >>= b;
+  lo = s & 4 ? hi : s & 8 ? 0 : lo;
+  hi = s >= 4 ? 0 : hi;
+  return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+}
+__device__ __forceinline__ void drop_front8(f32x4& a, f32x4& b, int s) {
+  const f32x4 z = {0, 0, 0, 0};
+  a = (s & 4) ? b : a;
+  b = (s & 4) ? z : b;
+  a = (s & 2) ? f32x4{a[2], a[3], b[0], b[1]} : a;
+  b = (s & 2) ? f32x4{b[2], b[3], 0, 0} : b;
+  a = (s & 1) ? f32x4{a[1], a[2], a[3], b[0]} : a;
+  b = (s & 1) ? f32x4{b[1], b[2], b[3], 0} : b;
+  a = s >= 8 ? z : a;
+  b = s >= 8 ? z : b;
 }
 
 // Elements c .. c + 7 of a row of `cols` bf16, zeros past its end, reading within the row

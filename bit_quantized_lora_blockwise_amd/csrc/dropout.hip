@@ -13,54 +13,78 @@ namespace {
 
 constexpr int kThreads = 256;
 
-template <bool kBf16>
+// kWhole: cols % 8 == 0, no piece crosses a row's end.
+template <bool kBf16, bool kWhole>
 __global__ __launch_bounds__(kThreads) void k_dropout(const void* __restrict__ X, int64_t rows, int64_t cols,
                                                       int64_t ld, drop::Params d, void* __restrict__ Y) {
-  const int64_t octs = (cols + 7) / 8;
-  const int64_t total = rows * octs, stride = (int64_t)gridDim.x * kThreads;
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += stride) {
-    const int64_t m = i / octs, q = i - m * octs;
-    const int n = (int)min((int64_t)8, cols - 8 * q);
-    u32x4 u = {};
+  const int64_t octs = (cols + 7) / 8, stride = (int64_t)gridDim.x * kThreads;
+  const int64_t first = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  // row and octet of the thread's pieces, `stride` apart: one division, then steps
+  const int64_t step_m = stride / octs, step_q = stride - step_m * octs;
+  int64_t m = first / octs, q = first - m * octs;
+  struct Piece {
+    u32x4 v[kBf16 ? 1 : 2];
+  };
+  auto load = [&](int64_t m, int64_t q) {
+    Piece x = {};
     if constexpr (kBf16) {
       const uint16_t* src = (const uint16_t*)X + m * ld;
-      u32x4 v;
-      if (n == 8) v = *(const u32x4_a2*)(src + 8 * q);
-      else v = qk::load8_row(src, 8 * q, cols);
-      if (d.cut) {
-        u = drop::draw8(d, (uint32_t)m, (uint32_t)q);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          v[j] &= drop::keep2(u[j], d.cut);
-          v[j] = qk::pack_bf16x2(__uint_as_float(v[j] << 16) * d.scale, __uint_as_float(v[j] & 0xFFFF0000u) * d.scale);
-        }
-      }
-      qk::store8_row((uint16_t*)Y + m * cols + 8 * q, v, n);
+      if (kWhole || 8 * q + 8 <= cols) x.v[0] = *(const u32x4_a2*)(src + 8 * q);
+      else x.v[0] = qk::load8_row(src, 8 * q, cols);
     } else {
       const float* src = (const float*)X + m * ld + 8 * q;
-      float* dst = (float*)Y + m * cols + 8 * q;
-      float v[8];
-      if (n == 8) {
-        *(f32x4*)v = *(const f32x4_a4*)src;
-        *(f32x4*)(v + 4) = *(const f32x4_a4*)(src + 4);
+      if (kWhole || 8 * q + 8 <= cols) {
+        x.v[0] = __builtin_bit_cast(u32x4, *(const f32x4_a4*)src);
+        x.v[1] = __builtin_bit_cast(u32x4, *(const f32x4_a4*)(src + 4));
       } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = j < n ? src[j] : 0.0f;
-      }
-      if (d.cut) {
-        u = drop::draw8(d, (uint32_t)m, (uint32_t)q);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = ((u[j >> 1] >> (16 * (j & 1))) & 0xFFFFu) >= d.cut ? v[j] * d.scale : 0.0f;
-      }
-      if (n == 8) {
-        *(f32x4_a4*)dst = *(f32x4*)v;
-        *(f32x4_a4*)(dst + 4) = *(f32x4*)(v + 4);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (j < n) dst[j] = v[j];
+        for (int j = 0; j < 7; ++j) x.v[j >> 2][j & 3] = 8 * q + j < cols ? __float_as_uint(src[j]) : 0u;
       }
     }
+    return x;
+  };
+  if (m >= rows) return;
+  Piece next = load(m, q);
+  while (m < rows) {
+    Piece x = next;
+    int64_t m1 = m + step_m, q1 = q + step_q;
+    if (q1 >= octs) {
+      q1 -= octs;
+      ++m1;
+    }
+    if (m1 < rows) next = load(m1, q1);              // on its way while this piece is drawn
+    const int n = kWhole ? 8 : (int)min((int64_t)8, cols - 8 * q);
+    if (d.cut) {
+      const u32x4 u = drop::draw8(d, (uint32_t)m, (uint32_t)q);
+      if constexpr (kBf16) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t y = x.v[0][j] & drop::keep2(u[j], d.cut);
+          x.v[0][j] = qk::pack_bf16x2(__uint_as_float(y << 16) * d.scale, __uint_as_float(y & 0xFFFF0000u) * d.scale);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const bool keep = ((u[j >> 1] >> (16 * (j & 1))) & 0xFFFFu) >= d.cut;
+          x.v[j >> 2][j & 3] = keep ? __float_as_uint(__uint_as_float(x.v[j >> 2][j & 3]) * d.scale) : 0u;
+        }
+      }
+    }
+    if constexpr (kBf16) {
+      qk::store8_row((uint16_t*)Y + m * cols + 8 * q, x.v[0], n);
+    } else {
+      float* dst = (float*)Y + m * cols + 8 * q;
+      if (n == 8) {
+        *(f32x4_a4*)dst = __builtin_bit_cast(f32x4, x.v[0]);
+        *(f32x4_a4*)(dst + 4) = __builtin_bit_cast(f32x4, x.v[1]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 7; ++j)
+          if (j < n) dst[j] = __uint_as_float(x.v[j >> 2][j & 3]);
+      }
+    }
+    m = m1;
+    q = q1;
   }
 }
 
@@ -71,9 +95,16 @@ hipError_t launch_dropout(const void* X, bool bf16, int64_t rows, int64_t cols, 
   const int64_t octs = rows * ((cols + 7) / 8);
   int64_t grid = (octs + kThreads - 1) / kThreads;
   if (grid > 8192) grid = 8192;
-  if (bf16)
-    hipLaunchKernelGGL(k_dropout<true>, dim3((unsigned)grid), dim3(kThreads), 0, s, X, rows, cols, ld, d, Y);
-  else
-    hipLaunchKernelGGL(k_dropout<false>, dim3((unsigned)grid), dim3(kThreads), 0, s, X, rows, cols, ld, d, Y);
+  const bool whole = cols % 8 == 0;
+#define QL_DROP(B, W) \
+  hipLaunchKernelGGL((k_dropout<B, W>), dim3((unsigned)grid), dim3(kThreads), 0, s, X, rows, cols, ld, d, Y)
+  if (bf16) {
+    if (whole) QL_DROP(true, true);
+    else QL_DROP(true, false);
+  } else {
+    if (whole) QL_DROP(false, true);
+    else QL_DROP(false, false);
+  }
+#undef QL_DROP
   return hipGetLastError();
 }

@@ -40,30 +40,30 @@ struct Tile {
   u32x4 v[2];
 };
 
+// How a tile is read: in aligned 16-byte pieces (ld and cols multiples of 8, base 16-byte
+// aligned), in pieces at any element (rows of at least eight), or element by element.
+enum Load { kPieces, kAnywhere, kElements };
+
 // Tile of a matrix with `ld` elements per row, its first row at `base`, its first column
 // c0; rows at or past `rows` and columns at or past `cols` read as zero.  Each thread
-// issues two 16-byte buffer loads, with no branch, so that the loads of later steps stay
-// in flight: aligned ones with kVec (ld and cols multiples of 8, base 16-byte aligned),
-// otherwise at any element, a piece that crosses the row's end read as the last eight
-// of the row and moved into place by fit_tile.  `bytes`: extent of the matrix from `base`.
-template <bool kVec>
+// issues two 16-byte buffer loads (or sixteen of one element), with no branch, so that
+// the loads of later steps stay in flight.  kAnywhere: a piece that crosses the row's end
+// is read as the last eight of the row and moved into place by fit_tile.  `bytes`: extent
+// of the matrix from `base`.
+template <Load kHow>
 __device__ __forceinline__ Tile load_tile(const uint16_t* base, int64_t c0, int64_t ld, int64_t rows, int64_t cols,
                                           uint64_t bytes) {
   const int t = threadIdx.x;
   const int64_t cc = c0 + (t & 7) * 8;
   const __amdgpu_buffer_rsrc_t rs = rsrc(base, bytes);
   Tile tl;
-  if (kVec || cols >= 8) {                 // uniform
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int row = (t >> 3) + 32 * i;
-      const int64_t at = row * ld + (kVec ? cc : min(cc, cols - 8));
+  for (int i = 0; i < 2; ++i) {
+    const int row = (t >> 3) + 32 * i;
+    if constexpr (kHow != kElements) {
+      const int64_t at = row * ld + (kHow == kPieces ? cc : min(cc, cols - 8));
       tl.v[i] = __builtin_amdgcn_raw_buffer_load_b128(rs, row < rows && cc < cols ? (uint32_t)(at * 2) : kOOB, 0, 0);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int row = (t >> 3) + 32 * i;
+    } else {
       uint32_t e[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j)
@@ -75,13 +75,14 @@ __device__ __forceinline__ Tile load_tile(const uint16_t* base, int64_t c0, int6
   return tl;
 }
 
-template <bool kVec>
+template <Load kHow>
 __device__ __forceinline__ void fit_tile(Tile& tl, int64_t c0, int64_t cols) {
-  if (kVec || cols < 8 || c0 + kTile <= cols) return;        // uniform
-  const int64_t over = c0 + (threadIdx.x & 7) * 8 + 8 - cols;
-  const int s = (int)max((int64_t)0, min((int64_t)8, over));
+  if constexpr (kHow == kAnywhere) {
+    const int64_t over = c0 + (threadIdx.x & 7) * 8 + 8 - cols;
+    const int s = (int)max((int64_t)0, min((int64_t)8, over));
 #pragma unroll
-  for (int i = 0; i < 2; ++i) tl.v[i] = qk::drop_front8(tl.v[i], s);
+    for (int i = 0; i < 2; ++i) tl.v[i] = qk::drop_front8(tl.v[i], s);
+  }
 }
 
 __device__ __forceinline__ void store_tile(const Tile& tl, LDS_AS uint16_t* dst) {
@@ -102,7 +103,7 @@ __device__ __forceinline__ void drop_tile(Tile& tl, const drop::Params& d, int64
 // C[M, r] partial over one reduction slice: A [M, R] (row stride lda) times B, where
 // B(k, c) = Bm[k * r + c] (kBkr, L1 [R, r]) or Bm[c * R + k] (!kBkr, L2 [r, R]).
 // kDrop: of D o A, not scaled.
-template <bool kBkr, bool kVecA, bool kVecB, bool kDrop = false>
+template <bool kBkr, Load kA, Load kB, bool kDrop = false>
 __global__ __launch_bounds__(kThreads) void k_lora_skinny(const uint16_t* __restrict__ A, int64_t M, int64_t R,
                                                           int64_t lda, const uint16_t* __restrict__ Bm, int r,
                                                           int64_t chunk, float* __restrict__ part, drop::Params d) {
@@ -120,15 +121,15 @@ __global__ __launch_bounds__(kThreads) void k_lora_skinny(const uint16_t* __rest
     const int64_t kl = k_end - k0;                     // columns of the slice left (<= 0: zeros)
     const int64_t k0c = kl > 0 ? k0 : 0;
     const int64_t ke = kl > 0 ? k_end : 0;             // past the slice: no columns
-    ta = load_tile<kVecA>(A + m0 * lda, k0c, lda, M - m0, ke, (uint64_t)((M - m0) * lda) * 2);
-    if (kBkr) tb = load_tile<kVecB>(Bm + k0c * r, 0, r, kl, r, (uint64_t)((R - k0c) * r) * 2);
-    else tb = load_tile<kVecB>(Bm, k0c, R, r, ke, (uint64_t)(r * R) * 2);
+    ta = load_tile<kA>(A + m0 * lda, k0c, lda, M - m0, ke, (uint64_t)((M - m0) * lda) * 2);
+    if (kBkr) tb = load_tile<kB>(Bm + k0c * r, 0, r, kl, r, (uint64_t)((R - k0c) * r) * 2);
+    else tb = load_tile<kB>(Bm, k0c, R, r, ke, (uint64_t)(r * R) * 2);
   };
   auto store = [&](int64_t st, Tile& ta, Tile& tb) {
     const int64_t k0 = k_beg + st * kTile;
-    fit_tile<kVecA>(ta, k0, k_end);
-    if (kBkr) fit_tile<kVecB>(tb, 0, r);
-    else fit_tile<kVecB>(tb, k0, k_end);
+    fit_tile<kA>(ta, k0, k_end);
+    if (kBkr) fit_tile<kB>(tb, 0, r);
+    else fit_tile<kB>(tb, k0, k_end);
     if constexpr (kDrop) drop_tile(ta, d, m0, k0);
     store_tile(ta, (LDS_AS uint16_t*)As[st & 1]);
     store_tile(tb, (LDS_AS uint16_t*)Bs[st & 1]);
@@ -439,7 +440,7 @@ __global__ __launch_bounds__(kThreads) void k_skinny_reduce3(const float* __rest
 // D o A, not scaled.  kPlanes: B is the sum of that many matrices, B + j M ldb.
 // lds: (2 + 2 kPlanes) tiles of kTile * kPitch.  scale: of what is written; tr: written
 // as part[c][p] (both for a product of one slice, whose partial is the result).
-template <bool kVecA, bool kVecB, bool kDrop = false, int kPlanes = 1>
+template <Load kA, Load kB, bool kDrop = false, int kPlanes = 1>
 __device__ __forceinline__ void tn_tile(const uint16_t* __restrict__ A, int64_t lda, const uint16_t* __restrict__ B,
                                         int64_t M, int64_t P, int r, int64_t chunk, float* __restrict__ part,
                                         int tile, int split, uint16_t* lds, const drop::Params& d, int ldb,
@@ -460,18 +461,18 @@ __device__ __forceinline__ void tn_tile(const uint16_t* __restrict__ A, int64_t 
     const int64_t mm = m_beg + st * kTile;
     const int64_t ml = m_end - mm;                     // rows of the slice left (<= 0: zeros)
     const int64_t mmc = ml > 0 ? mm : 0;
-    ta = load_tile<kVecA>(A + mmc * lda, p0, lda, ml, P, (uint64_t)((M - mmc) * lda) * 2);   // [m][p]
+    ta = load_tile<kA>(A + mmc * lda, p0, lda, ml, P, (uint64_t)((M - mmc) * lda) * 2);   // [m][p]
 #pragma unroll
     for (int j = 0; j < kPlanes; ++j)
-      tb.p[j] = load_tile<kVecB>(B + (j * M + mmc) * ldb, 0, ldb, ml, r, (uint64_t)((M - mmc) * ldb) * 2);   // [m][c]
+      tb.p[j] = load_tile<kB>(B + (j * M + mmc) * ldb, 0, ldb, ml, r, (uint64_t)((M - mmc) * ldb) * 2);   // [m][c]
   };
   auto store = [&](int64_t st, Tile& ta, BTiles& tb) {
-    fit_tile<kVecA>(ta, p0, P);
+    fit_tile<kA>(ta, p0, P);
     if constexpr (kDrop) drop_tile(ta, d, m_beg + st * kTile, p0);
     store_tile(ta, abuf(st));
 #pragma unroll
     for (int j = 0; j < kPlanes; ++j) {
-      fit_tile<kVecB>(tb.p[j], 0, r);
+      fit_tile<kB>(tb.p[j], 0, r);
       store_tile(tb.p[j], bbuf(st, j));
     }
   };
@@ -510,12 +511,12 @@ __device__ __forceinline__ void tn_tile(const uint16_t* __restrict__ A, int64_t 
   }
 }
 
-template <bool kVecA, bool kVecB>
+template <Load kA, Load kB>
 __global__ __launch_bounds__(kThreads) void k_lora_tn(const uint16_t* __restrict__ A, int64_t lda,
                                                       const uint16_t* __restrict__ B, int64_t M, int64_t P, int r,
                                                       int64_t chunk, float* __restrict__ part) {
   __shared__ __attribute__((aligned(16))) uint16_t lds[4 * kTile * kPitch];
-  tn_tile<kVecA, kVecB>(A, lda, B, M, P, r, chunk, part, blockIdx.x, blockIdx.y, lds, drop::Params{}, r);
+  tn_tile<kA, kB>(A, lda, B, M, P, r, chunk, part, blockIdx.x, blockIdx.y, lds, drop::Params{}, r);
 }
 
 // Two independent products of this kind in one launch (the backward's dL1 and
@@ -529,31 +530,31 @@ struct TnJob {
   int tiles, splits;
 };
 
-template <bool kVecA, bool kVecB>
+template <Load kA, Load kB>
 __global__ __launch_bounds__(kThreads) void k_lora_tn_pair(TnJob j0, TnJob j1, int64_t M, int r) {
   const int n0 = j0.tiles * j0.splits;
   const bool second = (int)blockIdx.x >= n0;         // uniform over the work group
   const TnJob j = second ? j1 : j0;
   const int b = second ? (int)blockIdx.x - n0 : (int)blockIdx.x;
   __shared__ __attribute__((aligned(16))) uint16_t lds[4 * kTile * kPitch];
-  tn_tile<kVecA, kVecB>(j.A, j.lda, j.B, M, j.P, r, j.chunk, j.part, b % j.tiles, b / j.tiles, lds, drop::Params{},
+  tn_tile<kA, kB>(j.A, j.lda, j.B, M, j.P, r, j.chunk, j.part, b % j.tiles, b / j.tiles, lds, drop::Params{},
                         r);
 }
 
 // The pair with dropout on the first product's A and its B in three planes of pitch
 // rp.  With one slice each, j0.part and j1.part are the results: scaled, the second
 // transposed.
-template <bool kVecA, bool kVecT, bool kDrop>
+template <Load kA, Load kT, bool kDrop>
 __global__ __launch_bounds__(kThreads) void k_lora_tn_pair3(TnJob j0, TnJob j1, int64_t M, int r, int rp,
                                                             drop::Params d, float scale0, float scale1, bool whole) {
   __shared__ __attribute__((aligned(16))) uint16_t lds[8 * kTile * kPitch];
   const int n0 = j0.tiles * j0.splits;
   const int b = (int)blockIdx.x;
   if (b < n0)
-    tn_tile<kVecA, true, kDrop, 3>(j0.A, j0.lda, j0.B, M, j0.P, r, j0.chunk, j0.part, b % j0.tiles, b / j0.tiles, lds, d,
+    tn_tile<kA, kPieces, kDrop, 3>(j0.A, j0.lda, j0.B, M, j0.P, r, j0.chunk, j0.part, b % j0.tiles, b / j0.tiles, lds, d,
                                    rp, scale0);
   else
-    tn_tile<kVecA, kVecT>(j1.A, j1.lda, j1.B, M, j1.P, r, j1.chunk, j1.part, (b - n0) % j1.tiles, (b - n0) / j1.tiles,
+    tn_tile<kA, kT>(j1.A, j1.lda, j1.B, M, j1.P, r, j1.chunk, j1.part, (b - n0) % j1.tiles, (b - n0) / j1.tiles,
                           lds, d, r, scale1, whole);
 }
 
@@ -765,16 +766,19 @@ hipError_t launch_lora_skinny(const uint16_t* A, int64_t M, int64_t R, int64_t l
 #define QL_SKINNY(BKR, VA, VB)                                                                                \
   hipLaunchKernelGGL((k_lora_skinny<BKR, VA, VB>), grid, dim3(kThreads), 0, s, A, M, R, lda, B, r, sp.chunk, ws, \
                      drop::Params{})
+  const bool few = R < 8 || (b_is_kr && r < 8);        // rows of fewer than eight elements
   if (b_is_kr) {
-    if (avec && bvec) QL_SKINNY(true, true, true);
-    else if (avec) QL_SKINNY(true, true, false);
-    else if (bvec) QL_SKINNY(true, false, true);
-    else QL_SKINNY(true, false, false);
+    if (avec && bvec) QL_SKINNY(true, kPieces, kPieces);
+    else if (few) QL_SKINNY(true, kElements, kElements);
+    else if (avec) QL_SKINNY(true, kPieces, kAnywhere);
+    else if (bvec) QL_SKINNY(true, kAnywhere, kPieces);
+    else QL_SKINNY(true, kAnywhere, kAnywhere);
   } else {
-    if (avec && bvec) QL_SKINNY(false, true, true);
-    else if (avec) QL_SKINNY(false, true, false);
-    else if (bvec) QL_SKINNY(false, false, true);
-    else QL_SKINNY(false, false, false);
+    if (avec && bvec) QL_SKINNY(false, kPieces, kPieces);
+    else if (few) QL_SKINNY(false, kElements, kElements);
+    else if (avec) QL_SKINNY(false, kPieces, kAnywhere);
+    else if (bvec) QL_SKINNY(false, kAnywhere, kPieces);
+    else QL_SKINNY(false, kAnywhere, kAnywhere);
   }
 #undef QL_SKINNY
   hipError_t e = hipGetLastError();
@@ -810,7 +814,7 @@ hipError_t launch_lora_tn_pair(const uint16_t* A0, int64_t lda0, const uint16_t*
   const TnJob j0{A0, lda0, B0, P0, sp0.chunk, ws, (int)((P0 + kTile - 1) / kTile), sp0.splits};
   const TnJob j1{A1, lda1, B1, P1, sp1.chunk, part1, (int)((P1 + kTile - 1) / kTile), sp1.splits};
   const unsigned nwg = (unsigned)(j0.tiles * j0.splits + j1.tiles * j1.splits);
-  hipLaunchKernelGGL((k_lora_tn_pair<true, true>), dim3(nwg), dim3(kThreads), 0, s, j0, j1, M, r);
+  hipLaunchKernelGGL((k_lora_tn_pair<kPieces, kPieces>), dim3(nwg), dim3(kThreads), 0, s, j0, j1, M, r);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int nb0 = grid_for((P0 * r + 3) / 4);
@@ -829,10 +833,11 @@ hipError_t launch_lora_tn(const uint16_t* A, int64_t lda, const uint16_t* B, int
   const bool bvec = (r % 8) == 0 && ((uintptr_t)B & 15) == 0;
 #define QL_TN(VA, VB) \
   hipLaunchKernelGGL((k_lora_tn<VA, VB>), grid, dim3(kThreads), 0, s, A, lda, B, M, P, r, sp.chunk, ws)
-  if (avec && bvec) QL_TN(true, true);
-  else if (avec) QL_TN(true, false);
-  else if (bvec) QL_TN(false, true);
-  else QL_TN(false, false);
+  if (avec && bvec) QL_TN(kPieces, kPieces);
+  else if (P < 8 || r < 8) QL_TN(kElements, kElements);
+  else if (avec) QL_TN(kPieces, kAnywhere);
+  else if (bvec) QL_TN(kAnywhere, kPieces);
+  else QL_TN(kAnywhere, kAnywhere);
 #undef QL_TN
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
@@ -897,14 +902,17 @@ static hipError_t low_pass(const uint16_t* A, int64_t M, int64_t R, const uint16
 #define QL_LOW(BKR, VA, VB, D)                                                                                     \
   hipLaunchKernelGGL((k_lora_skinny<BKR, VA, VB, D>), grid, dim3(kThreads), 0, s, A, M, R, R, B, r, sp.chunk, ws, d)
   if (!b_is_kr) {
-    if (vec) QL_LOW(false, true, true, false);
-    else QL_LOW(false, false, false, false);
+    if (vec) QL_LOW(false, kPieces, kPieces, false);
+    else if (R < 8) QL_LOW(false, kElements, kElements, false);
+    else QL_LOW(false, kAnywhere, kAnywhere, false);
   } else if (d.cut) {
-    if (vec) QL_LOW(true, true, false, true);
-    else QL_LOW(true, false, false, true);
+    if (R < 8 || r < 8) QL_LOW(true, kElements, kElements, true);
+    else if (vec) QL_LOW(true, kPieces, kAnywhere, true);
+    else QL_LOW(true, kAnywhere, kAnywhere, true);
   } else {
-    if (vec) QL_LOW(true, true, false, false);
-    else QL_LOW(true, false, false, false);
+    if (R < 8 || r < 8) QL_LOW(true, kElements, kElements, false);
+    else if (vec) QL_LOW(true, kPieces, kAnywhere, false);
+    else QL_LOW(true, kAnywhere, kAnywhere, false);
   }
 #undef QL_LOW
   return hipGetLastError();
@@ -951,10 +959,11 @@ hipError_t launch_lora_grads3(const uint16_t* X, int64_t K, const uint16_t* G, c
       hipLaunchKernelGGL((k_lora_tn_pair3<V, T, false>), dim3(nwg), dim3(kThreads), 0, s, j0, j1, M, r, g_pitch(r), d, \
                          s0, s1, whole);                                                                            \
   } while (0)
-  if (vec && vect) QL_TN3(true, true);
-  else if (vec) QL_TN3(true, false);
-  else if (vect) QL_TN3(false, true);
-  else QL_TN3(false, false);
+  if (vec && vect) QL_TN3(kPieces, kPieces);
+  else if (K < 8 || N < 8 || r < 8) QL_TN3(kElements, kElements);
+  else if (vec) QL_TN3(kPieces, kAnywhere);
+  else if (vect) QL_TN3(kAnywhere, kPieces);
+  else QL_TN3(kAnywhere, kAnywhere);
 #undef QL_TN3
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || whole) return e;

@@ -30,7 +30,8 @@ __device__ __forceinline__ uint32_t row_or(uint32_t v) {
 // position and group.  Rows past the end repeat the last one and are not written.
 constexpr int kRows = 16;
 
-template <bool kBf16>
+// kShort: rows of fewer than eight elements.
+template <bool kBf16, bool kShort>
 __global__ __launch_bounds__(kThreads) void k_mx4_quant(const void* __restrict__ X, int64_t rows, int64_t cols,
                                                         int64_t ld, int64_t words, uint32_t* __restrict__ codes,
                                                         uint32_t* __restrict__ scales) {
@@ -41,46 +42,63 @@ __global__ __launch_bounds__(kThreads) void k_mx4_quant(const void* __restrict__
     const int64_t rt = tile / words, w = tile - rt * words;      // row tile, 128-element piece
     const int64_t col = 128 * w + 8 * part;
     u32x4 v[kRows / 4];
-    float f[kRows / 4][8];
+    f32x4 f[kRows / 4][2];
+    // every load on its way before the first is used: a piece that crosses the row's end is
+    // read as the row's last eight and moved afterwards
+    const int64_t at = min(col, cols - 8);
 #pragma unroll
     for (int i = 0; i < kRows / 4; ++i) {
-      const int64_t row = kRows * rt + 4 * i + rl;
-      const bool whole = 128 * (w + 1) <= cols;                  // uniform
+      const int64_t row = min(kRows * rt + 4 * i + rl, rows - 1);
       if constexpr (kBf16) {
-        const uint16_t* p = (const uint16_t*)X + min(row, rows - 1) * ld;
-        if (whole) v[i] = *(const u32x4_a2*)(p + col);
-        else v[i] = qk::load8_row(p, col, cols);
+        const uint16_t* p = (const uint16_t*)X + row * ld;
+        if constexpr (kShort) v[i] = qk::load8_row(p, col, cols);
+        else v[i] = *(const u32x4_a2*)(p + at);
       } else {
-        const float* p = (const float*)X + min(row, rows - 1) * ld;
-        if (whole) {
-          *(f32x4*)f[i] = *(const f32x4_a4*)(p + col);
-          *(f32x4*)(f[i] + 4) = *(const f32x4_a4*)(p + col + 4);
-        } else {
+        const float* p = (const float*)X + row * ld;
+        if constexpr (kShort) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) f[i][j] = col + j < cols ? p[col + j] : 0.0f;
+          for (int j = 0; j < 8; ++j) f[i][j >> 2][j & 3] = col + j < cols ? p[col + j] : 0.0f;
+        } else {
+          f[i][0] = *(const f32x4_a4*)(p + at);
+          f[i][1] = *(const f32x4_a4*)(p + at + 4);
         }
       }
     }
+    if (!kShort && 128 * (w + 1) > cols) {                       // uniform
+      const int s = (int)min((int64_t)8, col - at);
+#pragma unroll
+      for (int i = 0; i < kRows / 4; ++i) {
+        if constexpr (kBf16) v[i] = qk::drop_front8(v[i], s);
+        else qk::drop_front8(f[i][0], f[i][1], s);
+      }
+    }
+    // packed before any is stored: a load's wait would wait for the stores before it
+    uint32_t c[kRows / 4], word[kRows / 4];
 #pragma unroll
     for (int i = 0; i < kRows / 4; ++i) {
-      const int64_t row = kRows * rt + 4 * i + rl;
       uint32_t top = 0;
       if constexpr (kBf16) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) top = max(top, max((v[i][j] << 16) & 0x7FFFFFFFu, v[i][j] & 0x7FFF0000u));
       } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(f[i][j]) & 0x7FFFFFFFu);
+        for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(f[i][j >> 2][j & 3]) & 0x7FFFFFFFu);
       }
       const uint32_t sb = scale_byte(quad_max(top));
-      uint32_t c;
-      if constexpr (kBf16) c = encode8(v[i], scale_f32(sb));
-      else c = encode8(f[i], scale_f32(sb));
-      if (sb == 255u) c = 0;
-      const uint32_t word = row_or(sb << (8 * (part >> 2)));
+      if constexpr (kBf16) c[i] = encode8(v[i], scale_f32(sb));
+      else {
+        const float e[8] = {f[i][0][0], f[i][0][1], f[i][0][2], f[i][0][3], f[i][1][0], f[i][1][1], f[i][1][2], f[i][1][3]};
+        c[i] = encode8(e, scale_f32(sb));
+      }
+      if (sb == 255u) c[i] = 0;
+      word[i] = row_or(sb << (8 * (part >> 2)));
+    }
+#pragma unroll
+    for (int i = 0; i < kRows / 4; ++i) {
+      const int64_t row = kRows * rt + 4 * i + rl;
       if (row < rows) {
-        codes[((4 * w + (part >> 2)) * rows + row) * 4 + (part & 3)] = c;
-        if (part == 0) scales[w * rows + row] = word;
+        codes[((4 * w + (part >> 2)) * rows + row) * 4 + (part & 3)] = c[i];
+        if (part == 0) scales[w * rows + row] = word[i];
       }
     }
   }
@@ -91,7 +109,8 @@ __global__ __launch_bounds__(kThreads) void k_mx4_quant(const void* __restrict__
 // each column), a lane two columns: no exchange between lanes, 256 contiguous
 // bytes read per row (bf16), 32 written per lane.  The four waves' scale bytes
 // meet in LDS.
-template <bool kBf16>
+// kOne: cols == 1.
+template <bool kBf16, bool kOne>
 __global__ __launch_bounds__(kThreads) void k_mx4_quant_t(const void* __restrict__ X, int64_t len, int64_t cols,
                                                           int64_t ld, u32x4* __restrict__ codes,
                                                           uint32_t* __restrict__ scales) {
@@ -100,46 +119,33 @@ __global__ __launch_bounds__(kThreads) void k_mx4_quant_t(const void* __restrict
   const int64_t ctiles = (cols + 127) / 128;
   const int64_t ct = blockIdx.x % ctiles, word = blockIdx.x / ctiles;
   const int64_t c0 = 128 * ct + 2 * l, r0 = 128 * word + 32 * wv;
-  const bool whole = 128 * (ct + 1) <= cols && r0 + 32 <= len;    // uniform
   typedef uint32_t u32_a2 __attribute__((aligned(2)));
   typedef float f32x2_a4 __attribute__((ext_vector_type(2), aligned(4)));
+  // rows past the end repeat the last one, columns past it the last pair; cleared below
+  const int64_t at = cols > 1 ? min(c0, cols - 2) : 0;
   float x[2][32];
-  if constexpr (kBf16) {
-    const uint16_t* p = (const uint16_t*)X + r0 * ld + c0;
-    uint32_t d[32];
-    if (whole) {
 #pragma unroll
-      for (int k = 0; k < 32; ++k) d[k] = *(const u32_a2*)(p + k * ld);
+  for (int k = 0; k < 32; ++k) {
+    const int64_t o = min(r0 + k, len - 1) * ld + at;
+    if constexpr (kBf16) {
+      const uint16_t* p = (const uint16_t*)X + o;
+      const uint32_t d = kOne ? *p : *(const u32_a2*)p;
+      x[0][k] = __uint_as_float(d << 16);
+      x[1][k] = __uint_as_float(d & 0xFFFF0000u);
     } else {
-#pragma unroll
-      for (int k = 0; k < 32; ++k) {
-        d[k] = 0;
-        if (r0 + k < len) {
-          if (c0 < cols) d[k] = p[k * ld];
-          if (c0 + 1 < cols) d[k] |= (uint32_t)p[k * ld + 1] << 16;
-        }
-      }
+      const float* p = (const float*)X + o;
+      const f32x2_a4 y = kOne ? f32x2_a4{*p, 0.0f} : *(const f32x2_a4*)p;
+      x[0][k] = y[0];
+      x[1][k] = y[1];
     }
+  }
+  if (128 * (ct + 1) > cols || r0 + 32 > len) {                  // uniform
+    const bool second = !kOne && c0 == cols - 1;                 // its pair was read one column early
 #pragma unroll
     for (int k = 0; k < 32; ++k) {
-      x[0][k] = __uint_as_float(d[k] << 16);
-      x[1][k] = __uint_as_float(d[k] & 0xFFFF0000u);
-    }
-  } else {
-    const float* p = (const float*)X + r0 * ld + c0;
-    if (whole) {
-#pragma unroll
-      for (int k = 0; k < 32; ++k) {
-        const f32x2_a4 y = *(const f32x2_a4*)(p + k * ld);
-        x[0][k] = y[0];
-        x[1][k] = y[1];
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < 32; ++k) {
-        x[0][k] = r0 + k < len && c0 < cols ? p[k * ld] : 0.0f;
-        x[1][k] = r0 + k < len && c0 + 1 < cols ? p[k * ld + 1] : 0.0f;
-      }
+      const bool in = r0 + k < len && c0 < cols;
+      x[0][k] = in ? (second ? x[1][k] : x[0][k]) : 0.0f;
+      x[1][k] = in && c0 + 1 < cols ? x[1][k] : 0.0f;
     }
   }
 #pragma unroll
@@ -177,19 +183,21 @@ __global__ __launch_bounds__(kThreads) void k_mx4_dequant(const uint32_t* __rest
     uint32_t c[kRows / 4], sw[kRows / 4];
 #pragma unroll
     for (int i = 0; i < kRows / 4; ++i) {
-      const int64_t row = kRows * rt + 4 * i + rl;
-      const bool in = row < rows;
-      c[i] = in ? codes[((4 * w + (part >> 2)) * rows + row) * 4 + (part & 3)] : 0u;
-      sw[i] = in ? scales[w * rows + row] : 0u;
+      const int64_t row = min(kRows * rt + 4 * i + rl, rows - 1);
+      c[i] = codes[((4 * w + (part >> 2)) * rows + row) * 4 + (part & 3)];
+      sw[i] = scales[w * rows + row];
+    }
+    u32x4 v[kRows / 4];
+#pragma unroll
+    for (int i = 0; i < kRows / 4; ++i) {
+      const uint32_t sb = (sw[i] >> (8 * (part >> 2))) & 255u;
+      v[i] = decode8(c[i], scale_f32(sb));
+      if (sb == 255u) v[i] = u32x4{0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u};
     }
 #pragma unroll
     for (int i = 0; i < kRows / 4; ++i) {
       const int64_t row = kRows * rt + 4 * i + rl;
-      const uint32_t sb = (sw[i] >> (8 * (part >> 2))) & 255u;
-      u32x4 v = decode8(c[i], scale_f32(sb));
-      if (sb == 255u) v = u32x4{0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u};
-      if (row >= rows) continue;
-      if (col < cols) qk::store8_row(out + row * cols + col, v, (int)min((int64_t)8, cols - col));
+      if (row < rows && col < cols) qk::store8_row(out + row * cols + col, v[i], (int)min((int64_t)8, cols - col));
     }
   }
 }
@@ -205,25 +213,33 @@ unsigned tile_grid(int64_t rows, int64_t words) {
 hipError_t launch_mx4_quant(const void* X, bool bf16, int64_t rows, int64_t cols, int64_t ld, uint8_t* codes,
                             uint8_t* scales, hipStream_t s) {
   const int64_t words = padded(cols) / kPad;
-  const dim3 grid(tile_grid(rows, words));
-  if (bf16)
-    hipLaunchKernelGGL(k_mx4_quant<true>, grid, dim3(kThreads), 0, s, X, rows, cols, ld, words, (uint32_t*)codes,
-                       (uint32_t*)scales);
-  else
-    hipLaunchKernelGGL(k_mx4_quant<false>, grid, dim3(kThreads), 0, s, X, rows, cols, ld, words, (uint32_t*)codes,
-                       (uint32_t*)scales);
+#define QL_MQ(B, S)                                                                                                \
+  hipLaunchKernelGGL((k_mx4_quant<B, S>), dim3(tile_grid(rows, words)), dim3(kThreads), 0, s, X, rows, cols, ld,   \
+                     words, (uint32_t*)codes, (uint32_t*)scales)
+  if (bf16) {
+    if (cols < 8) QL_MQ(true, true);
+    else QL_MQ(true, false);
+  } else {
+    if (cols < 8) QL_MQ(false, true);
+    else QL_MQ(false, false);
+  }
+#undef QL_MQ
   return hipGetLastError();
 }
 
 hipError_t launch_mx4_quant_t(const void* X, bool bf16, int64_t len, int64_t cols, int64_t ld, uint8_t* codes,
                               uint8_t* scales, hipStream_t s) {
   const dim3 grid((unsigned)((cols + 127) / 128 * (padded(len) / kPad)));
-  if (bf16)
-    hipLaunchKernelGGL(k_mx4_quant_t<true>, grid, dim3(kThreads), 0, s, X, len, cols, ld, (u32x4*)codes,
-                       (uint32_t*)scales);
-  else
-    hipLaunchKernelGGL(k_mx4_quant_t<false>, grid, dim3(kThreads), 0, s, X, len, cols, ld, (u32x4*)codes,
-                       (uint32_t*)scales);
+#define QL_MQ(B, O) \
+  hipLaunchKernelGGL((k_mx4_quant_t<B, O>), grid, dim3(kThreads), 0, s, X, len, cols, ld, (u32x4*)codes, (uint32_t*)scales)
+  if (bf16) {
+    if (cols == 1) QL_MQ(true, true);
+    else QL_MQ(true, false);
+  } else {
+    if (cols == 1) QL_MQ(false, true);
+    else QL_MQ(false, false);
+  }
+#undef QL_MQ
   return hipGetLastError();
 }
 
