@@ -327,13 +327,18 @@ def qlora_linear_bwd_workspace(M, K, N, r):
     return int(lib().qlora_linear_bwd_workspace(M, K, N, r))
 
 
-def _workspace(nbytes, like, workspace):
+def _workspace(nbytes, like, workspace, stream=None):
+    """The call's scratch.  Allocated here for another stream than the current one, it is not
+    handed out again before that stream has passed the call."""
     if workspace is not None:
         _need(workspace, "workspace", torch.uint8)
         if workspace.numel() < nbytes:
             raise ValueError(f"workspace must hold at least {nbytes} bytes, got {workspace.numel()}")
         return workspace
-    return torch.empty((max(nbytes, 16),), dtype=torch.uint8, device=like.device)
+    ws = torch.empty((max(nbytes, 16),), dtype=torch.uint8, device=like.device)
+    if stream is not None and ws.is_cuda:
+        ws.record_stream(stream)
+    return ws
 
 
 def _opt_out(t, name, dtype, shape, like):
@@ -675,7 +680,7 @@ def qlora_linear_fwd_dropout(X, codes, c2, c1, N, L1, L2, lora_scale=1.0, p=0.0,
     _need(L2, "L2", torch.bfloat16, shape=(r, N))
     Y = _out(Y, "Y", torch.bfloat16, (M, N), X)
     T_out = _opt_out(T_out, "T_out", torch.bfloat16, (M, r), X)
-    ws = _workspace(int(lib().qlora_linear_fwd_dropout_workspace(M, K, N, r)), X, workspace)
+    ws = _workspace(int(lib().qlora_linear_fwd_dropout_workspace(M, K, N, r)), X, workspace, stream)
     _check("qlora_linear_fwd_dropout", lib().qlora_linear_fwd_dropout(
         _ptr(X), M, K, N, _ptr(codes), _ptr(c2), _ptr(c1), _ptr(L1), _ptr(L2), r, float(lora_scale),
         *_draw(p, seed, offset), _ptr(Y), _ptr(T_out), _ptr(ws), ws.numel(), _stream(stream)))
@@ -699,7 +704,7 @@ def qlora_linear_bwd_dropout(X, dY, codes, c2, c1, L1, L2, lora_scale=1.0, p=0.0
     dX = _opt_out(dX, "dX", torch.bfloat16, (M, K), X)
     dL1 = _out(dL1, "dL1", torch.float32, (K, r), X)
     dL2 = _out(dL2, "dL2", torch.float32, (r, N), X)
-    ws = _workspace(int(lib().qlora_linear_bwd_dropout_workspace(M, K, N, r)), X, workspace)
+    ws = _workspace(int(lib().qlora_linear_bwd_dropout_workspace(M, K, N, r)), X, workspace, stream)
     _check("qlora_linear_bwd_dropout", lib().qlora_linear_bwd_dropout(
         _ptr(X), _ptr(dY), M, K, N, _ptr(codes), _ptr(c2), _ptr(c1), _ptr(L1), _ptr(L2), r, float(lora_scale),
         *_draw(p, seed, offset), _ptr(T), _ptr(dX), _ptr(dL1), _ptr(dL2), _ptr(ws), ws.numel(), _stream(stream)))
@@ -763,7 +768,7 @@ def mx4_linear_fwd(X, codes, scales, N, L1, L2, lora_scale=1.0, p=0.0, seed=0, o
     _need(L2, "L2", torch.bfloat16, shape=(r, N))
     Y = _out(Y, "Y", torch.bfloat16, (M, N), X)
     T_out = _opt_out(T_out, "T_out", torch.bfloat16, (M, r), X)
-    ws = _workspace(int(lib().mx4_linear_fwd_workspace(M, K, N, r)), X, workspace)
+    ws = _workspace(int(lib().mx4_linear_fwd_workspace(M, K, N, r)), X, workspace, stream)
     _check("mx4_linear_fwd", lib().mx4_linear_fwd(
         _ptr(X), M, K, N, _ptr(codes), _ptr(scales), _ptr(L1), _ptr(L2), r, float(lora_scale),
         *_draw(p, seed, offset), _ptr(Y), _ptr(T_out), _ptr(ws), ws.numel(), _stream(stream)))
@@ -789,7 +794,7 @@ def mx4_linear_bwd(X, dY, codes_t, scales_t, L1, L2, lora_scale=1.0, p=0.0, seed
     dX = _opt_out(dX, "dX", torch.bfloat16, (M, K), X)
     dL1 = _out(dL1, "dL1", torch.float32, (K, r), X)
     dL2 = _out(dL2, "dL2", torch.float32, (r, N), X)
-    ws = _workspace(int(lib().mx4_linear_bwd_workspace(M, K, N, r)), X, workspace)
+    ws = _workspace(int(lib().mx4_linear_bwd_workspace(M, K, N, r)), X, workspace, stream)
     _check("mx4_linear_bwd", lib().mx4_linear_bwd(
         _ptr(X), _ptr(dY), M, K, N, _ptr(codes_t), _ptr(scales_t), _ptr(L1), _ptr(L2), r, float(lora_scale),
         *_draw(p, seed, offset), _ptr(T), _ptr(dX), _ptr(dL1), _ptr(dL2), _ptr(ws), ws.numel(), _stream(stream)))

@@ -409,3 +409,28 @@ def test_streams_workspaces_and_graph():
             torch.cuda.synchronize()
             for a, b in zip((Y, T, dX, dL1, dL2), plain()):
                 assert torch.equal(a, b), i
+
+
+@pytest.mark.parametrize("M", [8, 1024])
+def test_own_workspace_outlives_a_call_on_another_stream(M):
+    q = qlib()
+    K, N, r = 1024, 2048, 16
+    d = layer_data(M, K, N, r)
+    w = q.mx4_quantize(d["W"])
+    wt = q.mx4_quantize(d["W"], transpose=True)
+    args = dict(p=0.1, seed=5)
+    Y, T = q.mx4_linear_fwd(d["X"], *w, N, d["L1"], d["L2"], T_out=True, **args)
+    grads = q.mx4_linear_bwd(d["X"], d["dY"], *wt, d["L1"], d["L2"], T=T, **args)
+    size = max(q.lib().mx4_linear_fwd_workspace(M, K, N, r), q.lib().mx4_linear_bwd_workspace(M, K, N, r))
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)                # the calls below wait behind this
+    Y2, _ = q.mx4_linear_fwd(d["X"], *w, N, d["L1"], d["L2"], stream=side, **args)
+    grads2 = q.mx4_linear_bwd(d["X"], d["dY"], *wt, d["L1"], d["L2"], T=T, stream=side, **args)
+    junk = [torch.full((size,), 255, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    torch.cuda.synchronize()
+    assert torch.equal(Y, Y2)
+    for a, b in zip(grads, grads2):
+        assert torch.equal(a, b)
+    del junk
