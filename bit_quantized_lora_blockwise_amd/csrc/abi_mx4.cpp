@@ -19,9 +19,10 @@ bool matrix_ok(int64_t rows, int64_t cols, int64_t ld) {
 // weight, the adapters, T and G below 2^31 bytes each (the kernels' offsets are 32-bit).
 bool layer_ok(int64_t M, int64_t K, int64_t N, int r) {
   return M > 0 && K > 0 && N > 0 && M < kLim && K < kLim && N < kLim && r >= 1 && r <= 64 && M <= kLim / 2 / K &&
-         M <= kLim / 2 / N && M < kLim / 2 / r && K < kLim / 2 / r && N < kLim / 2 / r && M * K * 2 < kLim && M * N * 2 < kLim && mx4::padded(K) <= kLim / N &&
-         mx4::padded(N) <= kLim / K && mx4::code_bytes(N, K) < kLim && mx4::code_bytes(K, N) < kLim &&
-         mx4::code_bytes(M, K) < kLim && mx4::code_bytes(M, N) < kLim;
+         M <= kLim / 2 / N && M < kLim / 2 / r && K < kLim / 2 / r && N < kLim / 2 / r && M * K * 2 < kLim &&
+         M * N * 2 < kLim && mx4::padded(K) <= kLim / N && mx4::padded(N) <= kLim / K &&
+         mx4::code_bytes(N, K) < kLim && mx4::code_bytes(K, N) < kLim && mx4::code_bytes(M, K) < kLim &&
+         mx4::code_bytes(M, N) < kLim;
 }
 
 // [packed activations: codes, scales][T or the three planes of G][dense G][T of a backward without one][fp32 partials]

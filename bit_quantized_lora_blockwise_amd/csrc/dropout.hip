@@ -4,7 +4,10 @@
 //
 // One thread takes the eight elements of a row that share a draw.  Bound: HBM for
 // large bf16 matrices; the draws' quarter-rate products cost about the same time
-// as the traffic of a bf16 element (4 bytes), and overlap with it.
+// as the traffic of a bf16 element (4 bytes), and overlap with it: a thread's next
+// piece is on its way while one is drawn.  4096 x 11008 bf16 33 us (5.5 TB/s; 43 us
+// with one piece at a time and a division for each), 4096 x 11007 36 us, 2048 x 8192
+// fp32 28 us.
 #include "philox.h"
 
 #include "kernels.h"

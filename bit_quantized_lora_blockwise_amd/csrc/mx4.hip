@@ -11,7 +11,6 @@ using namespace mx4;
 
 constexpr int kThreads = 256;
 
-
 // Largest of the four lanes of a quad.
 __device__ __forceinline__ uint32_t quad_max(uint32_t v) {
   v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, true));   // quad_perm [1,0,3,2]
@@ -28,6 +27,8 @@ __device__ __forceinline__ uint32_t row_or(uint32_t v) {
 // eight elements), a wave four rows at a time and kRows / 4 such groups with all
 // their loads in flight: 256 contiguous bytes read per row, 64 written per block
 // position and group.  Rows past the end repeat the last one and are not written.
+// 22016 x 8192 bf16 83 us (5.5 TB/s; a large copy moves 5.1), 4096 x 11007 21 us,
+// 512 x 1000 2.5 us.
 constexpr int kRows = 16;
 
 // kShort: rows of fewer than eight elements.
@@ -108,7 +109,7 @@ __global__ __launch_bounds__(kThreads) void k_mx4_quant(const void* __restrict__
 // group takes 128 columns and 128 rows, wave w its rows 32 w .. +31 (one block of
 // each column), a lane two columns: no exchange between lanes, 256 contiguous
 // bytes read per row (bf16), 32 written per lane.  The four waves' scale bytes
-// meet in LDS.
+// meet in LDS.  22016 x 8192 bf16 84 us (5.4 TB/s), 4096 x 11007 26 us.
 // kOne: cols == 1.
 template <bool kBf16, bool kOne>
 __global__ __launch_bounds__(kThreads) void k_mx4_quant_t(const void* __restrict__ X, int64_t len, int64_t cols,
@@ -170,7 +171,8 @@ __global__ __launch_bounds__(kThreads) void k_mx4_quant_t(const void* __restrict
     scales[word * cols + 128 * ct + threadIdx.x] = *(const uint32_t*)sbytes[threadIdx.x];
 }
 
-// Packed -> bf16 [rows, cols], the lanes as in k_mx4_quant.
+// Packed -> bf16 [rows, cols], the lanes as in k_mx4_quant.  22016 x 8192 76 to 95 us
+// (4.8 to 6 TB/s), 4096 x 11007 32 us.
 __global__ __launch_bounds__(kThreads) void k_mx4_dequant(const uint32_t* __restrict__ codes,
                                                           const uint32_t* __restrict__ scales, int64_t rows,
                                                           int64_t cols, int64_t words, uint16_t* __restrict__ out) {

@@ -130,6 +130,11 @@ struct Gemm {
   static_assert(kLds <= 160 * 1024, "fits the LDS of a CU");
 };
 
+// Smaller products: 128 x 128 tiles, four waves of 64 x 64, two work groups a CU, four LDS
+// stages.  The adapter's product comes first, while the first stages load, and starts the
+// sums.  Bound: filling and draining the pipeline and, with few tiles, the latency of a step
+// (0.45 us with one work group a CU): 1024 x 4096 -> 8192 24 us (2.9 PFLOP/s), 256 x 11008 ->
+// 4096 a whole forward 35 us.
 template <int kMode, int kWM, int kWP, int kMT, int kPT>
 __global__ __launch_bounds__(64 * kWM * kWP) void k_mx4_gemm(const uint8_t* __restrict__ ac,
                                                              const uint8_t* __restrict__ as, int M,
@@ -360,6 +365,13 @@ __global__ __launch_bounds__(64 * kWM * kWP) void k_mx4_gemm(const uint8_t* __re
 // during the reduction, a Philox round between two products: the vector unit is
 // free while the other wave's product runs, where a draw before the loop took 8 us
 // a tile.
+// Bound: the matrix unit under the chip's power limit.  A step of 128 takes 0.85 us on
+// random data (5.0 PFLOP/s; 0.51 us on zeros, and 6.7 PFLOP/s is what the products alone
+// reach on random data); the clock is then about 1.85 GHz and the matrix unit busy half of
+// its cycles (counters at 2048 x 8192 x 22016: 190 us, 3.9 PFLOP/s, with the last
+// of 2.7 rounds of tiles and 10 us of launch, first loads and last stores; no LDS bank
+// conflicts).  4096 x 11008 x 4096 backward with dropout 115 us.  A P that is no multiple
+// of 8 costs in the stores: 4093 x 4097 -> 11007 157 us, -> 11008 120 us.
 constexpr int kRT = 512;                    // threads
 constexpr int kRB = 256;                    // tile edge
 constexpr int kRCodes = kRB * 64;           // bytes of one operand's codes in a step
@@ -699,7 +711,11 @@ hipError_t launch(const uint8_t* ac, const uint8_t* as, int64_t M, const uint8_t
 
 hipError_t launch_mx4_gemm(const uint8_t* ac, const uint8_t* as, int64_t M, const uint8_t* bc, const uint8_t* bs,
                            int64_t P, int64_t R, const Mx4Lora& lora, uint16_t* C, hipStream_t s) {
-  const bool big = ((M + 255) / 256) * ((P + 255) / 256) >= 128 && padded(R) / kPad >= kRMinWords;
+  // The smaller tiles run two to a CU: while all of them fit on the chip at once they win,
+  // then the ring does.  Small and ring, us: 512 tiles of 128 x 128 (1024 x 4096 -> 8192) 24
+  // and 30, whole forward 42 and 45, backward 66 and 70; 516 (768 x 4096 -> 11008) 32 and 30,
+  // 54 and 45, 78 and 70; 256 (1024 x 4096 -> 4096) 16 and 26.
+  const bool big = ((M + 127) / 128) * ((P + 127) / 128) > 512 && padded(R) / kPad >= kRMinWords;
   const bool vec = P % 8 == 0 && (!lora.A || lora.r % 8 == 0);
 #define QL_MX(MODE)                                                                                      \
   return !big ? launch<MODE, 2, 2, 2, 2>(ac, as, M, bc, bs, P, R, lora, C, s)                            \

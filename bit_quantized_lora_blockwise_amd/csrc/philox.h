@@ -8,8 +8,9 @@
 // offset high), key (seed low, seed high); element k takes half k % 2 (low half
 // first) of output word (k % 8) / 2, so one call decides the eight elements that
 // a 16-byte load of bf16 brings.  32-bit products run at a quarter of the VALU
-// rate, which makes the seven rounds about 340 cycles a wave; 16 bits a decision
-// rather than 32 halve that, and leave p a step of 2^-16.
+// rate, which makes the seven rounds about 340 cycles a wave (12 us for the 45 M
+// elements of 4096 x 11008 on the whole chip); 16 bits a decision rather than 32 halve
+// that, and leave p a step of 2^-16.
 #pragma once
 
 #include "common.h"

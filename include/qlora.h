@@ -435,8 +435,9 @@ int mx4_matmul(const uint8_t* a_codes, const uint8_t* a_scales, int64_t M,
  *        passed straight through. The base gets no gradient.
  * G is kept to 24 bits for dL1 and rounded to bf16 for dX. T is the forward's T_out;
  * when NULL it is formed again with the same mask. Any K and N >= 1, 1 <= r <= 64;
- * X and dX, Y and dY, and each packed matrix must stay below 2^31 bytes. Device
- * pointers 16-byte aligned; workspaces from the queries.                         */
+ * X and dX, Y and dY, each packed matrix and each factor of the adapter must stay
+ * below 2^31 bytes (QL_ERR_SHAPE otherwise). Device pointers 16-byte aligned;
+ * workspaces from the queries.                                                   */
 size_t mx4_linear_fwd_workspace(int64_t M, int64_t K, int64_t N, int r);
 int mx4_linear_fwd(const uint16_t* X, int64_t M, int64_t K, int64_t N, const uint8_t* codes, const uint8_t* scales,
                    const uint16_t* L1, const uint16_t* L2, int r, float lora_scale,
