@@ -17,7 +17,7 @@ namespace {
 constexpr int kThreads = 256;
 
 // kWhole: cols % 8 == 0, no piece crosses a row's end.
-template <bool kBf16, bool kWhole>
+template <bool kBf16, bool kWhole, bool kPast>
 __global__ __launch_bounds__(kThreads) void k_dropout(const void* __restrict__ X, int64_t rows, int64_t cols,
                                                       int64_t ld, drop::Params d, void* __restrict__ Y) {
   const int64_t octs = (cols + 7) / 8, stride = (int64_t)gridDim.x * kThreads;
@@ -32,13 +32,13 @@ __global__ __launch_bounds__(kThreads) void k_dropout(const void* __restrict__ X
     Piece x = {};
     if constexpr (kBf16) {
       const uint16_t* src = (const uint16_t*)X + m * ld;
-      if (kWhole || 8 * q + 8 <= cols) x.v[0] = *(const u32x4_a2*)(src + 8 * q);
+      if (kWhole || 8 * q + 8 <= cols) x.v[0] = qk::load_past<kPast>((const u32x4_a2*)(src + 8 * q));
       else x.v[0] = qk::load8_row(src, 8 * q, cols);
     } else {
       const float* src = (const float*)X + m * ld + 8 * q;
       if (kWhole || 8 * q + 8 <= cols) {
-        x.v[0] = __builtin_bit_cast(u32x4, *(const f32x4_a4*)src);
-        x.v[1] = __builtin_bit_cast(u32x4, *(const f32x4_a4*)(src + 4));
+        x.v[0] = __builtin_bit_cast(u32x4, qk::load_past<kPast>((const f32x4_a4*)src));
+        x.v[1] = __builtin_bit_cast(u32x4, qk::load_past<kPast>((const f32x4_a4*)(src + 4)));
       } else {
 #pragma unroll
         for (int j = 0; j < 7; ++j) x.v[j >> 2][j & 3] = 8 * q + j < cols ? __float_as_uint(src[j]) : 0u;
@@ -74,12 +74,17 @@ __global__ __launch_bounds__(kThreads) void k_dropout(const void* __restrict__ X
       }
     }
     if constexpr (kBf16) {
-      qk::store8_row((uint16_t*)Y + m * cols + 8 * q, x.v[0], n);
+      qk::store8_row<kPast>((uint16_t*)Y + m * cols + 8 * q, x.v[0], n);
     } else {
       float* dst = (float*)Y + m * cols + 8 * q;
       if (n == 8) {
-        *(f32x4_a4*)dst = __builtin_bit_cast(f32x4, x.v[0]);
-        *(f32x4_a4*)(dst + 4) = __builtin_bit_cast(f32x4, x.v[1]);
+        if constexpr (kPast) {
+          __builtin_nontemporal_store(__builtin_bit_cast(f32x4, x.v[0]), (f32x4_a4*)dst);
+          __builtin_nontemporal_store(__builtin_bit_cast(f32x4, x.v[1]), (f32x4_a4*)(dst + 4));
+        } else {
+          *(f32x4_a4*)dst = __builtin_bit_cast(f32x4, x.v[0]);
+          *(f32x4_a4*)(dst + 4) = __builtin_bit_cast(f32x4, x.v[1]);
+        }
       } else {
 #pragma unroll
         for (int j = 0; j < 7; ++j)
@@ -99,15 +104,22 @@ hipError_t launch_dropout(const void* X, bool bf16, int64_t rows, int64_t cols, 
   int64_t grid = (octs + kThreads - 1) / kThreads;
   if (grid > 8192) grid = 8192;
   const bool whole = cols % 8 == 0;
-#define QL_DROP(B, W) \
-  hipLaunchKernelGGL((k_dropout<B, W>), dim3((unsigned)grid), dim3(kThreads), 0, s, X, rows, cols, ld, d, Y)
+  const bool past = rows * cols * (bf16 ? 2 : 4) > qk::kStreamBytes;
+#define QL_DROP(B, W, P) \
+  hipLaunchKernelGGL((k_dropout<B, W, P>), dim3((unsigned)grid), dim3(kThreads), 0, s, X, rows, cols, ld, d, Y)
+#define QL_DROP_W(B, P)           \
+  do {                            \
+    if (whole) QL_DROP(B, true, P); \
+    else QL_DROP(B, false, P);    \
+  } while (0)
   if (bf16) {
-    if (whole) QL_DROP(true, true);
-    else QL_DROP(true, false);
+    if (past) QL_DROP_W(true, true);
+    else QL_DROP_W(true, false);
   } else {
-    if (whole) QL_DROP(false, true);
-    else QL_DROP(false, false);
+    if (past) QL_DROP_W(false, true);
+    else QL_DROP_W(false, false);
   }
+#undef QL_DROP_W
 #undef QL_DROP
   return hipGetLastError();
 }

@@ -27,12 +27,12 @@ __device__ __forceinline__ uint32_t row_or(uint32_t v) {
 // eight elements), a wave four rows at a time and kRows / 4 such groups with all
 // their loads in flight: 256 contiguous bytes read per row, 64 written per block
 // position and group.  Rows past the end repeat the last one and are not written.
-// 22016 x 8192 bf16 83 us (5.5 TB/s; a large copy moves 5.1), 4096 x 11007 21 us,
+// 22016 x 8192 bf16 78 us (5.9 TB/s; a large copy moves 5.1), 4096 x 11007 21 us,
 // 512 x 1000 2.5 us.
 constexpr int kRows = 16;
 
 // kShort: rows of fewer than eight elements.
-template <bool kBf16, bool kShort>
+template <bool kBf16, bool kShort, bool kPast>
 __global__ __launch_bounds__(kThreads) void k_mx4_quant(const void* __restrict__ X, int64_t rows, int64_t cols,
                                                         int64_t ld, int64_t words, uint32_t* __restrict__ codes,
                                                         uint32_t* __restrict__ scales) {
@@ -53,15 +53,15 @@ __global__ __launch_bounds__(kThreads) void k_mx4_quant(const void* __restrict__
       if constexpr (kBf16) {
         const uint16_t* p = (const uint16_t*)X + row * ld;
         if constexpr (kShort) v[i] = qk::load8_row(p, col, cols);
-        else v[i] = *(const u32x4_a2*)(p + at);
+        else v[i] = qk::load_past<kPast>((const u32x4_a2*)(p + at));
       } else {
         const float* p = (const float*)X + row * ld;
         if constexpr (kShort) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) f[i][j >> 2][j & 3] = col + j < cols ? p[col + j] : 0.0f;
         } else {
-          f[i][0] = *(const f32x4_a4*)(p + at);
-          f[i][1] = *(const f32x4_a4*)(p + at + 4);
+          f[i][0] = qk::load_past<kPast>((const f32x4_a4*)(p + at));
+          f[i][1] = qk::load_past<kPast>((const f32x4_a4*)(p + at + 4));
         }
       }
     }
@@ -109,9 +109,9 @@ __global__ __launch_bounds__(kThreads) void k_mx4_quant(const void* __restrict__
 // group takes 128 columns and 128 rows, wave w its rows 32 w .. +31 (one block of
 // each column), a lane two columns: no exchange between lanes, 256 contiguous
 // bytes read per row (bf16), 32 written per lane.  The four waves' scale bytes
-// meet in LDS.  22016 x 8192 bf16 84 us (5.4 TB/s), 4096 x 11007 26 us.
+// meet in LDS.  22016 x 8192 bf16 77 us (5.9 TB/s), 4096 x 11007 26 us.
 // kOne: cols == 1.
-template <bool kBf16, bool kOne>
+template <bool kBf16, bool kOne, bool kPast>
 __global__ __launch_bounds__(kThreads) void k_mx4_quant_t(const void* __restrict__ X, int64_t len, int64_t cols,
                                                           int64_t ld, u32x4* __restrict__ codes,
                                                           uint32_t* __restrict__ scales) {
@@ -130,12 +130,12 @@ __global__ __launch_bounds__(kThreads) void k_mx4_quant_t(const void* __restrict
     const int64_t o = min(r0 + k, len - 1) * ld + at;
     if constexpr (kBf16) {
       const uint16_t* p = (const uint16_t*)X + o;
-      const uint32_t d = kOne ? *p : *(const u32_a2*)p;
+      const uint32_t d = kOne ? *p : qk::load_past<kPast>((const u32_a2*)p);
       x[0][k] = __uint_as_float(d << 16);
       x[1][k] = __uint_as_float(d & 0xFFFF0000u);
     } else {
       const float* p = (const float*)X + o;
-      const f32x2_a4 y = kOne ? f32x2_a4{*p, 0.0f} : *(const f32x2_a4*)p;
+      const f32x2_a4 y = kOne ? f32x2_a4{*p, 0.0f} : qk::load_past<kPast>((const f32x2_a4*)p);
       x[0][k] = y[0];
       x[1][k] = y[1];
     }
@@ -171,8 +171,9 @@ __global__ __launch_bounds__(kThreads) void k_mx4_quant_t(const void* __restrict
     scales[word * cols + 128 * ct + threadIdx.x] = *(const uint32_t*)sbytes[threadIdx.x];
 }
 
-// Packed -> bf16 [rows, cols], the lanes as in k_mx4_quant.  22016 x 8192 76 to 95 us
-// (4.8 to 6 TB/s), 4096 x 11007 32 us.
+// Packed -> bf16 [rows, cols], the lanes as in k_mx4_quant.  22016 x 8192 70 to 87 us
+// (5.2 to 6.5 TB/s), 4096 x 11007 32 us.
+template <bool kPast>
 __global__ __launch_bounds__(kThreads) void k_mx4_dequant(const uint32_t* __restrict__ codes,
                                                           const uint32_t* __restrict__ scales, int64_t rows,
                                                           int64_t cols, int64_t words, uint16_t* __restrict__ out) {
@@ -199,7 +200,7 @@ __global__ __launch_bounds__(kThreads) void k_mx4_dequant(const uint32_t* __rest
 #pragma unroll
     for (int i = 0; i < kRows / 4; ++i) {
       const int64_t row = kRows * rt + 4 * i + rl;
-      if (row < rows && col < cols) qk::store8_row(out + row * cols + col, v[i], (int)min((int64_t)8, cols - col));
+      if (row < rows && col < cols) qk::store8_row<kPast>(out + row * cols + col, v[i], (int)min((int64_t)8, cols - col));
     }
   }
 }
@@ -215,15 +216,18 @@ unsigned tile_grid(int64_t rows, int64_t words) {
 hipError_t launch_mx4_quant(const void* X, bool bf16, int64_t rows, int64_t cols, int64_t ld, uint8_t* codes,
                             uint8_t* scales, hipStream_t s) {
   const int64_t words = padded(cols) / kPad;
-#define QL_MQ(B, S)                                                                                                \
-  hipLaunchKernelGGL((k_mx4_quant<B, S>), dim3(tile_grid(rows, words)), dim3(kThreads), 0, s, X, rows, cols, ld,   \
+  const bool past = rows * cols * (bf16 ? 2 : 4) > qk::kStreamBytes;
+#define QL_MQ(B, S, P)                                                                                            \
+  hipLaunchKernelGGL((k_mx4_quant<B, S, P>), dim3(tile_grid(rows, words)), dim3(kThreads), 0, s, X, rows, cols, ld, \
                      words, (uint32_t*)codes, (uint32_t*)scales)
   if (bf16) {
-    if (cols < 8) QL_MQ(true, true);
-    else QL_MQ(true, false);
+    if (cols < 8) QL_MQ(true, true, false);
+    else if (past) QL_MQ(true, false, true);
+    else QL_MQ(true, false, false);
   } else {
-    if (cols < 8) QL_MQ(false, true);
-    else QL_MQ(false, false);
+    if (cols < 8) QL_MQ(false, true, false);
+    else if (past) QL_MQ(false, false, true);
+    else QL_MQ(false, false, false);
   }
 #undef QL_MQ
   return hipGetLastError();
@@ -232,14 +236,18 @@ hipError_t launch_mx4_quant(const void* X, bool bf16, int64_t rows, int64_t cols
 hipError_t launch_mx4_quant_t(const void* X, bool bf16, int64_t len, int64_t cols, int64_t ld, uint8_t* codes,
                               uint8_t* scales, hipStream_t s) {
   const dim3 grid((unsigned)((cols + 127) / 128 * (padded(len) / kPad)));
-#define QL_MQ(B, O) \
-  hipLaunchKernelGGL((k_mx4_quant_t<B, O>), grid, dim3(kThreads), 0, s, X, len, cols, ld, (u32x4*)codes, (uint32_t*)scales)
+  const bool past = len * cols * (bf16 ? 2 : 4) > qk::kStreamBytes;
+#define QL_MQ(B, O, P)                                                                                           \
+  hipLaunchKernelGGL((k_mx4_quant_t<B, O, P>), grid, dim3(kThreads), 0, s, X, len, cols, ld, (u32x4*)codes,      \
+                     (uint32_t*)scales)
   if (bf16) {
-    if (cols == 1) QL_MQ(true, true);
-    else QL_MQ(true, false);
+    if (cols == 1) QL_MQ(true, true, false);
+    else if (past) QL_MQ(true, false, true);
+    else QL_MQ(true, false, false);
   } else {
-    if (cols == 1) QL_MQ(false, true);
-    else QL_MQ(false, false);
+    if (cols == 1) QL_MQ(false, true, false);
+    else if (past) QL_MQ(false, false, true);
+    else QL_MQ(false, false, false);
   }
 #undef QL_MQ
   return hipGetLastError();
@@ -248,7 +256,8 @@ hipError_t launch_mx4_quant_t(const void* X, bool bf16, int64_t len, int64_t col
 hipError_t launch_mx4_dequant(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, uint16_t* out,
                               hipStream_t s) {
   const int64_t words = padded(cols) / kPad;
-  hipLaunchKernelGGL(k_mx4_dequant, dim3(tile_grid(rows, words)), dim3(kThreads), 0, s, (const uint32_t*)codes,
-                     (const uint32_t*)scales, rows, cols, words, out);
+  const bool past = rows * cols * 2 > qk::kStreamBytes;
+  hipLaunchKernelGGL((past ? k_mx4_dequant<true> : k_mx4_dequant<false>), dim3(tile_grid(rows, words)), dim3(kThreads), 0, s,
+                     (const uint32_t*)codes, (const uint32_t*)scales, rows, cols, words, out);
   return hipGetLastError();
 }

@@ -434,3 +434,33 @@ def test_own_workspace_outlives_a_call_on_another_stream(M):
     for a, b in zip(grads, grads2):
         assert torch.equal(a, b)
     del junk
+
+
+@pytest.mark.parametrize("rows,cols,dtype", [(16500, 8200, torch.bfloat16), (16411, 8203, torch.bfloat16),
+                                             (8300, 8203, torch.float32), (8208, 8192, torch.float32)])
+def test_larger_than_the_last_level_cache(rows, cols, dtype):
+    """The same bits as on parts of the matrix small enough to go through the cache."""
+    q = qlib()
+    X = torch.randn(rows, cols, device=DEV, dtype=torch.float32).to(dtype)
+    assert X.numel() * X.element_size() > 256 << 20
+    parts = [slice(0, 70), slice(rows // 2, rows // 2 + 33), slice(rows - 41, rows)]
+    cparts = [slice(0, 64), slice(cols - 72, cols)]
+    D = q.lora_dropout(X, 0.3, 7, 9)
+    assert torch.equal(D[:70], q.lora_dropout(X[:70], 0.3, 7, 9))
+    assert torch.equal(D[:, :64], q.lora_dropout(X[:, :64], 0.3, 7, 9))
+    kept = D != 0
+    assert abs(kept[:, -72:].float().mean().item() - 0.7) < 0.01
+    scale = 65536 / (65536 - X4.cut_of(0.3))
+    assert torch.equal(D[kept], (X[kept].float() * scale).to(dtype))
+    codes, scales = q.mx4_quantize(X)
+    for s in parts:
+        c, e = q.mx4_quantize(X[s].clone())
+        assert torch.equal(codes[:, s], c) and torch.equal(scales[:, s], e)
+    tc, te = q.mx4_quantize(X, transpose=True)
+    for s in cparts:
+        c, e = q.mx4_quantize(X[:, s].clone(), transpose=True)
+        assert torch.equal(tc[:, s], c) and torch.equal(te[:, s], e)
+    V = q.mx4_dequantize(codes, scales, rows, cols)
+    for s in parts:
+        n = s.stop - s.start
+        assert torch.equal(V[s], q.mx4_dequantize(codes[:, s].contiguous(), scales[:, s].contiguous(), n, cols))
