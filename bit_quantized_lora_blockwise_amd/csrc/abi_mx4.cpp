@@ -196,13 +196,11 @@ int qlora_linear_fwd_dropout(const uint16_t* X, int64_t M, int64_t K, int64_t N,
   // The decode kernel takes 16 rows; up to three passes of it over the packed weight stay
   // below the 256-row tiles of the large kernel (48 rows: 4096 -> 11008 41 and 80 us,
   // 11008 -> 4096 47 and 204 us, 8192 -> 22016 115 and 152 us, 512 -> 512 11 and 19 us).
-  const int64_t step = M <= 48 ? 16 : M;
-  for (int64_t m = 0; m < M; m += step) {
-    const int e = qlora_linear_fwd_t(X + m * K, std::min(step, M - m), K, N, codes, c2, c1, T + m * r, L2, r, lora_scale,
-                                     Y + m * N, stream);
-    if (e != QL_OK) return e;
+  if (fwd_small_ok(M, N)) {
+    QL_TRY(launch_fwd_small(X, M, K, N, codes, c2, c1, T, L2, r, lora_scale, Y, (hipStream_t)stream));
+    return QL_OK;
   }
-  return QL_OK;
+  return qlora_linear_fwd_t(X, M, K, N, codes, c2, c1, T, L2, r, lora_scale, Y, stream);
 }
 
 size_t qlora_linear_bwd_dropout_workspace(int64_t M, int64_t K, int64_t N, int r) {

@@ -1,4 +1,4 @@
-// dX of the NF4 layer for few rows:
+// The NF4 layer with dropout for few rows.  dX:
 //   dX = bf16(dY W' + D o (G L1^T))       (transposed-weight path)
 // Work group: 32 rows of dY, 64 columns of dX (one first-level block wide); eight waves
 // split the reduction over W's stored rows, 32 rows at a time.  A wave rebuilds its 32 x 64
@@ -129,12 +129,147 @@ __global__ __launch_bounds__(64 * kW) void k_dx_small(const uint16_t* __restrict
   }
 }
 
+// Y of the NF4 layer for few rows: Y = bf16(X W'^T + s T L2).  Work group: 32 kI rows of X,
+// 32 kJ rows of W; eight waves split the reduction, a block of 64 at a time.  The halves
+// of a wave take the halves of a block, in both operands: the codes that a lane needs are
+// 16 consecutive bytes, rebuilt in registers as the matrix operand, with no LDS but for
+// the waves' sums, which meet there in order.
+template <bool kVecR, int kI, int kJ>
+__global__ __launch_bounds__(64 * kW) void k_fwd_small(const uint16_t* __restrict__ X, int M, int K, int N,
+                                                       const uint8_t* __restrict__ codes,
+                                                       const uint8_t* __restrict__ c2, const float* __restrict__ c1,
+                                                       const uint16_t* __restrict__ T, const uint16_t* __restrict__ L2,
+                                                       int r, float scale, uint16_t* __restrict__ Y, Nf4Params q) {
+  __shared__ f32x16 red[kW][kI * kJ][64];
+  const int w = threadIdx.x >> 6, l = threadIdx.x & 63, h = l >> 5, x = l & 31;
+  const int n0 = 32 * kJ * (int)blockIdx.x, m0 = 32 * kI * (int)blockIdx.y;
+  const int kb = K / 64;
+  const __amdgpu_buffer_rsrc_t rx = rsrc(X, (uint64_t)M * K * 2), rc = rsrc(codes, (uint64_t)N * (K / 2)),
+                               r2 = rsrc(c2, (uint64_t)N * kb), r1 = rsrc(c1, 4 * (((uint64_t)N * kb + 255) / 256));
+  const SplitConst kc = split_const();
+
+  // block b: lane (x, h) holds columns 32 h .. +31 of it, of rows x, 32 + x, .. of X and W
+  struct Step {
+    u32x4 c[kJ];
+    uint32_t s2[kJ];
+    float s1[kJ];
+    bf16x8 a[kI][4];
+  };
+  auto load = [&](int b) {
+    Step s;
+#pragma unroll
+    for (int j = 0; j < kJ; ++j) {
+      const int n = n0 + 32 * j + x;
+      const bool in = n < N && b < kb;
+      const uint32_t at = (uint32_t)n * kb + b;
+      s.c[j] = __builtin_amdgcn_raw_buffer_load_b128(rc, in ? (uint32_t)n * (K / 2) + 32 * b + 16 * h : kOOB, 0, 0);
+      s.s2[j] = __builtin_amdgcn_raw_buffer_load_b8(r2, in ? at : kOOB, 0, 0);
+      s.s1[j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r1, in ? 4 * (at >> 8) : kOOB, 0, 0));
+    }
+#pragma unroll
+    for (int i = 0; i < kI; ++i) {
+      const int m = m0 + 32 * i + x;
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        s.a[i][u] = load8<true>(rx, ((uint32_t)m * K + 64 * b + 32 * h + 8 * u) * 2u, m < M && b < kb ? 8 : 0);
+    }
+    return s;
+  };
+  f32x16 acc[kI][kJ] = {};
+  Step cur = load(w);
+  for (int b = w; b < kb; b += kW) {
+    const Step nxt = load(b + kW);
+#pragma unroll
+    for (int j = 0; j < kJ; ++j) {
+      const BlockLut lut = make_lut(qk::e4m3fn_to_f32(cur.s2[j]) * cur.s1[j], q);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const bf16x8 v = __builtin_bit_cast(bf16x8, dequant8(lut, cur.c[j][u], kc));
+#pragma unroll
+        for (int i = 0; i < kI; ++i) acc[i][j] = qk::mfma32(v, cur.a[i][u], acc[i][j]);
+      }
+    }
+    cur = nxt;
+  }
+#pragma unroll
+  for (int i = 0; i < kI; ++i)
+#pragma unroll
+    for (int j = 0; j < kJ; ++j) red[w][kJ * i + j][l] = acc[i][j];
+  // the first waves finish a tile of 32 x 32 each
+  const int p = n0 + 32 * (w % kJ), m = m0 + 32 * (w / kJ) + x;
+  f32x16 low = {};
+  if (w < kI * kJ) {
+    const __amdgpu_buffer_rsrc_t rt = rsrc(T, (uint64_t)M * r * 2), rl = rsrc(L2, (uint64_t)N * r * 2);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const int c = 16 * s + 8 * h;
+      uint32_t e[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        e[k] = __builtin_amdgcn_raw_buffer_load_b16(rl, c + k < r && p + x < N ? (uint32_t)((c + k) * N + p + x) * 2u : kOOB, 0, 0);
+      const u32x4 a = {e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
+      const bf16x8 b = load8<kVecR>(rt, (uint32_t)(m * r + c) * 2u, m < M ? r - c : 0);
+      low = qk::mfma32(__builtin_bit_cast(bf16x8, a), b, low);
+    }
+  }
+  __syncthreads();
+  if (w >= kI * kJ || m >= M) return;
+  f32x16 sum = red[0][w][l];
+#pragma unroll
+  for (int i = 1; i < kW; ++i) sum += red[i][w][l];
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const int n = p + 8 * g + 4 * h;
+    uint16_t* y = Y + (int64_t)m * N + n;
+    const u32x2 o = {qk::pack_bf16x2(sum[4 * g] + scale * low[4 * g], sum[4 * g + 1] + scale * low[4 * g + 1]),
+                     qk::pack_bf16x2(sum[4 * g + 2] + scale * low[4 * g + 2], sum[4 * g + 3] + scale * low[4 * g + 3])};
+    if ((N & 3) == 0) {
+      if (n < N) *(u32x2*)y = o;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (n + e < N) y[e] = (uint16_t)(o[e >> 1] >> (16 * (e & 1)));
+    }
+  }
+}
+
 }  // namespace
 
-// Up to 64 rows, or more while the work groups (32 rows, 64 columns) are no more than
-// CUs.  With 32 rows of them: 11008 -> 4096 23 us here, 87 us with the large tiles;
-// 4096 -> 11008 53 and 213 us; 8192 -> 22016 117 and 406 us; 512 -> 512 5 and 22 us.
-bool dx_small_ok(int64_t M, int64_t K) { return M <= 64 || (K / kP) * ((M + 31) / 32) <= 256; }
+// More rows than the decode kernels take at once (and up to 48, three times as many, for any
+// N that L2's 32-bit offsets reach), up to 2.5 work groups of 64 x 64 a CU;
+// the large tiles walk the whole reduction in one work group, and leave CUs idle while they
+// are few.  Whole forwards with dropout, us, decode kernels in passes of 16 rows or large tiles / here: 32
+// rows 512 -> 512 14 / 13, 4096 -> 11008 38 / 30, 11008 -> 4096 45 / 44, 8192 -> 22016 92 /
+// 80; 128 rows 4096 -> 11008 95 / 69, 11008 -> 4096 222 / 58, 8576 -> 631 173 / 36; 512 rows 11008 ->
+// 4096 229 / 148; 256 rows 4096 -> 11008 (688 work groups) 98 / 100, 8192 -> 22016 (1376) 184 / 322.
+bool fwd_small_ok(int64_t M, int64_t N) {
+  return M > 16 && N < (int64_t(1) << 24) && (M <= 48 || (N + 63) / 64 * ((M + 63) / 64) <= 640);
+}
+
+// Bound: rebuilding the weights (3.6 vector instructions each) for every 32 kI rows, so
+// tiles are as large as fills the chip: 64 rows 4096 -> 4096 25, 29 and 38 us with 32 x 32,
+// 32 x 64 and 64 x 64 tiles, 128 rows 37, 30 and 39, 256 rows 62, 48 and 41.
+hipError_t launch_fwd_small(const uint16_t* X, int64_t M, int64_t K, int64_t N, const uint8_t* codes, const uint8_t* c2,
+                            const float* c1, const uint16_t* T, const uint16_t* L2, int r, float scale, uint16_t* Y,
+                            hipStream_t s) {
+  const int64_t rows = (M + 31) / 32;
+#define QL_FW(I, J)                                                                                                  \
+  hipLaunchKernelGGL((r % 8 == 0 ? k_fwd_small<true, I, J> : k_fwd_small<false, I, J>),                              \
+                     dim3((unsigned)((N + 32 * J - 1) / (32 * J)), (unsigned)((M + 32 * I - 1) / (32 * I))),         \
+                     dim3(64 * kW), 0, s, X, (int)M, (int)K, (int)N, codes, c2, c1, T, L2, r, scale, Y, nf4_params())
+  if ((N + 31) / 32 * rows <= 256) QL_FW(1, 1);
+  else if ((N + 63) / 64 * rows <= 256 || rows == 1) QL_FW(1, 2);
+  else QL_FW(2, 2);
+#undef QL_FW
+  return hipGetLastError();
+}
+
+// Up to 64 rows, or up to three work groups (32 rows, 64 columns of dX) a CU.  Whole backwards
+// with dropout, us, here / large tiles: 32 rows 4096 -> 11008 71 / 235, 11008 -> 4096 38 / 109,
+// 8192 -> 22016 144 / 438, 512 -> 512 18 / 41; 128 rows 11008 -> 4096 85 / 112 (688 work groups),
+// 8192 -> 22016 262 / 445 (512); 512 rows 4096 -> 4096 105 / 117 (1024); 256 rows 8192 -> 22016
+// 489 / 446 (1024), 11008 -> 4096 159 / 116 (1376).
+bool dx_small_ok(int64_t M, int64_t K) { return M <= 64 || (K / kP) * ((M + 31) / 32) <= 768; }
 
 hipError_t launch_dx_small(const uint16_t* dY, int64_t M, int64_t K, int64_t N, const uint8_t* codes, const uint8_t* c2,
                            const float* c1, const uint16_t* G, const uint16_t* L1, int r, uint16_t* dX,

@@ -226,6 +226,10 @@ hipError_t launch_qgemm_dx(const uint16_t* dY, int64_t M, int64_t K, int64_t N, 
                            const uint8_t* c2, const float* c1, const uint16_t* G, const uint16_t* L1, int r,
                            uint16_t* dX, hipStream_t s, const drop::Params* d = nullptr);
 // The same with dropout for few rows (gemm_small.hip): dX = bf16(dY W' + D o (G L1^T))
+bool fwd_small_ok(int64_t M, int64_t N);
+hipError_t launch_fwd_small(const uint16_t* X, int64_t M, int64_t K, int64_t N, const uint8_t* codes, const uint8_t* c2,
+                            const float* c1, const uint16_t* T, const uint16_t* L2, int r, float scale, uint16_t* Y,
+                            hipStream_t s);
 bool dx_small_ok(int64_t M, int64_t K);
 hipError_t launch_dx_small(const uint16_t* dY, int64_t M, int64_t K, int64_t N, const uint8_t* codes, const uint8_t* c2,
                            const float* c1, const uint16_t* G, const uint16_t* L1, int r, uint16_t* dX,
