@@ -35,13 +35,16 @@ Ws fwd_ws(int64_t M, int64_t K, int r) {
   w.total = w.codes + w.scales + w.low + w.part;
   return w;
 }
+// Rows up to which the NF4 layer with dropout forms T and G as slices that its products add up.
+constexpr int64_t kFew = 64;
+
 // packed = false: the backward over another base, which multiplies the bf16 gradient
 Ws bwd_ws(int64_t M, int64_t K, int64_t N, int r, bool packed) {
   Ws w{packed ? round_up(mx4::code_bytes(M, N)) : 0, packed ? round_up(mx4::scale_bytes(M, N)) : 0,
        round_up((size_t)3 * M * g_pitch(r) * 2), r == g_pitch(r) ? 0 : round_up((size_t)M * r * 2),
        round_up((size_t)M * r * 2), 0, 0};
   w.part = round_up(std::max({lora_skinny_ws(M, N, r), lora_skinny_ws(M, K, r), lora_grads3_ws(M, K, N, r),
-                              packed ? mx4_small_ws(M, r) : 0}));
+                              mx4_small_ws(packed ? M : std::min(M, kFew), r)}));
   w.total = w.codes + w.scales + w.low + w.dense + w.t + w.part;
   return w;
 }
@@ -172,8 +175,11 @@ int mx4_linear_bwd(const uint16_t* X, const uint16_t* dY, int64_t M, int64_t K, 
 }
 
 // ---- dropout on the adapter of the NF4 layer ------------------------------------
+static bool few_ok(int64_t M, int64_t K, int64_t N, int r) { return M <= kFew && layer_ok(M, K, N, r); }
+
 size_t qlora_linear_fwd_dropout_workspace(int64_t M, int64_t K, int64_t N, int r) {
-  return qlora_linear_fwd_workspace(M, K, N, r);
+  const size_t plain = qlora_linear_fwd_workspace(M, K, N, r);
+  return plain == 0 ? 0 : std::max(plain, round_up((size_t)M * r * 2) + mx4_small_ws(std::min(M, kFew), r));
 }
 
 int qlora_linear_fwd_dropout(const uint16_t* X, int64_t M, int64_t K, int64_t N, const uint8_t* codes,
@@ -181,7 +187,7 @@ int qlora_linear_fwd_dropout(const uint16_t* X, int64_t M, int64_t K, int64_t N,
                              float lora_scale, double p, uint64_t seed, uint64_t offset, uint16_t* Y, uint16_t* T_out,
                              void* workspace, size_t ws_bytes, void* stream) {
   if (!X || !codes || !c2 || !c1 || !L1 || !L2 || !Y) return QL_ERR_NULL;
-  const size_t need = qlora_linear_fwd_workspace(M, K, N, r);
+  const size_t need = qlora_linear_fwd_dropout_workspace(M, K, N, r);
   if (need == 0) return QL_ERR_SHAPE;
   drop::Params d;
   if (!drop_params(p, seed, offset, d)) return QL_ERR_VALUE;
@@ -192,13 +198,25 @@ int qlora_linear_fwd_dropout(const uint16_t* X, int64_t M, int64_t K, int64_t N,
   if (!aligned16(workspace)) return QL_ERR_ALIGN;
   uint16_t* T = T_out ? T_out : (uint16_t*)workspace;
   float* part = (float*)((char*)workspace + round_up((size_t)M * r * 2));
-  QL_TRY(launch_lora_down_drop(X, M, K, L1, r, d, T, nullptr, nullptr, part, (hipStream_t)stream));
-  // The decode kernel takes 16 rows; up to three passes of it over the packed weight stay
-  // below the 256-row tiles of the large kernel (48 rows: 4096 -> 11008 41 and 80 us,
-  // 11008 -> 4096 47 and 204 us, 8192 -> 22016 115 and 152 us, 512 -> 512 11 and 19 us).
-  if (fwd_small_ok(M, N)) {
-    QL_TRY(launch_fwd_small(X, M, K, N, codes, c2, c1, T, L2, r, lora_scale, Y, (hipStream_t)stream));
-    return QL_OK;
+  hipStream_t s = (hipStream_t)stream;
+  if (few_ok(M, K, N, r)) {
+    int S = 0;
+    QL_TRY(launch_small_slices(X, M, K, L1, true, r, d, d.scale, part, &S, s));
+    if (fwd_small_ok(M, N)) {
+      QL_TRY(launch_fwd_small(X, M, K, N, codes, c2, c1, nullptr, part, S, T_out, L2, r, lora_scale, Y, s));
+      return QL_OK;
+    }
+    if (M <= 16 && r % 4 == 0) {
+      QL_TRY(launch_qgemv_fwd_tpart(X, M, K, N, codes, c2, c1, part, S, T_out, L2, r, lora_scale, Y, s));
+      return QL_OK;
+    }
+    QL_TRY(launch_skinny_reduce(part, S, M * r, 1.0f, T, s));
+  } else {
+    QL_TRY(launch_lora_down_drop(X, M, K, L1, r, d, T, nullptr, nullptr, part, s));
+    if (fwd_small_ok(M, N)) {
+      QL_TRY(launch_fwd_small(X, M, K, N, codes, c2, c1, T, nullptr, 0, nullptr, L2, r, lora_scale, Y, s));
+      return QL_OK;
+    }
   }
   return qlora_linear_fwd_t(X, M, K, N, codes, c2, c1, T, L2, r, lora_scale, Y, stream);
 }
@@ -225,18 +243,33 @@ int qlora_linear_bwd_dropout(const uint16_t* X, const uint16_t* dY, int64_t M, i
   const GPlanes G{(uint16_t*)low, (uint16_t*)(w.dense ? low + w.low : low)};
   uint16_t* Tw = (uint16_t*)(low + w.low + w.dense);
   float* part = (float*)((uint8_t*)Tw + w.t);
+  const bool few = d.cut != 0 && few_ok(M, K, N, r);
+  int S = 0;
   if (!T) {
-    QL_TRY(launch_lora_down_drop(X, M, K, L1, r, d, Tw, nullptr, nullptr, part, s));
+    if (few) {
+      QL_TRY(launch_small_slices(X, M, K, L1, true, r, d, d.scale, part, &S, s));
+      QL_TRY(launch_skinny_reduce(part, S, M * r, 1.0f, Tw, s));
+    } else {
+      QL_TRY(launch_lora_down_drop(X, M, K, L1, r, d, Tw, nullptr, nullptr, part, s));
+    }
     T = Tw;
   }
-  QL_TRY(launch_lora_grad_in3(dY, M, N, L2, r, lora_scale, G, nullptr, nullptr, part, s));
-  if (dX) {
-    if (d.cut && dx_small_ok(M, K))
-      QL_TRY(launch_dx_small(dY, M, K, N, codes, c2, c1, G.dense, L1, r, dX, d, s));
-    else if (qgemm_big_ok(true, M, K, N))
-      QL_TRY(launch_qgemm_big(true, dY, M, K, N, codes, c2, c1, G.dense, L1, r, 1.0f, dX, s, 1, &d));
+  if (few) {
+    QL_TRY(launch_small_slices(dY, M, N, L2, false, r, d, lora_scale, part, &S, s));
+    if (dX)
+      QL_TRY(launch_dx_small(dY, M, K, N, codes, c2, c1, nullptr, part, S, G.planes, L1, r, dX, d, s));
     else
-      QL_TRY(launch_qgemm_dx(dY, M, K, N, codes, c2, c1, G.dense, L1, r, dX, s, &d));
+      QL_TRY(launch_skinny_reduce3(part, S, M, r, 1.0f, G, s));
+  } else {
+    QL_TRY(launch_lora_grad_in3(dY, M, N, L2, r, lora_scale, G, nullptr, nullptr, part, s));
+    if (dX) {
+      if (d.cut && dx_small_ok(M, K))
+        QL_TRY(launch_dx_small(dY, M, K, N, codes, c2, c1, G.dense, nullptr, 0, nullptr, L1, r, dX, d, s));
+      else if (qgemm_big_ok(true, M, K, N))
+        QL_TRY(launch_qgemm_big(true, dY, M, K, N, codes, c2, c1, G.dense, L1, r, 1.0f, dX, s, 1, &d));
+      else
+        QL_TRY(launch_qgemm_dx(dY, M, K, N, codes, c2, c1, G.dense, L1, r, dX, s, &d));
+    }
   }
   QL_TRY(launch_lora_grads3(X, K, G.planes, d, dL1, dY, N, T, lora_scale, dL2, M, r, part, s));
   return QL_OK;

@@ -34,12 +34,33 @@ __device__ __forceinline__ bf16x8 load8(__amdgpu_buffer_rsrc_t rs, uint32_t at, 
   return __builtin_bit_cast(bf16x8, u32x4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16});
 }
 
-// kVec: N % 8 == 0 (rows of dY in whole 16-byte pieces); kVecR: r % 8 == 0.
-template <bool kVec, bool kVecR, bool kDrop>
+// Elements c .. c + 7 of row m of T or G from its S <= kSlices fp32 slices [M][r], added in order.
+constexpr int kSlices = 8;
+__device__ __forceinline__ void sum8(__amdgpu_buffer_rsrc_t rp, int S, int M, int r, int m, int c, float (&sum)[8]) {
+  const uint32_t at = 4u * (uint32_t)(m * r + c);
+#pragma unroll
+  for (int k = 0; k < 8; k += 4) {
+    u32x4 v[kSlices];                    // slices past the last read as zeros
+#pragma unroll
+    for (int n = 0; n < kSlices; ++n)
+      v[n] = __builtin_amdgcn_raw_buffer_load_b128(rp, n < S && m < M && c < r ? at + 4u * k : kOOB, 4 * n * M * r, 0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float u = __uint_as_float(v[0][j]);
+#pragma unroll
+      for (int n = 1; n < kSlices; ++n) u += __uint_as_float(v[n][j]);
+      sum[k + j] = c + k + j < r ? u : 0.0f;
+    }
+  }
+}
+
+// kVec: N % 8 == 0 (rows of dY in whole 16-byte pieces); kVecR: r % 8 == 0; kSum: G as slices.
+template <bool kVec, bool kVecR, bool kSum>
 __global__ __launch_bounds__(64 * kW) void k_dx_small(const uint16_t* __restrict__ dY, int M, int K, int N,
                                                       const uint8_t* __restrict__ codes,
                                                       const uint8_t* __restrict__ c2, const float* __restrict__ c1,
-                                                      const uint16_t* __restrict__ G, const uint16_t* __restrict__ L1,
+                                                      const uint16_t* __restrict__ G, const float* __restrict__ Gp, int S,
+                                                      uint16_t* __restrict__ planes, const uint16_t* __restrict__ L1,
                                                       int r, uint16_t* __restrict__ dX, Nf4Params q, drop::Params d) {
   __shared__ __attribute__((aligned(16))) uint16_t wt[kW][kN * kPitch];
   __shared__ f32x16 red[kW][2][64];
@@ -94,22 +115,43 @@ __global__ __launch_bounds__(64 * kW) void k_dx_small(const uint16_t* __restrict
   uint32_t keep = 0;
   const int p = p0 + 32 * w;
   if (w < 2) {
-    const __amdgpu_buffer_rsrc_t rg = rsrc(G, (uint64_t)M * r * 2), rl = rsrc(L1, (uint64_t)K * r * 2);
+    const __amdgpu_buffer_rsrc_t rg = rsrc(kSum ? (const void*)Gp : G, (uint64_t)M * r * (kSum ? 4 * S : 2)),
+                                 rl = rsrc(L1, (uint64_t)K * r * 2);
+    const int pitch = (r + 7) / 8 * 8;
+    const int64_t plane = (int64_t)M * pitch;
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       const int c = 16 * s + 8 * h;
+      if (16 * s >= r) break;                      // uniform
       const bf16x8 a = load8<kVecR>(rl, (uint32_t)((p + x) * r + c) * 2u, r - c);
-      const bf16x8 b = load8<kVecR>(rg, (uint32_t)(m * r + c) * 2u, m < M ? r - c : 0);
+      bf16x8 b;
+      if constexpr (kSum) {
+        float sum[8];
+        sum8(rg, S, M, r, m, c, sum);
+        u32x4 v[3];                                // the planes: each what those before it rounded off
+#pragma unroll
+        for (int n = 0; n < 3; ++n)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            v[n][k] = qk::pack_bf16x2(sum[2 * k], sum[2 * k + 1]);
+            sum[2 * k] -= __uint_as_float(v[n][k] << 16);
+            sum[2 * k + 1] -= __uint_as_float(v[n][k] & 0xFFFF0000u);
+          }
+        b = __builtin_bit_cast(bf16x8, v[0]);
+        if (blockIdx.x == 0 && w == 0 && m < M && c < pitch)
+#pragma unroll
+          for (int n = 0; n < 3; ++n) *(u32x4*)(planes + n * plane + (int64_t)m * pitch + c) = v[n];
+      } else {
+        b = load8<kVecR>(rg, (uint32_t)(m * r + c) * 2u, m < M ? r - c : 0);
+      }
       low = qk::mfma32(a, b, low);
     }
-    if constexpr (kDrop) {
-      // half h draws octets 2 h and 2 h + 1 of its row; each lane takes its own columns 8 g + 4 h + e from both halves'
-      uint32_t mine = 0;
+    // half h draws octets 2 h and 2 h + 1 of its row; each lane takes its own columns 8 g + 4 h + e from both halves'
+    uint32_t mine = 0;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) mine |= drop::bits8(d, (uint32_t)m, (uint32_t)(p >> 3) + 2 * h + i) << (16 * h + 8 * i);
-      const u32x2 both = __builtin_amdgcn_permlane32_swap(mine, mine, false, false);
-      keep = (both[0] | both[1]) >> (4 * h);
-    }
+    for (int i = 0; i < 2; ++i) mine |= drop::bits8(d, (uint32_t)m, (uint32_t)(p >> 3) + 2 * h + i) << (16 * h + 8 * i);
+    const u32x2 both = __builtin_amdgcn_permlane32_swap(mine, mine, false, false);
+    keep = (both[0] | both[1]) >> (4 * h);
   }
   __syncthreads();
   if (w >= 2 || m >= M) return;
@@ -122,8 +164,7 @@ __global__ __launch_bounds__(64 * kW) void k_dx_small(const uint16_t* __restrict
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       o[e] = low[4 * g + e];
-      if constexpr (kDrop) o[e] = (keep >> (8 * g + e)) & 1u ? d.scale * o[e] : 0.0f;
-      o[e] += sum[4 * g + e];
+      o[e] = sum[4 * g + e] + ((keep >> (8 * g + e)) & 1u ? d.scale * o[e] : 0.0f);
     }
     *(u32x2*)(dX + (int64_t)m * K + p + 8 * g + 4 * h) = u32x2{qk::pack_bf16x2(o[0], o[1]), qk::pack_bf16x2(o[2], o[3])};
   }
@@ -133,13 +174,15 @@ __global__ __launch_bounds__(64 * kW) void k_dx_small(const uint16_t* __restrict
 // 32 kJ rows of W; eight waves split the reduction, a block of 64 at a time.  The halves
 // of a wave take the halves of a block, in both operands: the codes that a lane needs are
 // 16 consecutive bytes, rebuilt in registers as the matrix operand, with no LDS but for
-// the waves' sums, which meet there in order.
-template <bool kVecR, int kI, int kJ>
+// the waves' sums, which meet there in order.  kSum: T as slices.
+template <bool kVecR, int kI, int kJ, bool kSum>
 __global__ __launch_bounds__(64 * kW) void k_fwd_small(const uint16_t* __restrict__ X, int M, int K, int N,
                                                        const uint8_t* __restrict__ codes,
                                                        const uint8_t* __restrict__ c2, const float* __restrict__ c1,
-                                                       const uint16_t* __restrict__ T, const uint16_t* __restrict__ L2,
-                                                       int r, float scale, uint16_t* __restrict__ Y, Nf4Params q) {
+                                                       const uint16_t* __restrict__ T, const float* __restrict__ Tp,
+                                                       int S, uint16_t* __restrict__ T_out,
+                                                       const uint16_t* __restrict__ L2, int r, float scale,
+                                                       uint16_t* __restrict__ Y, Nf4Params q) {
   __shared__ f32x16 red[kW][kI * kJ][64];
   const int w = threadIdx.x >> 6, l = threadIdx.x & 63, h = l >> 5, x = l & 31;
   const int n0 = 32 * kJ * (int)blockIdx.x, m0 = 32 * kI * (int)blockIdx.y;
@@ -199,16 +242,29 @@ __global__ __launch_bounds__(64 * kW) void k_fwd_small(const uint16_t* __restric
   const int p = n0 + 32 * (w % kJ), m = m0 + 32 * (w / kJ) + x;
   f32x16 low = {};
   if (w < kI * kJ) {
-    const __amdgpu_buffer_rsrc_t rt = rsrc(T, (uint64_t)M * r * 2), rl = rsrc(L2, (uint64_t)N * r * 2);
+    const __amdgpu_buffer_rsrc_t rt = rsrc(kSum ? (const void*)Tp : T, (uint64_t)M * r * (kSum ? 4 * S : 2)),
+                                 rl = rsrc(L2, (uint64_t)N * r * 2);
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       const int c = 16 * s + 8 * h;
+      if (16 * s >= r) break;                      // uniform
       uint32_t e[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k)
         e[k] = __builtin_amdgcn_raw_buffer_load_b16(rl, c + k < r && p + x < N ? (uint32_t)((c + k) * N + p + x) * 2u : kOOB, 0, 0);
       const u32x4 a = {e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
-      const bf16x8 b = load8<kVecR>(rt, (uint32_t)(m * r + c) * 2u, m < M ? r - c : 0);
+      bf16x8 b;
+      if constexpr (kSum) {
+        float sum[8];
+        sum8(rt, S, M, r, m, c, sum);
+        u32x4 v;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = qk::pack_bf16x2(sum[2 * k], sum[2 * k + 1]);
+        b = __builtin_bit_cast(bf16x8, v);
+        if (T_out && n0 == 0 && w % kJ == 0 && m < M && c < r) qk::store8_row(T_out + (int64_t)m * r + c, v, min(8, r - c));
+      } else {
+        b = load8<kVecR>(rt, (uint32_t)(m * r + c) * 2u, m < M ? r - c : 0);
+      }
       low = qk::mfma32(__builtin_bit_cast(bf16x8, a), b, low);
     }
   }
@@ -250,16 +306,24 @@ bool fwd_small_ok(int64_t M, int64_t N) {
 // tiles are as large as fills the chip: 64 rows 4096 -> 4096 25, 29 and 38 us with 32 x 32,
 // 32 x 64 and 64 x 64 tiles, 128 rows 37, 30 and 39, 256 rows 62, 48 and 41.
 hipError_t launch_fwd_small(const uint16_t* X, int64_t M, int64_t K, int64_t N, const uint8_t* codes, const uint8_t* c2,
-                            const float* c1, const uint16_t* T, const uint16_t* L2, int r, float scale, uint16_t* Y,
-                            hipStream_t s) {
+                            const float* c1, const uint16_t* T, const float* Tp, int S, uint16_t* T_out,
+                            const uint16_t* L2, int r, float scale, uint16_t* Y, hipStream_t s) {
   const int64_t rows = (M + 31) / 32;
-#define QL_FW(I, J)                                                                                                  \
-  hipLaunchKernelGGL((r % 8 == 0 ? k_fwd_small<true, I, J> : k_fwd_small<false, I, J>),                              \
+#define QL_FW(V, I, J, A)                                                                                            \
+  hipLaunchKernelGGL((k_fwd_small<V, I, J, A>),                                                                      \
                      dim3((unsigned)((N + 32 * J - 1) / (32 * J)), (unsigned)((M + 32 * I - 1) / (32 * I))),         \
-                     dim3(64 * kW), 0, s, X, (int)M, (int)K, (int)N, codes, c2, c1, T, L2, r, scale, Y, nf4_params())
-  if ((N + 31) / 32 * rows <= 256) QL_FW(1, 1);
-  else if ((N + 63) / 64 * rows <= 256 || rows == 1) QL_FW(1, 2);
-  else QL_FW(2, 2);
+                     dim3(64 * kW), 0, s, X, (int)M, (int)K, (int)N, codes, c2, c1, T, Tp, S, T_out, L2, r, scale, Y, \
+                     nf4_params())
+#define QL_FWT(I, J)                          \
+  do {                                        \
+    if (!T) QL_FW(false, I, J, true);         \
+    else if (r % 8 == 0) QL_FW(true, I, J, false); \
+    else QL_FW(false, I, J, false);           \
+  } while (0)
+  if ((N + 31) / 32 * rows <= 256) QL_FWT(1, 1);
+  else if ((N + 63) / 64 * rows <= 256 || rows == 1) QL_FWT(1, 2);
+  else QL_FWT(2, 2);
+#undef QL_FWT
 #undef QL_FW
   return hipGetLastError();
 }
@@ -272,26 +336,23 @@ hipError_t launch_fwd_small(const uint16_t* X, int64_t M, int64_t K, int64_t N, 
 bool dx_small_ok(int64_t M, int64_t K) { return M <= 64 || (K / kP) * ((M + 31) / 32) <= 768; }
 
 hipError_t launch_dx_small(const uint16_t* dY, int64_t M, int64_t K, int64_t N, const uint8_t* codes, const uint8_t* c2,
-                           const float* c1, const uint16_t* G, const uint16_t* L1, int r, uint16_t* dX,
-                           const drop::Params& d, hipStream_t s) {
+                           const float* c1, const uint16_t* G, const float* Gp, int S, uint16_t* planes,
+                           const uint16_t* L1, int r, uint16_t* dX, const drop::Params& d, hipStream_t s) {
   const dim3 grid((unsigned)(K / kP), (unsigned)((M + 31) / 32));
-#define QL_DX(V, R, D)                                                                                                \
-  hipLaunchKernelGGL((k_dx_small<V, R, D>), grid, dim3(64 * kW), 0, s, dY, (int)M, (int)K, (int)N, codes, c2, c1, G, L1, r, \
-                     dX, nf4_params(), d)
-  const bool v = N % 8 == 0, vr = r % 8 == 0, dr = d.cut != 0;
-  if (v && vr) {
-    if (dr) QL_DX(true, true, true);
-    else QL_DX(true, true, false);
-  } else if (v) {
-    if (dr) QL_DX(true, false, true);
-    else QL_DX(true, false, false);
-  } else if (vr) {
-    if (dr) QL_DX(false, true, true);
-    else QL_DX(false, true, false);
-  } else {
-    if (dr) QL_DX(false, false, true);
-    else QL_DX(false, false, false);
-  }
+#define QL_DX(V, R, A)                                                                                                \
+  hipLaunchKernelGGL((k_dx_small<V, R, A>), grid, dim3(64 * kW), 0, s, dY, (int)M, (int)K, (int)N, codes, c2, c1, \
+                     G, Gp, S, planes, L1, r, dX, nf4_params(), d)
+#define QL_DXS(A)                          \
+  do {                                     \
+    if (v && vr) QL_DX(true, true, A);     \
+    else if (v) QL_DX(true, false, A);     \
+    else if (vr) QL_DX(false, true, A);    \
+    else QL_DX(false, false, A);           \
+  } while (0)
+  const bool v = N % 8 == 0, vr = r % 8 == 0;
+  if (G) QL_DXS(false);
+  else QL_DXS(true);
+#undef QL_DXS
 #undef QL_DX
   return hipGetLastError();
 }

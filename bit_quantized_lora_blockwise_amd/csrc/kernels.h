@@ -153,6 +153,10 @@ hipError_t launch_mx4_small_dx(const uint16_t* dY, int64_t M, int64_t K, int64_t
                                const uint16_t* L1, const uint16_t* L2, int r, float scale, const drop::Params& d,
                                uint16_t* dX, uint16_t* G, uint8_t* ac, uint8_t* as, float* part, hipStream_t s);
 // The forward's T and the backward's G alone (same bits).
+// fp32 slices (part: mx4_small_ws bytes) of scale (D o A) B (L1, b_is_kr) or scale A B^T (L2), to be
+// added in order.
+hipError_t launch_small_slices(const uint16_t* A, int64_t M, int64_t R, const uint16_t* B, bool b_is_kr, int r,
+                               const drop::Params& d, float scale, float* part, int* slices, hipStream_t s);
 hipError_t launch_mx4_small_t(const uint16_t* X, int64_t M, int64_t K, const uint16_t* L1, int r, const drop::Params& d,
                               uint16_t* T, float* part, hipStream_t s);
 hipError_t launch_mx4_small_g(const uint16_t* dY, int64_t M, int64_t N, const uint16_t* L2, int r, float scale,
@@ -227,10 +231,12 @@ hipError_t launch_qgemm_dx(const uint16_t* dY, int64_t M, int64_t K, int64_t N, 
                            uint16_t* dX, hipStream_t s, const drop::Params* d = nullptr);
 // The same with dropout for few rows (gemm_small.hip): dX = bf16(dY W' + D o (G L1^T))
 bool fwd_small_ok(int64_t M, int64_t N);
+// T, or with T = nullptr its slices Tp (S of them), added here; T_out then receives it.
 hipError_t launch_fwd_small(const uint16_t* X, int64_t M, int64_t K, int64_t N, const uint8_t* codes, const uint8_t* c2,
-                            const float* c1, const uint16_t* T, const uint16_t* L2, int r, float scale, uint16_t* Y,
-                            hipStream_t s);
+                            const float* c1, const uint16_t* T, const float* Tp, int S, uint16_t* T_out,
+                            const uint16_t* L2, int r, float scale, uint16_t* Y, hipStream_t s);
 bool dx_small_ok(int64_t M, int64_t K);
+// G, or with G = nullptr its slices Gp (S of them), added here; `planes` then receives it to 24 bits.
 hipError_t launch_dx_small(const uint16_t* dY, int64_t M, int64_t K, int64_t N, const uint8_t* codes, const uint8_t* c2,
-                           const float* c1, const uint16_t* G, const uint16_t* L1, int r, uint16_t* dX,
-                           const drop::Params& d, hipStream_t s);
+                           const float* c1, const uint16_t* G, const float* Gp, int S, uint16_t* planes,
+                           const uint16_t* L1, int r, uint16_t* dX, const drop::Params& d, hipStream_t s);

@@ -69,7 +69,8 @@ template <bool kBkr, bool kVec, bool kDrop, bool kQuant>
 __global__ __launch_bounds__(kDThreads) void k_small_down(const uint16_t* __restrict__ A, int M, int R,
                                                           const uint16_t* __restrict__ Bm, int r, int blocks,
                                                           int per_slice, drop::Params d, uint32_t* __restrict__ codes,
-                                                          uint8_t* __restrict__ scales, float* __restrict__ part) {
+                                                          uint8_t* __restrict__ scales, float* __restrict__ part,
+                                                          float out_scale) {
   __shared__ f32x4 red[kDW * 64];
   const int w = threadIdx.x >> 6, l = threadIdx.x & 63, g = l >> 4, x = l & 15;
   const int m = 16 * (int)blockIdx.x + x, c = 16 * (int)blockIdx.z + x, slice = blockIdx.y;
@@ -114,7 +115,7 @@ __global__ __launch_bounds__(kDThreads) void k_small_down(const uint16_t* __rest
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int mm = 16 * (int)blockIdx.x + 4 * g + j;
-      if (mm < M && c < r) part[((int64_t)slice * M + mm) * r + c] = acc[j];
+      if (mm < M && c < r) part[((int64_t)slice * M + mm) * r + c] = out_scale * acc[j];
     }
   }
 }
@@ -313,13 +314,13 @@ hipError_t launch_product(const SmallArgs& a, hipStream_t s) {
 
 template <bool kBkr>
 hipError_t launch_down(const uint16_t* A, int64_t M, int64_t R, const uint16_t* Bm, int r, const drop::Params& d,
-                       uint8_t* codes, uint8_t* scales, float* part, int* slices, hipStream_t s) {
+                       uint8_t* codes, uint8_t* scales, float* part, int* slices, hipStream_t s, float out_scale = 1.0f) {
   const int blocks = (int)(padded(R) / kBlock), per = slice_blocks(M, blocks, r);
   *slices = (blocks + per - 1) / per;
   const dim3 grid((unsigned)((M + 15) / 16), (unsigned)*slices, (unsigned)((r + 15) / 16));
 #define QL_SD(V, D, Q)                                                                                              \
   hipLaunchKernelGGL((k_small_down<kBkr, V, D, Q>), grid, dim3(kDThreads), 0, s, A, (int)M, (int)R, Bm, r, blocks, per, \
-                     d, (uint32_t*)codes, scales, part)
+                     d, (uint32_t*)codes, scales, part, out_scale)
   const bool vec = (R % 8) == 0, drop = kBkr && d.cut != 0;
   if constexpr (kBkr) {
     if (drop) {
@@ -390,4 +391,10 @@ hipError_t launch_mx4_small_g(const uint16_t* dY, int64_t M, int64_t N, const ui
   hipError_t e = launch_down<false>(dY, M, N, L2, r, drop::Params{}, nullptr, nullptr, part, &S, s);
   if (e != hipSuccess) return e;
   return launch_skinny_reduce3(part, S, M, r, scale, GPlanes{G, nullptr}, s);
+}
+
+hipError_t launch_small_slices(const uint16_t* A, int64_t M, int64_t R, const uint16_t* B, bool b_is_kr, int r,
+                               const drop::Params& d, float scale, float* part, int* slices, hipStream_t s) {
+  return b_is_kr ? launch_down<true>(A, M, R, B, r, d, nullptr, nullptr, part, slices, s, scale)
+                 : launch_down<false>(A, M, R, B, r, drop::Params{}, nullptr, nullptr, part, slices, s, scale);
 }

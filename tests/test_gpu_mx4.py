@@ -464,3 +464,19 @@ def test_larger_than_the_last_level_cache(rows, cols, dtype):
     for s in parts:
         n = s.stop - s.start
         assert torch.equal(V[s], q.mx4_dequantize(codes[:, s].contiguous(), scales[:, s].contiguous(), n, cols))
+
+
+@pytest.mark.parametrize("M,K,N,r", [(5, 512, 136, 8), (16, 256, 72, 7), (33, 704, 71, 20), (64, 1024, 264, 64), (65, 512, 136, 12)])
+def test_nf4_layer_forms_t_and_g_again_alike(M, K, N, r):
+    """Without T the backward forms the forward's, and dX does not change the gradients."""
+    q = qlib()
+    d = layer_data(M, K, N, r)
+    codes, absmax = q.nf4_quantize(d["W"])
+    base = (codes, *q.nf4_double_quant(absmax))
+    kw = dict(p=0.2, seed=3, offset=4)
+    Y, T = q.qlora_linear_fwd_dropout(d["X"], *base, N, d["L1"], d["L2"], 1.5, T_out=True, **kw)
+    Y2, _ = q.qlora_linear_fwd_dropout(d["X"], *base, N, d["L1"], d["L2"], 1.5, **kw)
+    assert torch.equal(Y, Y2)
+    dX, dL1, dL2 = q.qlora_linear_bwd_dropout(d["X"], d["dY"], *base, d["L1"], d["L2"], 1.5, T=T, **kw)
+    none, dL1b, dL2b = q.qlora_linear_bwd_dropout(d["X"], d["dY"], *base, d["L1"], d["L2"], 1.5, dX=False, **kw)
+    assert none is None and torch.equal(dL1, dL1b) and torch.equal(dL2, dL2b)
