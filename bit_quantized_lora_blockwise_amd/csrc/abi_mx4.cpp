@@ -35,8 +35,13 @@ Ws fwd_ws(int64_t M, int64_t K, int r) {
   w.total = w.codes + w.scales + w.low + w.part;
   return w;
 }
-// Rows up to which the NF4 layer with dropout forms T and G as slices that its products add up.
-constexpr int64_t kFew = 64;
+// Whether the NF4 layer with dropout forms T and G as slices that its products add up (a launch
+// less each): while the rank-r product has few 16 x 16 tiles.  Whole forwards, us, slices / sums of
+// their own: 64 rows of rank 64 (16 tiles) 11008 -> 4096 42 / 46, 128 rows of rank 36 (24) 8576 -> 631
+// 32 / 36, 192 rows (36) 38 / 37, 128 rows of rank 64 (32) 11008 -> 4096 58 / 57, 256 rows (64) 91 / 80.
+bool few_ok(int64_t M, int64_t K, int64_t N, int r) {
+  return (M + 15) / 16 * ((r + 15) / 16) <= 24 && layer_ok(M, K, N, r);
+}
 
 // packed = false: the backward over another base, which multiplies the bf16 gradient
 Ws bwd_ws(int64_t M, int64_t K, int64_t N, int r, bool packed) {
@@ -44,7 +49,7 @@ Ws bwd_ws(int64_t M, int64_t K, int64_t N, int r, bool packed) {
        round_up((size_t)3 * M * g_pitch(r) * 2), r == g_pitch(r) ? 0 : round_up((size_t)M * r * 2),
        round_up((size_t)M * r * 2), 0, 0};
   w.part = round_up(std::max({lora_skinny_ws(M, N, r), lora_skinny_ws(M, K, r), lora_grads3_ws(M, K, N, r),
-                              mx4_small_ws(packed ? M : std::min(M, kFew), r)}));
+                              packed || few_ok(M, K, N, r) ? mx4_small_ws(M, r) : 0}));
   w.total = w.codes + w.scales + w.low + w.dense + w.t + w.part;
   return w;
 }
@@ -175,11 +180,9 @@ int mx4_linear_bwd(const uint16_t* X, const uint16_t* dY, int64_t M, int64_t K, 
 }
 
 // ---- dropout on the adapter of the NF4 layer ------------------------------------
-static bool few_ok(int64_t M, int64_t K, int64_t N, int r) { return M <= kFew && layer_ok(M, K, N, r); }
-
 size_t qlora_linear_fwd_dropout_workspace(int64_t M, int64_t K, int64_t N, int r) {
   const size_t plain = qlora_linear_fwd_workspace(M, K, N, r);
-  return plain == 0 ? 0 : std::max(plain, round_up((size_t)M * r * 2) + mx4_small_ws(std::min(M, kFew), r));
+  return plain == 0 ? 0 : std::max(plain, round_up((size_t)M * r * 2) + (few_ok(M, K, N, r) ? mx4_small_ws(M, r) : 0));
 }
 
 int qlora_linear_fwd_dropout(const uint16_t* X, int64_t M, int64_t K, int64_t N, const uint8_t* codes,
@@ -243,7 +246,7 @@ int qlora_linear_bwd_dropout(const uint16_t* X, const uint16_t* dY, int64_t M, i
   const GPlanes G{(uint16_t*)low, (uint16_t*)(w.dense ? low + w.low : low)};
   uint16_t* Tw = (uint16_t*)(low + w.low + w.dense);
   float* part = (float*)((uint8_t*)Tw + w.t);
-  const bool few = d.cut != 0 && few_ok(M, K, N, r);
+  const bool few = d.cut != 0 && few_ok(M, K, N, r), small = dx_small_ok(M, K);
   int S = 0;
   if (!T) {
     if (few) {
@@ -254,7 +257,7 @@ int qlora_linear_bwd_dropout(const uint16_t* X, const uint16_t* dY, int64_t M, i
     }
     T = Tw;
   }
-  if (few) {
+  if (few && small) {
     QL_TRY(launch_small_slices(dY, M, N, L2, false, r, d, lora_scale, part, &S, s));
     if (dX)
       QL_TRY(launch_dx_small(dY, M, K, N, codes, c2, c1, nullptr, part, S, G.planes, L1, r, dX, d, s));
@@ -263,7 +266,7 @@ int qlora_linear_bwd_dropout(const uint16_t* X, const uint16_t* dY, int64_t M, i
   } else {
     QL_TRY(launch_lora_grad_in3(dY, M, N, L2, r, lora_scale, G, nullptr, nullptr, part, s));
     if (dX) {
-      if (d.cut && dx_small_ok(M, K))
+      if (d.cut && small)
         QL_TRY(launch_dx_small(dY, M, K, N, codes, c2, c1, G.dense, nullptr, 0, nullptr, L1, r, dX, d, s));
       else if (qgemm_big_ok(true, M, K, N))
         QL_TRY(launch_qgemm_big(true, dY, M, K, N, codes, c2, c1, G.dense, L1, r, 1.0f, dX, s, 1, &d));

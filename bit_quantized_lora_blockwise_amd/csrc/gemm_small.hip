@@ -291,13 +291,13 @@ __global__ __launch_bounds__(64 * kW) void k_fwd_small(const uint16_t* __restric
 
 }  // namespace
 
-// More rows than the decode kernels take at once (and up to 48, three times as many, for any
-// N that L2's 32-bit offsets reach), up to 2.5 work groups of 64 x 64 a CU;
-// the large tiles walk the whole reduction in one work group, and leave CUs idle while they
-// are few.  Whole forwards with dropout, us, decode kernels in passes of 16 rows or large tiles / here: 32
-// rows 512 -> 512 14 / 13, 4096 -> 11008 38 / 30, 11008 -> 4096 45 / 44, 8192 -> 22016 92 /
-// 80; 128 rows 4096 -> 11008 95 / 69, 11008 -> 4096 222 / 58, 8576 -> 631 173 / 36; 512 rows 11008 ->
-// 4096 229 / 148; 256 rows 4096 -> 11008 (688 work groups) 98 / 100, 8192 -> 22016 (1376) 184 / 322.
+// More rows than the decode kernels take at once (up to 48, three times as many, for any N
+// that L2's 32-bit offsets reach), up to 2.5 work groups of 64 x 64 a CU: the large tiles walk
+// the whole reduction in one work group, and leave CUs idle while they are few.  Whole forwards
+// with dropout, us, decode kernels in passes of 16 rows or large tiles / here: 32 rows 512 -> 512 14 /
+// 7.5, 4096 -> 11008 38 / 26, 11008 -> 4096 45 / 38, 8192 -> 22016 92 / 80; 128 rows 4096 -> 11008 95 / 67,
+// 11008 -> 4096 222 / 57, 8576 -> 631 173 / 32; 512 rows 11008 -> 4096 229 / 146; 256 rows 4096 -> 11008
+// (688 work groups) 98 / 97, 8192 -> 22016 (1376) 184 / 322.
 bool fwd_small_ok(int64_t M, int64_t N) {
   return M > 16 && N < (int64_t(1) << 24) && (M <= 48 || (N + 63) / 64 * ((M + 63) / 64) <= 640);
 }
@@ -329,9 +329,9 @@ hipError_t launch_fwd_small(const uint16_t* X, int64_t M, int64_t K, int64_t N, 
 }
 
 // Up to 64 rows, or up to three work groups (32 rows, 64 columns of dX) a CU.  Whole backwards
-// with dropout, us, here / large tiles: 32 rows 4096 -> 11008 71 / 235, 11008 -> 4096 38 / 109,
-// 8192 -> 22016 144 / 438, 512 -> 512 18 / 41; 128 rows 11008 -> 4096 85 / 112 (688 work groups),
-// 8192 -> 22016 262 / 445 (512); 512 rows 4096 -> 4096 105 / 117 (1024); 256 rows 8192 -> 22016
+// with dropout, us, here / large tiles: 32 rows 4096 -> 11008 67 / 235, 11008 -> 4096 36 / 109,
+// 8192 -> 22016 139 / 438, 512 -> 512 13 / 41; 128 rows 11008 -> 4096 85 / 112 (688 work groups),
+// 8192 -> 22016 260 / 445 (512); 512 rows 4096 -> 4096 105 / 117 (1024); 256 rows 8192 -> 22016
 // 489 / 446 (1024), 11008 -> 4096 159 / 116 (1376).
 bool dx_small_ok(int64_t M, int64_t K) { return M <= 64 || (K / kP) * ((M + 31) / 32) <= 768; }
 

@@ -466,7 +466,7 @@ def test_larger_than_the_last_level_cache(rows, cols, dtype):
         assert torch.equal(V[s], q.mx4_dequantize(codes[:, s].contiguous(), scales[:, s].contiguous(), n, cols))
 
 
-@pytest.mark.parametrize("M,K,N,r", [(5, 512, 136, 8), (16, 256, 72, 7), (33, 704, 71, 20), (64, 1024, 264, 64), (65, 512, 136, 12)])
+@pytest.mark.parametrize("M,K,N,r", [(5, 512, 136, 8), (16, 256, 72, 7), (33, 704, 71, 20), (64, 1024, 264, 64), (65, 512, 136, 12), (200, 1088, 136, 16), (300, 8192, 80, 5)])
 def test_nf4_layer_forms_t_and_g_again_alike(M, K, N, r):
     """Without T the backward forms the forward's, and dX does not change the gradients."""
     q = qlib()
