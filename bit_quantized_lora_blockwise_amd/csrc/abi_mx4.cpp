@@ -129,7 +129,7 @@ int mx4_linear_fwd(const uint16_t* X, int64_t M, int64_t K, int64_t N, const uin
   uint8_t* as = ac + w.codes;
   uint16_t* T = T_out ? T_out : (uint16_t*)(as + w.scales);
   float* part = (float*)(as + w.scales + w.low);
-  if (mx4_small_ok(M, N)) {
+  if (mx4_small_ok(M, N, K, r)) {
     QL_TRY(launch_mx4_small_fwd(X, M, K, N, codes, scales, L1, L2, r, lora_scale, d, Y, T_out, ac, as, part, s));
     return QL_OK;
   }
@@ -161,9 +161,9 @@ int mx4_linear_bwd(const uint16_t* X, const uint16_t* dY, int64_t M, int64_t K, 
   const GPlanes G{(uint16_t*)low, (uint16_t*)(w.dense ? low + w.low : low)};
   uint16_t* Tw = (uint16_t*)(low + w.low + w.dense);
   float* part = (float*)((uint8_t*)Tw + w.t);
-  const bool small = mx4_small_ok(M, K);
+  const bool small = mx4_small_ok(M, K, N, r);
   if (!T) {
-    if (mx4_small_ok(M, N)) QL_TRY(launch_mx4_small_t(X, M, K, L1, r, d, Tw, part, s));
+    if (mx4_small_ok(M, N, K, r)) QL_TRY(launch_mx4_small_t(X, M, K, L1, r, d, Tw, part, s));
     else QL_TRY(launch_lora_down_drop(X, M, K, L1, r, d, Tw, nullptr, nullptr, part, s));
     T = Tw;
   }

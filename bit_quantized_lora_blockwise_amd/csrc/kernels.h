@@ -144,7 +144,7 @@ hipError_t launch_mx4_gemm(const uint8_t* ac, const uint8_t* as, int64_t M, cons
 // The layer for few rows (mx4_small.hip): one call quantises the activations (into ac,
 // as), forms T or G and multiplies.  part: mx4_small_ws bytes.  Forward: T_out may be
 // nullptr.  Backward: G receives the planes alone.
-bool mx4_small_ok(int64_t M, int64_t P);   // P: columns of the result
+bool mx4_small_ok(int64_t M, int64_t P, int64_t R, int r);   // P: columns of the result, R: of the operand
 size_t mx4_small_ws(int64_t M, int r);
 hipError_t launch_mx4_small_fwd(const uint16_t* X, int64_t M, int64_t K, int64_t N, const uint8_t* bc, const uint8_t* bs,
                                 const uint16_t* L1, const uint16_t* L2, int r, float scale, const drop::Params& d,

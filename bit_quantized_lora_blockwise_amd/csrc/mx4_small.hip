@@ -347,10 +347,16 @@ hipError_t launch_down(const uint16_t* A, int64_t M, int64_t R, const uint16_t* 
 
 }  // namespace
 
-// Few rows, or few enough outputs that tiles of 128 x 128 would leave most of the
-// chip idle.  Whole forward calls, r = 64, queued back to back: 128 rows at 4096 -> 11008
-// 30 us here and 30 us with tiles, 8192 -> 22016 79 and 59 us, 1000 -> 777 9 and 27 us.
-bool mx4_small_ok(int64_t M, int64_t P) { return M <= 64 || (M <= 512 && M * P <= (int64_t(1) << 20)); }
+// Few rows, or outputs that one round of work groups (64 rows, 32 columns, one a CU) covers; two
+// rounds while the reduction and the rank are short.  Whole calls with dropout, us, here / with
+// tiles of 128 x 128: one round: forward 128 rows 4096 -> 4096 rank 64 14 / 27, 11008 -> 4096 29 /
+// 46, 512 rows 1024 -> 1024 9 / 18, backward 128 rows 4096 -> 4096 28 / 35, 11008 dY columns 43 / 37;
+// two: forward 256 rows 4096 -> 4096 rank 16 18 / 26, rank 64 24 / 28, 11008 -> 4096 51 / 48, backward
+// rank 16 27 / 36, rank 64 42 / 38, 11008 dY columns 74 / 40; 512 rows 4096 -> 4096 rank 64 36 / 30, 72 / 49.
+bool mx4_small_ok(int64_t M, int64_t P, int64_t R, int r) {
+  const int64_t groups = (P + 31) / 32 * ((M + 63) / 64);
+  return M <= 64 || (M <= 512 && (groups <= 256 || (groups <= 512 && R * ((r + 15) / 16) <= 4096)));
+}
 
 size_t mx4_small_ws(int64_t M, int r) { return (size_t)kMaxSlices * M * r * sizeof(float); }
 
