@@ -352,10 +352,13 @@ hipError_t launch_down(const uint16_t* A, int64_t M, int64_t R, const uint16_t* 
 // tiles of 128 x 128: one round: forward 128 rows 4096 -> 4096 rank 64 14 / 27, 11008 -> 4096 29 /
 // 46, 512 rows 1024 -> 1024 9 / 18, backward 128 rows 4096 -> 4096 28 / 35, 11008 dY columns 43 / 37;
 // two: forward 256 rows 4096 -> 4096 rank 16 18 / 26, rank 64 24 / 28, 11008 -> 4096 51 / 48, backward
-// rank 16 27 / 36, rank 64 42 / 38, 11008 dY columns 74 / 40; 512 rows 4096 -> 4096 rank 64 36 / 30, 72 / 49.
+// rank 16 27 / 36, rank 64 42 / 38, 11008 dY columns 74 / 40; 512 rows 4096 -> 4096 rank 64 36 / 30,
+// 72 / 49.  Above 512 rows one round, up to a reduction of 8192: forward 4096 rows 4096 -> 64 23 /
+// 35, 2048 rows 512 -> 256 10 / 18, 11008 -> 64 60 / 59; backward 39 / 52, 29 / 35, 85 / 79.
 bool mx4_small_ok(int64_t M, int64_t P, int64_t R, int r) {
   const int64_t groups = (P + 31) / 32 * ((M + 63) / 64);
-  return M <= 64 || (M <= 512 && (groups <= 256 || (groups <= 512 && R * ((r + 15) / 16) <= 4096)));
+  return M <= 64 || (groups <= 256 && (M <= 512 || R <= 8192)) ||
+         (M <= 512 && groups <= 512 && R * ((r + 15) / 16) <= 4096);
 }
 
 size_t mx4_small_ws(int64_t M, int r) { return (size_t)kMaxSlices * M * r * sizeof(float); }

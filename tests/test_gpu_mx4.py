@@ -480,3 +480,10 @@ def test_nf4_layer_forms_t_and_g_again_alike(M, K, N, r):
     dX, dL1, dL2 = q.qlora_linear_bwd_dropout(d["X"], d["dY"], *base, d["L1"], d["L2"], 1.5, T=T, **kw)
     none, dL1b, dL2b = q.qlora_linear_bwd_dropout(d["X"], d["dY"], *base, d["L1"], d["L2"], 1.5, dX=False, **kw)
     assert none is None and torch.equal(dL1, dL1b) and torch.equal(dL2, dL2b)
+
+
+@pytest.mark.parametrize("M,K,N,r", [(700, 1100, 60, 20), (1030, 260, 200, 33), (2000, 70, 24, 64), (520, 9000, 40, 8)])
+@pytest.mark.parametrize("p", [0.0, 0.1])
+def test_narrow_layer(M, K, N, r, p):
+    """Many rows, few columns on one side or the other."""
+    test_layer(M, K, N, r, p)
