@@ -487,3 +487,69 @@ def test_nf4_layer_forms_t_and_g_again_alike(M, K, N, r):
 def test_narrow_layer(M, K, N, r, p):
     """Many rows, few columns on one side or the other."""
     test_layer(M, K, N, r, p)
+
+
+@pytest.mark.parametrize("M,K,N,r", [(4, 512, 136, 8), (40, 512, 72, 5), (200, 320, 264, 64), (700, 1024, 512, 16),
+                                     (600, 320, 2048, 20)])
+@pytest.mark.parametrize("layer", ["mx4", "nf4"])
+def test_dropped_places_hold_anything(layer, M, K, N, r):
+    """Infinities and NaN in places that the mask drops do not reach T or dL1; the same bits as with zeros there."""
+    q = qlib()
+    d = layer_data(M, K, N, r)
+    kw = dict(p=0.3, seed=11, offset=5)
+    kept = q.lora_dropout(torch.ones((M, K), dtype=torch.bfloat16, device=DEV), **kw) != 0
+    zero = torch.where(kept, d["X"], torch.zeros_like(d["X"]))
+    odd = torch.tensor([float("nan"), float("inf"), float("-inf")], dtype=torch.bfloat16, device=DEV)
+    junk = odd[torch.arange(M * K, device=DEV).reshape(M, K) % 3]
+    bad = torch.where(kept, d["X"], junk)
+    if layer == "mx4":
+        w, wt = q.mx4_quantize(d["W"]), q.mx4_quantize(d["W"], transpose=True)
+        fwd = lambda X: q.mx4_linear_fwd(X, *w, N, d["L1"], d["L2"], 1.5, T_out=True, **kw)
+        bwd = lambda X, T: q.mx4_linear_bwd(X, d["dY"], *wt, d["L1"], d["L2"], 1.5, T=T, **kw)
+    else:
+        codes, absmax = q.nf4_quantize(d["W"])
+        base = (codes, *q.nf4_double_quant(absmax))
+        fwd = lambda X: q.qlora_linear_fwd_dropout(X, *base, N, d["L1"], d["L2"], 1.5, T_out=True, **kw)
+        bwd = lambda X, T: q.qlora_linear_bwd_dropout(X, d["dY"], *base, d["L1"], d["L2"], 1.5, T=T, **kw)
+    T = fwd(zero)[1]
+    assert torch.isfinite(T.float()).all() and torch.equal(T, fwd(bad)[1])
+    for a, b in zip(bwd(zero, T), bwd(bad, T)):
+        assert torch.isfinite(a.float()).all() and torch.equal(a, b)
+    for a, b in zip(bwd(zero, None), bwd(bad, None)):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("layer,M,K,N", [("mx4", 700, 512, 1024), ("mx4", 2100, 1024, 8200), ("nf4", 8, 512, 328),
+                                         ("nf4", 40, 512, 320), ("nf4", 600, 512, 2048)])
+def test_graph_replays(layer, M, K, N):
+    """Forward, backward and dropout captured together: every replay equals the eager calls on the input it then has."""
+    q = qlib()
+    r = 16
+    d = layer_data(M, K, N, r)
+    kw = dict(p=0.1, seed=1, offset=2)
+    X = d["X"].clone()
+    if layer == "mx4":
+        w, wt = q.mx4_quantize(d["W"]), q.mx4_quantize(d["W"], transpose=True)
+    else:
+        codes, absmax = q.nf4_quantize(d["W"])
+        base = (codes, *q.nf4_double_quant(absmax))
+
+    def calls():
+        H = q.lora_dropout(X, **kw)
+        if layer == "mx4":
+            y, t = q.mx4_linear_fwd(H, *w, N, d["L1"], d["L2"], 1.5, T_out=True, **kw)
+            return y, t, *q.mx4_linear_bwd(H, d["dY"], *wt, d["L1"], d["L2"], 1.5, T=t, **kw)
+        y, t = q.qlora_linear_fwd_dropout(H, *base, N, d["L1"], d["L2"], 1.5, T_out=True, **kw)
+        return y, t, *q.qlora_linear_bwd_dropout(H, d["dY"], *base, d["L1"], d["L2"], 1.5, T=t, **kw)
+
+    calls()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = calls()
+    for i in range(3):
+        X.copy_(d["X"] * (i + 1))
+        g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, calls()):
+            assert torch.equal(a, b), i
