@@ -12,6 +12,7 @@
 
 #include "../../include/qlora.h"
 #include "kernels.h"
+#include "side_stream.h"
 
 namespace {
 
@@ -132,47 +133,9 @@ hipError_t run_dx_gemm(const uint16_t* dY, int64_t M, int64_t K, int64_t N, cons
 // whole rounds there is no idle round to fill and the products stay in order
 // on the caller's stream.  The kernels, their work split and the order of
 // every sum are the same on both paths, so the results are identical.
-struct SideStream {
-  hipStream_t s = nullptr;
-  hipEvent_t fork = nullptr, join = nullptr;
-  int cus = 0;
-  bool failed = false;
-};
-
-constexpr int kMaxDevices = 64;
-
-// The calling thread's second stream on the current device (default priority,
-// created on first use and kept until the process ends), or nullptr when it
-// cannot be had; the caller then keeps everything on its own stream.
-SideStream* side_stream() {
-  thread_local SideStream per_dev[kMaxDevices];
-  int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
-  SideStream& d = per_dev[dev];
-  if (d.failed) return nullptr;
-  if (!d.s) {
-    int cus = 0;
-    if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus < 8 ||
-        hipEventCreateWithFlags(&d.fork, hipEventDisableTiming) != hipSuccess ||
-        hipEventCreateWithFlags(&d.join, hipEventDisableTiming) != hipSuccess ||
-        hipStreamCreateWithFlags(&d.s, hipStreamNonBlocking) != hipSuccess) {
-      d.failed = true;
-      d.s = nullptr;
-      return nullptr;
-    }
-    d.cus = cus;
-  }
-  return &d;
-}
-
-// Joins the second stream back into the caller's stream s, also after a failed
-// launch `e` on it, so that what was enqueued there stays ordered before s's
-// later work; returns the first error.
-hipError_t join_side(SideStream& d, hipStream_t s, hipError_t e) {
-  hipError_t j = hipEventRecord(d.join, d.s);
-  if (j == hipSuccess) j = hipStreamWaitEvent(s, d.join, 0);
-  return e != hipSuccess ? e : j;
-}
+using qlabi::SideStream;
+using qlabi::join_side;
+using qlabi::side_stream;
 
 // True when the dX product [M, K] runs on the persistent grid and its last
 // round of tiles (256 x 256 each) is partly empty.

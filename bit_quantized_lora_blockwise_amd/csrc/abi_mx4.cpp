@@ -4,6 +4,7 @@
 
 #include "abi_util.h"
 #include "mx4.h"
+#include "side_stream.h"
 
 namespace {
 
@@ -265,6 +266,19 @@ int qlora_linear_bwd_dropout(const uint16_t* X, const uint16_t* dY, int64_t M, i
       QL_TRY(launch_skinny_reduce3(part, S, M, r, 1.0f, G, s));
   } else {
     QL_TRY(launch_lora_grad_in3(dY, M, N, L2, r, lora_scale, G, nullptr, nullptr, part, s));
+    SideStream* sd = dX && !(d.cut && small) && qgemm_big_ok(true, M, K, N) ? side_stream() : nullptr;
+    const int64_t tiles = (M + 255) / 256 * ((K + 255) / 256), grid = sd ? sd->cus / 8 * 8 : 1;
+    if (sd && tiles > grid && tiles % grid != 0) {
+      // As in qlora_linear_bwd: the gradients take the CUs that dX's last round leaves idle.  2048 rows
+      // 22016 -> 8192 698 us, 717 one after the other, 11008 -> 4096 253 and 267; 4096 rows of it 428 and 425.
+      // (The microscaled backward stays in order: 196 us against 189 at 4096 rows 11008 -> 4096.)
+      QL_TRY(hipEventRecord(sd->fork, s));
+      QL_TRY(launch_qgemm_big(true, dY, M, K, N, codes, c2, c1, G.dense, L1, r, 1.0f, dX, s, 1, &d));
+      QL_TRY(hipStreamWaitEvent(sd->s, sd->fork, 0));
+      const hipError_t e = launch_lora_grads3(X, K, G.planes, d, dL1, dY, N, T, lora_scale, dL2, M, r, part, sd->s);
+      QL_TRY(join_side(*sd, s, e));
+      return QL_OK;
+    }
     if (dX) {
       if (d.cut && small)
         QL_TRY(launch_dx_small(dY, M, K, N, codes, c2, c1, G.dense, nullptr, 0, nullptr, L1, r, dX, d, s));

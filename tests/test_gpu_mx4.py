@@ -519,8 +519,8 @@ def test_dropped_places_hold_anything(layer, M, K, N, r):
         assert torch.equal(a, b)
 
 
-@pytest.mark.parametrize("layer,M,K,N", [("mx4", 700, 512, 1024), ("mx4", 2100, 1024, 8200), ("nf4", 8, 512, 328),
-                                         ("nf4", 40, 512, 320), ("nf4", 600, 512, 2048)])
+@pytest.mark.parametrize("layer,M,K,N", [("mx4", 700, 512, 1024), ("mx4", 2100, 1024, 8200), ("mx4", 2100, 8200, 700), ("nf4", 8, 512, 328),
+                                         ("nf4", 40, 512, 320), ("nf4", 600, 512, 2048), ("nf4", 2100, 8256, 320)])
 def test_graph_replays(layer, M, K, N):
     """Forward, backward and dropout captured together: every replay equals the eager calls on the input it then has."""
     q = qlib()
