@@ -17,7 +17,8 @@ bool matrix_ok(int64_t rows, int64_t cols, int64_t ld) {
 }
 
 // Layer sizes: X, Y and their gradients, the packed activations and the packed
-// weight, the adapters, T and G below 2^31 bytes each (the kernels' offsets are 32-bit).
+// weight, the adapters, T and each plane of G below 2^31 bytes (the kernels' offsets are
+// 32-bit; G's three planes together may pass it).
 bool layer_ok(int64_t M, int64_t K, int64_t N, int r) {
   return M > 0 && K > 0 && N > 0 && M < kLim && K < kLim && N < kLim && r >= 1 && r <= 64 && M <= kLim / 2 / K &&
          M <= kLim / 2 / N && M < kLim / 2 / r && K < kLim / 2 / r && N < kLim / 2 / r && M * K * 2 < kLim &&

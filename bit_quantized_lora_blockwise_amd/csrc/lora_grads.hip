@@ -60,7 +60,11 @@ __device__ __forceinline__ void run(const Job& jb, int M, int r, int tile, int s
   const int wp = w & 3, wk = w >> 2;
   const int p0 = tile * kP, m_beg = slice * jb.rows, m_end = min(M, m_beg + jb.rows);
   const int steps = (m_end - m_beg + kM - 1) / kM;
-  const __amdgpu_buffer_rsrc_t ra = rsrc(jb.A, (uint64_t)M * jb.P * 2), rb = rsrc(jb.B, (uint64_t)kPlanes * M * r * 2);
+  const __amdgpu_buffer_rsrc_t ra = rsrc(jb.A, (uint64_t)M * jb.P * 2);
+  // a descriptor for each plane: one stays below 2^31 bytes, all three together need not
+  __amdgpu_buffer_rsrc_t rb[kPlanes];
+#pragma unroll
+  for (int j = 0; j < kPlanes; ++j) rb[j] = rsrc(jb.B + (int64_t)j * M * r, (uint64_t)M * r * 2);
   // thread t: rows t / 32 + 16 i, columns 8 (t % 32) of A; row t / 8, columns 8 (t % 8) of each plane
   const int arow = t >> 5, ac = t & 31, brow = t >> 3, bc = t & 7;
   struct Regs {
@@ -77,7 +81,7 @@ __device__ __forceinline__ void run(const Job& jb, int M, int r, int tile, int s
 #pragma unroll
     for (int j = 0; j < kPlanes; ++j)
       g.b[j] = __builtin_amdgcn_raw_buffer_load_b128(
-          rb, m + brow < m_end && 8 * bc < r ? (uint32_t)((j * M + m + brow) * r + 8 * bc) * 2u : kOOB, 0, 0);
+          rb[j], m + brow < m_end && 8 * bc < r ? (uint32_t)((m + brow) * r + 8 * bc) * 2u : kOOB, 0, 0);
   };
   auto store = [&](int st, Regs& g) {
     LDS_AS uint8_t* a = lds + (st & 1) * kStage;

@@ -1,0 +1,97 @@
+"""The layers at sizes where an operand, or a few of them together, pass 2^31 or 2^32 bytes: against float64 on the
+rows and columns that hold anything.  The other elements are zeros, which add exactly, so that a sum's bound counts
+its non-zero terms alone:
+  a sum of n exact products in fp32, in any order: (n + 4) 2^-24 sum |a b| (scaling and the slices' sum included);
+  a bf16 result v: 2^-8 |v| on top (half an ulp); G enters dX after its own bf16 rounding.
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+X4 = O.mx4
+U = 2.0 ** -24
+BF = torch.bfloat16
+
+
+def qlib():
+    import bit_quantized_lora_blockwise_amd as q
+    return q
+
+
+def f64(t):
+    return t.detach().float().cpu().numpy().astype(np.float64)
+
+
+def dev(a, dtype=BF):
+    return torch.from_numpy(np.ascontiguousarray(a, np.float32)).to(dtype).to(DEV)
+
+
+def within(got, ref, tol, name):
+    g = f64(got)
+    assert g.shape == ref.shape, (name, g.shape, ref.shape)
+    assert np.all(np.isfinite(g)), f"{name}: non-finite"
+    print(f"{name}: max err/tol {np.max(np.abs(g - ref) / np.maximum(tol, 1e-300)):.3f}", flush=True)
+    assert np.all(np.abs(g - ref) <= tol), f"{name}: worst {np.max(np.abs(g - ref) - tol):.3e} past the tolerance"
+
+
+def mask_at(rows, cols, p, seed, offset):
+    """D (0 or the scale) at rows x cols, both arrays of indices."""
+    m, k = np.meshgrid(np.asarray(rows, np.uint64), np.asarray(cols, np.uint64), indexing="ij")
+    w = X4.philox4x32([k // np.uint64(8), m, offset % 2**32, offset // 2**32], (seed % 2**32, seed // 2**32))
+    w = np.stack([np.broadcast_to(x, m.shape) for x in w], -1)
+    u = np.take_along_axis(w, ((k % np.uint64(8)) // np.uint64(2)).astype(np.int64)[..., None], -1)[..., 0]
+    u = np.where(k % np.uint64(2), u >> np.uint64(16), u & np.uint64(0xFFFF))
+    cut = X4.cut_of(p)
+    return np.where(u >= cut, 65536 / (65536 - cut), 0.0)
+
+
+def test_mask_at_is_the_oracles():
+    rows, cols = np.array([0, 3, 6]), np.array([1, 8, 30])
+    full = X4.dropped(np.ones((7, 31)), 0.3, 2**33 + 5, 2**34 + 7)
+    assert np.array_equal(mask_at(rows, cols, 0.3, 2**33 + 5, 2**34 + 7), full[np.ix_(rows, cols)])
+
+
+@pytest.mark.parametrize("layer", ["mx4", "nf4"])
+@pytest.mark.parametrize("p", [0.0, 0.1])
+def test_planes_of_g_past_2_32_bytes(layer, p):
+    """12 million rows of rank 64: G's three planes are 4.6 GB together.  Rows all along the matrices hold values."""
+    q = qlib()
+    M, K, N, r, s, seed, off = 12_000_000, 64, 64, 64, 2.0, 2**40 + 9, 3
+    rows = np.unique(np.linspace(0, M - 1, 200).astype(np.int64))
+    n = len(rows)
+    rng = np.random.default_rng(5)
+    print(f"[{layer} M={M} p={p}]", flush=True)
+    at = torch.from_numpy(rows).to(DEV)
+
+    def spread(a):
+        full = torch.zeros((M, a.shape[1]), dtype=BF, device=DEV)
+        full[at] = dev(a)
+        return full
+
+    X, dY, T = (spread(rng.standard_normal((n, c))) for c in (K, N, r))
+    L1, L2 = dev(rng.standard_normal((K, r)) * 0.1), dev(rng.standard_normal((r, N)) * 0.1)
+    W = dev(rng.standard_normal((N, K)) * 0.05)
+    kw = dict(p=p, seed=seed, offset=off)
+    if layer == "mx4":
+        dX, dL1, dL2 = q.mx4_linear_bwd(X, dY, *q.mx4_quantize(W, transpose=True), L1, L2, s, T=T, **kw)
+        Wt, dyv = X4.rounded(f64(W).T), X4.rounded(f64(dY[at]))
+    else:
+        codes, absmax = q.nf4_quantize(W)
+        base = (codes, *q.nf4_double_quant(absmax))
+        dX, dL1, dL2 = q.qlora_linear_bwd_dropout(X, dY, *base, L1, L2, s, T=T, **kw)
+        Wt, dyv = f64(q.nf4_dequantize(*base, N, K)).T, f64(dY[at])
+    x, dy, t, l1, l2 = (f64(v) for v in (X[at], dY[at], T[at], L1, L2))
+    D = mask_at(rows, np.arange(K), p, seed, off)
+    G = s * dy @ l2.T
+    errG = (N + 4) * U * s * (np.abs(dy) @ np.abs(l2).T)
+    within(dL1, (x * D).T @ G, (n + 4) * U * (np.abs(x * D).T @ np.abs(G)) + np.abs(x * D).T @ errG, "dL1")
+    within(dL2, s * t.T @ dy, (n + 4) * U * s * (np.abs(t).T @ np.abs(dy)), "dL2")
+    ref = dyv @ Wt.T + D * (G @ l1.T)
+    tol = 2.0**-8 * np.abs(ref) + (N + 4) * U * (np.abs(dyv) @ np.abs(Wt).T)
+    tol += D * (((2.0**-8 + 70 * U) * np.abs(G) + errG) @ np.abs(l1).T)
+    within(dX[at], ref, tol, "dX")
+    assert int((dX != 0).any(1).sum()) <= n
