@@ -115,15 +115,17 @@ __global__ __launch_bounds__(64 * kW) void k_dx_small(const uint16_t* __restrict
   uint32_t keep = 0;
   const int p = p0 + 32 * w;
   if (w < 2) {
+    // L1 from this wave's first column on: all of it may pass 2^31 bytes
+    const int64_t first = __builtin_amdgcn_readfirstlane(p);
     const __amdgpu_buffer_rsrc_t rg = rsrc(kSum ? (const void*)Gp : G, (uint64_t)M * r * (kSum ? 4 * S : 2)),
-                                 rl = rsrc(L1, (uint64_t)K * r * 2);
+                                 rl = rsrc(L1 + first * r, (uint64_t)32 * r * 2);
     const int pitch = (r + 7) / 8 * 8;
     const int64_t plane = (int64_t)M * pitch;
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       const int c = 16 * s + 8 * h;
       if (16 * s >= r) break;                      // uniform
-      const bf16x8 a = load8<kVecR>(rl, (uint32_t)((p + x) * r + c) * 2u, r - c);
+      const bf16x8 a = load8<kVecR>(rl, (uint32_t)(x * r + c) * 2u, r - c);
       bf16x8 b;
       if constexpr (kSum) {
         float sum[8];

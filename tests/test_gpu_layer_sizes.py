@@ -95,3 +95,32 @@ def test_planes_of_g_past_2_32_bytes(layer, p):
     tol += D * (((2.0**-8 + 70 * U) * np.abs(G) + errG) @ np.abs(l1).T)
     within(dX[at], ref, tol, "dX")
     assert int((dX != 0).any(1).sum()) <= n
+
+
+@pytest.mark.parametrize("p", [0.0, 0.1])
+def test_l1_of_2_32_bytes(p):
+    """17 rows of 2^25 columns over NF4: L1 is 4.3 GB.  dX and dL1 in blocks of columns all along the matrix."""
+    q = qlib()
+    M, K, N, r, s, seed, off = 17, 2**25, 8, 64, 1.5, 7, 2**33 + 1
+    rng = np.random.default_rng(6)
+    print(f"[nf4 M={M} K={K} p={p}]", flush=True)
+    X = torch.empty((M, K), dtype=BF, device=DEV).normal_()
+    L1 = torch.empty((K, r), dtype=BF, device=DEV).normal_()
+    W = torch.empty((N, K), dtype=BF, device=DEV).normal_(0, 0.05)
+    dY, T, L2 = (dev(rng.standard_normal(shape)) for shape in ((M, N), (M, r), (r, N)))
+    codes, absmax = q.nf4_quantize(W)
+    base = (codes, *q.nf4_double_quant(absmax))
+    Wq = q.nf4_dequantize(*base, N, K)
+    dX, dL1, _ = q.qlora_linear_bwd_dropout(X, dY, *base, L1, L2, s, p=p, seed=seed, offset=off, T=T)
+    dy, l2 = f64(dY), f64(L2)
+    G = s * dy @ l2.T
+    errG = (N + 4) * U * s * (np.abs(dy) @ np.abs(l2).T)
+    for k in (0, 2**22 - 32, 2**24 + 64, 2**24 + 2**23, K - 128):
+        c = slice(k, k + 128)
+        D = mask_at(np.arange(M), np.arange(k, k + 128), p, seed, off)
+        x, l1, w = f64(X[:, c]), f64(L1[c]), f64(Wq[:, c])
+        ref = dy @ w + D * (G @ l1.T)
+        tol = 2.0**-8 * np.abs(ref) + (N + 4) * U * (np.abs(dy) @ np.abs(w))
+        tol += D * (((2.0**-8 + 70 * U) * np.abs(G) + errG) @ np.abs(l1).T)
+        within(dX[:, c], ref, tol, f"dX {k}")
+        within(dL1[c], (x * D).T @ G, (M + 4) * U * (np.abs(x * D).T @ np.abs(G)) + np.abs(x * D).T @ errG, f"dL1 {k}")
