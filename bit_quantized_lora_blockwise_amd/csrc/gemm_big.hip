@@ -413,7 +413,7 @@ __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict_
         for (int i = 0; i < 8; ++i) {
           const int idx = tp + 256 * i, row = idx >> 3, cc = (idx & 7) * 8;
           u32x4 v8 = {0, 0, 0, 0};
-          if (p0 + row < K) v8 = load_row8(lb_src + (p0 + row) * r, cc, r);
+          if (p0 + row < K) v8 = load_row8(lb_src + (int64_t)(p0 + row) * r, cc, r);
           *(LDS_AS u32x4*)(lb + row * kPL + cc) = v8;
         }
       }
@@ -575,7 +575,9 @@ __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict_
   // ---- store C (bf16), lane layout of the 32x32 accumulators, through a
   // buffer descriptor based at this wave's first output element whose size
   // ends with the last row of C (rows past M are dropped by the hardware);
-  // lane offsets are 32-bit (M P < 2^30), the (i, j) part a scalar offset.
+  // lane offsets are 32-bit, the (i, j) part a scalar offset.  Eight rows that
+  // all lie past M are skipped, which keeps every offset below 2^32: M P < 2^30,
+  // and seven rows more with P <= 2^27.
   {
     const int Pi = (int)P;
     const int rows_left = (int)M - (m0 + 64 * rg);
@@ -591,9 +593,13 @@ __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict_
       for (int j = 0; j < 4; ++j) {
         if (32 * j < prem) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int so = ((32 * i + 8 * (e >> 2) + (e & 3)) * Pi + 32 * j) * 2;
-            __builtin_amdgcn_raw_buffer_store_b16(qk::f32_to_bf16(acc[i][j][e]), rc_out, lane_b, so, 0);
+          for (int g = 0; g < 4; ++g) {
+            if (32 * i + 8 * g >= rows_left) break;   // uniform
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t so = ((uint32_t)(32 * i + 8 * g + e) * (uint32_t)Pi + 32 * j) * 2;
+              __builtin_amdgcn_raw_buffer_store_b16(qk::f32_to_bf16(acc[i][j][4 * g + e]), rc_out, lane_b, (int)so, 0);
+            }
           }
         }
       }

@@ -98,10 +98,12 @@ def test_planes_of_g_past_2_32_bytes(layer, p):
 
 
 @pytest.mark.parametrize("p", [0.0, 0.1])
-def test_l1_of_2_32_bytes(p):
-    """17 rows of 2^25 columns over NF4: L1 is 4.3 GB.  dX and dL1 in blocks of columns all along the matrix."""
+@pytest.mark.parametrize("K", [2**25, 2**25 + 2**22])
+def test_l1_of_2_32_bytes(K, p):
+    """17 rows of 2^25 columns and more over NF4: L1 is 4.3 GB, and past 2^31 elements.  dX and dL1 in blocks of columns
+    all along the matrix."""
     q = qlib()
-    M, K, N, r, s, seed, off = 17, 2**25, 8, 64, 1.5, 7, 2**33 + 1
+    M, N, r, s, seed, off = 17, 8, 64, 1.5, 7, 2**33 + 1
     rng = np.random.default_rng(6)
     print(f"[nf4 M={M} K={K} p={p}]", flush=True)
     X = torch.empty((M, K), dtype=BF, device=DEV).normal_()
@@ -124,3 +126,21 @@ def test_l1_of_2_32_bytes(p):
         tol += D * (((2.0**-8 + 70 * U) * np.abs(G) + errG) @ np.abs(l1).T)
         within(dX[:, c], ref, tol, f"dX {k}")
         within(dL1[c], (x * D).T @ G, (M + 4) * U * (np.abs(x * D).T @ np.abs(G)) + np.abs(x * D).T @ errG, f"dL1 {k}")
+
+
+def test_bf16_base_dx_of_2_27_columns():
+    """The widest dX over a bf16 base, 7 rows of nearly 2^27 columns: rows past the end of a tile of 256 stay unwritten."""
+    q = qlib()
+    M, K, N, r, s = 7, 2**27 - 64, 8, 8, 1.0
+    rng = np.random.default_rng(7)
+    W = torch.empty((N, K), dtype=BF, device=DEV).normal_(0, 0.05)
+    L1 = torch.empty((K, r), dtype=BF, device=DEV).normal_()
+    dY, G = dev(rng.standard_normal((M, N))), dev(rng.standard_normal((M, r)))
+    dX = q.lora_linear_dx(dY, W, G, L1)
+    dy, g = f64(dY), f64(G)
+    for k in (0, 2**24, 2**26 - 64, 2**26 + 2**25, K - 128):
+        c = slice(k, k + 128)
+        l1, w = f64(L1[c]), f64(W[:, c])
+        ref = dy @ w + g @ l1.T
+        tol = 2.0**-8 * np.abs(ref) + (N + 4) * U * (np.abs(dy) @ np.abs(w)) + (r + 4) * U * (np.abs(g) @ np.abs(l1).T)
+        within(dX[:, c], ref, tol, f"dX {k}")
