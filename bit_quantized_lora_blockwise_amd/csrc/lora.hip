@@ -41,8 +41,9 @@ struct Tile {
 };
 
 // How a tile is read: in aligned 16-byte pieces (ld and cols multiples of 8, base 16-byte
-// aligned), in pieces at any element (rows of at least eight), or element by element.
-enum Load { kPieces, kAnywhere, kElements };
+// aligned), in pieces at any element (rows of at least eight), element by element, or
+// that by 64-bit address (matrices past the 2^31 bytes that a buffer offset reaches).
+enum Load { kPieces, kAnywhere, kElements, kFar };
 
 // Tile of a matrix with `ld` elements per row, its first row at `base`, its first column
 // c0; rows at or past `rows` and columns at or past `cols` read as zero.  Each thread
@@ -60,7 +61,12 @@ __device__ __forceinline__ Tile load_tile(const uint16_t* base, int64_t c0, int6
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int row = (t >> 3) + 32 * i;
-    if constexpr (kHow != kElements) {
+    if constexpr (kHow == kFar) {
+      uint32_t e[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) e[j] = row < rows && cc + j < cols ? base[row * ld + cc + j] : 0;
+      tl.v[i] = u32x4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
+    } else if constexpr (kHow != kElements) {
       const int64_t at = row * ld + (kHow == kPieces ? cc : min(cc, cols - 8));
       tl.v[i] = __builtin_amdgcn_raw_buffer_load_b128(rs, row < rows && cc < cols ? (uint32_t)(at * 2) : kOOB, 0, 0);
     } else {
@@ -728,6 +734,9 @@ static bool skinny_stream_ok(const uint16_t* A, int64_t M, int64_t R, int64_t ld
          ((uintptr_t)B & 15) == 0 && M * lda * 2 < (int64_t(1) << 31) && R * r * 2 < (int64_t(1) << 31);
 }
 
+// L2 [r, R] that buffer offsets do not reach: read by 64-bit address.
+static bool past_2_31(int r, int64_t R) { return R * r * 2 >= (int64_t(1) << 31); }
+
 size_t lora_skinny_ws(int64_t M, int64_t R, int r) {
   const int64_t tiles = (M + kTile - 1) / kTile;
   int64_t splits = std::max<int64_t>(plan_rowsplit(tiles, R).splits, plan_stream(tiles, R).splits);
@@ -776,7 +785,8 @@ hipError_t launch_lora_skinny(const uint16_t* A, int64_t M, int64_t R, int64_t l
     else if (bvec) QL_SKINNY(true, kAnywhere, kPieces);
     else QL_SKINNY(true, kAnywhere, kAnywhere);
   } else {
-    if (avec && bvec) QL_SKINNY(false, kPieces, kPieces);
+    if (past_2_31(r, R)) QL_SKINNY(false, kAnywhere, kFar);
+    else if (avec && bvec) QL_SKINNY(false, kPieces, kPieces);
     else if (few) QL_SKINNY(false, kElements, kElements);
     else if (avec) QL_SKINNY(false, kPieces, kAnywhere);
     else if (bvec) QL_SKINNY(false, kAnywhere, kPieces);
@@ -904,7 +914,8 @@ static hipError_t low_pass(const uint16_t* A, int64_t M, int64_t R, const uint16
 #define QL_LOW(BKR, VA, VB, D)                                                                                     \
   hipLaunchKernelGGL((k_lora_skinny<BKR, VA, VB, D>), grid, dim3(kThreads), 0, s, A, M, R, R, B, r, sp.chunk, ws, d)
   if (!b_is_kr) {
-    if (vec) QL_LOW(false, kPieces, kPieces, false);
+    if (past_2_31(r, R)) QL_LOW(false, kAnywhere, kFar, false);
+    else if (vec) QL_LOW(false, kPieces, kPieces, false);
     else if (R < 8) QL_LOW(false, kElements, kElements, false);
     else QL_LOW(false, kAnywhere, kAnywhere, false);
   } else if (d.cut) {

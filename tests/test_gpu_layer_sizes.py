@@ -144,3 +144,40 @@ def test_bf16_base_dx_of_2_27_columns():
         ref = dy @ w + g @ l1.T
         tol = 2.0**-8 * np.abs(ref) + (N + 4) * U * (np.abs(dy) @ np.abs(w)) + (r + 4) * U * (np.abs(g) @ np.abs(l1).T)
         within(dX[:, c], ref, tol, f"dX {k}")
+
+
+@pytest.mark.parametrize("N", [2**25 + 5, 2**25 + 8])
+@pytest.mark.parametrize("call", ["grad_in", "linear", "linear_dropout"])
+def test_l2_past_2_32_bytes(call, N):
+    """3 rows of more than 2^25 columns: L2 is 4.3 GB.  2000 columns of dY all along the matrix hold values; dL1 shows
+    the layers' G."""
+    q = qlib()
+    M, K, r, s = 3, 64, 64, 2.0
+    rng = np.random.default_rng(8)
+    cols = np.unique(np.linspace(0, N - 1, 2000).astype(np.int64))
+    n = len(cols)
+    print(f"[{call} N={N}]", flush=True)
+    at = torch.from_numpy(cols).to(DEV)
+    L2 = torch.empty((r, N), dtype=BF, device=DEV).normal_()
+    dY = torch.zeros((M, N), dtype=BF, device=DEV)
+    dY[:, at] = dev(rng.standard_normal((M, n)))
+    dy, l2 = f64(dY[:, at]), f64(L2[:, at])
+    G = s * dy @ l2.T
+    errG = (n + 4) * U * s * (np.abs(dy) @ np.abs(l2).T)
+    if call == "grad_in":
+        within(q.qlora_lora_grad_in(dY, L2, s), G, 2.0**-8 * np.abs(G) + errG, "G")
+        return
+    X, L1, T = (dev(rng.standard_normal(shape)) for shape in ((M, K), (K, r), (M, r)))
+    W = torch.empty((N, K), dtype=BF, device=DEV).normal_(0, 0.05)
+    codes, absmax = q.nf4_quantize(W)
+    base = (codes, *q.nf4_double_quant(absmax))
+    x = f64(X)
+    if call == "linear":
+        _, dL1, dL2 = q.qlora_linear_bwd(X, dY, *base, L1, L2, s, T=T, dX=False)
+        errG = errG + 2.0**-8 * np.abs(G)                   # that layer's G is rounded to bf16
+    else:
+        _, dL1, dL2 = q.qlora_linear_bwd_dropout(X, dY, *base, L1, L2, s, T=T, dX=False, p=0.1, seed=1, offset=2)
+        x = x * mask_at(np.arange(M), np.arange(K), 0.1, 1, 2)
+    within(dL1, x.T @ G, (M + 4) * U * (np.abs(x).T @ np.abs(G)) + np.abs(x).T @ errG, "dL1")
+    t = f64(T)
+    within(dL2[:, at], s * t.T @ dy, (M + 4) * U * s * (np.abs(t).T @ np.abs(dy)), "dL2")
