@@ -334,18 +334,18 @@ def qlora_linear_bwd_workspace(M, K, N, r):
     return int(lib().qlora_linear_bwd_workspace(M, K, N, r))
 
 
-def _workspace(nbytes, like, workspace, stream=None):
-    """The call's scratch.  Allocated here for another stream than the current one, it is not
-    handed out again before that stream has passed the call."""
+def _workspace(nbytes, like, workspace, stream):
+    """The call's scratch.  For another stream than the current one it comes from that stream's own
+    memory: what the current stream may still be using is not handed to it, nor the reverse."""
     if workspace is not None:
         _need(workspace, "workspace", torch.uint8)
         if workspace.numel() < nbytes:
             raise ValueError(f"workspace must hold at least {nbytes} bytes, got {workspace.numel()}")
         return workspace
-    ws = _empty((max(nbytes, 16),), torch.uint8, like)
-    if stream is not None and ws.is_cuda:
-        ws.record_stream(stream)
-    return ws
+    if stream is None or not like.is_cuda or stream.cuda_stream == _stream():
+        return _empty((max(nbytes, 16),), torch.uint8, like)
+    with torch.cuda.stream(stream):
+        return _empty((max(nbytes, 16),), torch.uint8, like)
 
 
 def _opt_out(t, name, dtype, shape, like):
@@ -369,7 +369,7 @@ def qlora_linear_fwd(X, codes, c2, c1, N, L1, L2, lora_scale=1.0, Y=None, T_out=
     _need(L2, "L2", torch.bfloat16, shape=(r, N))
     Y = _out(Y, "Y", torch.bfloat16, (M, N), X)
     T_out = _opt_out(T_out, "T_out", torch.bfloat16, (M, r), X)
-    ws = _workspace(qlora_linear_fwd_workspace(M, K, N, r), X, workspace)
+    ws = _workspace(qlora_linear_fwd_workspace(M, K, N, r), X, workspace, stream)
     _check("qlora_linear_fwd", lib().qlora_linear_fwd(
         _ptr(X), M, K, N, _ptr(codes), _ptr(c2), _ptr(c1), _ptr(L1), _ptr(L2), r, float(lora_scale),
         _ptr(Y), _ptr(T_out), _ptr(ws), ws.numel(), _stream(stream)))
@@ -415,7 +415,7 @@ def qlora_linear_bwd(X, dY, codes, c2, c1, L1, L2, lora_scale=1.0, T=None, dX=Tr
     dX = _opt_out(dX, "dX", torch.bfloat16, (M, K), X)
     dL1 = _out(dL1, "dL1", torch.float32, (K, r), X)
     dL2 = _out(dL2, "dL2", torch.float32, (r, N), X)
-    ws = _workspace(qlora_linear_bwd_workspace(M, K, N, r), X, workspace)
+    ws = _workspace(qlora_linear_bwd_workspace(M, K, N, r), X, workspace, stream)
     _check("qlora_linear_bwd", lib().qlora_linear_bwd(
         _ptr(X), _ptr(dY), M, K, N, _ptr(codes), _ptr(c2), _ptr(c1), _ptr(L1), _ptr(L2), r, float(lora_scale),
         _ptr(T), _ptr(dX), _ptr(dL1), _ptr(dL2), _ptr(ws), ws.numel(), _stream(stream)))
@@ -441,7 +441,7 @@ def qlora_group_fwd(X, codes, c2, c1, N, G, L1, L2, lora_scale=1.0, Y=None, T_ou
     r = _group_adapters(L1, L2, G, K, N)
     Y = _out(Y, "Y", torch.bfloat16, (M, G * N), X)
     T_out = _opt_out(T_out, "T_out", torch.bfloat16, (G, M, r), X)
-    ws = _workspace(int(lib().qlora_group_fwd_workspace(M, K, N, G, r)), X, workspace)
+    ws = _workspace(int(lib().qlora_group_fwd_workspace(M, K, N, G, r)), X, workspace, stream)
     _check("qlora_group_fwd", lib().qlora_group_fwd(
         _ptr(X), M, K, N, G, _ptr(codes), _ptr(c2), _ptr(c1), _ptr(L1), _ptr(L2), r, float(lora_scale),
         _ptr(Y), _ptr(T_out), _ptr(ws), ws.numel(), _stream(stream)))
@@ -464,7 +464,7 @@ def qlora_group_bwd(X, dY, codes, c2, c1, G, L1, L2, lora_scale=1.0, T=None, dX=
     dX = _opt_out(dX, "dX", torch.bfloat16, (M, K), X)
     dL1 = _out(dL1, "dL1", torch.float32, (G, K, r), X)
     dL2 = _out(dL2, "dL2", torch.float32, (G, r, N), X)
-    ws = _workspace(int(lib().qlora_group_bwd_workspace(M, K, N, G, r)), X, workspace)
+    ws = _workspace(int(lib().qlora_group_bwd_workspace(M, K, N, G, r)), X, workspace, stream)
     _check("qlora_group_bwd", lib().qlora_group_bwd(
         _ptr(X), _ptr(dY), M, K, N, G, _ptr(codes), _ptr(c2), _ptr(c1), _ptr(L1), _ptr(L2), r, float(lora_scale),
         _ptr(T), _ptr(dX), _ptr(dL1), _ptr(dL2), _ptr(ws), ws.numel(), _stream(stream)))
@@ -504,7 +504,7 @@ def qlora_lora_down(X, L1, T=None, workspace=None, stream=None):
     M, K = X.shape
     r = _rank(L1, K)
     T = _out(T, "T", torch.bfloat16, (M, r), X)
-    ws = _workspace(int(lib().qlora_lora_down_workspace(M, K, r)), X, workspace)
+    ws = _workspace(int(lib().qlora_lora_down_workspace(M, K, r)), X, workspace, stream)
     _check("qlora_lora_down", lib().qlora_lora_down(_ptr(X), M, K, _ptr(L1), r, _ptr(T), _ptr(ws), ws.numel(),
                                                     _stream(stream)))
     return T
@@ -536,7 +536,7 @@ def qlora_lora_grad_in(dY, L2, lora_scale=1.0, G=None, workspace=None, stream=No
         raise ValueError(f"L2 must have {N} columns, got {tuple(L2.shape)}")
     r = L2.shape[0]
     G = _out(G, "G", torch.bfloat16, (M, r), dY)
-    ws = _workspace(int(lib().qlora_lora_grad_in_workspace(M, N, r)), dY, workspace)
+    ws = _workspace(int(lib().qlora_lora_grad_in_workspace(M, N, r)), dY, workspace, stream)
     _check("qlora_lora_grad_in", lib().qlora_lora_grad_in(_ptr(dY), M, N, _ptr(L2), r, float(lora_scale), _ptr(G),
                                                           _ptr(ws), ws.numel(), _stream(stream)))
     return G
@@ -575,7 +575,7 @@ def lora_linear_fwd(X, W, L1, L2, lora_scale=1.0, Y=None, T_out=None, workspace=
     _need(L2, "L2", torch.bfloat16, shape=(r, N))
     Y = _out(Y, "Y", torch.bfloat16, (M, N), X)
     T_out = _opt_out(T_out, "T_out", torch.bfloat16, (M, r), X)
-    ws = _workspace(qlora_linear_fwd_workspace(M, K, N, r), X, workspace)
+    ws = _workspace(qlora_linear_fwd_workspace(M, K, N, r), X, workspace, stream)
     _check("lora_linear_fwd", lib().lora_linear_fwd(
         _ptr(X), M, K, N, _ptr(W), _ptr(L1), _ptr(L2), r, float(lora_scale), _ptr(Y), _ptr(T_out), _ptr(ws),
         ws.numel(), _stream(stream)))
@@ -599,7 +599,7 @@ def lora_linear_bwd(X, dY, W, L1, L2, lora_scale=1.0, T=None, dX=True, dL1=None,
     dX = _opt_out(dX, "dX", torch.bfloat16, (M, K), X)
     dL1 = _out(dL1, "dL1", torch.float32, (K, r), X)
     dL2 = _out(dL2, "dL2", torch.float32, (r, N), X)
-    ws = _workspace(qlora_linear_bwd_workspace(M, K, N, r), X, workspace)
+    ws = _workspace(qlora_linear_bwd_workspace(M, K, N, r), X, workspace, stream)
     _check("lora_linear_bwd", lib().lora_linear_bwd(
         _ptr(X), _ptr(dY), M, K, N, _ptr(W), _ptr(L1), _ptr(L2), r, float(lora_scale), _ptr(T), _ptr(dX),
         _ptr(dL1), _ptr(dL2), _ptr(ws), ws.numel(), _stream(stream)))

@@ -1,0 +1,91 @@
+"""Calls on another stream than the current one: what they allocate themselves is theirs until that stream has passed
+them."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF = torch.bfloat16
+SLEEP = 20_000_000              # GPU cycles, some ten milliseconds
+
+
+def qlib():
+    import bit_quantized_lora_blockwise_amd as q
+    return q
+
+
+class Layer:
+    """Inputs of a layer over NF4, two of them stacked, and over bf16, and the calls with scratch of their own."""
+
+    def __init__(self, M, K=1024, N=2048, r=16):
+        q, g = qlib(), torch.Generator(device=DEV)
+        g.manual_seed(M)
+
+        def normal(*shape, std=1.0):
+            return (torch.randn(shape, generator=g, device=DEV) * std).to(BF)
+
+        self.X, self.dY, self.W = normal(M, K), normal(M, N), normal(N, K, std=0.05)
+        self.L1, self.L2 = normal(K, r, std=K ** -0.5), normal(r, N, std=0.1)
+        self.G1, self.G2 = normal(2, K, r, std=K ** -0.5), normal(2, r, N // 2, std=0.1)
+        codes, absmax = q.nf4_quantize(self.W)
+        self.base = (codes, *q.nf4_double_quant(absmax))
+        self.N = N
+
+    def calls(self, q, **kw):
+        X, dY, base, N, L1, L2 = self.X, self.dY, self.base, self.N, self.L1, self.L2
+        yield "qlora_linear_fwd", q.qlora_linear_fwd(X, *base, N, L1, L2, 1.5, **kw)
+        yield "qlora_linear_bwd", q.qlora_linear_bwd(X, dY, *base, L1, L2, 1.5, **kw)
+        if X.shape[0] > 16:
+            yield "qlora_group_fwd", q.qlora_group_fwd(X, *base, N // 2, 2, self.G1, self.G2, 1.5, **kw)
+            yield "qlora_group_bwd", q.qlora_group_bwd(X, dY, *base, 2, self.G1, self.G2, 1.5, **kw)
+        yield "qlora_lora_down", q.qlora_lora_down(X, L1, **kw)
+        yield "qlora_lora_grad_in", q.qlora_lora_grad_in(dY, L2, 1.5, **kw)
+        yield "lora_linear_fwd", q.lora_linear_fwd(X, self.W, L1, L2, 1.5, **kw)
+        yield "lora_linear_bwd", q.lora_linear_bwd(X, dY, self.W, L1, L2, 1.5, **kw)
+        yield "qlora_linear_fwd_dropout", q.qlora_linear_fwd_dropout(X, *base, N, L1, L2, 1.5, p=0.1, seed=1, **kw)
+        yield "qlora_linear_bwd_dropout", q.qlora_linear_bwd_dropout(X, dY, *base, L1, L2, 1.5, p=0.1, seed=1, **kw)
+
+
+def tensors(v):
+    return [t for t in (v if isinstance(v, tuple) else (v,)) if t is not None]
+
+
+@pytest.mark.parametrize("M", [8, 512])
+def test_scratch_outlives_a_call_on_another_stream(M, monkeypatch):
+    """Memory that the current stream takes right after the call, which still waits, is not the call's scratch."""
+    from bit_quantized_lora_blockwise_amd import _lib
+    q, d = qlib(), Layer(M)
+    side, scratch, own = torch.cuda.Stream(), [], _lib._workspace
+
+    def seen(*args):
+        ws = own(*args)
+        scratch.append((ws.data_ptr(), ws.numel()))
+        return ws
+
+    plain = dict(d.calls(q))
+    monkeypatch.setattr(_lib, "_workspace", seen)
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(SLEEP)                     # the calls wait behind this
+    for name, got in d.calls(q, stream=side):
+        at, n = scratch[-1]
+        taken = [torch.full((n,), 255, dtype=torch.uint8, device=DEV) for _ in range(3)]
+        assert at not in [t.data_ptr() for t in taken], name
+        plain[name] = (plain[name], got)
+    torch.cuda.synchronize()
+    assert len(scratch) == len(plain)
+    for name, (want, got) in plain.items():
+        for a, b in zip(tensors(want), tensors(got)):
+            assert torch.equal(a, b), name
+
+
+def test_scratch_is_not_what_the_current_stream_may_still_use():
+    """A block that a call on the current stream has just let go of, with its work still queued."""
+    from bit_quantized_lora_blockwise_amd import _lib
+    like, side = torch.empty(1, device=DEV), torch.cuda.Stream()
+    for n in (1000, 3 << 20):
+        first = _lib._workspace(n, like, None, None)
+        held = first.data_ptr()
+        del first
+        other = _lib._workspace(n, like, None, side).data_ptr()
+        again = _lib._workspace(n, like, None, torch.cuda.current_stream()).data_ptr()
+        assert other != held and again == held
