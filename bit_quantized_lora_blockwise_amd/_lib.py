@@ -160,11 +160,11 @@ def _packed(codes, c2, c1, rows, cols):
     _need(c1, "c1", torch.float32, numel=(nb + 255) // 256)
 
 
-def _out(t, name, dtype, shape, like):
+def _out(t, name, dtype, shape, like, stream):
     """An output: allocated here when None, else checked to have exactly the
     element count of `shape` (any contiguous layout of that many elements)."""
     if t is None:
-        return _empty(shape, dtype, like)
+        return _new(shape, dtype, like, stream)
     n = 1
     for d in shape:
         n *= d
@@ -176,15 +176,28 @@ def _check(fn, status):
         raise QloraError(fn, status)
 
 
-def _empty(shape, dtype, like):
-    """torch.empty on like's device; with the strides given it takes 1.3 us in place of 1.7."""
+def _empty(shape, dtype, like, stream=None):
+    """torch.empty on like's device; with the strides given it takes 1.3 us in place of 1.7.  For a call
+    on another stream than the current one it comes from that stream's own memory: what the current
+    stream may still be using is not handed to it, nor the reverse."""
     if len(shape) == 2:
         strides = (shape[1], 1)
     elif len(shape) == 1:
         strides = (1,)
     else:
         strides = (shape[1] * shape[2], shape[2], 1)
-    return torch.empty_strided(shape, strides, dtype=dtype, device=like.device)
+    if stream is None or not like.is_cuda or stream.cuda_stream == _stream():
+        return torch.empty_strided(shape, strides, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty_strided(shape, strides, dtype=dtype, device=like.device)
+
+
+def _new(shape, dtype, like, stream):
+    """An output allocated here; the current stream, which reads it next, has it until it lets go of it."""
+    t = _empty(shape, dtype, like, stream)
+    if stream is not None and t.is_cuda:
+        t.record_stream(torch.cuda.current_stream(t.device))
+    return t
 
 
 def _wdtype(W):
@@ -198,8 +211,8 @@ def nf4_quantize(W, codes=None, absmax=None, stream=None):
     dt = _wdtype(W)
     _need(W, "W", W.dtype, ndim=2)
     rows, cols = W.shape
-    codes = _out(codes, "codes", torch.uint8, (rows, cols // 2), W)
-    absmax = _out(absmax, "absmax", torch.float32, (rows * cols // 64,), W)
+    codes = _out(codes, "codes", torch.uint8, (rows, cols // 2), W, stream)
+    absmax = _out(absmax, "absmax", torch.float32, (rows * cols // 64,), W, stream)
     _check("nf4_quantize", lib().nf4_quantize(_ptr(W), dt, rows, cols, _ptr(codes), _ptr(absmax), _stream(stream)))
     return codes, absmax
 
@@ -210,13 +223,13 @@ def nf4_quantize_dq(W, codes=None, c2=None, c1=None, absmax=None, stream=None):
     _need(W, "W", W.dtype, ndim=2)
     rows, cols = W.shape
     nb = rows * cols // 64
-    codes = _out(codes, "codes", torch.uint8, (rows, cols // 2), W)
-    c2 = _out(c2, "c2", torch.uint8, (nb,), W)
-    c1 = _out(c1, "c1", torch.float32, ((nb + 255) // 256,), W)
+    codes = _out(codes, "codes", torch.uint8, (rows, cols // 2), W, stream)
+    c2 = _out(c2, "c2", torch.uint8, (nb,), W, stream)
+    c1 = _out(c1, "c1", torch.float32, ((nb + 255) // 256,), W, stream)
     if absmax is True:
-        absmax = _empty((nb,), torch.float32, W)
+        absmax = _new((nb,), torch.float32, W, stream)
     elif absmax is not None:
-        _out(absmax, "absmax", torch.float32, (nb,), W)
+        _out(absmax, "absmax", torch.float32, (nb,), W, stream)
     _check("nf4_quantize_dq", lib().nf4_quantize_dq(_ptr(W), dt, rows, cols, _ptr(codes), _ptr(absmax), _ptr(c2),
                                                     _ptr(c1), _stream(stream)))
     return codes, c2, c1, absmax
@@ -226,8 +239,8 @@ def nf4_double_quant(absmax, c2=None, c1=None, stream=None):
     """E4M3FN codes c2 [n_blocks] (uint8) and fp32 group scales c1 [ceil(n_blocks/256)]."""
     _need(absmax, "absmax", torch.float32)
     nb = absmax.numel()
-    c2 = _out(c2, "c2", torch.uint8, (nb,), absmax)
-    c1 = _out(c1, "c1", torch.float32, ((nb + 255) // 256,), absmax)
+    c2 = _out(c2, "c2", torch.uint8, (nb,), absmax, stream)
+    c1 = _out(c1, "c1", torch.float32, ((nb + 255) // 256,), absmax, stream)
     _check("nf4_double_quant", lib().nf4_double_quant(_ptr(absmax), nb, _ptr(c2), _ptr(c1), _stream(stream)))
     return c2, c1
 
@@ -235,7 +248,7 @@ def nf4_double_quant(absmax, c2=None, c1=None, stream=None):
 def nf4_dequantize(codes, c2, c1, rows, cols, out=None, stream=None):
     """Bit-exact bf16 doubleDequant(c1, c2, W_NF4) [rows, cols]."""
     _packed(codes, c2, c1, rows, cols)
-    out = _out(out, "out", torch.bfloat16, (rows, cols), codes)
+    out = _out(out, "out", torch.bfloat16, (rows, cols), codes, stream)
     _check("nf4_dequantize", lib().nf4_dequantize(_ptr(codes), _ptr(c2), _ptr(c1), rows, cols, _ptr(out),
                                                   _stream(stream)))
     return out
@@ -258,8 +271,8 @@ def q4_quantize(W, codebook="nf4", codes=None, absmax=None, stream=None):
     dt = _wdtype(W)
     _need(W, "W", W.dtype, ndim=2)
     rows, cols = W.shape
-    codes = _out(codes, "codes", torch.uint8, (rows, cols // 2), W)
-    absmax = _out(absmax, "absmax", torch.float32, (rows * cols // 64,), W)
+    codes = _out(codes, "codes", torch.uint8, (rows, cols // 2), W, stream)
+    absmax = _out(absmax, "absmax", torch.float32, (rows * cols // 64,), W, stream)
     _check("q4_quantize", lib().q4_quantize(_ptr(W), dt, rows, cols, _codebook(codebook), _ptr(codes), _ptr(absmax),
                                             _stream(stream)))
     return codes, absmax
@@ -273,9 +286,9 @@ def q4_double_quant(absmax, scale_code="groupmax", stream=None):
         raise ValueError("absmax scales need no second level")
     nb = absmax.numel()
     ng = (nb + 255) // 256
-    c2 = _empty((nb,), torch.uint8, absmax)
-    c1 = _empty((ng,), torch.float32, absmax)
-    mu = _empty((ng,), torch.float32, absmax) if scale_code == "mean" else None
+    c2 = _new((nb,), torch.uint8, absmax, stream)
+    c1 = _new((ng,), torch.float32, absmax, stream)
+    mu = _new((ng,), torch.float32, absmax, stream) if scale_code == "mean" else None
     _check("q4_double_quant", lib().q4_double_quant(_ptr(absmax), nb, sc, _ptr(c2), _ptr(c1),
                                                     _ptr(mu) if mu is not None else None, _stream(stream)))
     return c2, c1, mu
@@ -293,7 +306,7 @@ def q4_dequantize(codes, rows, cols, codebook="nf4", scale_code="groupmax", absm
                          (c1, "c1", torch.float32, ng), (mu, "mu", torch.float32, ng)):
         if t is not None:
             _need(t, n, d, numel=cnt)
-    out = _out(out, "out", torch.bfloat16, (rows, cols), codes)
+    out = _out(out, "out", torch.bfloat16, (rows, cols), codes, stream)
     p = lambda t: _ptr(t) if t is not None else None
     _check("q4_dequantize", lib().q4_dequantize(_ptr(codes), rows, cols, _codebook(codebook), _scale_code(scale_code),
                                                 p(absmax), p(c2), p(c1), p(mu), _ptr(out), _stream(stream)))
@@ -320,7 +333,7 @@ def qlora_merge(codes, c2, c1, N, K, L1, L2, lora_scale=1.0, out=None, stream=No
     _packed(codes, c2, c1, N, K)
     r = _rank(L1, K)
     _need(L2, "L2", torch.bfloat16, shape=(r, N))
-    out = _out(out, "out", torch.bfloat16, (N, K), codes)
+    out = _out(out, "out", torch.bfloat16, (N, K), codes, stream)
     _check("qlora_merge", lib().qlora_merge(_ptr(codes), _ptr(c2), _ptr(c1), N, K, _ptr(L1), _ptr(L2), r,
                                             float(lora_scale), _ptr(out), _stream(stream)))
     return out
@@ -335,26 +348,22 @@ def qlora_linear_bwd_workspace(M, K, N, r):
 
 
 def _workspace(nbytes, like, workspace, stream):
-    """The call's scratch.  For another stream than the current one it comes from that stream's own
-    memory: what the current stream may still be using is not handed to it, nor the reverse."""
+    """The call's scratch."""
     if workspace is not None:
         _need(workspace, "workspace", torch.uint8)
         if workspace.numel() < nbytes:
             raise ValueError(f"workspace must hold at least {nbytes} bytes, got {workspace.numel()}")
         return workspace
-    if stream is None or not like.is_cuda or stream.cuda_stream == _stream():
-        return _empty((max(nbytes, 16),), torch.uint8, like)
-    with torch.cuda.stream(stream):
-        return _empty((max(nbytes, 16),), torch.uint8, like)
+    return _empty((max(nbytes, 16),), torch.uint8, like, stream)
 
 
-def _opt_out(t, name, dtype, shape, like):
+def _opt_out(t, name, dtype, shape, like, stream):
     """Optional output: True -> allocated here, None/False -> absent, else checked."""
     if t is True:
-        return _empty(shape, dtype, like)
+        return _new(shape, dtype, like, stream)
     if t is None or t is False:
         return None
-    return _out(t, name, dtype, shape, like)
+    return _out(t, name, dtype, shape, like, stream)
 
 
 def qlora_linear_fwd(X, codes, c2, c1, N, L1, L2, lora_scale=1.0, Y=None, T_out=None, workspace=None,
@@ -367,8 +376,8 @@ def qlora_linear_fwd(X, codes, c2, c1, N, L1, L2, lora_scale=1.0, Y=None, T_out=
     _packed(codes, c2, c1, N, K)
     r = _rank(L1, K)
     _need(L2, "L2", torch.bfloat16, shape=(r, N))
-    Y = _out(Y, "Y", torch.bfloat16, (M, N), X)
-    T_out = _opt_out(T_out, "T_out", torch.bfloat16, (M, r), X)
+    Y = _out(Y, "Y", torch.bfloat16, (M, N), X, stream)
+    T_out = _opt_out(T_out, "T_out", torch.bfloat16, (M, r), X, stream)
     ws = _workspace(qlora_linear_fwd_workspace(M, K, N, r), X, workspace, stream)
     _check("qlora_linear_fwd", lib().qlora_linear_fwd(
         _ptr(X), M, K, N, _ptr(codes), _ptr(c2), _ptr(c1), _ptr(L1), _ptr(L2), r, float(lora_scale),
@@ -388,8 +397,8 @@ def qlora_linear_fwd_noalloc(X, codes, c2, c1, N, L1, L2, lora_scale=1.0, Y=None
     _packed(codes, c2, c1, N, K)
     r = _rank(L1, K)
     _need(L2, "L2", torch.bfloat16, shape=(r, N))
-    Y = _out(Y, "Y", torch.bfloat16, (M, N), X)
-    T_out = _opt_out(T_out, "T_out", torch.bfloat16, (M, r), X)
+    Y = _out(Y, "Y", torch.bfloat16, (M, N), X, stream)
+    T_out = _opt_out(T_out, "T_out", torch.bfloat16, (M, r), X, stream)
     _check("qlora_linear_fwd_noalloc", lib().qlora_linear_fwd_noalloc(
         _ptr(X), M, K, N, _ptr(codes), _ptr(c2), _ptr(c1), _ptr(L1), _ptr(L2), r, float(lora_scale),
         _ptr(Y), _ptr(T_out), _stream(stream)))
@@ -412,9 +421,9 @@ def qlora_linear_bwd(X, dY, codes, c2, c1, L1, L2, lora_scale=1.0, T=None, dX=Tr
     _need(L2, "L2", torch.bfloat16, shape=(r, N))
     if T is not None:
         _need(T, "T", torch.bfloat16, numel=M * r)
-    dX = _opt_out(dX, "dX", torch.bfloat16, (M, K), X)
-    dL1 = _out(dL1, "dL1", torch.float32, (K, r), X)
-    dL2 = _out(dL2, "dL2", torch.float32, (r, N), X)
+    dX = _opt_out(dX, "dX", torch.bfloat16, (M, K), X, stream)
+    dL1 = _out(dL1, "dL1", torch.float32, (K, r), X, stream)
+    dL2 = _out(dL2, "dL2", torch.float32, (r, N), X, stream)
     ws = _workspace(qlora_linear_bwd_workspace(M, K, N, r), X, workspace, stream)
     _check("qlora_linear_bwd", lib().qlora_linear_bwd(
         _ptr(X), _ptr(dY), M, K, N, _ptr(codes), _ptr(c2), _ptr(c1), _ptr(L1), _ptr(L2), r, float(lora_scale),
@@ -439,8 +448,8 @@ def qlora_group_fwd(X, codes, c2, c1, N, G, L1, L2, lora_scale=1.0, Y=None, T_ou
     M, K = X.shape
     _packed(codes, c2, c1, G * N, K)
     r = _group_adapters(L1, L2, G, K, N)
-    Y = _out(Y, "Y", torch.bfloat16, (M, G * N), X)
-    T_out = _opt_out(T_out, "T_out", torch.bfloat16, (G, M, r), X)
+    Y = _out(Y, "Y", torch.bfloat16, (M, G * N), X, stream)
+    T_out = _opt_out(T_out, "T_out", torch.bfloat16, (G, M, r), X, stream)
     ws = _workspace(int(lib().qlora_group_fwd_workspace(M, K, N, G, r)), X, workspace, stream)
     _check("qlora_group_fwd", lib().qlora_group_fwd(
         _ptr(X), M, K, N, G, _ptr(codes), _ptr(c2), _ptr(c1), _ptr(L1), _ptr(L2), r, float(lora_scale),
@@ -461,9 +470,9 @@ def qlora_group_bwd(X, dY, codes, c2, c1, G, L1, L2, lora_scale=1.0, T=None, dX=
     r = _group_adapters(L1, L2, G, K, N)
     if T is not None:
         _need(T, "T", torch.bfloat16, numel=G * M * r)
-    dX = _opt_out(dX, "dX", torch.bfloat16, (M, K), X)
-    dL1 = _out(dL1, "dL1", torch.float32, (G, K, r), X)
-    dL2 = _out(dL2, "dL2", torch.float32, (G, r, N), X)
+    dX = _opt_out(dX, "dX", torch.bfloat16, (M, K), X, stream)
+    dL1 = _out(dL1, "dL1", torch.float32, (G, K, r), X, stream)
+    dL2 = _out(dL2, "dL2", torch.float32, (G, r, N), X, stream)
     ws = _workspace(int(lib().qlora_group_bwd_workspace(M, K, N, G, r)), X, workspace, stream)
     _check("qlora_group_bwd", lib().qlora_group_bwd(
         _ptr(X), _ptr(dY), M, K, N, G, _ptr(codes), _ptr(c2), _ptr(c1), _ptr(L1), _ptr(L2), r, float(lora_scale),
@@ -503,7 +512,7 @@ def qlora_lora_down(X, L1, T=None, workspace=None, stream=None):
     _need(X, "X", torch.bfloat16, ndim=2)
     M, K = X.shape
     r = _rank(L1, K)
-    T = _out(T, "T", torch.bfloat16, (M, r), X)
+    T = _out(T, "T", torch.bfloat16, (M, r), X, stream)
     ws = _workspace(int(lib().qlora_lora_down_workspace(M, K, r)), X, workspace, stream)
     _check("qlora_lora_down", lib().qlora_lora_down(_ptr(X), M, K, _ptr(L1), r, _ptr(T), _ptr(ws), ws.numel(),
                                                     _stream(stream)))
@@ -520,7 +529,7 @@ def qlora_linear_fwd_t(X, codes, c2, c1, N, T, L2, lora_scale=1.0, Y=None, strea
         raise ValueError(f"T must have {M} rows, got {tuple(T.shape)}")
     r = T.shape[1]
     _need(L2, "L2", torch.bfloat16, shape=(r, N))
-    Y = _out(Y, "Y", torch.bfloat16, (M, N), X)
+    Y = _out(Y, "Y", torch.bfloat16, (M, N), X, stream)
     _check("qlora_linear_fwd_t", lib().qlora_linear_fwd_t(
         _ptr(X), M, K, N, _ptr(codes), _ptr(c2), _ptr(c1), _ptr(T), _ptr(L2), r, float(lora_scale), _ptr(Y),
         _stream(stream)))
@@ -535,7 +544,7 @@ def qlora_lora_grad_in(dY, L2, lora_scale=1.0, G=None, workspace=None, stream=No
     if L2.shape[1] != N:
         raise ValueError(f"L2 must have {N} columns, got {tuple(L2.shape)}")
     r = L2.shape[0]
-    G = _out(G, "G", torch.bfloat16, (M, r), dY)
+    G = _out(G, "G", torch.bfloat16, (M, r), dY, stream)
     ws = _workspace(int(lib().qlora_lora_grad_in_workspace(M, N, r)), dY, workspace, stream)
     _check("qlora_lora_grad_in", lib().qlora_lora_grad_in(_ptr(dY), M, N, _ptr(L2), r, float(lora_scale), _ptr(G),
                                                           _ptr(ws), ws.numel(), _stream(stream)))
@@ -552,7 +561,7 @@ def qlora_linear_dx(dY, codes, c2, c1, K, G, L1, dX=None, stream=None):
         raise ValueError(f"G must have {M} rows, got {tuple(G.shape)}")
     r = G.shape[1]
     _need(L1, "L1", torch.bfloat16, shape=(K, r))
-    dX = _out(dX, "dX", torch.bfloat16, (M, K), dY)
+    dX = _out(dX, "dX", torch.bfloat16, (M, K), dY, stream)
     _check("qlora_linear_dx", lib().qlora_linear_dx(
         _ptr(dY), M, K, N, _ptr(codes), _ptr(c2), _ptr(c1), _ptr(G), _ptr(L1), r, _ptr(dX), _stream(stream)))
     return dX
@@ -573,8 +582,8 @@ def lora_linear_fwd(X, W, L1, L2, lora_scale=1.0, Y=None, T_out=None, workspace=
     _bf16_weight(W, N, K)
     r = _rank(L1, K)
     _need(L2, "L2", torch.bfloat16, shape=(r, N))
-    Y = _out(Y, "Y", torch.bfloat16, (M, N), X)
-    T_out = _opt_out(T_out, "T_out", torch.bfloat16, (M, r), X)
+    Y = _out(Y, "Y", torch.bfloat16, (M, N), X, stream)
+    T_out = _opt_out(T_out, "T_out", torch.bfloat16, (M, r), X, stream)
     ws = _workspace(qlora_linear_fwd_workspace(M, K, N, r), X, workspace, stream)
     _check("lora_linear_fwd", lib().lora_linear_fwd(
         _ptr(X), M, K, N, _ptr(W), _ptr(L1), _ptr(L2), r, float(lora_scale), _ptr(Y), _ptr(T_out), _ptr(ws),
@@ -596,9 +605,9 @@ def lora_linear_bwd(X, dY, W, L1, L2, lora_scale=1.0, T=None, dX=True, dL1=None,
     _need(L2, "L2", torch.bfloat16, shape=(r, N))
     if T is not None:
         _need(T, "T", torch.bfloat16, numel=M * r)
-    dX = _opt_out(dX, "dX", torch.bfloat16, (M, K), X)
-    dL1 = _out(dL1, "dL1", torch.float32, (K, r), X)
-    dL2 = _out(dL2, "dL2", torch.float32, (r, N), X)
+    dX = _opt_out(dX, "dX", torch.bfloat16, (M, K), X, stream)
+    dL1 = _out(dL1, "dL1", torch.float32, (K, r), X, stream)
+    dL2 = _out(dL2, "dL2", torch.float32, (r, N), X, stream)
     ws = _workspace(qlora_linear_bwd_workspace(M, K, N, r), X, workspace, stream)
     _check("lora_linear_bwd", lib().lora_linear_bwd(
         _ptr(X), _ptr(dY), M, K, N, _ptr(W), _ptr(L1), _ptr(L2), r, float(lora_scale), _ptr(T), _ptr(dX),
@@ -618,7 +627,7 @@ def lora_linear_fwd_t(X, W, T, L2, lora_scale=1.0, Y=None, stream=None):
         raise ValueError(f"T must have {M} rows, got {tuple(T.shape)}")
     r = T.shape[1]
     _need(L2, "L2", torch.bfloat16, shape=(r, N))
-    Y = _out(Y, "Y", torch.bfloat16, (M, N), X)
+    Y = _out(Y, "Y", torch.bfloat16, (M, N), X, stream)
     _check("lora_linear_fwd_t", lib().lora_linear_fwd_t(
         _ptr(X), M, K, N, _ptr(W), _ptr(T), _ptr(L2), r, float(lora_scale), _ptr(Y), _stream(stream)))
     return Y
@@ -636,7 +645,7 @@ def lora_linear_dx(dY, W, G, L1, dX=None, stream=None):
         raise ValueError(f"G must have {M} rows, got {tuple(G.shape)}")
     r = G.shape[1]
     _need(L1, "L1", torch.bfloat16, shape=(K, r))
-    dX = _out(dX, "dX", torch.bfloat16, (M, K), dY)
+    dX = _out(dX, "dX", torch.bfloat16, (M, K), dY, stream)
     _check("lora_linear_dx", lib().lora_linear_dx(
         _ptr(dY), M, K, N, _ptr(W), _ptr(G), _ptr(L1), r, _ptr(dX), _stream(stream)))
     return dX
@@ -671,7 +680,7 @@ def lora_dropout(X, p, seed, offset=0, out=None, stream=None):
     """D o X for X [rows, cols] (fp32 or bf16, rows may be apart): kept elements over 1 - p, the others 0.
     The mask is a function of (p, seed, offset) and is never stored; the same call is the backward."""
     dt, rows, cols, ld = _rows(X, "X")
-    out = _out(out, "out", X.dtype, (rows, cols), X)
+    out = _out(out, "out", X.dtype, (rows, cols), X, stream)
     _check("lora_dropout", lib().lora_dropout(_ptr(X), dt, rows, cols, ld, *_draw(p, seed, offset), _ptr(out),
                                               _stream(stream)))
     return out
@@ -685,8 +694,8 @@ def qlora_linear_fwd_dropout(X, codes, c2, c1, N, L1, L2, lora_scale=1.0, p=0.0,
     _packed(codes, c2, c1, N, K)
     r = _rank(L1, K)
     _need(L2, "L2", torch.bfloat16, shape=(r, N))
-    Y = _out(Y, "Y", torch.bfloat16, (M, N), X)
-    T_out = _opt_out(T_out, "T_out", torch.bfloat16, (M, r), X)
+    Y = _out(Y, "Y", torch.bfloat16, (M, N), X, stream)
+    T_out = _opt_out(T_out, "T_out", torch.bfloat16, (M, r), X, stream)
     ws = _workspace(int(lib().qlora_linear_fwd_dropout_workspace(M, K, N, r)), X, workspace, stream)
     _check("qlora_linear_fwd_dropout", lib().qlora_linear_fwd_dropout(
         _ptr(X), M, K, N, _ptr(codes), _ptr(c2), _ptr(c1), _ptr(L1), _ptr(L2), r, float(lora_scale),
@@ -708,9 +717,9 @@ def qlora_linear_bwd_dropout(X, dY, codes, c2, c1, L1, L2, lora_scale=1.0, p=0.0
     _need(L2, "L2", torch.bfloat16, shape=(r, N))
     if T is not None:
         _need(T, "T", torch.bfloat16, numel=M * r)
-    dX = _opt_out(dX, "dX", torch.bfloat16, (M, K), X)
-    dL1 = _out(dL1, "dL1", torch.float32, (K, r), X)
-    dL2 = _out(dL2, "dL2", torch.float32, (r, N), X)
+    dX = _opt_out(dX, "dX", torch.bfloat16, (M, K), X, stream)
+    dL1 = _out(dL1, "dL1", torch.float32, (K, r), X, stream)
+    dL2 = _out(dL2, "dL2", torch.float32, (r, N), X, stream)
     ws = _workspace(int(lib().qlora_linear_bwd_dropout_workspace(M, K, N, r)), X, workspace, stream)
     _check("qlora_linear_bwd_dropout", lib().qlora_linear_bwd_dropout(
         _ptr(X), _ptr(dY), M, K, N, _ptr(codes), _ptr(c2), _ptr(c1), _ptr(L1), _ptr(L2), r, float(lora_scale),
@@ -743,8 +752,8 @@ def mx4_quantize(X, transpose=False, codes=None, scales=None, stream=None):
     its rows (R = rows), or with transpose down its columns (the packed matrix is X^T, R = cols)."""
     dt, rows, cols, ld = _rows(X, "X")
     sc, ss = _mx4_shapes(*((cols, rows) if transpose else (rows, cols)))
-    codes = _out(codes, "codes", torch.uint8, sc, X)
-    scales = _out(scales, "scales", torch.uint8, ss, X)
+    codes = _out(codes, "codes", torch.uint8, sc, X, stream)
+    scales = _out(scales, "scales", torch.uint8, ss, X, stream)
     _check("mx4_quantize", lib().mx4_quantize(_ptr(X), dt, rows, cols, ld, int(bool(transpose)), _ptr(codes),
                                               _ptr(scales), _stream(stream)))
     return codes, scales
@@ -753,7 +762,7 @@ def mx4_quantize(X, transpose=False, codes=None, scales=None, stream=None):
 def mx4_dequantize(codes, scales, rows, cols, out=None, stream=None):
     """bf16 values [rows, cols] of a packed matrix (exact)."""
     _mx4_packed(codes, scales, rows, cols)
-    out = _out(out, "out", torch.bfloat16, (rows, cols), codes)
+    out = _out(out, "out", torch.bfloat16, (rows, cols), codes, stream)
     _check("mx4_dequantize", lib().mx4_dequantize(_ptr(codes), _ptr(scales), rows, cols, _ptr(out), _stream(stream)))
     return out
 
@@ -762,7 +771,7 @@ def mx4_matmul(a_codes, a_scales, M, b_codes, b_scales, N, K, out=None, stream=N
     """bf16 [M, N] = A B^T of packed A [M, K] and B [N, K]."""
     _mx4_packed(a_codes, a_scales, M, K, "a_")
     _mx4_packed(b_codes, b_scales, N, K, "b_")
-    out = _out(out, "out", torch.bfloat16, (M, N), a_codes)
+    out = _out(out, "out", torch.bfloat16, (M, N), a_codes, stream)
     _check("mx4_matmul", lib().mx4_matmul(_ptr(a_codes), _ptr(a_scales), M, _ptr(b_codes), _ptr(b_scales), N, K,
                                           _ptr(out), _stream(stream)))
     return out
@@ -777,8 +786,8 @@ def mx4_linear_fwd(X, codes, scales, N, L1, L2, lora_scale=1.0, p=0.0, seed=0, o
     _mx4_packed(codes, scales, N, K)
     r = _rank(L1, K)
     _need(L2, "L2", torch.bfloat16, shape=(r, N))
-    Y = _out(Y, "Y", torch.bfloat16, (M, N), X)
-    T_out = _opt_out(T_out, "T_out", torch.bfloat16, (M, r), X)
+    Y = _out(Y, "Y", torch.bfloat16, (M, N), X, stream)
+    T_out = _opt_out(T_out, "T_out", torch.bfloat16, (M, r), X, stream)
     ws = _workspace(int(lib().mx4_linear_fwd_workspace(M, K, N, r)), X, workspace, stream)
     _check("mx4_linear_fwd", lib().mx4_linear_fwd(
         _ptr(X), M, K, N, _ptr(codes), _ptr(scales), _ptr(L1), _ptr(L2), r, float(lora_scale),
@@ -802,9 +811,9 @@ def mx4_linear_bwd(X, dY, codes_t, scales_t, L1, L2, lora_scale=1.0, p=0.0, seed
     _need(L2, "L2", torch.bfloat16, shape=(r, N))
     if T is not None:
         _need(T, "T", torch.bfloat16, numel=M * r)
-    dX = _opt_out(dX, "dX", torch.bfloat16, (M, K), X)
-    dL1 = _out(dL1, "dL1", torch.float32, (K, r), X)
-    dL2 = _out(dL2, "dL2", torch.float32, (r, N), X)
+    dX = _opt_out(dX, "dX", torch.bfloat16, (M, K), X, stream)
+    dL1 = _out(dL1, "dL1", torch.float32, (K, r), X, stream)
+    dL2 = _out(dL2, "dL2", torch.float32, (r, N), X, stream)
     ws = _workspace(int(lib().mx4_linear_bwd_workspace(M, K, N, r)), X, workspace, stream)
     _check("mx4_linear_bwd", lib().mx4_linear_bwd(
         _ptr(X), _ptr(dY), M, K, N, _ptr(codes_t), _ptr(scales_t), _ptr(L1), _ptr(L2), r, float(lora_scale),

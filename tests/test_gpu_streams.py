@@ -89,3 +89,61 @@ def test_scratch_is_not_what_the_current_stream_may_still_use():
         other = _lib._workspace(n, like, None, side).data_ptr()
         again = _lib._workspace(n, like, None, torch.cuda.current_stream()).data_ptr()
         assert other != held and again == held
+
+
+def test_outputs_outlive_a_call_on_another_stream():
+    """An output that the call allocates: let go of while the call still waits, it is not handed to the current stream;
+    nor is what that stream has just let go of, with its work queued, taken for one."""
+    q, d = qlib(), Layer(40)
+    codes, c2, c1 = d.base
+    absmax = q.nf4_quantize(d.W)[1]
+    q4c, q4a = q.q4_quantize(d.W, "fp4")
+    w, wt = q.mx4_quantize(d.W), q.mx4_quantize(d.W, transpose=True)
+    x = q.mx4_quantize(d.X)
+    T, G = q.qlora_lora_down(d.X, d.L1), q.qlora_lora_grad_in(d.dY, d.L2)
+    N, K = d.W.shape
+    calls = {
+        "nf4_quantize": lambda **k: q.nf4_quantize(d.W, **k),
+        "nf4_quantize_dq": lambda **k: q.nf4_quantize_dq(d.W, absmax=True, **k),
+        "nf4_double_quant": lambda **k: q.nf4_double_quant(absmax, **k),
+        "nf4_dequantize": lambda **k: q.nf4_dequantize(*d.base, N, K, **k),
+        "q4_quantize": lambda **k: q.q4_quantize(d.W, "fp4", **k),
+        "q4_double_quant": lambda **k: q.q4_double_quant(q4a, "mean", **k),
+        "q4_dequantize": lambda **k: q.q4_dequantize(q4c, N, K, "fp4", "absmax", absmax=q4a, **k),
+        "qlora_merge": lambda **k: q.qlora_merge(*d.base, N, K, d.L1, d.L2, **k),
+        "qlora_linear_fwd_t": lambda **k: q.qlora_linear_fwd_t(d.X, *d.base, N, T, d.L2, **k),
+        "qlora_linear_dx": lambda **k: q.qlora_linear_dx(d.dY, *d.base, K, G, d.L1, **k),
+        "lora_linear_fwd_t": lambda **k: q.lora_linear_fwd_t(d.X, d.W, T, d.L2, **k),
+        "lora_linear_dx": lambda **k: q.lora_linear_dx(d.dY, d.W, G, d.L1, **k),
+        "lora_dropout": lambda **k: q.lora_dropout(d.X, 0.1, 1, **k),
+        "mx4_quantize": lambda **k: q.mx4_quantize(d.X, **k),
+        "mx4_dequantize": lambda **k: q.mx4_dequantize(*w, N, K, **k),
+        "mx4_matmul": lambda **k: q.mx4_matmul(*x, 40, *w, N, K, **k),
+        "mx4_linear_fwd": lambda **k: q.mx4_linear_fwd(d.X, *w, N, d.L1, d.L2, T_out=True, p=0.1, **k),
+        "mx4_linear_bwd": lambda **k: q.mx4_linear_bwd(d.X, d.dY, *wt, d.L1, d.L2, T=T, **k),
+    }
+    for name, _ in d.calls(q):
+        calls[name] = lambda name=name, **k: dict(d.calls(q, **k))[name]
+    side = torch.cuda.Stream()
+    for name, call in calls.items():
+        own = tensors(call())
+        sizes = [t.numel() * t.element_size() for t in own]
+        held = {t.data_ptr() for t in own}
+        keep = [t.clone() for t in own]
+        del own
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(SLEEP)
+        got = tensors(call(stream=side))
+        at = {t.data_ptr() for t in got}
+        assert not at & held, name
+        side.synchronize()
+        for a, b in zip(keep, got):
+            assert torch.equal(a, b), name
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(SLEEP)
+        at = {t.data_ptr() for t in tensors(call(stream=side))}      # and gone at once
+        taken = [torch.empty(n, dtype=torch.uint8, device=DEV) for n in sizes for _ in range(3)]
+        assert not at & {t.data_ptr() for t in taken}, name
+        torch.cuda.synchronize()
+        del got, taken
