@@ -36,6 +36,8 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t top) {
   return e == 255u ? 255u : (e > 6u ? e - 2u : 4u);
 }
 
+// The scale operand of the conversions, which read its exponent bits alone: byte 0 stands
+// for 2^-127 there as in the matrix instruction.
 __device__ __forceinline__ float scale_f32(uint32_t byte) { return __uint_as_float(byte << 23); }
 
 // Largest over lanes l, l ^ 16, l ^ 32, l ^ 48.
