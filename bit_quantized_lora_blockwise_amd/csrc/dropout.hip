@@ -2,6 +2,9 @@
 // 65536 / (65536 - cut), dropped ones 0 whatever they hold.  D o is its own
 // transpose, so the same call is the backward.
 //
+// In place (Y = X): a thread stores only elements that it alone uses.  The piece at a
+// row's end is read with elements of the piece before it, which are shifted out.
+//
 // One thread takes the eight elements of a row that share a draw.  Bound: HBM for
 // large bf16 matrices; the draws' quarter-rate products cost about the same time
 // as the traffic of a bf16 element (4 bytes), and overlap with it: a thread's next

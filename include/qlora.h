@@ -364,8 +364,9 @@ int lora_linear_dx(const uint16_t* dY, int64_t M, int64_t K, int64_t N, const ui
  * layer. 0 <= p < 1 (QL_ERR_VALUE otherwise; p = 0 is no dropout).
  *
  * lora_dropout: Y = D o X, elementwise, for X [rows, cols] with rows `ld` elements
- * apart (fp32 or bf16 per x_dtype; rounded once to that type), Y dense. D o is
- * its own transpose: the same call is its backward.                             */
+ * apart (fp32 or bf16 per x_dtype; rounded once to that type), Y dense; Y may be
+ * X itself if that is dense too. D o is its own transpose: the same call is its
+ * backward.                                                                       */
 int lora_dropout(const void* X, int x_dtype, int64_t rows, int64_t cols, int64_t ld, double p, uint64_t seed,
                  uint64_t offset, void* Y, void* stream);
 
