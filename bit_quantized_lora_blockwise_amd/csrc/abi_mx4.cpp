@@ -31,9 +31,13 @@ bool layer_ok(int64_t M, int64_t K, int64_t N, int r) {
 struct Ws {
   size_t codes, scales, low, dense, t, part, total;
 };
-Ws fwd_ws(int64_t M, int64_t K, int r) {
+// The slices of T = (D o X) L1 of the microscaled layer; of G with K and N exchanged.
+size_t slices_ws(int64_t M, int64_t K, int64_t N, int r) {
+  return mx4_small_ok(M, N, K, r) ? mx4_small_ws(M, r) : lora_skinny_ws(M, K, r);
+}
+Ws fwd_ws(int64_t M, int64_t K, int64_t N, int r) {
   Ws w{round_up(mx4::code_bytes(M, K)), round_up(mx4::scale_bytes(M, K)), round_up((size_t)M * r * 2), 0, 0,
-       round_up(std::max(lora_skinny_ws(M, K, r), mx4_small_ws(M, r))), 0};
+       round_up(slices_ws(M, K, N, r)), 0};
   w.total = w.codes + w.scales + w.low + w.part;
   return w;
 }
@@ -45,13 +49,16 @@ bool few_ok(int64_t M, int64_t K, int64_t N, int r) {
   return (M + 15) / 16 * ((r + 15) / 16) <= 24 && layer_ok(M, K, N, r);
 }
 
-// packed = false: the backward over another base, which multiplies the bf16 gradient
+// packed = false: the backward over another base, which multiplies the bf16 gradient; its
+// slices are counted for every p
 Ws bwd_ws(int64_t M, int64_t K, int64_t N, int r, bool packed) {
   Ws w{packed ? round_up(mx4::code_bytes(M, N)) : 0, packed ? round_up(mx4::scale_bytes(M, N)) : 0,
        round_up((size_t)3 * M * g_pitch(r) * 2), r == g_pitch(r) ? 0 : round_up((size_t)M * r * 2),
        round_up((size_t)M * r * 2), 0, 0};
-  w.part = round_up(std::max({lora_skinny_ws(M, N, r), lora_skinny_ws(M, K, r), lora_grads3_ws(M, K, N, r),
-                              packed || few_ok(M, K, N, r) ? mx4_small_ws(M, r) : 0}));
+  const size_t slices = packed ? std::max(slices_ws(M, K, N, r), slices_ws(M, N, K, r))
+                               : std::max({lora_skinny_ws(M, N, r), lora_skinny_ws(M, K, r),
+                                           few_ok(M, K, N, r) ? mx4_small_ws(M, r) : 0});
+  w.part = round_up(std::max(slices, lora_grads3_ws(M, K, N, r)));
   w.total = w.codes + w.scales + w.low + w.dense + w.t + w.part;
   return w;
 }
@@ -112,7 +119,7 @@ int lora_dropout(const void* X, int x_dtype, int64_t rows, int64_t cols, int64_t
 }
 
 size_t mx4_linear_fwd_workspace(int64_t M, int64_t K, int64_t N, int r) {
-  return layer_ok(M, K, N, r) ? fwd_ws(M, K, r).total : 0;
+  return layer_ok(M, K, N, r) ? fwd_ws(M, K, N, r).total : 0;
 }
 
 int mx4_linear_fwd(const uint16_t* X, int64_t M, int64_t K, int64_t N, const uint8_t* codes, const uint8_t* scales,
@@ -123,7 +130,7 @@ int mx4_linear_fwd(const uint16_t* X, int64_t M, int64_t K, int64_t N, const uin
   drop::Params d;
   if (!drop_params(p, seed, offset, d)) return QL_ERR_VALUE;
   if (!aligned16(X, codes, scales, L1, L2, Y, T_out)) return QL_ERR_ALIGN;
-  const Ws w = fwd_ws(M, K, r);
+  const Ws w = fwd_ws(M, K, N, r);
   if (!workspace || ws_bytes < w.total) return QL_ERR_WORKSPACE;
   if (!aligned16(workspace)) return QL_ERR_ALIGN;
   hipStream_t s = (hipStream_t)stream;
