@@ -41,24 +41,26 @@ struct Tile {
 };
 
 // How a tile is read: in aligned 16-byte pieces (ld and cols multiples of 8, base 16-byte
-// aligned), in pieces at any element (rows of at least eight), element by element, or
-// that by 64-bit address (matrices past the 2^31 bytes that a buffer offset reaches).
-// Each operand by its own rows: a rank below 8 leaves the activation in pieces (with both
-// by elements, T of 4096 x 11008 at rank 1 took 58 us, with the activation in pieces 24).
-enum Load { kPieces, kAnywhere, kElements, kFar };
+// aligned), in pieces at any element (rows of at least eight), as the piece that begins
+// with the row and goes on into the next ones (dense rows of fewer than eight, eight
+// elements in all or more), element by element, or that by 64-bit address (matrices past
+// the 2^31 bytes that a buffer offset reaches).  Each operand by its own rows: T of 4096 x
+// 11008 at rank 1 took 58 us with both by elements, 24 so.
+enum Load { kPieces, kAnywhere, kShort, kElements, kFar };
 
 // Tile of a matrix with `ld` elements per row, its first row at `base`, its first column
 // c0; rows at or past `rows` and columns at or past `cols` read as zero.  Each thread
 // issues two 16-byte buffer loads (or sixteen of one element), with no branch, so that
 // the loads of later steps stay in flight.  kAnywhere: a piece that crosses the row's end
-// is read as the last eight of the row and moved into place by fit_tile.  `bytes`: extent
-// of the matrix from `base`.
+// is read as the last eight of the row and moved into place by fit_tile.  kShort: likewise
+// with the last eight of the matrix; `lead` elements of it, eight if there are as many, lie
+// before `base`.  `bytes`: extent of the matrix from `base`.
 template <Load kHow>
 __device__ __forceinline__ Tile load_tile(const uint16_t* base, int64_t c0, int64_t ld, int64_t rows, int64_t cols,
-                                          uint64_t bytes) {
+                                          uint64_t bytes, int lead = 0) {
   const int t = threadIdx.x;
   const int64_t cc = c0 + (t & 7) * 8;
-  const __amdgpu_buffer_rsrc_t rs = rsrc(base, bytes);
+  const __amdgpu_buffer_rsrc_t rs = kHow == kShort ? rsrc(base - lead, bytes + 2 * lead) : rsrc(base, bytes);
   Tile tl;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -68,6 +70,9 @@ __device__ __forceinline__ Tile load_tile(const uint16_t* base, int64_t c0, int6
 #pragma unroll
       for (int j = 0; j < 8; ++j) e[j] = row < rows && cc + j < cols ? base[row * ld + cc + j] : 0;
       tl.v[i] = u32x4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
+    } else if constexpr (kHow == kShort) {
+      const int64_t at = lead + min(row * ld, (int64_t)(bytes / 2) - 8);
+      tl.v[i] = __builtin_amdgcn_raw_buffer_load_b128(rs, row < rows && cc < cols ? (uint32_t)(at * 2) : kOOB, 0, 0);
     } else if constexpr (kHow != kElements) {
       const int64_t at = row * ld + (kHow == kPieces ? cc : min(cc, cols - 8));
       tl.v[i] = __builtin_amdgcn_raw_buffer_load_b128(rs, row < rows && cc < cols ? (uint32_t)(at * 2) : kOOB, 0, 0);
@@ -83,13 +88,23 @@ __device__ __forceinline__ Tile load_tile(const uint16_t* base, int64_t c0, int6
   return tl;
 }
 
+// total (kShort): elements of the matrix from the tile's first on.
 template <Load kHow>
-__device__ __forceinline__ void fit_tile(Tile& tl, int64_t c0, int64_t cols) {
+__device__ __forceinline__ void fit_tile(Tile& tl, int64_t c0, int64_t cols, int64_t total = 0) {
   if constexpr (kHow == kAnywhere) {
     const int64_t over = c0 + (threadIdx.x & 7) * 8 + 8 - cols;
     const int s = (int)max((int64_t)0, min((int64_t)8, over));
 #pragma unroll
     for (int i = 0; i < 2; ++i) tl.v[i] = qk::drop_front8(tl.v[i], s);
+  }
+  if constexpr (kHow == kShort) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int64_t over = ((threadIdx.x >> 3) + 32 * i) * cols + 8 - total;
+      tl.v[i] = qk::drop_front8(tl.v[i], (int)max((int64_t)0, min((int64_t)8, over)));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) tl.v[i][j] &= cols > 2 * j + 1 ? 0xFFFFFFFFu : cols > 2 * j ? 0xFFFFu : 0u;
+    }
   }
 }
 
@@ -130,13 +145,13 @@ __global__ __launch_bounds__(kThreads) void k_lora_skinny(const uint16_t* __rest
     const int64_t k0c = kl > 0 ? k0 : 0;
     const int64_t ke = kl > 0 ? k_end : 0;             // past the slice: no columns
     ta = load_tile<kA>(A + m0 * lda, k0c, lda, M - m0, ke, (uint64_t)((M - m0) * lda) * 2);
-    if (kBkr) tb = load_tile<kB>(Bm + k0c * r, 0, r, kl, r, (uint64_t)((R - k0c) * r) * 2);
+    if (kBkr) tb = load_tile<kB>(Bm + k0c * r, 0, r, kl, r, (uint64_t)((R - k0c) * r) * 2, (int)min((int64_t)8, k0c * r));
     else tb = load_tile<kB>(Bm, k0c, R, r, ke, (uint64_t)(r * R) * 2);
   };
   auto store = [&](int64_t st, Tile& ta, Tile& tb) {
     const int64_t k0 = k_beg + st * kTile;
     fit_tile<kA>(ta, k0, k_end);
-    if (kBkr) fit_tile<kB>(tb, 0, r);
+    if (kBkr) fit_tile<kB>(tb, 0, r, (R - (k0 < k_end ? k0 : 0)) * r);
     else fit_tile<kB>(tb, k0, k_end);
     if constexpr (kDrop) drop_tile(ta, d, m0, k0);
     store_tile(ta, (LDS_AS uint16_t*)As[st & 1]);
@@ -472,7 +487,8 @@ __device__ __forceinline__ void tn_tile(const uint16_t* __restrict__ A, int64_t 
     ta = load_tile<kA>(A + mmc * lda, p0, lda, ml, P, (uint64_t)((M - mmc) * lda) * 2);   // [m][p]
 #pragma unroll
     for (int j = 0; j < kPlanes; ++j)
-      tb.p[j] = load_tile<kB>(B + (j * M + mmc) * ldb, 0, ldb, ml, r, (uint64_t)((M - mmc) * ldb) * 2);   // [m][c]
+      tb.p[j] = load_tile<kB>(B + (j * M + mmc) * ldb, 0, ldb, ml, r, (uint64_t)((M - mmc) * ldb) * 2,
+                              (int)min((int64_t)8, mmc * ldb));   // [m][c]
   };
   auto store = [&](int64_t st, Tile& ta, BTiles& tb) {
     fit_tile<kA>(ta, p0, P);
@@ -480,7 +496,8 @@ __device__ __forceinline__ void tn_tile(const uint16_t* __restrict__ A, int64_t 
     store_tile(ta, abuf(st));
 #pragma unroll
     for (int j = 0; j < kPlanes; ++j) {
-      fit_tile<kB>(tb.p[j], 0, r);
+      const int64_t mm = m_beg + st * kTile;
+      fit_tile<kB>(tb.p[j], 0, r, (M - (mm < m_end ? mm : 0)) * ldb);
       store_tile(tb.p[j], bbuf(st, j));
     }
   };
@@ -782,10 +799,10 @@ hipError_t launch_lora_skinny(const uint16_t* A, int64_t M, int64_t R, int64_t l
   if (b_is_kr) {
     if (R < 8) QL_SKINNY(true, kElements, kElements);
     else if (avec && bvec) QL_SKINNY(true, kPieces, kPieces);
-    else if (avec && r < 8) QL_SKINNY(true, kPieces, kElements);
+    else if (avec && r < 8) QL_SKINNY(true, kPieces, kShort);
     else if (avec) QL_SKINNY(true, kPieces, kAnywhere);
     else if (bvec) QL_SKINNY(true, kAnywhere, kPieces);
-    else if (r < 8) QL_SKINNY(true, kAnywhere, kElements);
+    else if (r < 8) QL_SKINNY(true, kAnywhere, kShort);
     else QL_SKINNY(true, kAnywhere, kAnywhere);
   } else {
     if (past_2_31(r, R)) QL_SKINNY(false, kAnywhere, kFar);
@@ -848,12 +865,12 @@ hipError_t launch_lora_tn(const uint16_t* A, int64_t lda, const uint16_t* B, int
   const bool bvec = (r % 8) == 0 && ((uintptr_t)B & 15) == 0;
 #define QL_TN(VA, VB) \
   hipLaunchKernelGGL((k_lora_tn<VA, VB>), grid, dim3(kThreads), 0, s, A, lda, B, M, P, r, sp.chunk, ws)
-  if (P < 8) QL_TN(kElements, kElements);
+  if (P < 8 || M * r < 8) QL_TN(kElements, kElements);
   else if (avec && bvec) QL_TN(kPieces, kPieces);
-  else if (avec && r < 8) QL_TN(kPieces, kElements);
+  else if (avec && r < 8) QL_TN(kPieces, kShort);
   else if (avec) QL_TN(kPieces, kAnywhere);
   else if (bvec) QL_TN(kAnywhere, kPieces);
-  else if (r < 8) QL_TN(kAnywhere, kElements);
+  else if (r < 8) QL_TN(kAnywhere, kShort);
   else QL_TN(kAnywhere, kAnywhere);
 #undef QL_TN
   hipError_t e = hipGetLastError();
@@ -925,14 +942,14 @@ static hipError_t low_pass(const uint16_t* A, int64_t M, int64_t R, const uint16
     else QL_LOW(false, kAnywhere, kAnywhere, false);
   } else if (d.cut) {
     if (R < 8) QL_LOW(true, kElements, kElements, true);
-    else if (r < 8 && vec) QL_LOW(true, kPieces, kElements, true);
-    else if (r < 8) QL_LOW(true, kAnywhere, kElements, true);
+    else if (r < 8 && vec) QL_LOW(true, kPieces, kShort, true);
+    else if (r < 8) QL_LOW(true, kAnywhere, kShort, true);
     else if (vec) QL_LOW(true, kPieces, kAnywhere, true);
     else QL_LOW(true, kAnywhere, kAnywhere, true);
   } else {
     if (R < 8) QL_LOW(true, kElements, kElements, false);
-    else if (r < 8 && vec) QL_LOW(true, kPieces, kElements, false);
-    else if (r < 8) QL_LOW(true, kAnywhere, kElements, false);
+    else if (r < 8 && vec) QL_LOW(true, kPieces, kShort, false);
+    else if (r < 8) QL_LOW(true, kAnywhere, kShort, false);
     else if (vec) QL_LOW(true, kPieces, kAnywhere, false);
     else QL_LOW(true, kAnywhere, kAnywhere, false);
   }
@@ -981,11 +998,11 @@ hipError_t launch_lora_grads3(const uint16_t* X, int64_t K, const uint16_t* G, c
       hipLaunchKernelGGL((k_lora_tn_pair3<V, T, false>), dim3(nwg), dim3(kThreads), 0, s, j0, j1, M, r, g_pitch(r), d, \
                          s0, s1, whole);                                                                            \
   } while (0)
-  if (K < 8 || N < 8) QL_TN3(kElements, kElements);
+  if (K < 8 || N < 8 || M * r < 8) QL_TN3(kElements, kElements);
   else if (vec && vect) QL_TN3(kPieces, kPieces);
-  else if (vec && r < 8) QL_TN3(kPieces, kElements);
+  else if (vec && r < 8) QL_TN3(kPieces, kShort);
   else if (vec) QL_TN3(kPieces, kAnywhere);
-  else if (r < 8) QL_TN3(kAnywhere, kElements);
+  else if (r < 8) QL_TN3(kAnywhere, kShort);
   else if (vect) QL_TN3(kAnywhere, kPieces);
   else QL_TN3(kAnywhere, kAnywhere);
 #undef QL_TN3
