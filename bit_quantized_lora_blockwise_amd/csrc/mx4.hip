@@ -117,8 +117,9 @@ __global__ __launch_bounds__(kThreads) void k_mx4_quant_t(const void* __restrict
                                                           uint32_t* __restrict__ scales) {
   __shared__ uint8_t sbytes[128][4];
   const int l = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  const int64_t ctiles = (cols + 127) / 128;
-  const int64_t ct = blockIdx.x % ctiles, word = blockIdx.x / ctiles;
+  const int64_t ctiles = (cols + 127) / 128, wg = blockIdx.x + (int64_t)gridDim.x * blockIdx.y;
+  const int64_t ct = wg % ctiles, word = wg / ctiles;
+  if (word >= (len + 127) / 128) return;
   const int64_t c0 = 128 * ct + 2 * l, r0 = 128 * word + 32 * wv;
   typedef uint32_t u32_a2 __attribute__((aligned(2)));
   typedef float f32x2_a4 __attribute__((ext_vector_type(2), aligned(4)));
@@ -235,7 +236,9 @@ hipError_t launch_mx4_quant(const void* X, bool bf16, int64_t rows, int64_t cols
 
 hipError_t launch_mx4_quant_t(const void* X, bool bf16, int64_t len, int64_t cols, int64_t ld, uint8_t* codes,
                               uint8_t* scales, hipStream_t s) {
-  const dim3 grid((unsigned)((cols + 127) / 128 * (padded(len) / kPad)));
+  // a launch has fewer than 2^32 threads along x
+  const int64_t groups = (cols + 127) / 128 * (padded(len) / kPad), gx = groups < (1 << 22) ? groups : 1 << 22;
+  const dim3 grid((unsigned)gx, (unsigned)((groups + gx - 1) / gx));
   const bool past = len * cols * (bf16 ? 2 : 4) > qk::kStreamBytes;
 #define QL_MQ(B, O, P)                                                                                           \
   hipLaunchKernelGGL((k_mx4_quant_t<B, O, P>), grid, dim3(kThreads), 0, s, X, len, cols, ld, (u32x4*)codes,      \
