@@ -335,7 +335,10 @@ hipError_t launch_fwd_small(const uint16_t* X, int64_t M, int64_t K, int64_t N, 
 // 8192 -> 22016 139 / 438, 512 -> 512 13 / 41; 128 rows 11008 -> 4096 85 / 112 (688 work groups),
 // 8192 -> 22016 260 / 445 (512); 512 rows 4096 -> 4096 105 / 117 (1024); 256 rows 8192 -> 22016
 // 489 / 446 (1024), 11008 -> 4096 159 / 116 (1376).
-bool dx_small_ok(int64_t M, int64_t K) { return M <= 64 || (K / kP) * ((M + 31) / 32) <= 768; }
+// From 2^29 columns on its launch would have 2^32 threads along x or more, which wrap.
+bool dx_small_ok(int64_t M, int64_t K) {
+  return (M <= 64 && K < (int64_t(1) << 29)) || (K / kP) * ((M + 31) / 32) <= 768;
+}
 
 hipError_t launch_dx_small(const uint16_t* dY, int64_t M, int64_t K, int64_t N, const uint8_t* codes, const uint8_t* c2,
                            const float* c1, const uint16_t* G, const float* Gp, int S, uint16_t* planes,

@@ -181,3 +181,31 @@ def test_l2_past_2_32_bytes(call, N):
     within(dL1, x.T @ G, (M + 4) * U * (np.abs(x).T @ np.abs(G)) + np.abs(x).T @ errG, "dL1")
     t = f64(T)
     within(dL2[:, at], s * t.T @ dy, (M + 4) * U * s * (np.abs(t).T @ np.abs(dy)), "dL2")
+
+
+@pytest.mark.parametrize("K", [2**29 - 64, 2**29 + 128])
+def test_one_row_of_2_29_columns(K):
+    """One row over NF4, on both sides of the few-rows kernel's longest launch."""
+    q = qlib()
+    M, N, r, s, p, seed, off = 1, 3, 2, 1.5, 0.3, 5, 6
+    rng = np.random.default_rng(9)
+    X = torch.empty((M, K), dtype=BF, device=DEV).normal_()
+    L1 = torch.empty((K, r), dtype=BF, device=DEV).normal_()
+    W = torch.empty((N, K), dtype=BF, device=DEV).normal_(0, 0.05)
+    dY, T, L2 = (dev(rng.standard_normal(shape)) for shape in ((M, N), (M, r), (r, N)))
+    codes, absmax = q.nf4_quantize(W)
+    base = (codes, *q.nf4_double_quant(absmax))
+    Wq = q.nf4_dequantize(*base, N, K)
+    dX, dL1, _ = q.qlora_linear_bwd_dropout(X, dY, *base, L1, L2, s, p=p, seed=seed, offset=off, T=T)
+    dy, l2 = f64(dY), f64(L2)
+    G = s * dy @ l2.T
+    errG = (N + 4) * U * s * (np.abs(dy) @ np.abs(l2).T)
+    for k in (0, 2**27 - 64, 2**28 + 64, K - 128):
+        c = slice(k, k + 128)
+        D = mask_at(np.arange(M), np.arange(k, k + 128), p, seed, off)
+        x, l1, w = f64(X[:, c]), f64(L1[c]), f64(Wq[:, c])
+        ref = dy @ w + D * (G @ l1.T)
+        tol = 2.0**-8 * np.abs(ref) + (N + 4) * U * (np.abs(dy) @ np.abs(w))
+        tol += D * (((2.0**-8 + 70 * U) * np.abs(G) + errG) @ np.abs(l1).T)
+        within(dX[:, c], ref, tol, f"dX {k}")
+        within(dL1[c], (x * D).T @ G, (M + 4) * U * (np.abs(x * D).T @ np.abs(G)) + np.abs(x * D).T @ errG, f"dL1 {k}")
