@@ -106,12 +106,15 @@ BwdWs bwd_ws(int64_t M, int64_t K, int64_t N, int r) {
   return w;
 }
 
-// Forward product for M > 16: the large-tile kernel, which takes every shape
+// Rows that the decode kernels take: up to 16, of a layer whose L2 their 32-bit offsets reach.
+bool decode_ok(int64_t M, int64_t N, int r) { return M <= 16 && N * r * 2 < (int64_t(1) << 31); }
+
+// Forward product for the other rows: the large-tile kernel, which takes every shape
 // shapes_ok accepts (K % 64 == 0 makes its rows 16-byte aligned).
 hipError_t run_fwd_gemm(const uint16_t* X, int64_t M, int64_t K, int64_t N, const uint8_t* codes, const uint8_t* c2,
                         const float* c1, const uint16_t* T, const uint16_t* L2, int r, float scale, uint16_t* Y,
                         hipStream_t s) {
-  if (!qgemm_big_ok(false, M, K, N)) return hipErrorInvalidValue;
+  if (!qgemm_big_ok(false, std::max<int64_t>(M, 17), K, N)) return hipErrorInvalidValue;
   return launch_qgemm_big(false, X, M, K, N, codes, c2, c1, T, L2, r, scale, Y, s);
 }
 
@@ -158,7 +161,7 @@ bool group_ok(int64_t M, int64_t K, int64_t N, int G, int r) {
 // adapters and one decode launch over the stacked rows; X must fit the decode
 // kernel's LDS (M K <= 16384) and r be a multiple of 4.
 bool group_decode_ok(int64_t M, int64_t K, int64_t N, int G, int r) {
-  return G > 1 && G <= 16 && M >= 1 && M <= 16 && N > 0 && N % 256 == 0 && N <= (int64_t(1) << 31) / G &&
+  return G > 1 && G <= 16 && M >= 1 && decode_ok(M, N, r) && N > 0 && N % 256 == 0 && N <= (int64_t(1) << 31) / G &&
          shapes_ok(M, K, N * G, r) && (r % 4) == 0 && qgemv_group_ok(M, K, N, G);
 }
 
@@ -424,7 +427,7 @@ int qlora_linear_fwd(const uint16_t* X, int64_t M, int64_t K, int64_t N, const u
   char* ws = (char*)workspace;
   uint16_t* T = T_out ? T_out : (uint16_t*)ws;
   float* part = (float*)(ws + w.t_bytes);
-  if (qgemv_fused_ok(M, K, r) && decode_t_ok(M, K, X, L1) && !capturing(s)) {
+  if (decode_ok(M, N, r) && qgemv_fused_ok(M, K, r) && decode_t_ok(M, K, X, L1) && !capturing(s)) {
     // decode, small X: the slices of T = X L1 formed, added and rounded in the decode launch itself
     // (not under graph capture: a replay would reuse this call's epoch and could take an earlier
     // replay's T; the two launches below are safe to replay)
@@ -433,7 +436,7 @@ int qlora_linear_fwd(const uint16_t* X, int64_t M, int64_t K, int64_t N, const u
                                   T_out, L2, lora_scale, Y, s));
     return QL_OK;
   }
-  if (M <= 16 && (r % 4) == 0 && decode_t_ok(M, K, X, L1)) {
+  if (decode_ok(M, N, r) && (r % 4) == 0 && decode_t_ok(M, K, X, L1)) {
     // decode: the slices of T = X L1, added and rounded inside the decode kernel
     QL_TRY(launch_lora_part(X, M, K, L1, r, part, s));
     QL_TRY(launch_qgemv_fwd_tpart(X, M, K, N, codes, c2, c1, part, decode_t_slices(K), T_out, L2, r, lora_scale, Y,
@@ -441,7 +444,7 @@ int qlora_linear_fwd(const uint16_t* X, int64_t M, int64_t K, int64_t N, const u
     return QL_OK;
   }
   QL_TRY(launch_lora_skinny(X, M, K, K, L1, true, r, 1.0f, T, part, s));
-  if (M <= 16)
+  if (decode_ok(M, N, r))
     QL_TRY(launch_qgemv_fwd(X, M, K, N, codes, c2, c1, T, L2, r, lora_scale, Y, s));
   else
     QL_TRY(run_fwd_gemm(X, M, K, N, codes, c2, c1, T, L2, r, lora_scale, Y, s));
@@ -515,7 +518,7 @@ int qlora_linear_fwd_t(const uint16_t* X, int64_t M, int64_t K, int64_t N, const
       !aligned16(L2) || !aligned16(Y))
     return QL_ERR_ALIGN;
   hipStream_t s = (hipStream_t)stream;
-  if (M <= 16)
+  if (decode_ok(M, N, r))
     QL_TRY(launch_qgemv_fwd(X, M, K, N, codes, c2, c1, T, L2, r, lora_scale, Y, s));
   else
     QL_TRY(run_fwd_gemm(X, M, K, N, codes, c2, c1, T, L2, r, lora_scale, Y, s));

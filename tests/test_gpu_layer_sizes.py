@@ -209,3 +209,37 @@ def test_one_row_of_2_29_columns(K):
         tol += D * (((2.0**-8 + 70 * U) * np.abs(G) + errG) @ np.abs(l1).T)
         within(dX[:, c], ref, tol, f"dX {k}")
         within(dL1[c], (x * D).T @ G, (M + 4) * U * (np.abs(x * D).T @ np.abs(G)) + np.abs(x * D).T @ errG, f"dL1 {k}")
+
+
+@pytest.mark.parametrize("M", [3, 20])
+@pytest.mark.parametrize("call", ["linear", "linear_t", "linear_dropout"])
+def test_forward_of_l2_past_2_32_bytes(call, M):
+    """Few rows to more than 2^25 columns: Y in blocks of columns all along the matrix."""
+    q = qlib()
+    K, N, r, s = 64, 2**25 + 8, 64, 0.5
+    rng = np.random.default_rng(10)
+    print(f"[{call} M={M} N={N}]", flush=True)
+    L2 = torch.empty((r, N), dtype=BF, device=DEV).normal_()
+    W = torch.empty((N, K), dtype=BF, device=DEV).normal_(0, 0.05)
+    X, L1 = dev(rng.standard_normal((M, K))), dev(rng.standard_normal((K, r)) * 0.1)
+    codes, absmax = q.nf4_quantize(W)
+    base = (codes, *q.nf4_double_quant(absmax))
+    Wq = q.nf4_dequantize(*base, N, K)
+    x = f64(X)
+    if call == "linear_dropout":
+        Y, T = q.qlora_linear_fwd_dropout(X, *base, N, L1, L2, s, T_out=True, p=0.1, seed=1, offset=2)
+    elif call == "linear":
+        Y, T = q.qlora_linear_fwd(X, *base, N, L1, L2, s, T_out=True)
+    else:
+        T = q.qlora_lora_down(X, L1)
+        Y = q.qlora_linear_fwd_t(X, *base, N, T, L2, s)
+    D = mask_at(np.arange(M), np.arange(K), 0.1, 1, 2) if call == "linear_dropout" else np.ones((M, K))
+    rT = (x * D) @ f64(L1)
+    within(T, rT, 2.0**-8 * np.abs(rT) + (K + 4) * U * (np.abs(x * D) @ np.abs(f64(L1))), "T")
+    t = f64(T)
+    for n in (0, 2**22 + 16, 2**23, 2**24 - 64, 2**24 + 2**23, N - 128):
+        c = slice(n, n + 128)
+        w, l2 = f64(Wq[c]), f64(L2[:, c])
+        ref = x @ w.T + s * (t @ l2)
+        tol = 2.0**-8 * np.abs(ref) + (K + 4) * U * (np.abs(x) @ np.abs(w).T) + 70 * U * s * (np.abs(t) @ np.abs(l2))
+        within(Y[:, c], ref, tol, f"Y {n}")
