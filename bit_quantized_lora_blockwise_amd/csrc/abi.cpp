@@ -630,8 +630,8 @@ const char* ql_status_string(int status) {
     case QL_OK: return "ok";
     case QL_ERR_NULL: return "a required pointer is NULL";
     case QL_ERR_SHAPE:
-      return "invalid shape (sizes must be > 0, K and cols multiples of 64, 1 <= r <= 64, each activation "
-             "matrix and the packed codes below 2^31 bytes)";
+      return "invalid shape (sizes must be > 0, K and cols multiples of 64 in the calls over 64-element blocks, "
+             "1 <= r <= 64, each activation matrix and the packed codes below 2^31 bytes)";
     case QL_ERR_DTYPE: return "unsupported dtype, code book or scale code";
     case QL_ERR_VALUE: return "hyper-parameter out of range";
     case QL_ERR_ALIGN: return "device pointers must be 16-byte aligned";

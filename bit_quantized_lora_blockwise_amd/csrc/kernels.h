@@ -92,7 +92,10 @@ hipError_t launch_lora_tn_pair(const uint16_t* A0, int64_t lda0, const uint16_t*
 hipError_t launch_lora_tn(const uint16_t* A, int64_t lda, const uint16_t* B, int64_t M, int64_t P, int r,
                           float scale, bool transpose_out, float* out, float* ws, hipStream_t s);
 
-// The adapter branch with dropout on its input (d.cut = 0: none) and G to 24 bits:
+// The adapter branch with dropout on its input (d.cut = 0: none) and G to 24 bits.  T and G enter
+// their second products as bf16, which is what the matrix instruction takes, what the older layers
+// do and, for T, what the backward is given: it costs Y 2^-9 |T| |L2| and dX 2^-9 |G| |L1|, where
+// the result's own rounding costs 2^-9 of it.  dL1 is fp32 and has all of G:
 //   T = bf16((D o X) L1); ws as lora_skinny_ws(M, K, r).  With `codes`, the same pass
 //     also packs X (not D o X) in microscaled 4-bit; G and dY likewise
 //   G = scale dY L2^T; ws as lora_skinny_ws(M, N, r)
@@ -153,14 +156,14 @@ hipError_t launch_mx4_small_dx(const uint16_t* dY, int64_t M, int64_t K, int64_t
                                const uint16_t* L1, const uint16_t* L2, int r, float scale, const drop::Params& d,
                                uint16_t* dX, uint16_t* G, uint8_t* ac, uint8_t* as, float* part, hipStream_t s);
 // The forward's T and the backward's G alone (same bits).
-// fp32 slices (part: mx4_small_ws bytes) of scale (D o A) B (L1, b_is_kr) or scale A B^T (L2), to be
-// added in order.
-hipError_t launch_small_slices(const uint16_t* A, int64_t M, int64_t R, const uint16_t* B, bool b_is_kr, int r,
-                               const drop::Params& d, float scale, float* part, int* slices, hipStream_t s);
 hipError_t launch_mx4_small_t(const uint16_t* X, int64_t M, int64_t K, const uint16_t* L1, int r, const drop::Params& d,
                               uint16_t* T, float* part, hipStream_t s);
 hipError_t launch_mx4_small_g(const uint16_t* dY, int64_t M, int64_t N, const uint16_t* L2, int r, float scale,
                               uint16_t* G, float* part, hipStream_t s);
+// fp32 slices (part: mx4_small_ws bytes) of scale (D o A) B (L1, b_is_kr) or scale A B^T (L2), to be
+// added in order.
+hipError_t launch_small_slices(const uint16_t* A, int64_t M, int64_t R, const uint16_t* B, bool b_is_kr, int r,
+                               const drop::Params& d, float scale, float* part, int* slices, hipStream_t s);
 
 // --- adapter merge (merge.hip) ---------------------------------------------
 // W[n][k] = bf16(W'[n][k] + scale * sum_c L1[k][c] L2[c][n]), W' the bf16
@@ -229,14 +232,15 @@ hipError_t launch_bgemm_big(bool dx, const uint16_t* A, int64_t M, int64_t K, in
 hipError_t launch_qgemm_dx(const uint16_t* dY, int64_t M, int64_t K, int64_t N, const uint8_t* codes,
                            const uint8_t* c2, const float* c1, const uint16_t* G, const uint16_t* L1, int r,
                            uint16_t* dX, hipStream_t s, const drop::Params* d = nullptr);
-// The same with dropout for few rows (gemm_small.hip): dX = bf16(dY W' + D o (G L1^T))
+// The NF4 layer with dropout for few rows (gemm_small.hip).  Forward: Y = bf16(X W'^T + scale (T L2))
+// from T, or with T = nullptr from its slices Tp (S of them), added here; T_out then receives it.
 bool fwd_small_ok(int64_t M, int64_t N);
-// T, or with T = nullptr its slices Tp (S of them), added here; T_out then receives it.
 hipError_t launch_fwd_small(const uint16_t* X, int64_t M, int64_t K, int64_t N, const uint8_t* codes, const uint8_t* c2,
                             const float* c1, const uint16_t* T, const float* Tp, int S, uint16_t* T_out,
                             const uint16_t* L2, int r, float scale, uint16_t* Y, hipStream_t s);
+// dX = bf16(dY W' + D o (G L1^T)) from G, or with G = nullptr from its slices Gp (S of them), added
+// here; `planes` then receives it to 24 bits.
 bool dx_small_ok(int64_t M, int64_t K);
-// G, or with G = nullptr its slices Gp (S of them), added here; `planes` then receives it to 24 bits.
 hipError_t launch_dx_small(const uint16_t* dY, int64_t M, int64_t K, int64_t N, const uint8_t* codes, const uint8_t* c2,
                            const float* c1, const uint16_t* G, const float* Gp, int S, uint16_t* planes,
                            const uint16_t* L1, int r, uint16_t* dX, const drop::Params& d, hipStream_t s);

@@ -569,7 +569,7 @@ __global__ __launch_bounds__(kThreads) void k_lora_tn_pair(TnJob j0, TnJob j1, i
 // The pair with dropout on the first product's A and its B in three planes of pitch
 // rp.  With one slice each, j0.part and j1.part are the results: scaled, the second
 // transposed.  For what lora_grads.hip does not take (few rows, or sizes that are no
-// multiples of 8): 130 rows of 520 and 333 columns, rank 5, 8.6 us; 4093 rows of 4097 and
+// multiples of 8): 130 rows of 520 and 333 columns, rank 5, 7.4 us; 4093 rows of 4097 and
 // 11007, rank 37, 48 us (2.6 TB/s).
 template <Load kA, Load kT, bool kDrop>
 __global__ __launch_bounds__(kThreads) void k_lora_tn_pair3(TnJob j0, TnJob j1, int64_t M, int r, int rp,

@@ -365,12 +365,12 @@ __global__ __launch_bounds__(64 * kWM * kWP) void k_mx4_gemm(const uint8_t* __re
 // during the reduction, a Philox round between two products: the vector unit is
 // free while the other wave's product runs, where a draw before the loop took 8 us
 // a tile.
-// Bound: the matrix unit under the chip's power limit.  A step of 128 takes 0.85 us on
-// random data (5.0 PFLOP/s; 0.51 us on zeros, and 6.7 PFLOP/s is what the products alone
-// reach on random data); the clock is then about 1.85 GHz and the matrix unit busy half of
-// its cycles (counters at 2048 x 8192 x 22016: 190 us, 3.9 PFLOP/s, with the last
-// of 2.7 rounds of tiles and 10 us of launch, first loads and last stores; no LDS bank
-// conflicts).  4096 x 11008 x 4096 backward with dropout 115 us.  A P that is no multiple
+// Bound: the matrix unit under the chip's power limit.  A step of 128 of one round of 256
+// tiles takes 0.82 to 0.88 us on random data (5.2 to 4.9 PFLOP/s; 0.48 to 0.52 us on zeros,
+// and 6.7 PFLOP/s is what the products alone reach on random data); the clock is then about
+// 1.85 GHz and the matrix unit busy half of its cycles (2048 x 8192 x 22016 with the adapter:
+// 189 to 206 us, on zeros 139 to 144, the last of 2.7 rounds of tiles and 10 us of launch,
+// first loads and last stores among them; no LDS bank conflicts).  4096 x 11008 x 4096 backward with dropout 115 us.  A P that is no multiple
 // of 8 costs in the stores: 4093 x 4097 -> 11007 157 us, -> 11008 120 us.
 constexpr int kRT = 512;                    // threads
 constexpr int kRB = 256;                    // tile edge

@@ -378,7 +378,8 @@ int lora_dropout(const void* X, int x_dtype, int64_t rows, int64_t cols, int64_t
  * Sizes, layouts and errors as qlora_linear_fwd and qlora_linear_bwd, each with a
  * workspace query of its own. G is kept to 24 bits for dL1 (and rounded to bf16 for dX
  * alone), so dL1 is nearer the formula than qlora_linear_bwd's, which rounds G.
- * T is the forward's T_out; when NULL it is formed again with the same mask.
+ * T is the forward's T_out; when NULL it is formed again with the same mask. Y is
+ * formed from T as rounded, so that it is the Y that the backward differentiates.
  * With p = 0 the forward is qlora_linear_fwd.                                    */
 size_t qlora_linear_fwd_dropout_workspace(int64_t M, int64_t K, int64_t N, int r);
 int qlora_linear_fwd_dropout(const uint16_t* X, int64_t M, int64_t K, int64_t N,
@@ -410,7 +411,8 @@ int qlora_linear_bwd_dropout(const uint16_t* X, const uint16_t* dY, int64_t M, i
  * mx4_quantize: X [rows, cols] (fp32 or bf16 per x_dtype, rows `ld` elements apart) to
  * packed form; with `transpose` the packed matrix is X^T, cols rows of length rows
  * (blocks run down the columns).
- * mx4_dequantize: the bf16 values [rows, cols] of a packed matrix (exact).
+ * mx4_dequantize: the bf16 values [rows, cols] of a packed matrix, of any producer (exact;
+ * values past bf16's range are infinities, a block of scale byte 255 is NaN).
  * mx4_matmul: C [M, N] = bf16(A B^T) of packed A [M, K] and B [N, K], fp32
  * accumulation. Sizes as mx4_linear_fwd.                                         */
 size_t mx4_codes_bytes(int64_t rows, int64_t cols);
