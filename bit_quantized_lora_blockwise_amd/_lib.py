@@ -192,6 +192,8 @@ def _empty_on(stream, shape, dtype, like):
     What the current stream may still be using is not handed to it, nor the reverse."""
     if not like.is_cuda or stream.cuda_stream == _stream():
         return _empty(shape, dtype, like)
+    if not isinstance(stream, torch.cuda.Stream):             # anything that holds a stream's handle
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=like.device)
     with torch.cuda.stream(stream):
         return _empty(shape, dtype, like)
 

@@ -147,3 +147,17 @@ def test_outputs_outlive_a_call_on_another_stream():
         assert not at & {t.data_ptr() for t in taken}, name
         torch.cuda.synchronize()
         del got, taken
+
+
+def test_stream_by_its_handle_alone():
+    """An object that holds a stream's handle, from another library say, does for a stream."""
+    class Handle:
+        cuda_stream = torch.cuda.Stream().cuda_stream
+
+    q, d = qlib(), Layer(40)
+    plain = dict(d.calls(q))
+    torch.cuda.synchronize()
+    for name, got in d.calls(q, stream=Handle):
+        torch.cuda.synchronize()
+        for a, b in zip(tensors(plain[name]), tensors(got)):
+            assert torch.equal(a, b), name
