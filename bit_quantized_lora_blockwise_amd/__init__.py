@@ -15,4 +15,6 @@ from ._lib import (  # noqa: F401
     lora_linear_fwd, lora_linear_bwd, lora_linear_fwd_t, lora_linear_dx,
     lora_dropout, qlora_linear_fwd_dropout, qlora_linear_bwd_dropout,
     mx4_quantize, mx4_dequantize, mx4_matmul, mx4_linear_fwd, mx4_linear_bwd,
+    mx8_quantize, mx8_dequantize, rms_norm_fwd, rms_norm_bwd,
+    qlora_swiglu_fwd, qlora_swiglu_bwd, qlora_linear_bwd_mx8,
 )

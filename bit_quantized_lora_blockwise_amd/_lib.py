@@ -35,7 +35,11 @@ EXPORTS = ("nf4_quantize", "nf4_quantize_dq", "nf4_double_quant", "nf4_dequantiz
            "lora_dropout", "qlora_linear_fwd_dropout_workspace", "qlora_linear_fwd_dropout",
            "qlora_linear_bwd_dropout_workspace", "qlora_linear_bwd_dropout",
            "mx4_codes_bytes", "mx4_scales_bytes", "mx4_quantize", "mx4_dequantize", "mx4_matmul",
-           "mx4_linear_fwd_workspace", "mx4_linear_fwd", "mx4_linear_bwd_workspace", "mx4_linear_bwd")
+           "mx4_linear_fwd_workspace", "mx4_linear_fwd", "mx4_linear_bwd_workspace", "mx4_linear_bwd",
+           "mx8_codes_bytes", "mx8_scales_bytes", "mx8_quantize", "mx8_dequantize",
+           "rms_norm_fwd", "rms_norm_bwd_workspace", "rms_norm_bwd",
+           "qlora_swiglu_fwd_workspace", "qlora_swiglu_fwd", "qlora_swiglu_bwd_workspace", "qlora_swiglu_bwd",
+           "qlora_linear_bwd_mx8_workspace", "qlora_linear_bwd_mx8")
 
 
 class QloraError(RuntimeError):
@@ -102,6 +106,19 @@ def lib():
             "mx4_linear_fwd": ([P, I64, I64, I64, P, P, P, P, I32, F32, F64, U64, U64, P, P, P, SZ, P], I32),
             "mx4_linear_bwd_workspace": ([I64, I64, I64, I32], SZ),
             "mx4_linear_bwd": ([P, P, I64, I64, I64, P, P, P, P, I32, F32, F64, U64, U64, P, P, P, P, P, SZ, P], I32),
+            "mx8_codes_bytes": ([I64, I64], SZ),
+            "mx8_scales_bytes": ([I64, I64], SZ),
+            "mx8_quantize": ([P, I32, I64, I64, I64, P, P, P], I32),
+            "mx8_dequantize": ([P, P, I64, I64, P, P], I32),
+            "rms_norm_fwd": ([P, P, I32, I64, I64, P, I32, F32, P, P, P, P, P], I32),
+            "rms_norm_bwd_workspace": ([I64, I64], SZ),
+            "rms_norm_bwd": ([P, P, P, I32, I64, I64, P, I32, F32, P, P, P, SZ, P], I32),
+            "qlora_swiglu_fwd_workspace": ([I64, I64, I64, I32], SZ),
+            "qlora_swiglu_fwd": ([P, I64, I64, I64, P, P, P, P, P, I32, F32, P, P, P, P, P, SZ, P], I32),
+            "qlora_swiglu_bwd_workspace": ([I64, I64, I64, I32], SZ),
+            "qlora_swiglu_bwd": ([P, P, P, I64, I64, I64, P, P, P, P, P, I32, F32, P, P, P, P, P, P, P, SZ, P], I32),
+            "qlora_linear_bwd_mx8_workspace": ([I64, I64, I64, I32], SZ),
+            "qlora_linear_bwd_mx8": ([P, P, P, I64, I64, I64, P, P, P, P, P, I32, F32, P, P, P, P, P, SZ, P], I32),
         }
         for name, (args, res) in sig.items():
             f = getattr(L, name)
@@ -825,4 +842,170 @@ def mx4_linear_bwd(X, dY, codes_t, scales_t, L1, L2, lora_scale=1.0, p=0.0, seed
     _check("mx4_linear_bwd", lib().mx4_linear_bwd(
         _ptr(X), _ptr(dY), M, K, N, _ptr(codes_t), _ptr(scales_t), _ptr(L1), _ptr(L2), r, float(lora_scale),
         *_draw(p, seed, offset), _ptr(T), _ptr(dX), _ptr(dL1), _ptr(dL2), _ptr(ws), ws.numel(), _stream(stream)))
+    return dX, dL1, dL2
+
+
+# --- microscaled 8-bit activations (MXFP8) ---------------------------------------
+
+def _mx8_shapes(rows, cols):
+    if rows <= 0 or cols <= 0:
+        raise ValueError(f"matrix [{rows}, {cols}]: sizes must be > 0")
+    kb = -(-cols // 32)
+    return (rows, 32 * kb), (rows, kb)
+
+
+def _mx8_packed(packed, name, rows, cols):
+    """(codes [rows, Kp], scales [rows, Kp/32]) of a packed [rows, cols] matrix."""
+    if not isinstance(packed, (tuple, list)) or len(packed) != 2:
+        raise TypeError(f"{name} must be the pair (codes, scales) of a packed matrix")
+    sc, ss = _mx8_shapes(rows, cols)
+    _need(packed[0], f"{name} codes", torch.uint8, shape=sc)
+    _need(packed[1], f"{name} scales", torch.uint8, shape=ss)
+    return packed
+
+
+def _mx8_out(packed, name, rows, cols, like, stream):
+    """A packed output: None or False -> absent, True -> allocated here, else checked."""
+    if packed is None or packed is False:
+        return None
+    if packed is not True:
+        return tuple(_mx8_packed(packed, name, rows, cols))
+    sc, ss = _mx8_shapes(rows, cols)
+    return (_out(None, name, torch.uint8, sc, like, stream), _out(None, name, torch.uint8, ss, like, stream))
+
+
+def mx8_quantize(X, codes=None, scales=None, stream=None):
+    """(codes [rows, Kp], scales [rows, Kp/32]) of X (fp32 or bf16, rows may be apart) in blocks of 32 along its rows."""
+    dt, rows, cols, ld = _rows(X, "X")
+    sc, ss = _mx8_shapes(rows, cols)
+    codes = _out(codes, "codes", torch.uint8, sc, X, stream)
+    scales = _out(scales, "scales", torch.uint8, ss, X, stream)
+    _check("mx8_quantize", lib().mx8_quantize(_ptr(X), dt, rows, cols, ld, _ptr(codes), _ptr(scales), _stream(stream)))
+    return codes, scales
+
+
+def mx8_dequantize(codes, scales, rows, cols, out=None, stream=None):
+    """bf16 values [rows, cols] of a packed matrix (exact)."""
+    _mx8_packed((codes, scales), "packed", rows, cols)
+    out = _out(out, "out", torch.bfloat16, (rows, cols), codes, stream)
+    _check("mx8_dequantize", lib().mx8_dequantize(_ptr(codes), _ptr(scales), rows, cols, _ptr(out), _stream(stream)))
+    return out
+
+
+# --- root-mean-square norm --------------------------------------------------------
+
+def _norm_args(X, weight, name):
+    if not isinstance(X, torch.Tensor) or X.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"{name} must be a float32 or bfloat16 torch.Tensor")
+    _need(X, name, X.dtype, ndim=2)
+    rows, cols = X.shape
+    if not isinstance(weight, torch.Tensor) or weight.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("weight must be a float32 or bfloat16 torch.Tensor")
+    _need(weight, "weight", weight.dtype, shape=(cols,))
+    return rows, cols, QL_BF16 if X.dtype == torch.bfloat16 else QL_F32, QL_BF16 if weight.dtype == torch.bfloat16 else QL_F32
+
+
+def rms_norm_fwd(X, weight, eps, residual=None, Y=None, S=None, mx8=None, stream=None):
+    """Y = bf16(S w / sqrt(mean(S^2) + eps)) [rows, cols] with S = X + residual in X's type.
+    Returns (Y or None, S or None, packed or None).
+
+    Y: None (allocated here), False (skipped; then mx8 is wanted) or a bf16 [rows, cols] tensor.
+    S: the sum, None without a residual; given, it may be X or residual itself.
+    mx8: None or False (not written), True (allocated here) or the pair (codes, scales): Y in 8 bits."""
+    rows, cols, dt, wdt = _norm_args(X, weight, "X")
+    Y = _out(Y, "Y", torch.bfloat16, (rows, cols), X, stream) if Y is not False else None
+    if residual is not None:
+        _need(residual, "residual", X.dtype, shape=(rows, cols))
+        S = _out(S, "S", X.dtype, (rows, cols), X, stream)
+    elif S is not None:
+        raise ValueError("S is the sum with a residual: without one it is X")
+    packed = _mx8_out(mx8, "mx8", rows, cols, X, stream)
+    _check("rms_norm_fwd", lib().rms_norm_fwd(
+        _ptr(X), _ptr(residual), dt, rows, cols, _ptr(weight), wdt, float(eps), _ptr(S), _ptr(Y),
+        *((_ptr(packed[0]), _ptr(packed[1])) if packed else (None, None)), _stream(stream)))
+    return Y, S, packed
+
+
+def rms_norm_bwd(dY, S, weight, eps, dS=None, dX=True, dW=True, workspace=None, stream=None):
+    """(dX in S's type or None, dW fp32 [cols] or None) of rms_norm_fwd; dS is added to dX.
+
+    dX, dW: True (allocated here), False/None (skipped) or a tensor; dX may be S or dS itself."""
+    rows, cols, dt, wdt = _norm_args(S, weight, "S")
+    _need(dY, "dY", torch.bfloat16, shape=(rows, cols))
+    if dS is not None:
+        _need(dS, "dS", S.dtype, shape=(rows, cols))
+    dX = _opt_out(dX, "dX", S.dtype, (rows, cols), S, stream)
+    dW = _opt_out(dW, "dW", torch.float32, (cols,), S, stream)
+    ws = _workspace(int(lib().rms_norm_bwd_workspace(rows, cols)) if dW is not None else 0, S, workspace, stream)
+    _check("rms_norm_bwd", lib().rms_norm_bwd(
+        _ptr(dY), _ptr(S), _ptr(dS), dt, rows, cols, _ptr(weight), wdt, float(eps), _ptr(dX), _ptr(dW), _ptr(ws),
+        ws.numel(), _stream(stream)))
+    return dX, dW
+
+
+# --- gated feed-forward product, backward passes from 8-bit activations ------------
+
+def qlora_swiglu_fwd(X, codes, c2, c1, F, L1, L2, lora_scale=1.0, H=None, T_out=None, mx8=None, workspace=None,
+                     stream=None):
+    """H = bf16(silu(G) U) [M, F], [G | U] = X W'^T + s T L2 of a stacked gate|up weight W [2 F, K] (quantized as one;
+    L1 [2, K, r], L2 [2, r, F]).  Returns (H, T_out [2, M, r] or None, packed or None).
+
+    mx8: None or False (not written), True (allocated here) or the pair (codes, scales): G over U in 8 bits, 2 M rows."""
+    _need(X, "X", torch.bfloat16, ndim=2)
+    M, K = X.shape
+    _packed(codes, c2, c1, 2 * F, K)
+    r = _group_adapters(L1, L2, 2, K, F)
+    H = _out(H, "H", torch.bfloat16, (M, F), X, stream)
+    T_out = _opt_out(T_out, "T_out", torch.bfloat16, (2, M, r), X, stream)
+    packed = _mx8_out(mx8, "mx8", 2 * M, F, X, stream)
+    ws = _workspace(int(lib().qlora_swiglu_fwd_workspace(M, K, F, r)), X, workspace, stream)
+    _check("qlora_swiglu_fwd", lib().qlora_swiglu_fwd(
+        _ptr(X), M, K, F, _ptr(codes), _ptr(c2), _ptr(c1), _ptr(L1), _ptr(L2), r, float(lora_scale), _ptr(H),
+        _ptr(T_out), *((_ptr(packed[0]), _ptr(packed[1])) if packed else (None, None)), _ptr(ws), ws.numel(),
+        _stream(stream)))
+    return H, T_out, packed
+
+
+def qlora_swiglu_bwd(x8, dH, codes, c2, c1, L1, L2, gu8, T, lora_scale=1.0, dX=True, dL1=None, dL2=None,
+                     workspace=None, stream=None):
+    """(dX or None, dL1 [2, K, r], dL2 [2, r, F]) of qlora_swiglu_fwd from dH and what it left: x8, the packed
+    (codes, scales) of X; gu8, those of G over U; T.  dX as in qlora_linear_bwd."""
+    _need(dH, "dH", torch.bfloat16, ndim=2)
+    M, F = dH.shape
+    _need(L1, "L1", torch.bfloat16, ndim=3)
+    K = L1.shape[1]
+    _packed(codes, c2, c1, 2 * F, K)
+    r = _group_adapters(L1, L2, 2, K, F)
+    _mx8_packed(x8, "x8", M, K)
+    _mx8_packed(gu8, "gu8", 2 * M, F)
+    _need(T, "T", torch.bfloat16, numel=2 * M * r)
+    dX = _opt_out(dX, "dX", torch.bfloat16, (M, K), dH, stream)
+    dL1 = _out(dL1, "dL1", torch.float32, (2, K, r), dH, stream)
+    dL2 = _out(dL2, "dL2", torch.float32, (2, r, F), dH, stream)
+    ws = _workspace(int(lib().qlora_swiglu_bwd_workspace(M, K, F, r)), dH, workspace, stream)
+    _check("qlora_swiglu_bwd", lib().qlora_swiglu_bwd(
+        _ptr(x8[0]), _ptr(x8[1]), _ptr(dH), M, K, F, _ptr(codes), _ptr(c2), _ptr(c1), _ptr(L1), _ptr(L2), r,
+        float(lora_scale), _ptr(gu8[0]), _ptr(gu8[1]), _ptr(T), _ptr(dX), _ptr(dL1), _ptr(dL2), _ptr(ws), ws.numel(),
+        _stream(stream)))
+    return dX, dL1, dL2
+
+
+def qlora_linear_bwd_mx8(x8, dY, codes, c2, c1, L1, L2, T, lora_scale=1.0, dX=True, dL1=None, dL2=None,
+                         workspace=None, stream=None):
+    """qlora_linear_bwd with X as the packed pair (codes, scales) x8 and the forward's T [M, r]."""
+    _need(dY, "dY", torch.bfloat16, ndim=2)
+    M, N = dY.shape
+    _need(L1, "L1", torch.bfloat16, ndim=2)
+    K, r = L1.shape
+    _packed(codes, c2, c1, N, K)
+    _need(L2, "L2", torch.bfloat16, shape=(r, N))
+    _mx8_packed(x8, "x8", M, K)
+    _need(T, "T", torch.bfloat16, numel=M * r)
+    dX = _opt_out(dX, "dX", torch.bfloat16, (M, K), dY, stream)
+    dL1 = _out(dL1, "dL1", torch.float32, (K, r), dY, stream)
+    dL2 = _out(dL2, "dL2", torch.float32, (r, N), dY, stream)
+    ws = _workspace(int(lib().qlora_linear_bwd_mx8_workspace(M, K, N, r)), dY, workspace, stream)
+    _check("qlora_linear_bwd_mx8", lib().qlora_linear_bwd_mx8(
+        _ptr(x8[0]), _ptr(x8[1]), _ptr(dY), M, K, N, _ptr(codes), _ptr(c2), _ptr(c1), _ptr(L1), _ptr(L2), r,
+        float(lora_scale), _ptr(T), _ptr(dX), _ptr(dL1), _ptr(dL2), _ptr(ws), ws.numel(), _stream(stream)))
     return dX, dL1, dL2

@@ -1,0 +1,212 @@
+// Entry points of the 8-bit activations, of the norm and of the gated product: argument
+// checks, workspace layout and dispatch.  Contracts: include/qlora.h.
+#include <algorithm>
+#include <cmath>
+
+#include "abi_util.h"
+#include "mx8.h"
+
+namespace {
+
+using namespace qlabi;
+
+constexpr int64_t kMaxElems = int64_t(1) << 40;
+
+bool matrix_ok(int64_t rows, int64_t cols, int64_t ld) {
+  return rows > 0 && cols > 0 && rows < kLim && cols < kLim && ld >= cols && ld <= kMaxElems / rows &&
+         cols <= kMaxElems / rows - 32;
+}
+
+// Sizes of a layer over the NF4 base, as qlora_linear_fwd's: X and dX, Y and dY and W's codes
+// each below 2^31 bytes; n is the number of W's rows and ldy that of Y's columns as the kernels keep it.
+bool layer_ok(int64_t M, int64_t K, int64_t n, int64_t ldy, int r) {
+  return M > 0 && K > 0 && n > 0 && K % 64 == 0 && r >= 1 && r <= 64 && M < kLim && K < kLim && n < kLim &&
+         M * K < kLim / 2 && ldy < kLim && M * ldy < kLim / 2 && n * (K / 2) < kLim;
+}
+
+bool glu_ok(int64_t M, int64_t K, int64_t F, int r) {
+  return F > 0 && F < kLim / 2 && layer_ok(M, K, 2 * F, glu_ldz(F), r);
+}
+
+// Forward: [T's planes of both halves][fp32 slices of both].
+struct FwdWs {
+  size_t planes, part, total;
+};
+FwdWs fwd_ws(int64_t M, int64_t K, int r) {
+  FwdWs w{round_up((size_t)4 * M * g_pitch(r) * 2), round_up(lora_skinny_ws(M, K, r)), 0};
+  w.total = w.planes + 2 * w.part;
+  return w;
+}
+
+// Backward: [dZ (gated)][G][its planes, turned][T turned][fp32 partials, of G and then of the gradients].
+struct BwdWs {
+  size_t dz, g, gt, tt, part, total;
+};
+BwdWs bwd_ws(int64_t M, int64_t K, int64_t N, int halves, int r) {
+  const size_t turned = (size_t)halves * turn_rank(r) * turn_rows(M) * 2;
+  BwdWs w{halves == 2 ? round_up((size_t)M * glu_ldz(N) * 2) : 0, round_up((size_t)halves * M * r * 2),
+          round_up(3 * turned), round_up(turned), 0, 0};
+  w.part = round_up(std::max(halves == 2 ? glu_back_ws(M, N, r) : lora_skinny_ws(M, N, r), grads8_ws(M, K, N, halves, r)));
+  w.total = w.dz + w.g + w.gt + w.tt + w.part;
+  return w;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t mx8_codes_bytes(int64_t rows, int64_t cols) {
+  return matrix_ok(rows, cols, cols) ? (size_t)mx8::code_bytes(rows, cols) : 0;
+}
+
+size_t mx8_scales_bytes(int64_t rows, int64_t cols) {
+  return matrix_ok(rows, cols, cols) ? (size_t)mx8::scale_bytes(rows, cols) : 0;
+}
+
+int mx8_quantize(const void* X, int x_dtype, int64_t rows, int64_t cols, int64_t ld, uint8_t* codes, uint8_t* scales,
+                 void* stream) {
+  if (!X || !codes || !scales) return QL_ERR_NULL;
+  if (x_dtype != QL_F32 && x_dtype != QL_BF16) return QL_ERR_DTYPE;
+  if (!matrix_ok(rows, cols, ld)) return QL_ERR_SHAPE;
+  if (!aligned16(X, codes, scales)) return QL_ERR_ALIGN;
+  QL_TRY(launch_mx8_quant(X, x_dtype == QL_BF16, rows, cols, ld, codes, scales, (hipStream_t)stream));
+  return QL_OK;
+}
+
+int mx8_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, uint16_t* out, void* stream) {
+  if (!codes || !scales || !out) return QL_ERR_NULL;
+  if (!matrix_ok(rows, cols, cols)) return QL_ERR_SHAPE;
+  if (!aligned16(codes, scales, out)) return QL_ERR_ALIGN;
+  QL_TRY(launch_mx8_dequant(codes, scales, rows, cols, out, (hipStream_t)stream));
+  return QL_OK;
+}
+
+int rms_norm_fwd(const void* X, const void* R, int x_dtype, int64_t rows, int64_t cols, const void* weight, int w_dtype,
+                 float eps, void* S, uint16_t* Y, uint8_t* codes, uint8_t* scales, void* stream) {
+  if (!X || !weight || (R && !S) || (!Y && !codes) || !codes != !scales) return QL_ERR_NULL;
+  if ((x_dtype != QL_F32 && x_dtype != QL_BF16) || (w_dtype != QL_F32 && w_dtype != QL_BF16)) return QL_ERR_DTYPE;
+  if (!matrix_ok(rows, cols, cols) || cols > kNormCols) return QL_ERR_SHAPE;
+  if (!(eps > 0.0f) || !std::isfinite(eps)) return QL_ERR_VALUE;
+  if (!aligned16((const char*)X, (const char*)R, (const char*)weight, (const char*)S, Y, codes, scales)) return QL_ERR_ALIGN;
+  QL_TRY(launch_norm_fwd(X, R, x_dtype == QL_BF16, rows, cols, weight, w_dtype == QL_BF16, eps, S, Y, codes, scales,
+                         (hipStream_t)stream));
+  return QL_OK;
+}
+
+size_t rms_norm_bwd_workspace(int64_t rows, int64_t cols) {
+  return matrix_ok(rows, cols, cols) && cols <= kNormCols ? round_up(norm_bwd_ws(rows, cols)) : 0;
+}
+
+int rms_norm_bwd(const uint16_t* dY, const void* S, const void* dS, int x_dtype, int64_t rows, int64_t cols,
+                 const void* weight, int w_dtype, float eps, void* dX, float* dW, void* workspace, size_t ws_bytes,
+                 void* stream) {
+  if (!dY || !S || !weight || (!dX && !dW)) return QL_ERR_NULL;
+  if ((x_dtype != QL_F32 && x_dtype != QL_BF16) || (w_dtype != QL_F32 && w_dtype != QL_BF16)) return QL_ERR_DTYPE;
+  if (!matrix_ok(rows, cols, cols) || cols > kNormCols) return QL_ERR_SHAPE;
+  if (!(eps > 0.0f) || !std::isfinite(eps)) return QL_ERR_VALUE;
+  if (!aligned16(dY, (const char*)S, (const char*)dS, (const char*)weight, (const char*)dX, dW)) return QL_ERR_ALIGN;
+  if (dW) {
+    if (!workspace || ws_bytes < rms_norm_bwd_workspace(rows, cols)) return QL_ERR_WORKSPACE;
+    if (!aligned16((const char*)workspace)) return QL_ERR_ALIGN;
+  }
+  QL_TRY(launch_norm_bwd(dY, S, dS, x_dtype == QL_BF16, rows, cols, weight, w_dtype == QL_BF16, eps, dX, dW,
+                         (float*)workspace, (hipStream_t)stream));
+  return QL_OK;
+}
+
+size_t qlora_swiglu_fwd_workspace(int64_t M, int64_t K, int64_t F, int r) {
+  return glu_ok(M, K, F, r) ? fwd_ws(M, K, r).total : 0;
+}
+
+int qlora_swiglu_fwd(const uint16_t* X, int64_t M, int64_t K, int64_t F, const uint8_t* codes, const uint8_t* c2,
+                     const float* c1, const uint16_t* L1, const uint16_t* L2, int r, float lora_scale, uint16_t* H,
+                     uint16_t* T_out, uint8_t* gu_codes, uint8_t* gu_scales, void* workspace, size_t ws_bytes,
+                     void* stream) {
+  if (!X || !codes || !c2 || !c1 || !L1 || !L2 || !H || !gu_codes != !gu_scales) return QL_ERR_NULL;
+  if (!glu_ok(M, K, F, r)) return QL_ERR_SHAPE;
+  if (!aligned16(X, codes, c2, c1, L1, L2, H, T_out, gu_codes, gu_scales)) return QL_ERR_ALIGN;
+  const FwdWs w = fwd_ws(M, K, r);
+  if (!workspace || ws_bytes < w.total) return QL_ERR_WORKSPACE;
+  if (!aligned16((const char*)workspace)) return QL_ERR_ALIGN;
+  hipStream_t s = (hipStream_t)stream;
+  uint16_t* planes = (uint16_t*)workspace;
+  float* part = (float*)((char*)workspace + w.planes);
+  const int64_t pitch = w.part / sizeof(float);
+  int slices = 0;
+  for (int h = 0; h < 2; ++h)
+    QL_TRY(launch_lora_slices(X, M, K, L1 + h * K * r, true, r, part + h * pitch, &slices, s));
+  QL_TRY(launch_t_planes(part, pitch, slices, 2, M, r, planes, T_out, s));
+  QL_TRY(launch_glu_big(X, M, K, F, codes, c2, c1, planes, L2, r, lora_scale, H, gu_codes, gu_scales, s));
+  return QL_OK;
+}
+
+size_t qlora_swiglu_bwd_workspace(int64_t M, int64_t K, int64_t F, int r) {
+  return glu_ok(M, K, F, r) ? bwd_ws(M, K, F, 2, r).total : 0;
+}
+
+int qlora_swiglu_bwd(const uint8_t* x_codes, const uint8_t* x_scales, const uint16_t* dH, int64_t M, int64_t K, int64_t F,
+                     const uint8_t* codes, const uint8_t* c2, const float* c1, const uint16_t* L1, const uint16_t* L2,
+                     int r, float lora_scale, const uint8_t* gu_codes, const uint8_t* gu_scales, const uint16_t* T,
+                     uint16_t* dX, float* dL1, float* dL2, void* workspace, size_t ws_bytes, void* stream) {
+  if (!x_codes || !x_scales || !dH || !codes || !c2 || !c1 || !L1 || !L2 || !gu_codes || !gu_scales || !T || !dL1 || !dL2)
+    return QL_ERR_NULL;
+  if (!glu_ok(M, K, F, r)) return QL_ERR_SHAPE;
+  if (!aligned16(x_codes, x_scales, dH, codes, c2, c1, L1, L2, gu_codes, gu_scales, T, dX, dL1, dL2)) return QL_ERR_ALIGN;
+  const BwdWs w = bwd_ws(M, K, F, 2, r);
+  if (!workspace || ws_bytes < w.total) return QL_ERR_WORKSPACE;
+  if (!aligned16((const char*)workspace)) return QL_ERR_ALIGN;
+  hipStream_t s = (hipStream_t)stream;
+  char* ws = (char*)workspace;
+  uint16_t* dZ = (uint16_t*)ws;
+  uint16_t* G = (uint16_t*)(ws + w.dz);
+  uint16_t* Gt = (uint16_t*)(ws + w.dz + w.g);
+  uint16_t* Tt = (uint16_t*)(ws + w.dz + w.g + w.gt);
+  float* part = (float*)(ws + w.dz + w.g + w.gt + w.tt);
+  int slices = 0;
+  QL_TRY(launch_glu_back(dH, M, F, gu_codes, gu_scales, L2, r, dZ, part, &slices, s));
+  QL_TRY(launch_turn(Turn{part, slices, lora_scale, T, G, Gt, Tt}, 2, M, r, s));
+  if (dX)
+    QL_TRY(launch_qgemm_big(true, dZ, M, K, 2 * F, codes, c2, c1, G, L1, r, 1.0f, dX, s, 2, nullptr, glu_ldz(F)));
+  QL_TRY(launch_grads8(Grads8{x_codes, x_scales, dH, gu_codes, gu_scales, Gt, Tt, lora_scale, dL1, dL2}, M, K, F, 2, r,
+                       part, s));
+  return QL_OK;
+}
+
+size_t qlora_linear_bwd_mx8_workspace(int64_t M, int64_t K, int64_t N, int r) {
+  return layer_ok(M, K, N, N, r) ? bwd_ws(M, K, N, 1, r).total : 0;
+}
+
+int qlora_linear_bwd_mx8(const uint8_t* x_codes, const uint8_t* x_scales, const uint16_t* dY, int64_t M, int64_t K,
+                         int64_t N, const uint8_t* codes, const uint8_t* c2, const float* c1, const uint16_t* L1,
+                         const uint16_t* L2, int r, float lora_scale, const uint16_t* T, uint16_t* dX, float* dL1,
+                         float* dL2, void* workspace, size_t ws_bytes, void* stream) {
+  if (!x_codes || !x_scales || !dY || !codes || !c2 || !c1 || !L1 || !L2 || !T || !dL1 || !dL2) return QL_ERR_NULL;
+  if (!layer_ok(M, K, N, N, r)) return QL_ERR_SHAPE;
+  if (!aligned16(x_codes, x_scales, dY, codes, c2, c1, L1, L2, T, dX, dL1, dL2)) return QL_ERR_ALIGN;
+  const BwdWs w = bwd_ws(M, K, N, 1, r);
+  if (!workspace || ws_bytes < w.total) return QL_ERR_WORKSPACE;
+  if (!aligned16((const char*)workspace)) return QL_ERR_ALIGN;
+  hipStream_t s = (hipStream_t)stream;
+  char* ws = (char*)workspace;
+  uint16_t* G = (uint16_t*)ws;
+  uint16_t* Gt = (uint16_t*)(ws + w.g);
+  uint16_t* Tt = (uint16_t*)(ws + w.g + w.gt);
+  float* part = (float*)(ws + w.g + w.gt + w.tt);
+  int slices = 0;
+  QL_TRY(launch_lora_slices(dY, M, N, L2, false, r, part, &slices, s));
+  QL_TRY(launch_turn(Turn{part, slices, lora_scale, T, G, Gt, Tt}, 1, M, r, s));
+  if (dX) {
+    if (dx_small_ok(M, K))
+      QL_TRY(launch_dx_small(dY, M, K, N, codes, c2, c1, G, nullptr, 0, nullptr, L1, r, dX,
+                             drop::Params{0, 0, 0, 0, 0, 1.0f}, s));
+    else if (qgemm_big_ok(true, M, K, N))
+      QL_TRY(launch_qgemm_big(true, dY, M, K, N, codes, c2, c1, G, L1, r, 1.0f, dX, s));
+    else
+      QL_TRY(launch_qgemm_dx(dY, M, K, N, codes, c2, c1, G, L1, r, dX, s));
+  }
+  QL_TRY(launch_grads8(Grads8{x_codes, x_scales, dY, nullptr, nullptr, Gt, Tt, lora_scale, dL1, dL2}, M, K, N, 1, r, part,
+                       s));
+  return QL_OK;
+}
+
+}  // extern "C"

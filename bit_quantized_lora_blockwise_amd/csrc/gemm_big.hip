@@ -39,7 +39,9 @@
 #include <type_traits>
 
 #include "dequant.h"
+#include "glu.h"
 #include "kernels.h"
+#include "mx8.h"
 
 namespace {
 
@@ -58,6 +60,9 @@ constexpr int kPlane = kBP + 32;  // dX B tile: bytes per byte-plane row (72 dwo
 constexpr int kBufElems = (kBP * kPF > kBR * kPD) ? kBP * kPF : kBR * kPD;
 static_assert(2 * kBR * kPlane <= 2 * kBufElems, "dX byte-plane tile fits the B buffer");
 constexpr int kPL = 64 + 8;       // pitch of the LoRA operand tiles [row][c]
+constexpr int kBPG = kBP / 2;     // gated product: columns of H per tile
+constexpr int kPG = kBPG + 32;    // and the pitch of its L2 tile [c][column]
+static_assert(64 * kPG <= kBM * kBR, "the gated product's L2 tile fits an activation buffer");
 
 constexpr uint32_t kOOB = 0x80000000u;
 
@@ -144,11 +149,25 @@ __device__ __forceinline__ bf16x8 frag_kmajor_sw(const LDS_AS uint16_t* base, in
 // swizzle), or stage the dX weight tile [64 rows of W][256 columns] through
 // registers into a padded LDS tile that the consumers read with the transposing
 // LDS read.  No dequantisation.
+// kGlu: the gated product H = silu(G) U of a stacked gate|up weight, W [2 F, K] (N = 2 F).
+// A tile is 128 columns of H: its 256 weight rows are 128 of the gate and the same 128 of
+// the up half, laid out so that each consumer wave holds both for its 64 columns; G and U
+// never leave its registers, but for their 8-bit copies when the caller keeps them.  The
+// products are taken with their operands exchanged, so that a lane holds 16 of 32
+// consecutive columns of one row: the copies' block scales and the stores of 16 bytes
+// then take register swaps between the wave's halves alone.  LA holds T as two bf16
+// planes for each half (16 bits of it: G and U are rounded to 8 bits, and a T of 8 bits
+// would put one in 300 of their codes on the other side of a border).
 // kDrop (dX): the adapter term is D o (G L1^T).  All waves draw the tile's decisions
 // into LDS (a bit an element) while the LoRA operands arrive (by the producers alone,
 // one wave a SIMD, the draws took 12 us a tile), and the consumers apply them to the
 // accumulators before the base product.
-template <bool kDx, bool kTail, bool kB16 = false, bool kDrop = false>
+struct GluOut {
+  uint8_t* codes;     // G and U in 8 bits, one packed matrix of 2 M rows (mx8.h), or null
+  uint8_t* scales;
+};
+
+template <bool kDx, bool kTail, bool kB16 = false, bool kDrop = false, bool kGlu = false>
 __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict__ A, int64_t M, int64_t K,
                                                      int64_t N, const uint8_t* __restrict__ codes,
                                                      const uint8_t* __restrict__ c2,
@@ -157,7 +176,9 @@ __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict_
                                                      const uint16_t* __restrict__ LB,   // L2 (fwd) / L1 (dX)
                                                      int r, float scale, uint16_t* __restrict__ C,
                                                      Nf4Params p, int nseg, int64_t seg,
-                                                     const uint16_t* __restrict__ Wb, drop::Params dp) {
+                                                     const uint16_t* __restrict__ Wb, drop::Params dp, int64_t lda,
+                                                     GluOut gl) {
+  static_assert(!kGlu || !(kDx || kTail || kB16 || kDrop), "the gated product is a forward over the packed weight");
   __shared__ __attribute__((aligned(16))) uint16_t lds_b[2 * kBufElems];   // weight tiles; LoRA operands first
   __shared__ __attribute__((aligned(16))) uint16_t lds_a0[kBM * kBR];      // activation tiles (two buffers,
   __shared__ __attribute__((aligned(16))) uint16_t lds_a1[kBM * kBR];      //  filled by buffer-to-LDS loads)
@@ -166,7 +187,8 @@ __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict_
   const int w = __builtin_amdgcn_readfirstlane(t >> 6), l = t & 63;
   const bool producer = w >= 8;           // uniform per wave
   const int rg = w & 3, ch = (w >> 2) & 1;  // consumers: row group (64 rows), column half (128 columns)
-  const int64_t P = kDx ? K : N;          // output columns
+  const int64_t P = kDx ? K : kGlu ? N / 2 : N;   // output columns
+  constexpr int kTileP = kGlu ? kBPG : kBP;       // of a tile
   const int64_t R = kDx ? N : K;          // reduction length
   const int64_t kblocks = K / qk::kBlock;
   constexpr bool kPerm = kDx && !kB16;    // dX columns in the lookup order (0, 2, 4, 6, 1, 3, 5, 7)
@@ -175,7 +197,7 @@ __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict_
   // v % 8, and XCD x takes a contiguous run of tiles in row-major tile order.
   // The launch has ntiles work groups (one tile each) or a multiple of 8 that
   // take tiles v, v + G, ... in turn (persistent).
-  const int tiles_x = (int)((P + kBP - 1) / kBP);
+  const int tiles_x = (int)((P + kTileP - 1) / kTileP);
   const int ntiles = tiles_x * (int)((M + kBM - 1) / kBM);
   const int vfirst = blockIdx.x + gridDim.x * blockIdx.y;
   const int vstride = gridDim.x * gridDim.y;
@@ -184,7 +206,7 @@ __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict_
     const int per = ntiles / 8, extra = ntiles % 8, xcd = v % 8, q = v / 8;
     const int tile = xcd < extra ? xcd * (per + 1) + q : extra * (per + 1) + (xcd - extra) * per + q;
     m0 = __builtin_amdgcn_readfirstlane((tile / tiles_x) * kBM);
-    p0 = __builtin_amdgcn_readfirstlane((tile % tiles_x) * kBP);
+    p0 = __builtin_amdgcn_readfirstlane((tile % tiles_x) * kTileP);
   };
   const int ng = kDx ? nseg : 1;
   LDS_AS uint16_t* la = (LDS_AS uint16_t*)lds_b;                 // [256][kPL]: T / G rows
@@ -194,6 +216,8 @@ __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict_
   LDS_AS uint16_t* b1 = (LDS_AS uint16_t*)lds_b + kBufElems;
   LDS_AS uint16_t* a0 = (LDS_AS uint16_t*)lds_a0;
   LDS_AS uint16_t* a1 = (LDS_AS uint16_t*)lds_a1;
+  LDS_AS uint16_t* la2 = la + kBM * kPL;   // kGlu: T's second plane; L2 goes to an activation buffer, free then too
+  static_assert(2 * kBM * kPL <= 2 * kBufElems, "two planes fit the B buffers");
   const int64_t nsteps = (R + kBR - 1) / kBR;
 
   if (producer) {
@@ -218,9 +242,9 @@ __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict_
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int row = 64 * pw + 8 * j + (l >> 3);
-      arow_off[j] = (uint32_t)((int64_t)row * R * 2) + 16u * achunk[j & 1];
+      arow_off[j] = (uint32_t)((int64_t)row * lda * 2) + 16u * achunk[j & 1];
     }
-    // Step st of a matrix with `rows` rows from row r0 goes through a descriptor
+    // Step st of a matrix with `rows` rows (lda apart; what lies between R and lda is zeros) from row r0 goes through a descriptor
     // based at column 64 st of row r0 whose size ends at the end of the matrix:
     // rows past the end read as zeros, and a step past the reduction has size 0.
     // The loads are issued from inline assembly, which writes no register: the
@@ -230,8 +254,8 @@ __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict_
     auto dma_tile = [&](const uint16_t* src, int64_t rows, int64_t r0, int64_t st, LDS_AS uint16_t* buf) {
       const int64_t left = R - st * kBR;
       const int rem = __builtin_amdgcn_readfirstlane((int)(left < kBR ? left : kBR));   // columns in this step
-      const uint64_t nrec = rem > 0 ? (uint64_t)(rows - r0) * R * 2 - (uint64_t)st * kBR * 2 : 0;
-      const uint64_t base = (uint64_t)(uintptr_t)(src + r0 * R + (rem > 0 ? st * kBR : 0));
+      const uint64_t nrec = rem > 0 ? (uint64_t)(rows - r0) * lda * 2 - (uint64_t)st * kBR * 2 : 0;
+      const uint64_t base = (uint64_t)(uintptr_t)(src + r0 * lda + (rem > 0 ? st * kBR : 0));
       const uint16_t* pa = (const uint16_t*)(((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(base >> 32)) << 32) |
                                              (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)base));
       const __amdgpu_buffer_rsrc_t ra = rsrc(pa, (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)nrec));
@@ -263,7 +287,12 @@ __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict_
       Stage h;
       if constexpr (!kB16) {
         int64_t wrow, kb;
-        if (!kDx) { wrow = p0 + tp; kb = step; }
+        if constexpr (kGlu) {
+          // tile row 128 ch + 64 half + q: column p0 + 64 ch + q of the half
+          const int64_t c = p0 + 64 * (tp >> 7) + (tp & 63);
+          wrow = c < P ? (((tp >> 6) & 1) ? P : 0) + c : N;
+          kb = step;
+        } else if (!kDx) { wrow = p0 + tp; kb = step; }
         else { wrow = step * kBR + (tp >> 2); kb = p0 / 64 + (tp & 3); }
         // out-of-range blocks get bit 31 set in their offsets: past every buffer end
         const uint32_t oob = (wrow < N && kb < kblocks) ? 0u : kOOB;
@@ -343,7 +372,41 @@ __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict_
     set_tile(v);
     Stage hA, hB, h0;
     if constexpr (kDrop) drop::fill_bits<kBM, kBP>((LDS_AS uint8_t*)mask, dp, m0, p0, t, kT);
-    for (int g = 0; g < ng; ++g) {
+    if constexpr (kGlu) {
+      const int rp = (r + 7) / 8 * 8;   // g_pitch
+      for (int g = 0; g < 2; ++g) {
+        const uint16_t* ts = LA + (int64_t)g * 2 * M * rp;
+        const uint16_t* l2 = LB + (int64_t)g * r * P;
+        u32x4 v[2][8], u[4];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int idx = tp + 256 * i, row = idx >> 3, cc = (idx & 7) * 8;
+          const bool ok = m0 + row < M && cc < rp;
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+            v[n][i] = ok ? *(const u32x4*)(ts + ((int64_t)n * M + m0 + row) * rp + cc) : u32x4{0, 0, 0, 0};
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int idx = tp + 256 * i, c = idx >> 4, pp = (idx & 15) * 8;
+          u[i] = c < r && p0 + pp < P ? qk::load8_row(l2 + (int64_t)c * P, p0 + pp, P) : u32x4{0, 0, 0, 0};
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int idx = tp + 256 * i;
+          *(LDS_AS u32x4*)(la + (idx >> 3) * kPL + (idx & 7) * 8) = v[0][i];
+          *(LDS_AS u32x4*)(la2 + (idx >> 3) * kPL + (idx & 7) * 8) = v[1][i];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int idx = tp + 256 * i;
+          *(LDS_AS u32x4*)(a0 + (idx >> 4) * kPG + (idx & 15) * 8) = u[i];
+        }
+        __builtin_amdgcn_s_waitcnt(0x0070);
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_s_barrier();       // the consumers have read them
+      }
+    } else for (int g = 0; g < ng; ++g) {
       const int64_t gs = kDx ? g : p0 / seg;
       const uint16_t* la_src = LA + gs * M * r;
       if (lora_vec) {
@@ -501,8 +564,13 @@ __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict_
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        acc[0][j] = qk::mfma32(aq[s & 1][0], bq[s & 1][j], acc[0][j]);
-        acc[1][j] = qk::mfma32(aq[s & 1][1], bq[s & 1][j], acc[1][j]);
+        if constexpr (kGlu) {
+          acc[0][j] = qk::mfma32(bq[s & 1][j], aq[s & 1][0], acc[0][j]);
+          acc[1][j] = qk::mfma32(bq[s & 1][j], aq[s & 1][1], acc[1][j]);
+        } else {
+          acc[0][j] = qk::mfma32(aq[s & 1][0], bq[s & 1][j], acc[0][j]);
+          acc[1][j] = qk::mfma32(aq[s & 1][1], bq[s & 1][j], acc[1][j]);
+        }
       }
     }
   };
@@ -521,7 +589,29 @@ __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict_
     drop::fill_bits<kBM, kBP>((LDS_AS uint8_t*)mask, dp, m0, p0, t, kT);
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   }
-  for (int g = 0; g < ng; ++g) {
+  if constexpr (kGlu) {
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      __builtin_amdgcn_s_barrier();
+      const int ksteps = (r + 15) / 16;
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        if (s < ksteps) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const bf16x8 b = qk::frag_kmajor(a0, kPG, 16 * s, 64 * ch + 32 * j);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              acc[i][2 * g + j] = qk::mfma32(b, qk::frag_rowmajor(la, kPL, 64 * rg + 32 * i, 16 * s), acc[i][2 * g + j]);
+              acc[i][2 * g + j] = qk::mfma32(b, qk::frag_rowmajor(la2, kPL, 64 * rg + 32 * i, 16 * s), acc[i][2 * g + j]);
+            }
+          }
+        }
+      }
+      __builtin_amdgcn_s_waitcnt(0xC07F);
+      __builtin_amdgcn_s_barrier();
+    }
+  } else for (int g = 0; g < ng; ++g) {
     __builtin_amdgcn_s_barrier();          // the producers' LoRA operands are in LDS
     const int ksteps = (r + 15) / 16;
 #pragma unroll
@@ -572,6 +662,66 @@ __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict_
     __builtin_amdgcn_s_barrier();
   }
 
+  if constexpr (kGlu) {
+    // lane (x, h): row x of 32, columns 8 q + 4 h + 0 .. 3 of 32
+    const int h = l >> 5;
+    const int64_t fp = mx8::padded(P);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int64_t m = m0 + 64 * rg + 32 * i + (l & 31);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int64_t c0 = p0 + 64 * ch + 32 * j;
+        if (c0 >= P) break;                // uniform
+        u32x2 o[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float y[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              y[k] = glu::silu(acc[i][j][4 * q + 2 * e + k]) * acc[i][2 + j][4 * q + 2 * e + k];
+            o[q][e] = qk::pack_bf16x2(y[0], y[1]);
+          }
+#pragma unroll
+        for (int q = 0; q < 4; q += 2) {   // the halves exchange: eight consecutive columns a lane
+          const u32x2 s0 = __builtin_amdgcn_permlane32_swap(o[q][0], o[q + 1][0], false, false);
+          const u32x2 s1 = __builtin_amdgcn_permlane32_swap(o[q][1], o[q + 1][1], false, false);
+          const int64_t c = c0 + 8 * q + 8 * h;
+          if (m < M && c < P) qk::store8_row(C + m * P + c, u32x4{s0[0], s1[0], s0[1], s1[1]}, (int)min((int64_t)8, P - c));
+        }
+        if (gl.codes) {
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            f32x16 v = acc[i][2 * g + j];
+            if (c0 + 32 > P) {             // zeros past the end of the row
+#pragma unroll
+              for (int e = 0; e < 16; ++e) v[e] = c0 + 8 * (e >> 2) + 4 * h + (e & 3) < P ? v[e] : 0.0f;
+            }
+            uint32_t top = 0;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) top = max(top, mx8::mag(v[e]));
+            const u32x2 both = __builtin_amdgcn_permlane32_swap(top, top, false, false);
+            const uint32_t sb = mx8::scale_byte(max(both[0], both[1]));
+            const float inv = mx8::inverse(sb);
+            uint32_t k[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) k[q] = mx8::encode4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3], inv);
+            const u32x2 s01 = __builtin_amdgcn_permlane32_swap(k[0], k[1], false, false);
+            const u32x2 s23 = __builtin_amdgcn_permlane32_swap(k[2], k[3], false, false);
+            const u32x2 t0 = __builtin_amdgcn_permlane32_swap(s01[0], s23[0], false, false);
+            const u32x2 t1 = __builtin_amdgcn_permlane32_swap(s01[1], s23[1], false, false);
+            if (m < M) {
+              const int64_t row = g * M + m;
+              *(u32x4*)(gl.codes + row * fp + c0 + 16 * h) = u32x4{t0[0], t1[0], t0[1], t1[1]};
+              if (h == 0) gl.scales[row * (fp / 32) + (c0 >> 5)] = (uint8_t)sb;
+            }
+          }
+        }
+      }
+    }
+  } else
   // ---- store C (bf16), lane layout of the 32x32 accumulators, through a
   // buffer descriptor based at this wave's first output element whose size
   // ends with the last row of C (rows past M are dropped by the hardware);
@@ -619,7 +769,7 @@ bool qgemm_big_ok(bool dx, int64_t M, int64_t K, int64_t N) {
 // a persistent grid of the CU count rounded down to a multiple of 8 (each
 // work group then takes tiles v, v + grid, ... on one XCD), so that a work
 // group's output stores drain while its next tile starts.
-static dim3 tile_grid(int64_t M, int64_t P) {
+static dim3 tile_grid(int64_t M, int64_t P, int64_t width = kBP) {
   static const int cus = [] {
     int dev = 0, n = 0;
     if (hipGetDevice(&dev) != hipSuccess || hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) !=
@@ -627,7 +777,7 @@ static dim3 tile_grid(int64_t M, int64_t P) {
       n = 256;
     return n;
   }();
-  const int64_t tx = (P + kBP - 1) / kBP, ty = (M + kBM - 1) / kBM;
+  const int64_t tx = (P + width - 1) / width, ty = (M + kBM - 1) / kBM;
   const int64_t pers = cus / 8 * 8;
   if (tx * ty > pers) return dim3((unsigned)pers, 1);
   return dim3((unsigned)tx, (unsigned)ty);
@@ -635,27 +785,38 @@ static dim3 tile_grid(int64_t M, int64_t P) {
 
 hipError_t launch_qgemm_big(bool dx, const uint16_t* A, int64_t M, int64_t K, int64_t N, const uint8_t* codes,
                             const uint8_t* c2, const float* c1, const uint16_t* LA, const uint16_t* LB, int r,
-                            float scale, uint16_t* C, hipStream_t s, int nseg, const drop::Params* d) {
+                            float scale, uint16_t* C, hipStream_t s, int nseg, const drop::Params* d, int64_t ld) {
   const int64_t P = dx ? K : N;
+  const int64_t lda = ld ? ld : dx ? N : K;
   const int64_t seg = N / nseg;   // columns of W per segment (a multiple of 256 when nseg > 1)
   const dim3 grid = tile_grid(M, P);
   const uint16_t* nw = nullptr;
   if (!dx)
     hipLaunchKernelGGL((k_qgemm_big<false, false>), grid, dim3(kT), 0, s, A, M, K, N, codes, c2, c1, LA, LB, r,
-                       scale, C, nf4_params(), nseg, seg, nw, drop::Params{});
+                       scale, C, nf4_params(), nseg, seg, nw, drop::Params{}, lda, GluOut{});
   else if (d && d->cut) {
     if (N % kBR == 0)
       hipLaunchKernelGGL((k_qgemm_big<true, false, false, true>), grid, dim3(kT), 0, s, A, M, K, N, codes, c2, c1, LA,
-                         LB, r, scale, C, nf4_params(), nseg, seg, nw, *d);
+                         LB, r, scale, C, nf4_params(), nseg, seg, nw, *d, lda, GluOut{});
     else
       hipLaunchKernelGGL((k_qgemm_big<true, true, false, true>), grid, dim3(kT), 0, s, A, M, K, N, codes, c2, c1, LA,
-                         LB, r, scale, C, nf4_params(), nseg, seg, nw, *d);
+                         LB, r, scale, C, nf4_params(), nseg, seg, nw, *d, lda, GluOut{});
   } else if (N % kBR == 0)
     hipLaunchKernelGGL((k_qgemm_big<true, false>), grid, dim3(kT), 0, s, A, M, K, N, codes, c2, c1, LA, LB, r,
-                       scale, C, nf4_params(), nseg, seg, nw, drop::Params{});
+                       scale, C, nf4_params(), nseg, seg, nw, drop::Params{}, lda, GluOut{});
   else
     hipLaunchKernelGGL((k_qgemm_big<true, true>), grid, dim3(kT), 0, s, A, M, K, N, codes, c2, c1, LA, LB, r,
-                       scale, C, nf4_params(), nseg, seg, nw, drop::Params{});
+                       scale, C, nf4_params(), nseg, seg, nw, drop::Params{}, lda, GluOut{});
+  return hipGetLastError();
+}
+
+hipError_t launch_glu_big(const uint16_t* X, int64_t M, int64_t K, int64_t F, const uint8_t* codes, const uint8_t* c2,
+                          const float* c1, const uint16_t* T, const uint16_t* L2, int r, float scale, uint16_t* H,
+                          uint8_t* gu_codes, uint8_t* gu_scales, hipStream_t s) {
+  const uint16_t* nw = nullptr;
+  hipLaunchKernelGGL((k_qgemm_big<false, false, false, false, true>), tile_grid(M, F, kBPG), dim3(kT), 0, s, X, M, K, 2 * F,
+                     codes, c2, c1, T, L2, r, scale, H, nf4_params(), 1, F, nw, drop::Params{}, K,
+                     GluOut{gu_codes, gu_scales});
   return hipGetLastError();
 }
 
@@ -675,12 +836,12 @@ hipError_t launch_bgemm_big(bool dx, const uint16_t* A, int64_t M, int64_t K, in
   const float* nf = nullptr;
   if (!dx)
     hipLaunchKernelGGL((k_qgemm_big<false, false, true>), grid, dim3(kT), 0, s, A, M, K, N, nc, nc, nf, LA, LB, r,
-                       scale, C, nf4_params(), 1, N, W, drop::Params{});
+                       scale, C, nf4_params(), 1, N, W, drop::Params{}, dx ? N : K, GluOut{});
   else if (N % kBR == 0)
     hipLaunchKernelGGL((k_qgemm_big<true, false, true>), grid, dim3(kT), 0, s, A, M, K, N, nc, nc, nf, LA, LB, r,
-                       scale, C, nf4_params(), 1, N, W, drop::Params{});
+                       scale, C, nf4_params(), 1, N, W, drop::Params{}, dx ? N : K, GluOut{});
   else
     hipLaunchKernelGGL((k_qgemm_big<true, true, true>), grid, dim3(kT), 0, s, A, M, K, N, nc, nc, nf, LA, LB, r,
-                       scale, C, nf4_params(), 1, N, W, drop::Params{});
+                       scale, C, nf4_params(), 1, N, W, drop::Params{}, dx ? N : K, GluOut{});
   return hipGetLastError();
 }

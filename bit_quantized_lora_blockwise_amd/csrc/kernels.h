@@ -216,12 +216,13 @@ hipError_t launch_qgemv_fwd_fused(const uint16_t* X, int64_t M, int64_t K, int64
 // W [N, K] is nseg matrices of N / nseg rows stacked (N / nseg a multiple of
 // 256), each with its own adapter: LA holds nseg [M, r] blocks, LB nseg L2
 // [r, N / nseg] (fwd) or L1 [K, r] (dX) blocks.  d (dX, nseg = 1): dropout of the
-// adapter term, dX = bf16(dY W' + D o (G L1^T)).
+// adapter term, dX = bf16(dY W' + D o (G L1^T)).  lda: elements from one row of A to the
+// next, a multiple of 8, zeros past the row (0: dense).
 bool qgemm_big_ok(bool dx, int64_t M, int64_t K, int64_t N);
 hipError_t launch_qgemm_big(bool dx, const uint16_t* A, int64_t M, int64_t K, int64_t N, const uint8_t* codes,
                             const uint8_t* c2, const float* c1, const uint16_t* LA, const uint16_t* LB, int r,
                             float scale, uint16_t* C, hipStream_t s, int nseg = 1,
-                            const drop::Params* d = nullptr);
+                            const drop::Params* d = nullptr, int64_t lda = 0);
 // The same two GEMMs with a bf16 weight W [N, K] in place of the packed one
 // (LoRA over a bf16 base): dx = false Y = bf16(X W^T + scale T L2), dx = true
 // dX = bf16(dY W + G L1^T).  bgemm_ok says whether the shapes qualify.
@@ -244,3 +245,74 @@ bool dx_small_ok(int64_t M, int64_t K);
 hipError_t launch_dx_small(const uint16_t* dY, int64_t M, int64_t K, int64_t N, const uint8_t* codes, const uint8_t* c2,
                            const float* c1, const uint16_t* G, const float* Gp, int S, uint16_t* planes,
                            const uint16_t* L1, int r, uint16_t* dX, const drop::Params& d, hipStream_t s);
+
+// --- microscaled 8-bit activations (mx8.hip) -------------------------------------
+hipError_t launch_mx8_quant(const void* X, bool bf16, int64_t rows, int64_t cols, int64_t ld, uint8_t* codes,
+                            uint8_t* scales, hipStream_t s);
+hipError_t launch_mx8_dequant(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, uint16_t* out,
+                              hipStream_t s);
+
+// --- root-mean-square norm (norm.hip) ---------------------------------------------
+// X (+ R into S, when R is given) to Y and / or its packed form; cols <= kNormCols.
+constexpr int64_t kNormCols = 32768;
+hipError_t launch_norm_fwd(const void* X, const void* R, bool bf16, int64_t rows, int64_t cols, const void* w, bool w_bf16,
+                           float eps, void* S, uint16_t* Y, uint8_t* codes, uint8_t* scales, hipStream_t s);
+// dX (may be null) and dw (may be null; then no workspace).
+size_t norm_bwd_ws(int64_t rows, int64_t cols);
+hipError_t launch_norm_bwd(const uint16_t* dY, const void* S, const void* dS, bool bf16, int64_t rows, int64_t cols,
+                           const void* w, bool w_bf16, float eps, void* dX, float* dw, float* ws, hipStream_t s);
+
+// --- gated product over the stacked gate|up base (gemm_big.hip, glu.hip) ----------
+// H [M, F] = bf16(silu(G) U), [G | U] = X W'^T + scale T L2 for W [2 F, K]; T: two planes
+// [M][g_pitch(r)] for each half; G and U in 8 bits too when gu_codes is given.
+hipError_t launch_glu_big(const uint16_t* X, int64_t M, int64_t K, int64_t F, const uint8_t* codes, const uint8_t* c2,
+                          const float* c1, const uint16_t* T, const uint16_t* L2, int r, float scale, uint16_t* H,
+                          uint8_t* gu_codes, uint8_t* gu_scales, hipStream_t s);
+// fp32 slices [*slices][M][r] of A B (b_is_kr, L1 [R, r]) or A B^T (L2 [r, R]), to be added in order;
+// ws as lora_skinny_ws(M, R, r).
+hipError_t launch_lora_slices(const uint16_t* A, int64_t M, int64_t R, const uint16_t* B, bool b_is_kr, int r, float* ws,
+                              int* slices, hipStream_t s);
+// Slices of T for `halves` products (part + h pitch floats each) to its two bf16 planes [halves][2][M][g_pitch(r)]
+// and, when T_out is given, bf16(T) [halves][M][r].
+hipError_t launch_t_planes(const float* part, int64_t pitch, int slices, int halves, int64_t M, int r, uint16_t* planes,
+                           uint16_t* T_out, hipStream_t s);
+
+// The backward's operands that are read along M, turned: [c][turn_rows(M)] with zeros past M, c up
+// to turn_rank(r).
+inline int64_t turn_rows(int64_t M) { return (M + 31) / 32 * 32; }
+inline int turn_rank(int r) { return (r + 15) / 16 * 16; }
+struct Turn {
+  const float* part;      // fp32 slices [slices][halves][M][r] of G
+  int slices;
+  float scale;
+  const uint16_t* T;      // [halves][M][r]
+  uint16_t* G;            // bf16(G) [halves][M][r]
+  uint16_t* Gt;           // [halves][3][turn_rank][turn_rows]: planes whose sum is G to 24 bits
+  uint16_t* Tt;           // [halves][turn_rank][turn_rows]
+};
+hipError_t launch_turn(const Turn& t, int halves, int64_t M, int r, hipStream_t s);
+
+// dZ = the gradients of G and U from dH and their 8-bit copies: bf16 [M][glu_ldz(F)], gate columns first,
+// zeros past 2 F; and the fp32 slices of dZ L2^T, [*slices][2][M][r].
+inline int64_t glu_ldz(int64_t F) { return (2 * F + 7) / 8 * 8; }
+size_t glu_back_ws(int64_t M, int64_t F, int r);
+hipError_t launch_glu_back(const uint16_t* dH, int64_t M, int64_t F, const uint8_t* gu_codes, const uint8_t* gu_scales,
+                           const uint16_t* L2, int r, uint16_t* dZ, float* part, int* slices, hipStream_t s);
+
+// The adapter's gradients from packed activations, in one launch and one for the slices' sums:
+//   dL1 [halves][K, r] = X^T G (X packed, Gt);  dL2 [halves][r, N] = scale T^T dZ (Tt), where dZ is dY [M, N]
+//   (halves = 1) or formed again from dH and the packed G and U, in fp32 (halves = 2).
+struct Grads8 {
+  const uint8_t* x_codes;
+  const uint8_t* x_scales;
+  const uint16_t* d;          // dY or dH
+  const uint8_t* gu_codes;
+  const uint8_t* gu_scales;
+  const uint16_t* Gt;
+  const uint16_t* Tt;
+  float scale;
+  float* dL1;
+  float* dL2;
+};
+size_t grads8_ws(int64_t M, int64_t K, int64_t N, int halves, int r);
+hipError_t launch_grads8(const Grads8& g, int64_t M, int64_t K, int64_t N, int halves, int r, float* ws, hipStream_t s);

@@ -975,6 +975,11 @@ hipError_t launch_lora_grad_in3(const uint16_t* dY, int64_t M, int64_t N, const 
   return launch_skinny_reduce3(ws, slices, M, r, scale, G, s);
 }
 
+hipError_t launch_lora_slices(const uint16_t* A, int64_t M, int64_t R, const uint16_t* B, bool b_is_kr, int r, float* ws,
+                              int* slices, hipStream_t s) {
+  return low_pass(A, M, R, B, b_is_kr, r, drop::Params{}, nullptr, nullptr, ws, slices, s);
+}
+
 hipError_t launch_lora_grads3(const uint16_t* X, int64_t K, const uint16_t* G, const drop::Params& d, float* dL1,
                               const uint16_t* dY, int64_t N, const uint16_t* T, float scale, float* dL2, int64_t M,
                               int r, float* ws, hipStream_t s) {

@@ -454,6 +454,95 @@ int mx4_linear_bwd(const uint16_t* X, const uint16_t* dY, int64_t M, int64_t K, 
                    const uint16_t* T, uint16_t* dX, float* dL1, float* dL2,
                    void* workspace, size_t ws_bytes, void* stream);
 
+/* Microscaled 8-bit activations (OCP Microscaling Formats v1.0, MXFP8 with E4M3
+ * elements): the form that a forward's activations are kept in for the backward, 8.25
+ * bits a value. One power-of-two scale for each 32 consecutive elements of a row; any
+ * number of rows and columns.
+ *   block:  e = the least integer >= -117 with max|v| <= 448 2^e, scale byte e + 127;
+ *           element = the E4M3FN value nearest to v / 2^e (ties to the even code; none
+ *           saturates). A block of zeros has e = -117. A block with an infinity or NaN
+ *           has scale byte 255 and codes 0, and stands for 32 NaN.
+ *   packed: rows of cols elements, padded with zeros to Kp = 32 ceil(cols / 32):
+ *           codes [rows][Kp] bytes, scales [rows][Kp / 32] bytes. mx8_codes_bytes and
+ *           mx8_scales_bytes are their sizes (host calls; 0 for sizes out of range).
+ *
+ * mx8_quantize: X [rows, cols] (fp32 or bf16 per x_dtype, rows `ld` elements apart) to
+ * packed form.
+ * mx8_dequantize: the bf16 values [rows, cols] of a packed matrix (exact for one that this
+ * library packed; values past bf16's range are infinities, a block of scale byte 255 NaN). */
+size_t mx8_codes_bytes(int64_t rows, int64_t cols);
+size_t mx8_scales_bytes(int64_t rows, int64_t cols);
+int mx8_quantize(const void* X, int x_dtype, int64_t rows, int64_t cols, int64_t ld,
+                 uint8_t* codes, uint8_t* scales, void* stream);
+int mx8_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
+                   uint16_t* out, void* stream);
+
+/* Root-mean-square norm of the rows of a residual stream, before the linears that read it:
+ *   fwd: S = X + R, rounded to X's type (R NULL: S is X and not written)
+ *        Y = bf16(S * weight / sqrt(mean(S^2) + eps)), and the same values, rounded once
+ *        from fp32, as a packed 8-bit matrix (codes, scales: the layout above)
+ *   bwd: n = S / sqrt(mean(S^2) + eps), d = weight * dY,
+ *        dX = (d - n mean(n d)) / sqrt(mean(S^2) + eps) + dS  (dS NULL: 0; dX NULL: skipped),
+ *        dW = fp32(sum over rows of n * dY)                   (NULL: skipped)
+ * X, R, S, dS, dX [rows, cols] fp32 or bf16 per x_dtype; weight [cols] fp32 or bf16 per
+ * w_dtype; Y, dY bf16. Y or codes and scales may be NULL, not both. dX is the gradient of X
+ * and of R alike; dS is the one that reaches S past the norm. S may be X or R, dX may be S
+ * or dS. A row's squares must have a finite sum in fp32. 1 <= cols <= 32768 (QL_ERR_SHAPE
+ * otherwise), eps > 0 (QL_ERR_VALUE). The backward needs its workspace for dW alone.        */
+int rms_norm_fwd(const void* X, const void* R, int x_dtype, int64_t rows, int64_t cols,
+                 const void* weight, int w_dtype, float eps, void* S, uint16_t* Y,
+                 uint8_t* codes, uint8_t* scales, void* stream);
+size_t rms_norm_bwd_workspace(int64_t rows, int64_t cols);
+int rms_norm_bwd(const uint16_t* dY, const void* S, const void* dS, int x_dtype, int64_t rows, int64_t cols,
+                 const void* weight, int w_dtype, float eps, void* dX, float* dW,
+                 void* workspace, size_t ws_bytes, void* stream);
+
+/* Gated feed-forward product over a stacked gate|up base: W [2 F, K] holds the gate's F rows
+ * and then the up projection's, quantised as one matrix (as for qlora_group_fwd); each half
+ * has an adapter of its own (L1: 2 consecutive [K, r], L2: 2 consecutive [r, F]).
+ *   fwd: [G | U] = X W'^T + lora_scale * (T L2) with T = X L1, each half its own,
+ *        H = bf16(G / (1 + e^-G) * U)                       [M, F]
+ *        T_out = bf16(T), 2 consecutive [M, r]              (NULL: not written)
+ *        gu_codes, gu_scales: G over U as one packed 8-bit matrix of 2 M rows of F
+ *        elements                                           (NULL: not written)
+ *   bwd: from dH [M, F] and what the forward left, with sig = 1 / (1 + e^-G),
+ *        dG = dH * U * sig * (1 + G * (1 - sig)), dU = dH * G * sig, dZ = [dG | dU]
+ *        B = lora_scale * dZ L2^T                           (each half its own)
+ *        dX = bf16(dZ W' + B L1^T, the halves added)        (NULL: skipped)
+ *        dL1 = fp32(X^T B), dL2 = fp32(lora_scale * T^T dZ) (2 consecutive blocks each)
+ *        X is the packed 8-bit copy of the forward's input (from rms_norm_fwd or
+ *        mx8_quantize), T the forward's T_out.
+ * G and U are taken at their full fp32 sums and T to 16 bits in the forward. In the backward
+ * dZ and B are kept to 24 bits for dL1 and dL2 and rounded to bf16 for dX. M from one row on,
+ * any F, K % 64 == 0, 1 <= r <= 64; X, dZ (M rows of 2 F, to a multiple of 8, bf16) and the
+ * codes must each stay below 2^31 bytes. Workspaces from the queries.                        */
+size_t qlora_swiglu_fwd_workspace(int64_t M, int64_t K, int64_t F, int r);
+int qlora_swiglu_fwd(const uint16_t* X, int64_t M, int64_t K, int64_t F,
+                     const uint8_t* codes, const uint8_t* c2, const float* c1,
+                     const uint16_t* L1, const uint16_t* L2, int r, float lora_scale,
+                     uint16_t* H, uint16_t* T_out, uint8_t* gu_codes, uint8_t* gu_scales,
+                     void* workspace, size_t ws_bytes, void* stream);
+size_t qlora_swiglu_bwd_workspace(int64_t M, int64_t K, int64_t F, int r);
+int qlora_swiglu_bwd(const uint8_t* x_codes, const uint8_t* x_scales, const uint16_t* dH,
+                     int64_t M, int64_t K, int64_t F,
+                     const uint8_t* codes, const uint8_t* c2, const float* c1,
+                     const uint16_t* L1, const uint16_t* L2, int r, float lora_scale,
+                     const uint8_t* gu_codes, const uint8_t* gu_scales, const uint16_t* T,
+                     uint16_t* dX, float* dL1, float* dL2,
+                     void* workspace, size_t ws_bytes, void* stream);
+
+/* qlora_linear_bwd with X as a packed 8-bit matrix, for a linear whose input the forward kept
+ * so (the down projection's H). Formulas, sizes and errors as there, X being the values that
+ * the packed matrix stands for; T is required (it cannot be formed again as the forward had
+ * it), and G is kept to 24 bits for dL1.                                                     */
+size_t qlora_linear_bwd_mx8_workspace(int64_t M, int64_t K, int64_t N, int r);
+int qlora_linear_bwd_mx8(const uint8_t* x_codes, const uint8_t* x_scales, const uint16_t* dY,
+                         int64_t M, int64_t K, int64_t N,
+                         const uint8_t* codes, const uint8_t* c2, const float* c1,
+                         const uint16_t* L1, const uint16_t* L2, int r, float lora_scale,
+                         const uint16_t* T, uint16_t* dX, float* dL1, float* dL2,
+                         void* workspace, size_t ws_bytes, void* stream);
+
 /* Host-only helpers (no GPU needed). */
 /* The 16 NF4 levels (fp32, ascending) that the kernels use, copied to out[16].  */
 int qlora_nf4_levels(float* out16);
