@@ -28,26 +28,33 @@ bool glu_ok(int64_t M, int64_t K, int64_t F, int r) {
   return F > 0 && F < kLim / 2 && layer_ok(M, K, 2 * F, glu_ldz(F), r);
 }
 
+// Whether T goes into the product as slices, which it adds up itself (a launch less): while the
+// rank-r product has few tiles of 16 x 16, and the product is one of those for few rows.
+bool few_ok(int64_t M, int64_t K, int64_t F, int r) {
+  return (M + 15) / 16 * ((r + 15) / 16) <= 24 && glu_small_ok(M, K, F);
+}
+
 // Forward: [T's planes of both halves][fp32 slices of both].
 struct FwdWs {
   size_t planes, part, total;
 };
-FwdWs fwd_ws(int64_t M, int64_t K, int r) {
-  FwdWs w{round_up((size_t)4 * M * g_pitch(r) * 2), round_up(lora_skinny_ws(M, K, r)), 0};
+FwdWs fwd_ws(int64_t M, int64_t K, int64_t F, int r) {
+  FwdWs w{0, round_up(few_ok(M, K, F, r) ? mx4_small_ws(M, r) : lora_skinny_ws(M, K, r)), 0};
+  if (!few_ok(M, K, F, r)) w.planes = round_up((size_t)4 * M * g_pitch(r) * 2);
   w.total = w.planes + 2 * w.part;
   return w;
 }
 
-// Backward: [dZ (gated)][G][its planes, turned][T turned][fp32 partials, of G and then of the gradients].
+// Backward: [dZ (gated)][G][its planes][T with their pitch][fp32 partials, of G and then of the gradients].
 struct BwdWs {
-  size_t dz, g, gt, tt, part, total;
+  size_t dz, g, planes, tp, part, total;
 };
 BwdWs bwd_ws(int64_t M, int64_t K, int64_t N, int halves, int r) {
-  const size_t turned = (size_t)halves * turn_rank(r) * turn_rows(M) * 2;
+  const size_t low = (size_t)halves * M * g_pitch(r) * 2;
   BwdWs w{halves == 2 ? round_up((size_t)M * glu_ldz(N) * 2) : 0, round_up((size_t)halves * M * r * 2),
-          round_up(3 * turned), round_up(turned), 0, 0};
+          round_up(3 * low), r == g_pitch(r) ? 0 : round_up(low), 0, 0};
   w.part = round_up(std::max(halves == 2 ? glu_back_ws(M, N, r) : lora_skinny_ws(M, N, r), grads8_ws(M, K, N, halves, r)));
-  w.total = w.dz + w.g + w.gt + w.tt + w.part;
+  w.total = w.dz + w.g + w.planes + w.tp + w.part;
   return w;
 }
 
@@ -115,7 +122,7 @@ int rms_norm_bwd(const uint16_t* dY, const void* S, const void* dS, int x_dtype,
 }
 
 size_t qlora_swiglu_fwd_workspace(int64_t M, int64_t K, int64_t F, int r) {
-  return glu_ok(M, K, F, r) ? fwd_ws(M, K, r).total : 0;
+  return glu_ok(M, K, F, r) ? fwd_ws(M, K, F, r).total : 0;
 }
 
 int qlora_swiglu_fwd(const uint16_t* X, int64_t M, int64_t K, int64_t F, const uint8_t* codes, const uint8_t* c2,
@@ -125,7 +132,7 @@ int qlora_swiglu_fwd(const uint16_t* X, int64_t M, int64_t K, int64_t F, const u
   if (!X || !codes || !c2 || !c1 || !L1 || !L2 || !H || !gu_codes != !gu_scales) return QL_ERR_NULL;
   if (!glu_ok(M, K, F, r)) return QL_ERR_SHAPE;
   if (!aligned16(X, codes, c2, c1, L1, L2, H, T_out, gu_codes, gu_scales)) return QL_ERR_ALIGN;
-  const FwdWs w = fwd_ws(M, K, r);
+  const FwdWs w = fwd_ws(M, K, F, r);
   if (!workspace || ws_bytes < w.total) return QL_ERR_WORKSPACE;
   if (!aligned16((const char*)workspace)) return QL_ERR_ALIGN;
   hipStream_t s = (hipStream_t)stream;
@@ -133,10 +140,23 @@ int qlora_swiglu_fwd(const uint16_t* X, int64_t M, int64_t K, int64_t F, const u
   float* part = (float*)((char*)workspace + w.planes);
   const int64_t pitch = w.part / sizeof(float);
   int slices = 0;
+  if (few_ok(M, K, F, r)) {
+    QL_TRY(launch_small_slices(X, M, K, L1, true, r, drop::Params{}, 1.0f, part, &slices, s, 2));
+    if (glu_decode_ok(M, K) && !gu_codes)
+      QL_TRY(launch_glu_decode(X, M, K, F, codes, c2, c1, part, slices, T_out, L2, r, lora_scale, H, s));
+    else
+      QL_TRY(launch_glu_small(X, M, K, F, codes, c2, c1, nullptr, part, slices, T_out, L2, r, lora_scale, H, gu_codes,
+                              gu_scales, s));
+    return QL_OK;
+  }
   for (int h = 0; h < 2; ++h)
     QL_TRY(launch_lora_slices(X, M, K, L1 + h * K * r, true, r, part + h * pitch, &slices, s));
   QL_TRY(launch_t_planes(part, pitch, slices, 2, M, r, planes, T_out, s));
-  QL_TRY(launch_glu_big(X, M, K, F, codes, c2, c1, planes, L2, r, lora_scale, H, gu_codes, gu_scales, s));
+  if (glu_small_ok(M, K, F))
+    QL_TRY(launch_glu_small(X, M, K, F, codes, c2, c1, planes, nullptr, 0, nullptr, L2, r, lora_scale, H, gu_codes,
+                            gu_scales, s));
+  else
+    QL_TRY(launch_glu_big(X, M, K, F, codes, c2, c1, planes, L2, r, lora_scale, H, gu_codes, gu_scales, s));
   return QL_OK;
 }
 
@@ -159,16 +179,16 @@ int qlora_swiglu_bwd(const uint8_t* x_codes, const uint8_t* x_scales, const uint
   char* ws = (char*)workspace;
   uint16_t* dZ = (uint16_t*)ws;
   uint16_t* G = (uint16_t*)(ws + w.dz);
-  uint16_t* Gt = (uint16_t*)(ws + w.dz + w.g);
-  uint16_t* Tt = (uint16_t*)(ws + w.dz + w.g + w.gt);
-  float* part = (float*)(ws + w.dz + w.g + w.gt + w.tt);
+  uint16_t* planes = (uint16_t*)(ws + w.dz + w.g);
+  uint16_t* Tp = (uint16_t*)(ws + w.dz + w.g + w.planes);
+  float* part = (float*)(ws + w.dz + w.g + w.planes + w.tp);
   int slices = 0;
   QL_TRY(launch_glu_back(dH, M, F, gu_codes, gu_scales, L2, r, dZ, part, &slices, s));
-  QL_TRY(launch_turn(Turn{part, slices, lora_scale, T, G, Gt, Tt}, 2, M, r, s));
+  QL_TRY(launch_low(Low{part, slices, lora_scale, T, G, planes, Tp}, 2, M, r, s));
   if (dX)
     QL_TRY(launch_qgemm_big(true, dZ, M, K, 2 * F, codes, c2, c1, G, L1, r, 1.0f, dX, s, 2, nullptr, glu_ldz(F)));
-  QL_TRY(launch_grads8(Grads8{x_codes, x_scales, dH, gu_codes, gu_scales, Gt, Tt, lora_scale, dL1, dL2}, M, K, F, 2, r,
-                       part, s));
+  QL_TRY(launch_grads8(Grads8{x_codes, x_scales, dH, gu_codes, gu_scales, planes, w.tp ? Tp : T, lora_scale, dL1, dL2}, M, K,
+                       F, 2, r, part, s));
   return QL_OK;
 }
 
@@ -189,12 +209,12 @@ int qlora_linear_bwd_mx8(const uint8_t* x_codes, const uint8_t* x_scales, const 
   hipStream_t s = (hipStream_t)stream;
   char* ws = (char*)workspace;
   uint16_t* G = (uint16_t*)ws;
-  uint16_t* Gt = (uint16_t*)(ws + w.g);
-  uint16_t* Tt = (uint16_t*)(ws + w.g + w.gt);
-  float* part = (float*)(ws + w.g + w.gt + w.tt);
+  uint16_t* planes = (uint16_t*)(ws + w.g);
+  uint16_t* Tp = (uint16_t*)(ws + w.g + w.planes);
+  float* part = (float*)(ws + w.g + w.planes + w.tp);
   int slices = 0;
   QL_TRY(launch_lora_slices(dY, M, N, L2, false, r, part, &slices, s));
-  QL_TRY(launch_turn(Turn{part, slices, lora_scale, T, G, Gt, Tt}, 1, M, r, s));
+  QL_TRY(launch_low(Low{part, slices, lora_scale, T, G, planes, Tp}, 1, M, r, s));
   if (dX) {
     if (dx_small_ok(M, K))
       QL_TRY(launch_dx_small(dY, M, K, N, codes, c2, c1, G, nullptr, 0, nullptr, L1, r, dX,
@@ -204,8 +224,8 @@ int qlora_linear_bwd_mx8(const uint8_t* x_codes, const uint8_t* x_scales, const 
     else
       QL_TRY(launch_qgemm_dx(dY, M, K, N, codes, c2, c1, G, L1, r, dX, s));
   }
-  QL_TRY(launch_grads8(Grads8{x_codes, x_scales, dY, nullptr, nullptr, Gt, Tt, lora_scale, dL1, dL2}, M, K, N, 1, r, part,
-                       s));
+  QL_TRY(launch_grads8(Grads8{x_codes, x_scales, dY, nullptr, nullptr, planes, w.tp ? Tp : T, lora_scale, dL1, dL2}, M, K, N,
+                       1, r, part, s));
   return QL_OK;
 }
 

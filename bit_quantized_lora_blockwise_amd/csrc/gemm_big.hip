@@ -663,8 +663,6 @@ __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict_
   }
 
   if constexpr (kGlu) {
-    // lane (x, h): row x of 32, columns 8 q + 4 h + 0 .. 3 of 32
-    const int h = l >> 5;
     const int64_t fp = mx8::padded(P);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -673,51 +671,11 @@ __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict_
       for (int j = 0; j < 2; ++j) {
         const int64_t c0 = p0 + 64 * ch + 32 * j;
         if (c0 >= P) break;                // uniform
-        u32x2 o[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float y[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-              y[k] = glu::silu(acc[i][j][4 * q + 2 * e + k]) * acc[i][2 + j][4 * q + 2 * e + k];
-            o[q][e] = qk::pack_bf16x2(y[0], y[1]);
-          }
-#pragma unroll
-        for (int q = 0; q < 4; q += 2) {   // the halves exchange: eight consecutive columns a lane
-          const u32x2 s0 = __builtin_amdgcn_permlane32_swap(o[q][0], o[q + 1][0], false, false);
-          const u32x2 s1 = __builtin_amdgcn_permlane32_swap(o[q][1], o[q + 1][1], false, false);
-          const int64_t c = c0 + 8 * q + 8 * h;
-          if (m < M && c < P) qk::store8_row(C + m * P + c, u32x4{s0[0], s1[0], s0[1], s1[1]}, (int)min((int64_t)8, P - c));
-        }
+        glu::store_h(acc[i][j], acc[i][2 + j], C, m, M, c0, P);
         if (gl.codes) {
 #pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            f32x16 v = acc[i][2 * g + j];
-            if (c0 + 32 > P) {             // zeros past the end of the row
-#pragma unroll
-              for (int e = 0; e < 16; ++e) v[e] = c0 + 8 * (e >> 2) + 4 * h + (e & 3) < P ? v[e] : 0.0f;
-            }
-            uint32_t top = 0;
-#pragma unroll
-            for (int e = 0; e < 16; ++e) top = max(top, mx8::mag(v[e]));
-            const u32x2 both = __builtin_amdgcn_permlane32_swap(top, top, false, false);
-            const uint32_t sb = mx8::scale_byte(max(both[0], both[1]));
-            const float inv = mx8::inverse(sb);
-            uint32_t k[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) k[q] = mx8::encode4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3], inv);
-            const u32x2 s01 = __builtin_amdgcn_permlane32_swap(k[0], k[1], false, false);
-            const u32x2 s23 = __builtin_amdgcn_permlane32_swap(k[2], k[3], false, false);
-            const u32x2 t0 = __builtin_amdgcn_permlane32_swap(s01[0], s23[0], false, false);
-            const u32x2 t1 = __builtin_amdgcn_permlane32_swap(s01[1], s23[1], false, false);
-            if (m < M) {
-              const int64_t row = g * M + m;
-              *(u32x4*)(gl.codes + row * fp + c0 + 16 * h) = u32x4{t0[0], t1[0], t0[1], t1[1]};
-              if (h == 0) gl.scales[row * (fp / 32) + (c0 >> 5)] = (uint8_t)sb;
-            }
-          }
+          for (int g = 0; g < 2; ++g)
+            glu::store_8(acc[i][2 * g + j], gl.codes + g * M * fp, gl.scales + g * M * (fp / 32), m, M, c0, P);
         }
       }
     }

@@ -8,6 +8,7 @@
 // tiles of gemm_big.hip leave most CUs idle at such sizes and walk the whole reduction in
 // one work group.
 #include "dequant.h"
+#include "glu.h"
 #include "kernels.h"
 
 namespace {
@@ -291,7 +292,162 @@ __global__ __launch_bounds__(64 * kW) void k_fwd_small(const uint16_t* __restric
   }
 }
 
+// The gated product for few rows: H = bf16(silu(G) U), [G | U] = X W'^T + s T L2 for a stacked
+// W [2 F, K].  As k_fwd_small, for 32 kI rows and the same 32 columns of both halves; 2 kI more
+// waves form the adapter's term of one half of 32 rows each meanwhile, add the eight waves'
+// sums in order and finish.  T enters as two bf16 planes (16 bits: G and U may be
+// kept in 8): given [2 halves][2][M][pitch], or kSum: formed here from its slices [2][S][M][r].
+template <int kI, bool kSum>
+__global__ __launch_bounds__(64 * (kW + 2 * kI)) void k_glu_small(const uint16_t* __restrict__ X, int M, int K, int F,
+                                                       const uint8_t* __restrict__ codes,
+                                                       const uint8_t* __restrict__ c2, const float* __restrict__ c1,
+                                                       const uint16_t* __restrict__ T, const float* __restrict__ Tp,
+                                                       int S, uint16_t* __restrict__ T_out,
+                                                       const uint16_t* __restrict__ L2, int r, float scale,
+                                                       uint16_t* __restrict__ H, uint8_t* __restrict__ gu_codes,
+                                                       uint8_t* __restrict__ gu_scales, Nf4Params q) {
+  __shared__ f32x16 red[kW][kI * 2][64];
+  const int w = threadIdx.x >> 6, l = threadIdx.x & 63, h = l >> 5, x = l & 31;
+  const int n0 = 32 * (int)blockIdx.x, m0 = 32 * kI * (int)blockIdx.y;
+  const int kb = K / 64;
+  const int64_t N = 2 * (int64_t)F;
+  const __amdgpu_buffer_rsrc_t rx = rsrc(X, (uint64_t)M * K * 2), rc = rsrc(codes, (uint64_t)N * (K / 2)),
+                               r2 = rsrc(c2, (uint64_t)N * kb), r1 = rsrc(c1, 4 * (((uint64_t)N * kb + 255) / 256));
+  const SplitConst kc = split_const();
+  struct Step {
+    u32x4 c[2];
+    uint32_t s2[2];
+    float s1[2];
+    bf16x8 a[kI][4];
+  };
+  auto load = [&](int b) {
+    Step s;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t n = (uint32_t)(j ? F : 0) + n0 + x;
+      const bool in = n0 + x < F && b < kb;
+      const uint32_t at = n * kb + b;
+      s.c[j] = __builtin_amdgcn_raw_buffer_load_b128(rc, in ? n * (K / 2) + 32 * b + 16 * h : kOOB, 0, 0);
+      s.s2[j] = __builtin_amdgcn_raw_buffer_load_b8(r2, in ? at : kOOB, 0, 0);
+      s.s1[j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r1, in ? 4 * (at >> 8) : kOOB, 0, 0));
+    }
+#pragma unroll
+    for (int i = 0; i < kI; ++i) {
+      const int m = m0 + 32 * i + x;
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        s.a[i][u] = load8<true>(rx, ((uint32_t)m * K + 64 * b + 32 * h + 8 * u) * 2u, m < M && b < kb ? 8 : 0);
+    }
+    return s;
+  };
+  if (w < kW) {
+    f32x16 acc[kI][2] = {};
+    Step cur = load(w);
+    for (int b = w; b < kb; b += kW) {
+      const Step nxt = load(b + kW);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const BlockLut lut = make_lut(qk::e4m3fn_to_f32(cur.s2[j]) * cur.s1[j], q);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const bf16x8 v = __builtin_bit_cast(bf16x8, dequant8(lut, cur.c[j][u], kc));
+#pragma unroll
+          for (int i = 0; i < kI; ++i) acc[i][j] = qk::mfma32(v, cur.a[i][u], acc[i][j]);
+        }
+      }
+      cur = nxt;
+    }
+#pragma unroll
+    for (int i = 0; i < kI; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) red[w][2 * i + j][l] = acc[i][j];
+  }
+  const int wf = w - kW, j = wf & 1, i = wf >> 1, m = m0 + 32 * i + x;
+  f32x16 sum = {};
+  if (w >= kW) {
+    const int pitch = (r + 7) / 8 * 8;
+    const uint16_t* l2 = L2 + (int64_t)j * r * F;
+    const uint16_t* t = T + (int64_t)j * 2 * M * pitch;      // its two planes
+    const __amdgpu_buffer_rsrc_t rt = kSum ? rsrc(Tp + (int64_t)j * S * M * r, (uint64_t)M * r * 4 * S)
+                                           : rsrc(t, (uint64_t)M * pitch * 4);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const int c = 16 * s + 8 * h;
+      if (16 * s >= r) break;                      // uniform
+      uint32_t e[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) e[k] = c + k < r && n0 + x < F ? l2[(int64_t)(c + k) * F + n0 + x] : 0;
+      const bf16x8 a = __builtin_bit_cast(
+          bf16x8, u32x4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16});
+      bf16x8 b[2];
+      if constexpr (kSum) {
+        float v[8];
+        sum8(rt, S, M, r, m, c, v);
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          u32x4 p;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            p[k] = qk::pack_bf16x2(v[2 * k], v[2 * k + 1]);
+            v[2 * k] -= __uint_as_float(p[k] << 16);
+            v[2 * k + 1] -= __uint_as_float(p[k] & 0xFFFF0000u);
+          }
+          b[n] = __builtin_bit_cast(bf16x8, p);
+          if (n == 0 && T_out && n0 == 0 && m < M && c < r)
+            qk::store8_row(T_out + ((int64_t)j * M + m) * r + c, p, min(8, r - c));
+        }
+      } else {
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+          b[n] = load8<true>(rt, ((uint32_t)(n * M + m) * pitch + c) * 2u, m < M && c < pitch ? 8 : 0);
+      }
+      sum = qk::mfma32(a, b[0], sum);
+      sum = qk::mfma32(a, b[1], sum);
+    }
+    sum = scale * sum;
+  }
+  __syncthreads();
+  if (w >= kW) {
+    f32x16 base = red[0][wf][l];
+#pragma unroll
+    for (int k = 1; k < kW; ++k) base += red[k][wf][l];
+    sum += base;
+    if (gu_codes) {
+      const int64_t fp = mx8::padded(F);
+      glu::store_8(sum, gu_codes + j * M * fp, gu_scales + j * M * (fp / 32), m, M, n0, F);
+    }
+    if (j) red[0][wf][l] = sum;                    // this wave's alone until the barrier
+  }
+  __syncthreads();
+  if (w >= kW && !j) glu::store_h(sum, red[0][wf + 1][l], H, m, M, n0, F);
+}
+
 }  // namespace
+
+bool glu_small_ok(int64_t M, int64_t K, int64_t F) {
+  return F < (int64_t(1) << 24) && (M <= 32 || (F + 31) / 32 * ((M + 63) / 64) <= 640);
+}
+
+hipError_t launch_glu_small(const uint16_t* X, int64_t M, int64_t K, int64_t F, const uint8_t* codes, const uint8_t* c2,
+                            const float* c1, const uint16_t* T, const float* Tp, int S, uint16_t* T_out,
+                            const uint16_t* L2, int r, float scale, uint16_t* H, uint8_t* gu_codes, uint8_t* gu_scales,
+                            hipStream_t s) {
+  const unsigned cols = (unsigned)((F + 31) / 32);
+#define QL_GLU(I, A)                                                                                            \
+  hipLaunchKernelGGL((k_glu_small<I, A>), dim3(cols, (unsigned)((M + 32 * I - 1) / (32 * I))),                  \
+                     dim3(64 * (kW + 2 * I)), 0, s, X, (int)M, (int)K, (int)F, codes, c2, c1, T, Tp, S, T_out, L2, r, \
+                     scale, H, gu_codes, gu_scales, nf4_params())
+  const bool one = M <= 32 || cols * ((M + 31) / 32) <= 256;
+  if (T) {
+    if (one) QL_GLU(1, false);
+    else QL_GLU(2, false);
+  } else {
+    if (one) QL_GLU(1, true);
+    else QL_GLU(2, true);
+  }
+#undef QL_GLU
+  return hipGetLastError();
+}
 
 // More rows than the decode kernels take at once (up to 48, three times as many, for any N
 // that L2's 32-bit offsets reach), up to 2.5 work groups of 64 x 64 a CU: the large tiles walk

@@ -2,6 +2,7 @@
 #pragma once
 
 #include "common.h"
+#include "mx8.h"
 
 namespace glu {
 
@@ -19,6 +20,71 @@ __device__ __forceinline__ void back(float g, float u, float dh, float& dg, floa
   const float s = sigmoid(g), gs = g * s;
   du = dh * gs;
   dg = dh * u * fmaf(gs, 1.0f - s, s);
+}
+
+// Eight fp32 as bf16, which they keep the rest of.
+__device__ __forceinline__ u32x4 take_plane(float (&v)[8]) {
+  u32x4 p;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    p[k] = qk::pack_bf16x2(v[2 * k], v[2 * k + 1]);
+    v[2 * k] -= __uint_as_float(p[k] << 16);
+    v[2 * k + 1] -= __uint_as_float(p[k] & 0xFFFF0000u);
+  }
+  return p;
+}
+
+// ---- what a gated product does with 32 rows of G and U ---------------------------------
+// Lane (x, h) of a wave holds row m (x of 32) and, of 32 columns from c0 (a multiple of 32) on,
+// columns 8 q + 4 h + e at accumulator 4 q + e.
+
+// H = bf16(silu(G) U): the wave's halves exchange groups of four columns, so that a lane stores
+// eight consecutive ones.
+__device__ __forceinline__ void store_h(const f32x16& g, const f32x16& u, uint16_t* __restrict__ H, int64_t m, int64_t M,
+                                        int64_t c0, int64_t F) {
+  const int h = (threadIdx.x & 63) >> 5;
+  u32x2 o[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      o[q][e] = qk::pack_bf16x2(silu(g[4 * q + 2 * e]) * u[4 * q + 2 * e], silu(g[4 * q + 2 * e + 1]) * u[4 * q + 2 * e + 1]);
+#pragma unroll
+  for (int q = 0; q < 4; q += 2) {
+    const u32x2 s0 = __builtin_amdgcn_permlane32_swap(o[q][0], o[q + 1][0], false, false);
+    const u32x2 s1 = __builtin_amdgcn_permlane32_swap(o[q][1], o[q + 1][1], false, false);
+    const int64_t c = c0 + 8 * q + 8 * h;
+    if (m < M && c < F) qk::store8_row(H + m * F + c, u32x4{s0[0], s1[0], s0[1], s1[1]}, (int)min((int64_t)8, F - c));
+  }
+}
+
+// G or U in 8 bits: half the block's maximum is in the lane, and after two exchanges so are 16
+// consecutive codes.  codes, scales: of the packed matrix's row 0 of this half.
+__device__ __forceinline__ void store_8(f32x16 v, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales, int64_t m,
+                                        int64_t M, int64_t c0, int64_t F) {
+  const int h = (threadIdx.x & 63) >> 5;
+  const int64_t fp = mx8::padded(F);
+  if (c0 + 32 > F) {                       // zeros past the end of the row
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] = c0 + 8 * (e >> 2) + 4 * h + (e & 3) < F ? v[e] : 0.0f;
+  }
+  uint32_t top = 0;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) top = max(top, mx8::mag(v[e]));
+  const u32x2 both = __builtin_amdgcn_permlane32_swap(top, top, false, false);
+  const uint32_t sb = mx8::scale_byte(max(both[0], both[1]));
+  const float inv = mx8::inverse(sb);
+  uint32_t k[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) k[q] = mx8::encode4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3], inv);
+  const u32x2 s01 = __builtin_amdgcn_permlane32_swap(k[0], k[1], false, false);
+  const u32x2 s23 = __builtin_amdgcn_permlane32_swap(k[2], k[3], false, false);
+  const u32x2 t0 = __builtin_amdgcn_permlane32_swap(s01[0], s23[0], false, false);
+  const u32x2 t1 = __builtin_amdgcn_permlane32_swap(s01[1], s23[1], false, false);
+  if (m < M) {
+    *(u32x4*)(codes + m * fp + c0 + 16 * h) = u32x4{t0[0], t1[0], t0[1], t1[1]};
+    if (h == 0) scales[m * (fp / 32) + (c0 >> 5)] = (uint8_t)sb;
+  }
 }
 
 }  // namespace glu

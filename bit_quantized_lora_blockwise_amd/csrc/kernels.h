@@ -161,9 +161,10 @@ hipError_t launch_mx4_small_t(const uint16_t* X, int64_t M, int64_t K, const uin
 hipError_t launch_mx4_small_g(const uint16_t* dY, int64_t M, int64_t N, const uint16_t* L2, int r, float scale,
                               uint16_t* G, float* part, hipStream_t s);
 // fp32 slices (part: mx4_small_ws bytes) of scale (D o A) B (L1, b_is_kr) or scale A B^T (L2), to be
-// added in order.
+// added in order.  products > 1: of A with that many B one after another, slices [product][slice][M][r].
 hipError_t launch_small_slices(const uint16_t* A, int64_t M, int64_t R, const uint16_t* B, bool b_is_kr, int r,
-                               const drop::Params& d, float scale, float* part, int* slices, hipStream_t s);
+                               const drop::Params& d, float scale, float* part, int* slices, hipStream_t s,
+                               int products = 1);
 
 // --- adapter merge (merge.hip) ---------------------------------------------
 // W[n][k] = bf16(W'[n][k] + scale * sum_c L1[k][c] L2[c][n]), W' the bf16
@@ -268,6 +269,18 @@ hipError_t launch_norm_bwd(const uint16_t* dY, const void* S, const void* dS, bo
 hipError_t launch_glu_big(const uint16_t* X, int64_t M, int64_t K, int64_t F, const uint8_t* codes, const uint8_t* c2,
                           const float* c1, const uint16_t* T, const uint16_t* L2, int r, float scale, uint16_t* H,
                           uint8_t* gu_codes, uint8_t* gu_scales, hipStream_t s);
+// The same for few rows (gemm_small.hip), from T's planes as above or, T = nullptr, from its slices Tp
+// [2][S][M][r] (T_out, optional, then receives bf16(T)); and for up to 16 rows of up to 32 KB in all,
+// without the 8-bit copies (decode_glu.hip), from the slices.
+bool glu_decode_ok(int64_t M, int64_t K);
+bool glu_small_ok(int64_t M, int64_t K, int64_t F);
+hipError_t launch_glu_small(const uint16_t* X, int64_t M, int64_t K, int64_t F, const uint8_t* codes, const uint8_t* c2,
+                            const float* c1, const uint16_t* T, const float* Tp, int S, uint16_t* T_out,
+                            const uint16_t* L2, int r, float scale, uint16_t* H, uint8_t* gu_codes, uint8_t* gu_scales,
+                            hipStream_t s);
+hipError_t launch_glu_decode(const uint16_t* X, int64_t M, int64_t K, int64_t F, const uint8_t* codes, const uint8_t* c2,
+                             const float* c1, const float* Tp, int S, uint16_t* T_out, const uint16_t* L2, int r,
+                             float scale, uint16_t* H, hipStream_t s);
 // fp32 slices [*slices][M][r] of A B (b_is_kr, L1 [R, r]) or A B^T (L2 [r, R]), to be added in order;
 // ws as lora_skinny_ws(M, R, r).
 hipError_t launch_lora_slices(const uint16_t* A, int64_t M, int64_t R, const uint16_t* B, bool b_is_kr, int r, float* ws,
@@ -277,20 +290,18 @@ hipError_t launch_lora_slices(const uint16_t* A, int64_t M, int64_t R, const uin
 hipError_t launch_t_planes(const float* part, int64_t pitch, int slices, int halves, int64_t M, int r, uint16_t* planes,
                            uint16_t* T_out, hipStream_t s);
 
-// The backward's operands that are read along M, turned: [c][turn_rows(M)] with zeros past M, c up
-// to turn_rank(r).
-inline int64_t turn_rows(int64_t M) { return (M + 31) / 32 * 32; }
-inline int turn_rank(int r) { return (r + 15) / 16 * 16; }
-struct Turn {
-  const float* part;      // fp32 slices [slices][halves][M][r] of G
+// The rank-r operands of the backward's last products: G = scale (the sum of its slices) as bf16 and as
+// three planes whose sum is G to 24 bits, and T with the planes' pitch where r is not that.
+struct Low {
+  const float* part;      // fp32 slices [slices][halves][M][r]
   int slices;
   float scale;
   const uint16_t* T;      // [halves][M][r]
-  uint16_t* G;            // bf16(G) [halves][M][r]
-  uint16_t* Gt;           // [halves][3][turn_rank][turn_rows]: planes whose sum is G to 24 bits
-  uint16_t* Tt;           // [halves][turn_rank][turn_rows]
+  uint16_t* G;            // [halves][M][r]
+  uint16_t* planes;       // [halves][3][M][g_pitch(r)]
+  uint16_t* Tp;           // [halves][M][g_pitch(r)], unused if r is its pitch
 };
-hipError_t launch_turn(const Turn& t, int halves, int64_t M, int r, hipStream_t s);
+hipError_t launch_low(const Low& q, int halves, int64_t M, int r, hipStream_t s);
 
 // dZ = the gradients of G and U from dH and their 8-bit copies: bf16 [M][glu_ldz(F)], gate columns first,
 // zeros past 2 F; and the fp32 slices of dZ L2^T, [*slices][2][M][r].
@@ -299,17 +310,17 @@ size_t glu_back_ws(int64_t M, int64_t F, int r);
 hipError_t launch_glu_back(const uint16_t* dH, int64_t M, int64_t F, const uint8_t* gu_codes, const uint8_t* gu_scales,
                            const uint16_t* L2, int r, uint16_t* dZ, float* part, int* slices, hipStream_t s);
 
-// The adapter's gradients from packed activations, in one launch and one for the slices' sums:
-//   dL1 [halves][K, r] = X^T G (X packed, Gt);  dL2 [halves][r, N] = scale T^T dZ (Tt), where dZ is dY [M, N]
-//   (halves = 1) or formed again from dH and the packed G and U, in fp32 (halves = 2).
+// The adapter's gradients from packed activations (grads8.hip), in one launch and one for the slices' sums:
+//   dL1 [halves][K, r] = X^T G (X packed, G as planes);  dL2 [halves][r, N] = scale T^T dZ (T with the planes'
+//   pitch), where dZ is dY [M, N] (halves = 1) or formed again from dH and the packed G and U in fp32 (halves = 2).
 struct Grads8 {
   const uint8_t* x_codes;
   const uint8_t* x_scales;
   const uint16_t* d;          // dY or dH
   const uint8_t* gu_codes;
   const uint8_t* gu_scales;
-  const uint16_t* Gt;
-  const uint16_t* Tt;
+  const uint16_t* planes;
+  const uint16_t* T;
   float scale;
   float* dL1;
   float* dL2;

@@ -73,7 +73,7 @@ class Block:
         return dz[0], dz[1], np.stack(dt)
 
 
-FORWARD = [(1, 64, 1, 1), (1, 4096, 512, 64), (2, 128, 33, 3), (16, 256, 100, 8), (17, 320, 129, 64), (5, 1088, 777, 12),
+FORWARD = [(1, 64, 1, 1), (3, 4096, 48, 12), (9, 2048, 17, 5), (16, 4096, 64, 64), (24, 1024, 100, 37), (400, 64, 20, 64), (1, 4096, 512, 64), (2, 128, 33, 3), (16, 256, 100, 8), (17, 320, 129, 64), (5, 1088, 777, 12),
            (33, 64, 16, 5), (77, 1024, 777, 12), (130, 576, 128, 64), (257, 192, 300, 33), (300, 512, 130, 16), (64, 64, 3, 64)]
 
 
@@ -87,17 +87,19 @@ def test_forward(M, K, F, r):
     within(T, t, dt + 2.0**-8 * np.abs(t), "T")
     packed_between(gu8, np.concatenate([g, u]), np.concatenate([dg, du]), F, "GU")
     e = (np.abs(g) + 4) * 2.0**-23
-    within(H, h, (1 + 2.0**-8) * (1.1 * np.abs(u) * dg + np.abs(g * X8.sigmoid(g)) * du + 1.1 * dg * du + e * np.abs(h)) +
-           2.0**-8 * np.abs(h), "H")
+    tol = (1 + 2.0**-8) * (1.1 * np.abs(u) * dg + np.abs(g * X8.sigmoid(g)) * du + 1.1 * dg * du + e * np.abs(h)) + 2.0**-8 * np.abs(h)
+    within(H, h, tol, "H")
     rel = np.linalg.norm(f64(H) - h) / np.linalg.norm(h)
     # half a step of bf16 is at most 2^-8 of a value, and so of the norm of any number of them; the fp32 sums' part
     # (2^-24 K at most) is far below what that bound leaves
     assert rel <= 2.0**-8, rel
-    # without what the backward needs: the same H
+    # without what the backward needs: H by another kernel for up to 16 rows, the same one beyond
     H2, none, no8 = q.qlora_swiglu_fwd(b.X, *b.base, F, b.L1, b.L2, S)
-    assert none is None and no8 is None and torch.equal(H, H2)
+    assert none is None and no8 is None
+    within(H2, h, tol, "H alone")
     H3, T3, _ = q.qlora_swiglu_fwd(b.X, *b.base, F, b.L1, b.L2, S, T_out=True)
-    assert torch.equal(H, H3) and torch.equal(T, T3)
+    assert torch.equal(H2, H3) and torch.equal(T, T3)
+    assert M <= 16 or torch.equal(H, H2)
 
 
 def check_backward(q, b, x8, gu8, T, dX, dL1, dL2):
