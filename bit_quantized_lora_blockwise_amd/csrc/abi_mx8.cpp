@@ -11,6 +11,7 @@ namespace {
 using namespace qlabi;
 
 constexpr int64_t kMaxElems = int64_t(1) << 40;
+constexpr drop::Params kNoDrop{0, 0, 0, 0, 0, 1.0f};
 
 bool matrix_ok(int64_t rows, int64_t cols, int64_t ld) {
   return rows > 0 && cols > 0 && rows < kLim && cols < kLim && ld >= cols && ld <= kMaxElems / rows &&
@@ -18,14 +19,16 @@ bool matrix_ok(int64_t rows, int64_t cols, int64_t ld) {
 }
 
 // Sizes of a layer over the NF4 base, as qlora_linear_fwd's: X and dX, Y and dY and W's codes
-// each below 2^31 bytes; n is the number of W's rows and ldy that of Y's columns as the kernels keep it.
-bool layer_ok(int64_t M, int64_t K, int64_t n, int64_t ldy, int r) {
+// each below 2^31 bytes, and each factor of the adapters; n is the number of W's rows and ldy that of
+// Y's columns as the kernels keep it, halves that of the adapters.
+bool layer_ok(int64_t M, int64_t K, int64_t n, int64_t ldy, int r, int halves = 1) {
   return M > 0 && K > 0 && n > 0 && K % 64 == 0 && r >= 1 && r <= 64 && M < kLim && K < kLim && n < kLim &&
-         M * K < kLim / 2 && ldy < kLim && M * ldy < kLim / 2 && n * (K / 2) < kLim;
+         M * K < kLim / 2 && ldy < kLim && M * ldy < kLim / 2 && n * (K / 2) < kLim && n * r < kLim / 2 &&
+         halves * K * r < kLim / 2;
 }
 
 bool glu_ok(int64_t M, int64_t K, int64_t F, int r) {
-  return F > 0 && F < kLim / 2 && layer_ok(M, K, 2 * F, glu_ldz(F), r);
+  return F > 0 && F < kLim / 2 && layer_ok(M, K, 2 * F, glu_ldz(F), r, 2);
 }
 
 // Whether T goes into the product as slices, which it adds up itself (a launch less): while the
@@ -185,7 +188,9 @@ int qlora_swiglu_bwd(const uint8_t* x_codes, const uint8_t* x_scales, const uint
   int slices = 0;
   QL_TRY(launch_glu_back(dH, M, F, gu_codes, gu_scales, L2, r, dZ, part, &slices, s));
   QL_TRY(launch_low(Low{part, slices, lora_scale, T, G, planes, Tp}, 2, M, r, s));
-  if (dX)
+  if (dX && dx_small_ok(M, K))
+    QL_TRY(launch_dx_small(dZ, M, K, 2 * F, codes, c2, c1, G, nullptr, 0, nullptr, L1, r, dX, kNoDrop, s, glu_ldz(F), 2));
+  else if (dX)
     QL_TRY(launch_qgemm_big(true, dZ, M, K, 2 * F, codes, c2, c1, G, L1, r, 1.0f, dX, s, 2, nullptr, glu_ldz(F)));
   QL_TRY(launch_grads8(Grads8{x_codes, x_scales, dH, gu_codes, gu_scales, planes, w.tp ? Tp : T, lora_scale, dL1, dL2}, M, K,
                        F, 2, r, part, s));
@@ -217,8 +222,7 @@ int qlora_linear_bwd_mx8(const uint8_t* x_codes, const uint8_t* x_scales, const 
   QL_TRY(launch_low(Low{part, slices, lora_scale, T, G, planes, Tp}, 1, M, r, s));
   if (dX) {
     if (dx_small_ok(M, K))
-      QL_TRY(launch_dx_small(dY, M, K, N, codes, c2, c1, G, nullptr, 0, nullptr, L1, r, dX,
-                             drop::Params{0, 0, 0, 0, 0, 1.0f}, s));
+      QL_TRY(launch_dx_small(dY, M, K, N, codes, c2, c1, G, nullptr, 0, nullptr, L1, r, dX, kNoDrop, s));
     else if (qgemm_big_ok(true, M, K, N))
       QL_TRY(launch_qgemm_big(true, dY, M, K, N, codes, c2, c1, G, L1, r, 1.0f, dX, s));
     else

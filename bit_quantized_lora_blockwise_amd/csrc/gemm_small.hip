@@ -55,20 +55,22 @@ __device__ __forceinline__ void sum8(__amdgpu_buffer_rsrc_t rp, int S, int M, in
   }
 }
 
-// kVec: N % 8 == 0 (rows of dY in whole 16-byte pieces); kVecR: r % 8 == 0; kSum: G as slices.
+// kVec: ldy % 8 == 0 (rows of dY in whole 16-byte pieces, zeros from N to ldy); kVecR: r % 8 == 0; kSum: G
+// as slices.  halves: of W's stacked rows, each with a G [M][r] and an L1 [K][r] of its own.
 template <bool kVec, bool kVecR, bool kSum>
 __global__ __launch_bounds__(64 * kW) void k_dx_small(const uint16_t* __restrict__ dY, int M, int K, int N,
                                                       const uint8_t* __restrict__ codes,
                                                       const uint8_t* __restrict__ c2, const float* __restrict__ c1,
                                                       const uint16_t* __restrict__ G, const float* __restrict__ Gp, int S,
                                                       uint16_t* __restrict__ planes, const uint16_t* __restrict__ L1,
-                                                      int r, uint16_t* __restrict__ dX, Nf4Params q, drop::Params d) {
+                                                      int r, uint16_t* __restrict__ dX, Nf4Params q, drop::Params d,
+                                                      int ldy, int halves) {
   __shared__ __attribute__((aligned(16))) uint16_t wt[kW][kN * kPitch];
   __shared__ f32x16 red[kW][2][64];
   const int w = threadIdx.x >> 6, l = threadIdx.x & 63, h = l >> 5, x = l & 31;
   const int p0 = kP * (int)blockIdx.x, m0 = 32 * (int)blockIdx.y, m = m0 + x;
   const int kb = K / 64;
-  const __amdgpu_buffer_rsrc_t ry = rsrc(dY, (uint64_t)M * N * 2), rc = rsrc(codes, (uint64_t)N * (K / 2)),
+  const __amdgpu_buffer_rsrc_t ry = rsrc(dY, (uint64_t)M * ldy * 2), rc = rsrc(codes, (uint64_t)N * (K / 2)),
                                r2 = rsrc(c2, (uint64_t)N * kb), r1 = rsrc(c1, 4 * (((uint64_t)N * kb + 255) / 256));
   const SplitConst kc = split_const();
   LDS_AS uint16_t* const tile = (LDS_AS uint16_t*)wt[w];
@@ -90,7 +92,7 @@ __global__ __launch_bounds__(64 * kW) void k_dx_small(const uint16_t* __restrict
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int k = n0 + 16 * u + 8 * h;
-      s.y[u] = load8<kVec>(ry, (uint32_t)(m * N + k) * 2u, m < M ? N - k : 0);
+      s.y[u] = load8<kVec>(ry, (uint32_t)(m * ldy + k) * 2u, m < M ? N - k : 0);
     }
     return s;
   };
@@ -118,10 +120,12 @@ __global__ __launch_bounds__(64 * kW) void k_dx_small(const uint16_t* __restrict
   if (w < 2) {
     // L1 from this wave's first column on: all of it may pass 2^31 bytes
     const int64_t first = __builtin_amdgcn_readfirstlane(p);
-    const __amdgpu_buffer_rsrc_t rg = rsrc(kSum ? (const void*)Gp : G, (uint64_t)M * r * (kSum ? 4 * S : 2)),
-                                 rl = rsrc(L1 + first * r, (uint64_t)32 * r * 2);
     const int pitch = (r + 7) / 8 * 8;
     const int64_t plane = (int64_t)M * pitch;
+    for (int half = 0; half < halves; ++half) {
+    const __amdgpu_buffer_rsrc_t rg = kSum ? rsrc(Gp, (uint64_t)M * r * 4 * S)
+                                           : rsrc(G + (int64_t)half * M * r, (uint64_t)M * r * 2),
+                                 rl = rsrc(L1 + ((int64_t)half * K + first) * r, (uint64_t)32 * r * 2);
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       const int c = 16 * s + 8 * h;
@@ -148,6 +152,7 @@ __global__ __launch_bounds__(64 * kW) void k_dx_small(const uint16_t* __restrict
         b = load8<kVecR>(rg, (uint32_t)(m * r + c) * 2u, m < M ? r - c : 0);
       }
       low = qk::mfma32(a, b, low);
+    }
     }
     // half h draws octets 2 h and 2 h + 1 of its row; each lane takes its own columns 8 g + 4 h + e from both halves'
     uint32_t mine = 0;
@@ -498,11 +503,13 @@ bool dx_small_ok(int64_t M, int64_t K) {
 
 hipError_t launch_dx_small(const uint16_t* dY, int64_t M, int64_t K, int64_t N, const uint8_t* codes, const uint8_t* c2,
                            const float* c1, const uint16_t* G, const float* Gp, int S, uint16_t* planes,
-                           const uint16_t* L1, int r, uint16_t* dX, const drop::Params& d, hipStream_t s) {
+                           const uint16_t* L1, int r, uint16_t* dX, const drop::Params& d, hipStream_t s, int64_t ldy,
+                           int halves) {
+  if (!ldy) ldy = N;
   const dim3 grid((unsigned)(K / kP), (unsigned)((M + 31) / 32));
 #define QL_DX(V, R, A)                                                                                                \
   hipLaunchKernelGGL((k_dx_small<V, R, A>), grid, dim3(64 * kW), 0, s, dY, (int)M, (int)K, (int)N, codes, c2, c1, \
-                     G, Gp, S, planes, L1, r, dX, nf4_params(), d)
+                     G, Gp, S, planes, L1, r, dX, nf4_params(), d, (int)ldy, halves)
 #define QL_DXS(A)                          \
   do {                                     \
     if (v && vr) QL_DX(true, true, A);     \
@@ -510,7 +517,7 @@ hipError_t launch_dx_small(const uint16_t* dY, int64_t M, int64_t K, int64_t N, 
     else if (vr) QL_DX(false, true, A);    \
     else QL_DX(false, false, A);           \
   } while (0)
-  const bool v = N % 8 == 0, vr = r % 8 == 0;
+  const bool v = ldy % 8 == 0, vr = r % 8 == 0;
   if (G) QL_DXS(false);
   else QL_DXS(true);
 #undef QL_DXS

@@ -22,6 +22,32 @@ __device__ __forceinline__ void back(float g, float u, float dh, float& dg, floa
   dg = dh * u * fmaf(gs, 1.0f - s, s);
 }
 
+constexpr uint32_t kOOB = 0x80000000u;     // a buffer offset past every range: the load returns 0
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p, uint64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc((void*)p, (short)0, (int)bytes, 0x00020000);
+}
+
+// Elements c .. c + 7 of a row of `cols` bf16 that begins at byte `row`, in two halves: the load, which waits for
+// nothing, and what fits it when it is used.  kVec: rows of whole 16-byte pieces.  Otherwise a piece that
+// crosses the row's end is read as the row's last eight and moved; rows of fewer are read one by one.
+template <bool kVec>
+__device__ __forceinline__ u32x4 load8(__amdgpu_buffer_rsrc_t rs, uint32_t row, int c, int cols, bool on) {
+  const bool in = on && c < cols;
+  if constexpr (kVec) return __builtin_amdgcn_raw_buffer_load_b128(rs, in ? row + 2 * c : kOOB, 0, 0);
+  if (cols >= 8) return __builtin_amdgcn_raw_buffer_load_b128(rs, in ? row + 2 * min(c, cols - 8) : kOOB, 0, 0);
+  uint32_t e[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    e[j] = __builtin_amdgcn_raw_buffer_load_b16(rs, in && c + j < cols ? row + 2 * (c + j) : kOOB, 0, 0);
+  return u32x4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
+}
+template <bool kVec>
+__device__ __forceinline__ u32x4 fit8(u32x4 v, int c, int cols) {
+  if (kVec || cols < 8 || c + 8 <= cols || c >= cols) return v;
+  return qk::drop_front8(v, c + 8 - cols);
+}
+
 // Eight fp32 as bf16, which they keep the rest of.
 __device__ __forceinline__ u32x4 take_plane(float (&v)[8]) {
   u32x4 p;

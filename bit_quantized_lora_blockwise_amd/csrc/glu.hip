@@ -17,17 +17,10 @@
 
 namespace {
 
+using glu::kOOB;
+using glu::rsrc;
+
 constexpr int kT = 256;
-constexpr uint32_t kOOB = 0x80000000u;
-
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p, uint64_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc((void*)p, (short)0, (int)bytes, 0x00020000);
-}
-
-__device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
-}
-
 // ---- T's planes ------------------------------------------------------------------
 __global__ __launch_bounds__(kT) void k_t_planes(const float* __restrict__ part, int64_t pitch, int slices, int64_t M,
                                                  int r, int rp, uint16_t* __restrict__ planes,
@@ -111,140 +104,124 @@ __global__ __launch_bounds__(kT) void k_low(Low q, int halves, int64_t M, int r,
 }
 
 // ---- dZ and the slices of dZ L2^T ----------------------------------------------------
-// Work group: 128 rows, eight waves of 16, and a slice of the columns in steps of 64.  Lane
-// (x, q) holds row x, columns 16 q .. + 15 of a step: two matrix operands as they are, since a
-// product may take the reduction in any order that both sides share.  The step's columns of L2
-// (both halves) pass through LDS, two buffers; everything is loaded a step ahead.
-constexpr int kBW = 8;                     // waves
-constexpr int kBC = 64;                    // columns of a step
-constexpr int kBPitch = kBC + 8;           // LDS row of L2: 16 rows' pieces of 16 bytes on different banks
+// Work group: 32 rows, a slice of the columns in steps of 128.  A step's dZ is formed in row-major
+// pieces of eight columns a thread (so that a row's bytes are read and written in whole cache
+// lines: with 16 rows a wave and lanes that held operands as they are, lines were read and
+// written in quarters, 180 us at 4096 x 2 x 11008), stored, split into planes and put into LDS.
+// Wave w multiplies half w / 4, 32 ranks (w / 2 % 2), 64 of the step's columns (w % 2): L2's
+// share comes straight from memory, 64 bytes a lane.  Everything is loaded a step ahead; one
+// LDS buffer and two barriers a step, so that two work groups share a CU.
+constexpr int kBT = 512;
+constexpr int kBM = 32;                    // rows
+constexpr int kBC = 128;                   // columns of a step
+constexpr int kBPitch = kBC + 8;           // LDS row (elements): 16 rows' pieces of 16 bytes on different banks
 
-// Eight elements from element c of a row of `cols` on, zeros past its end, whose first is `row` bytes into rs: a
-// piece that crosses the end is read as the row's last eight and moved (one by one in rows of fewer).
-__device__ __forceinline__ u32x4 load8(__amdgpu_buffer_rsrc_t rs, uint32_t row, int c, int cols, bool on) {
-  const bool in = on && c < cols;
-  if (cols >= 8) {                         // uniform
-    const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(rs, in ? row + 2 * min(c, cols - 8) : kOOB, 0, 0);
-    return (cols & 7) == 0 || c + 8 <= cols ? v : qk::drop_front8(v, min(8, c + 8 - cols));
-  }
-  uint32_t e[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    e[j] = __builtin_amdgcn_raw_buffer_load_b16(rs, in && c + j < cols ? row + 2 * (c + j) : kOOB, 0, 0);
-  return u32x4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
-}
-
-__global__ __launch_bounds__(64 * kBW, 4) void k_glu_back(const uint16_t* __restrict__ dH, int M, int F,
-                                                          const uint8_t* __restrict__ codes,
-                                                          const uint8_t* __restrict__ scales,
-                                                          const uint16_t* __restrict__ L2, int r, int chunk, int ldz,
-                                                          uint16_t* __restrict__ dZ, float* __restrict__ part) {
-  __shared__ __attribute__((aligned(16))) uint16_t lds[2][2 * 64 * kBPitch];
-  const int t = threadIdx.x, w = t >> 6, l = t & 63, x = l & 15, q = l >> 4;
-  const int m = 16 * kBW * (int)blockIdx.x + 16 * w + x;
+// kVec: F % 8 == 0.
+template <bool kVec>
+__global__ __launch_bounds__(kBT, 4) void k_glu_back(const uint16_t* __restrict__ dH, int M, int F,
+                                                     const uint8_t* __restrict__ codes,
+                                                     const uint8_t* __restrict__ scales,
+                                                     const uint16_t* __restrict__ L2, int r, int chunk, int ldz,
+                                                     uint16_t* __restrict__ dZ, float* __restrict__ part) {
+  __shared__ __attribute__((aligned(16))) uint16_t lds[6 * kBM * kBPitch];      // [half][plane][row][column]
+  const int t = threadIdx.x, w = __builtin_amdgcn_readfirstlane(t >> 6), l = t & 63, hl = l >> 5;
+  const int wh = w >> 2, wc = (w >> 1) & 1, wk = w & 1;
   const int f_beg = (int)blockIdx.y * chunk, f_end = min(F, f_beg + chunk);
   const int fp = (F + 31) / 32 * 32, nb = fp / 32;
-  const bool ok = m < M;
   // all below 2^31 bytes; the up half's codes and scales follow the gate's
   const __amdgpu_buffer_rsrc_t rc = rsrc(codes, (uint64_t)2 * M * fp), rs = rsrc(scales, (uint64_t)2 * M * nb),
-                               rd = rsrc(dH, (uint64_t)M * F * 2);
+                               rd = rsrc(dH, (uint64_t)M * F * 2), rl = rsrc(L2, (uint64_t)2 * r * F * 2);
   const uint32_t up_c = (uint32_t)M * fp, up_s = (uint32_t)M * nb;
-  const int nt = (r + 15) / 16, rk = 16 * nt;
-  // L2's share of a thread: row lr of both halves, columns 8 lq .. + 7 of a step
-  const int lr = t >> 3, lq = t & 7;
-  f32x4 acc[2][4] = {};
+  // thread t: row t / 16, columns 8 (t % 16) of a step
+  const int row = t >> 4, col = 8 * (t & 15), m = kBM * (int)blockIdx.x + row;
+  // lane (x, hl) of a wave: rank 32 wc + x, columns 64 wk + 32 hl .. + 31 of a step
+  const int c = 32 * wc + (l & 31), kcol = 64 * wk + 32 * hl;
   struct Step {
-    u32x4 g, u, d[2], b[2];
-    uint32_t sg, su;
+    u32x2 g, u;
+    u32x4 d, b[4];
+    uint8_t sg, su;
   };
   auto load = [&](int f0) {
     Step s;
-    const int f = f0 + 16 * q;
-    const bool in = ok && f < f_end;       // rows of codes go on to a multiple of 32
+    const int f = f0 + col;
+    const bool in = m < M && f < f_end;    // rows of codes go on to a multiple of 32
     const uint32_t oc = in ? (uint32_t)m * fp + f : kOOB, os = in ? (uint32_t)m * nb + (f >> 5) : kOOB;
-    s.g = __builtin_amdgcn_raw_buffer_load_b128(rc, oc, 0, 0);
-    s.u = __builtin_amdgcn_raw_buffer_load_b128(rc, in ? oc + up_c : kOOB, 0, 0);
+    s.g = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rc, oc, 0, 0));
+    s.u = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rc, in ? oc + up_c : kOOB, 0, 0));
     s.sg = __builtin_amdgcn_raw_buffer_load_b8(rs, os, 0, 0);
     s.su = __builtin_amdgcn_raw_buffer_load_b8(rs, in ? os + up_s : kOOB, 0, 0);
-    s.d[0] = load8(rd, (uint32_t)m * F * 2u, f, F, in);
-    s.d[1] = load8(rd, (uint32_t)m * F * 2u, f + 8, F, in);
-    const int fb = f0 + 8 * lq;
+    s.d = glu::load8<kVec>(rd, (uint32_t)m * F * 2u, f, F, in);
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-      s.b[h] = lr < r && fb < f_end ? qk::load8_row(L2 + ((int64_t)h * r + lr) * F, fb, F) : u32x4{0, 0, 0, 0};
+    for (int i = 0; i < 4; ++i)
+      s.b[i] = glu::load8<kVec>(rl, (uint32_t)(wh * r + c) * F * 2u, f0 + kcol + 8 * i, F, c < r && f0 + kcol + 8 * i < f_end);
     return s;
   };
-  auto stage = [&](const Step& s, int buf) {
+  f32x16 acc = {};
+  Step cur = load(f_beg);
+  for (int f0 = f_beg; f0 < f_end; f0 += kBC) {
+    const int f = f0 + col;
+    const float ks = mx8::scale_f32(cur.sg), ku = mx8::scale_f32(cur.su);
+    const u32x4 d = glu::fit8<kVec>(cur.d, f, F);
+    float dz[2][8];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      float g[4], u[4];
+      mx8::decode4(cur.g[k], ks, g);
+      mx8::decode4(cur.u[k], ku, u);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        glu::back(g[j], u[j], __uint_as_float(j & 1 ? d[2 * k + (j >> 1)] & 0xFFFF0000u : d[2 * k + (j >> 1)] << 16),
+                  dz[0][4 * k + j], dz[1][4 * k + j]);
+    }
+    bf16x8 b[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) b[i] = __builtin_bit_cast(bf16x8, glu::fit8<kVec>(cur.b[i], f0 + kcol + 8 * i, F));
+    __syncthreads();                       // the last step has been read
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-      if (lr < rk) *(LDS_AS u32x4*)((LDS_AS uint16_t*)lds[buf] + (64 * h + lr) * kBPitch + 8 * lq) = s.b[h];
-  };
-  Step cur = load(f_beg);
-  stage(cur, 0);
-  int buf = 0;
-  for (int f0 = f_beg; f0 < f_end; f0 += kBC, buf ^= 1) {
-    const Step nxt = load(f0 + kBC);
-    __syncthreads();                       // this step's L2 is in LDS, and the last one's reads are done
-    const LDS_AS uint16_t* b2 = (const LDS_AS uint16_t*)lds[buf];
-    const float ks = mx8::scale_f32(cur.sg), ku = mx8::scale_f32(cur.su);
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int f = f0 + 16 * q + 8 * u;
-      float dz[2][8];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        float g[4], v[4];
-        mx8::decode4(cur.g[2 * u + k], ks, g);
-        mx8::decode4(cur.u[2 * u + k], ku, v);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          glu::back(g[j], v[j], __uint_as_float(j & 1 ? cur.d[u][2 * k + (j >> 1)] & 0xFFFF0000u : cur.d[u][2 * k + (j >> 1)] << 16),
-                    dz[0][4 * k + j], dz[1][4 * k + j]);
+      for (int n = 0; n < 3; ++n) {
+        const u32x4 a = glu::take_plane(dz[h]);
+        *(LDS_AS u32x4*)((LDS_AS uint16_t*)lds + ((3 * h + n) * kBM + row) * kBPitch + col) = a;
+        if (n == 0 && m < M && f < F) qk::store8_row(dZ + (int64_t)m * ldz + h * F + f, a, min(8, F - f));
       }
+    cur = load(f0 + kBC);
+    __syncthreads();
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        u32x4 b[4];
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (j < nt) b[j] = *(const LDS_AS u32x4*)(b2 + (64 * h + 16 * j + x) * kBPitch + 16 * q + 8 * u);
-#pragma unroll
-        for (int n = 0; n < 3; ++n) {
-          const u32x4 a = glu::take_plane(dz[h]);
-          if (n == 0 && ok && f < F) qk::store8_row(dZ + (int64_t)m * ldz + h * F + f, a, min(8, F - f));
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (j < nt) acc[h][j] = mfma16(a, b[j], acc[h][j]);
-        }
-      }
-    }
-    stage(nxt, buf ^ 1);
-    cur = nxt;
+      for (int n = 0; n < 3; ++n)
+        acc = qk::mfma32(*(const LDS_AS bf16x8*)((const LDS_AS uint16_t*)lds + ((3 * wh + n) * kBM + (l & 31)) * kBPitch +
+                                                 kcol + 8 * i),
+                         b[i], acc);
   }
-  if (f_end == F && ok && q == 0)
+  if (f_end == F && m < M && (t & 15) == 0)
     for (int f = 2 * F; f < ldz; ++f) dZ[(int64_t)m * ldz + f] = 0;
-  // lane: column 16 j + x, rows 4 q + v
+  // the two halves of the steps' columns
+  __syncthreads();
+  LDS_AS float* red = (LDS_AS float*)lds + (w >> 1) * 1024 + l;
+  if (wk)
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
+    for (int e = 0; e < 16; ++e) red[64 * e] = acc[e];
+  __syncthreads();
+  if (wk) return;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const int mm = 16 * kBW * (int)blockIdx.x + 16 * w + 4 * q + v;
-        const int c = 16 * j + x;
-        if (mm < M && c < r) part[(((int64_t)blockIdx.y * 2 + h) * M + mm) * r + c] = acc[h][j][v];
-      }
+  for (int e = 0; e < 16; ++e) {
+    const int mm = kBM * (int)blockIdx.x + qk::acc_row(e);
+    if (mm < M && c < r) part[(((int64_t)blockIdx.y * 2 + wh) * M + mm) * r + c] = acc[e] + red[64 * e];
+  }
 }
 
-// Slices of that pass: about 512 work groups, of 128 columns at least.
+// Slices of that pass: about 512 work groups.
 struct PlanBack {
   int tiles, slices;
   int64_t chunk;
 };
 PlanBack plan_back(int64_t M, int64_t F) {
   PlanBack p;
-  p.tiles = (int)((M + 16 * kBW - 1) / (16 * kBW));
-  int64_t s = std::max<int64_t>(1, std::min<int64_t>(512 / p.tiles, F / 128));
-  p.chunk = ((F + s - 1) / s + kBC - 1) / kBC * kBC;
+  p.tiles = (int)((M + kBM - 1) / kBM);
+  const int64_t steps = (F + kBC - 1) / kBC, s = std::max<int64_t>(1, std::min<int64_t>(512 / p.tiles, steps));
+  p.chunk = (steps + s - 1) / s * kBC;
   p.slices = (int)((F + p.chunk - 1) / p.chunk);
   return p;
 }
@@ -277,7 +254,12 @@ hipError_t launch_glu_back(const uint16_t* dH, int64_t M, int64_t F, const uint8
                            const uint16_t* L2, int r, uint16_t* dZ, float* part, int* slices, hipStream_t s) {
   const PlanBack p = plan_back(M, F);
   *slices = p.slices;
-  hipLaunchKernelGGL(k_glu_back, dim3((unsigned)p.tiles, (unsigned)p.slices), dim3(64 * kBW), 0, s, dH, (int)M, (int)F,
-                     gu_codes, gu_scales, L2, r, (int)p.chunk, (int)glu_ldz(F), dZ, part);
+  const dim3 grid((unsigned)p.tiles, (unsigned)p.slices);
+#define QL_BACK(V)                                                                                                      \
+  hipLaunchKernelGGL(k_glu_back<V>, grid, dim3(kBT), 0, s, dH, (int)M, (int)F, gu_codes, gu_scales, L2, r, (int)p.chunk, \
+                     (int)glu_ldz(F), dZ, part)
+  if (F % 8 == 0) QL_BACK(true);
+  else QL_BACK(false);
+#undef QL_BACK
   return hipGetLastError();
 }

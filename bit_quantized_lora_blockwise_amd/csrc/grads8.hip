@@ -31,7 +31,9 @@ constexpr int kGABytes = kGM * kGP * 2;    // of a plane of a half
 constexpr int kGBBytes = kGM * kPitchB * 2;
 constexpr int kLds = kABytes + 3 * kBBytes;
 static_assert(6 * kGABytes + 2 * kGBBytes <= kLds, "the gated step fits");
-constexpr uint32_t kOOB = 0x80000000u;
+
+using glu::kOOB;
+using glu::rsrc;
 
 enum Kind { kPacked, kDense, kGated };
 
@@ -45,25 +47,6 @@ struct Job {
   float* out;               // [slices] of P r (kGated: 2 P r) values
   float scale;
 };
-
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p, uint64_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc((void*)p, (short)0, (int)bytes, 0x00020000);
-}
-
-// Eight bf16 from element c of a row of `cols` on, zeros past its end, whose first is `row` bytes into rs: a piece
-// that crosses the end is read as the row's last eight and moved (one by one in rows of fewer).
-__device__ __forceinline__ u32x4 load8(__amdgpu_buffer_rsrc_t rs, uint32_t row, int c, int cols, bool on) {
-  const bool in = on && c < cols;
-  if (cols >= 8) {                         // uniform
-    const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(rs, in ? row + 2 * min(c, cols - 8) : kOOB, 0, 0);
-    return (cols & 7) == 0 || c + 8 <= cols ? v : qk::drop_front8(v, min(8, c + 8 - cols));
-  }
-  uint32_t e[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    e[j] = __builtin_amdgcn_raw_buffer_load_b16(rs, in && c + j < cols ? row + 2 * (c + j) : kOOB, 0, 0);
-  return u32x4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
-}
 
 // A tiles [m][columns], 16-byte piece c of row m in slot c ^ 4 (m % 4), so that the rows that a transposed read
 // touches fall on different banks.
@@ -81,7 +64,8 @@ __device__ __forceinline__ bf16x8 frag_a(const LDS_AS uint8_t* a, int m0, int p0
   return __builtin_bit_cast(bf16x8, u32x4{u[0], u[1], v[0], v[1]});
 }
 
-template <Kind kKind>
+// kVec (dense): rows of d in whole 16-byte pieces.
+template <Kind kKind, bool kVec>
 __device__ __forceinline__ void columns(const Job& jb, int M, int r, int rp, int tile, int slice, LDS_AS uint8_t* lds) {
   constexpr int kPlanes = kKind == kPacked ? 3 : 1;
   constexpr int kPieces = kKind == kPacked ? 2 : 4;
@@ -110,7 +94,7 @@ __device__ __forceinline__ void columns(const Job& jb, int M, int r, int rp, int
         g.s[i] = __builtin_amdgcn_raw_buffer_load_b8(rs, in ? (uint32_t)row * nb + (p >> 5) : kOOB, 0, 0);
       } else {                             // rows t / 32 + 16 i, columns 8 (t % 32)
         const int row = m + (t >> 5) + 16 * i;
-        g.a[i] = load8(ra, (uint32_t)row * jb.P * 2u, p0 + 8 * (t & 31), jb.P, row < m_end);
+        g.a[i] = glu::load8<kVec>(ra, (uint32_t)row * jb.P * 2u, p0 + 8 * (t & 31), jb.P, row < m_end);
       }
     }
 #pragma unroll
@@ -135,7 +119,7 @@ __device__ __forceinline__ void columns(const Job& jb, int M, int r, int rp, int
                     qk::pack_bf16x2(v[6], v[7])};
         }
       } else {
-        *(LDS_AS u32x4*)(lds + slot<2 * kP>((t >> 5) + 16 * i, t & 31)) = g.a[i];
+        *(LDS_AS u32x4*)(lds + slot<2 * kP>((t >> 5) + 16 * i, t & 31)) = glu::fit8<kVec>(g.a[i], p0 + 8 * (t & 31), jb.P);
       }
     }
 #pragma unroll
@@ -194,6 +178,7 @@ __device__ __forceinline__ void columns(const Job& jb, int M, int r, int rp, int
   }
 }
 
+template <bool kVec>
 __device__ __forceinline__ void gated(const Job& jb, int M, int r, int rp, int tile, int slice, LDS_AS uint8_t* lds) {
   const int t = threadIdx.x, w = __builtin_amdgcn_readfirstlane(t >> 6), l = t & 63;
   const int wp = w & 3, wh = w >> 2;
@@ -220,13 +205,14 @@ __device__ __forceinline__ void gated(const Job& jb, int M, int r, int rp, int t
     s.u = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rc, in ? oc + up_c : kOOB, 0, 0));
     s.sg = __builtin_amdgcn_raw_buffer_load_b8(rs, os, 0, 0);
     s.su = __builtin_amdgcn_raw_buffer_load_b8(rs, in ? os + up_s : kOOB, 0, 0);
-    s.d = load8(rd, (uint32_t)m * jb.P * 2u, p, jb.P, m < m_end);
+    s.d = glu::load8<kVec>(rd, (uint32_t)m * jb.P * 2u, p, jb.P, m < m_end);
     s.b = __builtin_amdgcn_raw_buffer_load_b128(
         rb, m0 + brow < m_end && 8 * bc < rp ? (uint32_t)((m0 + brow) * rp + 8 * bc) * 2u : kOOB, 0, 0);
     return s;
   };
   auto store = [&](const Regs& s) {
     const float kg = mx8::scale_f32(s.sg), ku = mx8::scale_f32(s.su);
+    const u32x4 d = glu::fit8<kVec>(s.d, p, jb.P);
     float dz[2][8];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -235,7 +221,7 @@ __device__ __forceinline__ void gated(const Job& jb, int M, int r, int rp, int t
       mx8::decode4(s.u[k], ku, u);
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        glu::back(g[j], u[j], __uint_as_float(j & 1 ? s.d[2 * k + (j >> 1)] & 0xFFFF0000u : s.d[2 * k + (j >> 1)] << 16),
+        glu::back(g[j], u[j], __uint_as_float(j & 1 ? d[2 * k + (j >> 1)] & 0xFFFF0000u : d[2 * k + (j >> 1)] << 16),
                   dz[0][4 * k + j], dz[1][4 * k + j]);
     }
 #pragma unroll
@@ -278,19 +264,19 @@ __device__ __forceinline__ void gated(const Job& jb, int M, int r, int rp, int t
 }
 
 // Work groups: dL1's tiles and slices (for a gated product of one half, then of the other), then dL2's.
-template <bool kGlu>
+template <bool kGlu, bool kVec>
 __global__ __launch_bounds__(kT, 4) void k_grads8(Job j0, Job j0u, Job j1, int M, int r, int rp) {
   __shared__ __attribute__((aligned(16))) uint8_t lds[kLds];
   const int n0 = j0.tiles * j0.slices;
   int b = (int)blockIdx.x;
-  if (b < n0) return columns<kPacked>(j0, M, r, rp, b % j0.tiles, b / j0.tiles, (LDS_AS uint8_t*)lds);
+  if (b < n0) return columns<kPacked, true>(j0, M, r, rp, b % j0.tiles, b / j0.tiles, (LDS_AS uint8_t*)lds);
   b -= n0;
   if constexpr (kGlu) {
-    if (b < n0) return columns<kPacked>(j0u, M, r, rp, b % j0.tiles, b / j0.tiles, (LDS_AS uint8_t*)lds);
+    if (b < n0) return columns<kPacked, true>(j0u, M, r, rp, b % j0.tiles, b / j0.tiles, (LDS_AS uint8_t*)lds);
     b -= n0;
-    gated(j1, M, r, rp, b % j1.tiles, b / j1.tiles, (LDS_AS uint8_t*)lds);
+    gated<kVec>(j1, M, r, rp, b % j1.tiles, b / j1.tiles, (LDS_AS uint8_t*)lds);
   } else {
-    columns<kDense>(j1, M, r, rp, b % j1.tiles, b / j1.tiles, (LDS_AS uint8_t*)lds);
+    columns<kDense, kVec>(j1, M, r, rp, b % j1.tiles, b / j1.tiles, (LDS_AS uint8_t*)lds);
   }
 }
 
@@ -375,8 +361,15 @@ hipError_t launch_grads8(const Grads8& g, int64_t M, int64_t K, int64_t N, int h
                 p.x.slices > 1 ? px[h] : g.dL1 + h * nx, 1.0f};
   const Job jz{g.gu_codes, g.gu_scales, g.d, g.T, (int)N, p.z.tiles, p.z.slices, p.z.rows, p.z.slices > 1 ? pz : g.dL2, g.scale};
   const dim3 grid((unsigned)(halves * p.x.tiles * p.x.slices + p.z.tiles * p.z.slices));
-  if (halves == 2) hipLaunchKernelGGL(k_grads8<true>, grid, dim3(kT), 0, s, jx[0], jx[1], jz, (int)M, r, rp);
-  else hipLaunchKernelGGL(k_grads8<false>, grid, dim3(kT), 0, s, jx[0], jx[1], jz, (int)M, r, rp);
+#define QL_G8(G, V) hipLaunchKernelGGL((k_grads8<G, V>), grid, dim3(kT), 0, s, jx[0], jx[1], jz, (int)M, r, rp)
+  if (halves == 2) {
+    if (N % 8 == 0) QL_G8(true, true);
+    else QL_G8(true, false);
+  } else {
+    if (N % 8 == 0) QL_G8(false, true);
+    else QL_G8(false, false);
+  }
+#undef QL_G8
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || (p.x.slices == 1 && p.z.slices == 1)) return e;
   auto sum = [](const float* part, float* out, int64_t n, int slices) {

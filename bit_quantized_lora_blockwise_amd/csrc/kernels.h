@@ -241,11 +241,13 @@ hipError_t launch_fwd_small(const uint16_t* X, int64_t M, int64_t K, int64_t N, 
                             const float* c1, const uint16_t* T, const float* Tp, int S, uint16_t* T_out,
                             const uint16_t* L2, int r, float scale, uint16_t* Y, hipStream_t s);
 // dX = bf16(dY W' + D o (G L1^T)) from G, or with G = nullptr from its slices Gp (S of them), added
-// here; `planes` then receives it to 24 bits.
+// here; `planes` then receives it to 24 bits.  ldy, halves (G given): rows of dY ldy elements apart, zeros
+// behind N (0: dense); W's rows in that many halves with a G and an L1 each.
 bool dx_small_ok(int64_t M, int64_t K);
 hipError_t launch_dx_small(const uint16_t* dY, int64_t M, int64_t K, int64_t N, const uint8_t* codes, const uint8_t* c2,
                            const float* c1, const uint16_t* G, const float* Gp, int S, uint16_t* planes,
-                           const uint16_t* L1, int r, uint16_t* dX, const drop::Params& d, hipStream_t s);
+                           const uint16_t* L1, int r, uint16_t* dX, const drop::Params& d, hipStream_t s, int64_t ldy = 0,
+                           int halves = 1);
 
 // --- microscaled 8-bit activations (mx8.hip) -------------------------------------
 hipError_t launch_mx8_quant(const void* X, bool bf16, int64_t rows, int64_t cols, int64_t ld, uint8_t* codes,
