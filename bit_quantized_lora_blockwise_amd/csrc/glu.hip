@@ -212,7 +212,7 @@ __global__ __launch_bounds__(kBT, 4) void k_glu_back(const uint16_t* __restrict_
   }
 }
 
-// Slices of that pass: about 512 work groups.
+// Slices of that pass: about 512 work groups, but no more than 32 slices to add up for each row.
 struct PlanBack {
   int tiles, slices;
   int64_t chunk;
@@ -220,7 +220,7 @@ struct PlanBack {
 PlanBack plan_back(int64_t M, int64_t F) {
   PlanBack p;
   p.tiles = (int)((M + kBM - 1) / kBM);
-  const int64_t steps = (F + kBC - 1) / kBC, s = std::max<int64_t>(1, std::min<int64_t>(512 / p.tiles, steps));
+  const int64_t steps = (F + kBC - 1) / kBC, s = std::max<int64_t>(1, std::min<int64_t>({512 / p.tiles, steps, 32}));
   p.chunk = (steps + s - 1) / s * kBC;
   p.slices = (int)((F + p.chunk - 1) / p.chunk);
   return p;

@@ -6,8 +6,9 @@
 // over it and the pass that uses the sum.  Sums and statistics are fp32 (a thread's at most
 // 32 squares, then a tree), the root fp64: one of them a row.
 //
-// A row belongs to a wave (up to 2048 columns), to 256 threads (8192) or to 1024 (32768), up
-// to four chunks of eight columns a thread.
+// A row belongs to a wave (up to 1024 columns) or to 256, 512 or 1024 threads, one or two
+// chunks of eight columns a thread (four past 16384 columns).  Rows are read through a
+// descriptor of their own, so that no load stands behind a branch.
 #include <algorithm>
 
 #include "kernels.h"
@@ -15,26 +16,71 @@
 
 namespace {
 
-// Eight values of a row as fp32, zeros past its end.
-__device__ __forceinline__ void load8(const uint16_t* row, int c, int cols, float* v) {
-  const u32x4 x = qk::load8_row(row, c, cols);
+constexpr uint32_t kOOB = 0x80000000u;
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p, uint64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc((void*)p, (short)0, (int)bytes, 0x00020000);
+}
+
+// Eight values of a row of `cols` as they lie in memory, from column c on.  kVec: cols % 8 == 0.  Otherwise a chunk
+// that crosses the end is read as the row's last eight and moved when it is used; rows of fewer are read one by one.
+template <typename T>
+struct Raw;
+template <>
+struct Raw<uint16_t> {
+  u32x4 v;
+};
+template <>
+struct Raw<float> {
+  f32x4 v[2];
+};
+
+template <bool kVec>
+__device__ __forceinline__ void load8(Raw<uint16_t>& r, __amdgpu_buffer_rsrc_t rs, int c, int cols) {
+  if (kVec || cols >= 8) {
+    r.v = __builtin_amdgcn_raw_buffer_load_b128(rs, c < cols ? 2u * (kVec ? c : min(c, cols - 8)) : kOOB, 0, 0);
+  } else {
+    uint32_t e[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) e[j] = __builtin_amdgcn_raw_buffer_load_b16(rs, c + j < cols ? 2u * (c + j) : kOOB, 0, 0);
+    r.v = u32x4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
+  }
+}
+template <bool kVec>
+__device__ __forceinline__ void load8(Raw<float>& r, __amdgpu_buffer_rsrc_t rs, int c, int cols) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if (kVec || cols >= 8) {
+      const uint32_t at = c < cols ? 4u * (kVec ? c : min(c, cols - 8)) + 16u * h : kOOB;
+      r.v[h] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, at, 0, 0));
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int k = c + 4 * h + j;
+        r.v[h][j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, k < cols ? 4u * k : kOOB, 0, 0));
+      }
+    }
+  }
+}
+
+template <bool kVec>
+__device__ __forceinline__ void values8(const Raw<uint16_t>& r, int c, int cols, float* v) {
+  u32x4 x = r.v;
+  if (!kVec && cols >= 8 && c + 8 > cols && c < cols) x = qk::drop_front8(x, c + 8 - cols);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     v[2 * j] = __uint_as_float(x[j] << 16);
     v[2 * j + 1] = __uint_as_float(x[j] & 0xFFFF0000u);
   }
 }
-__device__ __forceinline__ void load8(const float* row, int c, int cols, float* v) {
-  if (c + 8 <= cols) {
-    const f32x4 a = *(const f32x4_a4*)(row + c), b = *(const f32x4_a4*)(row + c + 4);
+template <bool kVec>
+__device__ __forceinline__ void values8(const Raw<float>& r, int c, int cols, float* v) {
+  f32x4 a = r.v[0], b = r.v[1];
+  if (!kVec && cols >= 8 && c + 8 > cols && c < cols) qk::drop_front8(a, b, c + 8 - cols);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[j] = a[j];
-      v[4 + j] = b[j];
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = c + j < cols ? row[c + j] : 0.0f;
+  for (int j = 0; j < 4; ++j) {
+    v[j] = a[j];
+    v[4 + j] = b[j];
   }
 }
 
@@ -43,11 +89,14 @@ __device__ __forceinline__ u32x4 pack8(const float* v) {
                qk::pack_bf16x2(v[6], v[7])};
 }
 
+template <bool kVec>
 __device__ __forceinline__ void store8(uint16_t* row, int c, int cols, const float* v) {
-  qk::store8_row(row + c, pack8(v), min(8, cols - c));
+  if constexpr (kVec) *(u32x4*)(row + c) = pack8(v);
+  else qk::store8_row(row + c, pack8(v), min(8, cols - c));
 }
+template <bool kVec>
 __device__ __forceinline__ void store8(float* row, int c, int cols, const float* v) {
-  if (c + 8 <= cols) {
+  if (kVec || c + 8 <= cols) {
     *(f32x4_a4*)(row + c) = f32x4{v[0], v[1], v[2], v[3]};
     *(f32x4_a4*)(row + c + 4) = f32x4{v[4], v[5], v[6], v[7]};
   } else {
@@ -68,82 +117,119 @@ __device__ __forceinline__ void round8(const uint16_t*, float* v) {
 }
 __device__ __forceinline__ void round8(const float*, float*) {}
 
-// Eight weights, fp32 or bf16.
-__device__ __forceinline__ void weight8(const void* w, bool bf16, int c, int cols, float* v) {
-  if (bf16) load8((const uint16_t*)w, c, cols, v);
-  else load8((const float*)w, c, cols, v);
-}
-
-// The sum of v over the kRow threads of a row, in all of them.  slot: kRow / 64 floats (unused for a wave).
+// Sums of two values over the kRow threads of a row, in all of them.  slot: two floats for each of the row's waves, not
+// those of the call before: its readers need not be done (one barrier a call).
 template <int kRow>
-__device__ __forceinline__ float row_sum(float v, float* slot) {
+__device__ __forceinline__ void row_sums(float& a, float& b, f32x4* slot) {
 #pragma unroll
-  for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o, 64);
-  if constexpr (kRow > 64) {
-    const int w = threadIdx.x >> 6;
-    __syncthreads();                       // the slots' last readers are done
-    if ((threadIdx.x & 63) == 0) slot[w] = v;
-    __syncthreads();
-    v = slot[0];
-#pragma unroll
-    for (int i = 1; i < kRow / 64; ++i) v += slot[i];
+  for (int o = 1; o < 64; o <<= 1) {
+    a += __shfl_xor(a, o, 64);
+    b += __shfl_xor(b, o, 64);
   }
-  return v;
+  if constexpr (kRow > 64) {
+    float* s = (float*)slot;
+    const int w = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0) {
+      s[2 * w] = a;
+      s[2 * w + 1] = b;
+    }
+    __syncthreads();
+    a = s[0];
+    b = s[1];
+#pragma unroll
+    for (int i = 1; i < kRow / 64; ++i) {
+      a += s[2 * i];
+      b += s[2 * i + 1];
+    }
+  }
 }
 
 // 1 / sqrt(sum / cols + eps): once a row, in fp64, so that it is off by its rounding alone.
-__device__ __forceinline__ float inverse_rms(float sum, int cols, float eps) {
-  return (float)(1.0 / sqrt((double)sum / cols + (double)eps));
+__device__ __forceinline__ float inverse_rms(float sum, double per, float eps) {
+  return (float)rsqrt((double)sum * per + (double)eps);
 }
+
+struct Norm {
+  int64_t rows;
+  int cols;
+  const void* w;
+  bool w_bf16;
+  float eps;
+};
+
+// A weight's chunk, fp32 or bf16.
+struct Weight {
+  Raw<float> f;
+  Raw<uint16_t> h;
+};
+template <bool kVec>
+__device__ __forceinline__ void load_w(Weight& r, const Norm& n, int c) {
+  if (n.w_bf16) load8<kVec>(r.h, rsrc(n.w, 2 * (uint64_t)n.cols), c, n.cols);
+  else load8<kVec>(r.f, rsrc(n.w, 4 * (uint64_t)n.cols), c, n.cols);
+}
+template <bool kVec>
+__device__ __forceinline__ void values_w(const Weight& r, const Norm& n, int c, float* v) {
+  if (n.w_bf16) values8<kVec>(r.h, c, n.cols, v);
+  else values8<kVec>(r.f, c, n.cols, v);
+}
+
+template <int kRow>
+constexpr int threads() { return kRow < 256 ? 256 : kRow; }
 
 // kRow threads a row (four rows a work group of 256 if 64), kC chunks a thread.  S may be X or R
 // (no __restrict__; a thread has read what it overwrites, and of other threads' columns uses none).
-template <typename T, int kRow, int kC>
-__global__ __launch_bounds__(kRow < 256 ? 256 : kRow) void k_norm_fwd(const T* X, const T* R, int64_t rows, int cols,
-                                                                     const void* __restrict__ w, bool w_bf16, float eps,
-                                                                     T* S, uint16_t* __restrict__ Y,
-                                                                     uint8_t* __restrict__ codes,
-                                                                     uint8_t* __restrict__ scales) {
-  constexpr int kRows = kRow < 256 ? 256 / kRow : 1;
-  __shared__ float slot[kRow / 64];
-  const int t = threadIdx.x % kRow;
+template <typename T, int kRow, int kC, bool kVec>
+__global__ __launch_bounds__(threads<kRow>()) void k_norm_fwd(const T* X, const T* R, Norm n, T* S,
+                                                             uint16_t* __restrict__ Y, uint8_t* __restrict__ codes,
+                                                             uint8_t* __restrict__ scales) {
+  constexpr int kRows = threads<kRow>() / kRow;
+  __shared__ f32x4 slot[2][kRow / 64];
+  const int t = threadIdx.x % kRow, cols = n.cols;
+  const double per = 1.0 / cols;
+  Weight w[kC];
+#pragma unroll
+  for (int i = 0; i < kC; ++i) load_w<kVec>(w[i], n, 8 * (t + kRow * i));
   // a row (four) a work group while the launch can count them; m is uniform over a row's threads
-  for (int64_t m = (int64_t)blockIdx.x * kRows + threadIdx.x / kRow; m < rows; m += (int64_t)gridDim.x * kRows) {
-    float v[kC][8], u[kC][8];
+  int turn = 0;
+  const int64_t first = (int64_t)blockIdx.x * kRows + __builtin_amdgcn_readfirstlane(threadIdx.x / kRow);
+  for (int64_t m = first; m < n.rows; m += (int64_t)gridDim.x * kRows, turn ^= 1) {
+    Raw<T> x[kC], u[kC];
+    const __amdgpu_buffer_rsrc_t rx = rsrc(X + m * cols, sizeof(T) * (uint64_t)cols),
+                                 rr = rsrc(R ? R + m * cols : X, R ? sizeof(T) * (uint64_t)cols : 0);
 #pragma unroll
     for (int i = 0; i < kC; ++i) {
-      const int c = 8 * (t + kRow * i);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = u[i][j] = 0.0f;
-      if (c < cols) {
-        load8(X + m * cols, c, cols, v[i]);
-        if (R) load8(R + m * cols, c, cols, u[i]);
-      }
+      load8<kVec>(x[i], rx, 8 * (t + kRow * i), cols);
+      load8<kVec>(u[i], rr, 8 * (t + kRow * i), cols);     // zeros without R
     }
-    float sum = 0.0f;
+    float v[kC][8];
+    float sum = 0.0f, none = 0.0f;
 #pragma unroll
     for (int i = 0; i < kC; ++i) {
       const int c = 8 * (t + kRow * i);
-      if (R && c < cols) {
+      values8<kVec>(x[i], c, cols, v[i]);
+      if (R) {
+        float a[8];
+        values8<kVec>(u[i], c, cols, a);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] += u[i][j];
-        round8(X, v[i]);                     // the norm is that of the sum as stored, which the backward reads
-        store8(S + m * cols, c, cols, v[i]);
+        for (int j = 0; j < 8; ++j) v[i][j] += a[j];
+        round8(X, v[i]);                   // the norm is that of the sum as stored, which the backward reads
+        if (c < cols) store8<kVec>(S + m * cols, c, cols, v[i]);
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) sum = fmaf(v[i][j], v[i][j], sum);
     }
-    const float inv = inverse_rms(row_sum<kRow>(sum, slot), cols, eps);
+    row_sums<kRow>(sum, none, slot[turn]);
+    const float inv = inverse_rms(sum, per, n.eps);
     const int pc = (int)mx8::padded(cols);
 #pragma unroll
     for (int i = 0; i < kC; ++i) {
       const int c = 8 * (t + kRow * i);
       if (c >= pc) break;
       float y[8];
-      if (c < cols) weight8(w, w_bf16, c, cols, y);
+      values_w<kVec>(w[i], n, c, y);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = c + j < cols ? v[i][j] * y[j] * inv : 0.0f;   // bf16 times bf16 is exact
-      if (Y && c < cols) store8(Y + m * cols, c, cols, y);
+      for (int j = 0; j < 8; ++j) y[j] = v[i][j] * y[j] * inv;      // bf16 times bf16 is exact; zeros past the end
+      if (Y && c < cols) store8<kVec>(Y + m * cols, c, cols, y);
       if (codes) {
         uint32_t top = 0;
 #pragma unroll
@@ -158,59 +244,78 @@ __global__ __launch_bounds__(kRow < 256 ? 256 : kRow) void k_norm_fwd(const T* X
   }
 }
 
-// A work group takes rows blockIdx.x, + gridDim.x, .. and keeps its share of dw in registers; the
-// shares, part[gridDim.x rows][cols], are added in order by k_norm_dw.  dX may be dS or S.
-template <typename T, int kRow, int kC>
-__global__ __launch_bounds__(kRow < 256 ? 256 : kRow) void k_norm_bwd(const uint16_t* __restrict__ dY, const T* S,
-                                                                     const T* dS, int64_t rows, int cols,
-                                                                     const void* __restrict__ w, bool w_bf16, float eps,
-                                                                     T* dX, float* __restrict__ part) {
-  constexpr int kRows = kRow < 256 ? 256 / kRow : 1;
-  __shared__ float slot[2][kRow / 64];
-  const int t = threadIdx.x % kRow;
-  float dw[kC][8], k[kC][8];
+// A work group takes rows blockIdx.x, + gridDim.x, .., the next one's in flight while it finishes
+// one, and keeps its share of dw in registers; the shares, part[gridDim.x][cols], are added
+// in order by k_norm_dw.  dX may be dS or S.
+template <typename T, int kRow, int kC, bool kVec>
+__global__ __launch_bounds__(threads<kRow>()) void k_norm_bwd(const uint16_t* __restrict__ dY, const T* S, const T* dS,
+                                                             Norm n, T* dX, float* __restrict__ part) {
+  constexpr int kRows = threads<kRow>() / kRow;
+  __shared__ f32x4 slot[2][kRow / 64];
+  const int t = threadIdx.x % kRow, cols = n.cols;
+  const double per = 1.0 / cols;
+  float dw[kC][8] = {};
+  Weight w[kC];
 #pragma unroll
-  for (int i = 0; i < kC; ++i) {
-    const int c = 8 * (t + kRow * i);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) dw[i][j] = k[i][j] = 0.0f;
-    if (c < cols) weight8(w, w_bf16, c, cols, k[i]);
-  }
-  const int64_t first = (int64_t)blockIdx.x * kRows + threadIdx.x / kRow;
-  for (int64_t m = first; m < rows; m += (int64_t)gridDim.x * kRows) {
-    float s[kC][8], d[kC][8], g[kC][8];
+  for (int i = 0; i < kC; ++i) load_w<kVec>(w[i], n, 8 * (t + kRow * i));
+  struct Row {
+    Raw<T> s[kC], g[kC];
+    Raw<uint16_t> d[kC];
+  };
+  auto load = [&](int64_t m) {
+    Row q;
+    const bool in = m < n.rows;            // past the last row: descriptors of no bytes
+    const uint64_t len = in ? (uint64_t)cols : 0;
+    const __amdgpu_buffer_rsrc_t rs = rsrc(in ? S + m * cols : S, sizeof(T) * len), rd = rsrc(in ? dY + m * cols : dY, 2 * len),
+                                 rg = rsrc(in && dS ? dS + m * cols : S, dS ? sizeof(T) * len : 0);
 #pragma unroll
     for (int i = 0; i < kC; ++i) {
       const int c = 8 * (t + kRow * i);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) s[i][j] = d[i][j] = g[i][j] = 0.0f;
-      if (c < cols) {
-        load8(S + m * cols, c, cols, s[i]);
-        load8(dY + m * cols, c, cols, d[i]);
-        if (dS) load8(dS + m * cols, c, cols, g[i]);
-      }
+      load8<kVec>(q.s[i], rs, c, cols);
+      load8<kVec>(q.d[i], rd, c, cols);
+      load8<kVec>(q.g[i], rg, c, cols);    // zeros without dS
     }
+    return q;
+  };
+  int turn = 0;
+  int64_t m = (int64_t)blockIdx.x * kRows + __builtin_amdgcn_readfirstlane(threadIdx.x / kRow);
+  Row cur = load(m);
+  for (; m < n.rows; m += (int64_t)gridDim.x * kRows, turn ^= 1) {
+    const Row nxt = load(m + (int64_t)gridDim.x * kRows);
     float sum = 0.0f, dot = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kC; ++i)
+    for (int i = 0; i < kC; ++i) {
+      const int c = 8 * (t + kRow * i);
+      float s[8], d[8], k[8];
+      values8<kVec>(cur.s[i], c, cols, s);
+      values8<kVec>(cur.d[i], c, cols, d);
+      values_w<kVec>(w[i], n, c, k);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        sum = fmaf(s[i][j], s[i][j], sum);
-        dot = fmaf(s[i][j] * k[i][j], d[i][j], dot);
+        sum = fmaf(s[j], s[j], sum);
+        dot = fmaf(s[j] * k[j], d[j], dot);
       }
-    const float inv = inverse_rms(row_sum<kRow>(sum, slot[0]), cols, eps);
-    const float mean = (float)((double)row_sum<kRow>(dot, slot[1]) * inv / cols);   // of n d
+    }
+    row_sums<kRow>(sum, dot, slot[turn]);
+    const float inv = inverse_rms(sum, per, n.eps);
+    const float mean = (float)((double)dot * inv * per);   // of n d
 #pragma unroll
     for (int i = 0; i < kC; ++i) {
       const int c = 8 * (t + kRow * i);
+      float s[8], d[8], k[8], g[8];
+      values8<kVec>(cur.s[i], c, cols, s);
+      values8<kVec>(cur.d[i], c, cols, d);
+      values_w<kVec>(w[i], n, c, k);
+      values8<kVec>(cur.g[i], c, cols, g);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float n = s[i][j] * inv;
-        dw[i][j] = fmaf(n, d[i][j], dw[i][j]);
-        g[i][j] = fmaf(inv, k[i][j] * d[i][j] - n * mean, g[i][j]);
+        const float nj = s[j] * inv;
+        dw[i][j] = fmaf(nj, d[j], dw[i][j]);
+        g[j] = fmaf(inv, k[j] * d[j] - nj * mean, g[j]);
       }
-      if (dX && c < cols) store8(dX + m * cols, c, cols, g[i]);
+      if (dX && c < cols) store8<kVec>(dX + m * cols, c, cols, g);
     }
+    cur = nxt;
   }
   if (!part) return;
   if constexpr (kRows > 1) {               // the waves' shares, added in order
@@ -230,7 +335,7 @@ __global__ __launch_bounds__(kRow < 256 ? 256 : kRow) void k_norm_bwd(const uint
 #pragma unroll
     for (int i = 0; i < kC; ++i) {
       const int c = 8 * (t + kRow * i);
-      if (c < cols) store8(part + (int64_t)blockIdx.x * cols, c, cols, dw[i]);
+      if (c < cols) store8<kVec>(part + (int64_t)blockIdx.x * cols, c, cols, dw[i]);
     }
   }
 }
@@ -244,10 +349,11 @@ __global__ __launch_bounds__(1024) void k_norm_dw(const float* __restrict__ part
   if (c < cols) {
     const int per = (shares + 15) / 16, end = min(shares, per * (w + 1));
     int i = per * w;
-    for (; i + 4 <= end; i += 4) {
-      const float a = part[(int64_t)i * cols + c], b = part[(int64_t)(i + 1) * cols + c];
-      const float d = part[(int64_t)(i + 2) * cols + c], e = part[(int64_t)(i + 3) * cols + c];
-      u += (a + b) + (d + e);
+    for (; i + 8 <= end; i += 8) {
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = part[(int64_t)(i + k) * cols + c];
+      u += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
     }
     for (; i < end; ++i) u += part[(int64_t)i * cols + c];
   }
@@ -261,46 +367,50 @@ __global__ __launch_bounds__(1024) void k_norm_dw(const float* __restrict__ part
 }
 
 int64_t shares_of(int64_t rows, int64_t cols) {
-  const int64_t per = cols <= 2048 ? 4 : 1;
+  const int64_t per = cols <= 1024 ? 4 : 1;
   return std::min<int64_t>((rows + per - 1) / per, 512);
 }
 
+// Calls f with the threads of a row and the chunks of a thread.
+template <typename F>
+void by_columns(int64_t cols, F f) {
+  if (cols <= 512) f(std::integral_constant<int, 64>{}, std::integral_constant<int, 1>{});
+  else if (cols <= 1024) f(std::integral_constant<int, 64>{}, std::integral_constant<int, 2>{});
+  else if (cols <= 2048) f(std::integral_constant<int, 256>{}, std::integral_constant<int, 1>{});
+  else if (cols <= 4096) f(std::integral_constant<int, 256>{}, std::integral_constant<int, 2>{});
+  else if (cols <= 8192) f(std::integral_constant<int, 512>{}, std::integral_constant<int, 2>{});
+  else if (cols <= 16384) f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 2>{});
+  else f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 4>{});
+}
+
 template <typename T>
-hipError_t fwd(const T* X, const T* R, int64_t rows, int cols, const void* w, bool w_bf16, float eps, T* S, uint16_t* Y,
-               uint8_t* codes, uint8_t* scales, hipStream_t s) {
-#define QL_NORM(R_, C_)                                                                                             \
-  hipLaunchKernelGGL((k_norm_fwd<T, R_, C_>), dim3((unsigned)std::min<int64_t>(R_ == 64 ? (rows + 3) / 4 : rows, 1 << 20)),  \
-                     dim3(R_ < 256 ? 256 : R_), 0, s, X, R, rows, cols, w, w_bf16, eps, S, Y, codes, scales)
-  if (cols <= 512) QL_NORM(64, 1);
-  else if (cols <= 1024) QL_NORM(64, 2);
-  else if (cols <= 2048) QL_NORM(64, 4);
-  else if (cols <= 4096) QL_NORM(256, 2);
-  else if (cols <= 8192) QL_NORM(256, 4);
-  else if (cols <= 16384) QL_NORM(1024, 2);
-  else QL_NORM(1024, 4);
-#undef QL_NORM
+hipError_t fwd(const T* X, const T* R, const Norm& n, T* S, uint16_t* Y, uint8_t* codes, uint8_t* scales, hipStream_t s) {
+  by_columns(n.cols, [&](auto row, auto chunks) {
+    constexpr int kRow = decltype(row)::value, kC = decltype(chunks)::value, kRows = threads<kRow>() / kRow;
+    const dim3 grid((unsigned)std::min<int64_t>((n.rows + kRows - 1) / kRows, 1 << 20));
+    if (n.cols % 8 == 0)
+      hipLaunchKernelGGL((k_norm_fwd<T, kRow, kC, true>), grid, dim3(threads<kRow>()), 0, s, X, R, n, S, Y, codes, scales);
+    else
+      hipLaunchKernelGGL((k_norm_fwd<T, kRow, kC, false>), grid, dim3(threads<kRow>()), 0, s, X, R, n, S, Y, codes, scales);
+  });
   return hipGetLastError();
 }
 
 template <typename T>
-hipError_t bwd(const uint16_t* dY, const T* S, const T* dS, int64_t rows, int cols, const void* w, bool w_bf16, float eps,
-               T* dX, float* dw, float* ws, hipStream_t s) {
-  const int shares = (int)shares_of(rows, cols);
+hipError_t bwd(const uint16_t* dY, const T* S, const T* dS, const Norm& n, T* dX, float* dw, float* ws, hipStream_t s) {
+  const int shares = (int)shares_of(n.rows, n.cols);
   float* part = dw ? ws : nullptr;
-#define QL_NORM(R_, C_)                                                                                            \
-  hipLaunchKernelGGL((k_norm_bwd<T, R_, C_>), dim3((unsigned)shares), dim3(R_ < 256 ? 256 : R_), 0, s, dY, S, dS,  \
-                     rows, cols, w, w_bf16, eps, dX, part)
-  if (cols <= 512) QL_NORM(64, 1);
-  else if (cols <= 1024) QL_NORM(64, 2);
-  else if (cols <= 2048) QL_NORM(64, 4);
-  else if (cols <= 4096) QL_NORM(256, 2);
-  else if (cols <= 8192) QL_NORM(256, 4);
-  else if (cols <= 16384) QL_NORM(1024, 2);
-  else QL_NORM(1024, 4);
-#undef QL_NORM
+  by_columns(n.cols, [&](auto row, auto chunks) {
+    constexpr int kRow = decltype(row)::value, kC = decltype(chunks)::value;
+    const dim3 grid((unsigned)shares);
+    if (n.cols % 8 == 0)
+      hipLaunchKernelGGL((k_norm_bwd<T, kRow, kC, true>), grid, dim3(threads<kRow>()), 0, s, dY, S, dS, n, dX, part);
+    else
+      hipLaunchKernelGGL((k_norm_bwd<T, kRow, kC, false>), grid, dim3(threads<kRow>()), 0, s, dY, S, dS, n, dX, part);
+  });
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !dw) return e;
-  hipLaunchKernelGGL(k_norm_dw, dim3((unsigned)((cols + 63) / 64)), dim3(1024), 0, s, ws, shares, cols, dw);
+  hipLaunchKernelGGL(k_norm_dw, dim3((unsigned)((n.cols + 63) / 64)), dim3(1024), 0, s, ws, shares, n.cols, dw);
   return hipGetLastError();
 }
 
@@ -308,16 +418,16 @@ hipError_t bwd(const uint16_t* dY, const T* S, const T* dS, int64_t rows, int co
 
 hipError_t launch_norm_fwd(const void* X, const void* R, bool bf16, int64_t rows, int64_t cols, const void* w, bool w_bf16,
                            float eps, void* S, uint16_t* Y, uint8_t* codes, uint8_t* scales, hipStream_t s) {
-  if (bf16)
-    return fwd((const uint16_t*)X, (const uint16_t*)R, rows, (int)cols, w, w_bf16, eps, (uint16_t*)S, Y, codes, scales, s);
-  return fwd((const float*)X, (const float*)R, rows, (int)cols, w, w_bf16, eps, (float*)S, Y, codes, scales, s);
+  const Norm n{rows, (int)cols, w, w_bf16, eps};
+  if (bf16) return fwd((const uint16_t*)X, (const uint16_t*)R, n, (uint16_t*)S, Y, codes, scales, s);
+  return fwd((const float*)X, (const float*)R, n, (float*)S, Y, codes, scales, s);
 }
 
 size_t norm_bwd_ws(int64_t rows, int64_t cols) { return (size_t)shares_of(rows, cols) * cols * sizeof(float); }
 
 hipError_t launch_norm_bwd(const uint16_t* dY, const void* S, const void* dS, bool bf16, int64_t rows, int64_t cols,
                            const void* w, bool w_bf16, float eps, void* dX, float* dw, float* ws, hipStream_t s) {
-  if (bf16)
-    return bwd(dY, (const uint16_t*)S, (const uint16_t*)dS, rows, (int)cols, w, w_bf16, eps, (uint16_t*)dX, dw, ws, s);
-  return bwd(dY, (const float*)S, (const float*)dS, rows, (int)cols, w, w_bf16, eps, (float*)dX, dw, ws, s);
+  const Norm n{rows, (int)cols, w, w_bf16, eps};
+  if (bf16) return bwd(dY, (const uint16_t*)S, (const uint16_t*)dS, n, (uint16_t*)dX, dw, ws, s);
+  return bwd(dY, (const float*)S, (const float*)dS, n, (float*)dX, dw, ws, s);
 }
