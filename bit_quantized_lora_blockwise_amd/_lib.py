@@ -859,6 +859,11 @@ def _mx8_packed(packed, name, rows, cols):
     if not isinstance(packed, (tuple, list)) or len(packed) != 2:
         raise TypeError(f"{name} must be the pair (codes, scales) of a packed matrix")
     sc, ss = _mx8_shapes(rows, cols)
+    codes, scales = packed
+    if (isinstance(codes, torch.Tensor) and codes.shape == sc and codes.dtype == torch.uint8 and codes.is_contiguous()
+            and isinstance(scales, torch.Tensor) and scales.shape == ss and scales.dtype == torch.uint8
+            and scales.is_contiguous()):
+        return packed
     _need(packed[0], f"{name} codes", torch.uint8, shape=sc)
     _need(packed[1], f"{name} scales", torch.uint8, shape=ss)
     return packed
@@ -894,7 +899,15 @@ def mx8_dequantize(codes, scales, rows, cols, out=None, stream=None):
 
 # --- root-mean-square norm --------------------------------------------------------
 
+_NORM_DTYPES = {torch.float32: QL_F32, torch.bfloat16: QL_BF16}
+
+
 def _norm_args(X, weight, name):
+    if (isinstance(X, torch.Tensor) and isinstance(weight, torch.Tensor) and X.dim() == 2 and X.dtype in _NORM_DTYPES
+            and weight.dtype in _NORM_DTYPES and weight.shape == X.shape[1:] and X.is_contiguous()
+            and weight.is_contiguous()):
+        rows, cols = X.shape
+        return rows, cols, _NORM_DTYPES[X.dtype], _NORM_DTYPES[weight.dtype]
     if not isinstance(X, torch.Tensor) or X.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError(f"{name} must be a float32 or bfloat16 torch.Tensor")
     _need(X, name, X.dtype, ndim=2)
@@ -902,7 +915,7 @@ def _norm_args(X, weight, name):
     if not isinstance(weight, torch.Tensor) or weight.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError("weight must be a float32 or bfloat16 torch.Tensor")
     _need(weight, "weight", weight.dtype, shape=(cols,))
-    return rows, cols, QL_BF16 if X.dtype == torch.bfloat16 else QL_F32, QL_BF16 if weight.dtype == torch.bfloat16 else QL_F32
+    return rows, cols, _NORM_DTYPES[X.dtype], _NORM_DTYPES[weight.dtype]
 
 
 def rms_norm_fwd(X, weight, eps, residual=None, Y=None, S=None, mx8=None, stream=None):

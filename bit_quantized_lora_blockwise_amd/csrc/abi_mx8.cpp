@@ -5,6 +5,7 @@
 
 #include "abi_util.h"
 #include "mx8.h"
+#include "side_stream.h"
 
 namespace {
 
@@ -48,17 +49,45 @@ FwdWs fwd_ws(int64_t M, int64_t K, int64_t F, int r) {
   return w;
 }
 
-// Backward: [dZ (gated)][G][its planes][T with their pitch][fp32 partials, of G and then of the gradients].
+// Whether a linear's G goes to dX for few rows as slices, which it adds up itself (a launch less).
+bool few_dx_ok(int64_t M, int64_t K, int r) { return (M + 15) / 16 * ((r + 15) / 16) <= 24 && dx_small_ok(M, K); }
+
+// Backward: [dZ (gated)][G][its planes][fp32 partials, of G and then of the gradients].
 struct BwdWs {
-  size_t dz, g, planes, tp, part, total;
+  size_t dz, g, planes, part, total;
 };
 BwdWs bwd_ws(int64_t M, int64_t K, int64_t N, int halves, int r) {
-  const size_t low = (size_t)halves * M * g_pitch(r) * 2;
   BwdWs w{halves == 2 ? round_up((size_t)M * glu_ldz(N) * 2) : 0, round_up((size_t)halves * M * r * 2),
-          round_up(3 * low), r == g_pitch(r) ? 0 : round_up(low), 0, 0};
-  w.part = round_up(std::max(halves == 2 ? glu_back_ws(M, N, r) : lora_skinny_ws(M, N, r), grads8_ws(M, K, N, halves, r)));
-  w.total = w.dz + w.g + w.planes + w.tp + w.part;
+          round_up((size_t)3 * halves * M * g_pitch(r) * 2), 0, 0};
+  const size_t slices = halves == 2 ? glu_back_ws(M, N, r) : few_dx_ok(M, K, r) ? std::max(mx4_small_ws(M, r), lora_skinny_ws(M, N, r))
+                                                                                : lora_skinny_ws(M, N, r);
+  w.part = round_up(std::max(slices, grads8_ws(M, K, N, halves, r)));
+  w.total = w.dz + w.g + w.planes + w.part;
   return w;
+}
+
+// Whether the large-tile dX product [M, K] leaves the last round of its persistent grid partly empty: the
+// adapter's gradients, which need nothing of it, then take those CUs from the second stream, as in qlora_linear_bwd.
+SideStream* beside_dx(int64_t M, int64_t K) {
+  SideStream* sd = side_stream();
+  if (!sd) return nullptr;
+  const int64_t tiles = (M + 255) / 256 * ((K + 255) / 256), grid = sd->cus / 8 * 8;
+  return tiles > grid && tiles % grid != 0 ? sd : nullptr;
+}
+
+// dX on `s` by `product`, then the gradients on `s` or, with sd, on the second stream beside it.
+template <typename F, typename G>
+int dx_and_grads(SideStream* sd, hipStream_t s, F product, G grads) {
+  if (!sd) {
+    QL_TRY(product());
+    QL_TRY(grads(s));
+    return QL_OK;
+  }
+  QL_TRY(hipEventRecord(sd->fork, s));
+  QL_TRY(product());
+  QL_TRY(hipStreamWaitEvent(sd->s, sd->fork, 0));
+  QL_TRY(join_side(*sd, s, grads(sd->s)));
+  return QL_OK;
 }
 
 }  // namespace
@@ -183,18 +212,24 @@ int qlora_swiglu_bwd(const uint8_t* x_codes, const uint8_t* x_scales, const uint
   uint16_t* dZ = (uint16_t*)ws;
   uint16_t* G = (uint16_t*)(ws + w.dz);
   uint16_t* planes = (uint16_t*)(ws + w.dz + w.g);
-  uint16_t* Tp = (uint16_t*)(ws + w.dz + w.g + w.planes);
-  float* part = (float*)(ws + w.dz + w.g + w.planes + w.tp);
+  float* part = (float*)(ws + w.dz + w.g + w.planes);
   int slices = 0;
-  QL_TRY(launch_glu_back(dH, M, F, gu_codes, gu_scales, L2, r, dZ, part, &slices, s));
-  QL_TRY(launch_low(Low{part, slices, lora_scale, T, G, planes, Tp}, 2, M, r, s));
-  if (dX && dx_small_ok(M, K))
-    QL_TRY(launch_dx_small(dZ, M, K, 2 * F, codes, c2, c1, G, nullptr, 0, nullptr, L1, r, dX, kNoDrop, s, glu_ldz(F), 2));
-  else if (dX)
-    QL_TRY(launch_qgemm_big(true, dZ, M, K, 2 * F, codes, c2, c1, G, L1, r, 1.0f, dX, s, 2, nullptr, glu_ldz(F)));
-  QL_TRY(launch_grads8(Grads8{x_codes, x_scales, dH, gu_codes, gu_scales, planes, w.tp ? Tp : T, lora_scale, dL1, dL2}, M, K,
-                       F, 2, r, part, s));
-  return QL_OK;
+  QL_TRY(launch_glu_back(dH, M, F, gu_codes, gu_scales, L2, r, lora_scale, dZ, part, &slices, s));
+  const bool small = dx_small_ok(M, K), sums = dX && small && slices <= kSmallSlices;
+  if (!sums) QL_TRY(launch_low(Low{part, slices, 1.0f, G, planes}, 2, M, r, s));
+  auto product = [&] {
+    if (!dX) return hipSuccess;
+    // G's planes from the product for few rows where it adds the slices up: a launch less
+    if (small)
+      return launch_dx_small(dZ, M, K, 2 * F, codes, c2, c1, sums ? nullptr : G, part, slices, planes, L1, r, dX, kNoDrop, s,
+                             glu_ldz(F), 2);
+    return launch_qgemm_big(true, dZ, M, K, 2 * F, codes, c2, c1, G, L1, r, 1.0f, dX, s, 2, nullptr, glu_ldz(F));
+  };
+  auto grads = [&](hipStream_t st) {
+    return launch_grads8(Grads8{x_codes, x_scales, dH, gu_codes, gu_scales, planes, T, lora_scale, dL1, dL2}, M, K, F, 2, r,
+                         part, st);
+  };
+  return dx_and_grads(dX && !small ? beside_dx(M, K) : nullptr, s, product, grads);
 }
 
 size_t qlora_linear_bwd_mx8_workspace(int64_t M, int64_t K, int64_t N, int r) {
@@ -215,22 +250,24 @@ int qlora_linear_bwd_mx8(const uint8_t* x_codes, const uint8_t* x_scales, const 
   char* ws = (char*)workspace;
   uint16_t* G = (uint16_t*)ws;
   uint16_t* planes = (uint16_t*)(ws + w.g);
-  uint16_t* Tp = (uint16_t*)(ws + w.g + w.planes);
-  float* part = (float*)(ws + w.g + w.planes + w.tp);
+  float* part = (float*)(ws + w.g + w.planes);
   int slices = 0;
-  QL_TRY(launch_lora_slices(dY, M, N, L2, false, r, part, &slices, s));
-  QL_TRY(launch_low(Low{part, slices, lora_scale, T, G, planes, Tp}, 1, M, r, s));
-  if (dX) {
-    if (dx_small_ok(M, K))
-      QL_TRY(launch_dx_small(dY, M, K, N, codes, c2, c1, G, nullptr, 0, nullptr, L1, r, dX, kNoDrop, s));
-    else if (qgemm_big_ok(true, M, K, N))
-      QL_TRY(launch_qgemm_big(true, dY, M, K, N, codes, c2, c1, G, L1, r, 1.0f, dX, s));
-    else
-      QL_TRY(launch_qgemm_dx(dY, M, K, N, codes, c2, c1, G, L1, r, dX, s));
-  }
-  QL_TRY(launch_grads8(Grads8{x_codes, x_scales, dY, nullptr, nullptr, planes, w.tp ? Tp : T, lora_scale, dL1, dL2}, M, K, N,
-                       1, r, part, s));
-  return QL_OK;
+  const bool few = few_dx_ok(M, K, r), small = dx_small_ok(M, K), big = qgemm_big_ok(true, M, K, N);
+  if (few) QL_TRY(launch_small_slices(dY, M, N, L2, false, r, kNoDrop, lora_scale, part, &slices, s));
+  else QL_TRY(launch_lora_slices(dY, M, N, L2, false, r, part, &slices, s));
+  if (!dX || !few) QL_TRY(launch_low(Low{part, slices, few ? 1.0f : lora_scale, G, planes}, 1, M, r, s));
+  auto product = [&] {
+    if (!dX) return hipSuccess;
+    if (small)
+      return launch_dx_small(dY, M, K, N, codes, c2, c1, few ? nullptr : G, part, slices, planes, L1, r, dX, kNoDrop, s);
+    if (big) return launch_qgemm_big(true, dY, M, K, N, codes, c2, c1, G, L1, r, 1.0f, dX, s);
+    return launch_qgemm_dx(dY, M, K, N, codes, c2, c1, G, L1, r, dX, s);
+  };
+  auto grads = [&](hipStream_t st) {
+    return launch_grads8(Grads8{x_codes, x_scales, dY, nullptr, nullptr, planes, T, lora_scale, dL1, dL2}, M, K, N, 1, r, part,
+                         st);
+  };
+  return dx_and_grads(dX && !small && big ? beside_dx(M, K) : nullptr, s, product, grads);
 }
 
 }  // extern "C"

@@ -35,16 +35,16 @@ __device__ __forceinline__ bf16x8 load8(__amdgpu_buffer_rsrc_t rs, uint32_t at, 
   return __builtin_bit_cast(bf16x8, u32x4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16});
 }
 
-// Elements c .. c + 7 of row m of T or G from its S <= kSlices fp32 slices [M][r], added in order.
-constexpr int kSlices = 8;
-__device__ __forceinline__ void sum8(__amdgpu_buffer_rsrc_t rp, int S, int M, int r, int m, int c, float (&sum)[8]) {
+// Elements c .. c + 7 of row m of T or G from its S <= kSlices fp32 slices [M][r], `next` elements apart, added in order.
+constexpr int kSlices = kSmallSlices;
+__device__ __forceinline__ void sum8(__amdgpu_buffer_rsrc_t rp, int S, int M, int r, int m, int c, int next, float (&sum)[8]) {
   const uint32_t at = 4u * (uint32_t)(m * r + c);
 #pragma unroll
   for (int k = 0; k < 8; k += 4) {
     u32x4 v[kSlices];                    // slices past the last read as zeros
 #pragma unroll
     for (int n = 0; n < kSlices; ++n)
-      v[n] = __builtin_amdgcn_raw_buffer_load_b128(rp, n < S && m < M && c < r ? at + 4u * k : kOOB, 4 * n * M * r, 0);
+      v[n] = __builtin_amdgcn_raw_buffer_load_b128(rp, n < S && m < M && c < r ? at + 4u * k : kOOB, 4 * n * next, 0);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       float u = __uint_as_float(v[0][j]);
@@ -56,7 +56,8 @@ __device__ __forceinline__ void sum8(__amdgpu_buffer_rsrc_t rp, int S, int M, in
 }
 
 // kVec: ldy % 8 == 0 (rows of dY in whole 16-byte pieces, zeros from N to ldy); kVecR: r % 8 == 0; kSum: G
-// as slices.  halves: of W's stacked rows, each with a G [M][r] and an L1 [K][r] of its own.
+// as slices.  halves: of W's stacked rows, each with a G [M][r] (slices [S][halves][M][r], planes [halves][3][M][..])
+// and an L1 [K][r] of its own.
 template <bool kVec, bool kVecR, bool kSum>
 __global__ __launch_bounds__(64 * kW) void k_dx_small(const uint16_t* __restrict__ dY, int M, int K, int N,
                                                       const uint8_t* __restrict__ codes,
@@ -123,7 +124,7 @@ __global__ __launch_bounds__(64 * kW) void k_dx_small(const uint16_t* __restrict
     const int pitch = (r + 7) / 8 * 8;
     const int64_t plane = (int64_t)M * pitch;
     for (int half = 0; half < halves; ++half) {
-    const __amdgpu_buffer_rsrc_t rg = kSum ? rsrc(Gp, (uint64_t)M * r * 4 * S)
+    const __amdgpu_buffer_rsrc_t rg = kSum ? rsrc(Gp + (int64_t)half * M * r, (uint64_t)M * r * 4 * (S * halves - half))
                                            : rsrc(G + (int64_t)half * M * r, (uint64_t)M * r * 2),
                                  rl = rsrc(L1 + ((int64_t)half * K + first) * r, (uint64_t)32 * r * 2);
 #pragma unroll
@@ -134,7 +135,7 @@ __global__ __launch_bounds__(64 * kW) void k_dx_small(const uint16_t* __restrict
       bf16x8 b;
       if constexpr (kSum) {
         float sum[8];
-        sum8(rg, S, M, r, m, c, sum);
+        sum8(rg, S, M, r, m, c, halves * M * r, sum);
         u32x4 v[3];                                // the planes: each what those before it rounded off
 #pragma unroll
         for (int n = 0; n < 3; ++n)
@@ -147,7 +148,7 @@ __global__ __launch_bounds__(64 * kW) void k_dx_small(const uint16_t* __restrict
         b = __builtin_bit_cast(bf16x8, v[0]);
         if (blockIdx.x == 0 && w == 0 && m < M && c < pitch)
 #pragma unroll
-          for (int n = 0; n < 3; ++n) *(u32x4*)(planes + n * plane + (int64_t)m * pitch + c) = v[n];
+          for (int n = 0; n < 3; ++n) *(u32x4*)(planes + (3 * half + n) * plane + (int64_t)m * pitch + c) = v[n];
       } else {
         b = load8<kVecR>(rg, (uint32_t)(m * r + c) * 2u, m < M ? r - c : 0);
       }
@@ -264,7 +265,7 @@ __global__ __launch_bounds__(64 * kW) void k_fwd_small(const uint16_t* __restric
       bf16x8 b;
       if constexpr (kSum) {
         float sum[8];
-        sum8(rt, S, M, r, m, c, sum);
+        sum8(rt, S, M, r, m, c, M * r, sum);
         u32x4 v;
 #pragma unroll
         for (int k = 0; k < 4; ++k) v[k] = qk::pack_bf16x2(sum[2 * k], sum[2 * k + 1]);
@@ -387,7 +388,7 @@ __global__ __launch_bounds__(64 * (kW + 2 * kI)) void k_glu_small(const uint16_t
       bf16x8 b[2];
       if constexpr (kSum) {
         float v[8];
-        sum8(rt, S, M, r, m, c, v);
+        sum8(rt, S, M, r, m, c, M * r, v);
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
           u32x4 p;

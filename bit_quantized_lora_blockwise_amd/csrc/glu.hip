@@ -44,22 +44,16 @@ __global__ __launch_bounds__(kT) void k_t_planes(const float* __restrict__ part,
 }
 
 // ---- Gr's planes ---------------------------------------------------------------------
-// The slices of Gr summed in order, scaled: bf16 [halves][M][r] and three planes [halves][3][M][rp]; and,
-// where r is not its pitch rp, T with that pitch.  kN columns a thread (16-byte loads if 4).
+// The slices of Gr summed in order, scaled: bf16 [halves][M][r] and three planes [halves][3][M][rp].  kN columns a
+// thread (16-byte loads if 4).
 template <int kN>
 __global__ __launch_bounds__(kT) void k_low(Low q, int halves, int64_t M, int r, int rp) {
   const int h = blockIdx.y;
-  const bool is_t = blockIdx.z == 1;
   const int64_t pitch = (int64_t)halves * M * r, n = M * rp;
   for (int64_t i = kN * ((int64_t)blockIdx.x * kT + threadIdx.x); i < n; i += (int64_t)kN * gridDim.x * kT) {
     const int64_t m = i / rp;
     const int c = (int)(i - m * rp);
     const int64_t at = ((int64_t)h * M + m) * r + c;
-    if (is_t) {
-#pragma unroll
-      for (int j = 0; j < kN; ++j) q.Tp[h * n + i + j] = c + j < r ? q.T[at + j] : 0;
-      continue;
-    }
     float x[kN] = {};
     if (c < r) {                           // kN = 4: r is a multiple of 4, and so all four or none
       const float* p = q.part + at;
@@ -121,7 +115,7 @@ template <bool kVec>
 __global__ __launch_bounds__(kBT, 4) void k_glu_back(const uint16_t* __restrict__ dH, int M, int F,
                                                      const uint8_t* __restrict__ codes,
                                                      const uint8_t* __restrict__ scales,
-                                                     const uint16_t* __restrict__ L2, int r, int chunk, int ldz,
+                                                     const uint16_t* __restrict__ L2, int r, float scale, int chunk, int ldz,
                                                      uint16_t* __restrict__ dZ, float* __restrict__ part) {
   __shared__ __attribute__((aligned(16))) uint16_t lds[6 * kBM * kBPitch];      // [half][plane][row][column]
   const int t = threadIdx.x, w = __builtin_amdgcn_readfirstlane(t >> 6), l = t & 63, hl = l >> 5;
@@ -208,11 +202,12 @@ __global__ __launch_bounds__(kBT, 4) void k_glu_back(const uint16_t* __restrict_
 #pragma unroll
   for (int e = 0; e < 16; ++e) {
     const int mm = kBM * (int)blockIdx.x + qk::acc_row(e);
-    if (mm < M && c < r) part[(((int64_t)blockIdx.y * 2 + wh) * M + mm) * r + c] = acc[e] + red[64 * e];
+    if (mm < M && c < r) part[(((int64_t)blockIdx.y * 2 + wh) * M + mm) * r + c] = scale * (acc[e] + red[64 * e]);
   }
 }
 
-// Slices of that pass: about 512 work groups, but no more than 32 slices to add up for each row.
+// Slices of that pass: about 512 work groups, but no more than 32 slices to add up for each row, and as many
+// as the product for few rows adds up itself where the pass is short all the same (up to four steps).
 struct PlanBack {
   int tiles, slices;
   int64_t chunk;
@@ -220,7 +215,7 @@ struct PlanBack {
 PlanBack plan_back(int64_t M, int64_t F) {
   PlanBack p;
   p.tiles = (int)((M + kBM - 1) / kBM);
-  const int64_t steps = (F + kBC - 1) / kBC, s = std::max<int64_t>(1, std::min<int64_t>({512 / p.tiles, steps, 32}));
+  const int64_t steps = (F + kBC - 1) / kBC, s = std::max<int64_t>(1, std::min<int64_t>({512 / p.tiles, steps, steps <= 4 * kSmallSlices ? kSmallSlices : 32}));
   p.chunk = (steps + s - 1) / s * kBC;
   p.slices = (int)((F + p.chunk - 1) / p.chunk);
   return p;
@@ -240,23 +235,22 @@ hipError_t launch_t_planes(const float* part, int64_t pitch, int slices, int hal
 
 hipError_t launch_low(const Low& q, int halves, int64_t M, int r, hipStream_t s) {
   const int rp = g_pitch(r);
-  const unsigned z = rp == r ? 1 : 2;
   if (r % 4 == 0)
-    hipLaunchKernelGGL(k_low<4>, dim3(blocks(M * rp / 4), (unsigned)halves, z), dim3(kT), 0, s, q, halves, M, r, rp);
+    hipLaunchKernelGGL(k_low<4>, dim3(blocks(M * rp / 4), (unsigned)halves), dim3(kT), 0, s, q, halves, M, r, rp);
   else
-    hipLaunchKernelGGL(k_low<1>, dim3(blocks(M * rp), (unsigned)halves, z), dim3(kT), 0, s, q, halves, M, r, rp);
+    hipLaunchKernelGGL(k_low<1>, dim3(blocks(M * rp), (unsigned)halves), dim3(kT), 0, s, q, halves, M, r, rp);
   return hipGetLastError();
 }
 
 size_t glu_back_ws(int64_t M, int64_t F, int r) { return (size_t)plan_back(M, F).slices * 2 * M * r * sizeof(float); }
 
 hipError_t launch_glu_back(const uint16_t* dH, int64_t M, int64_t F, const uint8_t* gu_codes, const uint8_t* gu_scales,
-                           const uint16_t* L2, int r, uint16_t* dZ, float* part, int* slices, hipStream_t s) {
+                           const uint16_t* L2, int r, float scale, uint16_t* dZ, float* part, int* slices, hipStream_t s) {
   const PlanBack p = plan_back(M, F);
   *slices = p.slices;
   const dim3 grid((unsigned)p.tiles, (unsigned)p.slices);
 #define QL_BACK(V)                                                                                                      \
-  hipLaunchKernelGGL(k_glu_back<V>, grid, dim3(kBT), 0, s, dH, (int)M, (int)F, gu_codes, gu_scales, L2, r, (int)p.chunk, \
+  hipLaunchKernelGGL(k_glu_back<V>, grid, dim3(kBT), 0, s, dH, (int)M, (int)F, gu_codes, gu_scales, L2, r, scale, (int)p.chunk, \
                      (int)glu_ldz(F), dZ, part)
   if (F % 8 == 0) QL_BACK(true);
   else QL_BACK(false);

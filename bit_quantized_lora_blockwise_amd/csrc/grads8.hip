@@ -35,13 +35,24 @@ static_assert(6 * kGABytes + 2 * kGBBytes <= kLds, "the gated step fits");
 using glu::kOOB;
 using glu::rsrc;
 
+// Ranks c .. c + 7 of a row of T [M][r]; kVecR: r % 8 == 0.
+template <bool kVecR>
+__device__ __forceinline__ u32x4 load_t(__amdgpu_buffer_rsrc_t rt, int m, int c, int r, bool on) {
+  const uint32_t at = 2u * (uint32_t)(m * r + c);
+  if constexpr (kVecR) return __builtin_amdgcn_raw_buffer_load_b128(rt, on && c < r ? at : kOOB, 0, 0);
+  uint32_t e[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) e[j] = __builtin_amdgcn_raw_buffer_load_b16(rt, on && c + j < r ? at + 2 * j : kOOB, 0, 0);
+  return u32x4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
+}
+
 enum Kind { kPacked, kDense, kGated };
 
 struct Job {
   const uint8_t* codes;     // kPacked: X; kGated: G over U
   const uint8_t* scales;
   const uint16_t* d;        // kDense: dY; kGated: dH
-  const uint16_t* B;        // [planes][M][rp]; kGated: [2][M][rp]
+  const uint16_t* B;        // kPacked: [planes][M][rp]; kDense: [M][r]; kGated: [2][M][r]
   int P, tiles, slices;
   int rows;                 // of a slice, a multiple of kM
   float* out;               // [slices] of P r (kGated: 2 P r) values
@@ -65,7 +76,7 @@ __device__ __forceinline__ bf16x8 frag_a(const LDS_AS uint8_t* a, int m0, int p0
 }
 
 // kVec (dense): rows of d in whole 16-byte pieces.
-template <Kind kKind, bool kVec>
+template <Kind kKind, bool kVec, bool kVecR>
 __device__ __forceinline__ void columns(const Job& jb, int M, int r, int rp, int tile, int slice, LDS_AS uint8_t* lds) {
   constexpr int kPlanes = kKind == kPacked ? 3 : 1;
   constexpr int kPieces = kKind == kPacked ? 2 : 4;
@@ -77,7 +88,7 @@ __device__ __forceinline__ void columns(const Job& jb, int M, int r, int rp, int
   const __amdgpu_buffer_rsrc_t rs = rsrc(jb.scales, kKind == kPacked ? (uint64_t)M * nb : 0);
   __amdgpu_buffer_rsrc_t rb[kPlanes];      // one plane stays below 2^31 bytes, all together need not
 #pragma unroll
-  for (int j = 0; j < kPlanes; ++j) rb[j] = rsrc(jb.B + (int64_t)j * M * rp, (uint64_t)M * rp * 2);
+  for (int j = 0; j < kPlanes; ++j) rb[j] = rsrc(jb.B + (int64_t)j * M * rp, (uint64_t)M * (kKind == kPacked ? rp : r) * 2);
   const int brow = t >> 3, bc = t & 7;
   struct Regs {
     u32x4 a[kPieces], b[kPlanes];
@@ -98,9 +109,12 @@ __device__ __forceinline__ void columns(const Job& jb, int M, int r, int rp, int
       }
     }
 #pragma unroll
-    for (int j = 0; j < kPlanes; ++j)
-      g.b[j] = __builtin_amdgcn_raw_buffer_load_b128(
-          rb[j], m + brow < m_end && 8 * bc < rp ? (uint32_t)((m + brow) * rp + 8 * bc) * 2u : kOOB, 0, 0);
+    for (int j = 0; j < kPlanes; ++j) {
+      if constexpr (kKind == kPacked)
+        g.b[j] = __builtin_amdgcn_raw_buffer_load_b128(
+            rb[j], m + brow < m_end && 8 * bc < rp ? (uint32_t)((m + brow) * rp + 8 * bc) * 2u : kOOB, 0, 0);
+      else g.b[j] = load_t<kVecR>(rb[j], m + brow, 8 * bc, r, m + brow < m_end);
+    }
     return g;
   };
   auto store = [&](const Regs& g) {
@@ -178,8 +192,8 @@ __device__ __forceinline__ void columns(const Job& jb, int M, int r, int rp, int
   }
 }
 
-template <bool kVec>
-__device__ __forceinline__ void gated(const Job& jb, int M, int r, int rp, int tile, int slice, LDS_AS uint8_t* lds) {
+template <bool kVec, bool kVecR>
+__device__ __forceinline__ void gated(const Job& jb, int M, int r, int tile, int slice, LDS_AS uint8_t* lds) {
   const int t = threadIdx.x, w = __builtin_amdgcn_readfirstlane(t >> 6), l = t & 63;
   const int wp = w & 3, wh = w >> 2;
   const int p0 = tile * kGP, m_beg = slice * jb.rows, m_end = min(M, m_beg + jb.rows);
@@ -190,7 +204,7 @@ __device__ __forceinline__ void gated(const Job& jb, int M, int r, int rp, int t
   // thread t: row t / 16, columns 8 (t % 16); of T half t / 256, row t / 8 % 32, ranks 8 (t % 8)
   const int row = t >> 4, piece = t & 15, p = p0 + 8 * piece;
   const int bh = t >> 8, brow = (t >> 3) & 31, bc = t & 7;
-  const __amdgpu_buffer_rsrc_t rb = rsrc(jb.B + (int64_t)__builtin_amdgcn_readfirstlane(bh) * M * rp, (uint64_t)M * rp * 2);
+  const __amdgpu_buffer_rsrc_t rb = rsrc(jb.B + (int64_t)__builtin_amdgcn_readfirstlane(bh) * M * r, (uint64_t)M * r * 2);
   struct Regs {
     u32x2 g, u;
     u32x4 d, b;
@@ -206,8 +220,7 @@ __device__ __forceinline__ void gated(const Job& jb, int M, int r, int rp, int t
     s.sg = __builtin_amdgcn_raw_buffer_load_b8(rs, os, 0, 0);
     s.su = __builtin_amdgcn_raw_buffer_load_b8(rs, in ? os + up_s : kOOB, 0, 0);
     s.d = glu::load8<kVec>(rd, (uint32_t)m * jb.P * 2u, p, jb.P, m < m_end);
-    s.b = __builtin_amdgcn_raw_buffer_load_b128(
-        rb, m0 + brow < m_end && 8 * bc < rp ? (uint32_t)((m0 + brow) * rp + 8 * bc) * 2u : kOOB, 0, 0);
+    s.b = load_t<kVecR>(rb, m0 + brow, 8 * bc, r, m0 + brow < m_end);
     return s;
   };
   auto store = [&](const Regs& s) {
@@ -264,19 +277,19 @@ __device__ __forceinline__ void gated(const Job& jb, int M, int r, int rp, int t
 }
 
 // Work groups: dL1's tiles and slices (for a gated product of one half, then of the other), then dL2's.
-template <bool kGlu, bool kVec>
+template <bool kGlu, bool kVec, bool kVecR>
 __global__ __launch_bounds__(kT, 4) void k_grads8(Job j0, Job j0u, Job j1, int M, int r, int rp) {
   __shared__ __attribute__((aligned(16))) uint8_t lds[kLds];
   const int n0 = j0.tiles * j0.slices;
   int b = (int)blockIdx.x;
-  if (b < n0) return columns<kPacked, true>(j0, M, r, rp, b % j0.tiles, b / j0.tiles, (LDS_AS uint8_t*)lds);
+  if (b < n0) return columns<kPacked, true, true>(j0, M, r, rp, b % j0.tiles, b / j0.tiles, (LDS_AS uint8_t*)lds);
   b -= n0;
   if constexpr (kGlu) {
-    if (b < n0) return columns<kPacked, true>(j0u, M, r, rp, b % j0.tiles, b / j0.tiles, (LDS_AS uint8_t*)lds);
+    if (b < n0) return columns<kPacked, true, true>(j0u, M, r, rp, b % j0.tiles, b / j0.tiles, (LDS_AS uint8_t*)lds);
     b -= n0;
-    gated<kVec>(j1, M, r, rp, b % j1.tiles, b / j1.tiles, (LDS_AS uint8_t*)lds);
+    gated<kVec, kVecR>(j1, M, r, b % j1.tiles, b / j1.tiles, (LDS_AS uint8_t*)lds);
   } else {
-    columns<kDense, kVec>(j1, M, r, rp, b % j1.tiles, b / j1.tiles, (LDS_AS uint8_t*)lds);
+    columns<kDense, kVec, kVecR>(j1, M, r, rp, b % j1.tiles, b / j1.tiles, (LDS_AS uint8_t*)lds);
   }
 }
 
@@ -324,7 +337,8 @@ Plan plan(int64_t P, int width, int64_t M, int groups) {
   Plan p;
   p.tiles = (int)((P + width - 1) / width);
   const int64_t steps = (M + kM - 1) / kM;
-  const int64_t s = std::max<int64_t>(1, std::min<int64_t>(groups / p.tiles, steps));
+  // up to four steps stay in one slice: their sum would be a launch of its own
+  const int64_t s = steps <= 4 ? 1 : std::max<int64_t>(1, std::min<int64_t>(groups / p.tiles, steps));
   const int64_t per = (steps + s - 1) / s;
   p.rows = (int)(per * kM);
   p.slices = (int)((steps + per - 1) / per);
@@ -361,14 +375,17 @@ hipError_t launch_grads8(const Grads8& g, int64_t M, int64_t K, int64_t N, int h
                 p.x.slices > 1 ? px[h] : g.dL1 + h * nx, 1.0f};
   const Job jz{g.gu_codes, g.gu_scales, g.d, g.T, (int)N, p.z.tiles, p.z.slices, p.z.rows, p.z.slices > 1 ? pz : g.dL2, g.scale};
   const dim3 grid((unsigned)(halves * p.x.tiles * p.x.slices + p.z.tiles * p.z.slices));
-#define QL_G8(G, V) hipLaunchKernelGGL((k_grads8<G, V>), grid, dim3(kT), 0, s, jx[0], jx[1], jz, (int)M, r, rp)
-  if (halves == 2) {
-    if (N % 8 == 0) QL_G8(true, true);
-    else QL_G8(true, false);
-  } else {
-    if (N % 8 == 0) QL_G8(false, true);
-    else QL_G8(false, false);
-  }
+#define QL_G8(G, V, R) hipLaunchKernelGGL((k_grads8<G, V, R>), grid, dim3(kT), 0, s, jx[0], jx[1], jz, (int)M, r, rp)
+#define QL_G8V(G)                          \
+  do {                                     \
+    if (N % 8 == 0 && r % 8 == 0) QL_G8(G, true, true); \
+    else if (N % 8 == 0) QL_G8(G, true, false);         \
+    else if (r % 8 == 0) QL_G8(G, false, true);         \
+    else QL_G8(G, false, false);           \
+  } while (0)
+  if (halves == 2) QL_G8V(true);
+  else QL_G8V(false);
+#undef QL_G8V
 #undef QL_G8
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || (p.x.slices == 1 && p.z.slices == 1)) return e;

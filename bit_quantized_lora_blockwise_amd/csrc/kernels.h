@@ -241,8 +241,9 @@ hipError_t launch_fwd_small(const uint16_t* X, int64_t M, int64_t K, int64_t N, 
                             const float* c1, const uint16_t* T, const float* Tp, int S, uint16_t* T_out,
                             const uint16_t* L2, int r, float scale, uint16_t* Y, hipStream_t s);
 // dX = bf16(dY W' + D o (G L1^T)) from G, or with G = nullptr from its slices Gp (S of them), added
-// here; `planes` then receives it to 24 bits.  ldy, halves (G given): rows of dY ldy elements apart, zeros
-// behind N (0: dense); W's rows in that many halves with a G and an L1 each.
+// here; `planes` then receives it to 24 bits.  ldy, halves: rows of dY ldy elements apart, zeros behind N
+// (0: dense); W's rows in that many halves with a G (slices [S][halves][M][r]) and an L1 each.
+constexpr int kSmallSlices = 8;   // of T and G that the products for few rows add up
 bool dx_small_ok(int64_t M, int64_t K);
 hipError_t launch_dx_small(const uint16_t* dY, int64_t M, int64_t K, int64_t N, const uint8_t* codes, const uint8_t* c2,
                            const float* c1, const uint16_t* G, const float* Gp, int S, uint16_t* planes,
@@ -292,29 +293,26 @@ hipError_t launch_lora_slices(const uint16_t* A, int64_t M, int64_t R, const uin
 hipError_t launch_t_planes(const float* part, int64_t pitch, int slices, int halves, int64_t M, int r, uint16_t* planes,
                            uint16_t* T_out, hipStream_t s);
 
-// The rank-r operands of the backward's last products: G = scale (the sum of its slices) as bf16 and as
-// three planes whose sum is G to 24 bits, and T with the planes' pitch where r is not that.
+// G = scale (the sum of its slices) as bf16 and as three planes whose sum is G to 24 bits.
 struct Low {
   const float* part;      // fp32 slices [slices][halves][M][r]
   int slices;
   float scale;
-  const uint16_t* T;      // [halves][M][r]
   uint16_t* G;            // [halves][M][r]
   uint16_t* planes;       // [halves][3][M][g_pitch(r)]
-  uint16_t* Tp;           // [halves][M][g_pitch(r)], unused if r is its pitch
 };
 hipError_t launch_low(const Low& q, int halves, int64_t M, int r, hipStream_t s);
 
 // dZ = the gradients of G and U from dH and their 8-bit copies: bf16 [M][glu_ldz(F)], gate columns first,
-// zeros past 2 F; and the fp32 slices of dZ L2^T, [*slices][2][M][r].
+// zeros past 2 F; and the fp32 slices of scale dZ L2^T, [*slices][2][M][r].
 inline int64_t glu_ldz(int64_t F) { return (2 * F + 7) / 8 * 8; }
 size_t glu_back_ws(int64_t M, int64_t F, int r);
 hipError_t launch_glu_back(const uint16_t* dH, int64_t M, int64_t F, const uint8_t* gu_codes, const uint8_t* gu_scales,
-                           const uint16_t* L2, int r, uint16_t* dZ, float* part, int* slices, hipStream_t s);
+                           const uint16_t* L2, int r, float scale, uint16_t* dZ, float* part, int* slices, hipStream_t s);
 
 // The adapter's gradients from packed activations (grads8.hip), in one launch and one for the slices' sums:
-//   dL1 [halves][K, r] = X^T G (X packed, G as planes);  dL2 [halves][r, N] = scale T^T dZ (T with the planes'
-//   pitch), where dZ is dY [M, N] (halves = 1) or formed again from dH and the packed G and U in fp32 (halves = 2).
+//   dL1 [halves][K, r] = X^T G (X packed, G as planes);  dL2 [halves][r, N] = scale T^T dZ, where dZ is dY [M, N]
+//   (halves = 1) or formed again from dH and the packed G and U in fp32 (halves = 2).
 struct Grads8 {
   const uint8_t* x_codes;
   const uint8_t* x_scales;
