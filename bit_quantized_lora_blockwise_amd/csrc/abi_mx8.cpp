@@ -44,7 +44,7 @@ struct FwdWs {
 };
 FwdWs fwd_ws(int64_t M, int64_t K, int64_t F, int r) {
   FwdWs w{0, round_up(few_ok(M, K, F, r) ? mx4_small_ws(M, r) : lora_skinny_ws(M, K, r)), 0};
-  if (!few_ok(M, K, F, r)) w.planes = round_up((size_t)4 * M * g_pitch(r) * 2);
+  if (!few_ok(M, K, F, r)) w.planes = round_up((size_t)6 * M * g_pitch(r) * 2);
   w.total = w.planes + 2 * w.part;
   return w;
 }

@@ -155,9 +155,11 @@ __device__ __forceinline__ bf16x8 frag_kmajor_sw(const LDS_AS uint16_t* base, in
 // never leave its registers, but for their 8-bit copies when the caller keeps them.  The
 // products are taken with their operands exchanged, so that a lane holds 16 of 32
 // consecutive columns of one row: the copies' block scales and the stores of 16 bytes
-// then take register swaps between the wave's halves alone.  LA holds T as two bf16
-// planes for each half (16 bits of it: G and U are rounded to 8 bits, and a T of 8 bits
-// would put one in 300 of their codes on the other side of a border).
+// then take register swaps between the wave's halves alone.  LA holds T as three bf16
+// planes for each half, 24 bits of it: G and U are rounded to 8 bits, and a T of 8 bits
+// would put one in 300 of their codes on the other side of a border, one of 16 bits one in
+// 20000, six times as many as the sums themselves.  The planes go straight to LDS in the
+// activation tile's layout.
 // kDrop (dX): the adapter term is D o (G L1^T).  All waves draw the tile's decisions
 // into LDS (a bit an element) while the LoRA operands arrive (by the producers alone,
 // one wave a SIMD, the draws took 12 us a tile), and the consumers apply them to the
@@ -216,8 +218,7 @@ __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict_
   LDS_AS uint16_t* b1 = (LDS_AS uint16_t*)lds_b + kBufElems;
   LDS_AS uint16_t* a0 = (LDS_AS uint16_t*)lds_a0;
   LDS_AS uint16_t* a1 = (LDS_AS uint16_t*)lds_a1;
-  LDS_AS uint16_t* la2 = la + kBM * kPL;   // kGlu: T's second plane; L2 goes to an activation buffer, free then too
-  static_assert(2 * kBM * kPL <= 2 * kBufElems, "two planes fit the B buffers");
+  static_assert(2 * kBM * kBR <= 2 * kBufElems, "two of T's planes fit the B buffers");
   const int64_t nsteps = (R + kBR - 1) / kBR;
 
   if (producer) {
@@ -373,34 +374,40 @@ __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict_
     Stage hA, hB, h0;
     if constexpr (kDrop) drop::fill_bits<kBM, kBP>((LDS_AS uint8_t*)mask, dp, m0, p0, t, kT);
     if constexpr (kGlu) {
-      const int rp = (r + 7) / 8 * 8;   // g_pitch
+      // T's planes of a half into the B buffers and the first activation buffer, all free now,
+      // as dma_tile sends activations; L2 into the second
+      const int rp = (r + 7) / 8 * 8;      // g_pitch
       for (int g = 0; g < 2; ++g) {
-        const uint16_t* ts = LA + (int64_t)g * 2 * M * rp;
         const uint16_t* l2 = LB + (int64_t)g * r * P;
-        u32x4 v[2][8], u[4];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int idx = tp + 256 * i, row = idx >> 3, cc = (idx & 7) * 8;
-          const bool ok = m0 + row < M && cc < rp;
-#pragma unroll
-          for (int n = 0; n < 2; ++n)
-            v[n][i] = ok ? *(const u32x4*)(ts + ((int64_t)n * M + m0 + row) * rp + cc) : u32x4{0, 0, 0, 0};
-        }
+        u32x4 u[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int idx = tp + 256 * i, c = idx >> 4, pp = (idx & 15) * 8;
           u[i] = c < r && p0 + pp < P ? qk::load8_row(l2 + (int64_t)c * P, p0 + pp, P) : u32x4{0, 0, 0, 0};
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int idx = tp + 256 * i;
-          *(LDS_AS u32x4*)(la + (idx >> 3) * kPL + (idx & 7) * 8) = v[0][i];
-          *(LDS_AS u32x4*)(la2 + (idx >> 3) * kPL + (idx & 7) * 8) = v[1][i];
+        for (int n = 0; n < 3; ++n) {
+          const uint64_t base = (uint64_t)(uintptr_t)(LA + ((int64_t)(3 * g + n) * M + m0) * rp);
+          const uint16_t* pt = (const uint16_t*)(((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(base >> 32)) << 32) |
+                                                 (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)base));
+          const __amdgpu_buffer_rsrc_t rt = rsrc(pt, (uint32_t)__builtin_amdgcn_readfirstlane((int)((M - m0) * rp * 2)));
+          LDS_AS uint16_t* buf = n == 2 ? a0 : b0 + n * kBM * kBR;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const uint32_t dst = (uint32_t)(uintptr_t)(buf + (64 * pw + 8 * j) * kBR);
+            const uint32_t vo = 8 * (int)achunk[j & 1] < rp ? (uint32_t)((64 * pw + 8 * j + (l >> 3)) * rp * 2) + 16u * achunk[j & 1] : kOOB;
+            uint32_t m0_saved;
+            asm volatile(
+                "s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\tbuffer_load_dwordx4 %2, %3, 0 offen lds\n\ts_mov_b32 m0, %0"
+                : "=&s"(m0_saved)
+                : "s"(__builtin_amdgcn_readfirstlane(dst)), "v"(vo), "s"(rt)
+                : "memory");
+          }
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int idx = tp + 256 * i;
-          *(LDS_AS u32x4*)(a0 + (idx >> 4) * kPG + (idx & 15) * 8) = u[i];
+          *(LDS_AS u32x4*)(a1 + (idx >> 4) * kPG + (idx & 15) * 8) = u[i];
         }
         __builtin_amdgcn_s_waitcnt(0x0070);
         __builtin_amdgcn_s_barrier();
@@ -599,12 +606,12 @@ __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict_
         if (s < ksteps) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const bf16x8 b = qk::frag_kmajor(a0, kPG, 16 * s, 64 * ch + 32 * j);
+            const bf16x8 b = qk::frag_kmajor(a1, kPG, 16 * s, 64 * ch + 32 * j);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              acc[i][2 * g + j] = qk::mfma32(b, qk::frag_rowmajor(la, kPL, 64 * rg + 32 * i, 16 * s), acc[i][2 * g + j]);
-              acc[i][2 * g + j] = qk::mfma32(b, qk::frag_rowmajor(la2, kPL, 64 * rg + 32 * i, 16 * s), acc[i][2 * g + j]);
-            }
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int n = 0; n < 3; ++n)
+                acc[i][2 * g + j] = qk::mfma32(b, afrag(n == 2 ? a0 : b0 + n * kBM * kBR, s, i), acc[i][2 * g + j]);
           }
         }
       }

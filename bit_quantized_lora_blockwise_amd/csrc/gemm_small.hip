@@ -301,8 +301,8 @@ __global__ __launch_bounds__(64 * kW) void k_fwd_small(const uint16_t* __restric
 // The gated product for few rows: H = bf16(silu(G) U), [G | U] = X W'^T + s T L2 for a stacked
 // W [2 F, K].  As k_fwd_small, for 32 kI rows and the same 32 columns of both halves; 2 kI more
 // waves form the adapter's term of one half of 32 rows each meanwhile, add the eight waves'
-// sums in order and finish.  T enters as two bf16 planes (16 bits: G and U may be
-// kept in 8): given [2 halves][2][M][pitch], or kSum: formed here from its slices [2][S][M][r].
+// sums in order and finish.  T enters as three bf16 planes (24 bits: G and U may be
+// kept in 8): given [2 halves][3][M][pitch], or kSum: formed here from its slices [2][S][M][r].
 template <int kI, bool kSum>
 __global__ __launch_bounds__(64 * (kW + 2 * kI)) void k_glu_small(const uint16_t* __restrict__ X, int M, int K, int F,
                                                        const uint8_t* __restrict__ codes,
@@ -373,9 +373,9 @@ __global__ __launch_bounds__(64 * (kW + 2 * kI)) void k_glu_small(const uint16_t
   if (w >= kW) {
     const int pitch = (r + 7) / 8 * 8;
     const uint16_t* l2 = L2 + (int64_t)j * r * F;
-    const uint16_t* t = T + (int64_t)j * 2 * M * pitch;      // its two planes
+    const uint16_t* t = T + (int64_t)j * 3 * M * pitch;      // its planes
     const __amdgpu_buffer_rsrc_t rt = kSum ? rsrc(Tp + (int64_t)j * S * M * r, (uint64_t)M * r * 4 * S)
-                                           : rsrc(t, (uint64_t)M * pitch * 4);
+                                           : rsrc(t, (uint64_t)M * pitch * 6);
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       const int c = 16 * s + 8 * h;
@@ -385,30 +385,24 @@ __global__ __launch_bounds__(64 * (kW + 2 * kI)) void k_glu_small(const uint16_t
       for (int k = 0; k < 8; ++k) e[k] = c + k < r && n0 + x < F ? l2[(int64_t)(c + k) * F + n0 + x] : 0;
       const bf16x8 a = __builtin_bit_cast(
           bf16x8, u32x4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16});
-      bf16x8 b[2];
+      bf16x8 b[3];
       if constexpr (kSum) {
         float v[8];
         sum8(rt, S, M, r, m, c, M * r, v);
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          u32x4 p;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            p[k] = qk::pack_bf16x2(v[2 * k], v[2 * k + 1]);
-            v[2 * k] -= __uint_as_float(p[k] << 16);
-            v[2 * k + 1] -= __uint_as_float(p[k] & 0xFFFF0000u);
-          }
+        for (int n = 0; n < 3; ++n) {
+          const u32x4 p = glu::take_plane(v);
           b[n] = __builtin_bit_cast(bf16x8, p);
           if (n == 0 && T_out && n0 == 0 && m < M && c < r)
             qk::store8_row(T_out + ((int64_t)j * M + m) * r + c, p, min(8, r - c));
         }
       } else {
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < 3; ++n)
           b[n] = load8<true>(rt, ((uint32_t)(n * M + m) * pitch + c) * 2u, m < M && c < pitch ? 8 : 0);
       }
-      sum = qk::mfma32(a, b[0], sum);
-      sum = qk::mfma32(a, b[1], sum);
+#pragma unroll
+      for (int n = 0; n < 3; ++n) sum = qk::mfma32(a, b[n], sum);
     }
     sum = scale * sum;
   }

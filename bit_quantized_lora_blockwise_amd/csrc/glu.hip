@@ -27,7 +27,7 @@ __global__ __launch_bounds__(kT) void k_t_planes(const float* __restrict__ part,
                                                  uint16_t* __restrict__ T_out) {
   const int h = blockIdx.y;
   part += h * pitch;
-  planes += h * 2 * M * rp;
+  planes += h * 3 * M * rp;
   for (int64_t i = (int64_t)blockIdx.x * kT + threadIdx.x; i < M * rp; i += (int64_t)gridDim.x * kT) {
     const int64_t m = i / rp;
     const int c = (int)(i - m * rp);
@@ -37,8 +37,12 @@ __global__ __launch_bounds__(kT) void k_t_planes(const float* __restrict__ part,
       for (int k = 0; k < slices; ++k) x += p[k * M * r];
     }
     const uint16_t hi = qk::f32_to_bf16(x);
-    planes[i] = hi;
-    planes[M * rp + i] = qk::f32_to_bf16(x - qk::bf16_to_f32(hi));
+#pragma unroll
+    for (int n = 0; n < 3; ++n) {
+      const uint16_t b = qk::f32_to_bf16(x);
+      planes[n * M * rp + i] = b;
+      x -= qk::bf16_to_f32(b);
+    }
     if (T_out && c < r) T_out[(h * M + m) * r + c] = hi;
   }
 }

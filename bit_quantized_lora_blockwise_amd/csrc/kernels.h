@@ -267,7 +267,7 @@ hipError_t launch_norm_bwd(const uint16_t* dY, const void* S, const void* dS, bo
                            const void* w, bool w_bf16, float eps, void* dX, float* dw, float* ws, hipStream_t s);
 
 // --- gated product over the stacked gate|up base (gemm_big.hip, glu.hip) ----------
-// H [M, F] = bf16(silu(G) U), [G | U] = X W'^T + scale T L2 for W [2 F, K]; T: two planes
+// H [M, F] = bf16(silu(G) U), [G | U] = X W'^T + scale T L2 for W [2 F, K]; T: three planes
 // [M][g_pitch(r)] for each half; G and U in 8 bits too when gu_codes is given.
 hipError_t launch_glu_big(const uint16_t* X, int64_t M, int64_t K, int64_t F, const uint8_t* codes, const uint8_t* c2,
                           const float* c1, const uint16_t* T, const uint16_t* L2, int r, float scale, uint16_t* H,
@@ -288,7 +288,7 @@ hipError_t launch_glu_decode(const uint16_t* X, int64_t M, int64_t K, int64_t F,
 // ws as lora_skinny_ws(M, R, r).
 hipError_t launch_lora_slices(const uint16_t* A, int64_t M, int64_t R, const uint16_t* B, bool b_is_kr, int r, float* ws,
                               int* slices, hipStream_t s);
-// Slices of T for `halves` products (part + h pitch floats each) to its two bf16 planes [halves][2][M][g_pitch(r)]
+// Slices of T for `halves` products (part + h pitch floats each) to its three bf16 planes [halves][3][M][g_pitch(r)]
 // and, when T_out is given, bf16(T) [halves][M][r].
 hipError_t launch_t_planes(const float* part, int64_t pitch, int slices, int halves, int64_t M, int r, uint16_t* planes,
                            uint16_t* T_out, hipStream_t s);

@@ -512,8 +512,9 @@ int rms_norm_bwd(const uint16_t* dY, const void* S, const void* dS, int x_dtype,
  *        dL1 = fp32(X^T B), dL2 = fp32(lora_scale * T^T dZ) (2 consecutive blocks each)
  *        X is the packed 8-bit copy of the forward's input (from rms_norm_fwd or
  *        mx8_quantize), T the forward's T_out.
- * G and U are taken at their full fp32 sums and T to 16 bits in the forward. In the backward
- * dZ and B are kept to 24 bits for dL1 and dL2 and rounded to bf16 for dX. M from one row on,
+ * G and U are taken at their full fp32 sums, with T to 24 bits (16 where 8-bit copies are not
+ * asked for and M <= 16). In the backward dZ and B are kept to 24 bits for dL1 and dL2 and
+ * rounded to bf16 for dX. M from one row on,
  * any F, K % 64 == 0, 1 <= r <= 64; X, dZ (M rows of 2 F, to a multiple of 8, bf16), the
  * codes, L1 and L2 must each stay below 2^31 bytes. Workspaces from the queries.             */
 size_t qlora_swiglu_fwd_workspace(int64_t M, int64_t K, int64_t F, int r);

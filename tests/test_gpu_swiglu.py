@@ -3,7 +3,7 @@ activations against the oracle.
 
 Tolerances, elementwise, derived from the rounding points (U = 2^-24, half a step of bf16 2^-8):
   a sum of n exact products in fp32, in any order: n U sum |a b|;
-  T in the product as two bf16 planes: 2^-16 |T| on top;
+  T in the product as two bf16 planes at least: 2^-16 |T| on top;
   H = silu(G) U: |silu'| <= 1.1, so G and U off by dg and du move it by 1.1 |U| dg + |silu(G)| du + 1.1 dg du,
   silu's own exponential, sum and reciprocal by E = (|G| + 4) 2^-23 of it (the exponent's rounding is
   relative to G), rounding to bf16 by 2^-8;
