@@ -74,7 +74,10 @@ class Block:
 
 
 FORWARD = [(1, 64, 1, 1), (3, 4096, 48, 12), (9, 2048, 17, 5), (16, 4096, 64, 64), (24, 1024, 100, 37), (400, 64, 20, 64), (1, 4096, 512, 64), (2, 128, 33, 3), (16, 256, 100, 8), (17, 320, 129, 64), (5, 1088, 777, 12),
-           (33, 64, 16, 5), (77, 1024, 777, 12), (130, 576, 128, 64), (257, 192, 300, 33), (300, 512, 130, 16), (64, 64, 3, 64)]
+           (33, 64, 16, 5), (77, 1024, 777, 12), (130, 576, 128, 64), (257, 192, 300, 33), (300, 512, 130, 16), (64, 64, 3, 64),
+           # eight rows in LDS at most 32 KB wide; then the large tiles: one round, several, one tile row, a step alone
+           (2, 8192, 40, 16), (4, 4096, 65, 64), (1300, 128, 1100, 12), (4100, 64, 2000, 64), (34, 192, 20601, 8),
+           (4100, 64, 300, 5)]
 
 
 @pytest.mark.parametrize("M,K,F,r", FORWARD)
@@ -133,7 +136,9 @@ def check_backward(q, b, x8, gu8, T, dX, dL1, dL2):
 
 
 BACKWARD = [(1, 64, 1, 1), (1, 128, 40, 8), (2, 128, 33, 3), (16, 256, 100, 8), (17, 320, 129, 64), (33, 64, 16, 5),
-            (130, 576, 777, 12), (257, 192, 300, 33), (520, 128, 68, 16), (300, 704, 130, 64), (64, 64, 3, 64)]
+            (130, 576, 777, 12), (257, 192, 300, 33), (520, 128, 68, 16), (300, 704, 130, 64), (64, 64, 3, 64),
+            # dX in large tiles, rows of dZ padded; 260 of them, the gradients beside the last round
+            (800, 2048, 37, 12), (1600, 1024, 136, 64), (1000, 16640, 20, 8)]
 
 
 @pytest.mark.parametrize("M,K,F,r", BACKWARD)
@@ -165,7 +170,8 @@ def test_backward_of_far_gates(level):
 
 
 LINEAR = [(1, 64, 1, 1), (1, 1088, 333, 5), (7, 128, 40, 8), (16, 64, 9, 64), (17, 320, 129, 33), (77, 1088, 333, 5),
-          (130, 576, 776, 12), (600, 192, 300, 16), (257, 4096, 64, 64), (300, 64, 7, 3)]
+          (130, 576, 776, 12), (600, 192, 300, 16), (257, 4096, 64, 64), (300, 64, 7, 3), (800, 2048, 37, 12),
+          (800, 2048, 40, 12), (1000, 16640, 24, 8)]
 
 
 @pytest.mark.parametrize("M,K,N,r", LINEAR)
@@ -259,6 +265,36 @@ def test_block_step_on_another_stream_and_captured():
         torch.cuda.synchronize()
         for a, v in zip(held, eager):
             assert torch.equal(a, v), k
+
+
+@pytest.mark.parametrize("M,K,F", [(1000, 16640, 24), (40, 128, 100)])
+def test_backward_captured(M, K, F):
+    """Captured with the gradients beside dX and without, then replayed between eager calls."""
+    q = qlib()
+    r = 8
+    b, c = Block(31, M, K, F, r), Block(32, M, K, F, r, halves=1)
+    x8 = q.mx8_quantize(b.X)
+    _, T, gu8 = q.qlora_swiglu_fwd(b.X, *b.base, F, b.L1, b.L2, S, T_out=True, mx8=True)
+    L1, L2 = c.L1[0].contiguous(), c.L2[0].contiguous()
+    Tl = q.qlora_lora_down(b.X, L1)
+    d = b.d.clone()
+
+    def both():
+        return (*q.qlora_swiglu_bwd(x8, d, *b.base, b.L1, b.L2, gu8, T, S),
+                *q.qlora_linear_bwd_mx8(x8, d, *c.base, L1, L2, Tl, S))
+
+    both()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = both()
+    for k in range(3):
+        d.copy_(b.d * (0.5 + k))
+        graph.replay()
+        eager = both()
+        torch.cuda.synchronize()
+        for u, v in zip(held, eager):
+            assert torch.equal(u, v), k
 
 
 def test_given_outputs_and_workspace():
