@@ -36,6 +36,7 @@
 //    and their output stores go through a buffer descriptor, so a tile's
 //    stores drain while the next tile's LoRA term and first steps run (the
 //    memory counter a wait would block on counts stores too).
+#include <algorithm>
 #include <type_traits>
 
 #include "dequant.h"
@@ -167,9 +168,10 @@ __device__ __forceinline__ bf16x8 frag_kmajor_sw(const LDS_AS uint16_t* base, in
 struct GluOut {
   uint8_t* codes;     // G and U in 8 bits, one packed matrix of 2 M rows (mx8.h), or null
   uint8_t* scales;
+  int full;           // tiles taken as 128 columns; the rest as two of 64 by a launch of their own
 };
 
-template <bool kDx, bool kTail, bool kB16 = false, bool kDrop = false, bool kGlu = false>
+template <bool kDx, bool kTail, bool kB16 = false, bool kDrop = false, int kCols = 0>
 __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict__ A, int64_t M, int64_t K,
                                                      int64_t N, const uint8_t* __restrict__ codes,
                                                      const uint8_t* __restrict__ c2,
@@ -180,6 +182,8 @@ __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict_
                                                      Nf4Params p, int nseg, int64_t seg,
                                                      const uint16_t* __restrict__ Wb, drop::Params dp, int64_t lda,
                                                      GluOut gl) {
+  constexpr bool kGlu = kCols != 0, kHalf = kCols == kBPG / 2;
+  static_assert(!kGlu || kHalf || kCols == kBPG, "columns of a tile of the gated product");
   static_assert(!kGlu || !(kDx || kTail || kB16 || kDrop), "the gated product is a forward over the packed weight");
   __shared__ __attribute__((aligned(16))) uint16_t lds_b[2 * kBufElems];   // weight tiles; LoRA operands first
   __shared__ __attribute__((aligned(16))) uint16_t lds_a0[kBM * kBR];      // activation tiles (two buffers,
@@ -201,14 +205,24 @@ __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict_
   // take tiles v, v + G, ... in turn (persistent).
   const int tiles_x = (int)((P + kTileP - 1) / kTileP);
   const int ntiles = tiles_x * (int)((M + kBM - 1) / kBM);
+  // kGlu: the tiles after the first gl.full (a multiple of 8) are cut in two, work items
+  // 16 (u / 8) + u % 8 (+ 8) for tile gl.full + u, on its XCD
+  const int nitems = !kGlu ? ntiles : kHalf ? (ntiles - gl.full + 7) / 8 * 16 : gl.full;
   const int vfirst = blockIdx.x + gridDim.x * blockIdx.y;
   const int vstride = gridDim.x * gridDim.y;
   int m0 = 0, p0 = 0;   // wave-uniform
   auto set_tile = [&](int v) {
+    int half = 0;
+    if constexpr (kHalf) {
+      half = (v >> 3) & 1;
+      v = gl.full + (v >> 4) * 8 + (v & 7);
+      if (v >= ntiles) return false;
+    }
     const int per = ntiles / 8, extra = ntiles % 8, xcd = v % 8, q = v / 8;
     const int tile = xcd < extra ? xcd * (per + 1) + q : extra * (per + 1) + (xcd - extra) * per + q;
     m0 = __builtin_amdgcn_readfirstlane((tile / tiles_x) * kBM);
-    p0 = __builtin_amdgcn_readfirstlane((tile % tiles_x) * kTileP);
+    p0 = __builtin_amdgcn_readfirstlane((tile % tiles_x) * kTileP + half * kCols);
+    return !kHalf || p0 < P;
   };
   const int ng = kDx ? nseg : 1;
   LDS_AS uint16_t* la = (LDS_AS uint16_t*)lds_b;                 // [256][kPL]: T / G rows
@@ -279,6 +293,7 @@ __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict_
 
     // Weight tiles.  Producer thread tp rebuilds one block per step:
     //  fwd: weight row p0 + tp, block st;                   tile [tp][k]
+    //       (kHalf: half of one, weight row tp / 2)
     //  dX : weight row 64 st + tp / 4, block p0 / 64 + tp % 4; byte-plane rows 2 (tp / 4) (+1)
     using Stage = typename std::conditional<kB16, NoCodes, BlockCodes>::type;
     const __amdgpu_buffer_rsrc_t rc = rsrc(codes, kB16 ? 0 : (uint64_t)N * (K / 2));
@@ -289,9 +304,11 @@ __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict_
       if constexpr (!kB16) {
         int64_t wrow, kb;
         if constexpr (kGlu) {
-          // tile row 128 ch + 64 half + q: column p0 + 64 ch + q of the half
-          const int64_t c = p0 + 64 * (tp >> 7) + (tp & 63);
-          wrow = c < P ? (((tp >> 6) & 1) ? P : 0) + c : N;
+          // tile row 128 ch + 64 half + q: column p0 + 64 ch + q of the half (kHalf: 64, 32, 32)
+          constexpr int kQ = kCols / 2;
+          const int row = kHalf ? tp >> 1 : tp;
+          const int64_t c = p0 + kQ * (row / (2 * kQ)) + row % kQ;
+          wrow = c < P ? ((row / kQ) % 2 ? P : 0) + c : N;
           kb = step;
         } else if (!kDx) { wrow = p0 + tp; kb = step; }
         else { wrow = step * kBR + (tp >> 2); kb = p0 / 64 + (tp & 3); }
@@ -299,8 +316,12 @@ __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict_
         const uint32_t oob = (wrow < N && kb < kblocks) ? 0u : kOOB;
         const uint32_t b = (uint32_t)(wrow * kblocks + kb);
         const uint32_t co = (uint32_t)(wrow * (K / 2) + kb * 32) | oob;
-        h.v[0] = __builtin_amdgcn_raw_buffer_load_b128(rc, co, 0, 0);
-        h.v[1] = __builtin_amdgcn_raw_buffer_load_b128(rc, co + 16, 0, 0);
+        if constexpr (kHalf) {
+          h.v[0] = __builtin_amdgcn_raw_buffer_load_b128(rc, co + 16 * (tp & 1), 0, 0);
+        } else {
+          h.v[0] = __builtin_amdgcn_raw_buffer_load_b128(rc, co, 0, 0);
+          h.v[1] = __builtin_amdgcn_raw_buffer_load_b128(rc, co + 16, 0, 0);
+        }
         h.c2b = __builtin_amdgcn_raw_buffer_load_b8(r2, b | oob, 0, 0);
         h.c1v = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r1, (4 * (b >> 8)) | oob, 0, 0));
       }
@@ -310,9 +331,11 @@ __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict_
       if constexpr (!kB16) {
         const BlockLut L = make_lut(qk::e4m3fn_to_f32(h.c2b) * h.c1v, p);
 #pragma unroll
-        for (int q8 = 0; q8 < 8; ++q8) {
+        for (int q8 = 0; q8 < (kHalf ? 4 : 8); ++q8) {
           const uint32_t c = h.v[q8 >> 2][q8 & 3];
-          if (kDx) {
+          if (kHalf) {
+            *(LDS_AS u32x4*)(buf + (tp >> 1) * kPF + 32 * (tp & 1) + 8 * q8) = dequant8(L, c, kc);
+          } else if (kDx) {
             u32x2 lo8, hi8;
             dequant8_planes(L, c, kc, lo8, hi8);
             // 8-byte chunk c of 32-byte column group G of weight row k at chunk
@@ -369,8 +392,8 @@ __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict_
     // first is written to LDS.
     const bool lora_vec = (r % 8) == 0 && (kDx || (seg % 8) == 0) && M * r * 2 < (int64_t(1) << 31) &&
                           (kDx ? K * r * 2 : r * seg * 2) < (int64_t(1) << 31);
-    for (int v = vfirst; v < ntiles; v += vstride) {
-    set_tile(v);
+    for (int v = vfirst; v < nitems; v += vstride) {
+    if (!set_tile(v)) continue;
     Stage hA, hB, h0;
     if constexpr (kDrop) drop::fill_bits<kBM, kBP>((LDS_AS uint8_t*)mask, dp, m0, p0, t, kT);
     if constexpr (kGlu) {
@@ -533,7 +556,9 @@ __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict_
   // They issue no loads: between barriers they only read LDS and store their
   // outputs, and they wait only for their LDS reads, so one tile's output
   // stores drain while the next tile's LoRA term and first steps run.
-  f32x16 acc[2][4];
+  // (kHalf: 32 columns of each half, accumulators 0 and 1)
+  constexpr int kJ = kHalf ? 2 : 4;
+  f32x16 acc[2][kJ];
   // A fragment of sub-step s, tile i: row 64 (c % 4) + 32 i + l % 32, chunk 2 s + l / 32.
   uint32_t afrag_off[4];
 #pragma unroll
@@ -551,26 +576,26 @@ __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict_
                                        (128 * ch + 32 * j) * kBR * 2);
     } else {
       return kDx ? frag_planes((const LDS_AS uint8_t*)bcur, 16 * s, 128 * ch + 32 * j)
-                 : qk::frag_rowmajor(bcur, kPF, 128 * ch + 32 * j, 16 * s);
+                 : qk::frag_rowmajor(bcur, kPF, (kHalf ? 64 : 128) * ch + 32 * j, 16 * s);
     }
   };
   // Fragments of sub-step s + 1 are read from LDS while sub-step s multiplies.
   auto compute = [&](const LDS_AS uint16_t* acur, const LDS_AS uint16_t* bcur) {
-    bf16x8 bq[2][4], aq[2][2];
+    bf16x8 bq[2][kJ], aq[2][2];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) bq[0][j] = bfrag(bcur, 0, j);
+    for (int j = 0; j < kJ; ++j) bq[0][j] = bfrag(bcur, 0, j);
     aq[0][0] = afrag(acur, 0, 0);
     aq[0][1] = afrag(acur, 0, 1);
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       if (s < 3) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) bq[(s + 1) & 1][j] = bfrag(bcur, s + 1, j);
+        for (int j = 0; j < kJ; ++j) bq[(s + 1) & 1][j] = bfrag(bcur, s + 1, j);
         aq[(s + 1) & 1][0] = afrag(acur, s + 1, 0);
         aq[(s + 1) & 1][1] = afrag(acur, s + 1, 1);
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < kJ; ++j) {
         if constexpr (kGlu) {
           acc[0][j] = qk::mfma32(bq[s & 1][j], aq[s & 1][0], acc[0][j]);
           acc[1][j] = qk::mfma32(bq[s & 1][j], aq[s & 1][1], acc[1][j]);
@@ -581,8 +606,8 @@ __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict_
       }
     }
   };
-  for (int v = vfirst; v < ntiles; v += vstride) {
-  set_tile(v);
+  for (int v = vfirst; v < nitems; v += vstride) {
+  if (!set_tile(v)) continue;
   // ---- LoRA term first: fwd acc = s * (T L2); dX acc = G L1^T (rank
   //      zero-padded to 64); the base product then accumulates onto it.  With
   //      nseg > 1 segments (stacked linears) the forward tile uses its own
@@ -591,7 +616,7 @@ __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict_
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = f32x16{};
+    for (int j = 0; j < kJ; ++j) acc[i][j] = f32x16{};
   if constexpr (kDrop) {
     drop::fill_bits<kBM, kBP>((LDS_AS uint8_t*)mask, dp, m0, p0, t, kT);
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -605,13 +630,13 @@ __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict_
       for (int s = 0; s < 4; ++s) {
         if (s < ksteps) {
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const bf16x8 b = qk::frag_kmajor(a1, kPG, 16 * s, 64 * ch + 32 * j);
+          for (int j = 0; j < kJ / 2; ++j) {
+            const bf16x8 b = qk::frag_kmajor(a1, kPG, 16 * s, kCols / 2 * ch + 32 * j);
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
               for (int n = 0; n < 3; ++n)
-                acc[i][2 * g + j] = qk::mfma32(b, afrag(n == 2 ? a0 : b0 + n * kBM * kBR, s, i), acc[i][2 * g + j]);
+                acc[i][kJ / 2 * g + j] = qk::mfma32(b, afrag(n == 2 ? a0 : b0 + n * kBM * kBR, s, i), acc[i][kJ / 2 * g + j]);
           }
         }
       }
@@ -657,7 +682,7 @@ __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict_
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = scale * acc[i][j];
+      for (int j = 0; j < kJ; ++j) acc[i][j] = scale * acc[i][j];
   }
   __builtin_amdgcn_s_barrier();            // first tiles in LDS
   for (int64_t st = 0; st < nsteps; st += 2) {
@@ -675,14 +700,14 @@ __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict_
     for (int i = 0; i < 2; ++i) {
       const int64_t m = m0 + 64 * rg + 32 * i + (l & 31);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int64_t c0 = p0 + 64 * ch + 32 * j;
+      for (int j = 0; j < kJ / 2; ++j) {
+        const int64_t c0 = p0 + kCols / 2 * ch + 32 * j;
         if (c0 >= P) break;                // uniform
-        glu::store_h(acc[i][j], acc[i][2 + j], C, m, M, c0, P);
+        glu::store_h(acc[i][j], acc[i][kJ / 2 + j], C, m, M, c0, P);
         if (gl.codes) {
 #pragma unroll
           for (int g = 0; g < 2; ++g)
-            glu::store_8(acc[i][2 * g + j], gl.codes + g * M * fp, gl.scales + g * M * (fp / 32), m, M, c0, P);
+            glu::store_8(acc[i][kJ / 2 * g + j], gl.codes + g * M * fp, gl.scales + g * M * (fp / 32), m, M, c0, P);
         }
       }
     }
@@ -734,7 +759,7 @@ bool qgemm_big_ok(bool dx, int64_t M, int64_t K, int64_t N) {
 // a persistent grid of the CU count rounded down to a multiple of 8 (each
 // work group then takes tiles v, v + grid, ... on one XCD), so that a work
 // group's output stores drain while its next tile starts.
-static dim3 tile_grid(int64_t M, int64_t P, int64_t width = kBP) {
+static int64_t cu_grid() {
   static const int cus = [] {
     int dev = 0, n = 0;
     if (hipGetDevice(&dev) != hipSuccess || hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) !=
@@ -742,8 +767,11 @@ static dim3 tile_grid(int64_t M, int64_t P, int64_t width = kBP) {
       n = 256;
     return n;
   }();
-  const int64_t tx = (P + width - 1) / width, ty = (M + kBM - 1) / kBM;
-  const int64_t pers = cus / 8 * 8;
+  return cus / 8 * 8;
+}
+
+static dim3 tile_grid(int64_t M, int64_t P) {
+  const int64_t tx = (P + kBP - 1) / kBP, ty = (M + kBM - 1) / kBM, pers = cu_grid();
   if (tx * ty > pers) return dim3((unsigned)pers, 1);
   return dim3((unsigned)tx, (unsigned)ty);
 }
@@ -779,9 +807,18 @@ hipError_t launch_glu_big(const uint16_t* X, int64_t M, int64_t K, int64_t F, co
                           const float* c1, const uint16_t* T, const uint16_t* L2, int r, float scale, uint16_t* H,
                           uint8_t* gu_codes, uint8_t* gu_scales, hipStream_t s) {
   const uint16_t* nw = nullptr;
-  hipLaunchKernelGGL((k_qgemm_big<false, false, false, false, true>), tile_grid(M, F, kBPG), dim3(kT), 0, s, X, M, K, 2 * F,
-                     codes, c2, c1, T, L2, r, scale, H, nf4_params(), 1, F, nw, drop::Params{}, K,
-                     GluOut{gu_codes, gu_scales});
+  const int64_t tiles = (F + kBPG - 1) / kBPG * ((M + kBM - 1) / kBM), wgs = cu_grid();
+  // The tiles of a last round of at most half the CUs go to twice as many, in halves
+  // The tiles of a last round of at most half the CUs go to twice as many, in halves
+  const int64_t rest = tiles % wgs, halves = (rest + 7) / 8 * 16;
+  const int64_t full = halves <= wgs ? tiles - rest : tiles;
+  const GluOut out{gu_codes, gu_scales, (int)full};
+  if (full)
+    hipLaunchKernelGGL((k_qgemm_big<false, false, false, false, kBPG>), dim3((unsigned)std::min(full, wgs)), dim3(kT), 0, s, X,
+                       M, K, 2 * F, codes, c2, c1, T, L2, r, scale, H, nf4_params(), 1, F, nw, drop::Params{}, K, out);
+  if (full < tiles)
+    hipLaunchKernelGGL((k_qgemm_big<false, false, false, false, kBPG / 2>), dim3((unsigned)halves), dim3(kT), 0, s, X, M, K,
+                       2 * F, codes, c2, c1, T, L2, r, scale, H, nf4_params(), 1, F, nw, drop::Params{}, K, out);
   return hipGetLastError();
 }
 
