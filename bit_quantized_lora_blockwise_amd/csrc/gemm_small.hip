@@ -424,8 +424,13 @@ __global__ __launch_bounds__(64 * (kW + 2 * kI)) void k_glu_small(const uint16_t
 
 }  // namespace
 
+// Up to a work group of 64 rows x 32 columns of H a CU, and for 32 rows at any F (one work
+// group's rows: no weight is rebuilt twice).  Whole forwards with the 8-bit copies, us, here / in
+// large tiles: 4096 -> 2 x 11008 32 rows 59 / 83, 64 rows (344 work groups) 85 / 85, 128 rows (688)
+// 132 / 87; 2048 -> 2 x 5504 64 rows (172) 37 / 58, 128 rows (344) 67 / 60; 512 -> 2 x 1376 256 rows
+// (172) 37 / 39, 512 rows (344) 46 / 41; 8192 -> 2 x 22016 32 rows 151 / 204.
 bool glu_small_ok(int64_t M, int64_t K, int64_t F) {
-  return F < (int64_t(1) << 24) && (M <= 32 || (F + 31) / 32 * ((M + 63) / 64) <= 640);
+  return F < (int64_t(1) << 24) && (M <= 32 || (F + 31) / 32 * ((M + 63) / 64) <= 256);
 }
 
 hipError_t launch_glu_small(const uint16_t* X, int64_t M, int64_t K, int64_t F, const uint8_t* codes, const uint8_t* c2,
