@@ -102,26 +102,36 @@ __global__ __launch_bounds__(kT) void k_low(Low q, int halves, int64_t M, int r,
 }
 
 // ---- dZ and the slices of dZ L2^T ----------------------------------------------------
-// Work group: 32 rows, a slice of the columns in steps of 128.  A step's dZ is formed in row-major
-// pieces of eight columns a thread (so that a row's bytes are read and written in whole cache
-// lines: with 16 rows a wave and lanes that held operands as they are, lines were read and
-// written in quarters, 180 us at 4096 x 2 x 11008), stored, split into planes and put into LDS.
-// Wave w multiplies half w / 4, 32 ranks (w / 2 % 2), 64 of the step's columns (w % 2): L2's
-// share comes straight from memory, 64 bytes a lane.  Everything is loaded a step ahead; one
-// LDS buffer and two barriers a step, so that two work groups share a CU.
+// Work group: 64 rows, a slice of the columns in steps of 64 (or 32 rows, steps of 128).  A
+// step's dZ is formed in row-major pieces of eight columns a thread (so that a row's bytes are
+// read and written in whole cache lines: with 16 rows a wave and lanes that held operands as
+// they are, lines were read and written in quarters, 180 us at 4096 x 2 x 11008), stored, split
+// into planes and put into LDS with L2's share of the step.  Wave w multiplies half w / 4, 32 ranks (w / 2 % 2),
+// half of the step's columns (w % 2).  The next step's dH, G and U are loaded as soon as this
+// one's have become dZ; one LDS buffer and two barriers a step, so that two work groups share a CU.
+// 32 rows take L2 from memory straight to registers, a row a lane: 64 lines an instruction,
+// which cost 45 of 127 us at 4096 rows, but a step less LDS and shorter: 64 rows 10 / 15 us (rows of
+// 32 / of 64), 256 rows 13 / 16, 512 rows 20 / 19, 1024 rows 36 / 32, 4096 rows 123 / 101.
+//
+// 4096 x 2 x 11008: 363 MB, 70 us at a copy's rate; 36 vector instructions an element take 43 us
+// of each SIMD, three planes' products 14, and what the two phases of a step do not overlap is the rest.
 constexpr int kBT = 512;
-constexpr int kBM = 32;                    // rows
-constexpr int kBC = 128;                   // columns of a step
-constexpr int kBPitch = kBC + 8;           // LDS row (elements): 16 rows' pieces of 16 bytes on different banks
+constexpr int kBElems = 4096;              // of a step: 32 rows x 128 columns or 64 x 64
 
 // kVec: F % 8 == 0.
-template <bool kVec>
+template <int kBM, bool kVec>
 __global__ __launch_bounds__(kBT, 4) void k_glu_back(const uint16_t* __restrict__ dH, int M, int F,
                                                      const uint8_t* __restrict__ codes,
                                                      const uint8_t* __restrict__ scales,
                                                      const uint16_t* __restrict__ L2, int r, float scale, int chunk, int ldz,
                                                      uint16_t* __restrict__ dZ, float* __restrict__ part) {
+  constexpr int kBC = kBElems / kBM;       // columns of a step
+  constexpr int kBPitch = kBC + 8;         // LDS row (elements): 16 rows' pieces of 16 bytes on different banks
+  constexpr int kRows = kBM / 32;          // row tiles of 32
+  constexpr int kKs = kBC / 32;            // MFMA steps of a wave's half of the columns
   __shared__ __attribute__((aligned(16))) uint16_t lds[6 * kBM * kBPitch];      // [half][plane][row][column]
+  // 64 rows: L2's share of a step, [half][rank][column]
+  __shared__ __attribute__((aligned(16))) uint16_t lds_b[kBM == 64 ? 2 * 64 * kBPitch : 8];
   const int t = threadIdx.x, w = __builtin_amdgcn_readfirstlane(t >> 6), l = t & 63, hl = l >> 5;
   const int wh = w >> 2, wc = (w >> 1) & 1, wk = w & 1;
   const int f_beg = (int)blockIdx.y * chunk, f_end = min(F, f_beg + chunk);
@@ -130,13 +140,13 @@ __global__ __launch_bounds__(kBT, 4) void k_glu_back(const uint16_t* __restrict_
   const __amdgpu_buffer_rsrc_t rc = rsrc(codes, (uint64_t)2 * M * fp), rs = rsrc(scales, (uint64_t)2 * M * nb),
                                rd = rsrc(dH, (uint64_t)M * F * 2), rl = rsrc(L2, (uint64_t)2 * r * F * 2);
   const uint32_t up_c = (uint32_t)M * fp, up_s = (uint32_t)M * nb;
-  // thread t: row t / 16, columns 8 (t % 16) of a step
-  const int row = t >> 4, col = 8 * (t & 15), m = kBM * (int)blockIdx.x + row;
-  // lane (x, hl) of a wave: rank 32 wc + x, columns 64 wk + 32 hl .. + 31 of a step
-  const int c = 32 * wc + (l & 31), kcol = 64 * wk + 32 * hl;
+  // thread t: eight columns of a row of the step
+  const int row = t / (kBC / 8), col = 8 * (t % (kBC / 8)), m = kBM * (int)blockIdx.x + row;
+  // lane (x, hl) of a wave: rank 32 wc + x, a quarter of a step's columns, number 2 wk + hl
+  const int c = 32 * wc + (l & 31), kcol = kBC / 4 * (2 * wk + hl);
   struct Step {
     u32x2 g, u;
-    u32x4 d, b[4];
+    u32x4 d;
     uint8_t sg, su;
   };
   auto load = [&](int f0) {
@@ -149,15 +159,19 @@ __global__ __launch_bounds__(kBT, 4) void k_glu_back(const uint16_t* __restrict_
     s.sg = __builtin_amdgcn_raw_buffer_load_b8(rs, os, 0, 0);
     s.su = __builtin_amdgcn_raw_buffer_load_b8(rs, in ? os + up_s : kOOB, 0, 0);
     s.d = glu::load8<kVec>(rd, (uint32_t)m * F * 2u, f, F, in);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      s.b[i] = glu::load8<kVec>(rl, (uint32_t)(wh * r + c) * F * 2u, f0 + kcol + 8 * i, F, c < r && f0 + kcol + 8 * i < f_end);
     return s;
   };
-  f32x16 acc = {};
+  f32x16 acc[kRows] = {};
   Step cur = load(f_beg);
   for (int f0 = f_beg; f0 < f_end; f0 += kBC) {
     const int f = f0 + col;
+    u32x4 b[kKs];
+#pragma unroll
+    for (int i = 0; i < kKs; ++i)
+      if constexpr (kBM == 64)             // half i, rank `row`, columns `col`
+        b[i] = glu::load8<kVec>(rl, (uint32_t)(i * r + row) * F * 2u, f, F, row < r && f < f_end);
+      else
+        b[i] = glu::load8<kVec>(rl, (uint32_t)(wh * r + c) * F * 2u, f0 + kcol + 8 * i, F, c < r && f0 + kcol + 8 * i < f_end);
     const float ks = mx8::scale_f32(cur.sg), ku = mx8::scale_f32(cur.su);
     const u32x4 d = glu::fit8<kVec>(cur.d, f, F);
     float dz[2][8];
@@ -171,9 +185,7 @@ __global__ __launch_bounds__(kBT, 4) void k_glu_back(const uint16_t* __restrict_
         glu::back(g[j], u[j], __uint_as_float(j & 1 ? d[2 * k + (j >> 1)] & 0xFFFF0000u : d[2 * k + (j >> 1)] << 16),
                   dz[0][4 * k + j], dz[1][4 * k + j]);
     }
-    bf16x8 b[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) b[i] = __builtin_bit_cast(bf16x8, glu::fit8<kVec>(cur.b[i], f0 + kcol + 8 * i, F));
+    cur = load(f0 + kBC);
     __syncthreads();                       // the last step has been read
 #pragma unroll
     for (int h = 0; h < 2; ++h)
@@ -183,44 +195,63 @@ __global__ __launch_bounds__(kBT, 4) void k_glu_back(const uint16_t* __restrict_
         *(LDS_AS u32x4*)((LDS_AS uint16_t*)lds + ((3 * h + n) * kBM + row) * kBPitch + col) = a;
         if (n == 0 && m < M && f < F) qk::store8_row(dZ + (int64_t)m * ldz + h * F + f, a, min(8, F - f));
       }
-    cur = load(f0 + kBC);
+    if constexpr (kBM == 64)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        *(LDS_AS u32x4*)((LDS_AS uint16_t*)lds_b + (64 * i + row) * kBPitch + col) = glu::fit8<kVec>(b[i], f, F);
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < kKs; ++i) {
+      bf16x8 l2;
+      if constexpr (kBM == 64)
+        l2 = *(const LDS_AS bf16x8*)((const LDS_AS uint16_t*)lds_b + (64 * wh + c) * kBPitch + kcol + 8 * i);
+      else
+        l2 = __builtin_bit_cast(bf16x8, glu::fit8<kVec>(b[i], f0 + kcol + 8 * i, F));
 #pragma unroll
       for (int n = 0; n < 3; ++n)
-        acc = qk::mfma32(*(const LDS_AS bf16x8*)((const LDS_AS uint16_t*)lds + ((3 * wh + n) * kBM + (l & 31)) * kBPitch +
-                                                 kcol + 8 * i),
-                         b[i], acc);
+#pragma unroll
+        for (int q = 0; q < kRows; ++q)
+          acc[q] = qk::mfma32(*(const LDS_AS bf16x8*)((const LDS_AS uint16_t*)lds +
+                                                      ((3 * wh + n) * kBM + 32 * q + (l & 31)) * kBPitch + kcol + 8 * i),
+                              l2, acc[q]);
+    }
   }
-  if (f_end == F && m < M && (t & 15) == 0)
+  if (f_end == F && m < M && col == 0)
     for (int f = 2 * F; f < ldz; ++f) dZ[(int64_t)m * ldz + f] = 0;
   // the two halves of the steps' columns
   __syncthreads();
-  LDS_AS float* red = (LDS_AS float*)lds + (w >> 1) * 1024 + l;
+  LDS_AS float* red = (LDS_AS float*)lds + (w >> 1) * (kRows * 1024) + l;
+  static_assert(4 * kRows * 1024 * sizeof(float) <= sizeof(lds), "the sums fit");
   if (wk)
 #pragma unroll
-    for (int e = 0; e < 16; ++e) red[64 * e] = acc[e];
+    for (int q = 0; q < kRows; ++q)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) red[64 * (16 * q + e)] = acc[q][e];
   __syncthreads();
   if (wk) return;
 #pragma unroll
-  for (int e = 0; e < 16; ++e) {
-    const int mm = kBM * (int)blockIdx.x + qk::acc_row(e);
-    if (mm < M && c < r) part[(((int64_t)blockIdx.y * 2 + wh) * M + mm) * r + c] = scale * (acc[e] + red[64 * e]);
-  }
+  for (int q = 0; q < kRows; ++q)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const int mm = kBM * (int)blockIdx.x + 32 * q + qk::acc_row(e);
+      if (mm < M && c < r)
+        part[(((int64_t)blockIdx.y * 2 + wh) * M + mm) * r + c] = scale * (acc[q][e] + red[64 * (16 * q + e)]);
+    }
 }
 
-// Slices of that pass: about 512 work groups, but no more than 32 slices to add up for each row, and as many
+// Slices of that pass: about 512 work groups (1024: 114 us for 111 at 4096 x 2 x 11008, 256: 121), but no more than 32 slices to add up for each row, and as many
 // as the product for few rows adds up itself where the pass is short all the same (up to four steps).
 struct PlanBack {
-  int tiles, slices;
+  int rows, tiles, slices;
   int64_t chunk;
 };
 PlanBack plan_back(int64_t M, int64_t F) {
   PlanBack p;
-  p.tiles = (int)((M + kBM - 1) / kBM);
-  const int64_t steps = (F + kBC - 1) / kBC, s = std::max<int64_t>(1, std::min<int64_t>({512 / p.tiles, steps, steps <= 4 * kSmallSlices ? kSmallSlices : 32}));
-  p.chunk = (steps + s - 1) / s * kBC;
+  p.rows = M >= 512 ? 64 : 32;             // both sides measured above
+  p.tiles = (int)((M + p.rows - 1) / p.rows);
+  const int cols = kBElems / p.rows;
+  const int64_t steps = (F + cols - 1) / cols, s = std::max<int64_t>(1, std::min<int64_t>({512 / p.tiles, steps, steps <= 4 * kSmallSlices ? kSmallSlices : 32}));
+  p.chunk = (steps + s - 1) / s * cols;
   p.slices = (int)((F + p.chunk - 1) / p.chunk);
   return p;
 }
@@ -253,11 +284,16 @@ hipError_t launch_glu_back(const uint16_t* dH, int64_t M, int64_t F, const uint8
   const PlanBack p = plan_back(M, F);
   *slices = p.slices;
   const dim3 grid((unsigned)p.tiles, (unsigned)p.slices);
-#define QL_BACK(V)                                                                                                      \
-  hipLaunchKernelGGL(k_glu_back<V>, grid, dim3(kBT), 0, s, dH, (int)M, (int)F, gu_codes, gu_scales, L2, r, scale, (int)p.chunk, \
+#define QL_BACK(R, V)                                                                                                      \
+  hipLaunchKernelGGL((k_glu_back<R, V>), grid, dim3(kBT), 0, s, dH, (int)M, (int)F, gu_codes, gu_scales, L2, r, scale, (int)p.chunk, \
                      (int)glu_ldz(F), dZ, part)
-  if (F % 8 == 0) QL_BACK(true);
-  else QL_BACK(false);
+  if (p.rows == 64) {
+    if (F % 8 == 0) QL_BACK(64, true);
+    else QL_BACK(64, false);
+  } else {
+    if (F % 8 == 0) QL_BACK(32, true);
+    else QL_BACK(32, false);
+  }
 #undef QL_BACK
   return hipGetLastError();
 }

@@ -347,9 +347,13 @@ Plan plan(int64_t P, int width, int64_t M, int groups) {
 struct Plans {
   Plan x, z;
 };
-// Two work groups a CU in all, shared by what the products cost.
+// Two work groups a CU in all, shared so that they end together: a half's dL1 against dL2 of both
+// is K to 5 N (4096 x 4096 with 2 x 11008: 88 us; K to 3 N 99, K to 12 N 131).
 Plans plans(int64_t M, int64_t K, int64_t N, int halves) {
-  if (halves == 2) return Plans{plan(K, kP, M, 64), plan(N, kGP, M, 384)};
+  if (halves == 2) {
+    const int gx = std::max(1, (int)(512.0 * K / (2.0 * K + 5.0 * N)));
+    return Plans{plan(K, kP, M, gx), plan(N, kGP, M, std::max(1, 512 - 2 * gx))};
+  }
   const double x = 1.5 * K, z = 1.0 * N;             // three planes against twice the bytes
   const int gx = std::max(1, (int)(512 * x / (x + z)));
   return Plans{plan(K, kP, M, gx), plan(N, kP, M, std::max(1, 512 - gx))};
