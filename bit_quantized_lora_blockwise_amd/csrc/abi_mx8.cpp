@@ -49,8 +49,21 @@ FwdWs fwd_ws(int64_t M, int64_t K, int64_t F, int r) {
   return w;
 }
 
+// Whether dX [M, K], whose reduction is over n columns, is taken in slices of the reduction.  The work
+// groups of the product for few rows (64 columns of 32 rows) and of the large tiles each walk all of it; slices
+// cost a launch and the partial sums' way to memory.  Whole backwards, us, walked / in slices: gated, K = 4096, n
+// = 22016 1 row 91 / 69, 64 rows 120 / 73, 512 rows 456 / 154, 1024 rows 505 / 246; K = 1024, n = 5504 64 rows 49 / 47, 512 rows 56 / 64, 1024
+// rows 84 / 73; K = 512, n = 2752 512 rows 48 / 57; linear, K = n = 4096 128 rows 41 / 48, 256 rows 62 / 52, 1024
+// rows 119 / 83; K = 11008, n = 4096 17 rows 35 / 53, 64 rows 62 / 55.
+bool split_ok(int64_t M, int64_t K, int64_t n) {
+  const int64_t groups = K / 64 * ((M + 31) / 32);
+  return n * std::max<int64_t>(groups, 256) >= 6144 * 256 && qgemm_dx_slices(M, K, n) > 1;
+}
+
 // Whether a linear's G goes to dX for few rows as slices, which it adds up itself (a launch less).
-bool few_dx_ok(int64_t M, int64_t K, int r) { return (M + 15) / 16 * ((r + 15) / 16) <= 24 && dx_small_ok(M, K); }
+bool few_dx_ok(int64_t M, int64_t K, int64_t N, int r) {
+  return (M + 15) / 16 * ((r + 15) / 16) <= 24 && dx_small_ok(M, K) && !(N % 8 == 0 && split_ok(M, K, N));
+}
 
 // Backward: [dZ (gated)][G][its planes][fp32 partials, of G and then of the gradients].
 struct BwdWs {
@@ -59,9 +72,11 @@ struct BwdWs {
 BwdWs bwd_ws(int64_t M, int64_t K, int64_t N, int halves, int r) {
   BwdWs w{halves == 2 ? round_up((size_t)M * glu_ldz(N) * 2) : 0, round_up((size_t)halves * M * r * 2),
           round_up((size_t)3 * halves * M * g_pitch(r) * 2), 0, 0};
-  const size_t slices = halves == 2 ? glu_back_ws(M, N, r) : few_dx_ok(M, K, r) ? std::max(mx4_small_ws(M, r), lora_skinny_ws(M, N, r))
+  const size_t slices = halves == 2 ? glu_back_ws(M, N, r) : few_dx_ok(M, K, N, r) ? std::max(mx4_small_ws(M, r), lora_skinny_ws(M, N, r))
                                                                                 : lora_skinny_ws(M, N, r);
-  w.part = round_up(std::max(slices, grads8_ws(M, K, N, halves, r)));
+  w.part = std::max(slices, grads8_ws(M, K, N, halves, r));
+  if ((halves == 2 || N % 8 == 0) && split_ok(M, K, halves * N)) w.part = std::max(w.part, qgemm_dx_split_ws(M, K, halves * N));
+  w.part = round_up(w.part);
   w.total = w.dz + w.g + w.planes + w.part;
   return w;
 }
@@ -215,7 +230,7 @@ int qlora_swiglu_bwd(const uint8_t* x_codes, const uint8_t* x_scales, const uint
   float* part = (float*)(ws + w.dz + w.g + w.planes);
   int slices = 0;
   QL_TRY(launch_glu_back(dH, M, F, gu_codes, gu_scales, L2, r, lora_scale, dZ, part, &slices, s));
-  const bool small = dx_small_ok(M, K), sums = dX && small && slices <= kSmallSlices;
+  const bool split = split_ok(M, K, 2 * F), small = !split && dx_small_ok(M, K), sums = dX && small && slices <= kSmallSlices;
   if (!sums) QL_TRY(launch_low(Low{part, slices, 1.0f, G, planes}, 2, M, r, s));
   auto product = [&] {
     if (!dX) return hipSuccess;
@@ -223,13 +238,15 @@ int qlora_swiglu_bwd(const uint8_t* x_codes, const uint8_t* x_scales, const uint
     if (small)
       return launch_dx_small(dZ, M, K, 2 * F, codes, c2, c1, sums ? nullptr : G, part, slices, planes, L1, r, dX, kNoDrop, s,
                              glu_ldz(F), 2);
+    if (split)
+      return launch_qgemm_dx_split(dZ, M, K, 2 * F, codes, c2, c1, G, L1, r, dX, part, s, 2, glu_ldz(F));
     return launch_qgemm_big(true, dZ, M, K, 2 * F, codes, c2, c1, G, L1, r, 1.0f, dX, s, 2, nullptr, glu_ldz(F));
   };
   auto grads = [&](hipStream_t st) {
     return launch_grads8(Grads8{x_codes, x_scales, dH, gu_codes, gu_scales, planes, T, lora_scale, dL1, dL2}, M, K, F, 2, r,
                          part, st);
   };
-  return dx_and_grads(dX && !small ? beside_dx(M, K) : nullptr, s, product, grads);
+  return dx_and_grads(dX && !small && !split ? beside_dx(M, K) : nullptr, s, product, grads);
 }
 
 size_t qlora_linear_bwd_mx8_workspace(int64_t M, int64_t K, int64_t N, int r) {
@@ -252,7 +269,8 @@ int qlora_linear_bwd_mx8(const uint8_t* x_codes, const uint8_t* x_scales, const 
   uint16_t* planes = (uint16_t*)(ws + w.g);
   float* part = (float*)(ws + w.g + w.planes);
   int slices = 0;
-  const bool few = few_dx_ok(M, K, r), small = dx_small_ok(M, K), big = qgemm_big_ok(true, M, K, N);
+  const bool few = few_dx_ok(M, K, N, r), big = qgemm_big_ok(true, M, K, N), split = N % 8 == 0 && split_ok(M, K, N),
+             small = !split && dx_small_ok(M, K);
   if (few) QL_TRY(launch_small_slices(dY, M, N, L2, false, r, kNoDrop, lora_scale, part, &slices, s));
   else QL_TRY(launch_lora_slices(dY, M, N, L2, false, r, part, &slices, s));
   if (!dX || !few) QL_TRY(launch_low(Low{part, slices, few ? 1.0f : lora_scale, G, planes}, 1, M, r, s));
@@ -260,6 +278,7 @@ int qlora_linear_bwd_mx8(const uint8_t* x_codes, const uint8_t* x_scales, const 
     if (!dX) return hipSuccess;
     if (small)
       return launch_dx_small(dY, M, K, N, codes, c2, c1, few ? nullptr : G, part, slices, planes, L1, r, dX, kNoDrop, s);
+    if (split) return launch_qgemm_dx_split(dY, M, K, N, codes, c2, c1, G, L1, r, dX, part, s);
     if (big) return launch_qgemm_big(true, dY, M, K, N, codes, c2, c1, G, L1, r, 1.0f, dX, s);
     return launch_qgemm_dx(dY, M, K, N, codes, c2, c1, G, L1, r, dX, s);
   };
@@ -267,7 +286,7 @@ int qlora_linear_bwd_mx8(const uint8_t* x_codes, const uint8_t* x_scales, const 
     return launch_grads8(Grads8{x_codes, x_scales, dY, nullptr, nullptr, planes, T, lora_scale, dL1, dL2}, M, K, N, 1, r, part,
                          st);
   };
-  return dx_and_grads(dX && !small && big ? beside_dx(M, K) : nullptr, s, product, grads);
+  return dx_and_grads(dX && !small && !split && big ? beside_dx(M, K) : nullptr, s, product, grads);
 }
 
 }  // extern "C"

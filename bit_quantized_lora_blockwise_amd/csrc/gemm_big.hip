@@ -61,6 +61,7 @@ constexpr int kPlane = kBP + 32;  // dX B tile: bytes per byte-plane row (72 dwo
 constexpr int kBufElems = (kBP * kPF > kBR * kPD) ? kBP * kPF : kBR * kPD;
 static_assert(2 * kBR * kPlane <= 2 * kBufElems, "dX byte-plane tile fits the B buffer");
 constexpr int kPL = 64 + 8;       // pitch of the LoRA operand tiles [row][c]
+constexpr int kTileVecs = kBM * kBP / 4;   // a tile's accumulators
 constexpr int kBPG = kBP / 2;     // gated product: columns of H per tile
 constexpr int kPG = kBPG + 32;    // and the pitch of its L2 tile [c][column]
 static_assert(64 * kPG <= kBM * kBR, "the gated product's L2 tile fits an activation buffer");
@@ -165,13 +166,19 @@ __device__ __forceinline__ bf16x8 frag_kmajor_sw(const LDS_AS uint16_t* base, in
 // into LDS (a bit an element) while the LoRA operands arrive (by the producers alone,
 // one wave a SIMD, the draws took 12 us a tile), and the consumers apply them to the
 // accumulators before the base product.
-struct GluOut {
-  uint8_t* codes;     // G and U in 8 bits, one packed matrix of 2 M rows (mx8.h), or null
+// kSplit (dX): the reduction is cut into slices, a work item is a tile of one of them, and what
+// it sums goes to `part` in fp32, for k_dx_join to add up in order: in whole accumulators, 1 KB a
+// store (row-major, 4 bytes a lane, the stores alone took as long as ten steps).  The first slice has the adapter's term.
+struct BigOut {
+  uint8_t* codes;     // kGlu: G and U in 8 bits, one packed matrix of 2 M rows (mx8.h), or null
   uint8_t* scales;
-  int full;           // tiles taken as 128 columns; the rest as two of 64 by a launch of their own
+  int full;           // kGlu: tiles taken as 128 columns; the rest as two of 64 by a launch of their own
+  float* part;        // kSplit: [slices][tiles], each a tile's accumulators as the waves hold them
+  int slices, steps;  // kSplit: and the steps of one, an even number
 };
 
-template <bool kDx, bool kTail, bool kB16 = false, bool kDrop = false, int kCols = 0>
+template <bool kDx, bool kTail, bool kB16 = false, bool kDrop = false, int kCols = 0,
+          bool kSplit = false>
 __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict__ A, int64_t M, int64_t K,
                                                      int64_t N, const uint8_t* __restrict__ codes,
                                                      const uint8_t* __restrict__ c2,
@@ -181,9 +188,10 @@ __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict_
                                                      int r, float scale, uint16_t* __restrict__ C,
                                                      Nf4Params p, int nseg, int64_t seg,
                                                      const uint16_t* __restrict__ Wb, drop::Params dp, int64_t lda,
-                                                     GluOut gl) {
+                                                     BigOut gl) {
   constexpr bool kGlu = kCols != 0, kHalf = kCols == kBPG / 2;
   static_assert(!kGlu || kHalf || kCols == kBPG, "columns of a tile of the gated product");
+  static_assert(!kSplit || (kDx && !kB16 && !kDrop), "a split reduction is of dX over the packed weight");
   static_assert(!kGlu || !(kDx || kTail || kB16 || kDrop), "the gated product is a forward over the packed weight");
   __shared__ __attribute__((aligned(16))) uint16_t lds_b[2 * kBufElems];   // weight tiles; LoRA operands first
   __shared__ __attribute__((aligned(16))) uint16_t lds_a0[kBM * kBR];      // activation tiles (two buffers,
@@ -207,10 +215,12 @@ __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict_
   const int ntiles = tiles_x * (int)((M + kBM - 1) / kBM);
   // kGlu: the tiles after the first gl.full (a multiple of 8) are cut in two, work items
   // 16 (u / 8) + u % 8 (+ 8) for tile gl.full + u, on its XCD
-  const int nitems = !kGlu ? ntiles : kHalf ? (ntiles - gl.full + 7) / 8 * 16 : gl.full;
+  const int nitems = kSplit ? ntiles * gl.slices : !kGlu ? ntiles : kHalf ? (ntiles - gl.full + 7) / 8 * 16 : gl.full;
   const int vfirst = blockIdx.x + gridDim.x * blockIdx.y;
   const int vstride = gridDim.x * gridDim.y;
-  int m0 = 0, p0 = 0;   // wave-uniform
+  const int64_t nsteps = (R + kBR - 1) / kBR;
+  int m0 = 0, p0 = 0, slice = 0, tile_at = 0, ng = kDx ? nseg : 1;   // wave-uniform
+  int64_t st0 = 0, st1 = nsteps;          // this item's steps
   auto set_tile = [&](int v) {
     int half = 0;
     if constexpr (kHalf) {
@@ -218,13 +228,21 @@ __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict_
       v = gl.full + (v >> 4) * 8 + (v & 7);
       if (v >= ntiles) return false;
     }
-    const int per = ntiles / 8, extra = ntiles % 8, xcd = v % 8, q = v / 8;
-    const int tile = xcd < extra ? xcd * (per + 1) + q : extra * (per + 1) + (xcd - extra) * per + q;
+    const int n = kSplit ? nitems : ntiles;
+    const int per = n / 8, extra = n % 8, xcd = v % 8, q = v / 8;
+    int tile = xcd < extra ? xcd * (per + 1) + q : extra * (per + 1) + (xcd - extra) * per + q;
+    if constexpr (kSplit) {
+      slice = __builtin_amdgcn_readfirstlane(tile / ntiles);
+      tile -= slice * ntiles;
+      tile_at = tile;
+      st0 = (int64_t)slice * gl.steps;
+      st1 = min(nsteps, st0 + gl.steps);
+      ng = slice ? 0 : nseg;
+    }
     m0 = __builtin_amdgcn_readfirstlane((tile / tiles_x) * kBM);
     p0 = __builtin_amdgcn_readfirstlane((tile % tiles_x) * kTileP + half * kCols);
     return !kHalf || p0 < P;
   };
-  const int ng = kDx ? nseg : 1;
   LDS_AS uint16_t* la = (LDS_AS uint16_t*)lds_b;                 // [256][kPL]: T / G rows
   LDS_AS uint16_t* lb = (LDS_AS uint16_t*)lds_b + kBM * kPL;     // fwd: L2 [64][kPD]; dX: L1 [256][kPL]
 
@@ -233,7 +251,6 @@ __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict_
   LDS_AS uint16_t* a0 = (LDS_AS uint16_t*)lds_a0;
   LDS_AS uint16_t* a1 = (LDS_AS uint16_t*)lds_a1;
   static_assert(2 * kBM * kBR <= 2 * kBufElems, "two of T's planes fit the B buffers");
-  const int64_t nsteps = (R + kBR - 1) / kBR;
 
   if (producer) {
     // ================================ producers ================================
@@ -516,9 +533,9 @@ __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict_
       __builtin_amdgcn_s_barrier();         // the consumers have read them
     }
     {
-      send(0, a0, b0);
-      h0 = load_stage(0);
-      hA = load_stage(1);
+      send(st0, a0, b0);
+      h0 = load_stage(st0);
+      hA = load_stage(st0 + 1);
       store_stage(h0, b0);
       __builtin_amdgcn_s_waitcnt(0x0070);   // vmcnt(0) lgkmcnt(0), seen by the compiler's wait tracking
       __builtin_amdgcn_s_barrier();
@@ -530,7 +547,7 @@ __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict_
     // arrived (the barrier waited for it) and tells the compiler's wait
     // tracking so, so that it places no wait after the loads to LDS it cannot
     // count.
-    for (int64_t st = 0; st < nsteps; st += 2) {
+    for (int64_t st = st0; st < st1; st += 2) {
       __builtin_amdgcn_s_waitcnt(0x0070);
       send(st + 1, a1, b1);
       hB = load_stage(st + 2);
@@ -685,7 +702,7 @@ __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict_
       for (int j = 0; j < kJ; ++j) acc[i][j] = scale * acc[i][j];
   }
   __builtin_amdgcn_s_barrier();            // first tiles in LDS
-  for (int64_t st = 0; st < nsteps; st += 2) {
+  for (int64_t st = st0; st < st1; st += 2) {
     compute(a0, b0);
     __builtin_amdgcn_s_waitcnt(0xC07F);    // lgkmcnt(0): this wave's fragment reads are done
     __builtin_amdgcn_s_barrier();
@@ -710,6 +727,17 @@ __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict_
             glu::store_8(acc[i][kJ / 2 * g + j], gl.codes + g * M * fp, gl.scales + g * M * (fp / 32), m, M, c0, P);
         }
       }
+    }
+  } else if constexpr (kSplit) {
+    f32x4* out = (f32x4*)gl.part + ((int64_t)slice * ntiles + tile_at) * kTileVecs + w * (kTileVecs / 8) + l;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (m0 + 64 * rg + 32 * i >= M) break;     // uniform
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          out[64 * (16 * i + 4 * j + q)] = f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
     }
   } else
   // ---- store C (bf16), lane layout of the 32x32 accumulators, through a
@@ -745,6 +773,47 @@ __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict_
       }
   }
   }   // tiles
+}
+
+// dX = bf16(the slices' sum), added in order; a work group takes one wave's 32 x 32 pieces of a tile, two a pass.
+__global__ __launch_bounds__(512) void k_dx_join(const float* __restrict__ part, int slices, int64_t M, int64_t K,
+                                                 uint16_t* __restrict__ C) {
+  const int tiles_x = (int)((K + kBP - 1) / kBP), ntiles = gridDim.x / 16;
+  const int tile = (int)blockIdx.x >> 4, w = ((int)blockIdx.x >> 1) & 7, i = (int)blockIdx.x & 1;
+  const int64_t m0 = (int64_t)(tile / tiles_x) * kBM + 64 * (w & 3) + 32 * i;
+  if (m0 >= M) return;
+  const int l = threadIdx.x & 63, h = threadIdx.x >> 6;    // h: register group 2 h (+ 1) of the sixteen
+  const f32x4* p = (const f32x4*)part + (int64_t)tile * kTileVecs + w * (kTileVecs / 8) + 64 * (16 * i + 2 * h) + l;
+  const int64_t pitch = (int64_t)ntiles * kTileVecs;
+  f32x4 u[2] = {p[0], p[64]};
+  int k = 1;
+  for (; k + 3 <= slices; k += 3) {        // three in flight
+    f32x4 v[3][2];
+#pragma unroll
+    for (int a = 0; a < 3; ++a) {
+      v[a][0] = p[(k + a) * pitch];
+      v[a][1] = p[(k + a) * pitch + 64];
+    }
+#pragma unroll
+    for (int a = 0; a < 3; ++a) {
+      u[0] += v[a][0];
+      u[1] += v[a][1];
+    }
+  }
+  for (; k < slices; ++k) {
+    u[0] += p[k * pitch];
+    u[1] += p[k * pitch + 64];
+  }
+#pragma unroll
+  for (int a = 0; a < 2; ++a) {
+    const int j = (2 * h + a) >> 2, q = (2 * h + a) & 3;
+    const int64_t c = (int64_t)(tile % tiles_x) * kBP + 128 * (w >> 2) + 32 * j + dx_slot_col(l & 31);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int64_t m = m0 + qk::acc_row(4 * q + e);
+      if (m < M && c < K) C[m * K + c] = qk::f32_to_bf16(u[a][e]);
+    }
+  }
 }
 
 }  // namespace
@@ -786,20 +855,50 @@ hipError_t launch_qgemm_big(bool dx, const uint16_t* A, int64_t M, int64_t K, in
   const uint16_t* nw = nullptr;
   if (!dx)
     hipLaunchKernelGGL((k_qgemm_big<false, false>), grid, dim3(kT), 0, s, A, M, K, N, codes, c2, c1, LA, LB, r,
-                       scale, C, nf4_params(), nseg, seg, nw, drop::Params{}, lda, GluOut{});
+                       scale, C, nf4_params(), nseg, seg, nw, drop::Params{}, lda, BigOut{});
   else if (d && d->cut) {
     if (N % kBR == 0)
       hipLaunchKernelGGL((k_qgemm_big<true, false, false, true>), grid, dim3(kT), 0, s, A, M, K, N, codes, c2, c1, LA,
-                         LB, r, scale, C, nf4_params(), nseg, seg, nw, *d, lda, GluOut{});
+                         LB, r, scale, C, nf4_params(), nseg, seg, nw, *d, lda, BigOut{});
     else
       hipLaunchKernelGGL((k_qgemm_big<true, true, false, true>), grid, dim3(kT), 0, s, A, M, K, N, codes, c2, c1, LA,
-                         LB, r, scale, C, nf4_params(), nseg, seg, nw, *d, lda, GluOut{});
+                         LB, r, scale, C, nf4_params(), nseg, seg, nw, *d, lda, BigOut{});
   } else if (N % kBR == 0)
     hipLaunchKernelGGL((k_qgemm_big<true, false>), grid, dim3(kT), 0, s, A, M, K, N, codes, c2, c1, LA, LB, r,
-                       scale, C, nf4_params(), nseg, seg, nw, drop::Params{}, lda, GluOut{});
+                       scale, C, nf4_params(), nseg, seg, nw, drop::Params{}, lda, BigOut{});
   else
     hipLaunchKernelGGL((k_qgemm_big<true, true>), grid, dim3(kT), 0, s, A, M, K, N, codes, c2, c1, LA, LB, r,
-                       scale, C, nf4_params(), nseg, seg, nw, drop::Params{}, lda, GluOut{});
+                       scale, C, nf4_params(), nseg, seg, nw, drop::Params{}, lda, BigOut{});
+  return hipGetLastError();
+}
+
+int qgemm_dx_slices(int64_t M, int64_t K, int64_t N) {
+  const int64_t tiles = (M + kBM - 1) / kBM * ((K + kBP - 1) / kBP), steps = (N + kBR - 1) / kBR;
+  const int64_t most = std::min(cu_grid() / tiles, steps / 8);
+  if (most < 2) return 1;
+  const int64_t per = (steps + 2 * most - 1) / (2 * most) * 2;
+  return (int)((steps + per - 1) / per);
+}
+
+size_t qgemm_dx_split_ws(int64_t M, int64_t K, int64_t N) {
+  return (size_t)qgemm_dx_slices(M, K, N) * ((M + kBM - 1) / kBM) * ((K + kBP - 1) / kBP) * kTileVecs * sizeof(f32x4);
+}
+
+hipError_t launch_qgemm_dx_split(const uint16_t* A, int64_t M, int64_t K, int64_t N, const uint8_t* codes,
+                                 const uint8_t* c2, const float* c1, const uint16_t* LA, const uint16_t* LB, int r,
+                                 uint16_t* C, float* part, hipStream_t s, int nseg, int64_t ld) {
+  const int slices = qgemm_dx_slices(M, K, N);
+  const int64_t steps = (N + kBR - 1) / kBR, tiles = (M + kBM - 1) / kBM * ((K + kBP - 1) / kBP);
+  const BigOut out{nullptr, nullptr, 0, part, slices, (int)((steps + 2 * slices - 1) / (2 * slices) * 2)};
+  const uint16_t* nw = nullptr;
+  const dim3 grid((unsigned)(tiles * slices));
+#define QL_SPLIT(T)                                                                                                   \
+  hipLaunchKernelGGL((k_qgemm_big<true, T, false, false, 0, true>), grid, dim3(kT), 0, s, A, M, K, N, codes, c2, c1, LA, LB, r, \
+                     1.0f, C, nf4_params(), nseg, N / nseg, nw, drop::Params{}, ld ? ld : N, out)
+  if (N % kBR == 0) QL_SPLIT(false);
+  else QL_SPLIT(true);
+#undef QL_SPLIT
+  hipLaunchKernelGGL(k_dx_join, dim3((unsigned)(16 * tiles)), dim3(512), 0, s, part, slices, M, K, C);
   return hipGetLastError();
 }
 
@@ -809,10 +908,9 @@ hipError_t launch_glu_big(const uint16_t* X, int64_t M, int64_t K, int64_t F, co
   const uint16_t* nw = nullptr;
   const int64_t tiles = (F + kBPG - 1) / kBPG * ((M + kBM - 1) / kBM), wgs = cu_grid();
   // The tiles of a last round of at most half the CUs go to twice as many, in halves
-  // The tiles of a last round of at most half the CUs go to twice as many, in halves
   const int64_t rest = tiles % wgs, halves = (rest + 7) / 8 * 16;
   const int64_t full = halves <= wgs ? tiles - rest : tiles;
-  const GluOut out{gu_codes, gu_scales, (int)full};
+  const BigOut out{gu_codes, gu_scales, (int)full, nullptr, 0, 0};
   if (full)
     hipLaunchKernelGGL((k_qgemm_big<false, false, false, false, kBPG>), dim3((unsigned)std::min(full, wgs)), dim3(kT), 0, s, X,
                        M, K, 2 * F, codes, c2, c1, T, L2, r, scale, H, nf4_params(), 1, F, nw, drop::Params{}, K, out);
@@ -838,12 +936,12 @@ hipError_t launch_bgemm_big(bool dx, const uint16_t* A, int64_t M, int64_t K, in
   const float* nf = nullptr;
   if (!dx)
     hipLaunchKernelGGL((k_qgemm_big<false, false, true>), grid, dim3(kT), 0, s, A, M, K, N, nc, nc, nf, LA, LB, r,
-                       scale, C, nf4_params(), 1, N, W, drop::Params{}, dx ? N : K, GluOut{});
+                       scale, C, nf4_params(), 1, N, W, drop::Params{}, dx ? N : K, BigOut{});
   else if (N % kBR == 0)
     hipLaunchKernelGGL((k_qgemm_big<true, false, true>), grid, dim3(kT), 0, s, A, M, K, N, nc, nc, nf, LA, LB, r,
-                       scale, C, nf4_params(), 1, N, W, drop::Params{}, dx ? N : K, GluOut{});
+                       scale, C, nf4_params(), 1, N, W, drop::Params{}, dx ? N : K, BigOut{});
   else
     hipLaunchKernelGGL((k_qgemm_big<true, true, true>), grid, dim3(kT), 0, s, A, M, K, N, nc, nc, nf, LA, LB, r,
-                       scale, C, nf4_params(), 1, N, W, drop::Params{}, dx ? N : K, GluOut{});
+                       scale, C, nf4_params(), 1, N, W, drop::Params{}, dx ? N : K, BigOut{});
   return hipGetLastError();
 }

@@ -224,6 +224,13 @@ hipError_t launch_qgemm_big(bool dx, const uint16_t* A, int64_t M, int64_t K, in
                             const uint8_t* c2, const float* c1, const uint16_t* LA, const uint16_t* LB, int r,
                             float scale, uint16_t* C, hipStream_t s, int nseg = 1,
                             const drop::Params* d = nullptr, int64_t lda = 0);
+// dX of few tiles: the reduction in slices, whose fp32 sums (part: qgemm_dx_split_ws bytes) a launch of its own
+// adds up in order.  1: not split.
+int qgemm_dx_slices(int64_t M, int64_t K, int64_t N);
+size_t qgemm_dx_split_ws(int64_t M, int64_t K, int64_t N);
+hipError_t launch_qgemm_dx_split(const uint16_t* A, int64_t M, int64_t K, int64_t N, const uint8_t* codes,
+                                 const uint8_t* c2, const float* c1, const uint16_t* LA, const uint16_t* LB, int r,
+                                 uint16_t* C, float* part, hipStream_t s, int nseg = 1, int64_t lda = 0);
 // The same two GEMMs with a bf16 weight W [N, K] in place of the packed one
 // (LoRA over a bf16 base): dx = false Y = bf16(X W^T + scale T L2), dx = true
 // dX = bf16(dY W + G L1^T).  bgemm_ok says whether the shapes qualify.

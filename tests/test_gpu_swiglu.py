@@ -138,7 +138,9 @@ def check_backward(q, b, x8, gu8, T, dX, dL1, dL2):
 BACKWARD = [(1, 64, 1, 1), (1, 128, 40, 8), (2, 128, 33, 3), (16, 256, 100, 8), (17, 320, 129, 64), (33, 64, 16, 5),
             (130, 576, 777, 12), (257, 192, 300, 33), (520, 128, 68, 16), (300, 704, 130, 64), (64, 64, 3, 64),
             # dX in large tiles, rows of dZ padded; 260 of them, the gradients beside the last round
-            (800, 2048, 37, 12), (1600, 1024, 136, 64), (1000, 16640, 20, 8)]
+            (800, 2048, 37, 12), (1600, 1024, 136, 64), (1000, 16640, 20, 8),
+            # its reduction in slices: of one row, of a whole tile and a part, of a length that ends inside a step
+            (1, 128, 3500, 8), (33, 320, 3501, 12), (257, 576, 3333, 64), (300, 4096, 1100, 5)]
 
 
 @pytest.mark.parametrize("M,K,F,r", BACKWARD)
@@ -171,7 +173,9 @@ def test_backward_of_far_gates(level):
 
 LINEAR = [(1, 64, 1, 1), (1, 1088, 333, 5), (7, 128, 40, 8), (16, 64, 9, 64), (17, 320, 129, 33), (77, 1088, 333, 5),
           (130, 576, 776, 12), (600, 192, 300, 16), (257, 4096, 64, 64), (300, 64, 7, 3), (800, 2048, 37, 12),
-          (800, 2048, 40, 12), (1000, 16640, 24, 8)]
+          (800, 2048, 40, 12), (1000, 16640, 24, 8),
+          # in slices
+          (1, 64, 6152, 3), (40, 192, 7000, 16), (300, 4096, 2056, 64)]
 
 
 @pytest.mark.parametrize("M,K,N,r", LINEAR)
