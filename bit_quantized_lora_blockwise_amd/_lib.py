@@ -147,6 +147,27 @@ def _stream(stream=None):
     return stream.cuda_stream
 
 
+def _ptrs(stream, *tensors):
+    """Device addresses of a call's tensor arguments (None -> NULL), which all have to be on the device of
+    its stream: a kernel runs there, and memory of another device may not be mapped on it."""
+    dev, out = None, []
+    for t in tensors:
+        if t is None:
+            out.append(None)
+            continue
+        at = t.get_device()
+        if at != dev:
+            out.append(_ptr(t))            # refuses what is not on a GPU
+            if dev is None:
+                dev = torch._C._cuda_getDevice() if stream is None else stream.device_index
+            if at != dev:
+                raise ValueError(f"every tensor argument must be on the device of the call's stream, cuda:{dev} (got a "
+                                 f"{t.device} tensor of shape {tuple(t.shape)})")
+        else:
+            out.append(t.data_ptr())
+    return out
+
+
 def _need(t, name, dtype, ndim=None, shape=None, numel=None):
     """Check a tensor argument: type, dtype, rank, shape or element count and
     contiguity (the device is checked when its pointer is taken, after every
@@ -885,7 +906,8 @@ def mx8_quantize(X, codes=None, scales=None, stream=None):
     sc, ss = _mx8_shapes(rows, cols)
     codes = _out(codes, "codes", torch.uint8, sc, X, stream)
     scales = _out(scales, "scales", torch.uint8, ss, X, stream)
-    _check("mx8_quantize", lib().mx8_quantize(_ptr(X), dt, rows, cols, ld, _ptr(codes), _ptr(scales), _stream(stream)))
+    px, pc, ps = _ptrs(stream, X, codes, scales)
+    _check("mx8_quantize", lib().mx8_quantize(px, dt, rows, cols, ld, pc, ps, _stream(stream)))
     return codes, scales
 
 
@@ -893,7 +915,8 @@ def mx8_dequantize(codes, scales, rows, cols, out=None, stream=None):
     """bf16 values [rows, cols] of a packed matrix (exact)."""
     _mx8_packed((codes, scales), "packed", rows, cols)
     out = _out(out, "out", torch.bfloat16, (rows, cols), codes, stream)
-    _check("mx8_dequantize", lib().mx8_dequantize(_ptr(codes), _ptr(scales), rows, cols, _ptr(out), _stream(stream)))
+    pc, ps, po = _ptrs(stream, codes, scales, out)
+    _check("mx8_dequantize", lib().mx8_dequantize(pc, ps, rows, cols, po, _stream(stream)))
     return out
 
 
@@ -933,9 +956,9 @@ def rms_norm_fwd(X, weight, eps, residual=None, Y=None, S=None, mx8=None, stream
     elif S is not None:
         raise ValueError("S is the sum with a residual: without one it is X")
     packed = _mx8_out(mx8, "mx8", rows, cols, X, stream)
-    _check("rms_norm_fwd", lib().rms_norm_fwd(
-        _ptr(X), _ptr(residual), dt, rows, cols, _ptr(weight), wdt, float(eps), _ptr(S), _ptr(Y),
-        *((_ptr(packed[0]), _ptr(packed[1])) if packed else (None, None)), _stream(stream)))
+    px, pr, pw, ps, py, pc, pk = _ptrs(stream, X, residual, weight, S, Y, *(packed or (None, None)))
+    _check("rms_norm_fwd", lib().rms_norm_fwd(px, pr, dt, rows, cols, pw, wdt, float(eps), ps, py, pc, pk,
+                                              _stream(stream)))
     return Y, S, packed
 
 
@@ -950,9 +973,9 @@ def rms_norm_bwd(dY, S, weight, eps, dS=None, dX=True, dW=True, workspace=None, 
     dX = _opt_out(dX, "dX", S.dtype, (rows, cols), S, stream)
     dW = _opt_out(dW, "dW", torch.float32, (cols,), S, stream)
     ws = _workspace(int(lib().rms_norm_bwd_workspace(rows, cols)) if dW is not None else 0, S, workspace, stream)
-    _check("rms_norm_bwd", lib().rms_norm_bwd(
-        _ptr(dY), _ptr(S), _ptr(dS), dt, rows, cols, _ptr(weight), wdt, float(eps), _ptr(dX), _ptr(dW), _ptr(ws),
-        ws.numel(), _stream(stream)))
+    py, ps, pd, pw, px, pg, pk = _ptrs(stream, dY, S, dS, weight, dX, dW, ws)
+    _check("rms_norm_bwd", lib().rms_norm_bwd(py, ps, pd, dt, rows, cols, pw, wdt, float(eps), px, pg, pk, ws.numel(),
+                                              _stream(stream)))
     return dX, dW
 
 
@@ -972,10 +995,9 @@ def qlora_swiglu_fwd(X, codes, c2, c1, F, L1, L2, lora_scale=1.0, H=None, T_out=
     T_out = _opt_out(T_out, "T_out", torch.bfloat16, (2, M, r), X, stream)
     packed = _mx8_out(mx8, "mx8", 2 * M, F, X, stream)
     ws = _workspace(int(lib().qlora_swiglu_fwd_workspace(M, K, F, r)), X, workspace, stream)
+    p = _ptrs(stream, X, codes, c2, c1, L1, L2, H, T_out, *(packed or (None, None)), ws)
     _check("qlora_swiglu_fwd", lib().qlora_swiglu_fwd(
-        _ptr(X), M, K, F, _ptr(codes), _ptr(c2), _ptr(c1), _ptr(L1), _ptr(L2), r, float(lora_scale), _ptr(H),
-        _ptr(T_out), *((_ptr(packed[0]), _ptr(packed[1])) if packed else (None, None)), _ptr(ws), ws.numel(),
-        _stream(stream)))
+        p[0], M, K, F, *p[1:6], r, float(lora_scale), *p[6:], ws.numel(), _stream(stream)))
     return H, T_out, packed
 
 
@@ -996,10 +1018,9 @@ def qlora_swiglu_bwd(x8, dH, codes, c2, c1, L1, L2, gu8, T, lora_scale=1.0, dX=T
     dL1 = _out(dL1, "dL1", torch.float32, (2, K, r), dH, stream)
     dL2 = _out(dL2, "dL2", torch.float32, (2, r, F), dH, stream)
     ws = _workspace(int(lib().qlora_swiglu_bwd_workspace(M, K, F, r)), dH, workspace, stream)
+    p = _ptrs(stream, *x8, dH, codes, c2, c1, L1, L2, *gu8, T, dX, dL1, dL2, ws)
     _check("qlora_swiglu_bwd", lib().qlora_swiglu_bwd(
-        _ptr(x8[0]), _ptr(x8[1]), _ptr(dH), M, K, F, _ptr(codes), _ptr(c2), _ptr(c1), _ptr(L1), _ptr(L2), r,
-        float(lora_scale), _ptr(gu8[0]), _ptr(gu8[1]), _ptr(T), _ptr(dX), _ptr(dL1), _ptr(dL2), _ptr(ws), ws.numel(),
-        _stream(stream)))
+        *p[:3], M, K, F, *p[3:8], r, float(lora_scale), *p[8:], ws.numel(), _stream(stream)))
     return dX, dL1, dL2
 
 
@@ -1018,7 +1039,7 @@ def qlora_linear_bwd_mx8(x8, dY, codes, c2, c1, L1, L2, T, lora_scale=1.0, dX=Tr
     dL1 = _out(dL1, "dL1", torch.float32, (K, r), dY, stream)
     dL2 = _out(dL2, "dL2", torch.float32, (r, N), dY, stream)
     ws = _workspace(int(lib().qlora_linear_bwd_mx8_workspace(M, K, N, r)), dY, workspace, stream)
+    p = _ptrs(stream, *x8, dY, codes, c2, c1, L1, L2, T, dX, dL1, dL2, ws)
     _check("qlora_linear_bwd_mx8", lib().qlora_linear_bwd_mx8(
-        _ptr(x8[0]), _ptr(x8[1]), _ptr(dY), M, K, N, _ptr(codes), _ptr(c2), _ptr(c1), _ptr(L1), _ptr(L2), r,
-        float(lora_scale), _ptr(T), _ptr(dX), _ptr(dL1), _ptr(dL2), _ptr(ws), ws.numel(), _stream(stream)))
+        *p[:3], M, K, N, *p[3:8], r, float(lora_scale), *p[8:], ws.numel(), _stream(stream)))
     return dX, dL1, dL2

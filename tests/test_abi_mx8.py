@@ -111,7 +111,7 @@ def test_forward_copies_go_together():
 
 
 def test_workspaces_cover_the_saved_sums():
-    """T's two planes and at least one slice of both halves; dZ, B's planes turned, and the gradients' slices."""
+    """T's planes and at least one slice of both halves; dZ, B's planes turned, and the gradients' slices."""
     _, L = _lib()
     for M, K, F, r in ((1, 64, 1, 1), (17, 4096, 777, 5), (4096, 4096, 11008, 64)):
         assert L.qlora_swiglu_fwd_workspace(M, K, F, r) >= 8 * M * r + 8 * M * r
@@ -171,3 +171,28 @@ def test_binding_checks():
         q.qlora_linear_bwd_mx8(gu8, z(4, 20), *base, L1[0], z(8, 20), z(4, 8))
     with pytest.raises(ValueError):
         q.qlora_linear_bwd_mx8(x8, z(4, 20), *base, L1[0], z(8, 20), z(4, 8))
+
+
+def test_binding_wants_one_device():
+    """Tensors are refused on another device than the call's stream, and off the GPU, before anything is launched."""
+    from bit_quantized_lora_blockwise_amd._lib import _ptrs
+
+    class On:
+        shape = (1,)
+
+        def __init__(self, at):
+            self.at, self.is_cuda, self.device = at, at >= 0, f"cuda:{at}" if at >= 0 else "cpu"
+
+        def get_device(self):
+            return self.at
+
+        def data_ptr(self):
+            return 4096 + self.at
+
+    class Stream:
+        device_index = 1
+
+    assert _ptrs(Stream, On(1), None, On(1)) == [4097, None, 4097]
+    for bad in ((On(0),), (On(1), On(0)), (On(1), None, On(-1)), (On(-1),)):
+        with pytest.raises(ValueError):
+            _ptrs(Stream, *bad)

@@ -361,3 +361,22 @@ def test_decoding_row_by_row_is_the_batch():
     one = torch.cat([q.qlora_swiglu_fwd(b.X[i:i + 1].contiguous(), *b.base, F, b.L1, b.L2, S)[0] for i in range(M)])
     within(one, h, tol, "one at a time")
     assert np.count_nonzero(bits(one) != bits(q.qlora_swiglu_fwd(b.X, *b.base, F, b.L1, b.L2, S)[0])) <= one.numel() // 50
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    q = qlib()
+    b = Block(25, 20, 128, 40, 8)
+    x8 = q.mx8_quantize(b.X)
+    _, T, gu8 = q.qlora_swiglu_fwd(b.X, *b.base, 40, b.L1, b.L2, S, T_out=True, mx8=True)
+    w = torch.ones(128, device=DEV)
+    c = Block(26, 20, 128, 40, 8, halves=1)
+    calls = [lambda: q.mx8_quantize(b.X), lambda: q.mx8_dequantize(*x8, 20, 128), lambda: q.rms_norm_fwd(b.X, w, 1e-5),
+             lambda: q.rms_norm_bwd(b.X, b.X, w, 1e-5), lambda: q.qlora_swiglu_fwd(b.X, *b.base, 40, b.L1, b.L2, S),
+             lambda: q.qlora_swiglu_bwd(x8, b.d, *b.base, b.L1, b.L2, gu8, T, S),
+             lambda: q.qlora_linear_bwd_mx8(x8, c.d, *c.base, c.L1[0], c.L2[0], T[0], S)]
+    for f in calls:
+        f()
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1)      # the current device, as the binding asks for it
+    for f in calls:
+        with pytest.raises(ValueError, match="cuda:1"):
+            f()
