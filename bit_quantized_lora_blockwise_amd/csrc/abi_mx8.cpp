@@ -65,12 +65,12 @@ bool few_dx_ok(int64_t M, int64_t K, int64_t N, int r) {
   return (M + 15) / 16 * ((r + 15) / 16) <= 24 && dx_small_ok(M, K) && !(N % 8 == 0 && split_ok(M, K, N));
 }
 
-// Backward: [dZ (gated)][G][its planes][fp32 partials, of G and then of the gradients].
+// Backward: [dZ (gated)][G (gated: two planes of it)][its three planes][fp32 partials, of G and then of the gradients].
 struct BwdWs {
   size_t dz, g, planes, part, total;
 };
 BwdWs bwd_ws(int64_t M, int64_t K, int64_t N, int halves, int r) {
-  BwdWs w{halves == 2 ? round_up((size_t)M * glu_ldz(N) * 2) : 0, round_up((size_t)halves * M * r * 2),
+  BwdWs w{halves == 2 ? round_up((size_t)M * glu_ldz(N) * 2) : 0, round_up((size_t)halves * halves * M * r * 2),
           round_up((size_t)3 * halves * M * g_pitch(r) * 2), 0, 0};
   const size_t slices = halves == 2 ? glu_back_ws(M, N, r) : few_dx_ok(M, K, N, r) ? std::max(mx4_small_ws(M, r), lora_skinny_ws(M, N, r))
                                                                                 : lora_skinny_ws(M, N, r);
@@ -231,7 +231,7 @@ int qlora_swiglu_bwd(const uint8_t* x_codes, const uint8_t* x_scales, const uint
   int slices = 0;
   QL_TRY(launch_glu_back(dH, M, F, gu_codes, gu_scales, L2, r, lora_scale, dZ, part, &slices, s));
   const bool split = split_ok(M, K, 2 * F), small = !split && dx_small_ok(M, K), sums = dX && small && slices <= kSmallSlices;
-  if (!sums) QL_TRY(launch_low(Low{part, slices, 1.0f, G, planes}, 2, M, r, s));
+  if (!sums) QL_TRY(launch_low(Low{part, slices, 1.0f, G, planes, true}, 2, M, r, s));
   auto product = [&] {
     if (!dX) return hipSuccess;
     // G's planes from the product for few rows where it adds the slices up: a launch less
@@ -239,8 +239,8 @@ int qlora_swiglu_bwd(const uint8_t* x_codes, const uint8_t* x_scales, const uint
       return launch_dx_small(dZ, M, K, 2 * F, codes, c2, c1, sums ? nullptr : G, part, slices, planes, L1, r, dX, kNoDrop, s,
                              glu_ldz(F), 2);
     if (split)
-      return launch_qgemm_dx_split(dZ, M, K, 2 * F, codes, c2, c1, G, L1, r, dX, part, s, 2, glu_ldz(F));
-    return launch_qgemm_big(true, dZ, M, K, 2 * F, codes, c2, c1, G, L1, r, 1.0f, dX, s, 2, nullptr, glu_ldz(F));
+      return launch_qgemm_dx_split(dZ, M, K, 2 * F, codes, c2, c1, G, L1, r, dX, part, s, 2, glu_ldz(F), true);
+    return launch_qgemm_big(true, dZ, M, K, 2 * F, codes, c2, c1, G, L1, r, 1.0f, dX, s, 2, nullptr, glu_ldz(F), true);
   };
   auto grads = [&](hipStream_t st) {
     return launch_grads8(Grads8{x_codes, x_scales, dH, gu_codes, gu_scales, planes, T, lora_scale, dL1, dL2}, M, K, F, 2, r,
@@ -273,7 +273,7 @@ int qlora_linear_bwd_mx8(const uint8_t* x_codes, const uint8_t* x_scales, const 
              small = !split && dx_small_ok(M, K);
   if (few) QL_TRY(launch_small_slices(dY, M, N, L2, false, r, kNoDrop, lora_scale, part, &slices, s));
   else QL_TRY(launch_lora_slices(dY, M, N, L2, false, r, part, &slices, s));
-  if (!dX || !few) QL_TRY(launch_low(Low{part, slices, few ? 1.0f : lora_scale, G, planes}, 1, M, r, s));
+  if (!dX || !few) QL_TRY(launch_low(Low{part, slices, few ? 1.0f : lora_scale, G, planes, false}, 1, M, r, s));
   auto product = [&] {
     if (!dX) return hipSuccess;
     if (small)

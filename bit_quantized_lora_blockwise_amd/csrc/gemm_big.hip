@@ -175,6 +175,7 @@ struct BigOut {
   int full;           // kGlu: tiles taken as 128 columns; the rest as two of 64 by a launch of their own
   float* part;        // kSplit: [slices][tiles], each a tile's accumulators as the waves hold them
   int slices, steps;  // kSplit: and the steps of one, an even number
+  int two;            // dX: LA holds two planes of each segment's G, high and low, and LB one L1 for both
 };
 
 template <bool kDx, bool kTail, bool kB16 = false, bool kDrop = false, int kCols = 0,
@@ -483,7 +484,7 @@ __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict_
             *(LDS_AS u32x4*)(lb + (idx >> 5) * kPD + (idx & 31) * 8) = vb[i];
           }
         } else {
-          const uint16_t* lb_src = LB + gs * K * r;
+          const uint16_t* lb_src = LB + (gs >> gl.two) * K * r;
           const __amdgpu_buffer_rsrc_t rlb = rsrc(lb_src, (uint64_t)K * r * 2);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
@@ -518,7 +519,7 @@ __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict_
           *(LDS_AS u32x4*)(lb + c * kPD + pp) = v8;
         }
       } else {
-        const uint16_t* lb_src = LB + gs * K * r;
+        const uint16_t* lb_src = LB + (gs >> gl.two) * K * r;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int idx = tp + 256 * i, row = idx >> 3, cc = (idx & 7) * 8;
@@ -847,12 +848,14 @@ static dim3 tile_grid(int64_t M, int64_t P) {
 
 hipError_t launch_qgemm_big(bool dx, const uint16_t* A, int64_t M, int64_t K, int64_t N, const uint8_t* codes,
                             const uint8_t* c2, const float* c1, const uint16_t* LA, const uint16_t* LB, int r,
-                            float scale, uint16_t* C, hipStream_t s, int nseg, const drop::Params* d, int64_t ld) {
+                            float scale, uint16_t* C, hipStream_t s, int nseg, const drop::Params* d, int64_t ld,
+                            bool two) {
   const int64_t P = dx ? K : N;
   const int64_t lda = ld ? ld : dx ? N : K;
   const int64_t seg = N / nseg;   // columns of W per segment (a multiple of 256 when nseg > 1)
   const dim3 grid = tile_grid(M, P);
   const uint16_t* nw = nullptr;
+  const BigOut planes{nullptr, nullptr, 0, nullptr, 0, 0, two};
   if (!dx)
     hipLaunchKernelGGL((k_qgemm_big<false, false>), grid, dim3(kT), 0, s, A, M, K, N, codes, c2, c1, LA, LB, r,
                        scale, C, nf4_params(), nseg, seg, nw, drop::Params{}, lda, BigOut{});
@@ -865,10 +868,10 @@ hipError_t launch_qgemm_big(bool dx, const uint16_t* A, int64_t M, int64_t K, in
                          LB, r, scale, C, nf4_params(), nseg, seg, nw, *d, lda, BigOut{});
   } else if (N % kBR == 0)
     hipLaunchKernelGGL((k_qgemm_big<true, false>), grid, dim3(kT), 0, s, A, M, K, N, codes, c2, c1, LA, LB, r,
-                       scale, C, nf4_params(), nseg, seg, nw, drop::Params{}, lda, BigOut{});
+                       scale, C, nf4_params(), nseg << two, seg, nw, drop::Params{}, lda, planes);
   else
     hipLaunchKernelGGL((k_qgemm_big<true, true>), grid, dim3(kT), 0, s, A, M, K, N, codes, c2, c1, LA, LB, r,
-                       scale, C, nf4_params(), nseg, seg, nw, drop::Params{}, lda, BigOut{});
+                       scale, C, nf4_params(), nseg << two, seg, nw, drop::Params{}, lda, planes);
   return hipGetLastError();
 }
 
@@ -886,15 +889,15 @@ size_t qgemm_dx_split_ws(int64_t M, int64_t K, int64_t N) {
 
 hipError_t launch_qgemm_dx_split(const uint16_t* A, int64_t M, int64_t K, int64_t N, const uint8_t* codes,
                                  const uint8_t* c2, const float* c1, const uint16_t* LA, const uint16_t* LB, int r,
-                                 uint16_t* C, float* part, hipStream_t s, int nseg, int64_t ld) {
+                                 uint16_t* C, float* part, hipStream_t s, int nseg, int64_t ld, bool two) {
   const int slices = qgemm_dx_slices(M, K, N);
   const int64_t steps = (N + kBR - 1) / kBR, tiles = (M + kBM - 1) / kBM * ((K + kBP - 1) / kBP);
-  const BigOut out{nullptr, nullptr, 0, part, slices, (int)((steps + 2 * slices - 1) / (2 * slices) * 2)};
+  const BigOut out{nullptr, nullptr, 0, part, slices, (int)((steps + 2 * slices - 1) / (2 * slices) * 2), two};
   const uint16_t* nw = nullptr;
   const dim3 grid((unsigned)(tiles * slices));
 #define QL_SPLIT(T)                                                                                                   \
   hipLaunchKernelGGL((k_qgemm_big<true, T, false, false, 0, true>), grid, dim3(kT), 0, s, A, M, K, N, codes, c2, c1, LA, LB, r, \
-                     1.0f, C, nf4_params(), nseg, N / nseg, nw, drop::Params{}, ld ? ld : N, out)
+                     1.0f, C, nf4_params(), nseg << two, N / nseg, nw, drop::Params{}, ld ? ld : N, out)
   if (N % kBR == 0) QL_SPLIT(false);
   else QL_SPLIT(true);
 #undef QL_SPLIT
@@ -910,7 +913,7 @@ hipError_t launch_glu_big(const uint16_t* X, int64_t M, int64_t K, int64_t F, co
   // The tiles of a last round of at most half the CUs go to twice as many, in halves
   const int64_t rest = tiles % wgs, halves = (rest + 7) / 8 * 16;
   const int64_t full = halves <= wgs ? tiles - rest : tiles;
-  const BigOut out{gu_codes, gu_scales, (int)full, nullptr, 0, 0};
+  const BigOut out{gu_codes, gu_scales, (int)full, nullptr, 0, 0, 0};
   if (full)
     hipLaunchKernelGGL((k_qgemm_big<false, false, false, false, kBPG>), dim3((unsigned)std::min(full, wgs)), dim3(kT), 0, s, X,
                        M, K, 2 * F, codes, c2, c1, T, L2, r, scale, H, nf4_params(), 1, F, nw, drop::Params{}, K, out);

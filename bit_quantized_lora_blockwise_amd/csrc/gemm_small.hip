@@ -56,7 +56,8 @@ __device__ __forceinline__ void sum8(__amdgpu_buffer_rsrc_t rp, int S, int M, in
 }
 
 // kVec: ldy % 8 == 0 (rows of dY in whole 16-byte pieces, zeros from N to ldy); kVecR: r % 8 == 0; kSum: G
-// as slices.  halves: of W's stacked rows, each with a G [M][r] (slices [S][halves][M][r], planes [halves][3][M][..])
+// as slices.  halves: of W's stacked rows, each with a G (two planes [M][r] where there are two; slices
+// [S][halves][M][r], planes [halves][3][M][..])
 // and an L1 [K][r] of its own.
 template <bool kVec, bool kVecR, bool kSum>
 __global__ __launch_bounds__(64 * kW) void k_dx_small(const uint16_t* __restrict__ dY, int M, int K, int N,
@@ -125,14 +126,14 @@ __global__ __launch_bounds__(64 * kW) void k_dx_small(const uint16_t* __restrict
     const int64_t plane = (int64_t)M * pitch;
     for (int half = 0; half < halves; ++half) {
     const __amdgpu_buffer_rsrc_t rg = kSum ? rsrc(Gp + (int64_t)half * M * r, (uint64_t)M * r * 4 * (S * halves - half))
-                                           : rsrc(G + (int64_t)half * M * r, (uint64_t)M * r * 2),
+                                           : rsrc(G + (int64_t)half * halves * M * r, (uint64_t)M * r * 2 * halves),
                                  rl = rsrc(L1 + ((int64_t)half * K + first) * r, (uint64_t)32 * r * 2);
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       const int c = 16 * s + 8 * h;
       if (16 * s >= r) break;                      // uniform
       const bf16x8 a = load8<kVecR>(rl, (uint32_t)(x * r + c) * 2u, r - c);
-      bf16x8 b;
+      bf16x8 b, rest;                              // two halves: 16 bits of G
       if constexpr (kSum) {
         float sum[8];
         sum8(rg, S, M, r, m, c, halves * M * r, sum);
@@ -146,13 +147,16 @@ __global__ __launch_bounds__(64 * kW) void k_dx_small(const uint16_t* __restrict
             sum[2 * k + 1] -= __uint_as_float(v[n][k] & 0xFFFF0000u);
           }
         b = __builtin_bit_cast(bf16x8, v[0]);
+        rest = __builtin_bit_cast(bf16x8, v[1]);
         if (blockIdx.x == 0 && w == 0 && m < M && c < pitch)
 #pragma unroll
           for (int n = 0; n < 3; ++n) *(u32x4*)(planes + (3 * half + n) * plane + (int64_t)m * pitch + c) = v[n];
       } else {
         b = load8<kVecR>(rg, (uint32_t)(m * r + c) * 2u, m < M ? r - c : 0);
+        if (halves == 2) rest = load8<kVecR>(rg, (uint32_t)((M + m) * r + c) * 2u, m < M ? r - c : 0);
       }
       low = qk::mfma32(a, b, low);
+      if (halves == 2) low = qk::mfma32(a, rest, low);
     }
     }
     // half h draws octets 2 h and 2 h + 1 of its row; each lane takes its own columns 8 g + 4 h + e from both halves'

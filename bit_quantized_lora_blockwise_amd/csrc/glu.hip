@@ -92,7 +92,7 @@ __global__ __launch_bounds__(kT) void k_low(Low q, int halves, int64_t M, int r,
       for (int j = 0; j < kN; ++j) {
         b[j] = qk::f32_to_bf16(x[j]);
         x[j] -= qk::bf16_to_f32(b[j]);
-        if (a == 0 && c < r) q.G[at + j] = b[j];
+        if (a <= q.two && c < r) q.G[at + (int64_t)((q.two ? h : 0) + a) * M * r + j] = b[j];
       }
       uint16_t* to = q.planes + ((int64_t)h * 3 + a) * n + i;
       if constexpr (kN == 4) *(u32x2*)to = u32x2{b[0] | (uint32_t)b[1] << 16, b[2] | (uint32_t)b[3] << 16};

@@ -218,19 +218,21 @@ hipError_t launch_qgemv_fwd_fused(const uint16_t* X, int64_t M, int64_t K, int64
 // 256), each with its own adapter: LA holds nseg [M, r] blocks, LB nseg L2
 // [r, N / nseg] (fwd) or L1 [K, r] (dX) blocks.  d (dX, nseg = 1): dropout of the
 // adapter term, dX = bf16(dY W' + D o (G L1^T)).  lda: elements from one row of A to the
-// next, a multiple of 8, zeros past the row (0: dense).
+// next, a multiple of 8, zeros past the row (0: dense).  two (dX): LA holds two planes [M, r] of each segment's G,
+// what bf16 takes of it and of the rest.
 bool qgemm_big_ok(bool dx, int64_t M, int64_t K, int64_t N);
 hipError_t launch_qgemm_big(bool dx, const uint16_t* A, int64_t M, int64_t K, int64_t N, const uint8_t* codes,
                             const uint8_t* c2, const float* c1, const uint16_t* LA, const uint16_t* LB, int r,
                             float scale, uint16_t* C, hipStream_t s, int nseg = 1,
-                            const drop::Params* d = nullptr, int64_t lda = 0);
+                            const drop::Params* d = nullptr, int64_t lda = 0, bool two = false);
 // dX of few tiles: the reduction in slices, whose fp32 sums (part: qgemm_dx_split_ws bytes) a launch of its own
 // adds up in order.  1: not split.
 int qgemm_dx_slices(int64_t M, int64_t K, int64_t N);
 size_t qgemm_dx_split_ws(int64_t M, int64_t K, int64_t N);
 hipError_t launch_qgemm_dx_split(const uint16_t* A, int64_t M, int64_t K, int64_t N, const uint8_t* codes,
                                  const uint8_t* c2, const float* c1, const uint16_t* LA, const uint16_t* LB, int r,
-                                 uint16_t* C, float* part, hipStream_t s, int nseg = 1, int64_t lda = 0);
+                                 uint16_t* C, float* part, hipStream_t s, int nseg = 1, int64_t lda = 0,
+                                 bool two = false);
 // The same two GEMMs with a bf16 weight W [N, K] in place of the packed one
 // (LoRA over a bf16 base): dx = false Y = bf16(X W^T + scale T L2), dx = true
 // dX = bf16(dY W + G L1^T).  bgemm_ok says whether the shapes qualify.
@@ -305,8 +307,9 @@ struct Low {
   const float* part;      // fp32 slices [slices][halves][M][r]
   int slices;
   float scale;
-  uint16_t* G;            // [halves][M][r]
+  uint16_t* G;            // [halves][two + 1][M][r]: the first planes
   uint16_t* planes;       // [halves][3][M][g_pitch(r)]
+  bool two;
 };
 hipError_t launch_low(const Low& q, int halves, int64_t M, int r, hipStream_t s);
 

@@ -10,8 +10,8 @@ Tolerances, elementwise, derived from the rounding points (U = 2^-24, half a ste
   a value in 8 bits is the rounding of one in [g - dg, g + dg];
   dZ: dU = dH G sig by E |dU|, dG = dH U sig (1 + G (1 - sig)) by E |dH U| sig (1 + |G|) (1 + |G|): the
   factor's two terms may cancel, and 1 - sig carries sig's error times G;
-  B and dL1, dL2 carry those and their own sums, three planes lose 2^-24; dX takes dZ and B in bf16:
-  2^-8 |dZ| |W| and 2^-8 |B| |L1| on top.
+  B and dL1, dL2 carry those and their own sums, three planes lose 2^-24; dX takes dZ in bf16 and B as
+  two bf16 planes: 2^-8 |dZ| |W| and 2^-16 |B| |L1| on top (a linear's dX takes B in bf16).
 """
 import numpy as np
 import pytest
@@ -124,7 +124,7 @@ def check_backward(q, b, x8, gu8, T, dX, dL1, dL2):
                f"dL2[{h}]")
         if dX is not None:
             tx = tx + ((2.0**-8 + (2 * F + 130) * U) * np.abs(dz[h]) + off[h]) @ w
-            tx = tx + ((2.0**-8 + (2 * F + 130) * U) * np.abs(B[h]) + ob) @ a1.T
+            tx = tx + ((2.0**-16 + (2 * F + 260) * U) * np.abs(B[h]) + ob) @ a1.T
     if dX is not None:
         within(dX, rx, tx, "dX")
         rel = np.linalg.norm(f64(dX) - rx) / np.linalg.norm(rx)
