@@ -32,10 +32,13 @@ bool glu_ok(int64_t M, int64_t K, int64_t F, int r) {
   return F > 0 && F < kLim / 2 && layer_ok(M, K, 2 * F, glu_ldz(F), r, 2);
 }
 
-// Whether T goes into the product as slices, which it adds up itself (a launch less): while the
-// rank-r product has few tiles of 16 x 16, and the product is one of those for few rows.
+// Whether T goes into the product as slices, which it adds up itself (a launch less): where the
+// product is one of those for few rows, while the rank-r product has at most 128 tiles of 16 x 16
+// (past 64 its launch takes one slice a tile).  Whole calls with 8-bit copies, us, planes of their
+// own / slices: 1024 -> 2 x 2752 17 rows 37 / 31, 128 rows 40 / 31; 2048 -> 2 x 1000 500 rows (128
+// tiles) 46 / 37, 1000 rows (252) 63 / 63; 8192 -> 2 x 256 1000 rows 67 / 76.
 bool few_ok(int64_t M, int64_t K, int64_t F, int r) {
-  return (M + 15) / 16 * ((r + 15) / 16) <= 24 && glu_small_ok(M, K, F);
+  return (M + 15) / 16 * ((r + 15) / 16) <= 128 && glu_small_ok(M, K, F);
 }
 
 // Forward: [T's planes of both halves][fp32 slices of both].
@@ -50,19 +53,22 @@ FwdWs fwd_ws(int64_t M, int64_t K, int64_t F, int r) {
 }
 
 // Whether dX [M, K], whose reduction is over n columns, is taken in slices of the reduction.  The work
-// groups of the product for few rows (64 columns of 32 rows) and of the large tiles each walk all of it; slices
-// cost a launch and the partial sums' way to memory.  Whole backwards, us, walked / in slices: gated, K = 4096, n
-// = 22016 1 row 91 / 69, 64 rows 120 / 73, 512 rows 456 / 154, 1024 rows 505 / 246; K = 1024, n = 5504 64 rows 49 / 47, 512 rows 56 / 64, 1024
-// rows 84 / 73; K = 512, n = 2752 512 rows 48 / 57; linear, K = n = 4096 128 rows 41 / 48, 256 rows 62 / 52, 1024
-// rows 119 / 83; K = 11008, n = 4096 17 rows 35 / 53, 64 rows 62 / 55.
+// groups of the product for few rows (64 columns of 32 rows) and of the large tiles each walk all of
+// it; slices cost a launch and the partial sums' way to memory.  Whole backwards, us, walked / in
+// slices: gated, K = 4096, n = 22016 1 row 91 / 69, 64 rows 120 / 73, 512 rows 456 / 154, 1024 rows
+// 505 / 246; K = 1024, n = 5504 64 rows 49 / 47, 512 rows 56 / 64, 1024 rows 84 / 73; K = 512, n =
+// 2752 512 rows 48 / 57; linear, K = n = 4096 128 rows 41 / 48, 256 rows 62 / 52, 1024 rows 119 / 83;
+// K = 11008, n = 4096 17 rows 35 / 53, 64 rows 62 / 55.
 bool split_ok(int64_t M, int64_t K, int64_t n) {
   const int64_t groups = K / 64 * ((M + 31) / 32);
   return n * std::max<int64_t>(groups, 256) >= 6144 * 256 && qgemm_dx_slices(M, K, n) > 1;
 }
 
 // Whether a linear's G goes to dX for few rows as slices, which it adds up itself (a launch less).
+// Whole backwards, us, apart / so: 4096 -> 4096 1 row 34 / 30, 96 rows (24 tiles) 42 / 39, 160 rows
+// (40) 63 / 65; 1024 -> 1024 256 rows (64) 31 / 28.
 bool few_dx_ok(int64_t M, int64_t K, int64_t N, int r) {
-  return (M + 15) / 16 * ((r + 15) / 16) <= 24 && dx_small_ok(M, K) && !(N % 8 == 0 && split_ok(M, K, N));
+  return (M + 15) / 16 * ((r + 15) / 16) <= 64 && dx_small_ok(M, K) && !(N % 8 == 0 && split_ok(M, K, N));
 }
 
 // Backward: [dZ (gated)][G (gated: two planes of it)][its three planes][fp32 partials, of G and then of the gradients].
@@ -72,8 +78,8 @@ struct BwdWs {
 BwdWs bwd_ws(int64_t M, int64_t K, int64_t N, int halves, int r) {
   BwdWs w{halves == 2 ? round_up((size_t)M * glu_ldz(N) * 2) : 0, round_up((size_t)halves * halves * M * r * 2),
           round_up((size_t)3 * halves * M * g_pitch(r) * 2), 0, 0};
-  const size_t slices = halves == 2 ? glu_back_ws(M, N, r) : few_dx_ok(M, K, N, r) ? std::max(mx4_small_ws(M, r), lora_skinny_ws(M, N, r))
-                                                                                : lora_skinny_ws(M, N, r);
+  size_t slices = halves == 2 ? glu_back_ws(M, N, r) : lora_skinny_ws(M, N, r);
+  if (halves == 1 && few_dx_ok(M, K, N, r)) slices = std::max(slices, mx4_small_ws(M, r));
   w.part = std::max(slices, grads8_ws(M, K, N, halves, r));
   if ((halves == 2 || N % 8 == 0) && split_ok(M, K, halves * N)) w.part = std::max(w.part, qgemm_dx_split_ws(M, K, halves * N));
   w.part = round_up(w.part);

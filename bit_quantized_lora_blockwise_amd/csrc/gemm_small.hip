@@ -307,6 +307,8 @@ __global__ __launch_bounds__(64 * kW) void k_fwd_small(const uint16_t* __restric
 // waves form the adapter's term of one half of 32 rows each meanwhile, add the eight waves'
 // sums in order and finish.  T enters as three bf16 planes (24 bits: G and U may be
 // kept in 8): given [2 halves][3][M][pitch], or kSum: formed here from its slices [2][S][M][r].
+// 17 rows 4096 -> 2 x 11008: 48 us, 47 MB; bound: the loads' way back.  A lane's row is its own, so
+// an instruction's 64 lanes read 64 lines whatever their width, 60 clocks each (TD busy 28 us, vector units 14).
 template <int kI, bool kSum>
 __global__ __launch_bounds__(64 * (kW + 2 * kI)) void k_glu_small(const uint16_t* __restrict__ X, int M, int K, int F,
                                                        const uint8_t* __restrict__ codes,
@@ -446,6 +448,9 @@ hipError_t launch_glu_small(const uint16_t* X, int64_t M, int64_t K, int64_t F, 
   hipLaunchKernelGGL((k_glu_small<I, A>), dim3(cols, (unsigned)((M + 32 * I - 1) / (32 * I))),                  \
                      dim3(64 * (kW + 2 * I)), 0, s, X, (int)M, (int)K, (int)F, codes, c2, c1, T, Tp, S, T_out, L2, r, \
                      scale, H, gu_codes, gu_scales, nf4_params())
+  // 32 rows a work group while those are at most one a CU: 4096 -> 2 x 1024 64 rows 26 us (64 rows a
+  // group: 40), 1024 -> 2 x 1024 200 rows (224 groups) 14 (16); past that a CU would rebuild weights
+  // twice: 2048 -> 2 x 5504 64 rows 45 us a call (37)
   const bool one = M <= 32 || cols * ((M + 31) / 32) <= 256;
   if (T) {
     if (one) QL_GLU(1, false);

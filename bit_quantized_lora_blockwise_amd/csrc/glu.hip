@@ -239,8 +239,9 @@ __global__ __launch_bounds__(kBT, 4) void k_glu_back(const uint16_t* __restrict_
     }
 }
 
-// Slices of that pass: about 512 work groups (1024: 114 us for 111 at 4096 x 2 x 11008, 256: 121), but no more than 32 slices to add up for each row, and as many
-// as the product for few rows adds up itself where the pass is short all the same (up to four steps).
+// Slices of that pass: about 512 work groups (1024: 114 us for 111 at 4096 x 2 x 11008, 256: 121), but no
+// more than 32 slices to add up for each row, and as many as the product for few rows adds up
+// itself where the pass is short all the same (up to four steps).
 struct PlanBack {
   int rows, tiles, slices;
   int64_t chunk;
@@ -250,7 +251,8 @@ PlanBack plan_back(int64_t M, int64_t F) {
   p.rows = M >= 512 ? 64 : 32;             // both sides measured above
   p.tiles = (int)((M + p.rows - 1) / p.rows);
   const int cols = kBElems / p.rows;
-  const int64_t steps = (F + cols - 1) / cols, s = std::max<int64_t>(1, std::min<int64_t>({512 / p.tiles, steps, steps <= 4 * kSmallSlices ? kSmallSlices : 32}));
+  const int64_t steps = (F + cols - 1) / cols, most = steps <= 4 * kSmallSlices ? kSmallSlices : 32;
+  const int64_t s = std::max<int64_t>(1, std::min<int64_t>({512 / p.tiles, steps, most}));
   p.chunk = (steps + s - 1) / s * cols;
   p.slices = (int)((F + p.chunk - 1) / p.chunk);
   return p;
@@ -285,8 +287,8 @@ hipError_t launch_glu_back(const uint16_t* dH, int64_t M, int64_t F, const uint8
   *slices = p.slices;
   const dim3 grid((unsigned)p.tiles, (unsigned)p.slices);
 #define QL_BACK(R, V)                                                                                                      \
-  hipLaunchKernelGGL((k_glu_back<R, V>), grid, dim3(kBT), 0, s, dH, (int)M, (int)F, gu_codes, gu_scales, L2, r, scale, (int)p.chunk, \
-                     (int)glu_ldz(F), dZ, part)
+  hipLaunchKernelGGL((k_glu_back<R, V>), grid, dim3(kBT), 0, s, dH, (int)M, (int)F, gu_codes, gu_scales, L2, r, scale,  \
+                     (int)p.chunk, (int)glu_ldz(F), dZ, part)
   if (p.rows == 64) {
     if (F % 8 == 0) QL_BACK(64, true);
     else QL_BACK(64, false);

@@ -6,6 +6,9 @@
 // over it and the pass that uses the sum.  Sums and statistics are fp32 (a thread's at most
 // 32 squares, then a tree), the root fp64: one of them a row.
 //
+// bf16: 2048 x 8192 with the residual and 8-bit copies 30 us, 5.0 TB/s; backward 4096 x 4096 with dS
+// 26.5 us, 5.1 TB/s, and 4 us for dw.
+//
 // A row belongs to a wave (up to 1024 columns) or to 256, 512 or 1024 threads, one or two
 // chunks of eight columns a thread (four past 16384 columns).  Rows are read through a
 // descriptor of their own, so that no load stands behind a branch.
@@ -371,7 +374,10 @@ int64_t shares_of(int64_t rows, int64_t cols) {
   return std::min<int64_t>((rows + per - 1) / per, 512);
 }
 
-// Calls f with the threads of a row and the chunks of a thread.
+// Calls f with the threads of a row and the chunks of a thread: two chunks before more threads, so
+// that more rows share a CU.  4096 rows of bf16 with the residual, us, so / with one chunk and twice
+// the threads: 8192 columns forward 47 / 59, backward 54 / 56; 4096 columns 23 / 22, 29.0 / 29.3; 1024
+// columns 12.6 / 12.5, 17.8 / 17.7.
 template <typename F>
 void by_columns(int64_t cols, F f) {
   if (cols <= 512) f(std::integral_constant<int, 64>{}, std::integral_constant<int, 1>{});
