@@ -38,17 +38,6 @@ static_assert(6 * kGABytes + 2 * kGBBytes <= kLds, "the gated step fits");
 using glu::kOOB;
 using glu::rsrc;
 
-// Ranks c .. c + 7 of a row of T [M][r]; kVecR: r % 8 == 0.
-template <bool kVecR>
-__device__ __forceinline__ u32x4 load_t(__amdgpu_buffer_rsrc_t rt, int m, int c, int r, bool on) {
-  const uint32_t at = 2u * (uint32_t)(m * r + c);
-  if constexpr (kVecR) return __builtin_amdgcn_raw_buffer_load_b128(rt, on && c < r ? at : kOOB, 0, 0);
-  uint32_t e[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) e[j] = __builtin_amdgcn_raw_buffer_load_b16(rt, on && c + j < r ? at + 2 * j : kOOB, 0, 0);
-  return u32x4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
-}
-
 enum Kind { kPacked, kDense, kGated };
 
 struct Job {
@@ -116,7 +105,7 @@ __device__ __forceinline__ void columns(const Job& jb, int M, int r, int rp, int
       if constexpr (kKind == kPacked)
         g.b[j] = __builtin_amdgcn_raw_buffer_load_b128(
             rb[j], m + brow < m_end && 8 * bc < rp ? (uint32_t)((m + brow) * rp + 8 * bc) * 2u : kOOB, 0, 0);
-      else g.b[j] = load_t<kVecR>(rb[j], m + brow, 8 * bc, r, m + brow < m_end);
+      else g.b[j] = glu::load8<kVecR>(rb[j], 2u * (uint32_t)((m + brow) * r), 8 * bc, r, m + brow < m_end);
     }
     return g;
   };
@@ -140,7 +129,8 @@ __device__ __forceinline__ void columns(const Job& jb, int M, int r, int rp, int
       }
     }
 #pragma unroll
-    for (int j = 0; j < kPlanes; ++j) *(LDS_AS u32x4*)(lds + kABytes + j * kBBytes + brow * (kPitchB * 2) + 16 * bc) = g.b[j];
+    for (int j = 0; j < kPlanes; ++j) *(LDS_AS u32x4*)(lds + kABytes + j * kBBytes + brow * (kPitchB * 2) + 16 * bc) =
+        kKind == kPacked ? g.b[j] : glu::fit8<kVecR>(g.b[j], 8 * bc, r);
   };
   f32x16 acc[2][2] = {};
   Regs g = load(m_beg);
@@ -223,7 +213,7 @@ __device__ __forceinline__ void gated(const Job& jb, int M, int r, int tile, int
     s.sg = __builtin_amdgcn_raw_buffer_load_b8(rs, os, 0, 0);
     s.su = __builtin_amdgcn_raw_buffer_load_b8(rs, in ? os + up_s : kOOB, 0, 0);
     s.d = glu::load8<kVec>(rd, (uint32_t)m * jb.P * 2u, p, jb.P, m < m_end);
-    s.b = load_t<kVecR>(rb, m0 + brow, 8 * bc, r, m0 + brow < m_end);
+    s.b = glu::load8<kVecR>(rb, 2u * (uint32_t)((m0 + brow) * r), 8 * bc, r, m0 + brow < m_end);
     return s;
   };
   auto store = [&](const Regs& s) {
@@ -245,7 +235,7 @@ __device__ __forceinline__ void gated(const Job& jb, int M, int r, int tile, int
 #pragma unroll
       for (int n = 0; n < 3; ++n)
         *(LDS_AS u32x4*)(lds + (3 * h + n) * kGABytes + slot<2 * kGP>(row, piece)) = glu::take_plane(dz[h]);
-    *(LDS_AS u32x4*)(lds + 6 * kGABytes + bh * kGBBytes + brow * (kPitchB * 2) + 16 * bc) = s.b;
+    *(LDS_AS u32x4*)(lds + 6 * kGABytes + bh * kGBBytes + brow * (kPitchB * 2) + 16 * bc) = glu::fit8<kVecR>(s.b, 8 * bc, r);
   };
   f32x16 acc[2] = {};
   Regs g = load(m_beg);
