@@ -149,7 +149,8 @@ def _stream(stream=None):
 
 def _ptrs(stream, *tensors):
     """Device addresses of a call's tensor arguments (None -> NULL), which all have to be on the device of
-    its stream: a kernel runs there, and memory of another device may not be mapped on it."""
+    its stream (of one another, where only the stream's handle is known): a kernel runs there, and memory of
+    another device may not be mapped on it."""
     dev, out = None, []
     for t in tensors:
         if t is None:
@@ -159,7 +160,7 @@ def _ptrs(stream, *tensors):
         if at != dev:
             out.append(_ptr(t))            # refuses what is not on a GPU
             if dev is None:
-                dev = torch._C._cuda_getDevice() if stream is None else stream.device_index
+                dev = torch._C._cuda_getDevice() if stream is None else getattr(stream, "device_index", at)
             if at != dev:
                 raise ValueError(f"every tensor argument must be on the device of the call's stream, cuda:{dev} (got a "
                                  f"{t.device} tensor of shape {tuple(t.shape)})")

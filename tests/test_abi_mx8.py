@@ -192,7 +192,13 @@ def test_binding_wants_one_device():
     class Stream:
         device_index = 1
 
+    class Handle:
+        cuda_stream = 0
+
     assert _ptrs(Stream, On(1), None, On(1)) == [4097, None, 4097]
+    assert _ptrs(Handle, None, On(1), On(1)) == [None, 4097, 4097]
+    with pytest.raises(ValueError):
+        _ptrs(Handle, On(1), On(0))
     for bad in ((On(0),), (On(1), On(0)), (On(1), None, On(-1)), (On(-1),)):
         with pytest.raises(ValueError):
             _ptrs(Stream, *bad)

@@ -301,6 +301,33 @@ def test_backward_captured(M, K, F):
             assert torch.equal(u, v), k
 
 
+def test_stream_given_by_argument_or_handle():
+    """Calls on a stream that is passed, as a stream or as an object with its handle alone."""
+    q = qlib()
+    b = Block(27, 70, 128, 104, 8)
+    w = torch.ones(128, device=DEV)
+
+    def run(**kw):
+        Y, Sm, y8 = q.rms_norm_fwd(b.X, w, 1e-5, residual=b.X, mx8=True, **kw)
+        H, T, gu8 = q.qlora_swiglu_fwd(Y, *b.base, 104, b.L1, b.L2, S, T_out=True, mx8=True, **kw)
+        g = q.qlora_swiglu_bwd(y8, b.d, *b.base, b.L1, b.L2, gu8, T, S, **kw)
+        dX, dw = q.rms_norm_bwd(g[0], Sm, w, 1e-5, **kw)
+        return (H, *g, dX, dw, q.mx8_dequantize(*q.mx8_quantize(dX, **kw), 70, 128, **kw))
+
+    want = run()
+    st = torch.cuda.Stream()
+
+    class Handle:
+        cuda_stream = st.cuda_stream
+
+    for stream in (st, Handle()):
+        st.wait_stream(torch.cuda.current_stream())
+        got = run(stream=stream)
+        st.synchronize()
+        for a, v in zip(got, want):
+            assert torch.equal(a, v)
+
+
 def test_given_outputs_and_workspace():
     q = qlib()
     M, K, F, r = 40, 128, 100, 8
