@@ -57,8 +57,8 @@ __device__ __forceinline__ void sum8(__amdgpu_buffer_rsrc_t rp, int S, int M, in
 
 // kVec: ldy % 8 == 0 (rows of dY in whole 16-byte pieces, zeros from N to ldy); kVecR: r % 8 == 0; kSum: G
 // as slices.  halves: of W's stacked rows, each with a G (two planes [M][r] where there are two; slices
-// [S][halves][M][r], planes [halves][3][M][..])
-// and an L1 [K][r] of its own.
+// [S][halves][M][r], planes [halves][3][M][..]) and an L1 [K][r] of its own.  terms: matrices [M][ldy] whose sum
+// is dY, one behind the other, all below 2^31 bytes.
 template <bool kVec, bool kVecR, bool kSum>
 __global__ __launch_bounds__(64 * kW) void k_dx_small(const uint16_t* __restrict__ dY, int M, int K, int N,
                                                       const uint8_t* __restrict__ codes,
@@ -66,13 +66,13 @@ __global__ __launch_bounds__(64 * kW) void k_dx_small(const uint16_t* __restrict
                                                       const uint16_t* __restrict__ G, const float* __restrict__ Gp, int S,
                                                       uint16_t* __restrict__ planes, const uint16_t* __restrict__ L1,
                                                       int r, uint16_t* __restrict__ dX, Nf4Params q, drop::Params d,
-                                                      int ldy, int halves) {
+                                                      int ldy, int halves, int terms) {
   __shared__ __attribute__((aligned(16))) uint16_t wt[kW][kN * kPitch];
   __shared__ f32x16 red[kW][2][64];
   const int w = threadIdx.x >> 6, l = threadIdx.x & 63, h = l >> 5, x = l & 31;
   const int p0 = kP * (int)blockIdx.x, m0 = 32 * (int)blockIdx.y, m = m0 + x;
   const int kb = K / 64;
-  const __amdgpu_buffer_rsrc_t ry = rsrc(dY, (uint64_t)M * ldy * 2), rc = rsrc(codes, (uint64_t)N * (K / 2)),
+  const __amdgpu_buffer_rsrc_t ry = rsrc(dY, (uint64_t)terms * M * ldy * 2), rc = rsrc(codes, (uint64_t)N * (K / 2)),
                                r2 = rsrc(c2, (uint64_t)N * kb), r1 = rsrc(c1, 4 * (((uint64_t)N * kb + 255) / 256));
   const SplitConst kc = split_const();
   LDS_AS uint16_t* const tile = (LDS_AS uint16_t*)wt[w];
@@ -84,8 +84,12 @@ __global__ __launch_bounds__(64 * kW) void k_dx_small(const uint16_t* __restrict
     float s1;
     bf16x8 y[2];
   };
+  // the second term's steps follow the first's, from a whole round of the waves on
+  const int next = (N + kN * kW - 1) / (kN * kW) * (kN * kW), end = terms == 1 ? N : next + N;
   auto load = [&](int n0) {
     Step s;
+    const uint32_t row0 = terms > 1 && n0 >= next ? (uint32_t)M : 0u;
+    n0 -= row0 ? next : 0;
     const int n = n0 + x;
     const uint32_t b = (uint32_t)n * kb + blockIdx.x;
     s.c = __builtin_amdgcn_raw_buffer_load_b128(rc, n < N ? (uint32_t)n * (K / 2) + 32 * blockIdx.x + 16 * h : kOOB, 0, 0);
@@ -94,13 +98,13 @@ __global__ __launch_bounds__(64 * kW) void k_dx_small(const uint16_t* __restrict
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int k = n0 + 16 * u + 8 * h;
-      s.y[u] = load8<kVec>(ry, (uint32_t)(m * ldy + k) * 2u, m < M ? N - k : 0);
+      s.y[u] = load8<kVec>(ry, (uint32_t)((row0 + m) * ldy + k) * 2u, m < M ? N - k : 0);
     }
     return s;
   };
   f32x16 acc[2] = {};
   Step cur = load(kN * w);
-  for (int n0 = kN * w; n0 < N; n0 += kN * kW) {
+  for (int n0 = kN * w; n0 < end; n0 += kN * kW) {
     const Step nxt = load(n0 + kN * kW);
     const BlockLut lut = make_lut(qk::e4m3fn_to_f32(cur.s2) * cur.s1, q);
 #pragma unroll
@@ -513,12 +517,12 @@ bool dx_small_ok(int64_t M, int64_t K) {
 hipError_t launch_dx_small(const uint16_t* dY, int64_t M, int64_t K, int64_t N, const uint8_t* codes, const uint8_t* c2,
                            const float* c1, const uint16_t* G, const float* Gp, int S, uint16_t* planes,
                            const uint16_t* L1, int r, uint16_t* dX, const drop::Params& d, hipStream_t s, int64_t ldy,
-                           int halves) {
+                           int halves, int terms) {
   if (!ldy) ldy = N;
   const dim3 grid((unsigned)(K / kP), (unsigned)((M + 31) / 32));
 #define QL_DX(V, R, A)                                                                                                \
   hipLaunchKernelGGL((k_dx_small<V, R, A>), grid, dim3(64 * kW), 0, s, dY, (int)M, (int)K, (int)N, codes, c2, c1, \
-                     G, Gp, S, planes, L1, r, dX, nf4_params(), d, (int)ldy, halves)
+                     G, Gp, S, planes, L1, r, dX, nf4_params(), d, (int)ldy, halves, terms)
 #define QL_DXS(A)                          \
   do {                                     \
     if (v && vr) QL_DX(true, true, A);     \

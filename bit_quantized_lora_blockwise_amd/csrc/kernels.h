@@ -251,13 +251,14 @@ hipError_t launch_fwd_small(const uint16_t* X, int64_t M, int64_t K, int64_t N, 
                             const uint16_t* L2, int r, float scale, uint16_t* Y, hipStream_t s);
 // dX = bf16(dY W' + D o (G L1^T)) from G, or with G = nullptr from its slices Gp (S of them), added
 // here; `planes` then receives it to 24 bits.  ldy, halves: rows of dY ldy elements apart, zeros behind N
-// (0: dense); W's rows in that many halves with a G (slices [S][halves][M][r]) and an L1 each.
+// (0: dense); W's rows in that many halves with a G (slices [S][halves][M][r]) and an L1 each.  terms: matrices
+// [M][ldy], one behind the other, whose sum is dY.
 constexpr int kSmallSlices = 8;   // of T and G that the products for few rows add up
 bool dx_small_ok(int64_t M, int64_t K);
 hipError_t launch_dx_small(const uint16_t* dY, int64_t M, int64_t K, int64_t N, const uint8_t* codes, const uint8_t* c2,
                            const float* c1, const uint16_t* G, const float* Gp, int S, uint16_t* planes,
                            const uint16_t* L1, int r, uint16_t* dX, const drop::Params& d, hipStream_t s, int64_t ldy = 0,
-                           int halves = 1);
+                           int halves = 1, int terms = 1);
 
 // --- microscaled 8-bit activations (mx8.hip) -------------------------------------
 hipError_t launch_mx8_quant(const void* X, bool bf16, int64_t rows, int64_t cols, int64_t ld, uint8_t* codes,
@@ -314,11 +315,12 @@ struct Low {
 hipError_t launch_low(const Low& q, int halves, int64_t M, int r, hipStream_t s);
 
 // dZ = the gradients of G and U from dH and their 8-bit copies: bf16 [M][glu_ldz(F)], gate columns first,
-// zeros past 2 F; and the fp32 slices of scale dZ L2^T, [*slices][2][M][r].
+// zeros past 2 F (two: and behind it the same of what it rounds off); and the fp32 slices of scale dZ L2^T,
+// [*slices][2][M][r].
 inline int64_t glu_ldz(int64_t F) { return (2 * F + 7) / 8 * 8; }
 size_t glu_back_ws(int64_t M, int64_t F, int r);
 hipError_t launch_glu_back(const uint16_t* dH, int64_t M, int64_t F, const uint8_t* gu_codes, const uint8_t* gu_scales,
-                           const uint16_t* L2, int r, float scale, uint16_t* dZ, float* part, int* slices, hipStream_t s);
+                           const uint16_t* L2, int r, float scale, uint16_t* dZ, float* part, int* slices, bool two, hipStream_t s);
 
 // The adapter's gradients from packed activations (grads8.hip), in one launch and one for the slices' sums:
 //   dL1 [halves][K, r] = X^T G (X packed, G as planes);  dL2 [halves][r, N] = scale T^T dZ, where dZ is dY [M, N]

@@ -11,7 +11,8 @@ Tolerances, elementwise, derived from the rounding points (U = 2^-24, half a ste
   dZ: dU = dH G sig by E |dU|, dG = dH U sig (1 + G (1 - sig)) by E |dH U| sig (1 + |G|) (1 + |G|): the
   factor's two terms may cancel, and 1 - sig carries sig's error times G;
   B and dL1, dL2 carry those and their own sums, three planes lose 2^-24; dX takes dZ in bf16 and B as
-  two bf16 planes: 2^-8 |dZ| |W| and 2^-16 |B| |L1| on top (a linear's dX takes B in bf16).
+  two bf16 planes: 2^-8 |dZ| |W| (2^-16 for few terms, whose planes' products double the sum's terms) and
+  2^-16 |B| |L1| on top (a linear's dX takes B in bf16).
 """
 import numpy as np
 import pytest
@@ -105,7 +106,7 @@ def test_forward(M, K, F, r):
     assert M <= 16 or torch.equal(H, H2)
 
 
-def check_backward(q, b, x8, gu8, T, dX, dL1, dL2):
+def check_backward(q, b, x8, gu8, T, dX, dL1, dL2, dz_bits=2.0**-8):
     M, K, F, r = b.M, b.K, b.F, b.r
     x = X8.values(x8[0].cpu().numpy(), x8[1].cpu().numpy(), K)
     gu = X8.values(gu8[0].cpu().numpy(), gu8[1].cpu().numpy(), F)
@@ -123,7 +124,8 @@ def check_backward(q, b, x8, gu8, T, dX, dL1, dL2):
         within(dL2[h], r2[h], S * (np.abs(t[h]).T @ off[h]) + (3 * M + 40) * U * S * (np.abs(t[h]).T @ np.abs(dz[h])),
                f"dL2[{h}]")
         if dX is not None:
-            tx = tx + ((2.0**-8 + (2 * F + 130) * U) * np.abs(dz[h]) + off[h]) @ w
+            terms = 2 * F if dz_bits == 2.0**-8 else 4 * F
+            tx = tx + ((dz_bits + (terms + 130) * U) * np.abs(dz[h]) + off[h]) @ w
             tx = tx + ((2.0**-16 + (2 * F + 260) * U) * np.abs(B[h]) + ob) @ a1.T
     if dX is not None:
         within(dX, rx, tx, "dX")
@@ -153,6 +155,17 @@ def test_backward(M, K, F, r):
     check_backward(q, b, x8, gu8, T, dX, dL1, dL2)
     none, a1, a2 = q.qlora_swiglu_bwd(x8, b.d, *b.base, b.L1, b.L2, gu8, T, S, dX=False)
     assert none is None and torch.equal(a1, dL1) and torch.equal(a2, dL2)
+
+
+@pytest.mark.parametrize("M,K,F,r", [(1, 64, 1, 1), (1, 320, 16, 54), (2, 192, 16, 1), (5, 512, 48, 37), (1, 128, 1024, 8),
+                                     (40, 64, 25, 64), (300, 704, 3, 9)])
+def test_backward_of_few_terms(M, K, F, r):
+    """dX of up to 1024 values of dH takes dZ as two bf16 planes: 2^-16 of it in place of 2^-8."""
+    q = qlib()
+    b = Block(M * 1021 + K + F, M, K, F, r)
+    x8 = q.mx8_quantize(b.X)
+    _, T, gu8 = q.qlora_swiglu_fwd(b.X, *b.base, F, b.L1, b.L2, S, T_out=True, mx8=True)
+    check_backward(q, b, x8, gu8, T, *q.qlora_swiglu_bwd(x8, b.d, *b.base, b.L1, b.L2, gu8, T, S), dz_bits=2.0**-16)
 
 
 @pytest.mark.parametrize("level", [40.0, 100.0, 400.0])
