@@ -161,15 +161,18 @@ __device__ __forceinline__ bf16x8 frag_kmajor_sw(const LDS_AS uint16_t* base, in
 // planes for each half, 24 bits of it: G and U are rounded to 8 bits, and a T of 8 bits
 // would put one in 300 of their codes on the other side of a border, one of 16 bits one in
 // 20000, six times as many as the sums themselves.  The planes go straight to LDS in the
-// activation tile's layout.  8192 -> 2 x 22016, 2048 rows with the 8-bit copies: 1422 us, 1039 TFLOP/s, 0.77 of a large
-// library product's rate (the same weight as a plain stacked product: 1313 to 1383 us); bound as that one.
+// activation tile's layout.  8192 -> 2 x 22016, 2048 rows with the 8-bit copies: 1422 us, 1039
+// TFLOP/s, 0.77 of a large library product's rate (the same weight as a plain stacked product:
+// 1313 to 1383 us); bound as that one.
 // kDrop (dX): the adapter term is D o (G L1^T).  All waves draw the tile's decisions
 // into LDS (a bit an element) while the LoRA operands arrive (by the producers alone,
 // one wave a SIMD, the draws took 12 us a tile), and the consumers apply them to the
 // accumulators before the base product.
 // kSplit (dX): the reduction is cut into slices, a work item is a tile of one of them, and what
 // it sums goes to `part` in fp32, for k_dx_join to add up in order: in whole accumulators, 1 KB a
-// store (row-major, 4 bytes a lane, the stores alone took as long as ten steps).  The first slice has the adapter's term.
+// store (row-major, 4 bytes a lane, the stores alone took as long as ten steps).  The first slice
+// has the adapter's term.  Reduction 22016, 4096 columns: 1024 rows 163 us in four slices and 13 for
+// the join (one slice: 418); 64 rows 43 and 9, of which a slice's 22 steps are latency, not rate.
 struct BigOut {
   uint8_t* codes;     // kGlu: G and U in 8 bits, one packed matrix of 2 M rows (mx8.h), or null
   uint8_t* scales;
@@ -278,7 +281,8 @@ __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict_
       const int row = 64 * pw + 8 * j + (l >> 3);
       arow_off[j] = (uint32_t)((int64_t)row * lda * 2) + 16u * achunk[j & 1];
     }
-    // Step st of a matrix with `rows` rows (lda apart; what lies between R and lda is zeros) from row r0 goes through a descriptor
+    // Step st of a matrix with `rows` rows (lda apart; what lies between R and lda is zeros) from row
+    // r0 goes through a descriptor
     // based at column 64 st of row r0 whose size ends at the end of the matrix:
     // rows past the end read as zeros, and a step past the reduction has size 0.
     // The loads are issued from inline assembly, which writes no register: the
