@@ -284,9 +284,38 @@ def test_block_step_on_another_stream_and_captured():
             assert torch.equal(a, v), k
 
 
-@pytest.mark.parametrize("M,K,F", [(1000, 16640, 24), (40, 128, 100)])
+def test_calls_at_once_on_two_streams():
+    """Two blocks in flight on streams of their own, sizes of every kind of dX, against one after the other."""
+    q = qlib()
+    sizes = [(96, 128, 192, 8), (40, 128, 6200, 8), (1000, 16640, 24, 8), (3, 4096, 65, 64)]
+    work = []
+    for n, (M, K, F, r) in enumerate(sizes):
+        b = Block(41 + n, M, K, F, r)
+        x8 = q.mx8_quantize(b.X)
+
+        def run(b=b, x8=x8, F=F):
+            H, T, gu8 = q.qlora_swiglu_fwd(b.X, *b.base, F, b.L1, b.L2, S, T_out=True, mx8=True)
+            return (H, T, *gu8, *q.qlora_swiglu_bwd(x8, b.d, *b.base, b.L1, b.L2, gu8, T, S))
+
+        work.append((run, run()))
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    for st in streams:
+        st.wait_stream(torch.cuda.current_stream())
+    for n in range(len(work)):
+        got = []
+        for k, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                f, want = work[(n + k) % len(work)]
+                got.append((f(), f(), want))
+        torch.cuda.synchronize()
+        for first, second, want in got:
+            for u, v, x in zip(first, second, want):
+                assert torch.equal(u, x) and torch.equal(v, x), n
+
+
+@pytest.mark.parametrize("M,K,F", [(1000, 16640, 24), (40, 128, 100), (40, 128, 6200)])
 def test_backward_captured(M, K, F):
-    """Captured with the gradients beside dX and without, then replayed between eager calls."""
+    """Captured with the gradients beside dX, without and with dX in slices, then replayed between eager calls."""
     q = qlib()
     r = 8
     b, c = Block(31, M, K, F, r), Block(32, M, K, F, r, halves=1)
@@ -341,9 +370,9 @@ def test_stream_given_by_argument_or_handle():
             assert torch.equal(a, v)
 
 
-def test_given_outputs_and_workspace():
+@pytest.mark.parametrize("M,K,F,r", [(40, 128, 100, 8), (3, 64, 20, 5), (40, 128, 6200, 8), (1300, 128, 1100, 12), (600, 64, 72, 64)])
+def test_given_outputs_and_workspace(M, K, F, r):
     q = qlib()
-    M, K, F, r = 40, 128, 100, 8
     b = Block(21, M, K, F, r)
     H, T, gu8 = q.qlora_swiglu_fwd(b.X, *b.base, F, b.L1, b.L2, S, T_out=True, mx8=True)
     L = q.lib()
