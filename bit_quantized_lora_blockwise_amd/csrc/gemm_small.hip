@@ -311,8 +311,10 @@ __global__ __launch_bounds__(64 * kW) void k_fwd_small(const uint16_t* __restric
 // waves form the adapter's term of one half of 32 rows each meanwhile, add the eight waves'
 // sums in order and finish.  T enters as three bf16 planes (24 bits: G and U may be
 // kept in 8): given [2 halves][3][M][pitch], or kSum: formed here from its slices [2][S][M][r].
-// 17 rows 4096 -> 2 x 11008: 48 us, 47 MB; bound: the loads' way back.  A lane's row is its own, so
-// an instruction's 64 lanes read 64 lines whatever their width, 60 clocks each (TD busy 28 us, vector units 14).
+// 17 rows 4096 -> 2 x 11008: 46 us, 47 MB at 1 TB/s; vector units busy for 14, the data return for 28
+// (a lane's row is its own, so an instruction's 64 lanes read 64 lines), about 10 a launch's first
+// loads and end.  Two blocks a step (a fifth fewer loads, half the tables) took 45 us, and 8192 -> 2
+// x 22016 153 for 145; a wave's blocks side by side 47; two steps' registers in turn 48.
 template <int kI, bool kSum>
 __global__ __launch_bounds__(64 * (kW + 2 * kI)) void k_glu_small(const uint16_t* __restrict__ X, int M, int K, int F,
                                                        const uint8_t* __restrict__ codes,
