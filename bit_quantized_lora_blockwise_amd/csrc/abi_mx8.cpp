@@ -29,7 +29,7 @@ bool layer_ok(int64_t M, int64_t K, int64_t n, int64_t ldy, int r, int halves = 
 }
 
 bool glu_ok(int64_t M, int64_t K, int64_t F, int r) {
-  return F > 0 && F < kLim / 2 && layer_ok(M, K, 2 * F, glu_ldz(F), r, 2);
+  return F > 0 && F < kLim / 2 && layer_ok(M, K, 2 * F, (2 * F + 7) / 8 * 8, r, 2);
 }
 
 // Whether T goes into the product as slices, which it adds up itself (a launch less): where the
@@ -64,10 +64,8 @@ bool split_ok(int64_t M, int64_t K, int64_t n) {
   return n * std::max<int64_t>(groups, 256) >= 6144 * 256 && qgemm_dx_slices(M, K, n) > 1;
 }
 
-// Whether dX takes dZ as two bf16 planes, 16 bits.  One rounding of dZ adds to dX about what dX's own does, 1.4 of its
-// error together, while many terms average it; of a few hundred, which a few large ones outweigh, the sum may be off by
-// twice as much.  At these sizes the second product hides in the launch.
-bool two_dz(int64_t M, int64_t K, int64_t F) { return M < 512 && M * F <= 1024 && !split_ok(M, K, 2 * F) && dx_small_ok(M, K); }
+// Length of the reduction that dX of the gated product walks: with two planes, both.
+int64_t glu_terms(int64_t F) { return glu_two(F) ? glu_ldz(F) : 2 * F; }
 
 // Whether a linear's G goes to dX for few rows as slices, which it adds up itself (a launch less).
 // Whole backwards, us, apart / so: 4096 -> 4096 1 row 34 / 30, 96 rows (24 tiles) 42 / 39, 160 rows
@@ -76,17 +74,18 @@ bool few_dx_ok(int64_t M, int64_t K, int64_t N, int r) {
   return (M + 15) / 16 * ((r + 15) / 16) <= 64 && dx_small_ok(M, K) && !(N % 8 == 0 && split_ok(M, K, N));
 }
 
-// Backward: [dZ (gated; up to two planes)][G (gated: two planes of it)][its three planes][fp32 partials, of G and then of the gradients].
+// Backward: [dZ (gated)][G (gated: two planes of it)][its three planes][fp32 partials, of G and then of the gradients].
 struct BwdWs {
   size_t dz, g, planes, part, total;
 };
 BwdWs bwd_ws(int64_t M, int64_t K, int64_t N, int halves, int r) {
-  BwdWs w{halves == 2 ? round_up((size_t)M * glu_ldz(N) * (two_dz(M, K, N) ? 4 : 2)) : 0, round_up((size_t)halves * halves * M * r * 2),
+  BwdWs w{halves == 2 ? round_up((size_t)M * glu_ldz(N) * 2) : 0, round_up((size_t)halves * halves * M * r * 2),
           round_up((size_t)3 * halves * M * g_pitch(r) * 2), 0, 0};
   size_t slices = halves == 2 ? glu_back_ws(M, N, r) : lora_skinny_ws(M, N, r);
   if (halves == 1 && few_dx_ok(M, K, N, r)) slices = std::max(slices, mx4_small_ws(M, r));
   w.part = std::max(slices, grads8_ws(M, K, N, halves, r));
-  if ((halves == 2 || N % 8 == 0) && split_ok(M, K, halves * N)) w.part = std::max(w.part, qgemm_dx_split_ws(M, K, halves * N));
+  const int64_t terms = halves == 2 ? glu_terms(N) : N;
+  if ((halves == 2 || N % 8 == 0) && split_ok(M, K, terms)) w.part = std::max(w.part, qgemm_dx_split_ws(M, K, terms));
   w.part = round_up(w.part);
   w.total = w.dz + w.g + w.planes + w.part;
   return w;
@@ -240,9 +239,9 @@ int qlora_swiglu_bwd(const uint8_t* x_codes, const uint8_t* x_scales, const uint
   uint16_t* planes = (uint16_t*)(ws + w.dz + w.g);
   float* part = (float*)(ws + w.dz + w.g + w.planes);
   int slices = 0;
-  const bool two = dX && two_dz(M, K, F);
-  QL_TRY(launch_glu_back(dH, M, F, gu_codes, gu_scales, L2, r, lora_scale, dZ, part, &slices, two, s));
-  const bool split = split_ok(M, K, 2 * F), small = !split && dx_small_ok(M, K), sums = dX && small && slices <= kSmallSlices;
+  const bool two = glu_two(F);
+  QL_TRY(launch_glu_back(dH, M, F, gu_codes, gu_scales, L2, r, lora_scale, dZ, part, &slices, s));
+  const bool split = split_ok(M, K, glu_terms(F)), small = !split && dx_small_ok(M, K), sums = dX && small && slices <= kSmallSlices;
   if (!sums) QL_TRY(launch_low(Low{part, slices, 1.0f, G, planes, true}, 2, M, r, s));
   auto product = [&] {
     if (!dX) return hipSuccess;
@@ -251,8 +250,8 @@ int qlora_swiglu_bwd(const uint8_t* x_codes, const uint8_t* x_scales, const uint
       return launch_dx_small(dZ, M, K, 2 * F, codes, c2, c1, sums ? nullptr : G, part, slices, planes, L1, r, dX, kNoDrop, s,
                              glu_ldz(F), 2, two ? 2 : 1);
     if (split)
-      return launch_qgemm_dx_split(dZ, M, K, 2 * F, codes, c2, c1, G, L1, r, dX, part, s, 2, glu_ldz(F), true);
-    return launch_qgemm_big(true, dZ, M, K, 2 * F, codes, c2, c1, G, L1, r, 1.0f, dX, s, 2, nullptr, glu_ldz(F), true);
+      return launch_qgemm_dx_split(dZ, M, K, 2 * F, codes, c2, c1, G, L1, r, dX, part, s, 2, glu_ldz(F), true, two);
+    return launch_qgemm_big(true, dZ, M, K, 2 * F, codes, c2, c1, G, L1, r, 1.0f, dX, s, 2, nullptr, glu_ldz(F), true, two);
   };
   auto grads = [&](hipStream_t st) {
     return launch_grads8(Grads8{x_codes, x_scales, dH, gu_codes, gu_scales, planes, T, lora_scale, dL1, dL2}, M, K, F, 2, r,

@@ -173,6 +173,8 @@ __device__ __forceinline__ bf16x8 frag_kmajor_sw(const LDS_AS uint16_t* base, in
 // store (row-major, 4 bytes a lane, the stores alone took as long as ten steps).  The first slice
 // has the adapter's term.  Reduction 22016, 4096 columns: 1024 rows 163 us in four slices and 13 for
 // the join (one slice: 418); 64 rows 43 and 9, of which a slice's 22 steps are latency, not rate.
+// kTwo (dX, of glu_two): A's rows hold two planes, lda / 2 columns each, whose sum is dZ; the reduction walks W under
+// both.  Whole gated backwards, 4096 columns, F = 1024, us, one plane / two: 1024 rows 77 / 91, 4096 rows 129 / 184.
 struct BigOut {
   uint8_t* codes;     // kGlu: G and U in 8 bits, one packed matrix of 2 M rows (mx8.h), or null
   uint8_t* scales;
@@ -183,7 +185,7 @@ struct BigOut {
 };
 
 template <bool kDx, bool kTail, bool kB16 = false, bool kDrop = false, int kCols = 0,
-          bool kSplit = false>
+          bool kSplit = false, bool kTwo = false>
 __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict__ A, int64_t M, int64_t K,
                                                      int64_t N, const uint8_t* __restrict__ codes,
                                                      const uint8_t* __restrict__ c2,
@@ -197,6 +199,7 @@ __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict_
   constexpr bool kGlu = kCols != 0, kHalf = kCols == kBPG / 2;
   static_assert(!kGlu || kHalf || kCols == kBPG, "columns of a tile of the gated product");
   static_assert(!kSplit || (kDx && !kB16 && !kDrop), "a split reduction is of dX over the packed weight");
+  static_assert(!kTwo || (kDx && !kTail && !kB16 && !kDrop), "two planes are those of the gated product's dZ");
   static_assert(!kGlu || !(kDx || kTail || kB16 || kDrop), "the gated product is a forward over the packed weight");
   __shared__ __attribute__((aligned(16))) uint16_t lds_b[2 * kBufElems];   // weight tiles; LoRA operands first
   __shared__ __attribute__((aligned(16))) uint16_t lds_a0[kBM * kBR];      // activation tiles (two buffers,
@@ -208,7 +211,7 @@ __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict_
   const int rg = w & 3, ch = (w >> 2) & 1;  // consumers: row group (64 rows), column half (128 columns)
   const int64_t P = kDx ? K : kGlu ? N / 2 : N;   // output columns
   constexpr int kTileP = kGlu ? kBPG : kBP;       // of a tile
-  const int64_t R = kDx ? N : K;          // reduction length
+  const int64_t R = kTwo ? lda : kDx ? N : K;     // reduction length
   const int64_t kblocks = K / qk::kBlock;
   constexpr bool kPerm = kDx && !kB16;    // dX columns in the lookup order (0, 2, 4, 6, 1, 3, 5, 7)
 
@@ -292,7 +295,8 @@ __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict_
     auto dma_tile = [&](const uint16_t* src, int64_t rows, int64_t r0, int64_t st, LDS_AS uint16_t* buf) {
       const int64_t left = R - st * kBR;
       const int rem = __builtin_amdgcn_readfirstlane((int)(left < kBR ? left : kBR));   // columns in this step
-      const uint64_t nrec = rem > 0 ? (uint64_t)(rows - r0) * lda * 2 - (uint64_t)st * kBR * 2 : 0;
+      // (two planes of all rows may pass 2^32 bytes, of a tile's not)
+      const uint64_t nrec = rem > 0 ? (uint64_t)(kTwo ? min(rows - r0, (int64_t)kBM) : rows - r0) * lda * 2 - (uint64_t)st * kBR * 2 : 0;
       const uint64_t base = (uint64_t)(uintptr_t)(src + r0 * lda + (rem > 0 ? st * kBR : 0));
       const uint16_t* pa = (const uint16_t*)(((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(base >> 32)) << 32) |
                                              (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)base));
@@ -334,7 +338,11 @@ __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict_
           wrow = c < P ? ((row / kQ) % 2 ? P : 0) + c : N;
           kb = step;
         } else if (!kDx) { wrow = p0 + tp; kb = step; }
-        else { wrow = step * kBR + (tp >> 2); kb = p0 / 64 + (tp & 3); }
+        else {
+          if (kTwo && step >= nsteps / 2) step -= nsteps / 2;    // the second plane's
+          wrow = step * kBR + (tp >> 2);
+          kb = p0 / 64 + (tp & 3);
+        }
         // out-of-range blocks get bit 31 set in their offsets: past every buffer end
         const uint32_t oob = (wrow < N && kb < kblocks) ? 0u : kOOB;
         const uint32_t b = (uint32_t)(wrow * kblocks + kb);
@@ -854,7 +862,7 @@ static dim3 tile_grid(int64_t M, int64_t P) {
 hipError_t launch_qgemm_big(bool dx, const uint16_t* A, int64_t M, int64_t K, int64_t N, const uint8_t* codes,
                             const uint8_t* c2, const float* c1, const uint16_t* LA, const uint16_t* LB, int r,
                             float scale, uint16_t* C, hipStream_t s, int nseg, const drop::Params* d, int64_t ld,
-                            bool two) {
+                            bool two, bool sum) {
   const int64_t P = dx ? K : N;
   const int64_t lda = ld ? ld : dx ? N : K;
   const int64_t seg = N / nseg;   // columns of W per segment (a multiple of 256 when nseg > 1)
@@ -871,7 +879,10 @@ hipError_t launch_qgemm_big(bool dx, const uint16_t* A, int64_t M, int64_t K, in
     else
       hipLaunchKernelGGL((k_qgemm_big<true, true, false, true>), grid, dim3(kT), 0, s, A, M, K, N, codes, c2, c1, LA,
                          LB, r, scale, C, nf4_params(), nseg, seg, nw, *d, lda, BigOut{});
-  } else if (N % kBR == 0)
+  } else if (sum)
+    hipLaunchKernelGGL((k_qgemm_big<true, false, false, false, 0, false, true>), grid, dim3(kT), 0, s, A, M, K, N, codes, c2,
+                       c1, LA, LB, r, scale, C, nf4_params(), nseg << two, seg, nw, drop::Params{}, lda, planes);
+  else if (N % kBR == 0)
     hipLaunchKernelGGL((k_qgemm_big<true, false>), grid, dim3(kT), 0, s, A, M, K, N, codes, c2, c1, LA, LB, r,
                        scale, C, nf4_params(), nseg << two, seg, nw, drop::Params{}, lda, planes);
   else
@@ -880,31 +891,33 @@ hipError_t launch_qgemm_big(bool dx, const uint16_t* A, int64_t M, int64_t K, in
   return hipGetLastError();
 }
 
-int qgemm_dx_slices(int64_t M, int64_t K, int64_t N) {
-  const int64_t tiles = (M + kBM - 1) / kBM * ((K + kBP - 1) / kBP), steps = (N + kBR - 1) / kBR;
+int qgemm_dx_slices(int64_t M, int64_t K, int64_t R) {
+  const int64_t tiles = (M + kBM - 1) / kBM * ((K + kBP - 1) / kBP), steps = (R + kBR - 1) / kBR;
   const int64_t most = std::min(cu_grid() / tiles, steps / 8);
   if (most < 2) return 1;
   const int64_t per = (steps + 2 * most - 1) / (2 * most) * 2;
   return (int)((steps + per - 1) / per);
 }
 
-size_t qgemm_dx_split_ws(int64_t M, int64_t K, int64_t N) {
-  return (size_t)qgemm_dx_slices(M, K, N) * ((M + kBM - 1) / kBM) * ((K + kBP - 1) / kBP) * kTileVecs * sizeof(f32x4);
+size_t qgemm_dx_split_ws(int64_t M, int64_t K, int64_t R) {
+  return (size_t)qgemm_dx_slices(M, K, R) * ((M + kBM - 1) / kBM) * ((K + kBP - 1) / kBP) * kTileVecs * sizeof(f32x4);
 }
 
 hipError_t launch_qgemm_dx_split(const uint16_t* A, int64_t M, int64_t K, int64_t N, const uint8_t* codes,
                                  const uint8_t* c2, const float* c1, const uint16_t* LA, const uint16_t* LB, int r,
-                                 uint16_t* C, float* part, hipStream_t s, int nseg, int64_t ld, bool two) {
-  const int slices = qgemm_dx_slices(M, K, N);
-  const int64_t steps = (N + kBR - 1) / kBR, tiles = (M + kBM - 1) / kBM * ((K + kBP - 1) / kBP);
+                                 uint16_t* C, float* part, hipStream_t s, int nseg, int64_t ld, bool two, bool sum) {
+  const int64_t R = sum ? ld : N;
+  const int slices = qgemm_dx_slices(M, K, R);
+  const int64_t steps = (R + kBR - 1) / kBR, tiles = (M + kBM - 1) / kBM * ((K + kBP - 1) / kBP);
   const BigOut out{nullptr, nullptr, 0, part, slices, (int)((steps + 2 * slices - 1) / (2 * slices) * 2), two};
   const uint16_t* nw = nullptr;
   const dim3 grid((unsigned)(tiles * slices));
-#define QL_SPLIT(T)                                                                                                   \
-  hipLaunchKernelGGL((k_qgemm_big<true, T, false, false, 0, true>), grid, dim3(kT), 0, s, A, M, K, N, codes, c2, c1, LA, LB, r, \
+#define QL_SPLIT(T, S)                                                                                                   \
+  hipLaunchKernelGGL((k_qgemm_big<true, T, false, false, 0, true, S>), grid, dim3(kT), 0, s, A, M, K, N, codes, c2, c1, LA, LB, r, \
                      1.0f, C, nf4_params(), nseg << two, N / nseg, nw, drop::Params{}, ld ? ld : N, out)
-  if (N % kBR == 0) QL_SPLIT(false);
-  else QL_SPLIT(true);
+  if (sum) QL_SPLIT(false, true);
+  else if (N % kBR == 0) QL_SPLIT(false, false);
+  else QL_SPLIT(true, false);
 #undef QL_SPLIT
   hipLaunchKernelGGL(k_dx_join, dim3((unsigned)(16 * tiles)), dim3(512), 0, s, part, slices, M, K, C);
   return hipGetLastError();

@@ -57,8 +57,8 @@ __device__ __forceinline__ void sum8(__amdgpu_buffer_rsrc_t rp, int S, int M, in
 
 // kVec: ldy % 8 == 0 (rows of dY in whole 16-byte pieces, zeros from N to ldy); kVecR: r % 8 == 0; kSum: G
 // as slices.  halves: of W's stacked rows, each with a G (two planes [M][r] where there are two; slices
-// [S][halves][M][r], planes [halves][3][M][..]) and an L1 [K][r] of its own.  terms: matrices [M][ldy] whose sum
-// is dY, one behind the other, all below 2^31 bytes.
+// [S][halves][M][r], planes [halves][3][M][..]) and an L1 [K][r] of its own.  terms: matrices of ldy / terms columns
+// whose sum is dY, side by side.
 template <bool kVec, bool kVecR, bool kSum>
 __global__ __launch_bounds__(64 * kW) void k_dx_small(const uint16_t* __restrict__ dY, int M, int K, int N,
                                                       const uint8_t* __restrict__ codes,
@@ -72,7 +72,7 @@ __global__ __launch_bounds__(64 * kW) void k_dx_small(const uint16_t* __restrict
   const int w = threadIdx.x >> 6, l = threadIdx.x & 63, h = l >> 5, x = l & 31;
   const int p0 = kP * (int)blockIdx.x, m0 = 32 * (int)blockIdx.y, m = m0 + x;
   const int kb = K / 64;
-  const __amdgpu_buffer_rsrc_t ry = rsrc(dY, (uint64_t)terms * M * ldy * 2), rc = rsrc(codes, (uint64_t)N * (K / 2)),
+  const __amdgpu_buffer_rsrc_t ry = rsrc(dY, (uint64_t)M * ldy * 2), rc = rsrc(codes, (uint64_t)N * (K / 2)),
                                r2 = rsrc(c2, (uint64_t)N * kb), r1 = rsrc(c1, 4 * (((uint64_t)N * kb + 255) / 256));
   const SplitConst kc = split_const();
   LDS_AS uint16_t* const tile = (LDS_AS uint16_t*)wt[w];
@@ -88,8 +88,8 @@ __global__ __launch_bounds__(64 * kW) void k_dx_small(const uint16_t* __restrict
   const int next = (N + kN * kW - 1) / (kN * kW) * (kN * kW), end = terms == 1 ? N : next + N;
   auto load = [&](int n0) {
     Step s;
-    const uint32_t row0 = terms > 1 && n0 >= next ? (uint32_t)M : 0u;
-    n0 -= row0 ? next : 0;
+    const int col0 = terms > 1 && n0 >= next ? ldy / 2 : 0;
+    n0 -= col0 ? next : 0;
     const int n = n0 + x;
     const uint32_t b = (uint32_t)n * kb + blockIdx.x;
     s.c = __builtin_amdgcn_raw_buffer_load_b128(rc, n < N ? (uint32_t)n * (K / 2) + 32 * blockIdx.x + 16 * h : kOOB, 0, 0);
@@ -98,7 +98,7 @@ __global__ __launch_bounds__(64 * kW) void k_dx_small(const uint16_t* __restrict
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int k = n0 + 16 * u + 8 * h;
-      s.y[u] = load8<kVec>(ry, (uint32_t)((row0 + m) * ldy + k) * 2u, m < M ? N - k : 0);
+      s.y[u] = load8<kVec>(ry, (uint32_t)(m * ldy + col0 + k) * 2u, m < M ? N - k : 0);
     }
     return s;
   };

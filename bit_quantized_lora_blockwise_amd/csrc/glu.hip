@@ -118,13 +118,13 @@ __global__ __launch_bounds__(kT) void k_low(Low q, int halves, int64_t M, int r,
 constexpr int kBT = 512;
 constexpr int kBElems = 4096;              // of a step: 32 rows x 128 columns or 64 x 64
 
-// kVec: F % 8 == 0.  two (32 rows): dZ's second plane behind the first.
+// kVec: F % 8 == 0.  plane: columns of a plane of dZ, of which a row holds ldz / plane.
 template <int kBM, bool kVec>
 __global__ __launch_bounds__(kBT, 4) void k_glu_back(const uint16_t* __restrict__ dH, int M, int F,
                                                      const uint8_t* __restrict__ codes,
                                                      const uint8_t* __restrict__ scales,
                                                      const uint16_t* __restrict__ L2, int r, float scale, int chunk, int ldz,
-                                                     int two, uint16_t* __restrict__ dZ, float* __restrict__ part) {
+                                                     int plane, uint16_t* __restrict__ dZ, float* __restrict__ part) {
   constexpr int kBC = kBElems / kBM;       // columns of a step
   constexpr int kBPitch = kBC + 8;         // LDS row (elements): 16 rows' pieces of 16 bytes on different banks
   constexpr int kRows = kBM / 32;          // row tiles of 32
@@ -193,8 +193,7 @@ __global__ __launch_bounds__(kBT, 4) void k_glu_back(const uint16_t* __restrict_
       for (int n = 0; n < 3; ++n) {
         const u32x4 a = glu::take_plane(dz[h]);
         *(LDS_AS u32x4*)((LDS_AS uint16_t*)lds + ((3 * h + n) * kBM + row) * kBPitch + col) = a;
-        if ((n == 0 || (kBM == 32 && n == 1 && two)) && m < M && f < F)
-          qk::store8_row(dZ + ((int64_t)n * M + m) * ldz + h * F + f, a, min(8, F - f));
+        if (n * plane < ldz && m < M && f < F) qk::store8_row(dZ + (int64_t)m * ldz + n * plane + h * F + f, a, min(8, F - f));
       }
     if constexpr (kBM == 64)
 #pragma unroll
@@ -217,9 +216,9 @@ __global__ __launch_bounds__(kBT, 4) void k_glu_back(const uint16_t* __restrict_
                               l2, acc[q]);
     }
   }
-  if (f_end == F && m < M && col == 0)
-    for (int n = 0; n <= (kBM == 32 ? two : 0); ++n)
-      for (int f = 2 * F; f < ldz; ++f) dZ[((int64_t)n * M + m) * ldz + f] = 0;
+  if (f_end == F && m < M)                 // up to 63 columns of a plane past 2 F
+    for (int n = 0; n < ldz; n += plane)
+      for (int f = 2 * F + col / 8; f < plane; f += kBC / 8) dZ[(int64_t)m * ldz + n + f] = 0;
   // the two halves of the steps' columns
   __syncthreads();
   LDS_AS float* red = (LDS_AS float*)lds + (w >> 1) * (kRows * 1024) + l;
@@ -284,13 +283,13 @@ hipError_t launch_low(const Low& q, int halves, int64_t M, int r, hipStream_t s)
 size_t glu_back_ws(int64_t M, int64_t F, int r) { return (size_t)plan_back(M, F).slices * 2 * M * r * sizeof(float); }
 
 hipError_t launch_glu_back(const uint16_t* dH, int64_t M, int64_t F, const uint8_t* gu_codes, const uint8_t* gu_scales,
-                           const uint16_t* L2, int r, float scale, uint16_t* dZ, float* part, int* slices, bool two, hipStream_t s) {
+                           const uint16_t* L2, int r, float scale, uint16_t* dZ, float* part, int* slices, hipStream_t s) {
   const PlanBack p = plan_back(M, F);
   *slices = p.slices;
   const dim3 grid((unsigned)p.tiles, (unsigned)p.slices);
 #define QL_BACK(R, V)                                                                                                      \
   hipLaunchKernelGGL((k_glu_back<R, V>), grid, dim3(kBT), 0, s, dH, (int)M, (int)F, gu_codes, gu_scales, L2, r, scale,  \
-                     (int)p.chunk, (int)glu_ldz(F), (int)two, dZ, part)
+                     (int)p.chunk, (int)glu_ldz(F), (int)glu_plane(F), dZ, part)
   if (p.rows == 64) {
     if (F % 8 == 0) QL_BACK(64, true);
     else QL_BACK(64, false);

@@ -219,20 +219,22 @@ hipError_t launch_qgemv_fwd_fused(const uint16_t* X, int64_t M, int64_t K, int64
 // [r, N / nseg] (fwd) or L1 [K, r] (dX) blocks.  d (dX, nseg = 1): dropout of the
 // adapter term, dX = bf16(dY W' + D o (G L1^T)).  lda: elements from one row of A to the
 // next, a multiple of 8, zeros past the row (0: dense).  two (dX): LA holds two planes [M, r] of each segment's G,
-// what bf16 takes of it and of the rest.
+// what bf16 takes of it and of the rest.  sum (dX): rows of A hold two matrices of lda / 2 columns, a multiple
+// of 64 with zeros past N, whose sum it is.
 bool qgemm_big_ok(bool dx, int64_t M, int64_t K, int64_t N);
 hipError_t launch_qgemm_big(bool dx, const uint16_t* A, int64_t M, int64_t K, int64_t N, const uint8_t* codes,
                             const uint8_t* c2, const float* c1, const uint16_t* LA, const uint16_t* LB, int r,
                             float scale, uint16_t* C, hipStream_t s, int nseg = 1,
-                            const drop::Params* d = nullptr, int64_t lda = 0, bool two = false);
-// dX of few tiles: the reduction in slices, whose fp32 sums (part: qgemm_dx_split_ws bytes) a launch of its own
-// adds up in order.  1: not split.
-int qgemm_dx_slices(int64_t M, int64_t K, int64_t N);
-size_t qgemm_dx_split_ws(int64_t M, int64_t K, int64_t N);
+                            const drop::Params* d = nullptr, int64_t lda = 0, bool two = false,
+                            bool sum = false);
+// dX of few tiles: the reduction, of length R (N, or lda with sum), in slices, whose fp32 sums (part:
+// qgemm_dx_split_ws bytes) a launch of its own adds up in order.  1: not split.
+int qgemm_dx_slices(int64_t M, int64_t K, int64_t R);
+size_t qgemm_dx_split_ws(int64_t M, int64_t K, int64_t R);
 hipError_t launch_qgemm_dx_split(const uint16_t* A, int64_t M, int64_t K, int64_t N, const uint8_t* codes,
                                  const uint8_t* c2, const float* c1, const uint16_t* LA, const uint16_t* LB, int r,
                                  uint16_t* C, float* part, hipStream_t s, int nseg = 1, int64_t lda = 0,
-                                 bool two = false);
+                                 bool two = false, bool sum = false);
 // The same two GEMMs with a bf16 weight W [N, K] in place of the packed one
 // (LoRA over a bf16 base): dx = false Y = bf16(X W^T + scale T L2), dx = true
 // dX = bf16(dY W + G L1^T).  bgemm_ok says whether the shapes qualify.
@@ -252,7 +254,7 @@ hipError_t launch_fwd_small(const uint16_t* X, int64_t M, int64_t K, int64_t N, 
 // dX = bf16(dY W' + D o (G L1^T)) from G, or with G = nullptr from its slices Gp (S of them), added
 // here; `planes` then receives it to 24 bits.  ldy, halves: rows of dY ldy elements apart, zeros behind N
 // (0: dense); W's rows in that many halves with a G (slices [S][halves][M][r]) and an L1 each.  terms: matrices
-// [M][ldy], one behind the other, whose sum is dY.
+// of ldy / terms columns, side by side, whose sum is dY.
 constexpr int kSmallSlices = 8;   // of T and G that the products for few rows add up
 bool dx_small_ok(int64_t M, int64_t K);
 hipError_t launch_dx_small(const uint16_t* dY, int64_t M, int64_t K, int64_t N, const uint8_t* codes, const uint8_t* c2,
@@ -314,13 +316,19 @@ struct Low {
 };
 hipError_t launch_low(const Low& q, int halves, int64_t M, int r, hipStream_t s);
 
-// dZ = the gradients of G and U from dH and their 8-bit copies: bf16 [M][glu_ldz(F)], gate columns first,
-// zeros past 2 F (two: and behind it the same of what it rounds off); and the fp32 slices of scale dZ L2^T,
-// [*slices][2][M][r].
-inline int64_t glu_ldz(int64_t F) { return (2 * F + 7) / 8 * 8; }
+// Whether dX takes dZ as two bf16 planes, 16 bits of it, for every number of rows.  One plane's rounding adds to a
+// row of dX about what the result's own does, 1.41 of its error together, if the sum's 2 F terms average it; a few
+// large terms' do not.  That share for dZ of normal G, U and dH, median / 99% / largest of a row: F = 1 1.32 / 2.22 / 2.5,
+// 16 1.38 / 1.92 / 2.4, 256 1.41 / 1.59 / 1.8, 1024 1.41 / 1.51 / 1.6, 11008 1.41 / 1.44 / 1.45.
+inline bool glu_two(int64_t F) { return F <= 1024; }
+// Columns of a plane of dZ, gate first, zeros past 2 F; two planes lie side by side in a row of glu_ldz(F) elements.
+inline int64_t glu_plane(int64_t F) { return glu_two(F) ? (2 * F + 63) / 64 * 64 : (2 * F + 7) / 8 * 8; }
+inline int64_t glu_ldz(int64_t F) { return glu_plane(F) << (int)glu_two(F); }
+// dZ = the gradients of G and U from dH and their 8-bit copies, bf16 [M][glu_ldz(F)], and the fp32 slices of scale
+// dZ L2^T, [*slices][2][M][r].
 size_t glu_back_ws(int64_t M, int64_t F, int r);
 hipError_t launch_glu_back(const uint16_t* dH, int64_t M, int64_t F, const uint8_t* gu_codes, const uint8_t* gu_scales,
-                           const uint16_t* L2, int r, float scale, uint16_t* dZ, float* part, int* slices, bool two, hipStream_t s);
+                           const uint16_t* L2, int r, float scale, uint16_t* dZ, float* part, int* slices, hipStream_t s);
 
 // The adapter's gradients from packed activations (grads8.hip), in one launch and one for the slices' sums:
 //   dL1 [halves][K, r] = X^T G (X packed, G as planes);  dL2 [halves][r, N] = scale T^T dZ, where dZ is dY [M, N]

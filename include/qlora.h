@@ -514,9 +514,10 @@ int rms_norm_bwd(const uint16_t* dY, const void* S, const void* dS, int x_dtype,
  *        mx8_quantize), T the forward's T_out.
  * G and U are taken at their full fp32 sums, with T to 24 bits (16 where 8-bit copies are not
  * asked for and M <= 16). In the backward dZ and B are kept to 24 bits for dL1 and dL2; for dX
- * dZ is rounded to bf16 (to 16 bits where M F <= 1024, M < 512 and K is not so large that the product
- * takes large tiles) and B to 16 bits. M from one row on, any F, K % 64 == 0, 1 <= r <= 64; X, dZ (M rows of 2 F, to a multiple of 8, bf16), the
- * codes, L1 and L2 must each stay below 2^31 bytes. Workspaces from the queries.             */
+ * B is kept to 16 bits, and dZ to 16 bits up to F = 1024 and rounded to bf16 beyond, for every
+ * M and K alike. M from one row on, any F, K % 64 == 0, 1 <= r <= 64; X, dZ (M rows of 2 F, to
+ * a multiple of 8, bf16), the codes, L1 and L2 must each stay below 2^31 bytes. Workspaces from
+ * the queries.                                                                               */
 size_t qlora_swiglu_fwd_workspace(int64_t M, int64_t K, int64_t F, int r);
 int qlora_swiglu_fwd(const uint16_t* X, int64_t M, int64_t K, int64_t F,
                      const uint8_t* codes, const uint8_t* c2, const float* c1,
