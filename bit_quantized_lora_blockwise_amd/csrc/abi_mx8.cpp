@@ -198,7 +198,7 @@ int qlora_swiglu_fwd(const uint16_t* X, int64_t M, int64_t K, int64_t F, const u
   const int64_t pitch = w.part / sizeof(float);
   int slices = 0;
   if (few_ok(M, K, F, r)) {
-    QL_TRY(launch_small_slices(X, M, K, L1, true, r, drop::Params{}, 1.0f, part, &slices, s, 2));
+    QL_TRY(launch_small_slices(X, M, K, L1, true, r, drop::Params{}, 1.0f, part, &slices, s, true));
     if (glu_decode_ok(M, K) && !gu_codes)
       QL_TRY(launch_glu_decode(X, M, K, F, codes, c2, c1, part, slices, T_out, L2, r, lora_scale, H, s));
     else
@@ -248,7 +248,7 @@ int qlora_swiglu_bwd(const uint8_t* x_codes, const uint8_t* x_scales, const uint
     // G's planes from the product for few rows where it adds the slices up: a launch less
     if (small)
       return launch_dx_small(dZ, M, K, 2 * F, codes, c2, c1, sums ? nullptr : G, part, slices, planes, L1, r, dX, kNoDrop, s,
-                             glu_ldz(F), 2, two ? 2 : 1);
+                             glu_ldz(F), two);
     if (split)
       return launch_qgemm_dx_split(dZ, M, K, 2 * F, codes, c2, c1, G, L1, r, dX, part, s, 2, glu_ldz(F), true, two);
     return launch_qgemm_big(true, dZ, M, K, 2 * F, codes, c2, c1, G, L1, r, 1.0f, dX, s, 2, nullptr, glu_ldz(F), true, two);

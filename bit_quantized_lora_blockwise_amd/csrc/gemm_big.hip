@@ -174,7 +174,7 @@ __device__ __forceinline__ bf16x8 frag_kmajor_sw(const LDS_AS uint16_t* base, in
 // has the adapter's term.  Reduction 22016, 4096 columns: 1024 rows 163 us in four slices and 13 for
 // the join (one slice: 418); 64 rows 43 and 9, of which a slice's 22 steps are latency, not rate.
 // kTwo (dX, of glu_two): A's rows hold two planes, lda / 2 columns each, whose sum is dZ; the reduction walks W under
-// both.  Whole gated backwards, 4096 columns, F = 1024, us, one plane / two: 1024 rows 77 / 91, 4096 rows 129 / 184.
+// both.  Whole gated backwards, 4096 columns, F = 1024, us, one plane / two: 1024 rows 78 / 90, 4096 rows 128 / 180.
 struct BigOut {
   uint8_t* codes;     // kGlu: G and U in 8 bits, one packed matrix of 2 M rows (mx8.h), or null
   uint8_t* scales;

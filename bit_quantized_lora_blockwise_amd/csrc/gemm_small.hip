@@ -55,18 +55,20 @@ __device__ __forceinline__ void sum8(__amdgpu_buffer_rsrc_t rp, int S, int M, in
   }
 }
 
-// kVec: ldy % 8 == 0 (rows of dY in whole 16-byte pieces, zeros from N to ldy); kVecR: r % 8 == 0; kSum: G
-// as slices.  halves: of W's stacked rows, each with a G (two planes [M][r] where there are two; slices
-// [S][halves][M][r], planes [halves][3][M][..]) and an L1 [K][r] of its own.  terms: matrices of ldy / terms columns
-// whose sum is dY, side by side.
-template <bool kVec, bool kVecR, bool kSum>
+// kVec: rows of dY in whole 16-byte pieces, zeros from N to ldy; kVecR: r % 8 == 0; kSum: G as slices.  kGlu: W's
+// rows in two halves, each with a G (two planes [M][r]; slices [S][2][M][r], planes [2][3][M][..]) and an L1 [K][r] of
+// its own, and no dropout; kTwo: rows of dY hold two matrices of ldy / 2 columns whose sum it is.  Both are the
+// gated product's; decided at run time they cost the other layers' backwards 0.7 to 2 us of 14 to 60.
+template <bool kVec, bool kVecR, bool kSum, bool kGlu, bool kTwo>
 __global__ __launch_bounds__(64 * kW) void k_dx_small(const uint16_t* __restrict__ dY, int M, int K, int N,
                                                       const uint8_t* __restrict__ codes,
                                                       const uint8_t* __restrict__ c2, const float* __restrict__ c1,
                                                       const uint16_t* __restrict__ G, const float* __restrict__ Gp, int S,
                                                       uint16_t* __restrict__ planes, const uint16_t* __restrict__ L1,
                                                       int r, uint16_t* __restrict__ dX, Nf4Params q, drop::Params d,
-                                                      int ldy, int halves, int terms) {
+                                                      int ldy) {
+  constexpr int halves = kGlu ? 2 : 1;
+  if constexpr (!kGlu) ldy = N;
   __shared__ __attribute__((aligned(16))) uint16_t wt[kW][kN * kPitch];
   __shared__ f32x16 red[kW][2][64];
   const int w = threadIdx.x >> 6, l = threadIdx.x & 63, h = l >> 5, x = l & 31;
@@ -85,11 +87,14 @@ __global__ __launch_bounds__(64 * kW) void k_dx_small(const uint16_t* __restrict
     bf16x8 y[2];
   };
   // the second term's steps follow the first's, from a whole round of the waves on
-  const int next = (N + kN * kW - 1) / (kN * kW) * (kN * kW), end = terms == 1 ? N : next + N;
+  const int next = (N + kN * kW - 1) / (kN * kW) * (kN * kW), end = kTwo ? next + N : N;
   auto load = [&](int n0) {
     Step s;
-    const int col0 = terms > 1 && n0 >= next ? ldy / 2 : 0;
-    n0 -= col0 ? next : 0;
+    int col0 = 0;
+    if (kTwo && n0 >= next) {
+      col0 = ldy / 2;
+      n0 -= next;
+    }
     const int n = n0 + x;
     const uint32_t b = (uint32_t)n * kb + blockIdx.x;
     s.c = __builtin_amdgcn_raw_buffer_load_b128(rc, n < N ? (uint32_t)n * (K / 2) + 32 * blockIdx.x + 16 * h : kOOB, 0, 0);
@@ -157,18 +162,20 @@ __global__ __launch_bounds__(64 * kW) void k_dx_small(const uint16_t* __restrict
           for (int n = 0; n < 3; ++n) *(u32x4*)(planes + (3 * half + n) * plane + (int64_t)m * pitch + c) = v[n];
       } else {
         b = load8<kVecR>(rg, (uint32_t)(m * r + c) * 2u, m < M ? r - c : 0);
-        if (halves == 2) rest = load8<kVecR>(rg, (uint32_t)((M + m) * r + c) * 2u, m < M ? r - c : 0);
+        if constexpr (kGlu) rest = load8<kVecR>(rg, (uint32_t)((M + m) * r + c) * 2u, m < M ? r - c : 0);
       }
       low = qk::mfma32(a, b, low);
-      if (halves == 2) low = qk::mfma32(a, rest, low);
+      if constexpr (kGlu) low = qk::mfma32(a, rest, low);
     }
     }
+    if constexpr (!kGlu) {
     // half h draws octets 2 h and 2 h + 1 of its row; each lane takes its own columns 8 g + 4 h + e from both halves'
     uint32_t mine = 0;
 #pragma unroll
     for (int i = 0; i < 2; ++i) mine |= drop::bits8(d, (uint32_t)m, (uint32_t)(p >> 3) + 2 * h + i) << (16 * h + 8 * i);
     const u32x2 both = __builtin_amdgcn_permlane32_swap(mine, mine, false, false);
     keep = (both[0] | both[1]) >> (4 * h);
+    }
   }
   __syncthreads();
   if (w >= 2 || m >= M) return;
@@ -181,7 +188,7 @@ __global__ __launch_bounds__(64 * kW) void k_dx_small(const uint16_t* __restrict
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       o[e] = low[4 * g + e];
-      o[e] = sum[4 * g + e] + ((keep >> (8 * g + e)) & 1u ? d.scale * o[e] : 0.0f);
+      o[e] = sum[4 * g + e] + (kGlu ? o[e] : (keep >> (8 * g + e)) & 1u ? d.scale * o[e] : 0.0f);
     }
     *(u32x2*)(dX + (int64_t)m * K + p + 8 * g + 4 * h) = u32x2{qk::pack_bf16x2(o[0], o[1]), qk::pack_bf16x2(o[2], o[3])};
   }
@@ -519,20 +526,23 @@ bool dx_small_ok(int64_t M, int64_t K) {
 hipError_t launch_dx_small(const uint16_t* dY, int64_t M, int64_t K, int64_t N, const uint8_t* codes, const uint8_t* c2,
                            const float* c1, const uint16_t* G, const float* Gp, int S, uint16_t* planes,
                            const uint16_t* L1, int r, uint16_t* dX, const drop::Params& d, hipStream_t s, int64_t ldy,
-                           int halves, int terms) {
-  if (!ldy) ldy = N;
+                           bool sum) {
   const dim3 grid((unsigned)(K / kP), (unsigned)((M + 31) / 32));
-#define QL_DX(V, R, A)                                                                                                \
-  hipLaunchKernelGGL((k_dx_small<V, R, A>), grid, dim3(64 * kW), 0, s, dY, (int)M, (int)K, (int)N, codes, c2, c1, \
-                     G, Gp, S, planes, L1, r, dX, nf4_params(), d, (int)ldy, halves, terms)
-#define QL_DXS(A)                          \
-  do {                                     \
-    if (v && vr) QL_DX(true, true, A);     \
-    else if (v) QL_DX(true, false, A);     \
-    else if (vr) QL_DX(false, true, A);    \
-    else QL_DX(false, false, A);           \
+#define QL_DX(V, R, A, U, T)                                                                                               \
+  hipLaunchKernelGGL((k_dx_small<V, R, A, U, T>), grid, dim3(64 * kW), 0, s, dY, (int)M, (int)K, (int)N, codes, c2, c1, \
+                     G, Gp, S, planes, L1, r, dX, nf4_params(), d, (int)ldy)
+#define QL_DXS(A)                                                       \
+  do {                                                                  \
+    if (glu && sum && vr) QL_DX(true, true, A, true, true);             \
+    else if (glu && sum) QL_DX(true, false, A, true, true);             \
+    else if (glu && vr) QL_DX(true, true, A, true, false);              \
+    else if (glu) QL_DX(true, false, A, true, false);                   \
+    else if (v && vr) QL_DX(true, true, A, false, false);               \
+    else if (v) QL_DX(true, false, A, false, false);                    \
+    else if (vr) QL_DX(false, true, A, false, false);                   \
+    else QL_DX(false, false, A, false, false);                          \
   } while (0)
-  const bool v = ldy % 8 == 0, vr = r % 8 == 0;
+  const bool glu = ldy != 0, v = N % 8 == 0, vr = r % 8 == 0;
   if (G) QL_DXS(false);
   else QL_DXS(true);
 #undef QL_DXS

@@ -161,10 +161,11 @@ hipError_t launch_mx4_small_t(const uint16_t* X, int64_t M, int64_t K, const uin
 hipError_t launch_mx4_small_g(const uint16_t* dY, int64_t M, int64_t N, const uint16_t* L2, int r, float scale,
                               uint16_t* G, float* part, hipStream_t s);
 // fp32 slices (part: mx4_small_ws bytes) of scale (D o A) B (L1, b_is_kr) or scale A B^T (L2), to be
-// added in order.  products > 1: of A with that many B one after another, slices [product][slice][M][r].
+// added in order.  pair (L1 of R % 64 == 0 rows, no dropout): of A with two B, one behind the other, slices
+// [2][slice][M][r].
 hipError_t launch_small_slices(const uint16_t* A, int64_t M, int64_t R, const uint16_t* B, bool b_is_kr, int r,
                                const drop::Params& d, float scale, float* part, int* slices, hipStream_t s,
-                               int products = 1);
+                               bool pair = false);
 
 // --- adapter merge (merge.hip) ---------------------------------------------
 // W[n][k] = bf16(W'[n][k] + scale * sum_c L1[k][c] L2[c][n]), W' the bf16
@@ -252,15 +253,15 @@ hipError_t launch_fwd_small(const uint16_t* X, int64_t M, int64_t K, int64_t N, 
                             const float* c1, const uint16_t* T, const float* Tp, int S, uint16_t* T_out,
                             const uint16_t* L2, int r, float scale, uint16_t* Y, hipStream_t s);
 // dX = bf16(dY W' + D o (G L1^T)) from G, or with G = nullptr from its slices Gp (S of them), added
-// here; `planes` then receives it to 24 bits.  ldy, halves: rows of dY ldy elements apart, zeros behind N
-// (0: dense); W's rows in that many halves with a G (slices [S][halves][M][r]) and an L1 each.  terms: matrices
-// of ldy / terms columns, side by side, whose sum is dY.
+// here; `planes` then receives it to 24 bits.  ldy: the gated product's dX; rows of dY are ldy elements (a multiple
+// of 8) apart, zeros behind N; W's rows in two halves with a G (two planes; slices [S][2][M][r]) and an L1 each; d is
+// not read.  sum: rows of dY hold two matrices of ldy / 2 columns whose sum it is.
 constexpr int kSmallSlices = 8;   // of T and G that the products for few rows add up
 bool dx_small_ok(int64_t M, int64_t K);
 hipError_t launch_dx_small(const uint16_t* dY, int64_t M, int64_t K, int64_t N, const uint8_t* codes, const uint8_t* c2,
                            const float* c1, const uint16_t* G, const float* Gp, int S, uint16_t* planes,
                            const uint16_t* L1, int r, uint16_t* dX, const drop::Params& d, hipStream_t s, int64_t ldy = 0,
-                           int halves = 1, int terms = 1);
+                           bool sum = false);
 
 // --- microscaled 8-bit activations (mx8.hip) -------------------------------------
 hipError_t launch_mx8_quant(const void* X, bool bf16, int64_t rows, int64_t cols, int64_t ld, uint8_t* codes,

@@ -64,20 +64,24 @@ __device__ __forceinline__ u32x4 load8(__amdgpu_buffer_rsrc_t rs, uint32_t row, 
 }
 
 // kBkr: B(k, c) = Bm[k][c] (L1 [R, r]), else Bm[c][k] (L2 [r, R]).  kQuant: also packs A.
-// blocks: of the packed length (a multiple of four).  ctiles: column tiles of one product; the
-// launch's others are those of the next ones, B and the slices one after another.
-template <bool kBkr, bool kVec, bool kDrop, bool kQuant>
+// blocks: of the packed length (a multiple of four).  kPair: the launch's second half of column tiles is a second
+// product's, B and the slices behind the first's.
+template <bool kBkr, bool kVec, bool kDrop, bool kQuant, bool kPair = false>
 __global__ __launch_bounds__(kDThreads) void k_small_down(const uint16_t* __restrict__ A, int M, int R,
                                                           const uint16_t* __restrict__ Bm, int r, int blocks,
                                                           int per_slice, drop::Params d, uint32_t* __restrict__ codes,
                                                           uint8_t* __restrict__ scales, float* __restrict__ part,
-                                                          float out_scale, int ctiles) {
+                                                          float out_scale) {
   __shared__ f32x4 red[kDW * 64];
   const int w = threadIdx.x >> 6, l = threadIdx.x & 63, g = l >> 4, x = l & 15;
-  const int seg = (int)blockIdx.z / ctiles;
-  const int m = 16 * (int)blockIdx.x + x, c = 16 * ((int)blockIdx.z - seg * ctiles) + x, slice = blockIdx.y;
-  Bm += (int64_t)seg * R * r;
-  part += (int64_t)seg * gridDim.y * M * r;
+  const int m = 16 * (int)blockIdx.x + x, slice = blockIdx.y;
+  int ctile = blockIdx.z;
+  if (kPair && ctile >= (int)gridDim.z / 2) {
+    ctile -= (int)gridDim.z / 2;
+    Bm += (int64_t)R * r;
+    part += (int64_t)gridDim.y * M * r;
+  }
+  const int c = 16 * ctile + x;
   const __amdgpu_buffer_rsrc_t ra = rsrc(A, (uint64_t)M * R * 2), rb = rsrc(Bm, (uint64_t)R * r * 2);
   const int last = min(blocks, (slice + 1) * per_slice);
   f32x4 acc = {0, 0, 0, 0};
@@ -319,14 +323,13 @@ hipError_t launch_product(const SmallArgs& a, hipStream_t s) {
 template <bool kBkr>
 hipError_t launch_down(const uint16_t* A, int64_t M, int64_t R, const uint16_t* Bm, int r, const drop::Params& d,
                        uint8_t* codes, uint8_t* scales, float* part, int* slices, hipStream_t s, float out_scale = 1.0f,
-                       int products = 1) {
+                       bool pair = false) {
   const int blocks = (int)(padded(R) / kBlock), per = slice_blocks(M, blocks, r);
   *slices = (blocks + per - 1) / per;
-  const int ctiles = (r + 15) / 16;
-  const dim3 grid((unsigned)((M + 15) / 16), (unsigned)*slices, (unsigned)(products * ctiles));
-#define QL_SD(V, D, Q)                                                                                              \
-  hipLaunchKernelGGL((k_small_down<kBkr, V, D, Q>), grid, dim3(kDThreads), 0, s, A, (int)M, (int)R, Bm, r, blocks, per, \
-                     d, (uint32_t*)codes, scales, part, out_scale, ctiles)
+  const dim3 grid((unsigned)((M + 15) / 16), (unsigned)*slices, (unsigned)((r + 15) / 16 << (int)pair));
+#define QL_SD(V, D, ...)                                                                                                  \
+  hipLaunchKernelGGL((k_small_down<kBkr, V, D, __VA_ARGS__>), grid, dim3(kDThreads), 0, s, A, (int)M, (int)R, Bm, r, blocks, \
+                     per, d, (uint32_t*)codes, scales, part, out_scale)
   const bool vec = (R % 8) == 0, drop = kBkr && d.cut != 0;
   if constexpr (kBkr) {
     if (drop) {
@@ -337,6 +340,10 @@ hipError_t launch_down(const uint16_t* A, int64_t M, int64_t R, const uint16_t* 
         if (vec) QL_SD(true, true, false);
         else QL_SD(false, true, false);
       }
+      return hipGetLastError();
+    }
+    if (pair) {                            // of rows of whole blocks of 64
+      QL_SD(true, false, false, true);
       return hipGetLastError();
     }
   }
@@ -409,7 +416,7 @@ hipError_t launch_mx4_small_g(const uint16_t* dY, int64_t M, int64_t N, const ui
 }
 
 hipError_t launch_small_slices(const uint16_t* A, int64_t M, int64_t R, const uint16_t* B, bool b_is_kr, int r,
-                               const drop::Params& d, float scale, float* part, int* slices, hipStream_t s, int products) {
-  return b_is_kr ? launch_down<true>(A, M, R, B, r, d, nullptr, nullptr, part, slices, s, scale, products)
-                 : launch_down<false>(A, M, R, B, r, drop::Params{}, nullptr, nullptr, part, slices, s, scale, products);
+                               const drop::Params& d, float scale, float* part, int* slices, hipStream_t s, bool pair) {
+  return b_is_kr ? launch_down<true>(A, M, R, B, r, d, nullptr, nullptr, part, slices, s, scale, pair)
+                 : launch_down<false>(A, M, R, B, r, drop::Params{}, nullptr, nullptr, part, slices, s, scale);
 }
