@@ -106,21 +106,12 @@ __global__ __launch_bounds__(kThr, 6) void k_glu_decode(const uint16_t* __restri
   Step sa, sb;
   load(0, sa);
   __builtin_amdgcn_sched_barrier(0);
-  // T in two planes
-  u32x2 ta[2];
   {
-    f32x4 v = {0, 0, 0, 0};
+    f32x4 tv = {0, 0, 0, 0};
 #pragma unroll
     for (int s = 0; s < kSlices; ++s)
-      if (s < S) v += ps[s];
-    ta[0] = u32x2{qk::pack_bf16x2(v[0], v[1]), qk::pack_bf16x2(v[2], v[3])};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] -= __uint_as_float(j & 1 ? ta[0][j >> 1] & 0xFFFF0000u : ta[0][j >> 1] << 16);
-    ta[1] = u32x2{qk::pack_bf16x2(v[0], v[1]), qk::pack_bf16x2(v[2], v[3])};
-    if (T_out && blockIdx.x == 0 && t_ok)
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (rb + j < r) T_out[((int64_t)half * M + x) * r + rb + j] = (uint16_t)(ta[0][j >> 1] >> (16 * (j & 1)));
+      if (s < S) tv += ps[s];
+    red[w][l] = tv;                        // this lane's own until the sums meet there
   }
 #pragma unroll
   for (int j = 0; j < kXPer; ++j) {
@@ -161,11 +152,19 @@ __global__ __launch_bounds__(kThr, 6) void k_glu_decode(const uint16_t* __restri
     uint16_t a0 = vl[0], a1 = vl[1], a2 = vl[2], a3 = vl[3];
     asm volatile("" : "+v"(a0), "+v"(a1), "+v"(a2), "+v"(a3));
     const u32x2 b = {__builtin_amdgcn_perm(a1, a0, 0x05040100u), __builtin_amdgcn_perm(a3, a2, 0x05040100u)};
-    f32x4 low = {0, 0, 0, 0};
+    f32x4 low = {0, 0, 0, 0}, tv = red[w][l];
+    // T in three planes, 24 bits, as every path of the gated product takes it
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
-      low = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(s16x4, ta[k]), __builtin_bit_cast(s16x4, b), low, 0,
-                                                      0, 0);
+    for (int k = 0; k < 3; ++k) {
+      const u32x2 a = {qk::pack_bf16x2(tv[0], tv[1]), qk::pack_bf16x2(tv[2], tv[3])};
+      low = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(s16x4, a), __builtin_bit_cast(s16x4, b), low, 0, 0, 0);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (k == 0 && T_out && blockIdx.x == 0 && t_ok && rb + j < r)
+          T_out[((int64_t)half * M + x) * r + rb + j] = (uint16_t)(a[j >> 1] >> (16 * (j & 1)));
+        tv[j] -= __uint_as_float(j & 1 ? a[j >> 1] & 0xFFFF0000u : a[j >> 1] << 16);
+      }
+    }
     acc += scale * low;
   }
   red[w][l] = acc;

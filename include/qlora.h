@@ -512,12 +512,11 @@ int rms_norm_bwd(const uint16_t* dY, const void* S, const void* dS, int x_dtype,
  *        dL1 = fp32(X^T B), dL2 = fp32(lora_scale * T^T dZ) (2 consecutive blocks each)
  *        X is the packed 8-bit copy of the forward's input (from rms_norm_fwd or
  *        mx8_quantize), T the forward's T_out.
- * G and U are taken at their full fp32 sums, with T to 24 bits (16 where 8-bit copies are not
- * asked for and M <= 16). In the backward dZ and B are kept to 24 bits for dL1 and dL2; for dX
- * B is kept to 16 bits, and dZ to 16 bits up to F = 1024 and rounded to bf16 beyond, for every
- * M and K alike. M from one row on, any F, K % 64 == 0, 1 <= r <= 64; X, dZ (M rows of 2 F, to
- * a multiple of 8, bf16), the codes, L1 and L2 must each stay below 2^31 bytes. Workspaces from
- * the queries.                                                                               */
+ * G and U are taken at their full fp32 sums, with T to 24 bits. In the backward dZ and B are
+ * kept to 24 bits for dL1 and dL2; for dX B is kept to 16 bits, and dZ to 16 bits up to F = 1024
+ * and rounded to bf16 beyond, for every M and K alike. M from one row on, any F, K % 64 == 0,
+ * 1 <= r <= 64; X, dZ (M rows of 2 F, to a multiple of 8, bf16), the codes, L1 and L2 must each
+ * stay below 2^31 bytes. Workspaces from the queries.                                        */
 size_t qlora_swiglu_fwd_workspace(int64_t M, int64_t K, int64_t F, int r);
 int qlora_swiglu_fwd(const uint16_t* X, int64_t M, int64_t K, int64_t F,
                      const uint8_t* codes, const uint8_t* c2, const float* c1,
@@ -534,9 +533,9 @@ int qlora_swiglu_bwd(const uint8_t* x_codes, const uint8_t* x_scales, const uint
                      void* workspace, size_t ws_bytes, void* stream);
 
 /* qlora_linear_bwd with X as a packed 8-bit matrix, for a linear whose input the forward kept
- * so (the down projection's H). Formulas, sizes and errors as there (L1 and L2 below 2^31
- * bytes too), X being the values that the packed matrix stands for; T is required (it cannot be formed again as the forward had
- * it), and G is kept to 24 bits for dL1.                                                     */
+ * so (the down projection's H). Formulas, sizes and errors as there (dX from G in bf16 as well;
+ * L1 and L2 below 2^31 bytes too), X being the values that the packed matrix stands for; T is
+ * required (it cannot be formed again as the forward had it), and G is kept to 24 bits for dL1. */
 size_t qlora_linear_bwd_mx8_workspace(int64_t M, int64_t K, int64_t N, int r);
 int qlora_linear_bwd_mx8(const uint8_t* x_codes, const uint8_t* x_scales, const uint16_t* dY,
                          int64_t M, int64_t K, int64_t N,

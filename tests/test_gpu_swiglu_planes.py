@@ -2,8 +2,14 @@
 
 The sums are made short or exact here, so that what is left of the tolerances is the rounding in question
 (U = 2^-24, half a step of bf16 2^-8):
+  T enters the gated product with 24 bits, with or without 8-bit copies.  X and L1 are whole numbers, so that T's
+  sums of K <= 512 terms are whole numbers below 2^24 and exact in any order, and the base is zero: G and U are
+  s T L2 of r terms in three planes, off by (3 r + 8) U S |T| |L2|.  Two planes lose 2^-18 of T and more, eight
+  times that.  H = silu(G) U carries 1.1 of G's error, U's, and its own exponential and product, (|G| + 4) 2^-23.
+  dX takes B with 16 bits: a zero base leaves B L1^T; one plane loses 2^-9.
   dX of a gated product of up to 1024 columns takes dZ to 16 bits for any number of rows (test_gpu_swiglu's
   bounds with 2^-16 |dZ| |W| in place of 2^-8).
+A result in bf16 or 8 bits has to be the rounding of a value within those bounds.
 """
 import numpy as np
 import pytest
@@ -11,11 +17,76 @@ import torch
 
 import oracle as O
 from test_gpu_swiglu import Block, S, U, check_backward, f64, qlib
-from test_gpu_norm import within
+from test_gpu_norm import packed_between, within
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
 X8 = O.mx8
+
+
+def rounds_between(got, ref, tol, name):
+    """Every value is the bf16 rounding of one in [ref - tol, ref + tol]."""
+    lo, hi = (torch.from_numpy(v).to(torch.bfloat16).float() for v in (ref - tol, ref + tol))
+    v = got.float().cpu()
+    out = (v < lo) | (v > hi)
+    print(f"{name}: {int(out.sum())} of {out.numel()} outside", flush=True)
+    assert not out.any(), f"{name}: {int(out.sum())} of {out.numel()}"
+
+
+def over_zero(seed, M, K, F, r):
+    """A gated block over a base of zeros."""
+    q = qlib()
+    b = Block(seed, M, K, F, r)
+    codes, absmax = q.nf4_quantize(torch.zeros(2 * F, K, dtype=torch.bfloat16, device=DEV))
+    b.base = (codes, *q.nf4_double_quant(absmax))
+    b.W = f64(q.nf4_dequantize(*b.base, 2 * F, K))
+    assert not b.W.any()
+    return b
+
+
+def whole_numbers(b, seed):
+    """X and L1 whole, T = X L1 below 2^24 and exact; L2 so small that G and U are about one."""
+    g = torch.Generator().manual_seed(seed)
+    whole = lambda m, *shape: torch.randint(-m, m + 1, shape, generator=g).to(torch.bfloat16).to(DEV)  # noqa: E731
+    b.X, b.L1 = whole(255, b.M, b.K), whole(127, 2, b.K, b.r)
+    assert b.K * 255 * 127 < 1 << 24
+    b.L2 = (torch.randn(2, b.r, b.F, generator=g) * 4e-6).to(torch.bfloat16).to(DEV)
+    return np.stack([f64(b.X) @ f64(b.L1[h]) for h in range(2)])
+
+
+@pytest.mark.parametrize("M,K,F,r", [
+    # up to 16 rows (decoding without copies), few rows from T's slices and from its planes, half and whole large tiles
+    (1, 512, 20000, 1), (16, 512, 4000, 3), (16, 512, 1000, 6), (32, 512, 16000, 1), (70, 512, 4000, 1),
+    (2100, 512, 128, 1), (1300, 512, 1100, 3), (1300, 64, 3000, 17)])
+def test_t_keeps_its_bits(M, K, F, r):
+    q = qlib()
+    b = over_zero(M * 1039 + K + F, M, K, F, r)
+    t = whole_numbers(b, M + F)
+    gu = [S * t[h] @ f64(b.L2[h]) for h in range(2)]
+    d = [(3 * r + 8) * U * S * np.abs(t[h]) @ np.abs(f64(b.L2[h])) for h in range(2)]
+    (g, u), (dg, du) = gu, d
+    h = g * X8.sigmoid(g) * u
+    dh = 1.1 * np.abs(u) * dg + np.abs(g * X8.sigmoid(g)) * du + 1.1 * dg * du + (np.abs(g) + 4) * 2.0**-23 * np.abs(h)
+    H, T, gu8 = q.qlora_swiglu_fwd(b.X, *b.base, F, b.L1, b.L2, S, T_out=True, mx8=True)
+    assert torch.equal(T.float().cpu(), torch.from_numpy(t).to(torch.bfloat16).float())
+    packed_between(gu8, np.concatenate(gu), np.concatenate(d), F, "GU")
+    rounds_between(H, h, dh, "H")
+    H, T2, _ = q.qlora_swiglu_fwd(b.X, *b.base, F, b.L1, b.L2, S, T_out=True)
+    assert torch.equal(T2, T)
+    rounds_between(H, h, dh, "H alone")
+
+
+@pytest.mark.parametrize("M,K,F,r", [
+    # few rows with B in slices and in planes, slices of the reduction, large tiles; one and two planes of dZ
+    (40, 128, 1100, 8), (40, 128, 100, 8), (64, 4096, 1030, 64), (300, 4096, 1100, 5), (4100, 2048, 1030, 8),
+    (800, 2048, 37, 12), (1100, 1024, 1000, 8)])
+def test_b_keeps_its_bits(M, K, F, r):
+    q = qlib()
+    b = over_zero(M * 1049 + K + F, M, K, F, r)
+    n = sparse(b)
+    _, T, gu8 = q.qlora_swiglu_fwd(b.X, *b.base, F, b.L1, b.L2, S, T_out=True, mx8=True)
+    dX = q.qlora_swiglu_bwd(q.mx8_quantize(b.X), b.d, *b.base, b.L1, b.L2, gu8, T, S)[0]
+    rounds_between(dX, *dx_bound(b, gu8, T, n, 0.0), "dX")
 
 
 @pytest.mark.parametrize("M,K,F,r", [
