@@ -68,12 +68,4 @@ __device__ __forceinline__ void decode4(uint32_t w, float s, float* v) {
   v[3] = hi[1] * s;
 }
 
-// Code t of four.
-__device__ __forceinline__ float decode1(uint32_t w, int t) {
-  return t == 0   ? __builtin_amdgcn_cvt_f32_fp8((int)w, 0)
-         : t == 1 ? __builtin_amdgcn_cvt_f32_fp8((int)w, 1)
-         : t == 2 ? __builtin_amdgcn_cvt_f32_fp8((int)w, 2)
-                  : __builtin_amdgcn_cvt_f32_fp8((int)w, 3);
-}
-
 }  // namespace mx8
