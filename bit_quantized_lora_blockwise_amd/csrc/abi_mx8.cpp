@@ -52,7 +52,7 @@ FwdWs fwd_ws(int64_t M, int64_t K, int64_t F, int r) {
   return w;
 }
 
-// Whether dX [M, K], whose reduction is over n columns, is taken in slices of the reduction.  The work
+// Whether dX [M, K], whose reduction walks n columns (both planes of dZ), is taken in slices of the reduction.  The work
 // groups of the product for few rows (64 columns of 32 rows) and of the large tiles each walk all of
 // it; slices cost a launch and the partial sums' way to memory.  Whole backwards, us, walked / in
 // slices: gated, K = 4096, n = 22016 1 row 91 / 69, 64 rows 120 / 73, 512 rows 456 / 154, 1024 rows

@@ -10,7 +10,7 @@
 // requested before the codes.  The waves' sums meet in LDS in order, where the gate meets its up
 // half, so neither goes to memory.
 //
-// One row 4096 -> 2 x 11008: 17 us, 47 MB at 2.7 TB/s (9 us at a copy's rate); 8192 -> 2 x 22016 55 us.
+// One row 4096 -> 2 x 11008: 17.4 us, 47 MB at 2.7 TB/s (9 us at a copy's rate); 8192 -> 2 x 22016 55 us.
 // Bound: the vector units, 4.15 instructions a weight, busy for 90% of the time that a CU has work;
 // the rest is the first loads' latency and the last work groups (2.7 a CU).  T's slices take 2.4 us
 // in a launch before it: formed in this one, behind flags as for a single linear, the two together

@@ -35,7 +35,10 @@
 //    The consumers issue no global loads and wait only for their LDS reads,
 //    and their output stores go through a buffer descriptor, so a tile's
 //    stores drain while the next tile's LoRA term and first steps run (the
-//    memory counter a wait would block on counts stores too).
+//    memory counter a wait would block on counts stores too).  Where an instance
+//    spills registers, their reloads are loads and wait so: two to fifteen of the dX
+//    producers' around the adapter's operands, 75 of the gated product's 128-column
+//    consumers around the adapter's term and in the stores; none in the step loop.
 #include <algorithm>
 #include <type_traits>
 
@@ -161,8 +164,8 @@ __device__ __forceinline__ bf16x8 frag_kmajor_sw(const LDS_AS uint16_t* base, in
 // planes for each half, 24 bits of it: G and U are rounded to 8 bits, and a T of 8 bits
 // would put one in 300 of their codes on the other side of a border, one of 16 bits one in
 // 20000, six times as many as the sums themselves.  The planes go straight to LDS in the
-// activation tile's layout.  8192 -> 2 x 22016, 2048 rows with the 8-bit copies: 1422 us, 1039
-// TFLOP/s, 0.77 of a large library product's rate (the same weight as a plain stacked product:
+// activation tile's layout.  8192 -> 2 x 22016, 2048 rows with the 8-bit copies: 1350 to 1430 us,
+// 1100 to 1040 TFLOP/s, 0.81 to 0.77 of a large library product's rate (the same weight as a plain stacked product:
 // 1313 to 1383 us); bound as that one.
 // kDrop (dX): the adapter term is D o (G L1^T).  All waves draw the tile's decisions
 // into LDS (a bit an element) while the LoRA operands arrive (by the producers alone,
@@ -584,9 +587,9 @@ __global__ __launch_bounds__(kT, 1) void k_qgemm_big(const uint16_t* __restrict_
   }
 
   // ================================ consumers ================================
-  // They issue no loads: between barriers they only read LDS and store their
-  // outputs, and they wait only for their LDS reads, so one tile's output
-  // stores drain while the next tile's LoRA term and first steps run.
+  // They issue no loads but of spilled registers, between tiles: between barriers
+  // they only read LDS and store their outputs, and they wait only for their LDS
+  // reads, so one tile's output stores drain while the next tile's first steps run.
   // (kHalf: 32 columns of each half, accumulators 0 and 1)
   constexpr int kJ = kHalf ? 2 : 4;
   f32x16 acc[2][kJ];

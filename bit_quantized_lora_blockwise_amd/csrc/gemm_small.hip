@@ -321,7 +321,8 @@ __global__ __launch_bounds__(64 * kW) void k_fwd_small(const uint16_t* __restric
 // 17 rows 4096 -> 2 x 11008: 46 us, 47 MB at 1 TB/s; vector units busy for 14, the data return for 28
 // (a lane's row is its own, so an instruction's 64 lanes read 64 lines), about 10 a launch's first
 // loads and end.  Two blocks a step (a fifth fewer loads, half the tables) took 45 us, and 8192 -> 2
-// x 22016 153 for 145; a wave's blocks side by side 47; two steps' registers in turn 48.
+// x 22016 153 for 145; a wave's blocks side by side 47; two steps' registers in turn 48.  kI = 2 spills 17
+// registers.
 template <int kI, bool kSum>
 __global__ __launch_bounds__(64 * (kW + 2 * kI)) void k_glu_small(const uint16_t* __restrict__ X, int M, int K, int F,
                                                        const uint8_t* __restrict__ codes,

@@ -6,9 +6,9 @@
 
 namespace glu {
 
-// 1 / (1 + e^-g): exp2 and the reciprocal are off by about one unit in the last place each,
-// which the rounding of H to bf16 does not see and that of gradients in fp32 takes as it
-// takes the sums'.  For g below -88 the exponential is infinite and the result 0, as in the limit.
+// 1 / (1 + e^-g), off by at most (|g| + 4) 2^-23 of itself: the exponent's product is rounded once, 2^-24 of
+// |g| log2(e), which the exponential turns into as large a share; exp2 and the reciprocal add about one unit in
+// the last place each.  H's rounding to bf16 does not see that before |g| is in the thousands.  For g below -88 the exponential is infinite and the result 0, as in the limit.
 __device__ __forceinline__ float sigmoid(float g) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.442695041f * g));
 }

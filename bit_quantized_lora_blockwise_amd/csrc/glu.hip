@@ -4,8 +4,8 @@
 //   dG = dH U sig (1 + G (1 - sig)), dU = dH G sig, sig = 1 / (1 + e^-G)     (glu.h)
 //   Gr = s dZ L2^T, dL1 = X^T Gr, dL2 = s T^T dZ       for dZ = dG and dU (or a linear's dY)
 //
-// dL1 and dL2 are fp32, so what enters them is kept to 24 bits: dZ and Gr as three bf16
-// planes whose sum they are (each takes what the ones before it rounded off).  dZ's planes
+// dL1 and dL2 are fp32, so what enters them is not rounded again: dZ and Gr, formed in fp32, go in as
+// three bf16 planes whose sum they are to 24 bits (each takes what the ones before it rounded off).  dZ's planes
 // exist on chip alone: the pass that forms Gr (k_glu_back) writes the first one, which is
 // what the dX product takes, and the pass that forms dL2 (grads8.hip) computes dZ again from the
 // 4 bytes an element that it came from.

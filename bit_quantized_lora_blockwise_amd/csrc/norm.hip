@@ -2,12 +2,20 @@
 //   forward   S = rnd(X + R);  inv = 1 / sqrt(mean(S^2) + eps);  Y = bf16(S w inv), and
 //             the same values in microscaled 8-bit (mx8.h) for the backward of what reads Y
 //   backward  n = S inv, d = w dY:  dX = inv (d - n mean(n d)) + dS,  dw = sum over rows of n dY
-// Bound: HBM, each matrix read or written once: a row stays in registers between the sum
-// over it and the pass that uses the sum.  Sums and statistics are fp32 (a thread's at most
+// Bound up to 8192 columns: HBM, each matrix read or written once: a row stays in registers
+// between the sum over it and the pass that uses the sum.  Sums and statistics are fp32 (a thread's at most
 // 32 squares, then a tree), the root fp64: one of them a row.
 //
 // bf16: 2048 x 8192 with the residual and 8-bit copies 30 us, 5.0 TB/s; backward 4096 x 4096 with dS
 // 26.5 us, 5.1 TB/s, and 4 us for dw.
+//
+// Past 8192 columns the 1024 threads of a row have 128 registers each.  The backward keeps two rows,
+// the weights and dw, and spills: 13 registers with two chunks of bf16 (42 if cols % 8), 41 (123) of
+// fp32, 183 (355) and 263 (708) with four; the forward 32 and 75 with four chunks if cols % 8.  Bound by
+// those there: 4096 rows, bf16 / fp32, us (a copy's time for the same bytes): backward 8192 columns 50 / 96
+// (52 / 91), 12288 107 / 310 (78 / 136), 16384 138 / 363 (103 / 181), 16390 867 / 1923, 22016 676 / 1245
+// (139 / 243); forward with residual and 8-bit copy 8192 53 / 93, 16384 118 / 184, 22016 169 / 254, 22018
+// 253 / 489.
 //
 // A row belongs to a wave (up to 1024 columns) or to 256, 512 or 1024 threads, one or two
 // chunks of eight columns a thread (four past 16384 columns).  Rows are read through a
