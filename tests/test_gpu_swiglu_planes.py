@@ -168,3 +168,34 @@ def test_two_planes_of_many_rows():
             tol += (2.0**-15 + 4 * F * U) * (np.abs(dz[h]) @ np.abs(w[h * F:(h + 1) * F]))
             tol += (2.0**-15 + 4 * F * U) * (S * np.abs(dz[h]) @ np.abs(f64(L2[h])).T @ np.abs(f64(L1[h])).T)
         within(dX[rows], rx, tol, "dX")
+
+
+@pytest.mark.parametrize("M,K,F,r", [(40, 128, 100, 8), (800, 2048, 37, 12), (1000, 16640, 20, 8), (1100, 1024, 1000, 8),
+                                     (600, 64, 33, 3)])
+def test_two_planes_in_a_given_workspace_and_captured(M, K, F, r):
+    """Few rows, large tiles, several rounds of them with the gradients beside, slices: from scratch memory full of
+    NaN, and captured, then replayed between eager calls."""
+    q = qlib()
+    b = Block(M * 1051 + K + F, M, K, F, r)
+    x8 = q.mx8_quantize(b.X)
+    _, T, gu8 = q.qlora_swiglu_fwd(b.X, *b.base, F, b.L1, b.L2, S, T_out=True, mx8=True)
+    d = b.d.clone()
+    ws = torch.full((q.lib().qlora_swiglu_bwd_workspace(M, K, F, r),), 255, dtype=torch.uint8, device=DEV)
+
+    def run(**kw):
+        return q.qlora_swiglu_bwd(x8, d, *b.base, b.L1, b.L2, gu8, T, S, **kw)
+
+    want = run()
+    for u, v in zip(run(workspace=ws), want):
+        assert torch.isfinite(v).all() and torch.equal(u, v)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = run(workspace=ws)
+    for k in range(3):
+        d.copy_(b.d * (0.5 + k))
+        graph.replay()
+        eager = run()
+        torch.cuda.synchronize()
+        for u, v in zip(held, eager):
+            assert torch.equal(u, v), k
